@@ -68,8 +68,10 @@ typedef struct CUstream_st *psw_stream_t;
 /* ---- return codes (host-detected) ---- */
 #define PSW_OK                 0
 #define PSW_ENULL             -1  /* a required pointer is NULL */
-#define PSW_EINVAL_HEADS      -2  /* n_q_heads or n_kv_heads <= 0, or n_q % n_kv != 0 */
-#define PSW_EINVAL_HDIM       -3  /* head_dim not 256 or 512 */
+#define PSW_EINVAL_HEADS      -2  /* n_q_heads or n_kv_heads <= 0, or n_q % n_kv != 0; latent
+                                     layers: n_heads outside [1, 128] */
+#define PSW_EINVAL_HDIM       -3  /* head_dim not 256 or 512; latent layers: latent_dim not 256 or
+                                     512, rope_dim not 64, nope_dim or v_dim not 128 */
 #define PSW_EINVAL_SOFTCAP    -4  /* softcap negative or not finite */
 #define PSW_EINVAL_WINDOW     -5  /* window negative */
 #define PSW_EINVAL_BLOCKSIZE  -6  /* block_size != 16 */
@@ -91,6 +93,8 @@ typedef struct CUstream_st *psw_stream_t;
                                      or a shared layer with no cache-owning layer of its type */
 #define PSW_ENOBLOCKS        -19  /* the block pool has fewer free blocks than asked for */
 #define PSW_EBLOCK           -20  /* a block id outside the pool, or freed more often than held */
+#define PSW_EINVAL_STRIDE    -21  /* a row or head stride shorter than its row, or not a multiple
+                                     of 8 elements */
 
 /* ---- device error bits (psw_get_error) ---- */
 #define PSW_DEVERR_BLOCK_ID    1  /* block id outside [0, num_blocks): access skipped */
@@ -358,6 +362,157 @@ PSW_API int attn_decode_paged_fp8(const psw_layer_t *layer, const void *q, const
                                   const float *v_scale, const psw_pages_t *pages,
                                   const int32_t *seq_lens, int32_t n_seqs, float *out,
                                   float *lse, void *ws, size_t ws_bytes, psw_stream_t stream);
+
+/*
+ * ---- latent attention: keys and values from one shared latent row per token
+ *
+ * The pages name no such layer; this group is the library's own. A token's
+ * cache row is L = latent_dim values c (an RMS-normalised latent) followed by
+ * R = rope_dim = 64 values r (a rotated key part that every head shares). The
+ * pool is [num_blocks][16][L + R], bf16 (or FP8, below), addressed through the
+ * block table as every other pool. Per head h, with up-projection rows
+ * w[h][0 .. 128) for the keys and w[h][128 .. 256) for the values:
+ *   expanded:  k_j = [w_k[h] c_j | r_j],  v_j = w_v[h] c_j,
+ *              s_j = scale * <q, k_j>,    out = sum_j softmax(s)_j v_j
+ *   absorbed:  q' = [w_k[h]^T q_nope | q_rope],
+ *              s_j = scale * <q', [c_j | r_j]>,  out' = sum_j softmax(s)_j c_j
+ * with out = w_v[h] out'. The absorbed form reads each row once for all heads
+ * and is the decode form; the expanded form does 320 instead of 2 L + R
+ * multiply-adds per (query, head, key) and is the prefill form. Window,
+ * softcap, masks and positions are those of attn_decode_paged and
+ * attn_prefill_chunked. `out` is bf16 here: it feeds the next projection.
+ */
+typedef struct {
+  int32_t n_heads;     /* query heads, 1 .. 128 */
+  int32_t latent_dim;  /* L: 256 or 512 */
+  int32_t rope_dim;    /* R: must be 64 */
+  int32_t nope_dim;    /* expanded key components per head beside R: must be 128 */
+  int32_t v_dim;       /* expanded value components per head: must be 128 */
+  int32_t window;      /* 0 = full causal attention; W > 0 = sliding window of W keys */
+  float   softcap;     /* 0 = off; > 0 applies cap * tanh(s / cap) */
+  float   scale;       /* multiplies q.k before the softcap; > 0 */
+  int32_t block_size;  /* tokens per page; must be 16 */
+} psw_latent_t;
+
+/* Norm of the latent and rotation of the shared key part and of the queries. */
+typedef struct {
+  float theta;                 /* RoPE base, > 0 */
+  float eps;                   /* RMS-norm epsilon, >= 0 */
+  const float *latent_weight;  /* device fp32 [L], 16-byte aligned, or NULL (weightless) */
+} psw_latent_norm_t;
+
+/* Workspace bytes of attn_decode_latent and attn_decode_latent_fp8 for a batch
+ * of up to n_seqs sequences (host arithmetic). It holds partial results within
+ * a call, needs no zeroing and carries nothing between calls; calls whose
+ * kernels could overlap on the GPU need one each. */
+PSW_API int psw_latent_workspace_bytes(const psw_latent_t *layer, int32_t n_seqs, size_t *bytes);
+
+/*
+ * The step before latent attention, fused: token t of sequence b at position
+ * pos = past_lens[b] + (t - cu_new[b]) gets the cache row
+ *   [ c / sqrt(mean(c^2) + eps) * latent_weight | rot(r, pos) ]
+ * from ckv[t] = [c | r], rounded to bf16 once, in its slot of the pool; and
+ * the rotary part of every query head is rotated, rot(q_rope[t][h], pos), into
+ * q_rope_out. rot turns pair (i, i + 32) of the 64 by pos * theta^(-i / 32).
+ *   ckv        device bf16, row t at ckv + t * ckv_stride elements, L + 64 long
+ *   q_rope     device bf16, head h of token t at t * q_token_stride +
+ *              h * q_head_stride elements, 64 long; or NULL (then q_rope_out
+ *              is NULL too): only the cache is written
+ *   q_rope_out likewise with qo_token_stride and qo_head_stride; it may be
+ *              q_rope itself with the same strides, and must not overlap it or
+ *              itself in any other way
+ *   cu_new, past_lens, pages, pool  as kv_cache_write
+ * All strides are multiples of 8 elements, ckv_stride >= L + 64, query strides
+ * >= 64 (PSW_EINVAL_STRIDE). Other errors as qkv_norm_rope_cache_write.
+ */
+PSW_API int latent_norm_rope_cache_write(
+    const psw_latent_t *layer, const psw_latent_norm_t *norm, const void *ckv, int64_t ckv_stride,
+    const void *q_rope, int64_t q_token_stride, int64_t q_head_stride, const int32_t *cu_new,
+    const int32_t *past_lens, int32_t n_seqs, const psw_pages_t *pages, void *q_rope_out,
+    int64_t qo_token_stride, int64_t qo_head_stride, void *pool, psw_stream_t stream);
+
+/* The same into FP8 pages: pool8 uint8 [num_blocks][16][L + 64] of E4M3 codes
+ * and row_scale fp32 [num_blocks][16], one scale per row by the rule of
+ * kv_cache_write_fp8 applied to the row's fp32 values (amax over all L + 64,
+ * rounded once, to the code). */
+PSW_API int latent_norm_rope_cache_write_fp8(
+    const psw_latent_t *layer, const psw_latent_norm_t *norm, const void *ckv, int64_t ckv_stride,
+    const void *q_rope, int64_t q_token_stride, int64_t q_head_stride, const int32_t *cu_new,
+    const int32_t *past_lens, int32_t n_seqs, const psw_pages_t *pages, void *q_rope_out,
+    int64_t qo_token_stride, int64_t qo_head_stride, void *pool8, float *row_scale,
+    psw_stream_t stream);
+
+/*
+ * Absorbed latent attention of one new token per sequence over its pages.
+ *   q         device bf16 [n_seqs][n_heads][L + 64], the absorbed queries
+ *   pool      device bf16 [num_blocks][16][L + 64]
+ *   seq_lens  device int32 [n_seqs], the new token's row included; 0 gives a
+ *             zero row and lse = -inf
+ *   out       device bf16 [n_seqs][n_heads][L]
+ *   lse       device fp32 [n_seqs][n_heads] or NULL
+ *   ws        device workspace, 16-byte aligned, of ws_bytes >=
+ *             psw_latent_workspace_bytes(layer, n_seqs)
+ * A page whose block id is outside the pool reads as zero rows and is flagged
+ * (PSW_DEVERR_BLOCK_ID); a length beyond the table row is clamped and flagged.
+ */
+PSW_API int attn_decode_latent(const psw_latent_t *layer, const void *q, const void *pool,
+                               const psw_pages_t *pages, const int32_t *seq_lens, int32_t n_seqs,
+                               void *out, float *lse, void *ws, size_t ws_bytes,
+                               psw_stream_t stream);
+
+/* The same over FP8 pages (row_scale device fp32 [num_blocks][16]). */
+PSW_API int attn_decode_latent_fp8(const psw_latent_t *layer, const void *q, const void *pool8,
+                                   const float *row_scale, const psw_pages_t *pages,
+                                   const int32_t *seq_lens, int32_t n_seqs, void *out, float *lse,
+                                   void *ws, size_t ws_bytes, psw_stream_t stream);
+
+/*
+ * Reads cached rows back and expands them: output row t of sequence b
+ * (cu_k[b] <= t < cu_k[b+1]) is position k_first[b] + (t - cu_k[b]):
+ *   kv[t][h][e] = sum_l c_l w[h][e][l]   (256 per head: 128 key, 128 value)
+ *   k_rope[t]   = r
+ *   cu_k      device int32 [n_seqs + 1], non-decreasing, cu_k[n_seqs] <= n_k_total
+ *   k_first   device int32 [n_seqs], first position wanted, or NULL (all 0);
+ *             a sliding layer needs only the keys its chunk can see
+ *   n_k_total host: rows of kv and k_rope; rows at or beyond cu_k[n_seqs] are
+ *             left as they were
+ *   w         device bf16 [n_heads][256][L]
+ *   kv        device bf16 [n_k_total][n_heads][256]
+ *   k_rope    device bf16 [n_k_total][64]
+ * A row whose page has a bad block id or lies beyond the table row becomes
+ * zero and is flagged; a sequence with a negative k_first is flagged
+ * (PSW_DEVERR_LENGTH) and its rows are zero.
+ */
+PSW_API int latent_kv_expand(const psw_latent_t *layer, const void *pool, const psw_pages_t *pages,
+                             const int32_t *cu_k, const int32_t *k_first, int32_t n_seqs,
+                             int32_t n_k_total, const void *w, void *kv, void *k_rope,
+                             psw_stream_t stream);
+
+/* The same from FP8 pages: c and r are code * row_scale. */
+PSW_API int latent_kv_expand_fp8(const psw_latent_t *layer, const void *pool8,
+                                 const float *row_scale, const psw_pages_t *pages,
+                                 const int32_t *cu_k, const int32_t *k_first, int32_t n_seqs,
+                                 int32_t n_k_total, const void *w, void *kv, void *k_rope,
+                                 psw_stream_t stream);
+
+/*
+ * Expanded latent attention of a chunk of queries per sequence over expanded
+ * keys and values (latent_kv_expand): chunk row i = t - cu_q[b] sits at
+ * position past_lens[b] + i; key row j = u - cu_k[b] at k_first[b] + j (k_first
+ * NULL: j). Visible: key position <= row position, and closer than the window.
+ *   q       device bf16 [n_q_total][n_heads][128 + 64]
+ *   cu_q, past_lens, n_q_total, max_q_len  as attn_prefill_chunked
+ *   kv, k_rope, cu_k, k_first, n_k_total   as latent_kv_expand
+ *   out     device bf16 [n_q_total][n_heads][128]; lse fp32 [n_q_total][n_heads] or NULL
+ * kv and k_rope may be NULL when n_k_total is 0.
+ * A row that sees no key gives zeros and lse = -inf. Rows of q beyond
+ * cu_q[n_seqs] are left as they were. Needs no workspace; n_seqs <= 65535.
+ */
+PSW_API int attn_prefill_latent(const psw_latent_t *layer, const void *q, const int32_t *cu_q,
+                                const int32_t *past_lens, int32_t n_seqs, int32_t n_q_total,
+                                int32_t max_q_len, const void *kv, const void *k_rope,
+                                const int32_t *cu_k, const int32_t *k_first, int32_t n_k_total,
+                                void *out, float *lse, psw_stream_t stream);
 
 /*
  * Layer types of a hybrid stack and its KV-sharing map. Host arithmetic only

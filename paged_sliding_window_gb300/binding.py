@@ -24,6 +24,7 @@ ERRORS = {
     -11: "PSW_ECAPACITY", -12: "PSW_EALIGN", -13: "PSW_EDEVICE", -14: "PSW_ELAUNCH",
     -15: "PSW_ETENSORMAP", -16: "PSW_ESCRATCH", -17: "PSW_EINVAL_ROPE",
     -18: "PSW_EINVAL_LAYERS", -19: "PSW_ENOBLOCKS", -20: "PSW_EBLOCK",
+    -21: "PSW_EINVAL_STRIDE",
 }
 DEVERR_BLOCK_ID, DEVERR_CAPACITY, DEVERR_LENGTH, DEVERR_PIPELINE = 1, 2, 4, 8
 EXPORTED = ("psw_workspace_bytes", "kv_cache_write", "attn_decode_paged",
@@ -33,7 +34,10 @@ EXPORTED = ("psw_workspace_bytes", "kv_cache_write", "attn_decode_paged",
             "psw_block_pool_allocate", "psw_block_pool_free", "psw_block_pool_get_cached",
             "psw_block_pool_cache", "psw_block_pool_ref_count", "psw_block_hash",
             "psw_block_pool_admit", "psw_block_pool_commit", "kv_cache_write_fp8",
-            "attn_decode_paged_fp8", "psw_testing_stall", "attn_decode_paged_append")
+            "attn_decode_paged_fp8", "psw_testing_stall", "attn_decode_paged_append",
+            "psw_latent_workspace_bytes", "latent_norm_rope_cache_write",
+            "latent_norm_rope_cache_write_fp8", "attn_decode_latent", "attn_decode_latent_fp8",
+            "latent_kv_expand", "latent_kv_expand_fp8", "attn_prefill_latent")
 
 
 class PswLayer(ctypes.Structure):
@@ -52,6 +56,19 @@ class PswNormRope(ctypes.Structure):
     _fields_ = [("theta", ctypes.c_float), ("partial_rotary_factor", ctypes.c_float),
                 ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
                 ("k_weight", ctypes.c_void_p), ("v_weight", ctypes.c_void_p)]
+
+
+class PswLatent(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("latent_dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("nope_dim", ctypes.c_int32),
+                ("v_dim", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("softcap", ctypes.c_float), ("scale", ctypes.c_float),
+                ("block_size", ctypes.c_int32)]
+
+
+class PswLatentNorm(ctypes.Structure):
+    _fields_ = [("theta", ctypes.c_float), ("eps", ctypes.c_float),
+                ("latent_weight", ctypes.c_void_p)]
 
 
 class PswError(RuntimeError):
@@ -124,6 +141,22 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.attn_decode_paged_append.argtypes = [lp, vp, vp, vp, vp, vp, pp, vp, i32, vp, vp, vp,
                                                  sz, vp]
         lib.attn_decode_paged_append.restype = ctypes.c_int
+        zp, zn = ctypes.POINTER(PswLatent), ctypes.POINTER(PswLatentNorm)
+        lib.psw_latent_workspace_bytes.argtypes = [zp, i32, ctypes.POINTER(sz)]
+        write = [zp, zn, vp, i64, vp, i64, i64, vp, vp, i32, pp, vp, i64, i64, vp]
+        lib.latent_norm_rope_cache_write.argtypes = write + [vp]
+        lib.latent_norm_rope_cache_write_fp8.argtypes = write + [vp, vp]
+        lib.attn_decode_latent.argtypes = [zp, vp, vp, pp, vp, i32, vp, vp, vp, sz, vp]
+        lib.attn_decode_latent_fp8.argtypes = [zp, vp, vp, vp, pp, vp, i32, vp, vp, vp, sz, vp]
+        lib.latent_kv_expand.argtypes = [zp, vp, pp, vp, vp, i32, i32, vp, vp, vp, vp]
+        lib.latent_kv_expand_fp8.argtypes = [zp, vp, vp, pp, vp, vp, i32, i32, vp, vp, vp, vp]
+        lib.attn_prefill_latent.argtypes = [zp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, i32, vp,
+                                            vp, vp]
+        for name in ("psw_latent_workspace_bytes", "latent_norm_rope_cache_write",
+                     "latent_norm_rope_cache_write_fp8", "attn_decode_latent",
+                     "attn_decode_latent_fp8", "latent_kv_expand", "latent_kv_expand_fp8",
+                     "attn_prefill_latent"):
+            getattr(lib, name).restype = ctypes.c_int
         lib.psw_testing_stall.argtypes = [i32, i32, i32]
         lib.psw_testing_stall.restype = ctypes.c_int
         lib.psw_get_error.argtypes = [vp, ctypes.POINTER(i32)]
@@ -355,6 +388,259 @@ def qkv_norm_rope_cache_write(layer, rn: PswNormRope, q, k, v, cu_new, past_lens
         None if pages is None else ctypes.byref(pages), _ptr(q_out), _ptr(k_pool), _ptr(v_pool),
         _stream(stream))
     _raise(rc, "qkv_norm_rope_cache_write")
+
+
+# ---------------------------------------------------------------- latent attention
+_LATENT_STRUCTS: dict = {}
+
+
+def make_latent_layer(layer) -> PswLatent:
+    """From any object with the psw_latent_t fields (e.g. workloads.LatentLayer)."""
+    if isinstance(layer, PswLatent):
+        return layer
+    key = (int(layer.n_heads), int(layer.latent_dim), int(layer.rope_dim), int(layer.nope_dim),
+           int(layer.v_dim), int(layer.window), float(layer.softcap), float(layer.scale),
+           int(getattr(layer, "block_size", 16)))
+    got = _LATENT_STRUCTS.get(key)
+    if got is None:
+        if len(_LATENT_STRUCTS) >= 1024:
+            _LATENT_STRUCTS.clear()
+        got = _LATENT_STRUCTS[key] = PswLatent(*key)
+    return got
+
+
+def make_latent_norm(theta: float = 1e4, eps: float = 1e-6, latent_weight=None) -> PswLatentNorm:
+    """psw_latent_norm_t from a device fp32 weight of latent_dim values (or None)."""
+    _check(latent_weight, torch.float32, "latent_weight")
+    norm = PswLatentNorm(float(theta), float(eps),
+                         None if latent_weight is None else latent_weight.data_ptr())
+    norm.weight = latent_weight  # keeps the tensor alive as long as its address is held
+    return norm
+
+
+def latent_workspace_bytes(layer, n_seqs: int) -> int:
+    out = ctypes.c_size_t(0)
+    _raise(load().psw_latent_workspace_bytes(ctypes.byref(make_latent_layer(layer)), int(n_seqs),
+                                             ctypes.byref(out)), "psw_latent_workspace_bytes")
+    return int(out.value)
+
+
+def alloc_latent_workspace(layer, n_seqs: int, device="cuda") -> torch.Tensor:
+    """A caller-owned workspace for attn_decode_latent(_fp8); it needs no zeroing."""
+    return torch.empty(max(latent_workspace_bytes(layer, n_seqs), 256), dtype=torch.uint8,
+                       device=device)
+
+
+def _want(t, dtype, shape, name, device, strided=False):
+    """Checks one tensor: dtype, device, shape (None: any extent), contiguity (`strided`: the
+    last dimension alone)."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda or t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor on device {device}")
+    have = t.shape
+    if len(have) != len(shape) or any(n is not None and n != m for n, m in zip(shape, have)):
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(have)}")
+    if strided:
+        if have[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must be contiguous in its last dimension")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _stream_of(device, stream):
+    """The stream of a call on `device`, which must be the current device (as for every call:
+    the library launches there)."""
+    if device != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on device {device}, the current device is "
+                         f"{torch.cuda.current_device()}")
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _strides(t):
+    """Strides of all but the last dimension; a dimension of extent 1 gets that of packed rows
+    (torch leaves any number there)."""
+    st, packed = list(t.stride()), 1
+    for d in range(t.dim() - 1, -1, -1):
+        if t.shape[d] == 1:
+            st[d] = packed
+        packed = max(packed, st[d] * t.shape[d])
+    return st[:-1]
+
+
+_I32, _F32, _BF16, _U8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
+
+
+def _latent_write(name, layer, norm, ckv, q_rope, cu_new, past_lens, pages, q_rope_out, pool,
+                  row_scale, stream):
+    z = make_latent_layer(layer)
+    row, dev = z.latent_dim + z.rope_dim, ckv.get_device()
+    n_seqs, n_tok = past_lens.shape[0], ckv.shape[0]
+    _want(ckv, _BF16, (None, row), "ckv", dev, strided=True)
+    _want(cu_new, _I32, (n_seqs + 1,), "cu_new", dev)
+    _want(past_lens, _I32, (n_seqs,), "past_lens", dev)
+    _want(pool, _BF16 if row_scale is None else _U8, (pages.num_blocks, 16, row), "pool", dev)
+    if norm.latent_weight and getattr(norm, "weight", None) is not None:
+        _want(norm.weight, _F32, (z.latent_dim,), "latent_weight", dev)
+    if (q_rope is None) != (q_rope_out is None):
+        raise ValueError("q_rope and q_rope_out go together")
+    q_args, qo_args = (None, 0, 0), (None, 0, 0)
+    if q_rope is not None:
+        shape = (n_tok, z.n_heads, z.rope_dim)
+        _want(q_rope, _BF16, shape, "q_rope", dev, strided=True)
+        _want(q_rope_out, _BF16, shape, "q_rope_out", dev, strided=True)
+        q_args = (q_rope.data_ptr(), *_strides(q_rope))
+        qo_args = (q_rope_out.data_ptr(), *_strides(q_rope_out))
+    tail = [pool.data_ptr()]
+    if row_scale is not None:
+        _want(row_scale, _F32, (pages.num_blocks, 16), "row_scale", dev)
+        tail.append(row_scale.data_ptr())
+    if n_tok == 0 or n_seqs == 0:
+        return
+    rc = getattr(load(), name)(ctypes.byref(z), ctypes.byref(norm), ckv.data_ptr(), *_strides(ckv),
+                               *q_args, cu_new.data_ptr(), past_lens.data_ptr(), n_seqs,
+                               ctypes.byref(pages), *qo_args, *tail, _stream_of(dev, stream))
+    if rc:
+        _raise(rc, name)
+
+
+def latent_norm_rope_cache_write(layer, norm: PswLatentNorm, ckv, q_rope, cu_new, past_lens,
+                                 pages: PswPages, q_rope_out, pool, stream=None) -> None:
+    """Norm, rotation and cache write of new latent rows. ckv bf16 [n, latent_dim + 64] (rows may
+    be strided, n = cu_new[n_seqs] at least); q_rope and q_rope_out bf16 [n, heads, 64] views of
+    any token and head stride (in place is fine), or both None."""
+    _latent_write("latent_norm_rope_cache_write", layer, norm, ckv, q_rope, cu_new, past_lens,
+                  pages, q_rope_out, pool, None, stream)
+
+
+def latent_norm_rope_cache_write_fp8(layer, norm: PswLatentNorm, ckv, q_rope, cu_new, past_lens,
+                                     pages: PswPages, q_rope_out, pool8, row_scale,
+                                     stream=None) -> None:
+    """The same into FP8 pages: pool8 uint8 [num_blocks, 16, latent_dim + 64] of E4M3 codes,
+    row_scale fp32 [num_blocks, 16]."""
+    if row_scale is None:
+        raise ValueError("row_scale is required")
+    _latent_write("latent_norm_rope_cache_write_fp8", layer, norm, ckv, q_rope, cu_new, past_lens,
+                  pages, q_rope_out, pool8, row_scale, stream)
+
+
+def _latent_decode(name, layer, q, pool, row_scale, pages, seq_lens, out, lse, ws, stream):
+    z = make_latent_layer(layer)
+    row, dev, n_seqs = z.latent_dim + z.rope_dim, q.get_device(), seq_lens.shape[0]
+    _want(q, _BF16, (n_seqs, z.n_heads, row), "q", dev)
+    _want(pool, _BF16 if row_scale is None else _U8, (pages.num_blocks, 16, row), "pool", dev)
+    _want(seq_lens, _I32, (n_seqs,), "seq_lens", dev)
+    _want(out, _BF16, (n_seqs, z.n_heads, z.latent_dim), "out", dev)
+    if lse is not None:
+        _want(lse, _F32, (n_seqs, z.n_heads), "lse", dev)
+    pools = [pool.data_ptr()]
+    if row_scale is not None:
+        _want(row_scale, _F32, (pages.num_blocks, 16), "row_scale", dev)
+        pools.append(row_scale.data_ptr())
+    ws_ptr, ws_bytes = None, 0
+    if ws is not None:
+        if not ws.is_cuda or ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be a contiguous CUDA tensor on device {dev}")
+        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    if n_seqs == 0:
+        return
+    rc = getattr(load(), name)(ctypes.byref(z), q.data_ptr(), *pools, ctypes.byref(pages),
+                               seq_lens.data_ptr(), n_seqs, out.data_ptr(),
+                               None if lse is None else lse.data_ptr(), ws_ptr, ws_bytes,
+                               _stream_of(dev, stream))
+    if rc:
+        _raise(rc, name)
+
+
+def attn_decode_latent(layer, q, pool, pages: PswPages, seq_lens, out, lse=None, ws=None,
+                       stream=None) -> None:
+    """Absorbed latent attention of one token per sequence: q bf16 [n, heads, latent_dim + 64],
+    out bf16 [n, heads, latent_dim], lse fp32 [n, heads] or None; ws from
+    alloc_latent_workspace (calls that may overlap on the GPU need one each)."""
+    _latent_decode("attn_decode_latent", layer, q, pool, None, pages, seq_lens, out, lse, ws,
+                   stream)
+
+
+def attn_decode_latent_fp8(layer, q, pool8, row_scale, pages: PswPages, seq_lens, out, lse=None,
+                           ws=None, stream=None) -> None:
+    """attn_decode_latent over FP8 pages."""
+    if row_scale is None:
+        raise ValueError("row_scale is required")
+    _latent_decode("attn_decode_latent_fp8", layer, q, pool8, row_scale, pages, seq_lens, out,
+                   lse, ws, stream)
+
+
+def _latent_expand(name, layer, pool, row_scale, pages, cu_k, w, kv, k_rope, k_first, stream):
+    z = make_latent_layer(layer)
+    row, dev = z.latent_dim + z.rope_dim, pool.get_device()
+    n_seqs, n_k, e = cu_k.shape[0] - 1, kv.shape[0], z.nope_dim + z.v_dim
+    _want(pool, _BF16 if row_scale is None else _U8, (pages.num_blocks, 16, row), "pool", dev)
+    _want(cu_k, _I32, (n_seqs + 1,), "cu_k", dev)
+    _want(w, _BF16, (z.n_heads, e, z.latent_dim), "w", dev)
+    _want(kv, _BF16, (n_k, z.n_heads, e), "kv", dev)
+    _want(k_rope, _BF16, (n_k, z.rope_dim), "k_rope", dev)
+    if k_first is not None:
+        _want(k_first, _I32, (n_seqs,), "k_first", dev)
+    pools = [pool.data_ptr()]
+    if row_scale is not None:
+        _want(row_scale, _F32, (pages.num_blocks, 16), "row_scale", dev)
+        pools.append(row_scale.data_ptr())
+    if n_k == 0 or n_seqs == 0:
+        return
+    rc = getattr(load(), name)(ctypes.byref(z), *pools, ctypes.byref(pages), cu_k.data_ptr(),
+                               None if k_first is None else k_first.data_ptr(), n_seqs, n_k,
+                               w.data_ptr(), kv.data_ptr(), k_rope.data_ptr(),
+                               _stream_of(dev, stream))
+    if rc:
+        _raise(rc, name)
+
+
+def latent_kv_expand(layer, pool, pages: PswPages, cu_k, w, kv, k_rope, k_first=None,
+                     stream=None) -> None:
+    """Expands cached rows: kv bf16 [n_k, heads, 256] (128 key, 128 value components) from
+    w bf16 [heads, 256, latent_dim], k_rope bf16 [n_k, 64]; row cu_k[b] + j of sequence b is
+    position k_first[b] + j (k_first None: j)."""
+    _latent_expand("latent_kv_expand", layer, pool, None, pages, cu_k, w, kv, k_rope, k_first,
+                   stream)
+
+
+def latent_kv_expand_fp8(layer, pool8, row_scale, pages: PswPages, cu_k, w, kv, k_rope,
+                         k_first=None, stream=None) -> None:
+    """latent_kv_expand from FP8 pages."""
+    if row_scale is None:
+        raise ValueError("row_scale is required")
+    _latent_expand("latent_kv_expand_fp8", layer, pool8, row_scale, pages, cu_k, w, kv, k_rope,
+                   k_first, stream)
+
+
+def attn_prefill_latent(layer, q, cu_q, past_lens, max_q_len: int, kv, k_rope, cu_k, out,
+                        lse=None, k_first=None, stream=None) -> None:
+    """Expanded latent attention of a chunk per sequence: q bf16 [n_q, heads, 192], kv and k_rope
+    from latent_kv_expand, out bf16 [n_q, heads, 128], lse fp32 [n_q, heads] or None."""
+    z = make_latent_layer(layer)
+    dev, n_seqs, n_q, n_k = q.get_device(), past_lens.shape[0], q.shape[0], kv.shape[0]
+    _want(q, _BF16, (n_q, z.n_heads, z.nope_dim + z.rope_dim), "q", dev)
+    _want(cu_q, _I32, (n_seqs + 1,), "cu_q", dev)
+    _want(past_lens, _I32, (n_seqs,), "past_lens", dev)
+    _want(kv, _BF16, (n_k, z.n_heads, z.nope_dim + z.v_dim), "kv", dev)
+    _want(k_rope, _BF16, (n_k, z.rope_dim), "k_rope", dev)
+    _want(cu_k, _I32, (n_seqs + 1,), "cu_k", dev)
+    _want(out, _BF16, (n_q, z.n_heads, z.v_dim), "out", dev)
+    if lse is not None:
+        _want(lse, _F32, (n_q, z.n_heads), "lse", dev)
+    if k_first is not None:
+        _want(k_first, _I32, (n_seqs,), "k_first", dev)
+    if n_q == 0 or n_seqs == 0:
+        return
+    rc = load().attn_prefill_latent(ctypes.byref(z), q.data_ptr(), cu_q.data_ptr(),
+                                    past_lens.data_ptr(), n_seqs, n_q, int(max_q_len),
+                                    kv.data_ptr() or None, k_rope.data_ptr() or None,
+                                    cu_k.data_ptr(),
+                                    None if k_first is None else k_first.data_ptr(), n_k,
+                                    out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                    _stream_of(dev, stream))
+    if rc:
+        _raise(rc, "attn_prefill_latent")
 
 
 def kv_share_map(n_layers: int, pattern: int, n_shared: int = 0):

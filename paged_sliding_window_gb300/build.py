@@ -19,8 +19,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpsw.so")
 SOURCES = ["api.cu", "kv_cache_write.cu", "decode.cu", "decode_noalloc.cu", "prefill.cu",
-           "norm_rope.cu", "block_pool.cpp"]
-HEADERS = ["ptx.cuh", "psw_internal.h"]
+           "norm_rope.cu", "latent_api.cu", "latent_cache.cu", "latent_decode.cu",
+           "latent_expand.cu", "latent_prefill.cu", "block_pool.cpp"]
+HEADERS = ["ptx.cuh", "latent.cuh", "psw_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -93,6 +93,8 @@ int check_layer(const psw_layer_t* layer, LayerArgs* out) {
   return PSW_OK;
 }
 
+}  // namespace
+
 int check_pages(const psw_pages_t* pages) {
   if (pages == nullptr || pages->block_table == nullptr) return PSW_ENULL;
   if (pages->max_blocks_per_seq <= 0 || pages->num_blocks <= 0) return PSW_ECAPACITY;
@@ -102,6 +104,8 @@ int check_pages(const psw_pages_t* pages) {
     return PSW_ECAPACITY;
   return PSW_OK;
 }
+
+namespace {
 
 // k_eq_v: V must be absent; otherwise present.
 int check_v(const LayerArgs& L, const void* v_ptr) {
@@ -251,6 +255,25 @@ int make_query_tensor_map(CUtensorMap* map, const void* q, int n_q_total, int n_
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides,
                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PSW_OK : PSW_ETENSORMAP;
+}
+
+int make_map_3d(CUtensorMap* map, bool bytes, const void* base, const int64_t (&dims)[3],
+                const int64_t (&strides)[2], const int (&box)[3]) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return PSW_ETENSORMAP;
+  const cuuint64_t d[3] = {static_cast<cuuint64_t>(dims[0]), static_cast<cuuint64_t>(dims[1]),
+                           static_cast<cuuint64_t>(dims[2])};
+  const cuuint64_t st[2] = {static_cast<cuuint64_t>(strides[0]),
+                            static_cast<cuuint64_t>(strides[1])};
+  const cuuint32_t bx[3] = {static_cast<cuuint32_t>(box[0]), static_cast<cuuint32_t>(box[1]),
+                            static_cast<cuuint32_t>(box[2])};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  memset(map, 0, sizeof(*map));
+  CUresult r = enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                   3, const_cast<void*>(base), d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? PSW_OK : PSW_ETENSORMAP;
 }
 
@@ -568,8 +591,12 @@ const char* psw_strerror(int code) {
   switch (code) {
     case PSW_OK: return "ok";
     case PSW_ENULL: return "a required pointer is NULL";
-    case PSW_EINVAL_HEADS: return "n_q_heads must be a positive multiple of n_kv_heads";
-    case PSW_EINVAL_HDIM: return "head_dim must be 256 or 512";
+    case PSW_EINVAL_HEADS:
+      return "n_q_heads must be a positive multiple of n_kv_heads (latent layers: n_heads in "
+             "[1, 128])";
+    case PSW_EINVAL_HDIM:
+      return "head_dim must be 256 or 512 (latent layers: latent_dim 256 or 512, rope_dim 64, "
+             "nope_dim and v_dim 128)";
     case PSW_EINVAL_SOFTCAP: return "softcap must be finite and >= 0 (0 = off)";
     case PSW_EINVAL_WINDOW: return "window must be >= 0 (0 = full attention)";
     case PSW_EINVAL_BLOCKSIZE: return "block_size must be 16";
@@ -589,6 +616,8 @@ const char* psw_strerror(int code) {
     case PSW_EINVAL_LAYERS:
       return "n_layers and pattern must be > 0, n_shared in [0, n_layers), and every shared "
              "layer needs a cache-owning layer of its type";
+    case PSW_EINVAL_STRIDE:
+      return "strides must be multiples of 8 elements and at least one row (or head) long";
     case PSW_EINVAL_ROPE:
       return "theta must be > 0, partial_rotary_factor in (0, 1], eps >= 0, all finite";
     default: return "unknown error";

@@ -42,6 +42,9 @@ int check_decode_args(const psw_layer_t* layer, const void* q, const void* k_poo
                       const void* v_pool, const psw_pages_t* pages, const int32_t* seq_lens,
                       int32_t n_seqs, const float* out, LayerArgs* L);
 
+// Host checks of a page table argument. Returns a PSW_* code.
+int check_pages(const psw_pages_t* pages);
+
 // Current device's properties (cached per device).
 cudaError_t device_info(DeviceInfo* info);
 
@@ -148,5 +151,57 @@ int make_pool_tensor_map(CUtensorMap* map, const void* pool, int64_t num_blocks,
 // [chunk][box_slots rows][128 B].
 int make_pool_page_map(CUtensorMap* map, const void* pool, int64_t num_blocks, int n_kv, int hd,
                        int box_slots, int box_chunks);
+
+// 3-D TMA descriptor, 128-byte swizzle, of bf16 elements (or of single bytes):
+// dims innermost first, strides in bytes of dims 1 and 2. Returns a PSW_* code.
+int make_map_3d(CUtensorMap* map, bool bytes, const void* base, const int64_t (&dims)[3],
+                const int64_t (&strides)[2], const int (&box)[3]);
+
+// ---- latent attention (latent_*.cu)
+constexpr int kLatentRope = 64;  // rotated key values shared by every head
+constexpr int kLatentNope = 128, kLatentV = 128;
+constexpr int kLatentKv = kLatentNope + kLatentV;  // expanded components per head
+
+struct LatentArgs {
+  int n_heads, latent, window;
+  float softcap, scale;
+  int row() const { return latent + kLatentRope; }
+};
+
+struct LatentRows {  // strided bf16 rows: element strides
+  const void* in;
+  int64_t in_token, in_head;
+  void* out;
+  int64_t out_token, out_head;
+};
+
+struct LatentPages {
+  const void* pool;        // bf16, or E4M3 codes with row_scale
+  const float* row_scale;  // NULL: bf16 pages
+  const int32_t* block_table;
+  int max_blocks;
+  int64_t num_blocks;
+};
+
+int launch_latent_write(const LatentArgs& L, float theta, float eps, const float* weight,
+                        const void* ckv, int64_t ckv_stride, const LatentRows& q,
+                        const int32_t* cu_new, const int32_t* past_lens, int n_seqs,
+                        const LatentPages& pages, void* pool, float* row_scale, int num_sms,
+                        int32_t* err, cudaStream_t stream);
+
+size_t latent_decode_workspace(const LatentArgs& L, int n_seqs);
+int launch_latent_decode(const LatentArgs& L, const void* q, const LatentPages& pages,
+                         const int32_t* seq_lens, int n_seqs, void* out, float* lse, void* ws,
+                         int num_sms, int32_t* err, cudaStream_t stream);
+
+int launch_latent_expand(const LatentArgs& L, const LatentPages& pages, const int32_t* cu_k,
+                         const int32_t* k_first, int n_seqs, int n_k_total, const void* w,
+                         void* kv, void* k_rope, int num_sms, int32_t* err, cudaStream_t stream);
+
+int launch_latent_prefill(const LatentArgs& L, const void* q, const int32_t* cu_q,
+                          const int32_t* past_lens, int n_seqs, int n_q_total, int max_q_len,
+                          const void* kv, const void* k_rope, const int32_t* cu_k,
+                          const int32_t* k_first, int n_k_total, void* out, float* lse,
+                          int num_sms, int32_t* err, cudaStream_t stream);
 
 }  // namespace psw

@@ -61,6 +61,25 @@ class Layer:
                     scale=self.scale, k_eq_v=int(self.k_eq_v), block_size=self.block_size)
 
 
+@dataclass(frozen=True)
+class LatentLayer:
+    """Parameters of a latent-attention layer (mirrors psw_latent_t)."""
+    n_heads: int
+    latent_dim: int = 512    # 256 or 512
+    rope_dim: int = 64
+    nope_dim: int = 128
+    v_dim: int = 128
+    window: int = 0          # 0 = full attention
+    softcap: float = 0.0     # 0 = off
+    scale: float = 1.0
+    block_size: int = BLOCK_SIZE
+
+    @property
+    def row_dim(self) -> int:
+        """Values of one cache row."""
+        return self.latent_dim + self.rope_dim
+
+
 # --------------------------------------------------------------------------- #
 # value generation
 # --------------------------------------------------------------------------- #
