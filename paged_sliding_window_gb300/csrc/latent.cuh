@@ -52,5 +52,74 @@ __device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
                     pack_bf16x2(y[6], y[7]));
 }
 
+// 2-D view of a pool (or of any rows) as the 3-D map's first two dimensions:
+// one box of shared memory rows at (x, y); z selects within a third dimension.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                                        int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// D[tmem] (+)= A[smem] * B[smem] on E4M3 operands, fp32 accumulators.
+__device__ __forceinline__ void mma_ss_fp8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor of kind::f8f6f4 with E4M3 A and B (format 0), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, int a_mn, int b_mn) {
+  return tc::idesc_bf16_f32(M, N, a_mn, b_mn) & ~((7u << 7) | (7u << 10));
+}
+
+// Whether `p` holds for any of `threads` threads of named barrier `id`.
+__device__ __forceinline__ bool bar_any(uint32_t id, uint32_t threads, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.u32 a, %1, 0;\n\t"
+      "barrier.cta.red.or.pred b, %2, %3, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(p)), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
+// Maximum over a warp (NaN inputs are ignored).
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Warp sums of N values at once (N a power of two up to 32): each round a lane
+// keeps one half of its list and trades the other with its partner; lane l ends
+// with the sum number l / (32 / N).
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&x)[N], int lane) {
+#pragma unroll
+  for (int r = 0; (N >> r) > 1; ++r) {
+    const int n = N >> r, mask = 16 >> r;
+    const bool up = (lane & mask) != 0;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float keep = up ? x[i + n / 2] : x[i], send = up ? x[i] : x[i + n / 2];
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, send, mask);
+    }
+  }
+  float s = x[0];
+#pragma unroll
+  for (int mask = 16 / N; mask > 0; mask >>= 1) s += __shfl_xor_sync(0xffffffffu, s, mask);
+  return s;
+}
+
 }  // namespace lat
 }  // namespace psw

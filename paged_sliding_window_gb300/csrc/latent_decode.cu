@@ -1,102 +1,884 @@
-// latent_decode.cu -- absorbed latent attention of one token per sequence:
-//   s_j = softcap(scale <q, row_j>), out = sum_j softmax(s)_j row_j[:L].
-// One CTA per (sequence, head): tiles of 128 keys, one score per thread, the
-// running maximum and sum of the softmax, then the values L / 128 per thread.
+// latent_decode.cu -- absorbed latent attention of one token per sequence over
+// its pages (split along the context, joined by the log-sum-exp rule).
+//
+// Mathematics, per sequence and head over the visible rows j:
+//   s_j = softcap(scale <q, row_j>),  out = sum_j softmax(s)_j row_j[:L].
+// Each cached row is read once for all heads (a chunk of up to 32), so the
+// call is bound by HBM: 2 (2 L + 64) operations a byte pair and head, 60 a byte
+// at 32 heads. That is far beyond what the CUDA cores and more than what
+// mma.sync sustain beside the loads, so both products run on tcgen05, turned
+// so that the padded operand side is the large one:
+//   S^T [128 keys x heads]  = K Q^T      (A: key rows as stored, K-major)
+//   O^T [128 dims x heads] += V^T P^T    (A: the same rows, read MN-major)
+// with the heads as the N side (16 or 32) and no wasted rows.
+//
+// Precision. bf16 pages: P enters as a bf16 part and the bf16 of the rest, two
+// column groups of one N (the A side is read once for both; one part alone
+// would add as much error as the output's own rounding). FP8 pages: the codes
+// are A as they are. q, times a power of two, is the exact sum of two E4M3
+// parts (8 significant bits), P (times the row's scale over the largest of the
+// segment) is taken in three, 2^-12 relative; again column groups. Row scales
+// multiply scores and P in fp32. Maxima and sums are fp32.
+//
+// Schedule: one CTA per SM. The visible pages of all (sequence, head chunk)
+// units form one list that is cut evenly; a CTA whose piece covers a unit
+// writes the result, the others leave (O, m, l) for latent_merge_kernel. Tiles
+// of 128 keys go through a ring of 16 KB slots (128 rows x 128 B, swizzled): a
+// tile is its rope unit and L / 128 blocks of 128 dims. Warp 4 loads, warp 5
+// issues the MMAs, warps 0-3 do the softmax with a thread per key and the
+// epilogue with a thread per dim. The rope slot of a tile is done with after
+// S, and then holds P, which leaves 2-3 slots more to load ahead.
+// The maximum that P is relative to is taken from a segment's first tile and
+// moved (O rescaled) only when a score exceeds it by 2^64 (bf16, whose P has
+// the range) or 2^4 (E4M3), so a tile costs its threads one barrier.
 #include <cuda_fp8.h>
+#include <math.h>
 
 #include "latent.cuh"
 
 namespace psw {
-namespace {
+namespace ldec {
 
-constexpr int kThreads = 128;
+constexpr int kTile = 128;                      // keys of a tile
+constexpr int kPages = kTile / kBlockSize;      // pages of a tile
+constexpr int kSlotBytes = kTile * 128;
+constexpr int kSoftThreads = 128;               // warps 0-3
+constexpr int kLoadWarp = 4, kMmaWarp = 5;
+constexpr int kThreads = 192;
+constexpr int kMaxCtas = 160;                   // pieces of the page list
+constexpr int kMinPages = 4;                    // pages a piece has at least
+constexpr int kMaxHeads = 32;                   // heads of a chunk
+constexpr int kSmemLimit = 232448;
 
-template <int LAT>
-__global__ void __launch_bounds__(kThreads)
-latent_decode_kernel(const __nv_bfloat16* __restrict__ q, const LatentPages pages,
-                     const int32_t* __restrict__ seq_lens, int heads, int window, float scale,
-                     float softcap, __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
-                     int32_t* err) {
-  constexpr int kRow = LAT + kLatentRope, kPer = LAT / kThreads;
-  __shared__ float s_q[kRow], s_p[kThreads], s_red[kThreads];
-  __shared__ int64_t s_slot[kThreads];
-  const int b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
-  int64_t len = seq_lens[b];
-  int32_t bits = 0;
-  if (len < 0) bits |= PSW_DEVERR_LENGTH, len = 0;
-  if (len > static_cast<int64_t>(pages.max_blocks) * kBlockSize)
-    bits |= PSW_DEVERR_CAPACITY, len = static_cast<int64_t>(pages.max_blocks) * kBlockSize;
-  if (bits != 0 && tid == 0 && h == 0) flag_error(err, bits);
-  const int64_t lo = window > 0 && len > window ? len - window : 0;
-  for (int e = tid; e < kRow; e += kThreads)
-    s_q[e] = __bfloat162float(q[(static_cast<int64_t>(b) * heads + h) * kRow + e]);
-  float m = -INFINITY, l = 0.f, acc[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-  auto value = [&](int64_t slot, int e) -> float {
-    if (slot < 0) return 0.f;
-    if (pages.row_scale != nullptr) {
-      __nv_fp8_e4m3 c;
-      c.__x = static_cast<const uint8_t*>(pages.pool)[slot * kRow + e];
-      return static_cast<float>(c) * pages.row_scale[slot];
-    }
-    return __bfloat162float(static_cast<const __nv_bfloat16*>(pages.pool)[slot * kRow + e]);
-  };
-  for (int64_t j0 = lo; j0 < len; j0 += kThreads) {
-    __syncthreads();
-    const int64_t j = j0 + tid;
-    float s = -INFINITY;
-    if (j < len) {
-      const int32_t blk = pages.block_table[static_cast<int64_t>(b) * pages.max_blocks + j / kBlockSize];
-      const bool ok = blk >= 0 && blk < pages.num_blocks;
-      if (!ok) flag_error(err, PSW_DEVERR_BLOCK_ID);
-      const int64_t slot = ok ? static_cast<int64_t>(blk) * kBlockSize + j % kBlockSize : -1;
-      s_slot[tid] = slot;
-      float d = 0.f;
-      for (int e = 0; e < kRow; ++e) d = fmaf(s_q[e], value(slot, e), d);
-      s = d * scale;
-      if (softcap > 0.f) s = softcap * tanhf(s / softcap);
-    }
-    s_red[tid] = s;
-    __syncthreads();
-    float mt = m;
-    for (int i = 0; i < kThreads; ++i) mt = fmaxf(mt, s_red[i]);
-    const float base = mt == -INFINITY ? 0.f : mt;
-    const float alpha = m == -INFINITY ? 0.f : expf(m - base);
-    s_p[tid] = j < len ? expf(s - base) : 0.f;
-    __syncthreads();
-    m = mt;
-    l *= alpha;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] *= alpha;
-    const int n = static_cast<int>(min(static_cast<int64_t>(kThreads), len - j0));
-    for (int i = 0; i < n; ++i) {
-      l += s_p[i];
-#pragma unroll
-      for (int d = 0; d < kPer; ++d) acc[d] = fmaf(s_p[i], value(s_slot[i], d * kThreads + tid), acc[d]);
-    }
-  }
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-#pragma unroll
-  for (int d = 0; d < kPer; ++d)
-    out[(static_cast<int64_t>(b) * heads + h) * LAT + d * kThreads + tid] =
-        __float2bfloat16_rn(acc[d] * inv);
-  if (lse != nullptr && tid == 0)
-    lse[static_cast<int64_t>(b) * heads + h] = len > 0 ? m + logf(l) : -INFINITY;
+__host__ __device__ inline int chunk_heads(int heads) { return heads <= 16 ? 16 : 32; }
+__host__ __device__ inline int chunks_of(int heads) {
+  return (heads + chunk_heads(heads) - 1) / chunk_heads(heads);
 }
 
-}  // namespace
+template <int LAT, int NH, bool FP8>
+struct Cfg {
+  static constexpr int kElems = FP8 ? 128 : 64;        // row values of a 128-byte slot row
+  static constexpr int kBlocks = LAT / 128;            // 128-dim blocks of the latent
+  static constexpr int kSlotsPerBlock = 128 / kElems;
+  static constexpr int kQParts = FP8 ? 2 : 1, kPParts = FP8 ? 3 : 2;
+  static constexpr int kQRows = NH * kQParts;          // N of S^T
+  static constexpr int kPCols = NH * kPParts;          // N of O^T
+  static constexpr int kQChunks = LAT / kElems + 1;    // 128-byte columns of Q, rope last
+  static constexpr int kQChunkBytes = kQRows * 128;
+  static constexpr int kQBytes = kQChunks * kQChunkBytes;
+  static constexpr int kRopeSteps = FP8 ? 2 : 4;       // 32-byte MMA steps of the rope chunk
+  static constexpr int kPSteps = FP8 ? 4 : 8;          // MMA steps along the keys
+  static constexpr int kPStepBytes = kTile / kPSteps * 128;
+  static constexpr int kMisc = 3072;
+  static constexpr int kSlots = (kSmemLimit - 1024 - kMisc - kQBytes) / kSlotBytes;
+  static constexpr int kSmemBytes = 1024 + kQBytes + kSlots * kSlotBytes + kMisc;
+  static constexpr int kTmemO = FP8 ? 64 : 32;         // S^T columns before it
+  static_assert(kQRows <= kTmemO && kTmemO + kBlocks * kPCols <= 512, "tensor memory columns");
+  static_assert(kSlots >= 1 + kBlocks * kSlotsPerBlock + (kSlotsPerBlock - 1),
+                "a tile fits, a slot left out included");
+  static_assert(kSlots <= 32, "phase bits");
+  // log2 distance by which a score may exceed the maximum in use, and the
+  // largest row scale relative to the one in use; E4M3 P = 16 p v then stays
+  // within 16 * 16 * 1.75 = 448
+  static constexpr float kLag = FP8 ? 4.f : 64.f;
+  static constexpr float kVLag = 1.75f;
+  static constexpr float kPUnit = FP8 ? 16.f : 1.f;
+};
 
-size_t latent_decode_workspace(const LatentArgs& L, int n_seqs) { return 256; }
+struct Misc {
+  uint64_t full[32], empty[32];
+  uint64_t q_full, s_full, p_full, o_full, o_free, drained;
+  int64_t p_begin, p_total;  // this CTA's first page; pages of all units
+  int32_t unit0, page0;      // its unit and the page within
+  int32_t pieces;
+  uint32_t tmem;
+  int32_t abort;
+  int32_t scan[8];
+  int64_t scan64[8];
+  float red[4][kMaxHeads];
+  float vred[4];
+  float qs[kMaxHeads];       // FP8: scale * log2(e) * what a unit of q's codes stands for
+  float lsum[kMaxHeads];
+};
+static_assert(sizeof(Misc) <= 3072, "misc block");
+
+// Visible pages of one sequence.
+struct Span {
+  int len, lo;          // keys [lo, len)
+  int first, count;     // pages
+};
+__device__ __forceinline__ Span span_of(int raw, int window, int max_blocks) {
+  Span s;
+  const int64_t cap = static_cast<int64_t>(max_blocks) * kBlockSize;
+  s.len = raw < 0 ? 0 : (raw > cap ? static_cast<int>(cap) : raw);
+  s.lo = window > 0 && s.len > window ? s.len - window : 0;
+  s.first = s.lo / kBlockSize;
+  s.count = s.len > 0 ? (s.len - 1) / kBlockSize - s.first + 1 : 0;
+  return s;
+}
+
+struct Part {  // what a unit's pieces left behind, per unit: pieces [x, y], x < 0: none
+  int32_t x, y;
+};
+
+// A CTA's segments in order: each role walks them by itself.
+struct Walk {
+  const int32_t* seq_lens;
+  int window, max_blocks, chunks, n_seqs;
+  int64_t left;   // pages of this CTA not yet given out
+  int unit, page; // next unit and the page within it
+  int b, chunk;
+  Span span;
+  int seg_first, seg_count;  // pages of the segment, relative to the span's first
+  __device__ __forceinline__ bool next() {
+    if (left <= 0) return false;
+    for (;; ++unit, page = 0) {
+      b = unit / chunks;
+      if (b >= n_seqs) return false;  // not reached: the list holds `left` more pages
+      chunk = unit - b * chunks;
+      span = span_of(__ldg(seq_lens + b), window, max_blocks);
+      if (page < span.count) break;
+    }
+    seg_first = page;
+    seg_count = static_cast<int>(min(static_cast<int64_t>(span.count - page), left));
+    left -= seg_count;
+    page += seg_count;
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return seg_first == 0 && seg_count == span.count; }
+  __device__ __forceinline__ int tiles() const { return (seg_count + kPages - 1) / kPages; }
+};
+
+// Ring slots in the order of use, and each slot's phase (bit s of `parity`:
+// that of this use). A block of two slots does not wrap: the last slot is then
+// left out, its phase unchanged.
+struct Ring {
+  int pos = 0;
+  uint32_t phase = 0;
+  template <int NS>
+  __device__ __forceinline__ int take(int n, uint32_t& parity) {
+    if (pos + n > NS) pos = 0;
+    const int s = pos;
+    parity = phase;
+    phase ^= ((1u << n) - 1u) << s;
+    pos += n;
+    if (pos == NS) pos = 0;
+    return s;
+  }
+};
+
+// tanh to a few units in the last place of 1, which is what the softcap needs.
+__device__ __forceinline__ float tanh_abs(float y) {
+  const float t = ex2_approx(-2.f * lat::kLog2e * fabsf(y));
+  return copysignf(__fdividef(1.f - t, 1.f + t), y);
+}
+
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 e4m3_values(uint32_t pair) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(pair), __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+template <int LAT, int NH, bool FP8>
+__global__ void __launch_bounds__(kThreads, 1)
+latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
+                     const __grid_constant__ CUtensorMap pool_map, const LatentPages pages,
+                     const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ seq_lens,
+                     int n_seqs, int heads, int window, float scale, float softcap,
+                     __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
+                     Part* __restrict__ parts, float2* __restrict__ part_ml,
+                     float* __restrict__ part_o, int32_t* err) {
+  using C = Cfg<LAT, NH, FP8>;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* q_smem = smem;
+  uint8_t* ring = smem + C::kQBytes;
+  Misc* ms = reinterpret_cast<Misc*>(ring + C::kSlots * kSlotBytes);
+  const int chunks = chunks_of(heads);
+
+  // ---- this CTA's piece of the page list: every CTA adds up all spans (a run
+  // of sequences per thread) and the thread whose run holds its first page
+  // finds the unit
+  const int per = (n_seqs + kThreads - 1) / kThreads;
+  const int b0 = min(n_seqs, tid * per), b1 = min(n_seqs, b0 + per);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int raw = __ldg(seq_lens + b);
+    mine += static_cast<int64_t>(span_of(raw, window, pages.max_blocks).count) * chunks;
+    if (blockIdx.x == 0) {
+      if (raw < 0) flag_error(err, PSW_DEVERR_LENGTH);
+      if (raw > static_cast<int64_t>(pages.max_blocks) * kBlockSize)
+        flag_error(err, PSW_DEVERR_CAPACITY);
+    }
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) ms->scan64[warp] = incl;
+  if (tid == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&ms->full[i], 1);
+      mbar_init(&ms->empty[i], 1);
+    }
+    mbar_init(&ms->q_full, FP8 ? 4 : 1);
+    mbar_init(&ms->s_full, 1);
+    mbar_init(&ms->p_full, 4);
+    mbar_init(&ms->o_full, 1);
+    mbar_init(&ms->o_free, 4);
+    mbar_init(&ms->drained, 1);
+    ms->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tc::alloc(&ms->tmem, 512);
+    tc::relinquish();
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  int64_t total = 0, before = incl - mine;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += ms->scan64[w];
+    total += ms->scan64[w];
+  }
+  const int64_t want = (total + kMinPages - 1) / kMinPages;
+  const int pieces = static_cast<int>(min(static_cast<int64_t>(gridDim.x), want));
+  const int64_t p0 = blockIdx.x < pieces ? total * blockIdx.x / pieces : 0;
+  const int64_t p1 = blockIdx.x < pieces ? total * (blockIdx.x + 1) / pieces : 0;
+  if (p0 < p1 && p0 >= before && p0 < before + mine) {
+    int64_t at = before;
+    for (int b = b0; b < b1; ++b) {
+      const int n = span_of(__ldg(seq_lens + b), window, pages.max_blocks).count;
+      if (p0 < at + static_cast<int64_t>(n) * chunks) {
+        const int c = static_cast<int>((p0 - at) / n);
+        ms->unit0 = b * chunks + c;
+        ms->page0 = static_cast<int>(p0 - at - static_cast<int64_t>(c) * n);
+        break;
+      }
+      at += static_cast<int64_t>(n) * chunks;
+    }
+  }
+  __syncthreads();
+  const uint32_t tmem = ms->tmem;
+  volatile int32_t* abort_flag = &ms->abort;
+  Walk walk;
+  walk.seq_lens = seq_lens;
+  walk.window = window;
+  walk.max_blocks = pages.max_blocks;
+  walk.chunks = chunks;
+  walk.n_seqs = n_seqs;
+  walk.left = p1 - p0;
+  walk.unit = p0 < p1 ? ms->unit0 : 0;
+  walk.page = p0 < p1 ? ms->page0 : 0;
+  Ring rg;
+  bool ok = true;
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0) prefetch_tensormap(&pool_map);
+    const int pg = lane & 7, half = (lane >> 3) & 1;  // page of the tile, slot of a block
+    uint32_t issued = 0;  // slots whose last load may be in flight, for the drain
+    while (ok && walk.next()) {
+      const int32_t* row = pages.block_table + static_cast<int64_t>(walk.b) * pages.max_blocks;
+      auto block_id = [&](int t) -> int {  // of this lane's page of tile t; -1: zero rows
+        const int i = t * kPages + pg;
+        if (i >= walk.seg_count) return -1;
+        const int blk = __ldg(row + walk.span.first + walk.seg_first + i);
+        if (blk >= 0 && blk < pages.num_blocks) return blk;
+        flag_error(err, PSW_DEVERR_BLOCK_ID);
+        return -1;
+      };
+      const int n_tiles = walk.tiles();
+      int next_blk = block_id(0);
+      for (int t = 0; ok && t < n_tiles; ++t) {
+        const int y = next_blk * kBlockSize;
+        if (t + 1 < n_tiles) next_blk = block_id(t + 1);
+        for (int u = 0; u <= C::kBlocks; ++u) {  // rope unit, then the blocks
+          const int n = u == 0 ? 1 : C::kSlotsPerBlock;
+          uint32_t parity;
+          const int s = rg.take<C::kSlots>(n, parity);
+          if (lane < n) {
+            ok = mbar_wait(&ms->empty[s + lane], (parity >> (s + lane) & 1u) ^ 1u) && !*abort_flag;
+            if (ok) mbar_arrive_expect_tx(&ms->full[s + lane], kSlotBytes);
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          issued |= ((1u << n) - 1u) << s;
+          const int x = u == 0 ? LAT : (u - 1) * 128 + half * 64;
+          if (lane < 8 * n)
+            lat::tma_box(smem_u32(ring + (s + half) * kSlotBytes + pg * 2048), &pool_map,
+                         &ms->full[s + half], x, y, 0);
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      flag_error(err, PSW_DEVERR_PIPELINE);
+      // copies in flight land before the CTA ends: the last phase of each slot
+      for (int s = 0; s < C::kSlots; ++s)
+        if (issued >> s & 1u) mbar_wait(&ms->full[s], ((rg.phase >> s) & 1u) ^ 1u);
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMAs
+    if (lane == 0) {
+      const uint32_t id_s = FP8 ? lat::idesc_e4m3_f32(128, C::kQRows, 0, 0)
+                                : tc::idesc_bf16_f32(128, C::kQRows, 0, 0);
+      const uint32_t id_o = FP8 ? lat::idesc_e4m3_f32(128, C::kPCols, 1, 1)
+                                : tc::idesc_bf16_f32(128, C::kPCols, 1, 1);
+      auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+        if (FP8) lat::mma_ss_fp8(d, a, b, id, acc);
+        else tc::mma_ss(d, a, b, id, acc);
+      };
+      const uint64_t q_desc = tc::smem_desc(smem_u32(q_smem), 16, 1024, tc::kSwizzle128B);
+      const uint32_t ring_at = smem_u32(ring);
+      int seg = 0, tile = 0;
+      for (; ok && walk.next(); ++seg) {
+        const int n_tiles = walk.tiles();
+        for (int t = 0; ok && t < n_tiles; ++t, ++tile) {
+          if (t == 0) ok = mbar_wait(&ms->q_full, seg & 1);
+          int slot[1 + C::kBlocks];
+#pragma unroll
+          for (int u = 0; u <= C::kBlocks; ++u) {
+            uint32_t parity;
+            slot[u] = rg.take<C::kSlots>(u == 0 ? 1 : C::kSlotsPerBlock, parity);
+            const int n_ch = u == 0 ? 1 : C::kSlotsPerBlock;
+            const int steps = u == 0 ? C::kRopeSteps : 4;
+            for (int c = 0; c < n_ch; ++c) {
+              ok = ok && mbar_wait(&ms->full[slot[u] + c], parity >> (slot[u] + c) & 1u);
+              if (!ok) break;
+              tc::fence_after();
+              const int qc = u == 0 ? C::kQChunks - 1 : (u - 1) * C::kSlotsPerBlock + c;
+              const uint64_t kd = tc::smem_desc(ring_at + (slot[u] + c) * kSlotBytes, 16, 1024,
+                                                tc::kSwizzle128B);
+              const uint64_t qd = q_desc + static_cast<uint32_t>(qc * C::kQChunkBytes >> 4);
+              for (int k = 0; k < steps; ++k)
+                mma(tmem, kd + k * 2, qd + k * 2, id_s, (u > 0 || k > 0) ? 1u : 0u);
+            }
+          }
+          if (!ok) break;
+          tc::commit(&ms->s_full);
+          ok = mbar_wait(&ms->p_full, tile & 1) &&
+               (t > 0 || seg == 0 || mbar_wait(&ms->o_free, (seg - 1) & 1)) && !*abort_flag;
+          if (!ok) break;
+          tc::fence_after();
+          const uint64_t p_desc =
+              tc::smem_desc(ring_at + slot[0] * kSlotBytes, 1024, 1024, tc::kSwizzle128B);
+#pragma unroll
+          for (int m = 0; m < C::kBlocks; ++m) {
+            const uint64_t v_desc = tc::smem_desc(ring_at + slot[1 + m] * kSlotBytes, kSlotBytes,
+                                                  1024, tc::kSwizzle128B);
+            for (int k = 0; k < C::kPSteps; ++k) {
+              const uint32_t off = static_cast<uint32_t>(k * C::kPStepBytes) >> 4;
+              mma(tmem + C::kTmemO + m * C::kPCols, v_desc + off, p_desc + off, id_o,
+                  (t > 0 || k > 0) ? 1u : 0u);
+            }
+            for (int c = 0; c < C::kSlotsPerBlock; ++c) tc::commit(&ms->empty[slot[1 + m] + c]);
+          }
+          tc::commit(&ms->empty[slot[0]]);
+          if (t == n_tiles - 1) tc::commit(&ms->o_full);
+        }
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        flag_error(err, PSW_DEVERR_PIPELINE);
+      }
+      tc::commit(&ms->drained);  // every MMA has ended before tensor memory is freed
+      mbar_wait(&ms->drained, 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax, epilogue
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const float mul = softcap > 0.f ? scale / softcap : scale * lat::kLog2e;
+    const float cap2 = softcap * lat::kLog2e;
+    auto load_q = [&](const Walk& w) {  // the queries of w's unit, into shared memory
+      const int h0 = w.chunk * NH;
+      if (!FP8) {
+        if (tid == 0) {
+          mbar_arrive_expect_tx(&ms->q_full, C::kQBytes);
+          for (int c = 0; c < C::kQChunks; ++c)
+            lat::tma_box(smem_u32(q_smem + c * C::kQChunkBytes), &q_map, &ms->q_full, c * 64, h0,
+                         w.b);
+        }
+      } else {
+        // warp by warp, a head at a time: its largest value gives the power of
+        // two; the value is the sum of the two parts, the second 16 times up
+        for (int h = warp; h < NH; h += 4) {
+          constexpr int kRow = LAT + kLatentRope, kPairs = kRow / 2;
+          float2 v[(kPairs + 31) / 32];
+          float amax = 0.f;
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(
+              q + (static_cast<int64_t>(w.b) * heads + h0 + h) * kRow);
+#pragma unroll
+          for (int i = 0; i < (kPairs + 31) / 32; ++i) {
+            const int e = i * 32 + lane;
+            v[i] = (h0 + h < heads && e < kPairs) ? unpack_bf16x2(__ldg(src + e)) : make_float2(0.f, 0.f);
+            amax = fmaxf(amax, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
+          }
+          amax = lat::warp_max(amax);
+          // 2^k with amax 2^k in [128, 256): the exponent field of amax, turned
+          const int ex = static_cast<int>(__float_as_uint(amax) >> 23);  // biased, sign 0
+          const int k = max(-126, min(126, 127 + 7 - ex));
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+          // (an infinite query has no such codes: its scores become NaN)
+          if (lane == 0)
+            ms->qs[h] = ex == 255 ? NAN : mul * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+#pragma unroll
+          for (int i = 0; i < (kPairs + 31) / 32; ++i) {
+            const int e = i * 32 + lane;
+            if (e >= kPairs) continue;
+            const float a = v[i].x * up, b = v[i].y * up;
+            const uint32_t hi = e4m3_pair(a, b);
+            const float2 got = e4m3_values(hi);
+            const uint32_t lo = e4m3_pair((a - got.x) * 16.f, (b - got.y) * 16.f);
+            const int byte = 2 * e, c = byte >> 7, in = byte & 127;
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              const int r = part * NH + h;
+              const int at = c * C::kQChunkBytes + r * 128 + ((((in >> 4) ^ (r & 7)) << 4) | (in & 15));
+              *reinterpret_cast<uint16_t*>(q_smem + at) = static_cast<uint16_t>(part == 0 ? hi : lo);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms->q_full);
+      }
+    };
+    int seg = 0, tile = 0;
+    bool more = walk.next();
+    if (more) load_q(walk);
+    for (; ok && more; ++seg) {
+      const Walk w = walk;
+      more = walk.next();
+      const int h0 = w.chunk * NH, nh = min(NH, heads - h0), n_tiles = w.tiles();
+      const int32_t* row = pages.block_table + static_cast<int64_t>(w.b) * pages.max_blocks;
+      auto scale_of = [&](int t) -> float {  // FP8: the row scale of this thread's key of tile t
+        const int i = t * kPages + tid / kBlockSize;
+        if (!FP8 || i >= w.seg_count) return 0.f;
+        const int blk = __ldg(row + w.span.first + w.seg_first + i);
+        return blk >= 0 && blk < pages.num_blocks
+                   ? __ldg(pages.row_scale + static_cast<int64_t>(blk) * kBlockSize + tid % kBlockSize)
+                   : 0.f;
+      };
+      float m[NH], l[NH], vref = 0.f, ks = scale_of(0);
+#pragma unroll
+      for (int h = 0; h < NH; ++h) m[h] = 0.f, l[h] = 0.f;
+      for (int t = 0; t < n_tiles; ++t, ++tile) {
+        const int page = w.span.first + w.seg_first + t * kPages + tid / kBlockSize;
+        const int key = page * kBlockSize + tid % kBlockSize;
+        const bool in_seg = t * kPages + tid / kBlockSize < w.seg_count;
+        const bool seen = in_seg && key >= w.span.lo && key < w.span.len;
+        const float vs = seen ? ks : 0.f;  // a hidden slot's scale may be anything
+        if (t + 1 < n_tiles) ks = scale_of(t + 1);
+        int slot[1 + C::kBlocks];
+#pragma unroll
+        for (int u = 0; u <= C::kBlocks; ++u) {
+          uint32_t parity;
+          slot[u] = rg.take<C::kSlots>(u == 0 ? 1 : C::kSlotsPerBlock, parity);
+        }
+        ok = mbar_wait(&ms->s_full, tile & 1);
+        tc::fence_after();
+        float z[NH];
+        {
+          uint32_t v[C::kQRows];
+#pragma unroll
+          for (int c = 0; c < C::kQRows / 16; ++c)
+            tc::ld16(tmem + lanes + c * 16, *reinterpret_cast<uint32_t(*)[16]>(&v[c * 16]));
+          tc::wait_ld();
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            if (FP8) z[h] = fmaf(__uint_as_float(v[(C::kQParts - 1) * NH + h]), 0.0625f, __uint_as_float(v[h])) * (ms->qs[h] * vs);
+            else z[h] = __uint_as_float(v[h]) * mul;
+          }
+        }
+        if (softcap > 0.f) {
+#pragma unroll
+          for (int h = 0; h < NH; ++h) z[h] = cap2 * tanh_abs(z[h]);
+        }
+#pragma unroll
+        for (int h = 0; h < NH; ++h) z[h] = seen ? z[h] : -INFINITY;
+        // values that must not enter the second product: rows of a page that
+        // hold no visible key (P is 0 there, but 0 times NaN is not)
+        if (in_seg && !seen) {
+#pragma unroll
+          for (int u = 1; u <= C::kBlocks; ++u)
+            for (int c = 0; c < C::kSlotsPerBlock; ++c)
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(ring + (slot[u] + c) * kSlotBytes + tid * 128 + i * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+        }
+        bool move = !ok || t == 0;
+        float over = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) over = fmaxf(over, z[h] - m[h]);
+        move |= over > C::kLag;
+        if (FP8) move |= vs > C::kVLag * vref;
+        if (lat::bar_any(1, kSoftThreads, move)) {
+          // the tile's maxima; the ones in use move to them where they lag
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            const float x = lat::warp_max(z[h]);
+            if (lane == 0) ms->red[warp][h] = x;
+          }
+          if (FP8) {
+            const float x = lat::warp_max(vs);
+            if (lane == 0) ms->vred[warp] = x;
+          }
+          if (lat::bar_any(1, kSoftThreads, !ok)) {
+            ok = false;
+            break;
+          }
+          float vmul = 1.f;
+          if (FP8) {
+            const float x = fmaxf(fmaxf(ms->vred[0], ms->vred[1]), fmaxf(ms->vred[2], ms->vred[3]));
+            if (t == 0 || x > C::kVLag * vref) {
+              const float to = fmaxf(x, 1e-30f);
+              vmul = t == 0 ? 1.f : vref / to;
+              vref = to;
+            }
+          }
+          float alpha[NH];
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            const float x = fmaxf(fmaxf(ms->red[0][h], ms->red[1][h]), fmaxf(ms->red[2][h], ms->red[3][h]));
+            alpha[h] = vmul;
+            if (t == 0) {
+              m[h] = x == -INFINITY ? 0.f : x;
+            } else if (x > m[h] + C::kLag) {
+              const float a = ex2_approx(m[h] - x);
+              alpha[h] *= a;
+              l[h] *= a;
+              m[h] = x;
+            }
+          }
+          if (t > 0) {  // the products before this tile have ended: S came after them
+#pragma unroll 1
+            for (int blk = 0; blk < C::kBlocks; ++blk) {
+#pragma unroll
+              for (int c = 0; c < C::kPCols / 16; ++c) {
+                uint32_t v[16];
+                const uint32_t at = tmem + lanes + C::kTmemO + blk * C::kPCols + c * 16;
+                tc::ld16(at, v);
+                tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha[(c * 16 + i) % NH]);
+                tc::st16(at, v);
+              }
+            }
+            tc::wait_st();
+          }
+          named_bar_sync(1, kSoftThreads);  // red and vred may be written again
+        }
+        // P into the rope slot: this key's row, parts of all heads, 16-byte
+        // vectors swizzled by the row
+        uint8_t* prow = ring + slot[0] * kSlotBytes + tid * 128;
+        const int sw = tid & 7;
+        if (!FP8) {
+#pragma unroll
+          for (int g = 0; g < NH / 8; ++g) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float a = ex2_approx(z[g * 8 + 2 * i] - m[g * 8 + 2 * i]);
+              const float b = ex2_approx(z[g * 8 + 2 * i + 1] - m[g * 8 + 2 * i + 1]);
+              l[g * 8 + 2 * i] += a;
+              l[g * 8 + 2 * i + 1] += b;
+              hi[i] = pack_bf16x2(a, b);
+              const float2 r = unpack_bf16x2(hi[i]);
+              lo[i] = pack_bf16x2(a - r.x, b - r.y);
+            }
+            *reinterpret_cast<uint4*>(prow + ((g ^ sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(prow + (((g + NH / 8) ^ sw) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        } else {
+          const float pv = vs * (C::kPUnit / vref);
+#pragma unroll
+          for (int g = 0; g < NH / 16; ++g) {
+            uint32_t part[3][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w3[3] = {0u, 0u, 0u};
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int h = g * 16 + 4 * i + 2 * j;
+                float a = ex2_approx(z[h] - m[h]), b = ex2_approx(z[h + 1] - m[h + 1]);
+                l[h] += a;
+                l[h + 1] += b;
+                a *= pv;
+                b *= pv;
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {
+                  const uint32_t c = e4m3_pair(a, b);
+                  w3[p] |= c << (16 * j);
+                  const float2 r = e4m3_values(c);
+                  a = (a - r.x) * 16.f;
+                  b = (b - r.y) * 16.f;
+                }
+              }
+#pragma unroll
+              for (int p = 0; p < 3; ++p) part[p][i] = w3[p];
+            }
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+              *reinterpret_cast<uint4*>(prow + (((p * (NH / 16) + g) ^ sw) << 4)) =
+                  make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
+          }
+        }
+        fence_proxy_async_smem();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms->p_full);
+      }
+      if (!ok) break;
+      // ---- the segment's end. S of its last tile is done: Q may be replaced
+      if (more) load_q(walk);
+      {
+        float x[NH];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) x[h] = l[h];
+        const float s = lat::warp_sums<NH>(x, lane);
+        if (lane % (32 / NH) == 0) ms->red[warp][lane / (32 / NH)] = s;
+      }
+      ok = mbar_wait(&ms->o_full, seg & 1);
+      if (lat::bar_any(1, kSoftThreads, !ok)) {
+        ok = false;
+        break;
+      }
+      tc::fence_after();
+      const bool whole = w.whole();
+      const int slot_id = 2 * blockIdx.x + (w.seg_first == 0 ? 1 : 0);
+      if (tid < nh) {  // thread h: the statistics of head h
+        float mh = 0.f;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) mh = h == tid ? m[h] : mh;
+        const float s = ms->red[0][tid] + ms->red[1][tid] + ms->red[2][tid] + ms->red[3][tid];
+        ms->lsum[tid] = whole ? (s == 0.f ? 0.f : 1.f / s) : 1.f;
+        if (whole) {
+          if (lse != nullptr)
+            lse[static_cast<int64_t>(w.b) * heads + h0 + tid] = (mh + __log2f(s)) * lat::kLn2;
+        } else {
+          part_ml[slot_id * kMaxHeads + tid] = make_float2(mh, s);
+        }
+      }
+      if (tid == 0 && w.seg_first == 0) {
+        // first page of the unit: note which pieces share it
+        const int64_t end = p1 - w.left - w.seg_count + w.span.count;  // list end of the unit
+        const int last = static_cast<int>((end * pieces - 1) / total);
+        parts[w.b * chunks + w.chunk] = whole ? Part{-1, -1} : Part{static_cast<int32_t>(blockIdx.x), last};
+      }
+      named_bar_sync(1, kSoftThreads);
+      const float ov = FP8 ? vref / C::kPUnit : 1.f;
+#pragma unroll 1
+      for (int blk = 0; blk < C::kBlocks; ++blk) {
+        const int d = blk * 128 + tid;
+        float o[NH];
+#pragma unroll
+        for (int p = 0; p < C::kPParts; ++p) {
+          uint32_t v[NH];
+#pragma unroll
+          for (int c = 0; c < NH / 16; ++c)
+            tc::ld16(tmem + lanes + C::kTmemO + blk * C::kPCols + p * NH + c * 16,
+                     *reinterpret_cast<uint32_t(*)[16]>(&v[c * 16]));
+          tc::wait_ld();
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            const float x = __uint_as_float(v[h]);
+            o[h] = p == 0 ? x : fmaf(x, FP8 ? (p == 1 ? 0.0625f : 0.00390625f) : 1.f, o[h]);
+          }
+        }
+        if (whole) {
+          __nv_bfloat16* dst = out + (static_cast<int64_t>(w.b) * heads + h0) * LAT + d;
+#pragma unroll
+          for (int h = 0; h < NH; ++h)
+            if (h < nh) dst[h * LAT] = __float2bfloat16_rn(o[h] * (ov * ms->lsum[h]));
+        } else {
+          float* dst = part_o + static_cast<int64_t>(slot_id) * kMaxHeads * LAT + d;
+#pragma unroll
+          for (int h = 0; h < NH; ++h)
+            if (h < nh) dst[h * LAT] = o[h] * ov;
+        }
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms->o_free);
+      named_bar_sync(1, kSoftThreads);  // red and lsum may be written again
+    }
+    if (!ok) {
+      if (tid == 0) {
+        *abort_flag = 1;
+        flag_error(err, PSW_DEVERR_PIPELINE);
+        if (!FP8) mbar_wait(&ms->q_full, seg & 1);  // a query copy in flight lands first
+      }
+    }
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) tc::dealloc(tmem, 512);
+}
+
+// Joins what the pieces of a unit left: out = sum_i 2^(m_i - M) O_i / sum_i
+// 2^(m_i - M) l_i. One CTA per (sequence, head), a thread per L / 128 dims; a
+// unit that one piece covered is left alone, an empty sequence gets its zeros.
+template <int LAT>
+__global__ void __launch_bounds__(128)
+latent_merge_kernel(const int32_t* __restrict__ seq_lens, int heads, int max_blocks,
+                    const Part* __restrict__ parts, const float2* __restrict__ part_ml,
+                    const float* __restrict__ part_o, __nv_bfloat16* __restrict__ out,
+                    float* __restrict__ lse) {
+  constexpr int kPer = LAT / 128;
+  __shared__ float s_w[kMaxCtas], s_red[8];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
+  const int nh = chunk_heads(heads), chunk = h / nh, hc = h - chunk * nh;
+  __nv_bfloat16* dst = out + (static_cast<int64_t>(b) * heads + h) * LAT + tid * kPer;
+  if (seq_lens[b] <= 0) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) dst[i] = __float2bfloat16_rn(0.f);
+    if (lse != nullptr && tid == 0) lse[static_cast<int64_t>(b) * heads + h] = -INFINITY;
+    return;
+  }
+  const Part pt = parts[b * chunks_of(heads) + chunk];
+  if (pt.x < 0) return;
+  const int n = pt.y - pt.x + 1;
+  auto slot = [&](int i) { return i == 0 ? 2 * pt.x + 1 : 2 * (pt.x + i); };
+  float mx = -INFINITY;
+  float2 ml[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = tid + k * 128;
+    ml[k] = i < n ? part_ml[slot(i) * kMaxHeads + hc] : make_float2(-INFINITY, 0.f);
+    mx = fmaxf(mx, ml[k].x);
+  }
+  mx = lat::warp_max(mx);
+  if ((tid & 31) == 0) s_red[tid >> 5] = mx;
+  __syncthreads();
+  mx = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+  float l = 0.f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = tid + k * 128;
+    if (i < n) {
+      const float w = ex2_approx(ml[k].x - mx);
+      s_w[i] = w;
+      l += w * ml[k].y;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if ((tid & 31) == 0) s_red[4 + (tid >> 5)] = l;
+  __syncthreads();
+  l = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
+  float acc[kPer] = {};
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) {
+    const float* src = part_o + (static_cast<int64_t>(slot(i)) * kMaxHeads + hc) * LAT + tid * kPer;
+    const float w = s_w[i];
+    if (kPer == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      acc[0] = fmaf(w, v.x, acc[0]);
+      acc[1] = fmaf(w, v.y, acc[1]);
+      acc[kPer - 2] = fmaf(w, v.z, acc[kPer - 2]);
+      acc[kPer - 1] = fmaf(w, v.w, acc[kPer - 1]);
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(src);
+      acc[0] = fmaf(w, v.x, acc[0]);
+      acc[1] = fmaf(w, v.y, acc[1]);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < kPer; i += 2)
+    *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+  if (lse != nullptr && tid == 0)
+    lse[static_cast<int64_t>(b) * heads + h] = (mx + __log2f(l)) * lat::kLn2;
+}
+
+struct Layout {
+  size_t ml, o, total;
+};
+Layout layout(const LatentArgs& L, int n_seqs) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  Layout y;
+  y.ml = up(sizeof(Part) * static_cast<size_t>(n_seqs) * chunks_of(L.n_heads));
+  y.o = y.ml + up(sizeof(float2) * 2 * kMaxCtas * kMaxHeads);
+  y.total = y.o + sizeof(float) * 2 * kMaxCtas * kMaxHeads * static_cast<size_t>(L.latent);
+  return y;
+}
+
+template <int LAT, int NH, bool FP8>
+int launch(const LatentArgs& L, const void* q, const LatentPages& pages, const int32_t* seq_lens,
+           int n_seqs, void* out, float* lse, void* ws, int num_sms, int32_t* err,
+           cudaStream_t stream) {
+  using C = Cfg<LAT, NH, FP8>;
+  CUtensorMap q_map, pool_map;
+  const int row = L.row();
+  int rc = make_map_3d(&q_map, false, q, {row, L.n_heads, n_seqs},
+                       {int64_t{2} * row, int64_t{2} * row * L.n_heads}, {64, NH, 1});
+  if (rc != PSW_OK) return rc;
+  const int64_t row_bytes = FP8 ? row : 2 * row;
+  rc = make_map_3d(&pool_map, FP8, pages.pool, {row, pages.num_blocks * kBlockSize, 1},
+                   {row_bytes, row_bytes},
+                   {C::kElems, kBlockSize, 1});
+  if (rc != PSW_OK) return rc;
+  auto* kernel = latent_decode_kernel<LAT, NH, FP8>;
+  rc = set_smem_limit(reinterpret_cast<const void*>(kernel), C::kSmemBytes);
+  if (rc != PSW_OK) return rc;
+  const Layout y = layout(L, n_seqs);
+  auto* base = static_cast<uint8_t*>(ws);
+  auto* parts = reinterpret_cast<Part*>(base);
+  auto* ml = reinterpret_cast<float2*>(base + y.ml);
+  auto* o = reinterpret_cast<float*>(base + y.o);
+  auto* ob = static_cast<__nv_bfloat16*>(out);
+  const int grid = num_sms < kMaxCtas ? num_sms : kMaxCtas;
+  kernel<<<grid, kThreads, C::kSmemBytes, stream>>>(
+      q_map, pool_map, pages, static_cast<const __nv_bfloat16*>(q), seq_lens, n_seqs, L.n_heads,
+      L.window, L.scale, L.softcap, ob, lse, parts, ml, o, err);
+  if (cudaGetLastError() != cudaSuccess) return PSW_ELAUNCH;
+  // the join may be launched while the pieces still run; it waits for them
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(n_seqs, L.n_heads);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(
+      &cfg, latent_merge_kernel<LAT>, seq_lens, L.n_heads, pages.max_blocks,
+      static_cast<const Part*>(parts), static_cast<const float2*>(ml),
+      static_cast<const float*>(o), ob, lse);
+  return e == cudaSuccess ? PSW_OK : PSW_ELAUNCH;
+}
+
+}  // namespace ldec
+
+size_t latent_decode_workspace(const LatentArgs& L, int n_seqs) {
+  return ldec::layout(L, n_seqs).total;
+}
 
 int launch_latent_decode(const LatentArgs& L, const void* q, const LatentPages& pages,
                          const int32_t* seq_lens, int n_seqs, void* out, float* lse, void* ws,
                          int num_sms, int32_t* err, cudaStream_t stream) {
-  auto* kernel = L.latent == 512 ? latent_decode_kernel<512> : latent_decode_kernel<256>;
-  kernel<<<dim3(n_seqs, L.n_heads), kThreads, 0, stream>>>(
-      static_cast<const __nv_bfloat16*>(q), pages, seq_lens, L.n_heads, L.window, L.scale,
-      L.softcap, static_cast<__nv_bfloat16*>(out), lse, err);
-  return cudaGetLastError() == cudaSuccess ? PSW_OK : PSW_ELAUNCH;
+#define PSW_PICK(LAT_, NH_)                                                                       \
+  (pages.row_scale != nullptr                                                                     \
+       ? ldec::launch<LAT_, NH_, true>(L, q, pages, seq_lens, n_seqs, out, lse, ws, num_sms, err, \
+                                       stream)                                                    \
+       : ldec::launch<LAT_, NH_, false>(L, q, pages, seq_lens, n_seqs, out, lse, ws, num_sms,     \
+                                        err, stream))
+  const bool few = ldec::chunk_heads(L.n_heads) == 16;
+  if (L.latent == 512) return few ? PSW_PICK(512, 16) : PSW_PICK(512, 32);
+  return few ? PSW_PICK(256, 16) : PSW_PICK(256, 32);
+#undef PSW_PICK
 }
 
 }  // namespace psw
