@@ -93,6 +93,27 @@ __device__ __forceinline__ bool bar_any(uint32_t id, uint32_t threads, bool p) {
   return r != 0;
 }
 
+// True on one lane of the (converged) warp. Code that issues MMAs stays converged
+// around it, so that descriptors live in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// 16 lanes x 256 bits, 2 repetitions (16 columns): register 4k + e of thread t
+// holds lane t/4 (e = 0, 1) or lane 8 + t/4 (e = 2, 3), column 8k + 2 (t mod 4)
+// + (e mod 2), as tc::ld16x256_x4.
+__device__ __forceinline__ void ld16x256_x2(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr));
+}
+
 // Maximum over a warp (NaN inputs are ignored).
 __device__ __forceinline__ float warp_max(float v) {
   float r;

@@ -23,14 +23,18 @@
 // Schedule: one CTA per SM. The visible pages of all (sequence, head chunk)
 // units form one list that is cut evenly; a CTA whose piece covers a unit
 // writes the result, the others leave (O, m, l) for latent_merge_kernel. Tiles
-// of 128 keys go through a ring of 16 KB slots (128 rows x 128 B, swizzled): a
-// tile is its rope unit and L / 128 blocks of 128 dims. Warp 4 loads, warp 5
-// issues the MMAs, warps 0-3 do the softmax with a thread per key and the
-// epilogue with a thread per dim. The rope slot of a tile is done with after
-// S, and then holds P, which leaves 2-3 slots more to load ahead.
-// The maximum that P is relative to is taken from a segment's first tile and
-// moved (O rescaled) only when a score exceeds it by 2^64 (bf16, whose P has
-// the range) or 2^4 (E4M3), so a tile costs its threads one barrier.
+// of 64 keys go through a ring of 8 KB slots (64 rows x 128 B, swizzled): a
+// tile is its rope unit and L / 128 blocks of 128 dims. L2 feeds an SM no
+// faster than HBM does, so the loads must never pause: what counts is how long
+// a byte stays in the ring. Hence small tiles, S of the next tile before the
+// second product of this one (two S buffers), MMAs issued from converged code
+// (40 cycles each, what reading their operands takes, against 80 to 260), and
+// blocks released one by one. The rope slot of a tile is done with after S, and
+// then holds P. Warp 4 loads, warp 5 issues the MMAs, warps 0-3 do the softmax
+// (a thread has two keys and a quarter of the heads) and the epilogue (a thread
+// per dim). The maximum that P is relative to is taken from a segment's first
+// tile and moved (O rescaled) only when a score exceeds it by 2^64 (bf16, whose
+// P has the range) or 2^4 (E4M3), so a tile costs its threads one barrier.
 #include <cuda_fp8.h>
 #include <math.h>
 
@@ -39,7 +43,7 @@
 namespace psw {
 namespace ldec {
 
-constexpr int kTile = 128;                      // keys of a tile
+constexpr int kTile = 64;                       // keys of a tile
 constexpr int kPages = kTile / kBlockSize;      // pages of a tile
 constexpr int kSlotBytes = kTile * 128;
 constexpr int kSoftThreads = 128;               // warps 0-3
@@ -67,15 +71,16 @@ struct Cfg {
   static constexpr int kQChunkBytes = kQRows * 128;
   static constexpr int kQBytes = kQChunks * kQChunkBytes;
   static constexpr int kRopeSteps = FP8 ? 2 : 4;       // 32-byte MMA steps of the rope chunk
-  static constexpr int kPSteps = FP8 ? 4 : 8;          // MMA steps along the keys
+  static constexpr int kPSteps = FP8 ? 2 : 4;          // MMA steps along the keys
   static constexpr int kPStepBytes = kTile / kPSteps * 128;
   static constexpr int kMisc = 3072;
   static constexpr int kSlots = (kSmemLimit - 1024 - kMisc - kQBytes) / kSlotBytes;
   static constexpr int kSmemBytes = 1024 + kQBytes + kSlots * kSlotBytes + kMisc;
-  static constexpr int kTmemO = FP8 ? 64 : 32;         // S^T columns before it
-  static_assert(kQRows <= kTmemO && kTmemO + kBlocks * kPCols <= 512, "tensor memory columns");
-  static_assert(kSlots >= 1 + kBlocks * kSlotsPerBlock + (kSlotsPerBlock - 1),
-                "a tile fits, a slot left out included");
+  static constexpr int kTmemO = 2 * kQRows;            // after the two S^T buffers
+  static_assert(kTmemO + kBlocks * kPCols <= 512, "tensor memory columns");
+  static_assert(kSlots >= 2 * (1 + kBlocks * kSlotsPerBlock) + 1,
+                "two tiles fit, a slot left out included");
+  static constexpr int kHeads = NH / 4;                // heads of a softmax thread
   static_assert(kSlots <= 32, "phase bits");
   // log2 distance by which a score may exceed the maximum in use, and the
   // largest row scale relative to the one in use; E4M3 P = 16 p v then stays
@@ -87,18 +92,16 @@ struct Cfg {
 
 struct Misc {
   uint64_t full[32], empty[32];
-  uint64_t q_full, s_full, p_full, o_full, o_free, drained;
-  int64_t p_begin, p_total;  // this CTA's first page; pages of all units
-  int32_t unit0, page0;      // its unit and the page within
-  int32_t pieces;
+  uint64_t q_full, s_full[2], p_full, pv_done, o_full, o_free, drained;
+  int32_t unit0, page0;      // this CTA's first unit and the page within it
   uint32_t tmem;
   int32_t abort;
-  int32_t scan[8];
   int64_t scan64[8];
   float red[4][kMaxHeads];
   float vred[4];
   float qs[kMaxHeads];       // FP8: scale * log2(e) * what a unit of q's codes stands for
   float lsum[kMaxHeads];
+  float alpha[kMaxHeads];    // factors of a rescale; at a segment's end, the maxima
 };
 static_assert(sizeof(Misc) <= 3072, "misc block");
 
@@ -204,9 +207,34 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
   // finds the unit
   const int per = (n_seqs + kThreads - 1) / kThreads;
   const int b0 = min(n_seqs, tid * per), b1 = min(n_seqs, b0 + per);
+  const int raw0 = b0 < b1 ? __ldg(seq_lens + b0) : 0;  // in flight during the set-up
+  if (warp == kMmaWarp) {
+    tc::alloc(&ms->tmem, 512);
+    tc::relinquish();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    prefetch_tensormap(&pool_map);
+    prefetch_tensormap(&q_map);
+  }
+  if (tid == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&ms->full[i], 1);
+      mbar_init(&ms->empty[i], 1);
+    }
+    mbar_init(&ms->q_full, FP8 ? 4 : 1);
+    mbar_init(&ms->s_full[0], 1);
+    mbar_init(&ms->s_full[1], 1);
+    mbar_init(&ms->p_full, 4);
+    mbar_init(&ms->pv_done, 1);
+    mbar_init(&ms->o_full, 1);
+    mbar_init(&ms->o_free, 4);
+    mbar_init(&ms->drained, 1);
+    ms->abort = 0;
+    fence_mbar_init();
+  }
   int64_t mine = 0;
   for (int b = b0; b < b1; ++b) {
-    const int raw = __ldg(seq_lens + b);
+    const int raw = b == b0 ? raw0 : __ldg(seq_lens + b);
     mine += static_cast<int64_t>(span_of(raw, window, pages.max_blocks).count) * chunks;
     if (blockIdx.x == 0) {
       if (raw < 0) flag_error(err, PSW_DEVERR_LENGTH);
@@ -221,24 +249,6 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     if (lane >= o) incl += y;
   }
   if (lane == 31) ms->scan64[warp] = incl;
-  if (tid == 0) {
-    for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(&ms->full[i], 1);
-      mbar_init(&ms->empty[i], 1);
-    }
-    mbar_init(&ms->q_full, FP8 ? 4 : 1);
-    mbar_init(&ms->s_full, 1);
-    mbar_init(&ms->p_full, 4);
-    mbar_init(&ms->o_full, 1);
-    mbar_init(&ms->o_free, 4);
-    mbar_init(&ms->drained, 1);
-    ms->abort = 0;
-    fence_mbar_init();
-  }
-  if (warp == kMmaWarp) {
-    tc::alloc(&ms->tmem, 512);
-    tc::relinquish();
-  }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -281,8 +291,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------ loads
-    if (lane == 0) prefetch_tensormap(&pool_map);
-    const int pg = lane & 7, half = (lane >> 3) & 1;  // page of the tile, slot of a block
+    const int pg = lane & 3, half = (lane >> 2) & 1;  // page of the tile, slot of a block
     uint32_t issued = 0;  // slots whose last load may be in flight, for the drain
     while (ok && walk.next()) {
       const int32_t* row = pages.block_table + static_cast<int64_t>(walk.b) * pages.max_blocks;
@@ -311,7 +320,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
           if (!ok) break;
           issued |= ((1u << n) - 1u) << s;
           const int x = u == 0 ? LAT : (u - 1) * 128 + half * 64;
-          if (lane < 8 * n)
+          if (lane < kPages * n)
             lat::tma_box(smem_u32(ring + (s + half) * kSlotBytes + pg * 2048), &pool_map,
                          &ms->full[s + half], x, y, 0);
         }
@@ -326,64 +335,88 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      const uint32_t id_s = FP8 ? lat::idesc_e4m3_f32(128, C::kQRows, 0, 0)
-                                : tc::idesc_bf16_f32(128, C::kQRows, 0, 0);
-      const uint32_t id_o = FP8 ? lat::idesc_e4m3_f32(128, C::kPCols, 1, 1)
-                                : tc::idesc_bf16_f32(128, C::kPCols, 1, 1);
-      auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-        if (FP8) lat::mma_ss_fp8(d, a, b, id, acc);
-        else tc::mma_ss(d, a, b, id, acc);
-      };
-      const uint64_t q_desc = tc::smem_desc(smem_u32(q_smem), 16, 1024, tc::kSwizzle128B);
-      const uint32_t ring_at = smem_u32(ring);
-      int seg = 0, tile = 0;
-      for (; ok && walk.next(); ++seg) {
-        const int n_tiles = walk.tiles();
-        for (int t = 0; ok && t < n_tiles; ++t, ++tile) {
-          if (t == 0) ok = mbar_wait(&ms->q_full, seg & 1);
-          int slot[1 + C::kBlocks];
+    // The whole warp walks along, converged; one lane issues. Descriptors are a
+    // base, the slot's place in it, and offsets known when compiling.
+    const uint32_t id_s = FP8 ? lat::idesc_e4m3_f32(kTile, C::kQRows, 0, 0)
+                              : tc::idesc_bf16_f32(kTile, C::kQRows, 0, 0);
+    const uint32_t id_o = FP8 ? lat::idesc_e4m3_f32(128, C::kPCols, 1, 1)
+                              : tc::idesc_bf16_f32(128, C::kPCols, 1, 1);
+    auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+      if (FP8) lat::mma_ss_fp8(d, a, b, id, acc);
+      else tc::mma_ss(d, a, b, id, acc);
+    };
+    const uint64_t q_desc = tc::smem_desc(smem_u32(q_smem), 16, 1024, tc::kSwizzle128B);
+    const uint64_t k_desc = tc::smem_desc(smem_u32(ring), 16, 1024, tc::kSwizzle128B);
+    const uint64_t v_desc = tc::smem_desc(smem_u32(ring), kSlotBytes, 1024, tc::kSwizzle128B);
+    const uint64_t p_desc = tc::smem_desc(smem_u32(ring), 1024, 1024, tc::kSwizzle128B);
+    constexpr uint32_t kSlotStep = kSlotBytes >> 4;
+    const bool one = lat::elect_one();
+    int slot[2][1 + C::kBlocks];  // of the tile S is formed for, and of the one before
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u));
+    };
+    auto scores = [&](int tile, int (&sl)[1 + C::kBlocks]) {
+      const uint32_t d = tmem + (tile & 1) * C::kQRows;
 #pragma unroll
-          for (int u = 0; u <= C::kBlocks; ++u) {
-            uint32_t parity;
-            slot[u] = rg.take<C::kSlots>(u == 0 ? 1 : C::kSlotsPerBlock, parity);
-            const int n_ch = u == 0 ? 1 : C::kSlotsPerBlock;
-            const int steps = u == 0 ? C::kRopeSteps : 4;
-            for (int c = 0; c < n_ch; ++c) {
-              ok = ok && mbar_wait(&ms->full[slot[u] + c], parity >> (slot[u] + c) & 1u);
-              if (!ok) break;
-              tc::fence_after();
-              const int qc = u == 0 ? C::kQChunks - 1 : (u - 1) * C::kSlotsPerBlock + c;
-              const uint64_t kd = tc::smem_desc(ring_at + (slot[u] + c) * kSlotBytes, 16, 1024,
-                                                tc::kSwizzle128B);
-              const uint64_t qd = q_desc + static_cast<uint32_t>(qc * C::kQChunkBytes >> 4);
-              for (int k = 0; k < steps; ++k)
-                mma(tmem, kd + k * 2, qd + k * 2, id_s, (u > 0 || k > 0) ? 1u : 0u);
-            }
-          }
-          if (!ok) break;
-          tc::commit(&ms->s_full);
-          ok = mbar_wait(&ms->p_full, tile & 1) &&
-               (t > 0 || seg == 0 || mbar_wait(&ms->o_free, (seg - 1) & 1)) && !*abort_flag;
-          if (!ok) break;
+      for (int u = 0; u <= C::kBlocks; ++u) {
+        uint32_t parity;
+        const int n_ch = u == 0 ? 1 : C::kSlotsPerBlock;
+        sl[u] = rg.take<C::kSlots>(n_ch, parity);
+#pragma unroll
+        for (int c = 0; c < n_ch; ++c) {
+          ok = ok && wait(&ms->full[sl[u] + c], parity >> (sl[u] + c));
+          if (!ok) return;
           tc::fence_after();
-          const uint64_t p_desc =
-              tc::smem_desc(ring_at + slot[0] * kSlotBytes, 1024, 1024, tc::kSwizzle128B);
+          const uint64_t kd = k_desc + (sl[u] + c) * kSlotStep;
+          const uint64_t qd =
+              q_desc + static_cast<uint32_t>((u == 0 ? C::kQChunks - 1 : (u - 1) * C::kSlotsPerBlock + c) *
+                                             C::kQChunkBytes >> 4);
+          if (one) {
 #pragma unroll
-          for (int m = 0; m < C::kBlocks; ++m) {
-            const uint64_t v_desc = tc::smem_desc(ring_at + slot[1 + m] * kSlotBytes, kSlotBytes,
-                                                  1024, tc::kSwizzle128B);
-            for (int k = 0; k < C::kPSteps; ++k) {
-              const uint32_t off = static_cast<uint32_t>(k * C::kPStepBytes) >> 4;
-              mma(tmem + C::kTmemO + m * C::kPCols, v_desc + off, p_desc + off, id_o,
-                  (t > 0 || k > 0) ? 1u : 0u);
-            }
-            for (int c = 0; c < C::kSlotsPerBlock; ++c) tc::commit(&ms->empty[slot[1 + m] + c]);
+            for (int k = 0; k < (u == 0 ? C::kRopeSteps : 4); ++k)
+              mma(d, kd + k * 2, qd + k * 2, id_s, (u > 0 || k > 0) ? 1u : 0u);
           }
-          tc::commit(&ms->empty[slot[0]]);
-          if (t == n_tiles - 1) tc::commit(&ms->o_full);
         }
       }
+      if (one) tc::commit(&ms->s_full[tile & 1]);
+    };
+    int seg = 0, tile = 0;
+    for (; ok && walk.next(); ++seg) {
+      const int n_tiles = walk.tiles();
+      ok = wait(&ms->q_full, seg);
+      if (ok) scores(tile, slot[0]);
+      for (int t = 0; ok && t < n_tiles; ++t, ++tile) {
+        if (t + 1 < n_tiles) scores(tile + 1, slot[1]);
+        ok = ok && wait(&ms->p_full, tile) && (t > 0 || seg == 0 || wait(&ms->o_free, seg - 1)) &&
+             __all_sync(0xffffffffu, *abort_flag == 0);
+        if (!ok) break;
+        tc::fence_after();
+        const uint64_t pd = p_desc + slot[0][0] * kSlotStep;
+#pragma unroll
+        for (int m = 0; m < C::kBlocks; ++m) {
+          const uint64_t vd = v_desc + slot[0][1 + m] * kSlotStep;
+          if (one) {
+#pragma unroll
+            for (int k = 0; k < C::kPSteps; ++k) {
+              constexpr uint32_t kStep = C::kPStepBytes >> 4;
+              mma(tmem + C::kTmemO + m * C::kPCols, vd + k * kStep, pd + k * kStep, id_o,
+                  (t > 0 || k > 0) ? 1u : 0u);
+            }
+#pragma unroll
+            for (int c = 0; c < C::kSlotsPerBlock; ++c) tc::commit(&ms->empty[slot[0][1 + m] + c]);
+          }
+        }
+        if (one) {
+          tc::commit(&ms->empty[slot[0][0]]);
+          tc::commit(&ms->pv_done);
+          if (t == n_tiles - 1) tc::commit(&ms->o_full);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u <= C::kBlocks; ++u) slot[0][u] = slot[1][u];
+      }
+    }
+    if (one) {
       if (!ok) {
         *abort_flag = 1;
         flag_error(err, PSW_DEVERR_PIPELINE);
@@ -409,31 +442,40 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       } else {
         // warp by warp, a head at a time: its largest value gives the power of
         // two; the value is the sum of the two parts, the second 16 times up
-        for (int h = warp; h < NH; h += 4) {
-          constexpr int kRow = LAT + kLatentRope, kPairs = kRow / 2;
-          float2 v[(kPairs + 31) / 32];
-          float amax = 0.f;
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(
-              q + (static_cast<int64_t>(w.b) * heads + h0 + h) * kRow);
+        constexpr int kRow = LAT + kLatentRope, kPairs = kRow / 2, kWords = (kPairs + 31) / 32;
+        uint32_t raw[NH / 4][kWords];  // all loads in flight at once
 #pragma unroll
-          for (int i = 0; i < (kPairs + 31) / 32; ++i) {
-            const int e = i * 32 + lane;
-            v[i] = (h0 + h < heads && e < kPairs) ? unpack_bf16x2(__ldg(src + e)) : make_float2(0.f, 0.f);
-            amax = fmaxf(amax, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
+        for (int j = 0; j < NH / 4; ++j) {
+          const int h = h0 + warp + 4 * j;
+          const uint32_t* src =
+              reinterpret_cast<const uint32_t*>(q + (static_cast<int64_t>(w.b) * heads + h) * kRow);
+#pragma unroll
+          for (int i = 0; i < kWords; ++i)
+            raw[j][i] = (h < heads && i * 32 + lane < kPairs) ? __ldg(src + i * 32 + lane) : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < NH / 4; ++j) {
+          const int h = warp + 4 * j;
+          float amax = 0.f;
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) {
+            const float2 v = unpack_bf16x2(raw[j][i]);
+            amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
           }
           amax = lat::warp_max(amax);
-          // 2^k with amax 2^k in [128, 256): the exponent field of amax, turned
-          const int ex = static_cast<int>(__float_as_uint(amax) >> 23);  // biased, sign 0
+          // 2^k with amax 2^k in [128, 256), from amax's exponent field
+          const int ex = static_cast<int>(__float_as_uint(amax) >> 23);
           const int k = max(-126, min(126, 127 + 7 - ex));
           const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
           // (an infinite query has no such codes: its scores become NaN)
           if (lane == 0)
             ms->qs[h] = ex == 255 ? NAN : mul * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
 #pragma unroll
-          for (int i = 0; i < (kPairs + 31) / 32; ++i) {
+          for (int i = 0; i < kWords; ++i) {
             const int e = i * 32 + lane;
             if (e >= kPairs) continue;
-            const float a = v[i].x * up, b = v[i].y * up;
+            const float2 v = unpack_bf16x2(raw[j][i]);
+            const float a = v.x * up, b = v.y * up;
             const uint32_t hi = e4m3_pair(a, b);
             const float2 got = e4m3_values(hi);
             const uint32_t lo = e4m3_pair((a - got.x) * 16.f, (b - got.y) * 16.f);
@@ -454,87 +496,117 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     int seg = 0, tile = 0;
     bool more = walk.next();
     if (more) load_q(walk);
+    // this thread's keys of a tile, rows 16 warp + lane / 4 and 8 further; its
+    // heads 8 g + 2 (lane mod 4) + {0, 1}, number 2 g + {0, 1} here
+    const int r0 = warp * 16 + (lane >> 2), quad = lane & 3;
     for (; ok && more; ++seg) {
       const Walk w = walk;
       more = walk.next();
       const int h0 = w.chunk * NH, nh = min(NH, heads - h0), n_tiles = w.tiles();
       const int32_t* row = pages.block_table + static_cast<int64_t>(w.b) * pages.max_blocks;
-      auto scale_of = [&](int t) -> float {  // FP8: the row scale of this thread's key of tile t
-        const int i = t * kPages + tid / kBlockSize;
-        if (!FP8 || i >= w.seg_count) return 0.f;
+      auto scale_of = [&](int t, float (&ks)[2]) {  // FP8: the scales of this thread's rows of tile t
+        const int i = t * kPages + warp;
+        ks[0] = ks[1] = 0.f;
+        if (!FP8 || i >= w.seg_count) return;
         const int blk = __ldg(row + w.span.first + w.seg_first + i);
-        return blk >= 0 && blk < pages.num_blocks
-                   ? __ldg(pages.row_scale + static_cast<int64_t>(blk) * kBlockSize + tid % kBlockSize)
-                   : 0.f;
+        if (blk < 0 || blk >= pages.num_blocks) return;
+        const float* p = pages.row_scale + static_cast<int64_t>(blk) * kBlockSize + (lane >> 2);
+        ks[0] = __ldg(p);
+        ks[1] = __ldg(p + 8);
       };
-      float m[NH], l[NH], vref = 0.f, ks = scale_of(0);
+      constexpr int HN = C::kHeads;
+      float m[HN], l[HN], vref = 0.f, ks[2];
+      scale_of(0, ks);
 #pragma unroll
-      for (int h = 0; h < NH; ++h) m[h] = 0.f, l[h] = 0.f;
+      for (int i = 0; i < HN; ++i) m[i] = 0.f, l[i] = 0.f;
       for (int t = 0; t < n_tiles; ++t, ++tile) {
-        const int page = w.span.first + w.seg_first + t * kPages + tid / kBlockSize;
-        const int key = page * kBlockSize + tid % kBlockSize;
-        const bool in_seg = t * kPages + tid / kBlockSize < w.seg_count;
-        const bool seen = in_seg && key >= w.span.lo && key < w.span.len;
-        const float vs = seen ? ks : 0.f;  // a hidden slot's scale may be anything
-        if (t + 1 < n_tiles) ks = scale_of(t + 1);
+        const bool in_seg = t * kPages + warp < w.seg_count;  // a page per warp
+        const int key = (w.span.first + w.seg_first + t * kPages + warp) * kBlockSize + (lane >> 2);
+        bool seen[2];
+        float vs[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          seen[j] = in_seg && key + 8 * j >= w.span.lo && key + 8 * j < w.span.len;
+          vs[j] = seen[j] ? ks[j] : 0.f;  // a hidden slot's scale may be anything
+        }
+        if (t + 1 < n_tiles) scale_of(t + 1, ks);
         int slot[1 + C::kBlocks];
 #pragma unroll
         for (int u = 0; u <= C::kBlocks; ++u) {
           uint32_t parity;
           slot[u] = rg.take<C::kSlots>(u == 0 ? 1 : C::kSlotsPerBlock, parity);
         }
-        ok = mbar_wait(&ms->s_full, tile & 1);
+        ok = mbar_wait(&ms->s_full[tile & 1], (tile >> 1) & 1);
         tc::fence_after();
-        float z[NH];
+        float z[2][HN];
         {
-          uint32_t v[C::kQRows];
+          uint32_t v[C::kQParts][NH / 2];
 #pragma unroll
-          for (int c = 0; c < C::kQRows / 16; ++c)
-            tc::ld16(tmem + lanes + c * 16, *reinterpret_cast<uint32_t(*)[16]>(&v[c * 16]));
+          for (int p = 0; p < C::kQParts; ++p) {
+            const uint32_t at = tmem + lanes + (tile & 1) * C::kQRows + p * NH;
+            if (NH == 16) lat::ld16x256_x2(at, *reinterpret_cast<uint32_t(*)[8]>(&v[p][0]));
+            else tc::ld16x256_x4(at, *reinterpret_cast<uint32_t(*)[16]>(&v[p][0]));
+          }
           tc::wait_ld();
 #pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            if (FP8) z[h] = fmaf(__uint_as_float(v[(C::kQParts - 1) * NH + h]), 0.0625f, __uint_as_float(v[h])) * (ms->qs[h] * vs);
-            else z[h] = __uint_as_float(v[h]) * mul;
+          for (int i = 0; i < HN; ++i) {
+            const int r = 4 * (i >> 1) + (i & 1);
+            const float qs = FP8 ? ms->qs[8 * (i >> 1) + 2 * quad + (i & 1)] : mul;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float x = __uint_as_float(v[0][r + 2 * j]);
+              z[j][i] = FP8 ? fmaf(__uint_as_float(v[C::kQParts - 1][r + 2 * j]), 0.0625f, x) * (qs * vs[j])
+                            : x * qs;
+            }
           }
         }
         if (softcap > 0.f) {
 #pragma unroll
-          for (int h = 0; h < NH; ++h) z[h] = cap2 * tanh_abs(z[h]);
-        }
+          for (int i = 0; i < HN; ++i)
 #pragma unroll
-        for (int h = 0; h < NH; ++h) z[h] = seen ? z[h] : -INFINITY;
-        // values that must not enter the second product: rows of a page that
-        // hold no visible key (P is 0 there, but 0 times NaN is not)
-        if (in_seg && !seen) {
-#pragma unroll
-          for (int u = 1; u <= C::kBlocks; ++u)
-            for (int c = 0; c < C::kSlotsPerBlock; ++c)
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(ring + (slot[u] + c) * kSlotBytes + tid * 128 + i * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
+            for (int j = 0; j < 2; ++j) z[j][i] = cap2 * tanh_abs(z[j][i]);
         }
-        bool move = !ok || t == 0;
         float over = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < NH; ++h) over = fmaxf(over, z[h] - m[h]);
-        move |= over > C::kLag;
-        if (FP8) move |= vs > C::kVLag * vref;
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int i = 0; i < HN; ++i) {
+            z[j][i] = seen[j] ? z[j][i] : -INFINITY;
+            over = fmaxf(over, z[j][i] - m[i]);
+          }
+          // rows of a loaded page that hold no visible key must not enter the
+          // second product (P is 0 there, but 0 times NaN is not)
+          if (in_seg && !seen[j]) {
+#pragma unroll
+            for (int u = 1; u <= C::kBlocks; ++u)
+              for (int c = 0; c < C::kSlotsPerBlock; ++c)
+                for (int i = 0; i < 2; ++i)
+                  *reinterpret_cast<uint4*>(ring + (slot[u] + c) * kSlotBytes + (r0 + 8 * j) * 128 +
+                                            quad * 32 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        bool move = !ok || t == 0 || over > C::kLag;
+        if (FP8) move |= fmaxf(vs[0], vs[1]) > C::kVLag * vref;
         if (lat::bar_any(1, kSoftThreads, move)) {
           // the tile's maxima; the ones in use move to them where they lag
 #pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            const float x = lat::warp_max(z[h]);
-            if (lane == 0) ms->red[warp][h] = x;
+          for (int i = 0; i < HN; ++i) {
+            float x = fmaxf(z[0][i], z[1][i]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+            if (lane < 4) ms->red[warp][8 * (i >> 1) + 2 * quad + (i & 1)] = x;
           }
           if (FP8) {
-            const float x = lat::warp_max(vs);
+            const float x = lat::warp_max(fmaxf(vs[0], vs[1]));
             if (lane == 0) ms->vred[warp] = x;
           }
+          // O is rescaled below: the products up to the tile before have ended
+          if (t > 0 && ok) ok = mbar_wait(&ms->pv_done, (tile - 1) & 1);
           if (lat::bar_any(1, kSoftThreads, !ok)) {
             ok = false;
             break;
           }
+          tc::fence_after();
           float vmul = 1.f;
           if (FP8) {
             const float x = fmaxf(fmaxf(ms->vred[0], ms->vred[1]), fmaxf(ms->vred[2], ms->vred[3]));
@@ -544,21 +616,22 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
               vref = to;
             }
           }
-          float alpha[NH];
 #pragma unroll
-          for (int h = 0; h < NH; ++h) {
+          for (int i = 0; i < HN; ++i) {
+            const int h = 8 * (i >> 1) + 2 * quad + (i & 1);
             const float x = fmaxf(fmaxf(ms->red[0][h], ms->red[1][h]), fmaxf(ms->red[2][h], ms->red[3][h]));
-            alpha[h] = vmul;
+            float a = 1.f;
             if (t == 0) {
-              m[h] = x == -INFINITY ? 0.f : x;
-            } else if (x > m[h] + C::kLag) {
-              const float a = ex2_approx(m[h] - x);
-              alpha[h] *= a;
-              l[h] *= a;
-              m[h] = x;
+              m[i] = x == -INFINITY ? 0.f : x;
+            } else if (x > m[i] + C::kLag) {
+              a = ex2_approx(m[i] - x);
+              l[i] *= a;
+              m[i] = x;
             }
+            if (warp == 0 && lane < 4) ms->alpha[h] = a * vmul;
           }
-          if (t > 0) {  // the products before this tile have ended: S came after them
+          named_bar_sync(1, kSoftThreads);
+          if (t > 0) {
 #pragma unroll 1
             for (int blk = 0; blk < C::kBlocks; ++blk) {
 #pragma unroll
@@ -569,67 +642,47 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                 tc::wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                  v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha[(c * 16 + i) % NH]);
+                  v[i] = __float_as_uint(__uint_as_float(v[i]) * ms->alpha[(c * 16 + i) % NH]);
                 tc::st16(at, v);
               }
             }
             tc::wait_st();
           }
-          named_bar_sync(1, kSoftThreads);  // red and vred may be written again
+          named_bar_sync(1, kSoftThreads);  // red, vred and alpha may be written again
         }
-        // P into the rope slot: this key's row, parts of all heads, 16-byte
-        // vectors swizzled by the row
-        uint8_t* prow = ring + slot[0] * kSlotBytes + tid * 128;
-        const int sw = tid & 7;
-        if (!FP8) {
+        // P into the rope slot: a key's row holds the parts of all heads,
+        // 16-byte vectors swizzled by the row
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = r0 + 8 * j, sw = r & 7;
+          uint8_t* prow = ring + slot[0] * kSlotBytes + r * 128;
+          const float pv = FP8 ? vs[j] * (C::kPUnit / vref) : 1.f;
 #pragma unroll
           for (int g = 0; g < NH / 8; ++g) {
-            uint32_t hi[4], lo[4];
+            float a = ex2_approx(z[j][2 * g] - m[2 * g]);
+            float b = ex2_approx(z[j][2 * g + 1] - m[2 * g + 1]);
+            l[2 * g] += a;
+            l[2 * g + 1] += b;
+            if (!FP8) {
+              const uint32_t hi = pack_bf16x2(a, b);
+              const float2 got = unpack_bf16x2(hi);
+              *reinterpret_cast<uint32_t*>(prow + ((g ^ sw) << 4) + quad * 4) = hi;
+              *reinterpret_cast<uint32_t*>(prow + (((g + NH / 8) ^ sw) << 4) + quad * 4) =
+                  pack_bf16x2(a - got.x, b - got.y);
+            } else {
+              a *= pv;
+              b *= pv;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float a = ex2_approx(z[g * 8 + 2 * i] - m[g * 8 + 2 * i]);
-              const float b = ex2_approx(z[g * 8 + 2 * i + 1] - m[g * 8 + 2 * i + 1]);
-              l[g * 8 + 2 * i] += a;
-              l[g * 8 + 2 * i + 1] += b;
-              hi[i] = pack_bf16x2(a, b);
-              const float2 r = unpack_bf16x2(hi[i]);
-              lo[i] = pack_bf16x2(a - r.x, b - r.y);
-            }
-            *reinterpret_cast<uint4*>(prow + ((g ^ sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(prow + (((g + NH / 8) ^ sw) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-        } else {
-          const float pv = vs * (C::kPUnit / vref);
-#pragma unroll
-          for (int g = 0; g < NH / 16; ++g) {
-            uint32_t part[3][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t w3[3] = {0u, 0u, 0u};
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int h = g * 16 + 4 * i + 2 * j;
-                float a = ex2_approx(z[h] - m[h]), b = ex2_approx(z[h + 1] - m[h + 1]);
-                l[h] += a;
-                l[h + 1] += b;
-                a *= pv;
-                b *= pv;
-#pragma unroll
-                for (int p = 0; p < 3; ++p) {
-                  const uint32_t c = e4m3_pair(a, b);
-                  w3[p] |= c << (16 * j);
-                  const float2 r = e4m3_values(c);
-                  a = (a - r.x) * 16.f;
-                  b = (b - r.y) * 16.f;
-                }
+              for (int p = 0; p < 3; ++p) {
+                const uint32_t c = e4m3_pair(a, b);
+                const int at = p * NH + g * 8 + quad * 2;
+                *reinterpret_cast<uint16_t*>(prow + (((at >> 4) ^ sw) << 4) + (at & 15)) =
+                    static_cast<uint16_t>(c);
+                const float2 got = e4m3_values(c);
+                a = (a - got.x) * 16.f;
+                b = (b - got.y) * 16.f;
               }
-#pragma unroll
-              for (int p = 0; p < 3; ++p) part[p][i] = w3[p];
             }
-#pragma unroll
-            for (int p = 0; p < 3; ++p)
-              *reinterpret_cast<uint4*>(prow + (((p * (NH / 16) + g) ^ sw) << 4)) =
-                  make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
           }
         }
         fence_proxy_async_smem();
@@ -640,12 +693,14 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       if (!ok) break;
       // ---- the segment's end. S of its last tile is done: Q may be replaced
       if (more) load_q(walk);
-      {
-        float x[NH];
 #pragma unroll
-        for (int h = 0; h < NH; ++h) x[h] = l[h];
-        const float s = lat::warp_sums<NH>(x, lane);
-        if (lane % (32 / NH) == 0) ms->red[warp][lane / (32 / NH)] = s;
+      for (int i = 0; i < C::kHeads; ++i) {
+        float x = l[i];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        const int h = 8 * (i >> 1) + 2 * quad + (i & 1);
+        if (lane < 4) ms->red[warp][h] = x;
+        if (warp == 0 && lane < 4) ms->alpha[h] = m[i];
       }
       ok = mbar_wait(&ms->o_full, seg & 1);
       if (lat::bar_any(1, kSoftThreads, !ok)) {
@@ -656,9 +711,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       const bool whole = w.whole();
       const int slot_id = 2 * blockIdx.x + (w.seg_first == 0 ? 1 : 0);
       if (tid < nh) {  // thread h: the statistics of head h
-        float mh = 0.f;
-#pragma unroll
-        for (int h = 0; h < NH; ++h) mh = h == tid ? m[h] : mh;
+        const float mh = ms->alpha[tid];
         const float s = ms->red[0][tid] + ms->red[1][tid] + ms->red[2][tid] + ms->red[3][tid];
         ms->lsum[tid] = whole ? (s == 0.f ? 0.f : 1.f / s) : 1.f;
         if (whole) {
