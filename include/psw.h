@@ -432,7 +432,7 @@ PSW_API int latent_norm_rope_cache_write(
     int64_t qo_token_stride, int64_t qo_head_stride, void *pool, psw_stream_t stream);
 
 /* The same into FP8 pages: pool8 uint8 [num_blocks][16][L + 64] of E4M3 codes
- * and row_scale fp32 [num_blocks][16], one scale per row by the rule of
+ * and row_scale fp32 [num_blocks][16] (16-byte aligned), one scale per row by the rule of
  * kv_cache_write_fp8 applied to the row's fp32 values (amax over all L + 64,
  * rounded once, to the code). */
 PSW_API int latent_norm_rope_cache_write_fp8(

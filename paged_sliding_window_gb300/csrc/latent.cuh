@@ -63,6 +63,18 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, ui
       : "memory");
 }
 
+// Plain copy of `bytes` (a multiple of 16; both addresses 16-byte aligned) into
+// shared memory, counted on `bar`. (A tensor copy's destination would have to be
+// 128-byte aligned.)
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // D[tmem] (+)= A[smem] * B[smem] on E4M3 operands, fp32 accumulators.
 __device__ __forceinline__ void mma_ss_fp8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                            uint32_t idesc, uint32_t accumulate) {

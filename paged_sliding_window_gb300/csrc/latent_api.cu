@@ -77,7 +77,7 @@ int write_rows(const psw_latent_t* layer, const psw_latent_norm_t* norm, const v
       return PSW_EINVAL_STRIDE;
   }
   if (!aligned(ckv, 16) || !aligned(q_rope, 16) || !aligned(q_rope_out, 16) ||
-      !aligned(pool, 16) || !aligned(norm->latent_weight, 16) || !aligned(row_scale, 4))
+      !aligned(pool, 16) || !aligned(norm->latent_weight, 16) || !aligned(row_scale, 16))
     return PSW_EALIGN;
   if (n_seqs == 0) return PSW_OK;
   DeviceInfo info;
@@ -100,7 +100,7 @@ int decode(const psw_latent_t* layer, const void* q, const void* pool, const flo
   if ((rc = check_pages(pages)) != PSW_OK) return rc;
   if (n_seqs < 0) return PSW_EINVAL_NSEQS;
   if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
-      !aligned(row_scale, 4) || !aligned(ws, 16))
+      !aligned(row_scale, 16) || !aligned(ws, 16))
     return PSW_EALIGN;
   if (n_seqs == 0) return PSW_OK;
   if (ws == nullptr || ws_bytes < latent_decode_workspace(L, n_seqs)) return PSW_EWORKSPACE;
@@ -123,7 +123,7 @@ int expand(const psw_latent_t* layer, const void* pool, const float* row_scale,
   if (n_seqs < 0) return PSW_EINVAL_NSEQS;
   if (n_k_total < 0) return PSW_ECAPACITY;
   if (!aligned(pool, 16) || !aligned(w, 16) || !aligned(kv, 16) || !aligned(k_rope, 16) ||
-      !aligned(row_scale, 4))
+      !aligned(row_scale, 16))
     return PSW_EALIGN;
   if (n_seqs == 0 || n_k_total == 0) return PSW_OK;
   DeviceInfo info;

@@ -26,8 +26,8 @@
 // of 64 keys go through a ring of 8 KB slots (64 rows x 128 B, swizzled): a
 // tile is its rope unit and L / 128 blocks of 128 dims. L2 feeds an SM no
 // faster than HBM does, so the loads must never pause: what counts is how long
-// a byte stays in the ring. Hence small tiles, S of the next tile before the
-// second product of this one (two S buffers), MMAs issued from converged code
+// a byte stays in the ring. Hence small tiles, S of the next tiles ahead of
+// the second product of this one (two S buffers, a warp each), MMAs issued from converged code
 // (40 cycles each, what reading their operands takes, against 80 to 260), and
 // blocks released one by one. The rope slot of a tile is done with after S, and
 // then holds P. Warp 4 loads, warp 5 issues the MMAs, warps 0-3 do the softmax
@@ -47,8 +47,8 @@ constexpr int kTile = 64;                       // keys of a tile
 constexpr int kPages = kTile / kBlockSize;      // pages of a tile
 constexpr int kSlotBytes = kTile * 128;
 constexpr int kSoftThreads = 128;               // warps 0-3
-constexpr int kLoadWarp = 4, kMmaWarp = 5;
-constexpr int kThreads = 192;
+constexpr int kLoadWarp = 4, kScoreWarp = 5, kValueWarp = 6;  // loads; MMAs of S; of O
+constexpr int kThreads = 224;
 constexpr int kMaxCtas = 160;                   // pieces of the page list
 constexpr int kMinPages = 4;                    // pages a piece has at least
 constexpr int kMaxHeads = 32;                   // heads of a chunk
@@ -73,13 +73,19 @@ struct Cfg {
   static constexpr int kRopeSteps = FP8 ? 2 : 4;       // 32-byte MMA steps of the rope chunk
   static constexpr int kPSteps = FP8 ? 2 : 4;          // MMA steps along the keys
   static constexpr int kPStepBytes = kTile / kPSteps * 128;
-  static constexpr int kMisc = 3072;
+  static constexpr int kMisc = FP8 ? 6144 : 2048;
   static constexpr int kSlots = (kSmemLimit - 1024 - kMisc - kQBytes) / kSlotBytes;
   static constexpr int kSmemBytes = 1024 + kQBytes + kSlots * kSlotBytes + kMisc;
   static constexpr int kTmemO = 2 * kQRows;            // after the two S^T buffers
   static_assert(kTmemO + kBlocks * kPCols <= 512, "tensor memory columns");
   static_assert(kSlots >= 2 * (1 + kBlocks * kSlotsPerBlock) + 1,
                 "two tiles fit, a slot left out included");
+  // FP8: row scales of the tiles in the ring, in turn (after the misc block)
+  static constexpr int kScaleTiles = 16;
+  static constexpr int kScales = 2048, kScaleBytes = kTile * 4;
+  static_assert(!FP8 || (kScales + kScaleTiles * kScaleBytes <= kMisc &&
+                         kSlots / (1 + kBlocks * kSlotsPerBlock) + 2 <= kScaleTiles),
+                "no tile's scales are overwritten while it is in the ring");
   static constexpr int kHeads = NH / 4;                // heads of a softmax thread
   static_assert(kSlots <= 32, "phase bits");
   // log2 distance by which a score may exceed the maximum in use, and the
@@ -92,7 +98,7 @@ struct Cfg {
 
 struct Misc {
   uint64_t full[32], empty[32];
-  uint64_t q_full, s_full[2], p_full, pv_done, o_full, o_free, drained;
+  uint64_t q_full, s_full[2], p_full[2], pv_done[2], o_full, o_free, drained;
   int32_t unit0, page0;      // this CTA's first unit and the page within it
   uint32_t tmem;
   int32_t abort;
@@ -103,7 +109,10 @@ struct Misc {
   float lsum[kMaxHeads];
   float alpha[kMaxHeads];    // factors of a rescale; at a segment's end, the maxima
 };
-static_assert(sizeof(Misc) <= 3072, "misc block");
+static_assert(sizeof(Misc) <= 2048, "misc block");
+
+// Row scales of a page that is not there (its codes read as zeros).
+__device__ const float4 g_zero_scales[kBlockSize / 4] = {};
 
 // Visible pages of one sequence.
 struct Span {
@@ -200,7 +209,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
   uint8_t* q_smem = smem;
   uint8_t* ring = smem + C::kQBytes;
   Misc* ms = reinterpret_cast<Misc*>(ring + C::kSlots * kSlotBytes);
+  uint8_t* scales = reinterpret_cast<uint8_t*>(ms) + C::kScales;
   const int chunks = chunks_of(heads);
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may queue up
 
   // ---- this CTA's piece of the page list: every CTA adds up all spans (a run
   // of sequences per thread) and the thread whose run holds its first page
@@ -208,7 +220,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
   const int per = (n_seqs + kThreads - 1) / kThreads;
   const int b0 = min(n_seqs, tid * per), b1 = min(n_seqs, b0 + per);
   const int raw0 = b0 < b1 ? __ldg(seq_lens + b0) : 0;  // in flight during the set-up
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tc::alloc(&ms->tmem, 512);
     tc::relinquish();
   }
@@ -224,11 +236,13 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     mbar_init(&ms->q_full, FP8 ? 4 : 1);
     mbar_init(&ms->s_full[0], 1);
     mbar_init(&ms->s_full[1], 1);
-    mbar_init(&ms->p_full, 4);
-    mbar_init(&ms->pv_done, 1);
+    mbar_init(&ms->p_full[0], 4);
+    mbar_init(&ms->p_full[1], 4);
+    mbar_init(&ms->pv_done[0], 1);
+    mbar_init(&ms->pv_done[1], 1);
     mbar_init(&ms->o_full, 1);
     mbar_init(&ms->o_free, 4);
-    mbar_init(&ms->drained, 1);
+    mbar_init(&ms->drained, 2);
     ms->abort = 0;
     fence_mbar_init();
   }
@@ -253,7 +267,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
   __syncthreads();
   tc::fence_after();
   int64_t total = 0, before = incl - mine;
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {  // (a warp's run of sequences)
     if (w < warp) before += ms->scan64[w];
     total += ms->scan64[w];
   }
@@ -293,6 +307,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     // ------------------------------------------------------------ loads
     const int pg = lane & 3, half = (lane >> 2) & 1;  // page of the tile, slot of a block
     uint32_t issued = 0;  // slots whose last load may be in flight, for the drain
+    int tile = 0;
     while (ok && walk.next()) {
       const int32_t* row = pages.block_table + static_cast<int64_t>(walk.b) * pages.max_blocks;
       auto block_id = [&](int t) -> int {  // of this lane's page of tile t; -1: zero rows
@@ -305,8 +320,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       };
       const int n_tiles = walk.tiles();
       int next_blk = block_id(0);
-      for (int t = 0; ok && t < n_tiles; ++t) {
-        const int y = next_blk * kBlockSize;
+      for (int t = 0; ok && t < n_tiles; ++t, ++tile) {
+        const int blk = next_blk, y = blk * kBlockSize;
         if (t + 1 < n_tiles) next_blk = block_id(t + 1);
         for (int u = 0; u <= C::kBlocks; ++u) {  // rope unit, then the blocks
           const int n = u == 0 ? 1 : C::kSlotsPerBlock;
@@ -314,7 +329,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
           const int s = rg.take<C::kSlots>(n, parity);
           if (lane < n) {
             ok = mbar_wait(&ms->empty[s + lane], (parity >> (s + lane) & 1u) ^ 1u) && !*abort_flag;
-            if (ok) mbar_arrive_expect_tx(&ms->full[s + lane], kSlotBytes);
+            if (ok)
+              mbar_arrive_expect_tx(&ms->full[s + lane], kSlotBytes + (FP8 && u == 0 ? C::kScaleBytes : 0));
           }
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -323,6 +339,11 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
           if (lane < kPages * n)
             lat::tma_box(smem_u32(ring + (s + half) * kSlotBytes + pg * 2048), &pool_map,
                          &ms->full[s + half], x, y, 0);
+          if (FP8 && u == 0 && lane < kPages)
+            lat::bulk_load(smem_u32(scales + (tile % C::kScaleTiles) * C::kScaleBytes + lane * 64),
+                           blk >= 0 ? pages.row_scale + static_cast<int64_t>(blk) * kBlockSize
+                                    : reinterpret_cast<const float*>(g_zero_scales),
+                           kBlockSize * 4, &ms->full[s]);
         }
       }
     }
@@ -333,87 +354,86 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       for (int s = 0; s < C::kSlots; ++s)
         if (issued >> s & 1u) mbar_wait(&ms->full[s], ((rg.phase >> s) & 1u) ^ 1u);
     }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMAs
-    // The whole warp walks along, converged; one lane issues. Descriptors are a
-    // base, the slot's place in it, and offsets known when compiling.
-    const uint32_t id_s = FP8 ? lat::idesc_e4m3_f32(kTile, C::kQRows, 0, 0)
-                              : tc::idesc_bf16_f32(kTile, C::kQRows, 0, 0);
-    const uint32_t id_o = FP8 ? lat::idesc_e4m3_f32(128, C::kPCols, 1, 1)
-                              : tc::idesc_bf16_f32(128, C::kPCols, 1, 1);
+  } else if (warp >= kScoreWarp) {
+    // ------------------------------------------------------------ MMAs of S and of O
+    // Two warps, so that neither product waits for the other's data. A warp
+    // walks along converged and one lane issues; descriptors are a base, the
+    // slot's place in it, and offsets known when compiling.
+    const bool one = lat::elect_one();
+    const uint64_t k_desc = tc::smem_desc(smem_u32(ring), 16, 1024, tc::kSwizzle128B);
+    constexpr uint32_t kSlotStep = kSlotBytes >> 4;
     auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
       if (FP8) lat::mma_ss_fp8(d, a, b, id, acc);
       else tc::mma_ss(d, a, b, id, acc);
     };
-    const uint64_t q_desc = tc::smem_desc(smem_u32(q_smem), 16, 1024, tc::kSwizzle128B);
-    const uint64_t k_desc = tc::smem_desc(smem_u32(ring), 16, 1024, tc::kSwizzle128B);
-    const uint64_t v_desc = tc::smem_desc(smem_u32(ring), kSlotBytes, 1024, tc::kSwizzle128B);
-    const uint64_t p_desc = tc::smem_desc(smem_u32(ring), 1024, 1024, tc::kSwizzle128B);
-    constexpr uint32_t kSlotStep = kSlotBytes >> 4;
-    const bool one = lat::elect_one();
-    int slot[2][1 + C::kBlocks];  // of the tile S is formed for, and of the one before
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u));
-    };
-    auto scores = [&](int tile, int (&sl)[1 + C::kBlocks]) {
-      const uint32_t d = tmem + (tile & 1) * C::kQRows;
-#pragma unroll
-      for (int u = 0; u <= C::kBlocks; ++u) {
-        uint32_t parity;
-        const int n_ch = u == 0 ? 1 : C::kSlotsPerBlock;
-        sl[u] = rg.take<C::kSlots>(n_ch, parity);
-#pragma unroll
-        for (int c = 0; c < n_ch; ++c) {
-          ok = ok && wait(&ms->full[sl[u] + c], parity >> (sl[u] + c));
-          if (!ok) return;
-          tc::fence_after();
-          const uint64_t kd = k_desc + (sl[u] + c) * kSlotStep;
-          const uint64_t qd =
-              q_desc + static_cast<uint32_t>((u == 0 ? C::kQChunks - 1 : (u - 1) * C::kSlotsPerBlock + c) *
-                                             C::kQChunkBytes >> 4);
-          if (one) {
-#pragma unroll
-            for (int k = 0; k < (u == 0 ? C::kRopeSteps : 4); ++k)
-              mma(d, kd + k * 2, qd + k * 2, id_s, (u > 0 || k > 0) ? 1u : 0u);
-          }
-        }
-      }
-      if (one) tc::commit(&ms->s_full[tile & 1]);
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u) && *abort_flag == 0);
     };
     int seg = 0, tile = 0;
     for (; ok && walk.next(); ++seg) {
       const int n_tiles = walk.tiles();
-      ok = wait(&ms->q_full, seg);
-      if (ok) scores(tile, slot[0]);
+      if (warp == kScoreWarp) ok = wait(&ms->q_full, seg);
       for (int t = 0; ok && t < n_tiles; ++t, ++tile) {
-        if (t + 1 < n_tiles) scores(tile + 1, slot[1]);
-        ok = ok && wait(&ms->p_full, tile) && (t > 0 || seg == 0 || wait(&ms->o_free, seg - 1)) &&
-             __all_sync(0xffffffffu, *abort_flag == 0);
-        if (!ok) break;
-        tc::fence_after();
-        const uint64_t pd = p_desc + slot[0][0] * kSlotStep;
+        int slot[1 + C::kBlocks];
+        uint32_t parity[1 + C::kBlocks];
 #pragma unroll
-        for (int m = 0; m < C::kBlocks; ++m) {
-          const uint64_t vd = v_desc + slot[0][1 + m] * kSlotStep;
-          if (one) {
+        for (int u = 0; u <= C::kBlocks; ++u)
+          slot[u] = rg.take<C::kSlots>(u == 0 ? 1 : C::kSlotsPerBlock, parity[u]);
+        if (warp == kScoreWarp) {
+          const uint32_t id_s = FP8 ? lat::idesc_e4m3_f32(kTile, C::kQRows, 0, 0)
+                                    : tc::idesc_bf16_f32(kTile, C::kQRows, 0, 0);
+          const uint64_t q_desc = tc::smem_desc(smem_u32(q_smem), 16, 1024, tc::kSwizzle128B);
+          const uint32_t d = tmem + (tile & 1) * C::kQRows;
+          // two tiles ago is over, its S read and its products done: no role is
+          // ever two phases of a barrier behind another
+          if (tile >= 2) ok = wait(&ms->pv_done[tile & 1], (tile >> 1) - 1);
 #pragma unroll
-            for (int k = 0; k < C::kPSteps; ++k) {
-              constexpr uint32_t kStep = C::kPStepBytes >> 4;
-              mma(tmem + C::kTmemO + m * C::kPCols, vd + k * kStep, pd + k * kStep, id_o,
-                  (t > 0 || k > 0) ? 1u : 0u);
+          for (int u = 0; u <= C::kBlocks; ++u) {
+#pragma unroll
+            for (int c = 0; c < (u == 0 ? 1 : C::kSlotsPerBlock); ++c) {
+              ok = ok && wait(&ms->full[slot[u] + c], parity[u] >> (slot[u] + c));
+              tc::fence_after();
+              const uint64_t kd = k_desc + (slot[u] + c) * kSlotStep;
+              const uint64_t qd =
+                  q_desc + static_cast<uint32_t>((u == 0 ? C::kQChunks - 1 : (u - 1) * C::kSlotsPerBlock + c) *
+                                                 C::kQChunkBytes >> 4);
+              if (ok && one) {
+#pragma unroll
+                for (int k = 0; k < (u == 0 ? C::kRopeSteps : 4); ++k)
+                  mma(d, kd + k * 2, qd + k * 2, id_s, (u > 0 || k > 0) ? 1u : 0u);
+              }
             }
+          }
+          if (ok && one) tc::commit(&ms->s_full[tile & 1]);
+        } else {
+          const uint32_t id_o = FP8 ? lat::idesc_e4m3_f32(128, C::kPCols, 1, 1)
+                                    : tc::idesc_bf16_f32(128, C::kPCols, 1, 1);
+          const uint64_t v_desc = tc::smem_desc(smem_u32(ring), kSlotBytes, 1024, tc::kSwizzle128B);
+          const uint64_t p_desc = tc::smem_desc(smem_u32(ring), 1024, 1024, tc::kSwizzle128B);
+          // (P comes after S, and S after the tile has landed)
+          ok = wait(&ms->p_full[tile & 1], tile >> 1) &&
+               (t > 0 || seg == 0 || wait(&ms->o_free, seg - 1));
+          tc::fence_after();
+          const uint64_t pd = p_desc + slot[0] * kSlotStep;
+          if (ok && one) {
 #pragma unroll
-            for (int c = 0; c < C::kSlotsPerBlock; ++c) tc::commit(&ms->empty[slot[0][1 + m] + c]);
+            for (int m = 0; m < C::kBlocks; ++m) {
+              const uint64_t vd = v_desc + slot[1 + m] * kSlotStep;
+#pragma unroll
+              for (int k = 0; k < C::kPSteps; ++k) {
+                constexpr uint32_t kStep = C::kPStepBytes >> 4;
+                mma(tmem + C::kTmemO + m * C::kPCols, vd + k * kStep, pd + k * kStep, id_o,
+                    (t > 0 || k > 0) ? 1u : 0u);
+              }
+#pragma unroll
+              for (int c = 0; c < C::kSlotsPerBlock; ++c) tc::commit(&ms->empty[slot[1 + m] + c]);
+            }
+            tc::commit(&ms->empty[slot[0]]);
+            tc::commit(&ms->pv_done[tile & 1]);
+            if (t == n_tiles - 1) tc::commit(&ms->o_full);
           }
         }
-        if (one) {
-          tc::commit(&ms->empty[slot[0][0]]);
-          tc::commit(&ms->pv_done);
-          if (t == n_tiles - 1) tc::commit(&ms->o_full);
-        }
         __syncwarp();
-#pragma unroll
-        for (int u = 0; u <= C::kBlocks; ++u) slot[0][u] = slot[1][u];
       }
     }
     if (one) {
@@ -503,41 +523,32 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       const Walk w = walk;
       more = walk.next();
       const int h0 = w.chunk * NH, nh = min(NH, heads - h0), n_tiles = w.tiles();
-      const int32_t* row = pages.block_table + static_cast<int64_t>(w.b) * pages.max_blocks;
-      auto scale_of = [&](int t, float (&ks)[2]) {  // FP8: the scales of this thread's rows of tile t
-        const int i = t * kPages + warp;
-        ks[0] = ks[1] = 0.f;
-        if (!FP8 || i >= w.seg_count) return;
-        const int blk = __ldg(row + w.span.first + w.seg_first + i);
-        if (blk < 0 || blk >= pages.num_blocks) return;
-        const float* p = pages.row_scale + static_cast<int64_t>(blk) * kBlockSize + (lane >> 2);
-        ks[0] = __ldg(p);
-        ks[1] = __ldg(p + 8);
-      };
       constexpr int HN = C::kHeads;
-      float m[HN], l[HN], vref = 0.f, ks[2];
-      scale_of(0, ks);
+      float m[HN], l[HN], vref = 0.f;
 #pragma unroll
       for (int i = 0; i < HN; ++i) m[i] = 0.f, l[i] = 0.f;
       for (int t = 0; t < n_tiles; ++t, ++tile) {
         const bool in_seg = t * kPages + warp < w.seg_count;  // a page per warp
         const int key = (w.span.first + w.seg_first + t * kPages + warp) * kBlockSize + (lane >> 2);
+        int slot[1 + C::kBlocks];
+        uint32_t parity[1 + C::kBlocks];
+#pragma unroll
+        for (int u = 0; u <= C::kBlocks; ++u)
+          slot[u] = rg.take<C::kSlots>(u == 0 ? 1 : C::kSlotsPerBlock, parity[u]);
+        ok = mbar_wait(&ms->s_full[tile & 1], (tile >> 1) & 1);
+        tc::fence_after();
         bool seen[2];
         float vs[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           seen[j] = in_seg && key + 8 * j >= w.span.lo && key + 8 * j < w.span.len;
-          vs[j] = seen[j] ? ks[j] : 0.f;  // a hidden slot's scale may be anything
+          // the row's scale (it landed with the rope unit, whose phase every
+          // reader looks at itself); a hidden slot's may be anything
+          if (FP8 && j == 0) ok = ok && mbar_wait(&ms->full[slot[0]], parity[0] >> slot[0] & 1u);
+          vs[j] = FP8 && seen[j]
+                      ? reinterpret_cast<const float*>(scales + (tile % C::kScaleTiles) * C::kScaleBytes)[r0 + 8 * j]
+                      : 0.f;
         }
-        if (t + 1 < n_tiles) scale_of(t + 1, ks);
-        int slot[1 + C::kBlocks];
-#pragma unroll
-        for (int u = 0; u <= C::kBlocks; ++u) {
-          uint32_t parity;
-          slot[u] = rg.take<C::kSlots>(u == 0 ? 1 : C::kSlotsPerBlock, parity);
-        }
-        ok = mbar_wait(&ms->s_full[tile & 1], (tile >> 1) & 1);
-        tc::fence_after();
         float z[2][HN];
         {
           uint32_t v[C::kQParts][NH / 2];
@@ -579,10 +590,12 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
           if (in_seg && !seen[j]) {
 #pragma unroll
             for (int u = 1; u <= C::kBlocks; ++u)
-              for (int c = 0; c < C::kSlotsPerBlock; ++c)
+              for (int c = 0; c < C::kSlotsPerBlock; ++c) {
+                ok = ok && mbar_wait(&ms->full[slot[u] + c], parity[u] >> (slot[u] + c) & 1u);
                 for (int i = 0; i < 2; ++i)
                   *reinterpret_cast<uint4*>(ring + (slot[u] + c) * kSlotBytes + (r0 + 8 * j) * 128 +
                                             quad * 32 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+              }
           }
         }
         bool move = !ok || t == 0 || over > C::kLag;
@@ -601,7 +614,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             if (lane == 0) ms->vred[warp] = x;
           }
           // O is rescaled below: the products up to the tile before have ended
-          if (t > 0 && ok) ok = mbar_wait(&ms->pv_done, (tile - 1) & 1);
+          if (t > 0 && ok) ok = mbar_wait(&ms->pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
           if (lat::bar_any(1, kSoftThreads, !ok)) {
             ok = false;
             break;
@@ -688,7 +701,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         fence_proxy_async_smem();
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ms->p_full);
+        if (lane == 0) mbar_arrive(&ms->p_full[tile & 1]);
       }
       if (!ok) break;
       // ---- the segment's end. S of its last tile is done: Q may be replaced
@@ -775,84 +788,84 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
   __syncwarp();
   tc::fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) tc::dealloc(tmem, 512);
+  if (warp == kScoreWarp) tc::dealloc(tmem, 512);
 }
 
 // Joins what the pieces of a unit left: out = sum_i 2^(m_i - M) O_i / sum_i
-// 2^(m_i - M) l_i. One CTA per (sequence, head), a thread per L / 128 dims; a
-// unit that one piece covered is left alone, an empty sequence gets its zeros.
+// 2^(m_i - M) l_i. One CTA per (sequence, head); a group of L / 4 threads, four
+// dims each, takes every groups-th piece, and the groups' sums meet in shared
+// memory. A unit that one piece covered is left alone, an empty sequence gets
+// its zeros.
+constexpr int kMergeThreads = 512;
 template <int LAT>
-__global__ void __launch_bounds__(128)
-latent_merge_kernel(const int32_t* __restrict__ seq_lens, int heads, int max_blocks,
+__global__ void __launch_bounds__(kMergeThreads)
+latent_merge_kernel(const int32_t* __restrict__ seq_lens, int heads,
                     const Part* __restrict__ parts, const float2* __restrict__ part_ml,
                     const float* __restrict__ part_o, __nv_bfloat16* __restrict__ out,
                     float* __restrict__ lse) {
-  constexpr int kPer = LAT / 128;
-  __shared__ float s_w[kMaxCtas], s_red[8];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
+  constexpr int kRow = LAT / 4;  // threads of a group
+  __shared__ float s_w[kMaxCtas];
+  __shared__ float4 s_o[kMergeThreads];
+  const int b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+  const int group = tid / kRow, groups = blockDim.x / kRow, col = tid - group * kRow;
   const int nh = chunk_heads(heads), chunk = h / nh, hc = h - chunk * nh;
-  __nv_bfloat16* dst = out + (static_cast<int64_t>(b) * heads + h) * LAT + tid * kPer;
-  if (seq_lens[b] <= 0) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) dst[i] = __float2bfloat16_rn(0.f);
-    if (lse != nullptr && tid == 0) lse[static_cast<int64_t>(b) * heads + h] = -INFINITY;
+  const int64_t row = static_cast<int64_t>(b) * heads + h;
+  uint2* dst = reinterpret_cast<uint2*>(out + row * LAT) + col;
+  const int len = __ldg(seq_lens + b);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (len <= 0) {
+    if (group == 0) *dst = make_uint2(0u, 0u);
+    if (lse != nullptr && tid == 0) lse[row] = -INFINITY;
     return;
   }
   const Part pt = parts[b * chunks_of(heads) + chunk];
   if (pt.x < 0) return;
   const int n = pt.y - pt.x + 1;
   auto slot = [&](int i) { return i == 0 ? 2 * pt.x + 1 : 2 * (pt.x + i); };
-  float mx = -INFINITY;
-  float2 ml[2];
+  // every warp forms the pieces' weights by itself
+  float2 ml[kMaxCtas / 32];
+  float mx = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int i = tid + k * 128;
+  for (int k = 0; k < kMaxCtas / 32; ++k) {
+    const int i = lane + k * 32;
     ml[k] = i < n ? part_ml[slot(i) * kMaxHeads + hc] : make_float2(-INFINITY, 0.f);
     mx = fmaxf(mx, ml[k].x);
   }
   mx = lat::warp_max(mx);
-  if ((tid & 31) == 0) s_red[tid >> 5] = mx;
-  __syncthreads();
-  mx = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
-  float l = 0.f;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int i = tid + k * 128;
-    if (i < n) {
-      const float w = ex2_approx(ml[k].x - mx);
-      s_w[i] = w;
-      l += w * ml[k].y;
-    }
+  for (int k = 0; k < kMaxCtas / 32; ++k) {
+    const int i = lane + k * 32;
+    const float w = i < n ? ex2_approx(ml[k].x - mx) : 0.f;
+    if (tid < 32 && i < n) s_w[i] = w;
+    l = fmaf(w, ml[k].y, l);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if ((tid & 31) == 0) s_red[4 + (tid >> 5)] = l;
   __syncthreads();
-  l = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
-  float acc[kPer] = {};
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int i = 0; i < n; ++i) {
-    const float* src = part_o + (static_cast<int64_t>(slot(i)) * kMaxHeads + hc) * LAT + tid * kPer;
+  for (int i = group; i < n; i += groups) {
+    const float4 v = __ldcg(
+        reinterpret_cast<const float4*>(part_o + (static_cast<int64_t>(slot(i)) * kMaxHeads + hc) * LAT) + col);
     const float w = s_w[i];
-    if (kPer == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      acc[0] = fmaf(w, v.x, acc[0]);
-      acc[1] = fmaf(w, v.y, acc[1]);
-      acc[kPer - 2] = fmaf(w, v.z, acc[kPer - 2]);
-      acc[kPer - 1] = fmaf(w, v.w, acc[kPer - 1]);
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(src);
-      acc[0] = fmaf(w, v.x, acc[0]);
-      acc[1] = fmaf(w, v.y, acc[1]);
-    }
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
+  }
+  s_o[tid] = acc;
+  __syncthreads();
+  if (group != 0) return;
+  for (int g = 1; g < groups; ++g) {
+    const float4 v = s_o[g * kRow + col];
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int i = 0; i < kPer; i += 2)
-    *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-  if (lse != nullptr && tid == 0)
-    lse[static_cast<int64_t>(b) * heads + h] = (mx + __log2f(l)) * lat::kLn2;
+  *dst = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (lse != nullptr && tid == 0) lse[row] = (mx + __log2f(l)) * lat::kLn2;
 }
 
 struct Layout {
@@ -899,7 +912,12 @@ int launch(const LatentArgs& L, const void* q, const LatentPages& pages, const i
   // the join may be launched while the pieces still run; it waits for them
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(n_seqs, L.n_heads);
-  cfg.blockDim = dim3(128);
+  // pieces a unit has on average, eight loads in flight per group of threads
+  const int64_t units = static_cast<int64_t>(n_seqs) * chunks_of(L.n_heads);
+  const int row_threads = L.latent / 4;
+  const int want = static_cast<int>(1 + (grid / units) / 8);
+  const int fit = kMergeThreads / row_threads;
+  cfg.blockDim = dim3(row_threads * (want < fit ? want : fit));
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -907,7 +925,7 @@ int launch(const LatentArgs& L, const void* q, const LatentPages& pages, const i
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(
-      &cfg, latent_merge_kernel<LAT>, seq_lens, L.n_heads, pages.max_blocks,
+      &cfg, latent_merge_kernel<LAT>, seq_lens, L.n_heads,
       static_cast<const Part*>(parts), static_cast<const float2*>(ml),
       static_cast<const float*>(o), ob, lse);
   return e == cudaSuccess ? PSW_OK : PSW_ELAUNCH;

@@ -152,7 +152,7 @@ int make_pool_tensor_map(CUtensorMap* map, const void* pool, int64_t num_blocks,
 int make_pool_page_map(CUtensorMap* map, const void* pool, int64_t num_blocks, int n_kv, int hd,
                        int box_slots, int box_chunks);
 
-// 3-D TMA descriptor, 128-byte swizzle, of bf16 elements (or of single bytes):
+// 3-D TMA descriptor, 128-byte swizzle, of bf16 elements or of single bytes:
 // dims innermost first, strides in bytes of dims 1 and 2. Returns a PSW_* code.
 int make_map_3d(CUtensorMap* map, bool bytes, const void* base, const int64_t (&dims)[3],
                 const int64_t (&strides)[2], const int (&box)[3]);
