@@ -47,8 +47,8 @@ constexpr int kTile = 64;                       // keys of a tile
 constexpr int kPages = kTile / kBlockSize;      // pages of a tile
 constexpr int kSlotBytes = kTile * 128;
 constexpr int kSoftThreads = 128;               // warps 0-3
-constexpr int kLoadWarp = 4, kScoreWarp = 5, kValueWarp = 6;  // loads; MMAs of S; of O
-constexpr int kThreads = 224;
+constexpr int kScoreWarp = 4, kValueWarp = 5;   // MMAs of S, of O
+constexpr int kLoadWarp = 6;                    // and 7 with FP8 pages
 constexpr int kMaxCtas = 160;                   // pieces of the page list
 constexpr int kMinPages = 4;                    // pages a piece has at least
 constexpr int kMaxHeads = 32;                   // heads of a chunk
@@ -73,18 +73,22 @@ struct Cfg {
   static constexpr int kRopeSteps = FP8 ? 2 : 4;       // 32-byte MMA steps of the rope chunk
   static constexpr int kPSteps = FP8 ? 2 : 4;          // MMA steps along the keys
   static constexpr int kPStepBytes = kTile / kPSteps * 128;
+  static constexpr int kLoadWarps = FP8 ? 2 : 1;
+  static constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
   static constexpr int kMisc = FP8 ? 6144 : 2048;
-  static constexpr int kSlots = (kSmemLimit - 1024 - kMisc - kQBytes) / kSlotBytes;
+  static constexpr int kTileSlots = 1 + kBlocks * kSlotsPerBlock;
+  static constexpr int kSlotsFit = (kSmemLimit - 1024 - kMisc - kQBytes) / kSlotBytes;
+  static constexpr int kSlots = FP8 ? kSlotsFit / kTileSlots * kTileSlots : kSlotsFit;
   static constexpr int kSmemBytes = 1024 + kQBytes + kSlots * kSlotBytes + kMisc;
   static constexpr int kTmemO = 2 * kQRows;            // after the two S^T buffers
   static_assert(kTmemO + kBlocks * kPCols <= 512, "tensor memory columns");
-  static_assert(kSlots >= 2 * (1 + kBlocks * kSlotsPerBlock) + 1,
-                "two tiles fit, a slot left out included");
+  static_assert(kSlots >= 2 * kTileSlots + (FP8 ? kTileSlots : 1),
+                "two tiles fit, a slot left out included; three with FP8 pages");
   // FP8: row scales of the tiles in the ring, in turn (after the misc block)
   static constexpr int kScaleTiles = 16;
   static constexpr int kScales = 2048, kScaleBytes = kTile * 4;
   static_assert(!FP8 || (kScales + kScaleTiles * kScaleBytes <= kMisc &&
-                         kSlots / (1 + kBlocks * kSlotsPerBlock) + 2 <= kScaleTiles),
+                         kSlots / kTileSlots + 2 <= kScaleTiles),
                 "no tile's scales are overwritten while it is in the ring");
   static constexpr int kHeads = NH / 4;                // heads of a softmax thread
   static_assert(kSlots <= 32, "phase bits");
@@ -102,7 +106,8 @@ struct Misc {
   int32_t unit0, page0;      // this CTA's first unit and the page within it
   uint32_t tmem;
   int32_t abort;
-  int64_t scan64[8];
+  int64_t total, p0, p1;     // pages of all units; this CTA's piece of them
+  int32_t pieces;
   float red[4][kMaxHeads];
   float vred[4];
   float qs[kMaxHeads];       // FP8: scale * log2(e) * what a unit of q's codes stands for
@@ -110,9 +115,6 @@ struct Misc {
   float alpha[kMaxHeads];    // factors of a rescale; at a segment's end, the maxima
 };
 static_assert(sizeof(Misc) <= 2048, "misc block");
-
-// Row scales of a page that is not there (its codes read as zeros).
-__device__ const float4 g_zero_scales[kBlockSize / 4] = {};
 
 // Visible pages of one sequence.
 struct Span {
@@ -127,6 +129,13 @@ __device__ __forceinline__ Span span_of(int raw, int window, int max_blocks) {
   s.first = s.lo / kBlockSize;
   s.count = s.len > 0 ? (s.len - 1) / kBlockSize - s.first + 1 : 0;
   return s;
+}
+
+// First page of piece i of n.
+__device__ __forceinline__ int64_t share_of(int64_t total, int i, int n) {
+  if (total < (1 << 23))  // times up to kMaxCtas fits 32 bits
+    return static_cast<uint32_t>(total) * static_cast<uint32_t>(i) / static_cast<uint32_t>(n);
+  return total * i / n;
 }
 
 struct Part {  // what a unit's pieces left behind, per unit: pieces [x, y], x < 0: none
@@ -194,7 +203,7 @@ __device__ __forceinline__ float2 e4m3_values(uint32_t pair) {
 }
 
 template <int LAT, int NH, bool FP8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<LAT, NH, FP8>::kThreads, 1)
 latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                      const __grid_constant__ CUtensorMap pool_map, const LatentPages pages,
                      const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ seq_lens,
@@ -214,82 +223,91 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may queue up
 
-  // ---- this CTA's piece of the page list: every CTA adds up all spans (a run
-  // of sequences per thread) and the thread whose run holds its first page
-  // finds the unit
-  const int per = (n_seqs + kThreads - 1) / kThreads;
-  const int b0 = min(n_seqs, tid * per), b1 = min(n_seqs, b0 + per);
-  const int raw0 = b0 < b1 ? __ldg(seq_lens + b0) : 0;  // in flight during the set-up
-  if (warp == kScoreWarp) {
-    tc::alloc(&ms->tmem, 512);
-    tc::relinquish();
-  }
-  if (warp == kLoadWarp && lane == 0) {
-    prefetch_tensormap(&pool_map);
-    prefetch_tensormap(&q_map);
-  }
-  if (tid == 0) {
-    for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(&ms->full[i], 1);
-      mbar_init(&ms->empty[i], 1);
-    }
-    mbar_init(&ms->q_full, FP8 ? 4 : 1);
-    mbar_init(&ms->s_full[0], 1);
-    mbar_init(&ms->s_full[1], 1);
-    mbar_init(&ms->p_full[0], 4);
-    mbar_init(&ms->p_full[1], 4);
-    mbar_init(&ms->pv_done[0], 1);
-    mbar_init(&ms->pv_done[1], 1);
-    mbar_init(&ms->o_full, 1);
-    mbar_init(&ms->o_free, 4);
-    mbar_init(&ms->drained, 2);
-    ms->abort = 0;
-    fence_mbar_init();
-  }
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int raw = b == b0 ? raw0 : __ldg(seq_lens + b);
-    mine += static_cast<int64_t>(span_of(raw, window, pages.max_blocks).count) * chunks;
-    if (blockIdx.x == 0) {
-      if (raw < 0) flag_error(err, PSW_DEVERR_LENGTH);
-      if (raw > static_cast<int64_t>(pages.max_blocks) * kBlockSize)
-        flag_error(err, PSW_DEVERR_CAPACITY);
-    }
-  }
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) ms->scan64[warp] = incl;
-  tc::fence_before();
-  __syncthreads();
-  tc::fence_after();
-  int64_t total = 0, before = incl - mine;
-  for (int w = 0; w < kThreads / 32; ++w) {  // (a warp's run of sequences)
-    if (w < warp) before += ms->scan64[w];
-    total += ms->scan64[w];
-  }
-  const int64_t want = (total + kMinPages - 1) / kMinPages;
-  const int pieces = static_cast<int>(min(static_cast<int64_t>(gridDim.x), want));
-  const int64_t p0 = blockIdx.x < pieces ? total * blockIdx.x / pieces : 0;
-  const int64_t p1 = blockIdx.x < pieces ? total * (blockIdx.x + 1) / pieces : 0;
-  if (p0 < p1 && p0 >= before && p0 < before + mine) {
-    int64_t at = before;
+  if (warp == kLoadWarp) {
+    // ---- set-up and this CTA's piece of the page list, by the warp whose loads
+    // everything waits for: it adds up all spans, a run of sequences per lane,
+    // and the lane whose run holds the piece's first page finds the unit
+    const int per = (n_seqs + 31) / 32;
+    const int b0 = min(n_seqs, lane * per), b1 = min(n_seqs, b0 + per);
+    int64_t mine = 0;
+#pragma unroll 4
     for (int b = b0; b < b1; ++b) {
-      const int n = span_of(__ldg(seq_lens + b), window, pages.max_blocks).count;
-      if (p0 < at + static_cast<int64_t>(n) * chunks) {
-        const int c = static_cast<int>((p0 - at) / n);
-        ms->unit0 = b * chunks + c;
-        ms->page0 = static_cast<int>(p0 - at - static_cast<int64_t>(c) * n);
-        break;
+      const int raw = __ldg(seq_lens + b);
+      mine += static_cast<int64_t>(span_of(raw, window, pages.max_blocks).count) * chunks;
+      if (blockIdx.x == 0) {
+        if (raw < 0) flag_error(err, PSW_DEVERR_LENGTH);
+        if (raw > static_cast<int64_t>(pages.max_blocks) * kBlockSize)
+          flag_error(err, PSW_DEVERR_CAPACITY);
       }
-      at += static_cast<int64_t>(n) * chunks;
     }
+    if (lane == 0) {
+      for (int i = 0; i < C::kSlots; ++i) {
+        mbar_init(&ms->full[i], C::kLoadWarps);
+        mbar_init(&ms->empty[i], 1);
+      }
+      mbar_init(&ms->q_full, FP8 ? 4 : 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&ms->s_full[i], 1);
+        mbar_init(&ms->p_full[i], 4);
+        mbar_init(&ms->pv_done[i], 1);
+      }
+      mbar_init(&ms->o_full, 1);
+      mbar_init(&ms->o_free, 4);
+      mbar_init(&ms->drained, 2);
+      ms->abort = 0;
+      fence_mbar_init();
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const int64_t total = __shfl_sync(0xffffffffu, incl, 31), before = incl - mine;
+    const int64_t most = (total + kMinPages - 1) / kMinPages;
+    const int pieces = most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
+    const bool work = static_cast<int>(blockIdx.x) < pieces;
+    const int64_t p0 = work ? share_of(total, blockIdx.x, pieces) : 0;
+    const int64_t p1 = work ? share_of(total, blockIdx.x + 1, pieces) : 0;
+    if (p0 < p1 && p0 >= before && p0 < before + mine) {
+      int64_t at = before;
+      for (int b = b0; b < b1; ++b) {
+        const int n = span_of(__ldg(seq_lens + b), window, pages.max_blocks).count;
+        const int64_t end = at + static_cast<int64_t>(n) * chunks;
+        if (p0 < end) {
+          int c = 0;
+          for (; p0 >= at + n; at += n) ++c;
+          ms->unit0 = b * chunks + c;
+          ms->page0 = static_cast<int>(p0 - at);
+          break;
+        }
+        at = end;
+      }
+    }
+    if (lane == 0) {
+      ms->total = total;
+      ms->pieces = pieces;
+      ms->p0 = p0;
+      ms->p1 = p1;
+    }
+    __threadfence_block();
+    __syncwarp();
+    asm volatile("bar.arrive 2, %0;" ::"r"(C::kThreads) : "memory");  // goes straight on
+  } else {
+    if (warp == kScoreWarp) {
+      tc::alloc(&ms->tmem, 512);
+      tc::relinquish();
+    }
+    if (warp == kValueWarp && lane == 0) {
+      prefetch_tensormap(&pool_map);
+      prefetch_tensormap(&q_map);
+    }
+    tc::fence_before();
+    named_bar_sync(2, C::kThreads);
+    tc::fence_after();
   }
-  __syncthreads();
-  const uint32_t tmem = ms->tmem;
+  const int64_t p1 = ms->p1;
+  const uint32_t tmem = warp == kLoadWarp ? 0u : ms->tmem;  // (may not be there yet)
   volatile int32_t* abort_flag = &ms->abort;
   Walk walk;
   walk.seq_lens = seq_lens;
@@ -297,62 +315,135 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
   walk.max_blocks = pages.max_blocks;
   walk.chunks = chunks;
   walk.n_seqs = n_seqs;
-  walk.left = p1 - p0;
-  walk.unit = p0 < p1 ? ms->unit0 : 0;
-  walk.page = p0 < p1 ? ms->page0 : 0;
+  walk.left = p1 - ms->p0;
+  walk.unit = walk.left > 0 ? ms->unit0 : 0;
+  walk.page = walk.left > 0 ? ms->page0 : 0;
   Ring rg;
   bool ok = true;
 
-  if (warp == kLoadWarp) {
+  if (warp >= kLoadWarp) {
     // ------------------------------------------------------------ loads
-    const int pg = lane & 3, half = (lane >> 2) & 1;  // page of the tile, slot of a block
-    uint32_t issued = 0;  // slots whose last load may be in flight, for the drain
-    int tile = 0;
-    while (ok && walk.next()) {
-      const int32_t* row = pages.block_table + static_cast<int64_t>(walk.b) * pages.max_blocks;
-      auto block_id = [&](int t) -> int {  // of this lane's page of tile t; -1: zero rows
-        const int i = t * kPages + pg;
-        if (i >= walk.seg_count) return -1;
-        const int blk = __ldg(row + walk.span.first + walk.seg_first + i);
-        if (blk >= 0 && blk < pages.num_blocks) return blk;
-        flag_error(err, PSW_DEVERR_BLOCK_ID);
-        return -1;
-      };
-      const int n_tiles = walk.tiles();
-      int next_blk = block_id(0);
-      for (int t = 0; ok && t < n_tiles; ++t, ++tile) {
-        const int blk = next_blk, y = blk * kBlockSize;
-        if (t + 1 < n_tiles) next_blk = block_id(t + 1);
-        for (int u = 0; u <= C::kBlocks; ++u) {  // rope unit, then the blocks
-          const int n = u == 0 ? 1 : C::kSlotsPerBlock;
-          uint32_t parity;
-          const int s = rg.take<C::kSlots>(n, parity);
-          if (lane < n) {
-            ok = mbar_wait(&ms->empty[s + lane], (parity >> (s + lane) & 1u) ^ 1u) && !*abort_flag;
-            if (ok)
-              mbar_arrive_expect_tx(&ms->full[s + lane], kSlotBytes + (FP8 && u == 0 ? C::kScaleBytes : 0));
+    // block id of page i of the segment; -1: zero rows
+    auto block_id = [&](int i) -> int {
+      if (i >= walk.seg_count) return -1;
+      const int blk = __ldg(pages.block_table + static_cast<int64_t>(walk.b) * pages.max_blocks +
+                            walk.span.first + walk.seg_first + i);
+      if (blk >= 0 && blk < pages.num_blocks) return blk;
+      flag_error(err, PSW_DEVERR_BLOCK_ID);
+      return -1;
+    };
+    if constexpr (!FP8) {
+      // TMA boxes of 16 rows x 128 bytes, issued by one lane of the converged
+      // warp (issued by a lane each, a box costs 90 cycles: longer than it takes
+      // to arrive)
+      const bool one = lat::elect_one();
+      uint32_t issued = 0;  // slots whose last load may be in flight, for the drain
+      while (ok && walk.next()) {
+        const int n_tiles = walk.tiles();
+        int next_blk = block_id(lane & 3);
+        for (int t = 0; ok && t < n_tiles; ++t) {
+          int y[kPages];
+#pragma unroll
+          for (int pg = 0; pg < kPages; ++pg)
+            y[pg] = __shfl_sync(0xffffffffu, next_blk, pg) * kBlockSize;
+          if (t + 1 < n_tiles) next_blk = block_id((t + 1) * kPages + (lane & 3));
+#pragma unroll
+          for (int u = 0; u <= C::kBlocks; ++u) {  // rope unit, then the blocks
+            const int n = u == 0 ? 1 : C::kSlotsPerBlock;
+            uint32_t parity;
+            const int s = rg.take<C::kSlots>(n, parity);
+#pragma unroll
+            for (int c = 0; c < n; ++c) {
+              ok = ok && mbar_wait(&ms->empty[s + c], (parity >> (s + c) & 1u) ^ 1u);
+              if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+              }
+              issued |= 1u << (s + c);
+              if (one) {
+                mbar_arrive_expect_tx(&ms->full[s + c], kSlotBytes);
+#pragma unroll
+                for (int pg = 0; pg < kPages; ++pg)
+                  lat::tma_box(smem_u32(ring + (s + c) * kSlotBytes + pg * 2048), &pool_map,
+                               &ms->full[s + c], u == 0 ? LAT : (u - 1) * 128 + c * 64, y[pg], 0);
+              }
+            }
+            if (!ok) break;
           }
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          issued |= ((1u << n) - 1u) << s;
-          const int x = u == 0 ? LAT : (u - 1) * 128 + half * 64;
-          if (lane < kPages * n)
-            lat::tma_box(smem_u32(ring + (s + half) * kSlotBytes + pg * 2048), &pool_map,
-                         &ms->full[s + half], x, y, 0);
-          if (FP8 && u == 0 && lane < kPages)
-            lat::bulk_load(smem_u32(scales + (tile % C::kScaleTiles) * C::kScaleBytes + lane * 64),
-                           blk >= 0 ? pages.row_scale + static_cast<int64_t>(blk) * kBlockSize
-                                    : reinterpret_cast<const float*>(g_zero_scales),
-                           kBlockSize * 4, &ms->full[s]);
+          ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
         }
       }
-    }
-    if (!ok && lane == 0) {
-      *abort_flag = 1;
-      flag_error(err, PSW_DEVERR_PIPELINE);
-      // copies in flight land before the CTA ends: the last phase of each slot
-      for (int s = 0; s < C::kSlots; ++s)
-        if (issued >> s & 1u) mbar_wait(&ms->full[s], ((rg.phase >> s) & 1u) ^ 1u);
+      if (!ok && lane == 0) {
+        *abort_flag = 1;
+        flag_error(err, PSW_DEVERR_PIPELINE);
+        // copies in flight land before the CTA ends: the last phase of each slot
+        for (int s = 0; s < C::kSlots; ++s)
+          if (issued >> s & 1u) mbar_wait(&ms->full[s], ((rg.phase >> s) & 1u) ^ 1u);
+      }
+    } else {
+      // An FP8 row is 4.5 or 2.5 lines long, so that boxes of 128 bytes straddle
+      // lines, and the SM's rate is one of lines (a TMA loader took 137 cycles a
+      // box, 91 with the aligned bf16 rows). Here a page, whole lines in a row,
+      // is read front to back with 16-byte asynchronous copies into the same
+      // swizzled rows. A tile is announced kAhead tiles after its issue, when
+      // its copies have been waited for and fenced for the tensor core.
+      constexpr int kRow = LAT + kLatentRope, kCopies = kBlockSize * kRow / 512;
+      constexpr int kStages = C::kSlots / C::kTileSlots, kAhead = kStages - 2;
+      int dst[kCopies];  // where this lane's vectors of a page go, from the tile's first slot
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) {
+        const int o = i * 512 + lane * 16, r = o / kRow, x = o - r * kRow;
+        const int slot = x >= LAT ? 0 : 1 + x / 128;
+        dst[i] = slot * kSlotBytes + r * 128 + ((((x & 127) >> 4) ^ (r & 7)) << 4);
+      }
+      const uint32_t ring_at = smem_u32(ring), scales_at = smem_u32(scales);
+      const auto* pool = static_cast<const uint8_t*>(pages.pool);
+      const int lw = warp - kLoadWarp;
+      int tile = 0, told = 0;  // tiles issued, tiles announced
+      auto announce = [&]() {  // (after this lane's copies of the tile have landed)
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane < C::kTileSlots)
+          mbar_arrive(&ms->full[told % kStages * C::kTileSlots + lane]);
+        ++told;
+      };
+      while (ok && walk.next()) {
+        const int n_tiles = walk.tiles();
+        int next_blk = lane < 2 ? block_id(lw + 2 * lane) : -1;  // lanes 0 and 1: this warp's pages
+        for (int t = 0; ok && t < n_tiles; ++t, ++tile) {
+          const int blks = next_blk;
+          if (t + 1 < n_tiles && lane < 2) next_blk = block_id((t + 1) * kPages + lw + 2 * lane);
+          const int s = tile % kStages * C::kTileSlots;
+          if (lane < C::kTileSlots)
+            ok = mbar_wait(&ms->empty[s + lane], (tile / kStages & 1u) ^ 1u) && !*abort_flag;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int pg = lw + 2 * k, blk = __shfl_sync(0xffffffffu, blks, k);
+            const uint32_t bytes = blk >= 0 ? 16u : 0u;  // 0: the destination becomes zero
+            const uint8_t* src = pool + static_cast<int64_t>(max(blk, 0)) * (kBlockSize * kRow) + lane * 16;
+            const uint32_t to = ring_at + s * kSlotBytes + pg * 2048;
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) lat::copy16(to + dst[i], src + i * 512, bytes);
+            if (lane < 4)
+              lat::copy16(scales_at + tile % C::kScaleTiles * C::kScaleBytes + pg * 64 + lane * 16,
+                          pages.row_scale + static_cast<int64_t>(max(blk, 0)) * kBlockSize + lane * 4, bytes);
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (tile >= kAhead) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+            announce();
+          }
+        }
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      if (ok) {
+        while (told < tile) announce();
+      } else if (lane == 0) {
+        *abort_flag = 1;
+        flag_error(err, PSW_DEVERR_PIPELINE);
+      }
     }
   } else if (warp >= kScoreWarp) {
     // ------------------------------------------------------------ MMAs of S and of O
@@ -463,10 +554,12 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         // warp by warp, a head at a time: its largest value gives the power of
         // two; the value is the sum of the two parts, the second 16 times up
         constexpr int kRow = LAT + kLatentRope, kPairs = kRow / 2, kWords = (kPairs + 31) / 32;
-        uint32_t raw[NH / 4][kWords];  // all loads in flight at once
+#pragma unroll 1
+        for (int j0 = 0; j0 < NH / 4; j0 += 4) {
+        uint32_t raw[4][kWords];  // the loads of four heads in flight at once
 #pragma unroll
-        for (int j = 0; j < NH / 4; ++j) {
-          const int h = h0 + warp + 4 * j;
+        for (int j = 0; j < 4; ++j) {
+          const int h = h0 + warp + 4 * (j0 + j);
           const uint32_t* src =
               reinterpret_cast<const uint32_t*>(q + (static_cast<int64_t>(w.b) * heads + h) * kRow);
 #pragma unroll
@@ -474,8 +567,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             raw[j][i] = (h < heads && i * 32 + lane < kPairs) ? __ldg(src + i * 32 + lane) : 0u;
         }
 #pragma unroll
-        for (int j = 0; j < NH / 4; ++j) {
-          const int h = warp + 4 * j;
+        for (int j = 0; j < 4; ++j) {
+          const int h = warp + 4 * (j0 + j);
           float amax = 0.f;
 #pragma unroll
           for (int i = 0; i < kWords; ++i) {
@@ -508,6 +601,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             }
           }
         }
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms->q_full);
@@ -527,16 +621,22 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       float m[HN], l[HN], vref = 0.f;
 #pragma unroll
       for (int i = 0; i < HN; ++i) m[i] = 0.f, l[i] = 0.f;
-      for (int t = 0; t < n_tiles; ++t, ++tile) {
-        const bool in_seg = t * kPages + warp < w.seg_count;  // a page per warp
+      // Before its first tile a CTA goes through the tile's code once without
+      // effect: fetching that code costs 1200 (bf16) to 5000 (FP8) cycles, now
+      // while the first loads are on their way.
+      for (int t = seg == 0 ? -1 : 0; t < n_tiles; ++t) {
+        const bool live = t >= 0;
+        const bool in_seg = live && t * kPages + warp < w.seg_count;  // a page per warp
         const int key = (w.span.first + w.seg_first + t * kPages + warp) * kBlockSize + (lane >> 2);
-        int slot[1 + C::kBlocks];
-        uint32_t parity[1 + C::kBlocks];
+        int slot[1 + C::kBlocks] = {};
+        uint32_t parity[1 + C::kBlocks] = {};
+        if (live) {
 #pragma unroll
-        for (int u = 0; u <= C::kBlocks; ++u)
-          slot[u] = rg.take<C::kSlots>(u == 0 ? 1 : C::kSlotsPerBlock, parity[u]);
-        ok = mbar_wait(&ms->s_full[tile & 1], (tile >> 1) & 1);
-        tc::fence_after();
+          for (int u = 0; u <= C::kBlocks; ++u)
+            slot[u] = rg.take<C::kSlots>(u == 0 ? 1 : C::kSlotsPerBlock, parity[u]);
+          ok = mbar_wait(&ms->s_full[tile & 1], (tile >> 1) & 1);
+          tc::fence_after();
+        }
         bool seen[2];
         float vs[2];
 #pragma unroll
@@ -544,7 +644,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
           seen[j] = in_seg && key + 8 * j >= w.span.lo && key + 8 * j < w.span.len;
           // the row's scale (it landed with the rope unit, whose phase every
           // reader looks at itself); a hidden slot's may be anything
-          if (FP8 && j == 0) ok = ok && mbar_wait(&ms->full[slot[0]], parity[0] >> slot[0] & 1u);
+          if (FP8 && j == 0 && live) ok = ok && mbar_wait(&ms->full[slot[0]], parity[0] >> slot[0] & 1u);
           vs[j] = FP8 && seen[j]
                       ? reinterpret_cast<const float*>(scales + (tile % C::kScaleTiles) * C::kScaleBytes)[r0 + 8 * j]
                       : 0.f;
@@ -598,7 +698,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
               }
           }
         }
-        bool move = !ok || t == 0 || over > C::kLag;
+        bool move = !ok || t <= 0 || over > C::kLag;
         if (FP8) move |= fmaxf(vs[0], vs[1]) > C::kVLag * vref;
         if (lat::bar_any(1, kSoftThreads, move)) {
           // the tile's maxima; the ones in use move to them where they lag
@@ -623,9 +723,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
           float vmul = 1.f;
           if (FP8) {
             const float x = fmaxf(fmaxf(ms->vred[0], ms->vred[1]), fmaxf(ms->vred[2], ms->vred[3]));
-            if (t == 0 || x > C::kVLag * vref) {
+            if (t <= 0 || x > C::kVLag * vref) {
               const float to = fmaxf(x, 1e-30f);
-              vmul = t == 0 ? 1.f : vref / to;
+              vmul = t <= 0 ? 1.f : vref / to;
               vref = to;
             }
           }
@@ -634,7 +734,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             const int h = 8 * (i >> 1) + 2 * quad + (i & 1);
             const float x = fmaxf(fmaxf(ms->red[0][h], ms->red[1][h]), fmaxf(ms->red[2][h], ms->red[3][h]));
             float a = 1.f;
-            if (t == 0) {
+            if (t <= 0) {
+              l[i] = 0.f;
               m[i] = x == -INFINITY ? 0.f : x;
             } else if (x > m[i] + C::kLag) {
               a = ex2_approx(m[i] - x);
@@ -679,6 +780,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             if (!FP8) {
               const uint32_t hi = pack_bf16x2(a, b);
               const float2 got = unpack_bf16x2(hi);
+              if (!live) continue;
               *reinterpret_cast<uint32_t*>(prow + ((g ^ sw) << 4) + quad * 4) = hi;
               *reinterpret_cast<uint32_t*>(prow + (((g + NH / 8) ^ sw) << 4) + quad * 4) =
                   pack_bf16x2(a - got.x, b - got.y);
@@ -689,8 +791,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
               for (int p = 0; p < 3; ++p) {
                 const uint32_t c = e4m3_pair(a, b);
                 const int at = p * NH + g * 8 + quad * 2;
-                *reinterpret_cast<uint16_t*>(prow + (((at >> 4) ^ sw) << 4) + (at & 15)) =
-                    static_cast<uint16_t>(c);
+                if (live)
+                  *reinterpret_cast<uint16_t*>(prow + (((at >> 4) ^ sw) << 4) + (at & 15)) =
+                      static_cast<uint16_t>(c);
                 const float2 got = e4m3_values(c);
                 a = (a - got.x) * 16.f;
                 b = (b - got.y) * 16.f;
@@ -701,7 +804,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         fence_proxy_async_smem();
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ms->p_full[tile & 1]);
+        if (live) {
+          if (lane == 0) mbar_arrive(&ms->p_full[tile & 1]);
+          ++tile;
+        }
       }
       if (!ok) break;
       // ---- the segment's end. S of its last tile is done: Q may be replaced
@@ -737,7 +843,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       if (tid == 0 && w.seg_first == 0) {
         // first page of the unit: note which pieces share it
         const int64_t end = p1 - w.left - w.seg_count + w.span.count;  // list end of the unit
-        const int last = static_cast<int>((end * pieces - 1) / total);
+        const int last = static_cast<int>((end * ms->pieces - 1) / ms->total);
         parts[w.b * chunks + w.chunk] = whole ? Part{-1, -1} : Part{static_cast<int32_t>(blockIdx.x), last};
       }
       named_bar_sync(1, kSoftThreads);
@@ -905,7 +1011,7 @@ int launch(const LatentArgs& L, const void* q, const LatentPages& pages, const i
   auto* o = reinterpret_cast<float*>(base + y.o);
   auto* ob = static_cast<__nv_bfloat16*>(out);
   const int grid = num_sms < kMaxCtas ? num_sms : kMaxCtas;
-  kernel<<<grid, kThreads, C::kSmemBytes, stream>>>(
+  kernel<<<grid, C::kThreads, C::kSmemBytes, stream>>>(
       q_map, pool_map, pages, static_cast<const __nv_bfloat16*>(q), seq_lens, n_seqs, L.n_heads,
       L.window, L.scale, L.softcap, ob, lse, parts, ml, o, err);
   if (cudaGetLastError() != cudaSuccess) return PSW_ELAUNCH;
