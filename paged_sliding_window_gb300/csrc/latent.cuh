@@ -63,11 +63,16 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, ui
       : "memory");
 }
 
-// Asynchronous 16-byte copy into shared memory (this thread's group); with
-// `bytes` 0 nothing is read and the destination becomes zero.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
+// Plain copy of `bytes` (a multiple of 16; both addresses 16-byte aligned) into
+// shared memory, counted on `bar`. (A tensor copy's destination would have to be
+// 128-byte aligned.)
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
 }
 
 // D[tmem] (+)= A[smem] * B[smem] on E4M3 operands, fp32 accumulators.

@@ -48,7 +48,8 @@ constexpr int kPages = kTile / kBlockSize;      // pages of a tile
 constexpr int kSlotBytes = kTile * 128;
 constexpr int kSoftThreads = 128;               // warps 0-3
 constexpr int kScoreWarp = 4, kValueWarp = 5;   // MMAs of S, of O
-constexpr int kLoadWarp = 6;                    // and 7 with FP8 pages
+constexpr int kLoadWarp = 6;
+constexpr int kThreads = 224;
 constexpr int kMaxCtas = 160;                   // pieces of the page list
 constexpr int kMinPages = 4;                    // pages a piece has at least
 constexpr int kMaxHeads = 32;                   // heads of a chunk
@@ -73,17 +74,13 @@ struct Cfg {
   static constexpr int kRopeSteps = FP8 ? 2 : 4;       // 32-byte MMA steps of the rope chunk
   static constexpr int kPSteps = FP8 ? 2 : 4;          // MMA steps along the keys
   static constexpr int kPStepBytes = kTile / kPSteps * 128;
-  static constexpr int kLoadWarps = FP8 ? 2 : 1;
-  static constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
   static constexpr int kMisc = FP8 ? 6144 : 2048;
   static constexpr int kTileSlots = 1 + kBlocks * kSlotsPerBlock;
-  static constexpr int kSlotsFit = (kSmemLimit - 1024 - kMisc - kQBytes) / kSlotBytes;
-  static constexpr int kSlots = FP8 ? kSlotsFit / kTileSlots * kTileSlots : kSlotsFit;
+  static constexpr int kSlots = (kSmemLimit - 1024 - kMisc - kQBytes) / kSlotBytes;
   static constexpr int kSmemBytes = 1024 + kQBytes + kSlots * kSlotBytes + kMisc;
   static constexpr int kTmemO = 2 * kQRows;            // after the two S^T buffers
   static_assert(kTmemO + kBlocks * kPCols <= 512, "tensor memory columns");
-  static_assert(kSlots >= 2 * kTileSlots + (FP8 ? kTileSlots : 1),
-                "two tiles fit, a slot left out included; three with FP8 pages");
+  static_assert(kSlots >= 2 * kTileSlots + 1, "two tiles fit, a slot left out included");
   // FP8: row scales of the tiles in the ring, in turn (after the misc block)
   static constexpr int kScaleTiles = 16;
   static constexpr int kScales = 2048, kScaleBytes = kTile * 4;
@@ -115,6 +112,9 @@ struct Misc {
   float alpha[kMaxHeads];    // factors of a rescale; at a segment's end, the maxima
 };
 static_assert(sizeof(Misc) <= 2048, "misc block");
+
+// Row scales of a page that is not there (its codes read as zeros).
+__device__ const float4 g_zero_scales[kBlockSize / 4] = {};
 
 // Visible pages of one sequence.
 struct Span {
@@ -202,8 +202,15 @@ __device__ __forceinline__ float2 e4m3_values(uint32_t pair) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// The kernels of a call are launched while what is ahead of them in the stream
+// may still run: nothing of the inputs, the outputs or the workspace is touched
+// before this.
+__device__ __forceinline__ void wait_for_inputs() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 template <int LAT, int NH, bool FP8>
-__global__ void __launch_bounds__(Cfg<LAT, NH, FP8>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                      const __grid_constant__ CUtensorMap pool_map, const LatentPages pages,
                      const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ seq_lens,
@@ -227,6 +234,22 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     // ---- set-up and this CTA's piece of the page list, by the warp whose loads
     // everything waits for: it adds up all spans, a run of sequences per lane,
     // and the lane whose run holds the piece's first page finds the unit
+    mbar_init(&ms->full[lane], 1);
+    mbar_init(&ms->empty[lane], 1);
+    if (lane < 2) {
+      mbar_init(&ms->s_full[lane], 1);
+      mbar_init(&ms->p_full[lane], 4);
+      mbar_init(&ms->pv_done[lane], 1);
+    } else if (lane == 2) {
+      mbar_init(&ms->q_full, FP8 ? 4 : 1);
+      mbar_init(&ms->o_full, 1);
+      mbar_init(&ms->o_free, 4);
+      mbar_init(&ms->drained, 2);
+      ms->abort = 0;
+    }
+    fence_mbar_init();
+    __syncwarp();
+    wait_for_inputs();
     const int per = (n_seqs + 31) / 32;
     const int b0 = min(n_seqs, lane * per), b1 = min(n_seqs, b0 + per);
     int64_t mine = 0;
@@ -239,23 +262,6 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         if (raw > static_cast<int64_t>(pages.max_blocks) * kBlockSize)
           flag_error(err, PSW_DEVERR_CAPACITY);
       }
-    }
-    if (lane == 0) {
-      for (int i = 0; i < C::kSlots; ++i) {
-        mbar_init(&ms->full[i], C::kLoadWarps);
-        mbar_init(&ms->empty[i], 1);
-      }
-      mbar_init(&ms->q_full, FP8 ? 4 : 1);
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&ms->s_full[i], 1);
-        mbar_init(&ms->p_full[i], 4);
-        mbar_init(&ms->pv_done[i], 1);
-      }
-      mbar_init(&ms->o_full, 1);
-      mbar_init(&ms->o_free, 4);
-      mbar_init(&ms->drained, 2);
-      ms->abort = 0;
-      fence_mbar_init();
     }
     int64_t incl = mine;
 #pragma unroll
@@ -292,7 +298,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     }
     __threadfence_block();
     __syncwarp();
-    asm volatile("bar.arrive 2, %0;" ::"r"(C::kThreads) : "memory");  // goes straight on
+    asm volatile("bar.arrive 2, %0;" ::"r"(kThreads) : "memory");  // goes straight on
   } else {
     if (warp == kScoreWarp) {
       tc::alloc(&ms->tmem, 512);
@@ -302,8 +308,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       prefetch_tensormap(&pool_map);
       prefetch_tensormap(&q_map);
     }
+    wait_for_inputs();
     tc::fence_before();
-    named_bar_sync(2, C::kThreads);
+    named_bar_sync(2, kThreads);
     tc::fence_after();
   }
   const int64_t p1 = ms->p1;
@@ -332,118 +339,62 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       flag_error(err, PSW_DEVERR_BLOCK_ID);
       return -1;
     };
-    if constexpr (!FP8) {
-      // TMA boxes of 16 rows x 128 bytes, issued by one lane of the converged
-      // warp (issued by a lane each, a box costs 90 cycles: longer than it takes
-      // to arrive)
-      const bool one = lat::elect_one();
-      uint32_t issued = 0;  // slots whose last load may be in flight, for the drain
-      while (ok && walk.next()) {
-        const int n_tiles = walk.tiles();
-        int next_blk = block_id(lane & 3);
-        for (int t = 0; ok && t < n_tiles; ++t) {
-          int y[kPages];
+    // TMA boxes of 16 rows x 128 bytes, issued by one lane of the converged warp
+    // (issued by a lane each, a box costs 90 cycles: longer than it takes to
+    // arrive). FP8 rows are 4.5 or 2.5 lines long and half of them straddle the
+    // boxes' lines, which costs a gather of pages 6 % against whole pages.
+    const bool one = lat::elect_one();
+    uint32_t issued = 0;  // slots whose last load may be in flight, for the drain
+    int tile = 0;
+    while (ok && walk.next()) {
+      const int n_tiles = walk.tiles();
+      int next_blk = block_id(lane & 3);
+      for (int t = 0; ok && t < n_tiles; ++t, ++tile) {
+        int blk[kPages];
 #pragma unroll
-          for (int pg = 0; pg < kPages; ++pg)
-            y[pg] = __shfl_sync(0xffffffffu, next_blk, pg) * kBlockSize;
-          if (t + 1 < n_tiles) next_blk = block_id((t + 1) * kPages + (lane & 3));
+        for (int pg = 0; pg < kPages; ++pg) blk[pg] = __shfl_sync(0xffffffffu, next_blk, pg);
+        if (t + 1 < n_tiles) next_blk = block_id((t + 1) * kPages + (lane & 3));
 #pragma unroll
-          for (int u = 0; u <= C::kBlocks; ++u) {  // rope unit, then the blocks
-            const int n = u == 0 ? 1 : C::kSlotsPerBlock;
-            uint32_t parity;
-            const int s = rg.take<C::kSlots>(n, parity);
+        for (int u = 0; u <= C::kBlocks; ++u) {  // rope unit, then the blocks
+          const int n = u == 0 ? 1 : C::kSlotsPerBlock;
+          uint32_t parity;
+          const int s = rg.take<C::kSlots>(n, parity);
 #pragma unroll
-            for (int c = 0; c < n; ++c) {
-              ok = ok && mbar_wait(&ms->empty[s + c], (parity >> (s + c) & 1u) ^ 1u);
-              if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-              }
-              issued |= 1u << (s + c);
-              if (one) {
-                mbar_arrive_expect_tx(&ms->full[s + c], kSlotBytes);
+          for (int c = 0; c < n; ++c) {
+            ok = ok && mbar_wait(&ms->empty[s + c], (parity >> (s + c) & 1u) ^ 1u);
+            if (!__all_sync(0xffffffffu, ok)) {
+              ok = false;
+              break;
+            }
+            issued |= 1u << (s + c);
+            if (one) {
+              uint64_t* full = &ms->full[s + c];
+              mbar_arrive_expect_tx(full, kSlotBytes + (FP8 && u == 0 ? C::kScaleBytes : 0));
 #pragma unroll
-                for (int pg = 0; pg < kPages; ++pg)
-                  lat::tma_box(smem_u32(ring + (s + c) * kSlotBytes + pg * 2048), &pool_map,
-                               &ms->full[s + c], u == 0 ? LAT : (u - 1) * 128 + c * 64, y[pg], 0);
+              for (int pg = 0; pg < kPages; ++pg) {
+                lat::tma_box(smem_u32(ring + (s + c) * kSlotBytes + pg * 2048), &pool_map, full,
+                             u == 0 ? LAT : (u - 1) * 128 + c * 64, blk[pg] * kBlockSize, 0);
+                if (FP8 && u == 0)
+                  lat::bulk_load(
+                      smem_u32(scales + tile % C::kScaleTiles * C::kScaleBytes + pg * 64),
+                      blk[pg] >= 0 ? static_cast<const void*>(pages.row_scale +
+                                                              static_cast<int64_t>(blk[pg]) * kBlockSize)
+                                   : g_zero_scales,
+                      kBlockSize * 4, full);
               }
             }
-            if (!ok) break;
           }
-          ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
-        }
-      }
-      if (!ok && lane == 0) {
-        *abort_flag = 1;
-        flag_error(err, PSW_DEVERR_PIPELINE);
-        // copies in flight land before the CTA ends: the last phase of each slot
-        for (int s = 0; s < C::kSlots; ++s)
-          if (issued >> s & 1u) mbar_wait(&ms->full[s], ((rg.phase >> s) & 1u) ^ 1u);
-      }
-    } else {
-      // An FP8 row is 4.5 or 2.5 lines long, so that boxes of 128 bytes straddle
-      // lines, and the SM's rate is one of lines (a TMA loader took 137 cycles a
-      // box, 91 with the aligned bf16 rows). Here a page, whole lines in a row,
-      // is read front to back with 16-byte asynchronous copies into the same
-      // swizzled rows. A tile is announced kAhead tiles after its issue, when
-      // its copies have been waited for and fenced for the tensor core.
-      constexpr int kRow = LAT + kLatentRope, kCopies = kBlockSize * kRow / 512;
-      constexpr int kStages = C::kSlots / C::kTileSlots, kAhead = kStages - 2;
-      int dst[kCopies];  // where this lane's vectors of a page go, from the tile's first slot
-#pragma unroll
-      for (int i = 0; i < kCopies; ++i) {
-        const int o = i * 512 + lane * 16, r = o / kRow, x = o - r * kRow;
-        const int slot = x >= LAT ? 0 : 1 + x / 128;
-        dst[i] = slot * kSlotBytes + r * 128 + ((((x & 127) >> 4) ^ (r & 7)) << 4);
-      }
-      const uint32_t ring_at = smem_u32(ring), scales_at = smem_u32(scales);
-      const auto* pool = static_cast<const uint8_t*>(pages.pool);
-      const int lw = warp - kLoadWarp;
-      int tile = 0, told = 0;  // tiles issued, tiles announced
-      auto announce = [&]() {  // (after this lane's copies of the tile have landed)
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane < C::kTileSlots)
-          mbar_arrive(&ms->full[told % kStages * C::kTileSlots + lane]);
-        ++told;
-      };
-      while (ok && walk.next()) {
-        const int n_tiles = walk.tiles();
-        int next_blk = lane < 2 ? block_id(lw + 2 * lane) : -1;  // lanes 0 and 1: this warp's pages
-        for (int t = 0; ok && t < n_tiles; ++t, ++tile) {
-          const int blks = next_blk;
-          if (t + 1 < n_tiles && lane < 2) next_blk = block_id((t + 1) * kPages + lw + 2 * lane);
-          const int s = tile % kStages * C::kTileSlots;
-          if (lane < C::kTileSlots)
-            ok = mbar_wait(&ms->empty[s + lane], (tile / kStages & 1u) ^ 1u) && !*abort_flag;
-          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int pg = lw + 2 * k, blk = __shfl_sync(0xffffffffu, blks, k);
-            const uint32_t bytes = blk >= 0 ? 16u : 0u;  // 0: the destination becomes zero
-            const uint8_t* src = pool + static_cast<int64_t>(max(blk, 0)) * (kBlockSize * kRow) + lane * 16;
-            const uint32_t to = ring_at + s * kSlotBytes + pg * 2048;
-#pragma unroll
-            for (int i = 0; i < kCopies; ++i) lat::copy16(to + dst[i], src + i * 512, bytes);
-            if (lane < 4)
-              lat::copy16(scales_at + tile % C::kScaleTiles * C::kScaleBytes + pg * 64 + lane * 16,
-                          pages.row_scale + static_cast<int64_t>(max(blk, 0)) * kBlockSize + lane * 4, bytes);
-          }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          if (tile >= kAhead) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
-            announce();
-          }
         }
+        ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
       }
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      if (ok) {
-        while (told < tile) announce();
-      } else if (lane == 0) {
-        *abort_flag = 1;
-        flag_error(err, PSW_DEVERR_PIPELINE);
-      }
+    }
+    if (!ok && one) {
+      *abort_flag = 1;
+      flag_error(err, PSW_DEVERR_PIPELINE);
+      // copies in flight land before the CTA ends: the last phase of each slot
+      for (int s = 0; s < C::kSlots; ++s)
+        if (issued >> s & 1u) mbar_wait(&ms->full[s], ((rg.phase >> s) & 1u) ^ 1u);
     }
   } else if (warp >= kScoreWarp) {
     // ------------------------------------------------------------ MMAs of S and of O
@@ -900,8 +851,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 // Joins what the pieces of a unit left: out = sum_i 2^(m_i - M) O_i / sum_i
 // 2^(m_i - M) l_i. One CTA per (sequence, head); a group of L / 4 threads, four
 // dims each, takes every groups-th piece, and the groups' sums meet in shared
-// memory. A unit that one piece covered is left alone, an empty sequence gets
-// its zeros.
+// memory. The kernel is a chain of three loads (lengths, which pieces, then
+// statistics and the first eight pieces together). A unit that one piece covered
+// is left alone, an empty sequence gets its zeros.
 constexpr int kMergeThreads = 512;
 template <int LAT>
 __global__ void __launch_bounds__(kMergeThreads)
@@ -910,64 +862,81 @@ latent_merge_kernel(const int32_t* __restrict__ seq_lens, int heads,
                     const float* __restrict__ part_o, __nv_bfloat16* __restrict__ out,
                     float* __restrict__ lse) {
   constexpr int kRow = LAT / 4;  // threads of a group
-  __shared__ float s_w[kMaxCtas];
+  __shared__ float s_w[kMergeThreads / 32][kMaxCtas];
   __shared__ float4 s_o[kMergeThreads];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   const int group = tid / kRow, groups = blockDim.x / kRow, col = tid - group * kRow;
   const int nh = chunk_heads(heads), chunk = h / nh, hc = h - chunk * nh;
   const int64_t row = static_cast<int64_t>(b) * heads + h;
   uint2* dst = reinterpret_cast<uint2*>(out + row * LAT) + col;
+  wait_for_inputs();
   const int len = __ldg(seq_lens + b);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Part pt = len > 0 ? parts[b * chunks_of(heads) + chunk] : Part{-1, -1};
   if (len <= 0) {
     if (group == 0) *dst = make_uint2(0u, 0u);
     if (lse != nullptr && tid == 0) lse[row] = -INFINITY;
     return;
   }
-  const Part pt = parts[b * chunks_of(heads) + chunk];
   if (pt.x < 0) return;
   const int n = pt.y - pt.x + 1;
   auto slot = [&](int i) { return i == 0 ? 2 * pt.x + 1 : 2 * (pt.x + i); };
+  auto piece = [&](int i) -> float4 {
+    return i < n ? __ldcg(reinterpret_cast<const float4*>(
+                              part_o + (static_cast<int64_t>(slot(i)) * kMaxHeads + hc) * LAT) +
+                          col)
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  float4 v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = piece(group + k * groups);
   // every warp forms the pieces' weights by itself
   float2 ml[kMaxCtas / 32];
   float mx = -INFINITY, l = 0.f;
 #pragma unroll
   for (int k = 0; k < kMaxCtas / 32; ++k) {
     const int i = lane + k * 32;
-    ml[k] = i < n ? part_ml[slot(i) * kMaxHeads + hc] : make_float2(-INFINITY, 0.f);
+    ml[k] = i < n ? __ldcg(part_ml + slot(i) * kMaxHeads + hc) : make_float2(-INFINITY, 0.f);
     mx = fmaxf(mx, ml[k].x);
   }
   mx = lat::warp_max(mx);
+  float* w = s_w[tid >> 5];
 #pragma unroll
   for (int k = 0; k < kMaxCtas / 32; ++k) {
     const int i = lane + k * 32;
-    const float w = i < n ? ex2_approx(ml[k].x - mx) : 0.f;
-    if (tid < 32 && i < n) s_w[i] = w;
-    l = fmaf(w, ml[k].y, l);
+    const float x = i < n ? ex2_approx(ml[k].x - mx) : 0.f;
+    w[i] = x;
+    l = fmaf(x, ml[k].y, l);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  __syncthreads();
+  __syncwarp();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = group; i < n; i += groups) {
-    const float4 v = __ldcg(
-        reinterpret_cast<const float4*>(part_o + (static_cast<int64_t>(slot(i)) * kMaxHeads + hc) * LAT) + col);
-    const float w = s_w[i];
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
+  for (int i0 = group; i0 < n; i0 += 8 * groups) {
+    if (i0 != group) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = piece(i0 + k * groups);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float x = i0 + k * groups < n ? w[i0 + k * groups] : 0.f;
+      acc.x = fmaf(x, v[k].x, acc.x);
+      acc.y = fmaf(x, v[k].y, acc.y);
+      acc.z = fmaf(x, v[k].z, acc.z);
+      acc.w = fmaf(x, v[k].w, acc.w);
+    }
   }
-  s_o[tid] = acc;
-  __syncthreads();
-  if (group != 0) return;
-  for (int g = 1; g < groups; ++g) {
-    const float4 v = s_o[g * kRow + col];
-    acc.x += v.x;
-    acc.y += v.y;
-    acc.z += v.z;
-    acc.w += v.w;
+  if (groups > 1) {
+    s_o[tid] = acc;
+    __syncthreads();
+    if (group != 0) return;
+    for (int g = 1; g < groups; ++g) {
+      const float4 x = s_o[g * kRow + col];
+      acc.x += x.x;
+      acc.y += x.y;
+      acc.z += x.z;
+      acc.w += x.w;
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   *dst = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
@@ -1011,25 +980,28 @@ int launch(const LatentArgs& L, const void* q, const LatentPages& pages, const i
   auto* o = reinterpret_cast<float*>(base + y.o);
   auto* ob = static_cast<__nv_bfloat16*>(out);
   const int grid = num_sms < kMaxCtas ? num_sms : kMaxCtas;
-  kernel<<<grid, C::kThreads, C::kSmemBytes, stream>>>(
-      q_map, pool_map, pages, static_cast<const __nv_bfloat16*>(q), seq_lens, n_seqs, L.n_heads,
-      L.window, L.scale, L.softcap, ob, lse, parts, ml, o, err);
-  if (cudaGetLastError() != cudaSuccess) return PSW_ELAUNCH;
-  // the join may be launched while the pieces still run; it waits for them
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n_seqs, L.n_heads);
-  // pieces a unit has on average, eight loads in flight per group of threads
-  const int64_t units = static_cast<int64_t>(n_seqs) * chunks_of(L.n_heads);
-  const int row_threads = L.latent / 4;
-  const int want = static_cast<int>(1 + (grid / units) / 8);
-  const int fit = kMergeThreads / row_threads;
-  cfg.blockDim = dim3(row_threads * (want < fit ? want : fit));
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, q_map, pool_map, pages,
+                         static_cast<const __nv_bfloat16*>(q), seq_lens, n_seqs, L.n_heads,
+                         L.window, L.scale, L.softcap, ob, lse, parts, ml, o, err) != cudaSuccess)
+    return PSW_ELAUNCH;
+  cfg.gridDim = dim3(n_seqs, L.n_heads);
+  cfg.dynamicSmemBytes = 0;
+  // pieces a unit has on average, eight loads in flight per group of threads
+  const int64_t units = static_cast<int64_t>(n_seqs) * chunks_of(L.n_heads);
+  const int row_threads = L.latent / 4;
+  const int want = static_cast<int>(1 + (grid / units) / 8);
+  const int fit = kMergeThreads / row_threads;
+  cfg.blockDim = dim3(row_threads * (want < fit ? want : fit));
   const cudaError_t e = cudaLaunchKernelEx(
       &cfg, latent_merge_kernel<LAT>, seq_lens, L.n_heads,
       static_cast<const Part*>(parts), static_cast<const float2*>(ml),
