@@ -48,8 +48,8 @@ constexpr int kPages = kTile / kBlockSize;      // pages of a tile
 constexpr int kSlotBytes = kTile * 128;
 constexpr int kSoftThreads = 128;               // warps 0-3
 constexpr int kScoreWarp = 4, kValueWarp = 5;   // MMAs of S, of O
-constexpr int kLoadWarp = 6;
-constexpr int kThreads = 224;
+constexpr int kLoadWarp = 6;                    // pages
+constexpr int kQueryWarp = 7;                   // queries: this warp, and 8-10 with FP8 pages
 constexpr int kMaxCtas = 160;                   // pieces of the page list
 constexpr int kMinPages = 4;                    // pages a piece has at least
 constexpr int kMaxHeads = 32;                   // heads of a chunk
@@ -74,6 +74,8 @@ struct Cfg {
   static constexpr int kRopeSteps = FP8 ? 2 : 4;       // 32-byte MMA steps of the rope chunk
   static constexpr int kPSteps = FP8 ? 2 : 4;          // MMA steps along the keys
   static constexpr int kPStepBytes = kTile / kPSteps * 128;
+  static constexpr int kQueryWarps = FP8 ? 4 : 1;
+  static constexpr int kThreads = 32 * (kQueryWarp + kQueryWarps);
   static constexpr int kMisc = FP8 ? 6144 : 2048;
   static constexpr int kTileSlots = 1 + kBlocks * kSlotsPerBlock;
   static constexpr int kSlots = (kSmemLimit - 1024 - kMisc - kQBytes) / kSlotBytes;
@@ -99,7 +101,7 @@ struct Cfg {
 
 struct Misc {
   uint64_t full[32], empty[32];
-  uint64_t q_full, s_full[2], p_full[2], pv_done[2], o_full, o_free, drained;
+  uint64_t q_full, q_free, s_full[2], p_full[3], pv_done[3], o_full, o_free, drained;
   int32_t unit0, page0;      // this CTA's first unit and the page within it
   uint32_t tmem;
   int32_t abort;
@@ -107,7 +109,7 @@ struct Misc {
   int32_t pieces;
   float red[4][kMaxHeads];
   float vred[4];
-  float qs[kMaxHeads];       // FP8: scale * log2(e) * what a unit of q's codes stands for
+  float qs[3][kMaxHeads];    // FP8, segments in turn: scale * log2(e) * a unit of q's codes
   float lsum[kMaxHeads];
   float alpha[kMaxHeads];    // factors of a rescale; at a segment's end, the maxima
 };
@@ -210,7 +212,7 @@ __device__ __forceinline__ void wait_for_inputs() {
 }
 
 template <int LAT, int NH, bool FP8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<LAT, NH, FP8>::kThreads, 1)
 latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                      const __grid_constant__ CUtensorMap pool_map, const LatentPages pages,
                      const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ seq_lens,
@@ -236,12 +238,13 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     // and the lane whose run holds the piece's first page finds the unit
     mbar_init(&ms->full[lane], 1);
     mbar_init(&ms->empty[lane], 1);
-    if (lane < 2) {
-      mbar_init(&ms->s_full[lane], 1);
+    if (lane < 3) {
+      if (lane < 2) mbar_init(&ms->s_full[lane], 1);
       mbar_init(&ms->p_full[lane], 4);
       mbar_init(&ms->pv_done[lane], 1);
-    } else if (lane == 2) {
-      mbar_init(&ms->q_full, FP8 ? 4 : 1);
+    } else if (lane == 3) {
+      mbar_init(&ms->q_full, C::kQueryWarps);
+      mbar_init(&ms->q_free, 1);
       mbar_init(&ms->o_full, 1);
       mbar_init(&ms->o_free, 4);
       mbar_init(&ms->drained, 2);
@@ -298,7 +301,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     }
     __threadfence_block();
     __syncwarp();
-    asm volatile("bar.arrive 2, %0;" ::"r"(kThreads) : "memory");  // goes straight on
+    asm volatile("bar.arrive 2, %0;" ::"r"(C::kThreads) : "memory");  // goes straight on
   } else {
     if (warp == kScoreWarp) {
       tc::alloc(&ms->tmem, 512);
@@ -310,7 +313,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     }
     wait_for_inputs();
     tc::fence_before();
-    named_bar_sync(2, kThreads);
+    named_bar_sync(2, C::kThreads);
     tc::fence_after();
   }
   const int64_t p1 = ms->p1;
@@ -327,8 +330,88 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
   walk.page = walk.left > 0 ? ms->page0 : 0;
   Ring rg;
   bool ok = true;
+  const float mul = softcap > 0.f ? scale / softcap : scale * lat::kLog2e;  // (times cap2 later)
 
-  if (warp >= kLoadWarp) {
+  if (warp >= kQueryWarp) {
+    // ------------------------------------------------------------ queries
+    const int h_first = warp - kQueryWarp;
+    int seg = 0;
+    for (; ok && walk.next(); ++seg) {
+      const int h0 = walk.chunk * NH;
+      if constexpr (!FP8) {
+        // (the previous unit's queries are done with when its last S is)
+        if (seg > 0) ok = __all_sync(0xffffffffu, mbar_wait(&ms->q_free, (seg - 1) & 1));
+        if (ok && lat::elect_one()) {
+          mbar_arrive_expect_tx(&ms->q_full, C::kQBytes);
+#pragma unroll
+          for (int c = 0; c < C::kQChunks; ++c)
+            lat::tma_box(smem_u32(q_smem + c * C::kQChunkBytes), &q_map, &ms->q_full, c * 64, h0,
+                         walk.b);
+        }
+      } else {
+        // a warp has every fourth head: its largest value gives the power of two,
+        // a value is the sum of two parts, the second 16 times up
+        constexpr int kRow = LAT + kLatentRope, kPairs = kRow / 2, kWords = (kPairs + 31) / 32;
+        uint32_t raw[NH / 4][kWords];
+#pragma unroll
+        for (int j = 0; j < NH / 4; ++j) {
+          const int h = h0 + h_first + 4 * j;
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(
+              q + (static_cast<int64_t>(walk.b) * heads + h) * kRow);
+#pragma unroll
+          for (int i = 0; i < kWords; ++i)
+            raw[j][i] = (h < heads && i * 32 + lane < kPairs) ? __ldg(src + i * 32 + lane) : 0u;
+        }
+        if (seg > 0) ok = __all_sync(0xffffffffu, mbar_wait(&ms->q_free, (seg - 1) & 1));
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < NH / 4; ++j) {
+          const int h = h_first + 4 * j;
+          float amax = 0.f;
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) {
+            const float2 v = unpack_bf16x2(raw[j][i]);
+            amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+          }
+          amax = lat::warp_max(amax);
+          // 2^k with amax 2^k in [128, 256), from amax's exponent field
+          const int ex = static_cast<int>(__float_as_uint(amax) >> 23);
+          const int k = max(-126, min(126, 127 + 7 - ex));
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+          // (an infinite query has no such codes: its scores become NaN)
+          if (lane == 0)
+            ms->qs[seg % 3][h] =
+                ex == 255 ? NAN : mul * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) {
+            const int e = i * 32 + lane;
+            if (e >= kPairs) continue;
+            const float2 v = unpack_bf16x2(raw[j][i]);
+            const float a = v.x * up, b = v.y * up;
+            const uint32_t hi = e4m3_pair(a, b);
+            const float2 got = e4m3_values(hi);
+            const uint32_t lo = e4m3_pair((a - got.x) * 16.f, (b - got.y) * 16.f);
+            const int byte = 2 * e, c = byte >> 7, in = byte & 127;
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              const int r = part * NH + h;
+              const int at = c * C::kQChunkBytes + r * 128 + ((((in >> 4) ^ (r & 7)) << 4) | (in & 15));
+              *reinterpret_cast<uint16_t*>(q_smem + at) = static_cast<uint16_t>(part == 0 ? hi : lo);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms->q_full);
+      }
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      flag_error(err, PSW_DEVERR_PIPELINE);
+    }
+    // a copy in flight lands before the CTA ends
+    if (!FP8 && seg > 0 && *abort_flag) mbar_wait(&ms->q_full, (seg - 1) & 1);
+  } else if (warp == kLoadWarp) {
     // ------------------------------------------------------------ loads
     // block id of page i of the segment; -1: zero rows
     auto block_id = [&](int i) -> int {
@@ -408,13 +491,12 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       if (FP8) lat::mma_ss_fp8(d, a, b, id, acc);
       else tc::mma_ss(d, a, b, id, acc);
     };
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u) && *abort_flag == 0);
-    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && mbar_wait(bar, parity & 1u); };
     int seg = 0, tile = 0;
     for (; ok && walk.next(); ++seg) {
       const int n_tiles = walk.tiles();
-      if (warp == kScoreWarp) ok = wait(&ms->q_full, seg);
+      if (warp == kScoreWarp) wait(&ms->q_full, seg);
+      ok = __all_sync(0xffffffffu, ok);
       for (int t = 0; ok && t < n_tiles; ++t, ++tile) {
         int slot[1 + C::kBlocks];
         uint32_t parity[1 + C::kBlocks];
@@ -426,14 +508,15 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                                     : tc::idesc_bf16_f32(kTile, C::kQRows, 0, 0);
           const uint64_t q_desc = tc::smem_desc(smem_u32(q_smem), 16, 1024, tc::kSwizzle128B);
           const uint32_t d = tmem + (tile & 1) * C::kQRows;
-          // two tiles ago is over, its S read and its products done: no role is
-          // ever two phases of a barrier behind another
-          if (tile >= 2) ok = wait(&ms->pv_done[tile & 1], (tile >> 1) - 1);
+          // this buffer's S of two tiles ago has been read; and the tile before
+          // that is over, so that no role is two phases of a barrier behind
+          if (tile >= 2) wait(&ms->p_full[(tile - 2) % 3], (tile - 2) / 3);
+          if (tile >= 3) wait(&ms->pv_done[tile % 3], tile / 3 - 1);
 #pragma unroll
           for (int u = 0; u <= C::kBlocks; ++u) {
 #pragma unroll
             for (int c = 0; c < (u == 0 ? 1 : C::kSlotsPerBlock); ++c) {
-              ok = ok && wait(&ms->full[slot[u] + c], parity[u] >> (slot[u] + c));
+              wait(&ms->full[slot[u] + c], parity[u] >> (slot[u] + c));
               tc::fence_after();
               const uint64_t kd = k_desc + (slot[u] + c) * kSlotStep;
               const uint64_t qd =
@@ -446,15 +529,18 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
               }
             }
           }
-          if (ok && one) tc::commit(&ms->s_full[tile & 1]);
+          if (ok && one) {
+            tc::commit(&ms->s_full[tile & 1]);
+            if (t == n_tiles - 1) tc::commit(&ms->q_free);
+          }
         } else {
           const uint32_t id_o = FP8 ? lat::idesc_e4m3_f32(128, C::kPCols, 1, 1)
                                     : tc::idesc_bf16_f32(128, C::kPCols, 1, 1);
           const uint64_t v_desc = tc::smem_desc(smem_u32(ring), kSlotBytes, 1024, tc::kSwizzle128B);
           const uint64_t p_desc = tc::smem_desc(smem_u32(ring), 1024, 1024, tc::kSwizzle128B);
           // (P comes after S, and S after the tile has landed)
-          ok = wait(&ms->p_full[tile & 1], tile >> 1) &&
-               (t > 0 || seg == 0 || wait(&ms->o_free, seg - 1));
+          wait(&ms->p_full[tile % 3], tile / 3);
+          if (t == 0 && seg > 0) wait(&ms->o_free, seg - 1);
           tc::fence_after();
           const uint64_t pd = p_desc + slot[0] * kSlotStep;
           if (ok && one) {
@@ -471,11 +557,11 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
               for (int c = 0; c < C::kSlotsPerBlock; ++c) tc::commit(&ms->empty[slot[1 + m] + c]);
             }
             tc::commit(&ms->empty[slot[0]]);
-            tc::commit(&ms->pv_done[tile & 1]);
+            tc::commit(&ms->pv_done[tile % 3]);
             if (t == n_tiles - 1) tc::commit(&ms->o_full);
           }
         }
-        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
       }
     }
     if (one) {
@@ -490,77 +576,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
   } else {
     // ------------------------------------------------------------ softmax, epilogue
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const float mul = softcap > 0.f ? scale / softcap : scale * lat::kLog2e;
     const float cap2 = softcap * lat::kLog2e;
-    auto load_q = [&](const Walk& w) {  // the queries of w's unit, into shared memory
-      const int h0 = w.chunk * NH;
-      if (!FP8) {
-        if (tid == 0) {
-          mbar_arrive_expect_tx(&ms->q_full, C::kQBytes);
-          for (int c = 0; c < C::kQChunks; ++c)
-            lat::tma_box(smem_u32(q_smem + c * C::kQChunkBytes), &q_map, &ms->q_full, c * 64, h0,
-                         w.b);
-        }
-      } else {
-        // warp by warp, a head at a time: its largest value gives the power of
-        // two; the value is the sum of the two parts, the second 16 times up
-        constexpr int kRow = LAT + kLatentRope, kPairs = kRow / 2, kWords = (kPairs + 31) / 32;
-#pragma unroll 1
-        for (int j0 = 0; j0 < NH / 4; j0 += 4) {
-        uint32_t raw[4][kWords];  // the loads of four heads in flight at once
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int h = h0 + warp + 4 * (j0 + j);
-          const uint32_t* src =
-              reinterpret_cast<const uint32_t*>(q + (static_cast<int64_t>(w.b) * heads + h) * kRow);
-#pragma unroll
-          for (int i = 0; i < kWords; ++i)
-            raw[j][i] = (h < heads && i * 32 + lane < kPairs) ? __ldg(src + i * 32 + lane) : 0u;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int h = warp + 4 * (j0 + j);
-          float amax = 0.f;
-#pragma unroll
-          for (int i = 0; i < kWords; ++i) {
-            const float2 v = unpack_bf16x2(raw[j][i]);
-            amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
-          }
-          amax = lat::warp_max(amax);
-          // 2^k with amax 2^k in [128, 256), from amax's exponent field
-          const int ex = static_cast<int>(__float_as_uint(amax) >> 23);
-          const int k = max(-126, min(126, 127 + 7 - ex));
-          const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-          // (an infinite query has no such codes: its scores become NaN)
-          if (lane == 0)
-            ms->qs[h] = ex == 255 ? NAN : mul * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-#pragma unroll
-          for (int i = 0; i < kWords; ++i) {
-            const int e = i * 32 + lane;
-            if (e >= kPairs) continue;
-            const float2 v = unpack_bf16x2(raw[j][i]);
-            const float a = v.x * up, b = v.y * up;
-            const uint32_t hi = e4m3_pair(a, b);
-            const float2 got = e4m3_values(hi);
-            const uint32_t lo = e4m3_pair((a - got.x) * 16.f, (b - got.y) * 16.f);
-            const int byte = 2 * e, c = byte >> 7, in = byte & 127;
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              const int r = part * NH + h;
-              const int at = c * C::kQChunkBytes + r * 128 + ((((in >> 4) ^ (r & 7)) << 4) | (in & 15));
-              *reinterpret_cast<uint16_t*>(q_smem + at) = static_cast<uint16_t>(part == 0 ? hi : lo);
-            }
-          }
-        }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms->q_full);
-      }
-    };
     int seg = 0, tile = 0;
     bool more = walk.next();
-    if (more) load_q(walk);
     // this thread's keys of a tile, rows 16 warp + lane / 4 and 8 further; its
     // heads 8 g + 2 (lane mod 4) + {0, 1}, number 2 g + {0, 1} here
     const int r0 = warp * 16 + (lane >> 2), quad = lane & 3;
@@ -613,7 +631,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
           for (int i = 0; i < HN; ++i) {
             const int r = 4 * (i >> 1) + (i & 1);
-            const float qs = FP8 ? ms->qs[8 * (i >> 1) + 2 * quad + (i & 1)] : mul;
+            const float qs = FP8 ? ms->qs[seg % 3][8 * (i >> 1) + 2 * quad + (i & 1)] : mul;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const float x = __uint_as_float(v[0][r + 2 * j]);
@@ -665,7 +683,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             if (lane == 0) ms->vred[warp] = x;
           }
           // O is rescaled below: the products up to the tile before have ended
-          if (t > 0 && ok) ok = mbar_wait(&ms->pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
+          if (t > 0 && ok) ok = mbar_wait(&ms->pv_done[(tile - 1) % 3], (tile - 1) / 3 & 1);
           if (lat::bar_any(1, kSoftThreads, !ok)) {
             ok = false;
             break;
@@ -756,13 +774,12 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         tc::fence_before();
         __syncwarp();
         if (live) {
-          if (lane == 0) mbar_arrive(&ms->p_full[tile & 1]);
+          if (lane == 0) mbar_arrive(&ms->p_full[tile % 3]);
           ++tile;
         }
       }
       if (!ok) break;
-      // ---- the segment's end. S of its last tile is done: Q may be replaced
-      if (more) load_q(walk);
+      // ---- the segment's end
 #pragma unroll
       for (int i = 0; i < C::kHeads; ++i) {
         float x = l[i];
@@ -838,7 +855,6 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       if (tid == 0) {
         *abort_flag = 1;
         flag_error(err, PSW_DEVERR_PIPELINE);
-        if (!FP8) mbar_wait(&ms->q_full, seg & 1);  // a query copy in flight lands first
       }
     }
   }
@@ -982,7 +998,7 @@ int launch(const LatentArgs& L, const void* q, const LatentPages& pages, const i
   const int grid = num_sms < kMaxCtas ? num_sms : kMaxCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
