@@ -14,7 +14,6 @@
 // spreads over many SMs, and the row's own loads are issued before the chain
 // starts. The 32 angles of a token sit one per lane; the query lanes, which
 // hold 8 + 8 values each for 16-byte accesses, fetch theirs by shuffles.
-#include <cuda_fp8.h>
 #include <math.h>
 
 #include "latent.cuh"
@@ -73,9 +72,7 @@ __device__ __forceinline__ void turn_of(int pos, float2 fq, double fd, float& cs
 }
 
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float k) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a * k, b * k), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c * k, d * k), __NV_SATFINITE, __NV_E4M3);
-  return lo | hi << 16;
+  return lat::e4m3_pair(a * k, b * k) | lat::e4m3_pair(c * k, d * k) << 16;
 }
 
 template <int LAT, bool FP8>

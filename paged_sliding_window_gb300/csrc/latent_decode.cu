@@ -35,7 +35,6 @@
 // per dim). The maximum that P is relative to is taken from a segment's first
 // tile and moved (O rescaled) only when a score exceeds it by 2^64 (bf16, whose
 // P has the range) or 2^4 (E4M3), so a tile costs its threads one barrier.
-#include <cuda_fp8.h>
 #include <math.h>
 
 #include "latent.cuh"
@@ -194,14 +193,6 @@ struct Ring {
 __device__ __forceinline__ float tanh_abs(float y) {
   const float t = ex2_approx(-2.f * lat::kLog2e * fabsf(y));
   return copysignf(__fdividef(1.f - t, 1.f + t), y);
-}
-
-__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ float2 e4m3_values(uint32_t pair) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(pair), __NV_E4M3);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 // The kernels of a call are launched while what is ahead of them in the stream
@@ -388,9 +379,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             if (e >= kPairs) continue;
             const float2 v = unpack_bf16x2(raw[j][i]);
             const float a = v.x * up, b = v.y * up;
-            const uint32_t hi = e4m3_pair(a, b);
-            const float2 got = e4m3_values(hi);
-            const uint32_t lo = e4m3_pair((a - got.x) * 16.f, (b - got.y) * 16.f);
+            const uint32_t hi = lat::e4m3_pair(a, b);
+            const float2 got = lat::e4m3_values(hi);
+            const uint32_t lo = lat::e4m3_pair((a - got.x) * 16.f, (b - got.y) * 16.f);
             const int byte = 2 * e, c = byte >> 7, in = byte & 127;
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
@@ -758,12 +749,12 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
               b *= pv;
 #pragma unroll
               for (int p = 0; p < 3; ++p) {
-                const uint32_t c = e4m3_pair(a, b);
+                const uint32_t c = lat::e4m3_pair(a, b);
                 const int at = p * NH + g * 8 + quad * 2;
                 if (live)
                   *reinterpret_cast<uint16_t*>(prow + (((at >> 4) ^ sw) << 4) + (at & 15)) =
                       static_cast<uint16_t>(c);
-                const float2 got = e4m3_values(c);
+                const float2 got = lat::e4m3_values(c);
                 a = (a - got.x) * 16.f;
                 b = (b - got.y) * 16.f;
               }

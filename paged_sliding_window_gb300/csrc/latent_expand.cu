@@ -1,98 +1,404 @@
 // latent_expand.cu -- cached latent rows read back from their pages and
 // expanded to every head's key and value components:
 //   kv[t][h][e] = sum_l c_l w[h][e][l],  k_rope[t] = r.
-// 16 rows per CTA and one head: the rows in shared memory as fp32, one output
-// component per thread.
-#include <cuda_fp8.h>
-
+// A matrix product of gathered rows, 512 or 1024 operations per output byte:
+// bound by the tensor cores, beside writing 512 bytes per row and head.
+//
+// Schedule: the list of units (tile of 128 rows, head, keys or values: 128 x 128
+// outputs) is cut evenly over one CTA per SM. A CTA holds the rows of its tile in
+// shared memory (L / 64 chunks of 128 rows x 128 B, swizzled) while w streams
+// past them in boxes of 128 x 64 (warp 5, TMA). Warp 4 issues tcgen05.mma into
+// four accumulators in tensor memory, warps 0-3 round, turn the rows around
+// through shared memory and write 64-byte pieces. Warps 6-9 gather rows: rows of
+// a tile are any rows of any pages, so they are copied 16 bytes at a time
+// (asynchronously; FP8 codes are exact in bf16 and are converted on the way, the
+// row's scale multiplies the fp32 result). A chunk of the next tile is loaded as
+// soon as the last unit of this one has used it.
 #include "latent.cuh"
 
 namespace psw {
-namespace {
+namespace lexp {
 
-constexpr int kTile = 16;
+constexpr int kTile = 128;
+constexpr int kUnit = kTile * 128;              // bytes of a chunk and of a box of w
+constexpr int kMmaWarp = 4, kWeightWarp = 5, kRowWarp = 6;
+constexpr int kRowThreads = 128;                // warps 6-9
+constexpr int kThreads = 320;
+constexpr int kAcc = 4;                         // accumulators of 128 columns
+constexpr int kStage = 4 * 32 * 64;             // epilogue: 32 rows x 64 B per warp
+constexpr int kMisc = 3072;
+constexpr int kSmemLimit = 232448;
 
 template <int LAT>
-__global__ void __launch_bounds__(kLatentKv)
-latent_expand_kernel(const LatentPages pages, const int32_t* __restrict__ cu_k,
-                     const int32_t* __restrict__ k_first, int n_seqs, int n_k, int heads,
-                     const __nv_bfloat16* __restrict__ w, __nv_bfloat16* __restrict__ kv,
+struct Cfg {
+  static constexpr int kChunks = LAT / 64;
+  static constexpr int kRing = (kSmemLimit - 1024 - kMisc - kStage - kChunks * kUnit) / kUnit;
+  static constexpr int kSmemBytes = 1024 + (kChunks + kRing) * kUnit + kStage + kMisc;
+  static_assert(kRing >= 4 && kRing <= 16, "boxes of w in flight");
+};
+
+struct Misc {
+  uint64_t a_full[8], a_empty[8], w_full[16], w_empty[16], d_full[kAcc], d_empty[kAcc];
+  uint64_t rows_done[2], rows_set[2], drained;
+  uint32_t tmem;
+  int32_t abort;
+  int32_t slot[2][kTile];   // pool slot of each row of a tile, -1: a zero row; tiles in turn
+  float scale[2][kTile];
+};
+static_assert(sizeof(Misc) <= kMisc, "misc block");
+
+template <int LAT, bool FP8>
+__global__ void __launch_bounds__(kThreads, 1)
+latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPages pages,
+                     const int32_t* __restrict__ cu_k, const int32_t* __restrict__ k_first,
+                     int n_seqs, int n_k, int heads, __nv_bfloat16* __restrict__ kv,
                      __nv_bfloat16* __restrict__ k_rope, int32_t* err) {
+  using C = Cfg<LAT>;
   constexpr int kRow = LAT + kLatentRope;
-  __shared__ float s[kTile][kRow];
-  const int t0 = blockIdx.x * kTile, head = blockIdx.y;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = min(kTile, min(n_k, __ldg(cu_k + n_seqs)) - t0);
-  if (rows <= 0) return;
-  for (int i = warp; i < rows; i += 8) {
-    int b, start;
-    int64_t slot = -1;
-    int32_t bits = 0;
-    if (!lat::owner_of(cu_k, n_seqs, t0 + i, lane, b, start)) {
-      bits = PSW_DEVERR_LENGTH;
-    } else {
-      const int first = k_first != nullptr ? __ldg(k_first + b) : 0;
-      const int64_t pos = static_cast<int64_t>(first) + (t0 + i - start);
-      if (first < 0) {
-        bits = PSW_DEVERR_LENGTH;
-      } else if (pos / kBlockSize >= pages.max_blocks) {
-        bits = PSW_DEVERR_CAPACITY;
-      } else {
-        const int32_t blk =
-            __ldg(pages.block_table + static_cast<int64_t>(b) * pages.max_blocks + pos / kBlockSize);
-        if (blk < 0 || blk >= pages.num_blocks) bits = PSW_DEVERR_BLOCK_ID;
-        else slot = static_cast<int64_t>(blk) * kBlockSize + pos % kBlockSize;
-      }
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* a_smem = smem;
+  uint8_t* w_ring = smem + C::kChunks * kUnit;
+  uint8_t* stage = w_ring + C::kRing * kUnit;
+  Misc* ms = reinterpret_cast<Misc*>(stage + kStage);
+
+  if (warp == kMmaWarp) {
+    tc::alloc(&ms->tmem, 512);
+    tc::relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&ms->a_full[i], 4);
+      mbar_init(&ms->a_empty[i], 1);
     }
-    if (bits != 0 && lane == 0) flag_error(err, bits);
-    for (int e = lane; e < kRow; e += 32) {
-      float x = 0.f;
-      if (slot >= 0) {
-        if (pages.row_scale != nullptr) {
-          __nv_fp8_e4m3 c;
-          c.__x = static_cast<const uint8_t*>(pages.pool)[slot * kRow + e];
-          x = static_cast<float>(c) * pages.row_scale[slot];
-        } else {
-          x = __bfloat162float(static_cast<const __nv_bfloat16*>(pages.pool)[slot * kRow + e]);
+    for (int i = 0; i < 16; ++i) {
+      mbar_init(&ms->w_full[i], 1);
+      mbar_init(&ms->w_empty[i], 1);
+    }
+    for (int i = 0; i < kAcc; ++i) {
+      mbar_init(&ms->d_full[i], 1);
+      mbar_init(&ms->d_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms->rows_set[i], 4);
+      mbar_init(&ms->rows_done[i], 4);
+    }
+    mbar_init(&ms->drained, 1);
+    ms->abort = 0;
+    fence_mbar_init();
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = ms->tmem;
+  volatile int32_t* abort_flag = &ms->abort;
+  const int total = max(0, min(n_k, __ldg(cu_k + n_seqs)));
+  const int per_tile = heads * 2;
+  const int64_t units = static_cast<int64_t>((total + kTile - 1) / kTile) * per_tile;
+  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  const int first_tile = static_cast<int>(u0 / per_tile);
+  const int first_sub = static_cast<int>(u0 - static_cast<int64_t>(first_tile) * per_tile);
+  const int count = static_cast<int>(u1 - u0);
+  bool ok = true;
+
+  if (count == 0) {
+    // nothing to do
+  } else if (warp >= kRowWarp) {
+    // ------------------------------------------------------------ rows
+    const int t = tid - kRowWarp * 32, rw = warp - kRowWarp;
+    const int n_tiles = (first_sub + count + per_tile - 1) / per_tile;
+    for (int n = 0; ok && n < n_tiles; ++n) {
+      const int tile = first_tile + n, buf = n & 1;
+      // where row t of the tile lives; the results of two tiles ago are written
+      if (n >= 2) ok = mbar_wait(&ms->rows_done[buf], ((n >> 1) - 1) & 1);
+      {
+        const int row = tile * kTile + t;
+        int64_t slot = -1;
+        if (row < total) {
+          int lo = 0, hi = n_seqs;  // the largest b with cu_k[b] <= row
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (__ldg(cu_k + mid) <= row) lo = mid;
+            else hi = mid;
+          }
+          const int start = __ldg(cu_k + lo), end = __ldg(cu_k + lo + 1);
+          const int first = k_first != nullptr ? __ldg(k_first + lo) : 0;
+          const int64_t pos = static_cast<int64_t>(first) + (row - start);
+          int32_t bits = 0;
+          if (row < start || row >= end || first < 0) {
+            bits = PSW_DEVERR_LENGTH;
+          } else if (pos / kBlockSize >= pages.max_blocks) {
+            bits = PSW_DEVERR_CAPACITY;
+          } else {
+            const int32_t blk = __ldg(pages.block_table + static_cast<int64_t>(lo) * pages.max_blocks +
+                                      pos / kBlockSize);
+            if (blk < 0 || blk >= pages.num_blocks) bits = PSW_DEVERR_BLOCK_ID;
+            else slot = static_cast<int64_t>(blk) * kBlockSize + pos % kBlockSize;
+          }
+          if (bits != 0) flag_error(err, bits);
+        }
+        ms->slot[buf][t] = static_cast<int32_t>(slot);
+        if (FP8) ms->scale[buf][t] = slot >= 0 ? __ldg(pages.row_scale + slot) : 0.f;
+      }
+      named_bar_sync(1, kRowThreads);
+      if (lane == 0) mbar_arrive(&ms->rows_set[buf]);
+      const int32_t* slots = ms->slot[buf];
+      // the rotary part, by the CTA that has the tile's first unit
+      if (n > 0 || first_sub == 0) {
+        for (int i = t; i < kTile * 8; i += kRowThreads) {
+          const int r = i >> 3, v = i & 7, row = tile * kTile + r;
+          if (row >= total) break;
+          const int64_t slot = slots[r];
+          uint4 y = make_uint4(0u, 0u, 0u, 0u);
+          if (slot >= 0) {
+            if (FP8) {
+              const uint2 c = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pages.pool) + slot * kRow + LAT) + v);
+              const float s = ms->scale[buf][r];
+              float f[8];
+              const uint32_t cc[2] = {c.x, c.y};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 x = lat::e4m3_values(cc[e >> 1] >> (16 * (e & 1)) & 0xFFFFu);
+                f[2 * e] = x.x * s;
+                f[2 * e + 1] = x.y * s;
+              }
+              y = lat::pack8(f);
+            } else {
+              y = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(pages.pool) + slot * kRow + LAT) + v);
+            }
+          }
+          reinterpret_cast<uint4*>(k_rope)[static_cast<int64_t>(row) * 8 + v] = y;
         }
       }
-      s[i][e] = x;
+      // chunk by chunk: free, filled, fenced for the tensor core, announced
+      auto free = [&](int c) {
+        if (n > 0) ok = ok && mbar_wait(&ms->a_empty[c], (n - 1) & 1);
+      };
+      auto announce = [&](int c) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms->a_full[c]);
+      };
+      if constexpr (!FP8) {
+        const auto* pool = static_cast<const __nv_bfloat16*>(pages.pool);
+        const int v = lane & 7;  // eight lanes to a row's 128 bytes
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c) {
+          free(c);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int r = k * 16 + rw * 4 + (lane >> 3);
+            const int64_t slot = slots[r];
+            lat::copy16(smem_u32(a_smem + c * kUnit + r * 128 + ((v ^ (r & 7)) << 4)),
+                        pool + max(slot, static_cast<int64_t>(0)) * kRow + c * 64 + v * 8,
+                        slot >= 0 ? 16u : 0u);
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c) {
+          lat::copy_wait(C::kChunks - 1 - c);
+          announce(c);
+        }
+      } else {
+        const auto* pool = static_cast<const uint8_t*>(pages.pool);
+        const int v = lane & 3;  // four lanes to a row's 64 codes
+        constexpr int kBatch = 4;  // chunks whose loads are in flight together
+#pragma unroll
+        for (int c0 = 0; c0 < C::kChunks; c0 += kBatch) {
+          uint4 raw[kBatch][4];
+#pragma unroll
+          for (int c = 0; c < kBatch; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int64_t slot = slots[k * 32 + rw * 8 + (lane >> 2)];
+              raw[c][k] = slot >= 0 ? __ldg(reinterpret_cast<const uint4*>(pool + slot * kRow + (c0 + c) * 64) + v)
+                                    : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+          for (int c = 0; c < kBatch; ++c) {
+            free(c0 + c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int r = k * 32 + rw * 8 + (lane >> 2);
+              const uint32_t cc[4] = {raw[c][k].x, raw[c][k].y, raw[c][k].z, raw[c][k].w};
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float2 x = lat::e4m3_values(cc[e >> 1] >> (16 * (e & 1)) & 0xFFFFu);
+                y[e] = pack_bf16x2(x.x, x.y);  // exact
+              }
+              uint8_t* at = a_smem + (c0 + c) * kUnit + r * 128;
+              *reinterpret_cast<uint4*>(at + (((2 * v) ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(at + (((2 * v + 1) ^ (r & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+            }
+            announce(c0 + c);
+          }
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
+      // (a warp that gives up alone would leave the others at the barrier)
+      ok = !lat::bar_any(1, kRowThreads, !ok);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!ok && t == 0) {
+      *abort_flag = 1;
+      flag_error(err, PSW_DEVERR_PIPELINE);
+    }
+  } else if (warp == kWeightWarp) {
+    // ------------------------------------------------------------ weights
+    const bool one = lat::elect_one();
+    int sub = first_sub, box = 0;
+    for (int u = 0; ok && u < count; ++u) {
+#pragma unroll
+      for (int c = 0; c < C::kChunks; ++c, ++box) {
+        const int s = box % C::kRing;
+        ok = ok && mbar_wait(&ms->w_empty[s], (box / C::kRing & 1u) ^ 1u);
+        if (ok && one) {
+          mbar_arrive_expect_tx(&ms->w_full[s], kUnit);
+          lat::tma_box(smem_u32(w_ring + s * kUnit), &w_map, &ms->w_full[s], c * 64, sub * kTile, 0);
+        }
+      }
+      sub = sub + 1 == per_tile ? 0 : sub + 1;
+      ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
+    }
+    if (!ok && one) {
+      *abort_flag = 1;
+      flag_error(err, PSW_DEVERR_PIPELINE);
+      // copies in flight land before the CTA ends
+      for (int i = max(0, box - C::kRing); i < box; ++i)
+        mbar_wait(&ms->w_full[i % C::kRing], i / C::kRing & 1);
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMAs
+    const bool one = lat::elect_one();
+    constexpr uint32_t id = tc::idesc_bf16_f32(kTile, kTile, 0, 0);
+    constexpr uint32_t kStep = kUnit >> 4;
+    const uint64_t a_desc = tc::smem_desc(smem_u32(a_smem), 16, 1024, tc::kSwizzle128B);
+    const uint64_t w_desc = tc::smem_desc(smem_u32(w_ring), 16, 1024, tc::kSwizzle128B);
+    int sub = first_sub, n = 0, box = 0;
+    for (int u = 0; ok && u < count; ++u) {
+      const bool last = u == count - 1 || sub == per_tile - 1;  // of this tile here
+      const bool begins = u == 0 || sub == 0;
+      const int acc = u % kAcc;
+      ok = mbar_wait(&ms->d_empty[acc], (u / kAcc & 1u) ^ 1u);
+#pragma unroll
+      for (int c = 0; c < C::kChunks; ++c, ++box) {
+        const int s = box % C::kRing;
+        if (begins) ok = ok && mbar_wait(&ms->a_full[c], n & 1);
+        ok = ok && mbar_wait(&ms->w_full[s], box / C::kRing & 1);
+        tc::fence_after();
+        const uint64_t ad = a_desc + c * kStep, wd = w_desc + s * kStep;
+        if (ok && one) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc::mma_ss(tmem + acc * kTile, ad + k * 2, wd + k * 2, id, (c > 0 || k > 0) ? 1u : 0u);
+          tc::commit(&ms->w_empty[s]);
+          if (last) tc::commit(&ms->a_empty[c]);
+        }
+      }
+      if (ok && one) tc::commit(&ms->d_full[acc]);
+      if (last) ++n;
+      sub = sub + 1 == per_tile ? 0 : sub + 1;
+      ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
+    }
+    if (one) {
+      if (!ok) {
+        *abort_flag = 1;
+        flag_error(err, PSW_DEVERR_PIPELINE);
+      }
+      tc::commit(&ms->drained);  // every MMA has ended before tensor memory is freed
+      mbar_wait(&ms->drained, 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ results
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    uint8_t* mine = stage + warp * 2048;
+    int sub = first_sub, n = 0;
+    for (int u = 0; u < count; ++u) {
+      const int tile = first_tile + n, acc = u % kAcc, buf = n & 1;
+      const bool last = u == count - 1 || sub == per_tile - 1;
+      if (FP8 && (u == 0 || sub == 0)) ok = mbar_wait(&ms->rows_set[buf], n >> 1 & 1);
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(&ms->d_full[acc], u / kAcc & 1) && *abort_flag == 0);
+      if (!ok) break;
+      tc::fence_after();
+      const float s = FP8 ? ms->scale[buf][warp * 32 + lane] : 1.f;
+      const int row0 = tile * kTile + warp * 32;
+      const int head = sub >> 1, part = sub & 1;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {  // 32 columns at a time
+        uint32_t v[32];
+        tc::ld32(tmem + lanes + acc * kTile + g * 32, v);
+        tc::wait_ld();
+        if (g == 3) {  // the accumulator has been read
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms->d_empty[acc]);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = FP8 ? __uint_as_float(v[q * 8 + e]) * s : __uint_as_float(v[q * 8 + e]);
+          *reinterpret_cast<uint4*>(mine + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) = lat::pack8(y);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = k * 8 + (lane >> 2), q = lane & 3;
+          const uint4 y = *reinterpret_cast<const uint4*>(mine + r * 64 + ((q ^ (r >> 1 & 3)) << 4));
+          if (row0 + r < total)
+            *reinterpret_cast<uint4*>(kv + (static_cast<int64_t>(row0 + r) * heads + head) * kLatentKv +
+                                      part * kTile + g * 32 + q * 8) = y;
+        }
+        __syncwarp();
+      }
+      if (last) {
+        if (lane == 0) mbar_arrive(&ms->rows_done[buf]);
+        ++n;
+      }
+      sub = sub + 1 == per_tile ? 0 : sub + 1;
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      flag_error(err, PSW_DEVERR_PIPELINE);
     }
   }
+  __syncwarp();
+  tc::fence_before();
   __syncthreads();
-  const int e = threadIdx.x;
-  float acc[kTile];
-#pragma unroll
-  for (int i = 0; i < kTile; ++i) acc[i] = 0.f;
-  const __nv_bfloat16* wr = w + (static_cast<int64_t>(head) * kLatentKv + e) * LAT;
-  for (int l = 0; l < LAT; l += 8) {
-    float x[8];
-    lat::unpack8(__ldg(reinterpret_cast<const uint4*>(wr + l)), x);
-#pragma unroll
-    for (int d = 0; d < 8; ++d)
-#pragma unroll
-      for (int i = 0; i < kTile; ++i) acc[i] = fmaf(s[i][l + d], x[d], acc[i]);
-  }
-  for (int i = 0; i < kTile; ++i) {
-    if (i >= rows) break;
-    kv[(static_cast<int64_t>(t0 + i) * heads + head) * kLatentKv + e] = __float2bfloat16_rn(acc[i]);
-    if (head == 0 && e < kLatentRope)
-      k_rope[static_cast<int64_t>(t0 + i) * kLatentRope + e] = __float2bfloat16_rn(s[i][LAT + e]);
-  }
+  if (warp == kMmaWarp) tc::dealloc(tmem, 512);
 }
 
-}  // namespace
+template <int LAT, bool FP8>
+int launch(const LatentArgs& L, const LatentPages& pages, const int32_t* cu_k,
+           const int32_t* k_first, int n_seqs, int n_k_total, const void* w, void* kv,
+           void* k_rope, int num_sms, int32_t* err, cudaStream_t stream) {
+  using C = Cfg<LAT>;
+  CUtensorMap w_map;
+  int rc = make_map_3d(&w_map, false, w, {LAT, static_cast<int64_t>(L.n_heads) * kLatentKv, 1},
+                       {2 * LAT, 2 * LAT}, {64, kTile, 1});
+  if (rc != PSW_OK) return rc;
+  auto* kernel = latent_expand_kernel<LAT, FP8>;
+  rc = set_smem_limit(reinterpret_cast<const void*>(kernel), C::kSmemBytes);
+  if (rc != PSW_OK) return rc;
+  kernel<<<num_sms, kThreads, C::kSmemBytes, stream>>>(
+      w_map, pages, cu_k, k_first, n_seqs, n_k_total, L.n_heads,
+      static_cast<__nv_bfloat16*>(kv), static_cast<__nv_bfloat16*>(k_rope), err);
+  return cudaGetLastError() == cudaSuccess ? PSW_OK : PSW_ELAUNCH;
+}
+
+}  // namespace lexp
 
 int launch_latent_expand(const LatentArgs& L, const LatentPages& pages, const int32_t* cu_k,
                          const int32_t* k_first, int n_seqs, int n_k_total, const void* w,
                          void* kv, void* k_rope, int num_sms, int32_t* err, cudaStream_t stream) {
-  const dim3 grid((n_k_total + kTile - 1) / kTile, L.n_heads);
-  auto* kernel = L.latent == 512 ? latent_expand_kernel<512> : latent_expand_kernel<256>;
-  kernel<<<grid, kLatentKv, 0, stream>>>(pages, cu_k, k_first, n_seqs, n_k_total, L.n_heads,
-                                         static_cast<const __nv_bfloat16*>(w),
-                                         static_cast<__nv_bfloat16*>(kv),
-                                         static_cast<__nv_bfloat16*>(k_rope), err);
-  return cudaGetLastError() == cudaSuccess ? PSW_OK : PSW_ELAUNCH;
+  const bool fp8 = pages.row_scale != nullptr;
+  auto* go = L.latent == 512 ? (fp8 ? lexp::launch<512, true> : lexp::launch<512, false>)
+                             : (fp8 ? lexp::launch<256, true> : lexp::launch<256, false>);
+  return go(L, pages, cu_k, k_first, n_seqs, n_k_total, w, kv, k_rope, num_sms, err, stream);
 }
 
 }  // namespace psw
