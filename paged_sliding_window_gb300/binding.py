@@ -432,20 +432,18 @@ def alloc_latent_workspace(layer, n_seqs: int, device="cuda") -> torch.Tensor:
 
 
 def _want(t, dtype, shape, name, device, strided=False):
-    """Checks one tensor: dtype, device, shape (None: any extent), contiguity (`strided`: the
-    last dimension alone)."""
+    """Checks one tensor: dtype, device, shape, contiguity (`strided`: the last dimension
+    alone)."""
+    if (t.dtype is dtype and t.get_device() == device and t.shape == shape
+            and (t.is_contiguous() or (strided and (t.stride(-1) == 1 or shape[-1] <= 1)))):
+        return  # (a serving step makes several of these checks per launch)
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda or t.get_device() != device:
         raise ValueError(f"{name} must be a CUDA tensor on device {device}")
-    have = t.shape
-    if len(have) != len(shape) or any(n is not None and n != m for n, m in zip(shape, have)):
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(have)}")
-    if strided:
-        if have[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{name} must be contiguous in its last dimension")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous" + (" in its last dimension" if strided else ""))
 
 
 def _stream_of(device, stream):
@@ -454,17 +452,21 @@ def _stream_of(device, stream):
     if device != torch.cuda.current_device():
         raise ValueError(f"the tensors are on device {device}, the current device is "
                          f"{torch.cuda.current_device()}")
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream
 
 
 def _strides(t):
     """Strides of all but the last dimension; a dimension of extent 1 gets that of packed rows
     (torch leaves any number there)."""
-    st, packed = list(t.stride()), 1
-    for d in range(t.dim() - 1, -1, -1):
-        if t.shape[d] == 1:
-            st[d] = packed
-        packed = max(packed, st[d] * t.shape[d])
+    st = t.stride()
+    if 1 in t.shape:
+        st, packed = list(st), 1
+        for d in range(t.dim() - 1, -1, -1):
+            if t.shape[d] == 1:
+                st[d] = packed
+            packed = max(packed, st[d] * t.shape[d])
     return st[:-1]
 
 
@@ -476,7 +478,7 @@ def _latent_write(name, layer, norm, ckv, q_rope, cu_new, past_lens, pages, q_ro
     z = make_latent_layer(layer)
     row, dev = z.latent_dim + z.rope_dim, ckv.get_device()
     n_seqs, n_tok = past_lens.shape[0], ckv.shape[0]
-    _want(ckv, _BF16, (None, row), "ckv", dev, strided=True)
+    _want(ckv, _BF16, (n_tok, row), "ckv", dev, strided=True)
     _want(cu_new, _I32, (n_seqs + 1,), "cu_new", dev)
     _want(past_lens, _I32, (n_seqs,), "past_lens", dev)
     _want(pool, _BF16 if row_scale is None else _U8, (pages.num_blocks, 16, row), "pool", dev)
