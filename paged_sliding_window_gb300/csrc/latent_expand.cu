@@ -4,10 +4,13 @@
 // A matrix product of gathered rows, 512 or 1024 operations per output byte:
 // bound by the tensor cores, beside writing 512 bytes per row and head.
 //
-// Schedule: the list of units (tile of 128 rows, head, keys or values: 128 x 128
-// outputs) is cut evenly over one CTA per SM. A CTA holds the rows of its tile in
-// shared memory (L / 64 chunks of 128 rows x 128 B, swizzled) while w streams
-// past them in boxes of 128 x 64 (warp 5, TMA). Warp 4 issues tcgen05.mma into
+// Schedule: the list of units (two tiles of 128 rows, a head, keys or values: 128
+// outputs of each row) is cut evenly over clusters of two CTAs, one per SM, each
+// with one of the two tiles. A CTA holds its rows in shared memory (L / 64 chunks
+// of 128 rows x 128 B, swizzled) while w streams past them in boxes of 128 x 64
+// (warp 5, TMA). w would need 64 bytes a cycle of every SM and L2 gives them 28
+// (148 us for 36k rows of 16 heads that way); each CTA loads half of a box for
+// both. Warp 4 issues tcgen05.mma into
 // four accumulators in tensor memory, warps 0-3 round, turn the rows around
 // through shared memory and write 64-byte pieces. Warps 6-9 gather rows: rows of
 // a tile are any rows of any pages, so they are copied 16 bytes at a time
@@ -27,6 +30,8 @@ constexpr int kThreads = 320;
 constexpr int kAcc = 4;                         // accumulators of 128 columns
 constexpr int kStage = 4 * 32 * 64;             // epilogue: 32 rows x 64 B per warp
 constexpr int kMisc = 3072;
+constexpr int kCluster = 2;
+constexpr uint16_t kBoth = 3;
 constexpr int kSmemLimit = 232448;
 
 template <int LAT>
@@ -48,7 +53,7 @@ struct Misc {
 static_assert(sizeof(Misc) <= kMisc, "misc block");
 
 template <int LAT, bool FP8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
 latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPages pages,
                      const int32_t* __restrict__ cu_k, const int32_t* __restrict__ k_first,
                      int n_seqs, int n_k, int heads, __nv_bfloat16* __restrict__ kv,
@@ -74,7 +79,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
     }
     for (int i = 0; i < 16; ++i) {
       mbar_init(&ms->w_full[i], 1);
-      mbar_init(&ms->w_empty[i], 1);
+      mbar_init(&ms->w_empty[i], kCluster);
     }
     for (int i = 0; i < kAcc; ++i) {
       mbar_init(&ms->d_full[i], 1);
@@ -88,15 +93,19 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
     ms->abort = 0;
     fence_mbar_init();
   }
+  __syncwarp();
   tc::fence_before();
-  __syncthreads();
+  lat::cluster_sync();
   tc::fence_after();
-  const uint32_t tmem = ms->tmem;
+  const uint32_t tmem = ms->tmem, rank = lat::cluster_rank();
   volatile int32_t* abort_flag = &ms->abort;
   const int total = max(0, min(n_k, __ldg(cu_k + n_seqs)));
   const int per_tile = heads * 2;
-  const int64_t units = static_cast<int64_t>((total + kTile - 1) / kTile) * per_tile;
-  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  const int pair = blockIdx.x / kCluster, pairs = gridDim.x / kCluster;
+  const int64_t units =
+      (static_cast<int64_t>(total) + kCluster * kTile - 1) / (kCluster * kTile) * per_tile;
+  const int64_t u0 = units * pair / pairs, u1 = units * (pair + 1) / pairs;
+  // tile n of this CTA is number kCluster (first_tile + n) + rank
   const int first_tile = static_cast<int>(u0 / per_tile);
   const int first_sub = static_cast<int>(u0 - static_cast<int64_t>(first_tile) * per_tile);
   const int count = static_cast<int>(u1 - u0);
@@ -109,13 +118,14 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
     const int t = tid - kRowWarp * 32, rw = warp - kRowWarp;
     const int n_tiles = (first_sub + count + per_tile - 1) / per_tile;
     for (int n = 0; ok && n < n_tiles; ++n) {
-      const int tile = first_tile + n, buf = n & 1;
+      const int64_t row0 = (static_cast<int64_t>(first_tile + n) * kCluster + rank) * kTile;
+      const int buf = n & 1;
       // where row t of the tile lives; the results of two tiles ago are written
       if (n >= 2) ok = mbar_wait(&ms->rows_done[buf], ((n >> 1) - 1) & 1);
       {
-        const int row = tile * kTile + t;
         int64_t slot = -1;
-        if (row < total) {
+        if (row0 + t < total) {
+          const int row = static_cast<int>(row0) + t;
           int lo = 0, hi = n_seqs;  // the largest b with cu_k[b] <= row
           while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -147,7 +157,8 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
       // the rotary part, by the CTA that has the tile's first unit
       if (n > 0 || first_sub == 0) {
         for (int i = t; i < kTile * 8; i += kRowThreads) {
-          const int r = i >> 3, v = i & 7, row = tile * kTile + r;
+          const int r = i >> 3, v = i & 7;
+          const int64_t row = row0 + r;
           if (row >= total) break;
           const int64_t slot = slots[r];
           uint4 y = make_uint4(0u, 0u, 0u, 0u);
@@ -168,7 +179,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
               y = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(pages.pool) + slot * kRow + LAT) + v);
             }
           }
-          reinterpret_cast<uint4*>(k_rope)[static_cast<int64_t>(row) * 8 + v] = y;
+          reinterpret_cast<uint4*>(k_rope)[row * 8 + v] = y;
         }
       }
       // chunk by chunk: free, filled, fenced for the tensor core, announced
@@ -257,7 +268,9 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
         ok = ok && mbar_wait(&ms->w_empty[s], (box / C::kRing & 1u) ^ 1u);
         if (ok && one) {
           mbar_arrive_expect_tx(&ms->w_full[s], kUnit);
-          lat::tma_box(smem_u32(w_ring + s * kUnit), &w_map, &ms->w_full[s], c * 64, sub * kTile, 0);
+          lat::tma_box_multicast(smem_u32(w_ring + s * kUnit + rank * (kUnit / kCluster)), &w_map,
+                                 &ms->w_full[s], c * 64, sub * kTile + rank * (kTile / kCluster),
+                                 0, kBoth);
         }
       }
       sub = sub + 1 == per_tile ? 0 : sub + 1;
@@ -266,7 +279,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
     if (!ok && one) {
       *abort_flag = 1;
       flag_error(err, PSW_DEVERR_PIPELINE);
-      // copies in flight land before the CTA ends
+      // copies in flight land before the CTAs end
       for (int i = max(0, box - C::kRing); i < box; ++i)
         mbar_wait(&ms->w_full[i % C::kRing], i / C::kRing & 1);
     }
@@ -294,7 +307,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             tc::mma_ss(tmem + acc * kTile, ad + k * 2, wd + k * 2, id, (c > 0 || k > 0) ? 1u : 0u);
-          tc::commit(&ms->w_empty[s]);
+          lat::commit_multicast(&ms->w_empty[s], kBoth);
           if (last) tc::commit(&ms->a_empty[c]);
         }
       }
@@ -318,14 +331,15 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
     uint8_t* mine = stage + warp * 2048;
     int sub = first_sub, n = 0;
     for (int u = 0; u < count; ++u) {
-      const int tile = first_tile + n, acc = u % kAcc, buf = n & 1;
+      const int acc = u % kAcc, buf = n & 1;
       const bool last = u == count - 1 || sub == per_tile - 1;
       if (FP8 && (u == 0 || sub == 0)) ok = mbar_wait(&ms->rows_set[buf], n >> 1 & 1);
       ok = __all_sync(0xffffffffu, ok && mbar_wait(&ms->d_full[acc], u / kAcc & 1) && *abort_flag == 0);
       if (!ok) break;
       tc::fence_after();
       const float s = FP8 ? ms->scale[buf][warp * 32 + lane] : 1.f;
-      const int row0 = tile * kTile + warp * 32;
+      const int64_t row0 =
+          (static_cast<int64_t>(first_tile + n) * kCluster + rank) * kTile + warp * 32;
       const int head = sub >> 1, part = sub & 1;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {  // 32 columns at a time
@@ -350,7 +364,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
           const int r = k * 8 + (lane >> 2), q = lane & 3;
           const uint4 y = *reinterpret_cast<const uint4*>(mine + r * 64 + ((q ^ (r >> 1 & 3)) << 4));
           if (row0 + r < total)
-            *reinterpret_cast<uint4*>(kv + (static_cast<int64_t>(row0 + r) * heads + head) * kLatentKv +
+            *reinterpret_cast<uint4*>(kv + ((row0 + r) * heads + head) * kLatentKv +
                                       part * kTile + g * 32 + q * 8) = y;
         }
         __syncwarp();
@@ -368,7 +382,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
   }
   __syncwarp();
   tc::fence_before();
-  __syncthreads();
+  lat::cluster_sync();  // nobody leaves while the other may still reach into it
   if (warp == kMmaWarp) tc::dealloc(tmem, 512);
 }
 
@@ -379,12 +393,12 @@ int launch(const LatentArgs& L, const LatentPages& pages, const int32_t* cu_k,
   using C = Cfg<LAT>;
   CUtensorMap w_map;
   int rc = make_map_3d(&w_map, false, w, {LAT, static_cast<int64_t>(L.n_heads) * kLatentKv, 1},
-                       {2 * LAT, 2 * LAT}, {64, kTile, 1});
+                       {2 * LAT, 2 * LAT}, {64, kTile / kCluster, 1});
   if (rc != PSW_OK) return rc;
   auto* kernel = latent_expand_kernel<LAT, FP8>;
   rc = set_smem_limit(reinterpret_cast<const void*>(kernel), C::kSmemBytes);
   if (rc != PSW_OK) return rc;
-  kernel<<<num_sms, kThreads, C::kSmemBytes, stream>>>(
+  kernel<<<num_sms / kCluster * kCluster, kThreads, C::kSmemBytes, stream>>>(
       w_map, pages, cu_k, k_first, n_seqs, n_k_total, L.n_heads,
       static_cast<__nv_bfloat16*>(kv), static_cast<__nv_bfloat16*>(k_rope), err);
   return cudaGetLastError() == cudaSuccess ? PSW_OK : PSW_ELAUNCH;
