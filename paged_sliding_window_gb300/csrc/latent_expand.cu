@@ -6,17 +6,18 @@
 //
 // Schedule: the list of units (two tiles of 128 rows, a head, keys or values: 128
 // outputs of each row) is cut evenly over clusters of two CTAs, one per SM, each
-// with one of the two tiles. A CTA holds its rows in shared memory (L / 64 chunks
-// of 128 rows x 128 B, swizzled) while w streams past them in boxes of 128 x 64
-// (warp 5, TMA). w would need 64 bytes a cycle of every SM and L2 gives them 28
-// (148 us for 36k rows of 16 heads that way); each CTA loads half of a box for
-// both. Warp 4 issues tcgen05.mma into
-// four accumulators in tensor memory, warps 0-3 round, turn the rows around
-// through shared memory and write 64-byte pieces. Warps 6-9 gather rows: rows of
-// a tile are any rows of any pages, so they are copied 16 bytes at a time
-// (asynchronously; FP8 codes are exact in bf16 and are converted on the way, the
-// row's scale multiplies the fp32 result). A chunk of the next tile is loaded as
-// soon as the last unit of this one has used it.
+// with one of the two tiles. A CTA holds its rows in tensor memory (A of the
+// products: 128 lanes x L / 2 columns) while w streams past them in boxes of
+// 128 x 64 (warp 5, TMA; each CTA loads half of a box for both). With the rows in
+// shared memory instead, that memory's 128 bytes a cycle were the bound (a product
+// of 128 x 128 then reads as many as it takes cycles, and w's boxes, another
+// half of that, come on top): 144 us for 36k rows of 16 heads. Warp 4 issues
+// tcgen05.mma into two accumulators, warps 0-3 round, turn the rows around through
+// shared memory and write 64-byte pieces. Warps 6-9 gather rows: rows of a tile are
+// any rows of any pages, so they are copied 16 bytes at a time (asynchronously; FP8
+// codes are exact in bf16 and are converted on the way, the row's scale multiplies
+// the fp32 result) into shared memory, a tile ahead, and moved into tensor memory
+// chunk by chunk as the last unit of the tile before is done with them.
 #include "latent.cuh"
 
 namespace psw {
@@ -27,7 +28,7 @@ constexpr int kUnit = kTile * 128;              // bytes of a chunk and of a box
 constexpr int kMmaWarp = 4, kWeightWarp = 5, kRowWarp = 6;
 constexpr int kRowThreads = 128;                // warps 6-9
 constexpr int kThreads = 320;
-constexpr int kAcc = 4;                         // accumulators of 128 columns
+constexpr int kAcc = 2;                         // accumulators of 128 columns
 constexpr int kStage = 4 * 32 * 64;             // epilogue: 32 rows x 64 B per warp
 constexpr int kMisc = 3072;
 constexpr int kCluster = 2;
@@ -40,6 +41,8 @@ struct Cfg {
   static constexpr int kRing = (kSmemLimit - 1024 - kMisc - kStage - kChunks * kUnit) / kUnit;
   static constexpr int kSmemBytes = 1024 + (kChunks + kRing) * kUnit + kStage + kMisc;
   static_assert(kRing >= 4 && kRing <= 16, "boxes of w in flight");
+  static constexpr int kTmemD = LAT / 2;          // after the rows
+  static_assert(kTmemD + kAcc * kTile <= 512, "tensor memory columns");
 };
 
 struct Misc {
@@ -63,7 +66,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* a_smem = smem;
+  uint8_t* a_smem = smem;  // rows of the next tile
   uint8_t* w_ring = smem + C::kChunks * kUnit;
   uint8_t* stage = w_ring + C::kRing * kUnit;
   Misc* ms = reinterpret_cast<Misc*>(stage + kStage);
@@ -117,11 +120,13 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
     // ------------------------------------------------------------ rows
     const int t = tid - kRowWarp * 32, rw = warp - kRowWarp;
     const int n_tiles = (first_sub + count + per_tile - 1) / per_tile;
-    for (int n = 0; ok && n < n_tiles; ++n) {
+    // tile n into shared memory: where each row lives, the rotary part (written
+    // by the CTA that has the tile's first unit), the latents
+    auto fetch = [&](int n) {
       const int64_t row0 = (static_cast<int64_t>(first_tile + n) * kCluster + rank) * kTile;
       const int buf = n & 1;
-      // where row t of the tile lives; the results of two tiles ago are written
-      if (n >= 2) ok = mbar_wait(&ms->rows_done[buf], ((n >> 1) - 1) & 1);
+      // (the results of two tiles ago are written: its scales are done with)
+      if (n >= 2) ok = ok && mbar_wait(&ms->rows_done[buf], ((n >> 1) - 1) & 1);
       {
         int64_t slot = -1;
         if (row0 + t < total) {
@@ -154,49 +159,11 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
       named_bar_sync(1, kRowThreads);
       if (lane == 0) mbar_arrive(&ms->rows_set[buf]);
       const int32_t* slots = ms->slot[buf];
-      // the rotary part, by the CTA that has the tile's first unit
-      if (n > 0 || first_sub == 0) {
-        for (int i = t; i < kTile * 8; i += kRowThreads) {
-          const int r = i >> 3, v = i & 7;
-          const int64_t row = row0 + r;
-          if (row >= total) break;
-          const int64_t slot = slots[r];
-          uint4 y = make_uint4(0u, 0u, 0u, 0u);
-          if (slot >= 0) {
-            if (FP8) {
-              const uint2 c = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pages.pool) + slot * kRow + LAT) + v);
-              const float s = ms->scale[buf][r];
-              float f[8];
-              const uint32_t cc[2] = {c.x, c.y};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 x = lat::e4m3_values(cc[e >> 1] >> (16 * (e & 1)) & 0xFFFFu);
-                f[2 * e] = x.x * s;
-                f[2 * e + 1] = x.y * s;
-              }
-              y = lat::pack8(f);
-            } else {
-              y = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(pages.pool) + slot * kRow + LAT) + v);
-            }
-          }
-          reinterpret_cast<uint4*>(k_rope)[row * 8 + v] = y;
-        }
-      }
-      // chunk by chunk: free, filled, fenced for the tensor core, announced
-      auto free = [&](int c) {
-        if (n > 0) ok = ok && mbar_wait(&ms->a_empty[c], (n - 1) & 1);
-      };
-      auto announce = [&](int c) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms->a_full[c]);
-      };
       if constexpr (!FP8) {
         const auto* pool = static_cast<const __nv_bfloat16*>(pages.pool);
         const int v = lane & 7;  // eight lanes to a row's 128 bytes
 #pragma unroll
         for (int c = 0; c < C::kChunks; ++c) {
-          free(c);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int r = k * 16 + rw * 4 + (lane >> 3);
@@ -206,11 +173,6 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
                         slot >= 0 ? 16u : 0u);
           }
           asm volatile("cp.async.commit_group;" ::: "memory");
-        }
-#pragma unroll
-        for (int c = 0; c < C::kChunks; ++c) {
-          lat::copy_wait(C::kChunks - 1 - c);
-          announce(c);
         }
       } else {
         const auto* pool = static_cast<const uint8_t*>(pages.pool);
@@ -228,8 +190,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
                                     : make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
-          for (int c = 0; c < kBatch; ++c) {
-            free(c0 + c);
+          for (int c = 0; c < kBatch; ++c)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int r = k * 32 + rw * 8 + (lane >> 2);
@@ -244,13 +205,66 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
               *reinterpret_cast<uint4*>(at + (((2 * v) ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
               *reinterpret_cast<uint4*>(at + (((2 * v + 1) ^ (r & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
             }
-            announce(c0 + c);
-          }
         }
       }
-      ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
-      // (a warp that gives up alone would leave the others at the barrier)
-      ok = !lat::bar_any(1, kRowThreads, !ok);
+      if (n == 0 && first_sub != 0) return;
+      for (int i = t; i < kTile * 8; i += kRowThreads) {
+        const int r = i >> 3, v = i & 7;
+        const int64_t row = row0 + r;
+        if (row >= total) break;
+        const int64_t slot = slots[r];
+        uint4 y = make_uint4(0u, 0u, 0u, 0u);
+        if (slot >= 0) {
+          if (FP8) {
+            const uint2 c = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pages.pool) + slot * kRow + LAT) + v);
+            const float s = ms->scale[buf][r];
+            const uint32_t cc[2] = {c.x, c.y};
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 x = lat::e4m3_values(cc[e >> 1] >> (16 * (e & 1)) & 0xFFFFu);
+              f[2 * e] = x.x * s;
+              f[2 * e + 1] = x.y * s;
+            }
+            y = lat::pack8(f);
+          } else {
+            y = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(pages.pool) + slot * kRow + LAT) + v);
+          }
+        }
+        reinterpret_cast<uint4*>(k_rope)[row * 8 + v] = y;
+      }
+    };
+    // this warp's lanes of tensor memory are the rows 32 (warp mod 4) + lane
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    fetch(0);
+    for (int n = 0; n < n_tiles; ++n) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      // (all copies have landed; a warp that gives up takes the others along)
+      if (lat::bar_any(1, kRowThreads, !ok || *abort_flag != 0)) {
+        ok = false;
+        break;
+      }
+#pragma unroll
+      for (int c = 0; c < C::kChunks; ++c) {
+        uint32_t y[32];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const uint4 x = *reinterpret_cast<const uint4*>(a_smem + c * kUnit + r * 128 + ((v ^ (r & 7)) << 4));
+          y[4 * v] = x.x, y[4 * v + 1] = x.y, y[4 * v + 2] = x.z, y[4 * v + 3] = x.w;
+        }
+        if (n > 0) ok = ok && mbar_wait(&ms->a_empty[c], (n - 1) & 1);
+        tc::fence_after();
+        __syncwarp();
+        tc::st16(tmem + lanes + c * 32, *reinterpret_cast<uint32_t(*)[16]>(&y[0]));
+        tc::st16(tmem + lanes + c * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(&y[16]));
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms->a_full[c]);
+      }
+      named_bar_sync(1, kRowThreads);  // the rows have been read: the next may come
+      if (n + 1 < n_tiles) fetch(n + 1);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (!ok && t == 0) {
@@ -288,7 +302,6 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
     const bool one = lat::elect_one();
     constexpr uint32_t id = tc::idesc_bf16_f32(kTile, kTile, 0, 0);
     constexpr uint32_t kStep = kUnit >> 4;
-    const uint64_t a_desc = tc::smem_desc(smem_u32(a_smem), 16, 1024, tc::kSwizzle128B);
     const uint64_t w_desc = tc::smem_desc(smem_u32(w_ring), 16, 1024, tc::kSwizzle128B);
     int sub = first_sub, n = 0, box = 0;
     for (int u = 0; ok && u < count; ++u) {
@@ -302,11 +315,12 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
         if (begins) ok = ok && mbar_wait(&ms->a_full[c], n & 1);
         ok = ok && mbar_wait(&ms->w_full[s], box / C::kRing & 1);
         tc::fence_after();
-        const uint64_t ad = a_desc + c * kStep, wd = w_desc + s * kStep;
+        const uint64_t wd = w_desc + s * kStep;
         if (ok && one) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc::mma_ss(tmem + acc * kTile, ad + k * 2, wd + k * 2, id, (c > 0 || k > 0) ? 1u : 0u);
+            tc::mma_ts(tmem + C::kTmemD + acc * kTile, tmem + c * 32 + k * 8, wd + k * 2, id,
+                       (c > 0 || k > 0) ? 1u : 0u);
           lat::commit_multicast(&ms->w_empty[s], kBoth);
           if (last) tc::commit(&ms->a_empty[c]);
         }
@@ -344,7 +358,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
 #pragma unroll
       for (int g = 0; g < 4; ++g) {  // 32 columns at a time
         uint32_t v[32];
-        tc::ld32(tmem + lanes + acc * kTile + g * 32, v);
+        tc::ld32(tmem + lanes + C::kTmemD + acc * kTile + g * 32, v);
         tc::wait_ld();
         if (g == 3) {  // the accumulator has been read
           tc::fence_before();
