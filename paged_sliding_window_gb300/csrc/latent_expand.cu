@@ -16,8 +16,11 @@
 // shared memory and write 64-byte pieces. Warps 6-9 gather rows: rows of a tile are
 // any rows of any pages, so they are copied 16 bytes at a time (asynchronously; FP8
 // codes are exact in bf16 and are converted on the way, the row's scale multiplies
-// the fp32 result) into shared memory, a tile ahead, and moved into tensor memory
-// chunk by chunk as the last unit of the tile before is done with them.
+// the fp32 result) into shared memory, four chunks of the next tile ahead, and
+// moved into tensor memory chunk by chunk as the last unit of the tile before is
+// done with them. The rest of shared memory, 147 KB, is w on its way: at 64 bytes a
+// cycle a smaller ring waits for L2's latency (80 KB, with all of the next tile's
+// rows ahead: 135 us).
 #include "latent.cuh"
 
 namespace psw {
@@ -31,6 +34,7 @@ constexpr int kThreads = 320;
 constexpr int kAcc = 2;                         // accumulators of 128 columns
 constexpr int kStage = 4 * 32 * 64;             // epilogue: 32 rows x 64 B per warp
 constexpr int kMisc = 3072;
+constexpr int kAhead = 4;                       // chunks of rows in shared memory
 constexpr int kCluster = 2;
 constexpr uint16_t kBoth = 3;
 constexpr int kSmemLimit = 232448;
@@ -38,8 +42,9 @@ constexpr int kSmemLimit = 232448;
 template <int LAT>
 struct Cfg {
   static constexpr int kChunks = LAT / 64;
-  static constexpr int kRing = (kSmemLimit - 1024 - kMisc - kStage - kChunks * kUnit) / kUnit;
-  static constexpr int kSmemBytes = 1024 + (kChunks + kRing) * kUnit + kStage + kMisc;
+  static constexpr int kRing = (kSmemLimit - 1024 - kMisc - kStage - kAhead * kUnit) / kUnit;
+  static constexpr int kSmemBytes = 1024 + (kAhead + kRing) * kUnit + kStage + kMisc;
+  static_assert(kChunks % kAhead == 0, "rows come in groups of chunks");
   static_assert(kRing >= 4 && kRing <= 16, "boxes of w in flight");
   static constexpr int kTmemD = LAT / 2;          // after the rows
   static_assert(kTmemD + kAcc * kTile <= 512, "tensor memory columns");
@@ -66,8 +71,8 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* a_smem = smem;  // rows of the next tile
-  uint8_t* w_ring = smem + C::kChunks * kUnit;
+  uint8_t* a_smem = smem;  // rows on their way
+  uint8_t* w_ring = smem + kAhead * kUnit;
   uint8_t* stage = w_ring + C::kRing * kUnit;
   Misc* ms = reinterpret_cast<Misc*>(stage + kStage);
 
@@ -120,56 +125,60 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
     // ------------------------------------------------------------ rows
     const int t = tid - kRowWarp * 32, rw = warp - kRowWarp;
     const int n_tiles = (first_sub + count + per_tile - 1) / per_tile;
-    // tile n into shared memory: where each row lives, the rotary part (written
-    // by the CTA that has the tile's first unit), the latents
-    auto fetch = [&](int n) {
+    const int r = (warp & 3) * 32 + lane;  // this warp's lanes of tensor memory are these rows
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    uint4 raw[kAhead][4];  // FP8: the codes of a group of chunks
+
+    // where each row of tile n lives
+    auto locate = [&](int n) {
       const int64_t row0 = (static_cast<int64_t>(first_tile + n) * kCluster + rank) * kTile;
       const int buf = n & 1;
       // (the results of two tiles ago are written: its scales are done with)
       if (n >= 2) ok = ok && mbar_wait(&ms->rows_done[buf], ((n >> 1) - 1) & 1);
-      {
-        int64_t slot = -1;
-        if (row0 + t < total) {
-          const int row = static_cast<int>(row0) + t;
-          int lo = 0, hi = n_seqs;  // the largest b with cu_k[b] <= row
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (__ldg(cu_k + mid) <= row) lo = mid;
-            else hi = mid;
-          }
-          const int start = __ldg(cu_k + lo), end = __ldg(cu_k + lo + 1);
-          const int first = k_first != nullptr ? __ldg(k_first + lo) : 0;
-          const int64_t pos = static_cast<int64_t>(first) + (row - start);
-          int32_t bits = 0;
-          if (row < start || row >= end || first < 0) {
-            bits = PSW_DEVERR_LENGTH;
-          } else if (pos / kBlockSize >= pages.max_blocks) {
-            bits = PSW_DEVERR_CAPACITY;
-          } else {
-            const int32_t blk = __ldg(pages.block_table + static_cast<int64_t>(lo) * pages.max_blocks +
-                                      pos / kBlockSize);
-            if (blk < 0 || blk >= pages.num_blocks) bits = PSW_DEVERR_BLOCK_ID;
-            else slot = static_cast<int64_t>(blk) * kBlockSize + pos % kBlockSize;
-          }
-          if (bits != 0) flag_error(err, bits);
+      int64_t slot = -1;
+      if (row0 + t < total) {
+        const int row = static_cast<int>(row0) + t;
+        int lo = 0, hi = n_seqs;  // the largest b with cu_k[b] <= row
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (__ldg(cu_k + mid) <= row) lo = mid;
+          else hi = mid;
         }
-        ms->slot[buf][t] = static_cast<int32_t>(slot);
-        if (FP8) ms->scale[buf][t] = slot >= 0 ? __ldg(pages.row_scale + slot) : 0.f;
+        const int start = __ldg(cu_k + lo), end = __ldg(cu_k + lo + 1);
+        const int first = k_first != nullptr ? __ldg(k_first + lo) : 0;
+        const int64_t pos = static_cast<int64_t>(first) + (row - start);
+        int32_t bits = 0;
+        if (row < start || row >= end || first < 0) {
+          bits = PSW_DEVERR_LENGTH;
+        } else if (pos / kBlockSize >= pages.max_blocks) {
+          bits = PSW_DEVERR_CAPACITY;
+        } else {
+          const int32_t blk = __ldg(pages.block_table + static_cast<int64_t>(lo) * pages.max_blocks +
+                                    pos / kBlockSize);
+          if (blk < 0 || blk >= pages.num_blocks) bits = PSW_DEVERR_BLOCK_ID;
+          else slot = static_cast<int64_t>(blk) * kBlockSize + pos % kBlockSize;
+        }
+        if (bits != 0) flag_error(err, bits);
       }
+      ms->slot[buf][t] = static_cast<int32_t>(slot);
+      if (FP8) ms->scale[buf][t] = slot >= 0 ? __ldg(pages.row_scale + slot) : 0.f;
       named_bar_sync(1, kRowThreads);
       if (lane == 0) mbar_arrive(&ms->rows_set[buf]);
-      const int32_t* slots = ms->slot[buf];
+    };
+    // the group of chunks from c0 on of the rows in slots: on their way (bf16: to
+    // shared memory, a copy group per chunk; FP8: to registers)
+    auto start = [&](const int32_t* slots, int c0) {
       if constexpr (!FP8) {
         const auto* pool = static_cast<const __nv_bfloat16*>(pages.pool);
         const int v = lane & 7;  // eight lanes to a row's 128 bytes
 #pragma unroll
-        for (int c = 0; c < C::kChunks; ++c) {
+        for (int c = 0; c < kAhead; ++c) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const int r = k * 16 + rw * 4 + (lane >> 3);
-            const int64_t slot = slots[r];
-            lat::copy16(smem_u32(a_smem + c * kUnit + r * 128 + ((v ^ (r & 7)) << 4)),
-                        pool + max(slot, static_cast<int64_t>(0)) * kRow + c * 64 + v * 8,
+            const int q = k * 16 + rw * 4 + (lane >> 3);
+            const int64_t slot = slots[q];
+            lat::copy16(smem_u32(a_smem + c * kUnit + q * 128 + ((v ^ (q & 7)) << 4)),
+                        pool + max(slot, static_cast<int64_t>(0)) * kRow + (c0 + c) * 64 + v * 8,
                         slot >= 0 ? 16u : 0u);
           }
           asm volatile("cp.async.commit_group;" ::: "memory");
@@ -177,47 +186,48 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
       } else {
         const auto* pool = static_cast<const uint8_t*>(pages.pool);
         const int v = lane & 3;  // four lanes to a row's 64 codes
-        constexpr int kBatch = 4;  // chunks whose loads are in flight together
 #pragma unroll
-        for (int c0 = 0; c0 < C::kChunks; c0 += kBatch) {
-          uint4 raw[kBatch][4];
+        for (int c = 0; c < kAhead; ++c)
 #pragma unroll
-          for (int c = 0; c < kBatch; ++c)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int64_t slot = slots[k * 32 + rw * 8 + (lane >> 2)];
-              raw[c][k] = slot >= 0 ? __ldg(reinterpret_cast<const uint4*>(pool + slot * kRow + (c0 + c) * 64) + v)
-                                    : make_uint4(0u, 0u, 0u, 0u);
-            }
-#pragma unroll
-          for (int c = 0; c < kBatch; ++c)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int r = k * 32 + rw * 8 + (lane >> 2);
-              const uint32_t cc[4] = {raw[c][k].x, raw[c][k].y, raw[c][k].z, raw[c][k].w};
-              uint32_t y[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float2 x = lat::e4m3_values(cc[e >> 1] >> (16 * (e & 1)) & 0xFFFFu);
-                y[e] = pack_bf16x2(x.x, x.y);  // exact
-              }
-              uint8_t* at = a_smem + (c0 + c) * kUnit + r * 128;
-              *reinterpret_cast<uint4*>(at + (((2 * v) ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-              *reinterpret_cast<uint4*>(at + (((2 * v + 1) ^ (r & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
-            }
-        }
+          for (int k = 0; k < 4; ++k) {
+            const int64_t slot = slots[k * 32 + rw * 8 + (lane >> 2)];
+            raw[c][k] = slot >= 0 ? __ldg(reinterpret_cast<const uint4*>(pool + slot * kRow + (c0 + c) * 64) + v)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+          }
       }
-      if (n == 0 && first_sub != 0) return;
+    };
+    auto convert = [&]() {  // FP8: the codes in registers, as bf16 (exact), to shared memory
+      const int v = lane & 3;
+#pragma unroll
+      for (int c = 0; c < kAhead; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int q = k * 32 + rw * 8 + (lane >> 2);
+          const uint32_t cc[4] = {raw[c][k].x, raw[c][k].y, raw[c][k].z, raw[c][k].w};
+          uint32_t y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 x = lat::e4m3_values(cc[e >> 1] >> (16 * (e & 1)) & 0xFFFFu);
+            y[e] = pack_bf16x2(x.x, x.y);
+          }
+          uint8_t* at = a_smem + c * kUnit + q * 128;
+          *reinterpret_cast<uint4*>(at + (((2 * v) ^ (q & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(at + (((2 * v + 1) ^ (q & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+    };
+    // the rotary part of tile n
+    auto rotary = [&](int n) {
+      const int64_t row0 = (static_cast<int64_t>(first_tile + n) * kCluster + rank) * kTile;
       for (int i = t; i < kTile * 8; i += kRowThreads) {
-        const int r = i >> 3, v = i & 7;
-        const int64_t row = row0 + r;
+        const int q = i >> 3, v = i & 7;
+        const int64_t row = row0 + q;
         if (row >= total) break;
-        const int64_t slot = slots[r];
+        const int64_t slot = ms->slot[n & 1][q];
         uint4 y = make_uint4(0u, 0u, 0u, 0u);
         if (slot >= 0) {
           if (FP8) {
             const uint2 c = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pages.pool) + slot * kRow + LAT) + v);
-            const float s = ms->scale[buf][r];
+            const float s = ms->scale[n & 1][q];
             const uint32_t cc[2] = {c.x, c.y};
             float f[8];
 #pragma unroll
@@ -234,28 +244,42 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
         reinterpret_cast<uint4*>(k_rope)[row * 8 + v] = y;
       }
     };
-    // this warp's lanes of tensor memory are the rows 32 (warp mod 4) + lane
-    const int r = (warp & 3) * 32 + lane;
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    fetch(0);
+    locate(0);
+    start(ms->slot[0], 0);
+    bool over = false;  // the same in all four warps
     for (int n = 0; n < n_tiles; ++n) {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      // (all copies have landed; a warp that gives up takes the others along)
-      if (lat::bar_any(1, kRowThreads, !ok || *abort_flag != 0)) {
-        ok = false;
-        break;
-      }
 #pragma unroll
       for (int c = 0; c < C::kChunks; ++c) {
+        if (c % kAhead == 0) {
+          if (c > 0) {
+            named_bar_sync(1, kRowThreads);  // the group before has been read
+            if (!FP8) start(ms->slot[n & 1], c);
+          }
+          if (FP8) {
+            convert();
+            if (c + kAhead < C::kChunks) start(ms->slot[n & 1], c + kAhead);
+          }
+        }
+        if (!FP8) {
+          if (c % kAhead == 0) asm volatile("cp.async.wait_group 3;" ::: "memory");
+          if (c % kAhead == 1) asm volatile("cp.async.wait_group 2;" ::: "memory");
+          if (c % kAhead == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+          if (c % kAhead == 3) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        // everybody's part of the chunk is there (a warp that gives up takes the
+        // others along)
+        over = lat::bar_any(1, kRowThreads, !ok || *abort_flag != 0);
+        if (over) break;
         uint32_t y[32];
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
-          const uint4 x = *reinterpret_cast<const uint4*>(a_smem + c * kUnit + r * 128 + ((v ^ (r & 7)) << 4));
+          const uint4 x = *reinterpret_cast<const uint4*>(a_smem + c % kAhead * kUnit + r * 128 +
+                                                          ((v ^ (r & 7)) << 4));
           y[4 * v] = x.x, y[4 * v + 1] = x.y, y[4 * v + 2] = x.z, y[4 * v + 3] = x.w;
         }
         if (n > 0) ok = ok && mbar_wait(&ms->a_empty[c], (n - 1) & 1);
-        tc::fence_after();
         __syncwarp();
+        tc::fence_after();
         tc::st16(tmem + lanes + c * 32, *reinterpret_cast<uint32_t(*)[16]>(&y[0]));
         tc::st16(tmem + lanes + c * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(&y[16]));
         tc::wait_st();
@@ -263,11 +287,16 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms->a_full[c]);
       }
-      named_bar_sync(1, kRowThreads);  // the rows have been read: the next may come
-      if (n + 1 < n_tiles) fetch(n + 1);
+      // the rows have been read: the next may come
+      if (over || (over = lat::bar_any(1, kRowThreads, !ok))) break;
+      if (n + 1 < n_tiles) {
+        locate(n + 1);
+        start(ms->slot[(n + 1) & 1], 0);
+      }
+      if (n > 0 || first_sub == 0) rotary(n);  // by the CTA that has the tile's first unit
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (!ok && t == 0) {
+    if (over && lane == 0) {
       *abort_flag = 1;
       flag_error(err, PSW_DEVERR_PIPELINE);
     }
