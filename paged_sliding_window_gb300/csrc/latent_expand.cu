@@ -332,25 +332,35 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
     constexpr uint32_t id = tc::idesc_bf16_f32(kTile, kTile, 0, 0);
     constexpr uint32_t kStep = kUnit >> 4;
     const uint64_t w_desc = tc::smem_desc(smem_u32(w_ring), 16, 1024, tc::kSwizzle128B);
-    int sub = first_sub, n = 0, box = 0;
+    int sub = first_sub, n = 0, s = 0;
+    uint32_t phase = 0;
+    bool there = false;  // box s has been seen to have landed
     for (int u = 0; ok && u < count; ++u) {
       const bool last = u == count - 1 || sub == per_tile - 1;  // of this tile here
       const bool begins = u == 0 || sub == 0;
       const int acc = u % kAcc;
       ok = mbar_wait(&ms->d_empty[acc], (u / kAcc & 1u) ^ 1u);
+      tc::fence_after();
 #pragma unroll
-      for (int c = 0; c < C::kChunks; ++c, ++box) {
-        const int s = box % C::kRing;
-        if (begins) ok = ok && mbar_wait(&ms->a_full[c], n & 1);
-        ok = ok && mbar_wait(&ms->w_full[s], box / C::kRing & 1);
-        tc::fence_after();
+      for (int c = 0; c < C::kChunks; ++c) {
+        if (begins) {
+          ok = ok && mbar_wait(&ms->a_full[c], n & 1);
+          tc::fence_after();
+        }
+        if (!there) ok = ok && mbar_wait(&ms->w_full[s], phase);
         const uint64_t wd = w_desc + s * kStep;
+        uint64_t* empty = &ms->w_empty[s];
+        // a box is 256 cycles of the tensor core and as much of this warp's time:
+        // whether the next has landed is asked while the products are issued
+        s = s + 1 == C::kRing ? 0 : s + 1;
+        phase ^= s == 0 ? 1u : 0u;
+        there = mbar_test(&ms->w_full[s], phase);
         if (ok && one) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             tc::mma_ts(tmem + C::kTmemD + acc * kTile, tmem + c * 32 + k * 8, wd + k * 2, id,
                        (c > 0 || k > 0) ? 1u : 0u);
-          lat::commit_multicast(&ms->w_empty[s], kBoth);
+          lat::commit_multicast(empty, kBoth);
           if (last) tc::commit(&ms->a_empty[c]);
         }
       }
