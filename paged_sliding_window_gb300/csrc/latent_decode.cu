@@ -101,7 +101,7 @@ struct Cfg {
 struct Misc {
   uint64_t full[32], empty[32];
   uint64_t q_full, q_free, s_full[2], p_full[3], pv_done[3], o_full, o_free, drained;
-  int32_t unit0, page0;      // this CTA's first unit and the page within it
+  int32_t b0, chunk0, page0; // this CTA's first unit and the page within it
   uint32_t tmem;
   int32_t abort;
   int64_t total, p0, p1;     // pages of all units; this CTA's piece of them
@@ -147,20 +147,22 @@ struct Part {  // what a unit's pieces left behind, per unit: pieces [x, y], x <
 struct Walk {
   const int32_t* seq_lens;
   int window, max_blocks, chunks, n_seqs;
-  int64_t left;   // pages of this CTA not yet given out
-  int unit, page; // next unit and the page within it
+  int64_t left;          // pages of this CTA not yet given out
+  int next_b, next_chunk, page;  // unit of the next page, and the page within it
   int b, chunk;
   Span span;
   int seg_first, seg_count;  // pages of the segment, relative to the span's first
   __device__ __forceinline__ bool next() {
     if (left <= 0) return false;
-    for (;; ++unit, page = 0) {
-      b = unit / chunks;
-      if (b >= n_seqs) return false;  // not reached: the list holds `left` more pages
-      chunk = unit - b * chunks;
-      span = span_of(__ldg(seq_lens + b), window, max_blocks);
+    for (;;) {
+      if (next_b >= n_seqs) return false;  // not reached: the list holds `left` more pages
+      span = span_of(__ldg(seq_lens + next_b), window, max_blocks);
       if (page < span.count) break;
+      page = 0;
+      if (++next_chunk == chunks) next_chunk = 0, ++next_b;
     }
+    b = next_b;
+    chunk = next_chunk;
     seg_first = page;
     seg_count = static_cast<int>(min(static_cast<int64_t>(span.count - page), left));
     left -= seg_count;
@@ -277,7 +279,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         if (p0 < end) {
           int c = 0;
           for (; p0 >= at + n; at += n) ++c;
-          ms->unit0 = b * chunks + c;
+          ms->b0 = b;
+          ms->chunk0 = c;
           ms->page0 = static_cast<int>(p0 - at);
           break;
         }
@@ -292,7 +295,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     }
     __threadfence_block();
     __syncwarp();
-    asm volatile("bar.arrive 2, %0;" ::"r"(C::kThreads) : "memory");  // goes straight on
+    // goes straight on; the others come to these barriers when they are ready
+    asm volatile("bar.arrive 2, %0;" ::"r"(C::kThreads - kSoftThreads) : "memory");
+    asm volatile("bar.arrive 4, %0;" ::"r"(kSoftThreads + 32) : "memory");
   } else {
     if (warp == kScoreWarp) {
       tc::alloc(&ms->tmem, 512);
@@ -302,23 +307,31 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       prefetch_tensormap(&pool_map);
       prefetch_tensormap(&q_map);
     }
-    wait_for_inputs();
-    tc::fence_before();
-    named_bar_sync(2, C::kThreads);
-    tc::fence_after();
+    if (warp <= kScoreWarp) {
+      tc::fence_before();
+      named_bar_sync(3, 32 * (kScoreWarp + 1));
+      tc::fence_after();
+    }
+    if (warp >= kScoreWarp) {  // (the softmax warps come to this later)
+      wait_for_inputs();
+      named_bar_sync(2, C::kThreads - kSoftThreads);
+    }
   }
-  const int64_t p1 = ms->p1;
-  const uint32_t tmem = warp == kLoadWarp ? 0u : ms->tmem;  // (may not be there yet)
+  const uint32_t tmem = warp <= kScoreWarp || warp == kValueWarp ? ms->tmem : 0u;
   volatile int32_t* abort_flag = &ms->abort;
   Walk walk;
-  walk.seq_lens = seq_lens;
-  walk.window = window;
-  walk.max_blocks = pages.max_blocks;
-  walk.chunks = chunks;
-  walk.n_seqs = n_seqs;
-  walk.left = p1 - ms->p0;
-  walk.unit = walk.left > 0 ? ms->unit0 : 0;
-  walk.page = walk.left > 0 ? ms->page0 : 0;
+  auto begin = [&]() {  // once the piece is known
+    walk.seq_lens = seq_lens;
+    walk.window = window;
+    walk.max_blocks = pages.max_blocks;
+    walk.chunks = chunks;
+    walk.n_seqs = n_seqs;
+    walk.left = ms->p1 - ms->p0;
+    walk.next_b = ms->b0;  // (anything, where there is no page)
+    walk.next_chunk = ms->chunk0;
+    walk.page = ms->page0;
+  };
+  if (warp >= kScoreWarp) begin();
   Ring rg;
   bool ok = true;
   const float mul = softcap > 0.f ? scale / softcap : scale * lat::kLog2e;  // (times cap2 later)
@@ -413,6 +426,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       flag_error(err, PSW_DEVERR_BLOCK_ID);
       return -1;
     };
+    constexpr int kGroup = 32 / kPages;  // tiles whose block ids the lanes hold
     // TMA boxes of 16 rows x 128 bytes, issued by one lane of the converged warp
     // (issued by a lane each, a box costs 90 cycles: longer than it takes to
     // arrive). FP8 rows are 4.5 or 2.5 lines long and half of them straddle the
@@ -422,12 +436,16 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     int tile = 0;
     while (ok && walk.next()) {
       const int n_tiles = walk.tiles();
-      int next_blk = block_id(lane & 3);
+      int ids = block_id(lane), next_ids = block_id(32 + lane);
       for (int t = 0; ok && t < n_tiles; ++t, ++tile) {
+        if (t > 0 && t % kGroup == 0) {
+          ids = next_ids;
+          next_ids = block_id((t / kGroup + 1) * 32 + lane);
+        }
         int blk[kPages];
 #pragma unroll
-        for (int pg = 0; pg < kPages; ++pg) blk[pg] = __shfl_sync(0xffffffffu, next_blk, pg);
-        if (t + 1 < n_tiles) next_blk = block_id((t + 1) * kPages + (lane & 3));
+        for (int pg = 0; pg < kPages; ++pg)
+          blk[pg] = __shfl_sync(0xffffffffu, ids, t % kGroup * kPages + pg);
 #pragma unroll
         for (int u = 0; u <= C::kBlocks; ++u) {  // rope unit, then the blocks
           const int n = u == 0 ? 1 : C::kSlotsPerBlock;
@@ -568,23 +586,27 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     // ------------------------------------------------------------ softmax, epilogue
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const float cap2 = softcap * lat::kLog2e;
-    int seg = 0, tile = 0;
-    bool more = walk.next();
     // this thread's keys of a tile, rows 16 warp + lane / 4 and 8 further; its
     // heads 8 g + 2 (lane mod 4) + {0, 1}, number 2 g + {0, 1} here
     const int r0 = warp * 16 + (lane >> 2), quad = lane & 3;
+    // Before anything else a CTA goes through the tile's code once without
+    // effect (segment -1): fetching that code costs 1200 (bf16) to 5000 (FP8)
+    // cycles, several times that behind the first loads, now none of them of the
+    // first tile's.
+    int seg = -1, tile = 0;
+    bool more = true;
+    Walk w = {};
     for (; ok && more; ++seg) {
-      const Walk w = walk;
-      more = walk.next();
+      if (seg >= 0) {
+        w = walk;
+        more = walk.next();
+      }
       const int h0 = w.chunk * NH, nh = min(NH, heads - h0), n_tiles = w.tiles();
       constexpr int HN = C::kHeads;
       float m[HN], l[HN], vref = 0.f;
 #pragma unroll
       for (int i = 0; i < HN; ++i) m[i] = 0.f, l[i] = 0.f;
-      // Before its first tile a CTA goes through the tile's code once without
-      // effect: fetching that code costs 1200 (bf16) to 5000 (FP8) cycles, now
-      // while the first loads are on their way.
-      for (int t = seg == 0 ? -1 : 0; t < n_tiles; ++t) {
+      for (int t = seg < 0 ? -1 : 0; t < n_tiles; ++t) {
         const bool live = t >= 0;
         const bool in_seg = live && t * kPages + warp < w.seg_count;  // a page per warp
         const int key = (w.span.first + w.seg_first + t * kPages + warp) * kBlockSize + (lane >> 2);
@@ -770,6 +792,13 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         }
       }
       if (!ok) break;
+      if (seg < 0) {
+        wait_for_inputs();
+        named_bar_sync(4, kSoftThreads + 32);
+        begin();
+        more = walk.next();
+        continue;
+      }
       // ---- the segment's end
 #pragma unroll
       for (int i = 0; i < C::kHeads; ++i) {
@@ -801,7 +830,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       }
       if (tid == 0 && w.seg_first == 0) {
         // first page of the unit: note which pieces share it
-        const int64_t end = p1 - w.left - w.seg_count + w.span.count;  // list end of the unit
+        const int64_t end = ms->p1 - w.left - w.seg_count + w.span.count;  // list end of the unit
         const int last = static_cast<int>((end * ms->pieces - 1) / ms->total);
         parts[w.b * chunks + w.chunk] = whole ? Part{-1, -1} : Part{static_cast<int32_t>(blockIdx.x), last};
       }
