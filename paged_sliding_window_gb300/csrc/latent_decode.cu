@@ -88,6 +88,11 @@ struct Cfg {
   static_assert(!FP8 || (kScales + kScaleTiles * kScaleBytes <= kMisc &&
                          kSlots / kTileSlots + 2 <= kScaleTiles),
                 "no tile's scales are overwritten while it is in the ring");
+  // Pages that a unit counts for beyond its own: a piece that goes from one unit to
+  // the next writes out, loads queries and fills the pipeline again meanwhile
+  // (0, 4, 8, 12, 16, 24: 42.5, 41.0, 40.1, 41.0, 41.0, 42.4 us for 64 sequences of
+  // bf16 pages; 34.2, 31.8, 31.4, 30.8, 31.4, 33.0 us of FP8 pages).
+  static constexpr int kBegin = FP8 ? 12 : 8;
   static constexpr int kHeads = NH / 4;                // heads of a softmax thread
   static_assert(kSlots <= 32, "phase bits");
   // log2 distance by which a score may exceed the maximum in use, and the
@@ -101,10 +106,10 @@ struct Cfg {
 struct Misc {
   uint64_t full[32], empty[32];
   uint64_t q_full, q_free, s_full[2], p_full[3], pv_done[3], o_full, o_free, drained;
-  int32_t b0, chunk0, page0; // this CTA's first unit and the page within it
+  int32_t b0, chunk0, at0;   // this CTA's first unit and the place within it
   uint32_t tmem;
   int32_t abort;
-  int64_t total, p0, p1;     // pages of all units; this CTA's piece of them
+  int64_t total, p0, p1;     // what all units count for; this CTA's piece of it
   int32_t pieces;
   float red[4][kMaxHeads];
   float vred[4];
@@ -121,6 +126,8 @@ __device__ const float4 g_zero_scales[kBlockSize / 4] = {};
 struct Span {
   int len, lo;          // keys [lo, len)
   int first, count;     // pages
+  // what a unit of these pages counts for in the list that is cut evenly
+  __device__ __forceinline__ int cost(int begin) const { return count > 0 ? begin + count : 0; }
 };
 __device__ __forceinline__ Span span_of(int raw, int window, int max_blocks) {
   Span s;
@@ -147,27 +154,31 @@ struct Part {  // what a unit's pieces left behind, per unit: pieces [x, y], x <
 struct Walk {
   const int32_t* seq_lens;
   int window, max_blocks, chunks, n_seqs;
-  int64_t left;          // pages of this CTA not yet given out
-  int next_b, next_chunk, page;  // unit of the next page, and the page within it
+  int64_t left;          // of this CTA's piece (pages, `begin` more for each unit)
+  int begin;
+  int next_b, next_chunk, at;  // unit that comes next, and the place within what it counts for
   int b, chunk;
   Span span;
   int seg_first, seg_count;  // pages of the segment, relative to the span's first
   __device__ __forceinline__ bool next() {
-    if (left <= 0) return false;
-    for (;;) {
-      if (next_b >= n_seqs) return false;  // not reached: the list holds `left` more pages
+    while (left > 0 && next_b < n_seqs) {
       span = span_of(__ldg(seq_lens + next_b), window, max_blocks);
-      if (page < span.count) break;
-      page = 0;
-      if (++next_chunk == chunks) next_chunk = 0, ++next_b;
+      b = next_b;
+      chunk = next_chunk;
+      const int cost = span.cost(begin);
+      const int take = static_cast<int>(min(static_cast<int64_t>(cost - at), left));
+      // of [at, at + take) the first `begin` are no pages
+      seg_first = max(at - begin, 0);
+      seg_count = max(at + take - begin, 0) - seg_first;
+      left -= take;
+      at += take;
+      if (at == cost) {
+        at = 0;
+        if (++next_chunk == chunks) next_chunk = 0, ++next_b;
+      }
+      if (seg_count > 0) return true;
     }
-    b = next_b;
-    chunk = next_chunk;
-    seg_first = page;
-    seg_count = static_cast<int>(min(static_cast<int64_t>(span.count - page), left));
-    left -= seg_count;
-    page += seg_count;
-    return true;
+    return false;
   }
   __device__ __forceinline__ bool whole() const { return seg_first == 0 && seg_count == span.count; }
   __device__ __forceinline__ int tiles() const { return (seg_count + kPages - 1) / kPages; }
@@ -252,7 +263,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll 4
     for (int b = b0; b < b1; ++b) {
       const int raw = __ldg(seq_lens + b);
-      mine += static_cast<int64_t>(span_of(raw, window, pages.max_blocks).count) * chunks;
+      mine += static_cast<int64_t>(span_of(raw, window, pages.max_blocks).cost(C::kBegin)) * chunks;
       if (blockIdx.x == 0) {
         if (raw < 0) flag_error(err, PSW_DEVERR_LENGTH);
         if (raw > static_cast<int64_t>(pages.max_blocks) * kBlockSize)
@@ -274,14 +285,14 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     if (p0 < p1 && p0 >= before && p0 < before + mine) {
       int64_t at = before;
       for (int b = b0; b < b1; ++b) {
-        const int n = span_of(__ldg(seq_lens + b), window, pages.max_blocks).count;
+        const int n = span_of(__ldg(seq_lens + b), window, pages.max_blocks).cost(C::kBegin);
         const int64_t end = at + static_cast<int64_t>(n) * chunks;
         if (p0 < end) {
           int c = 0;
           for (; p0 >= at + n; at += n) ++c;
           ms->b0 = b;
           ms->chunk0 = c;
-          ms->page0 = static_cast<int>(p0 - at);
+          ms->at0 = static_cast<int>(p0 - at);
           break;
         }
         at = end;
@@ -329,7 +340,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     walk.left = ms->p1 - ms->p0;
     walk.next_b = ms->b0;  // (anything, where there is no page)
     walk.next_chunk = ms->chunk0;
-    walk.page = ms->page0;
+    walk.at = ms->at0;
+    walk.begin = C::kBegin;
   };
   if (warp >= kScoreWarp) begin();
   Ring rg;
@@ -829,7 +841,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         }
       }
       if (tid == 0 && w.seg_first == 0) {
-        // first page of the unit: note which pieces share it
+        // first page of the unit: note which pieces share it (the segment ends
+        // where w.left is left of this piece)
         const int64_t end = ms->p1 - w.left - w.seg_count + w.span.count;  // list end of the unit
         const int last = static_cast<int>((end * ms->pieces - 1) / ms->total);
         parts[w.b * chunks + w.chunk] = whole ? Part{-1, -1} : Part{static_cast<int32_t>(blockIdx.x), last};
