@@ -454,6 +454,8 @@ PSW_API int latent_norm_rope_cache_write_fp8(
  *             psw_latent_workspace_bytes(layer, n_seqs)
  * A page whose block id is outside the pool reads as zero rows and is flagged
  * (PSW_DEVERR_BLOCK_ID); a length beyond the table row is clamped and flagged.
+ * n_seqs * (max_blocks_per_seq + 12) * ceil(n_heads / 16) must stay below 2^31
+ * (PSW_ECAPACITY).
  */
 PSW_API int attn_decode_latent(const psw_latent_t *layer, const void *q, const void *pool,
                                const psw_pages_t *pages, const int32_t *seq_lens, int32_t n_seqs,

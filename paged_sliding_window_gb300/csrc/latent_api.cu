@@ -102,6 +102,9 @@ int decode(const psw_latent_t* layer, const void* q, const void* pool, const flo
   if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
       !aligned(row_scale, 16) || !aligned(ws, 16))
     return PSW_EALIGN;
+  if (static_cast<int64_t>(n_seqs) * (pages->max_blocks_per_seq + 12) * ((L.n_heads + 15) / 16) >
+      INT32_MAX)
+    return PSW_ECAPACITY;
   if (n_seqs == 0) return PSW_OK;
   if (ws == nullptr || ws_bytes < latent_decode_workspace(L, n_seqs)) return PSW_EWORKSPACE;
   DeviceInfo info;

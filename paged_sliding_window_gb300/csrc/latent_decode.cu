@@ -103,14 +103,24 @@ struct Cfg {
   static constexpr float kPUnit = FP8 ? 16.f : 1.f;
 };
 
+// The list, cut into n pieces: of q + 1 for the first r, of q for the others.
+struct Cut {
+  int q, r;
+  __device__ __forceinline__ int first(int i) const { return q * i + min(i, r); }
+  __device__ __forceinline__ int piece(int x) const {  // that holds place x
+    const int wide = (q + 1) * r;
+    return x < wide ? x / (q + 1) : r + (x - wide) / q;
+  }
+};
+
 struct Misc {
   uint64_t full[32], empty[32];
   uint64_t q_full, q_free, s_full[2], p_full[3], pv_done[3], o_full, o_free, drained;
   int32_t b0, chunk0, at0;   // this CTA's first unit and the place within it
   uint32_t tmem;
   int32_t abort;
-  int64_t total, p0, p1;     // what all units count for; this CTA's piece of it
-  int32_t pieces;
+  Cut cut;                   // of what all units count for
+  int32_t p0, p1;            // this CTA's piece of it
   float red[4][kMaxHeads];
   float vred[4];
   float qs[3][kMaxHeads];    // FP8, segments in turn: scale * log2(e) * a unit of q's codes
@@ -139,13 +149,6 @@ __device__ __forceinline__ Span span_of(int raw, int window, int max_blocks) {
   return s;
 }
 
-// First page of piece i of n.
-__device__ __forceinline__ int64_t share_of(int64_t total, int i, int n) {
-  if (total < (1 << 23))  // times up to kMaxCtas fits 32 bits
-    return static_cast<uint32_t>(total) * static_cast<uint32_t>(i) / static_cast<uint32_t>(n);
-  return total * i / n;
-}
-
 struct Part {  // what a unit's pieces left behind, per unit: pieces [x, y], x < 0: none
   int32_t x, y;
 };
@@ -154,7 +157,7 @@ struct Part {  // what a unit's pieces left behind, per unit: pieces [x, y], x <
 struct Walk {
   const int32_t* seq_lens;
   int window, max_blocks, chunks, n_seqs;
-  int64_t left;          // of this CTA's piece (pages, `begin` more for each unit)
+  int left;              // of this CTA's piece (pages, `begin` more for each unit)
   int begin;
   int next_b, next_chunk, at;  // unit that comes next, and the place within what it counts for
   int b, chunk;
@@ -166,7 +169,7 @@ struct Walk {
       b = next_b;
       chunk = next_chunk;
       const int cost = span.cost(begin);
-      const int take = static_cast<int>(min(static_cast<int64_t>(cost - at), left));
+      const int take = min(cost - at, left);
       // of [at, at + take) the first `begin` are no pages
       seg_first = max(at - begin, 0);
       seg_count = max(at + take - begin, 0) - seg_first;
@@ -259,48 +262,45 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     wait_for_inputs();
     const int per = (n_seqs + 31) / 32;
     const int b0 = min(n_seqs, lane * per), b1 = min(n_seqs, b0 + per);
-    int64_t mine = 0;
+    int mine = 0;  // (the host has seen to it that 32 bits hold the sum)
 #pragma unroll 4
     for (int b = b0; b < b1; ++b) {
       const int raw = __ldg(seq_lens + b);
-      mine += static_cast<int64_t>(span_of(raw, window, pages.max_blocks).cost(C::kBegin)) * chunks;
+      mine += span_of(raw, window, pages.max_blocks).cost(C::kBegin) * chunks;
       if (blockIdx.x == 0) {
         if (raw < 0) flag_error(err, PSW_DEVERR_LENGTH);
         if (raw > static_cast<int64_t>(pages.max_blocks) * kBlockSize)
           flag_error(err, PSW_DEVERR_CAPACITY);
       }
     }
-    int64_t incl = mine;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    const int64_t total = __shfl_sync(0xffffffffu, incl, 31), before = incl - mine;
-    const int64_t most = (total + kMinPages - 1) / kMinPages;
-    const int pieces = most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
+    const int total = __shfl_sync(0xffffffffu, incl, 31);
+    const int pieces = max(1, min(static_cast<int>(gridDim.x), (total + kMinPages - 1) / kMinPages));
+    const Cut cut{total / pieces, total % pieces};
     const bool work = static_cast<int>(blockIdx.x) < pieces;
-    const int64_t p0 = work ? share_of(total, blockIdx.x, pieces) : 0;
-    const int64_t p1 = work ? share_of(total, blockIdx.x + 1, pieces) : 0;
-    if (p0 < p1 && p0 >= before && p0 < before + mine) {
-      int64_t at = before;
+    const int p0 = work ? cut.first(blockIdx.x) : 0, p1 = work ? cut.first(blockIdx.x + 1) : 0;
+    if (p0 < p1 && p0 >= incl - mine && p0 < incl) {
+      int at = incl - mine;
       for (int b = b0; b < b1; ++b) {
         const int n = span_of(__ldg(seq_lens + b), window, pages.max_blocks).cost(C::kBegin);
-        const int64_t end = at + static_cast<int64_t>(n) * chunks;
-        if (p0 < end) {
+        if (p0 < at + n * chunks) {
           int c = 0;
           for (; p0 >= at + n; at += n) ++c;
           ms->b0 = b;
           ms->chunk0 = c;
-          ms->at0 = static_cast<int>(p0 - at);
+          ms->at0 = p0 - at;
           break;
         }
-        at = end;
+        at += n * chunks;
       }
     }
     if (lane == 0) {
-      ms->total = total;
-      ms->pieces = pieces;
+      ms->cut = cut;
       ms->p0 = p0;
       ms->p1 = p1;
     }
@@ -843,8 +843,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       if (tid == 0 && w.seg_first == 0) {
         // first page of the unit: note which pieces share it (the segment ends
         // where w.left is left of this piece)
-        const int64_t end = ms->p1 - w.left - w.seg_count + w.span.count;  // list end of the unit
-        const int last = static_cast<int>((end * ms->pieces - 1) / ms->total);
+        const int end = ms->p1 - w.left - w.seg_count + w.span.count;  // list end of the unit
+        const int last = ms->cut.piece(end - 1);
         parts[w.b * chunks + w.chunk] = whole ? Part{-1, -1} : Part{static_cast<int32_t>(blockIdx.x), last};
       }
       named_bar_sync(1, kSoftThreads);

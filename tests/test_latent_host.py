@@ -97,6 +97,7 @@ def test_layer_refusals(lib, name, kw, code):
     (DECODES, dict(q=None), "PSW_ENULL"), (DECODES, dict(seq=None), "PSW_ENULL"),
     (DECODES, dict(out=None), "PSW_ENULL"), (DECODES, dict(out=FAKE + 8), "PSW_EALIGN"),
     (DECODES, dict(ws=FAKE + 8), "PSW_EALIGN"), (DECODES, dict(lse=FAKE + 2), "PSW_EALIGN"),
+    (DECODES, dict(n_seqs=1 << 20, pages=_pages(mbps=1 << 12)), "PSW_ECAPACITY"),
     (DECODES, dict(n_seqs=4, ws=None), "PSW_EWORKSPACE"),
     (DECODES, dict(n_seqs=4, ws_bytes=100), "PSW_EWORKSPACE"),
     (EXPANDS, dict(w=None), "PSW_ENULL"), (EXPANDS, dict(kv=None), "PSW_ENULL"),
