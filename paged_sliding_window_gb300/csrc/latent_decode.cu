@@ -30,8 +30,8 @@
 // the second product of this one (two S buffers, a warp each), MMAs issued from converged code
 // (40 cycles each, what reading their operands takes, against 80 to 260), and
 // blocks released one by one. The rope slot of a tile is done with after S, and
-// then holds P. Warp 4 loads, warp 5 issues the MMAs, warps 0-3 do the softmax
-// (a thread has two keys and a quarter of the heads) and the epilogue (a thread
+// then holds P. Warp 4 loads, warp 5 issues the MMAs, four warps for
+// every 16 heads do the softmax (a thread has two keys and four heads) and the epilogue (a thread
 // per dim). The maximum that P is relative to is taken from a segment's first
 // tile and moved (O rescaled) only when a score exceeds it by 2^64 (bf16, whose
 // P has the range) or 2^4 (E4M3), so a tile costs its threads one barrier.
@@ -45,10 +45,6 @@ namespace ldec {
 constexpr int kTile = 64;                       // keys of a tile
 constexpr int kPages = kTile / kBlockSize;      // pages of a tile
 constexpr int kSlotBytes = kTile * 128;
-constexpr int kSoftThreads = 128;               // warps 0-3
-constexpr int kScoreWarp = 4, kValueWarp = 5;   // MMAs of S, of O
-constexpr int kLoadWarp = 6;                    // pages
-constexpr int kQueryWarp = 7;                   // queries: this warp, and 8-10 with FP8 pages
 constexpr int kMaxCtas = 160;                   // pieces of the page list
 constexpr int kMinPages = 4;                    // pages a piece has at least
 constexpr int kMaxHeads = 32;                   // heads of a chunk
@@ -73,6 +69,12 @@ struct Cfg {
   static constexpr int kRopeSteps = FP8 ? 2 : 4;       // 32-byte MMA steps of the rope chunk
   static constexpr int kPSteps = FP8 ? 2 : 4;          // MMA steps along the keys
   static constexpr int kPStepBytes = kTile / kPSteps * 128;
+  // Roles by warp: softmax, four warps for every 16 heads; MMAs of S; MMAs of O;
+  // pages; queries.
+  static constexpr int kGroups = NH / 16;
+  static constexpr int kSoftThreads = 128 * kGroups;
+  static constexpr int kScoreWarp = 4 * kGroups, kValueWarp = kScoreWarp + 1;
+  static constexpr int kLoadWarp = kScoreWarp + 2, kQueryWarp = kScoreWarp + 3;
   static constexpr int kQueryWarps = FP8 ? 4 : 1;
   static constexpr int kThreads = 32 * (kQueryWarp + kQueryWarps);
   static constexpr int kMisc = FP8 ? 6144 : 2048;
@@ -93,7 +95,7 @@ struct Cfg {
   // (0, 4, 8, 12, 16, 24: 42.5, 41.0, 40.1, 41.0, 41.0, 42.4 us for 64 sequences of
   // bf16 pages; 34.2, 31.8, 31.4, 30.8, 31.4, 33.0 us of FP8 pages).
   static constexpr int kBegin = FP8 ? 12 : 8;
-  static constexpr int kHeads = NH / 4;                // heads of a softmax thread
+  static constexpr int kHeads = 4;                     // heads of a softmax thread
   static_assert(kSlots <= 32, "phase bits");
   // log2 distance by which a score may exceed the maximum in use, and the
   // largest row scale relative to the one in use; E4M3 P = 16 p v then stays
@@ -229,6 +231,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                      float* __restrict__ part_o, int32_t* err) {
   using C = Cfg<LAT, NH, FP8>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kSoftThreads = C::kSoftThreads, kScoreWarp = C::kScoreWarp;
+  constexpr int kValueWarp = C::kValueWarp, kLoadWarp = C::kLoadWarp, kQueryWarp = C::kQueryWarp;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* q_smem = smem;
@@ -247,13 +251,13 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     mbar_init(&ms->empty[lane], 1);
     if (lane < 3) {
       if (lane < 2) mbar_init(&ms->s_full[lane], 1);
-      mbar_init(&ms->p_full[lane], 4);
+      mbar_init(&ms->p_full[lane], kSoftThreads / 32);
       mbar_init(&ms->pv_done[lane], 1);
     } else if (lane == 3) {
       mbar_init(&ms->q_full, C::kQueryWarps);
       mbar_init(&ms->q_free, 1);
       mbar_init(&ms->o_full, 1);
-      mbar_init(&ms->o_free, 4);
+      mbar_init(&ms->o_free, kSoftThreads / 32);
       mbar_init(&ms->drained, 2);
       ms->abort = 0;
     }
@@ -320,7 +324,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     }
     if (warp <= kScoreWarp) {
       tc::fence_before();
-      named_bar_sync(3, 32 * (kScoreWarp + 1));
+      named_bar_sync(3, kSoftThreads + 32);
       tc::fence_after();
     }
     if (warp >= kScoreWarp) {  // (the softmax warps come to this later)
@@ -596,11 +600,13 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax, epilogue
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const int row_warp = warp & 3, head0 = (warp >> 2) * 16;  // which rows, which heads
+    const uint32_t lanes = static_cast<uint32_t>(row_warp * 32) << 16;
     const float cap2 = softcap * lat::kLog2e;
-    // this thread's keys of a tile, rows 16 warp + lane / 4 and 8 further; its
-    // heads 8 g + 2 (lane mod 4) + {0, 1}, number 2 g + {0, 1} here
-    const int r0 = warp * 16 + (lane >> 2), quad = lane & 3;
+    // this thread's keys of a tile, rows 16 row_warp + lane / 4 and 8 further; its
+    // heads head0 + 8 g + 2 (lane mod 4) + {0, 1}, number 2 g + {0, 1} here
+    const int r0 = row_warp * 16 + (lane >> 2), quad = lane & 3;
+    auto head_of = [&](int i) { return head0 + 8 * (i >> 1) + 2 * quad + (i & 1); };
     // Before anything else a CTA goes through the tile's code once without
     // effect (segment -1): fetching that code costs 1200 (bf16) to 5000 (FP8)
     // cycles, several times that behind the first loads, now none of them of the
@@ -620,8 +626,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       for (int i = 0; i < HN; ++i) m[i] = 0.f, l[i] = 0.f;
       for (int t = seg < 0 ? -1 : 0; t < n_tiles; ++t) {
         const bool live = t >= 0;
-        const bool in_seg = live && t * kPages + warp < w.seg_count;  // a page per warp
-        const int key = (w.span.first + w.seg_first + t * kPages + warp) * kBlockSize + (lane >> 2);
+        const bool in_seg = live && t * kPages + row_warp < w.seg_count;  // a page per warp
+        const int key = (w.span.first + w.seg_first + t * kPages + row_warp) * kBlockSize + (lane >> 2);
         int slot[1 + C::kBlocks] = {};
         uint32_t parity[1 + C::kBlocks] = {};
         if (live) {
@@ -645,18 +651,15 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         }
         float z[2][HN];
         {
-          uint32_t v[C::kQParts][NH / 2];
+          uint32_t v[C::kQParts][8];
 #pragma unroll
-          for (int p = 0; p < C::kQParts; ++p) {
-            const uint32_t at = tmem + lanes + (tile & 1) * C::kQRows + p * NH;
-            if (NH == 16) lat::ld16x256_x2(at, *reinterpret_cast<uint32_t(*)[8]>(&v[p][0]));
-            else tc::ld16x256_x4(at, *reinterpret_cast<uint32_t(*)[16]>(&v[p][0]));
-          }
+          for (int p = 0; p < C::kQParts; ++p)
+            lat::ld16x256_x2(tmem + lanes + (tile & 1) * C::kQRows + p * NH + head0, v[p]);
           tc::wait_ld();
 #pragma unroll
           for (int i = 0; i < HN; ++i) {
             const int r = 4 * (i >> 1) + (i & 1);
-            const float qs = FP8 ? ms->qs[seg % 3][8 * (i >> 1) + 2 * quad + (i & 1)] : mul;
+            const float qs = FP8 ? ms->qs[(seg + 3) % 3][head_of(i)] : mul;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const float x = __uint_as_float(v[0][r + 2 * j]);
@@ -681,7 +684,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
           }
           // rows of a loaded page that hold no visible key must not enter the
           // second product (P is 0 there, but 0 times NaN is not)
-          if (in_seg && !seen[j]) {
+          if (in_seg && !seen[j] && head0 == 0) {
 #pragma unroll
             for (int u = 1; u <= C::kBlocks; ++u)
               for (int c = 0; c < C::kSlotsPerBlock; ++c) {
@@ -701,11 +704,11 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             float x = fmaxf(z[0][i], z[1][i]);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-            if (lane < 4) ms->red[warp][8 * (i >> 1) + 2 * quad + (i & 1)] = x;
+            if (lane < 4) ms->red[row_warp][head_of(i)] = x;
           }
           if (FP8) {
             const float x = lat::warp_max(fmaxf(vs[0], vs[1]));
-            if (lane == 0) ms->vred[warp] = x;
+            if (lane == 0 && head0 == 0) ms->vred[row_warp] = x;
           }
           // O is rescaled below: the products up to the tile before have ended
           if (t > 0 && ok) ok = mbar_wait(&ms->pv_done[(tile - 1) % 3], (tile - 1) / 3 & 1);
@@ -725,7 +728,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
           }
 #pragma unroll
           for (int i = 0; i < HN; ++i) {
-            const int h = 8 * (i >> 1) + 2 * quad + (i & 1);
+            const int h = head_of(i);
             const float x = fmaxf(fmaxf(ms->red[0][h], ms->red[1][h]), fmaxf(ms->red[2][h], ms->red[3][h]));
             float a = 1.f;
             if (t <= 0) {
@@ -736,12 +739,12 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
               l[i] *= a;
               m[i] = x;
             }
-            if (warp == 0 && lane < 4) ms->alpha[h] = a * vmul;
+            if (row_warp == 0 && lane < 4) ms->alpha[h] = a * vmul;
           }
           named_bar_sync(1, kSoftThreads);
           if (t > 0) {
 #pragma unroll 1
-            for (int blk = 0; blk < C::kBlocks; ++blk) {
+            for (int blk = warp >> 2; blk < C::kBlocks; blk += C::kGroups) {
 #pragma unroll
               for (int c = 0; c < C::kPCols / 16; ++c) {
                 uint32_t v[16];
@@ -766,7 +769,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
           uint8_t* prow = ring + slot[0] * kSlotBytes + r * 128;
           const float pv = FP8 ? vs[j] * (C::kPUnit / vref) : 1.f;
 #pragma unroll
-          for (int g = 0; g < NH / 8; ++g) {
+          for (int g = 0; g < 2; ++g) {
             float a = ex2_approx(z[j][2 * g] - m[2 * g]);
             float b = ex2_approx(z[j][2 * g + 1] - m[2 * g + 1]);
             l[2 * g] += a;
@@ -775,8 +778,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
               const uint32_t hi = pack_bf16x2(a, b);
               const float2 got = unpack_bf16x2(hi);
               if (!live) continue;
-              *reinterpret_cast<uint32_t*>(prow + ((g ^ sw) << 4) + quad * 4) = hi;
-              *reinterpret_cast<uint32_t*>(prow + (((g + NH / 8) ^ sw) << 4) + quad * 4) =
+              const int vec = (head0 >> 3) + g;
+              *reinterpret_cast<uint32_t*>(prow + ((vec ^ sw) << 4) + quad * 4) = hi;
+              *reinterpret_cast<uint32_t*>(prow + (((vec + NH / 8) ^ sw) << 4) + quad * 4) =
                   pack_bf16x2(a - got.x, b - got.y);
             } else {
               a *= pv;
@@ -784,7 +788,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
               for (int p = 0; p < 3; ++p) {
                 const uint32_t c = lat::e4m3_pair(a, b);
-                const int at = p * NH + g * 8 + quad * 2;
+                const int at = p * NH + head0 + g * 8 + quad * 2;
                 if (live)
                   *reinterpret_cast<uint16_t*>(prow + (((at >> 4) ^ sw) << 4) + (at & 15)) =
                       static_cast<uint16_t>(c);
@@ -817,9 +821,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         float x = l[i];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        const int h = 8 * (i >> 1) + 2 * quad + (i & 1);
-        if (lane < 4) ms->red[warp][h] = x;
-        if (warp == 0 && lane < 4) ms->alpha[h] = m[i];
+        const int h = head_of(i);
+        if (lane < 4) ms->red[row_warp][h] = x;
+        if (row_warp == 0 && lane < 4) ms->alpha[h] = m[i];
       }
       ok = mbar_wait(&ms->o_full, seg & 1);
       if (lat::bar_any(1, kSoftThreads, !ok)) {
@@ -850,8 +854,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       named_bar_sync(1, kSoftThreads);
       const float ov = FP8 ? vref / C::kPUnit : 1.f;
 #pragma unroll 1
-      for (int blk = 0; blk < C::kBlocks; ++blk) {
-        const int d = blk * 128 + tid;
+      for (int blk = warp >> 2; blk < C::kBlocks; blk += C::kGroups) {
+        const int d = blk * 128 + row_warp * 32 + lane;
         float o[NH];
 #pragma unroll
         for (int p = 0; p < C::kPParts; ++p) {
