@@ -422,14 +422,17 @@ PSW_API int psw_latent_workspace_bytes(const psw_latent_t *layer, int32_t n_seqs
  *              q_rope itself with the same strides, and must not overlap it or
  *              itself in any other way
  *   cu_new, past_lens, pages, pool  as kv_cache_write
+ *   n_new_total  host: rows of ckv, q_rope and q_rope_out; rows that cu_new names
+ *              beyond it are not touched and flagged (PSW_DEVERR_LENGTH)
  * All strides are multiples of 8 elements, ckv_stride >= L + 64, query strides
  * >= 64 (PSW_EINVAL_STRIDE). Other errors as qkv_norm_rope_cache_write.
  */
 PSW_API int latent_norm_rope_cache_write(
     const psw_latent_t *layer, const psw_latent_norm_t *norm, const void *ckv, int64_t ckv_stride,
     const void *q_rope, int64_t q_token_stride, int64_t q_head_stride, const int32_t *cu_new,
-    const int32_t *past_lens, int32_t n_seqs, const psw_pages_t *pages, void *q_rope_out,
-    int64_t qo_token_stride, int64_t qo_head_stride, void *pool, psw_stream_t stream);
+    const int32_t *past_lens, int32_t n_seqs, int32_t n_new_total, const psw_pages_t *pages,
+    void *q_rope_out, int64_t qo_token_stride, int64_t qo_head_stride, void *pool,
+    psw_stream_t stream);
 
 /* The same into FP8 pages: pool8 uint8 [num_blocks][16][L + 64] of E4M3 codes
  * and row_scale fp32 [num_blocks][16] (16-byte aligned), one scale per row by the rule of
@@ -438,9 +441,9 @@ PSW_API int latent_norm_rope_cache_write(
 PSW_API int latent_norm_rope_cache_write_fp8(
     const psw_latent_t *layer, const psw_latent_norm_t *norm, const void *ckv, int64_t ckv_stride,
     const void *q_rope, int64_t q_token_stride, int64_t q_head_stride, const int32_t *cu_new,
-    const int32_t *past_lens, int32_t n_seqs, const psw_pages_t *pages, void *q_rope_out,
-    int64_t qo_token_stride, int64_t qo_head_stride, void *pool8, float *row_scale,
-    psw_stream_t stream);
+    const int32_t *past_lens, int32_t n_seqs, int32_t n_new_total, const psw_pages_t *pages,
+    void *q_rope_out, int64_t qo_token_stride, int64_t qo_head_stride, void *pool8,
+    float *row_scale, psw_stream_t stream);
 
 /*
  * Absorbed latent attention of one new token per sequence over its pages.
@@ -474,6 +477,7 @@ PSW_API int attn_decode_latent_fp8(const psw_latent_t *layer, const void *q, con
  *   kv[t][h][e] = sum_l c_l w[h][e][l]   (256 per head: 128 key, 128 value)
  *   k_rope[t]   = r
  *   cu_k      device int32 [n_seqs + 1], non-decreasing, cu_k[n_seqs] <= n_k_total
+ *             (flagged otherwise, PSW_DEVERR_LENGTH)
  *   k_first   device int32 [n_seqs], first position wanted, or NULL (all 0);
  *             a sliding layer needs only the keys its chunk can see
  *   n_k_total host: rows of kv and k_rope; rows at or beyond cu_k[n_seqs] are

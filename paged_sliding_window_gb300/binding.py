@@ -143,7 +143,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.attn_decode_paged_append.restype = ctypes.c_int
         zp, zn = ctypes.POINTER(PswLatent), ctypes.POINTER(PswLatentNorm)
         lib.psw_latent_workspace_bytes.argtypes = [zp, i32, ctypes.POINTER(sz)]
-        write = [zp, zn, vp, i64, vp, i64, i64, vp, vp, i32, pp, vp, i64, i64, vp]
+        write = [zp, zn, vp, i64, vp, i64, i64, vp, vp, i32, i32, pp, vp, i64, i64, vp]
         lib.latent_norm_rope_cache_write.argtypes = write + [vp]
         lib.latent_norm_rope_cache_write_fp8.argtypes = write + [vp, vp]
         lib.attn_decode_latent.argtypes = [zp, vp, vp, pp, vp, i32, vp, vp, vp, sz, vp]
@@ -185,7 +185,9 @@ def make_layer(layer) -> PswLayer:
 
 def make_pages(block_table: torch.Tensor, num_blocks: int) -> PswPages:
     _check(block_table, torch.int32, "block_table")
-    return PswPages(block_table.data_ptr(), int(block_table.shape[1]), int(num_blocks))
+    pages = PswPages(block_table.data_ptr(), int(block_table.shape[1]), int(num_blocks))
+    pages.table = block_table  # keeps the tensor alive as long as its address is held
+    return pages
 
 
 def _ptr(t):
@@ -446,6 +448,14 @@ def _want(t, dtype, shape, name, device, strided=False):
     raise ValueError(f"{name} must be contiguous" + (" in its last dimension" if strided else ""))
 
 
+def _want_rows(pages, n_seqs, device):
+    """The page table has a row for every sequence (where it came from make_pages)."""
+    table = getattr(pages, "table", None)
+    if table is not None and (table.shape[0] < n_seqs or table.get_device() != device):
+        raise ValueError(f"the block table must have {n_seqs} rows or more on device {device}, "
+                         f"got {tuple(table.shape)} on {table.device}")
+
+
 def _stream_of(device, stream):
     """The stream of a call on `device`, which must be the current device (as for every call:
     the library launches there)."""
@@ -497,10 +507,11 @@ def _latent_write(name, layer, norm, ckv, q_rope, cu_new, past_lens, pages, q_ro
     if row_scale is not None:
         _want(row_scale, _F32, (pages.num_blocks, 16), "row_scale", dev)
         tail.append(row_scale.data_ptr())
+    _want_rows(pages, n_seqs, dev)
     if n_tok == 0 or n_seqs == 0:
         return
     rc = getattr(load(), name)(ctypes.byref(z), ctypes.byref(norm), ckv.data_ptr(), *_strides(ckv),
-                               *q_args, cu_new.data_ptr(), past_lens.data_ptr(), n_seqs,
+                               *q_args, cu_new.data_ptr(), past_lens.data_ptr(), n_seqs, n_tok,
                                ctypes.byref(pages), *qo_args, *tail, _stream_of(dev, stream))
     if rc:
         _raise(rc, name)
@@ -509,7 +520,7 @@ def _latent_write(name, layer, norm, ckv, q_rope, cu_new, past_lens, pages, q_ro
 def latent_norm_rope_cache_write(layer, norm: PswLatentNorm, ckv, q_rope, cu_new, past_lens,
                                  pages: PswPages, q_rope_out, pool, stream=None) -> None:
     """Norm, rotation and cache write of new latent rows. ckv bf16 [n, latent_dim + 64] (rows may
-    be strided, n = cu_new[n_seqs] at least); q_rope and q_rope_out bf16 [n, heads, 64] views of
+    be strided); q_rope and q_rope_out bf16 [n, heads, 64] views of
     any token and head stride (in place is fine), or both None."""
     _latent_write("latent_norm_rope_cache_write", layer, norm, ckv, q_rope, cu_new, past_lens,
                   pages, q_rope_out, pool, None, stream)
@@ -544,6 +555,7 @@ def _latent_decode(name, layer, q, pool, row_scale, pages, seq_lens, out, lse, w
         if not ws.is_cuda or ws.get_device() != dev or not ws.is_contiguous():
             raise ValueError(f"ws must be a contiguous CUDA tensor on device {dev}")
         ws_ptr, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    _want_rows(pages, n_seqs, dev)
     if n_seqs == 0:
         return
     rc = getattr(load(), name)(ctypes.byref(z), q.data_ptr(), *pools, ctypes.byref(pages),
@@ -587,6 +599,7 @@ def _latent_expand(name, layer, pool, row_scale, pages, cu_k, w, kv, k_rope, k_f
     if row_scale is not None:
         _want(row_scale, _F32, (pages.num_blocks, 16), "row_scale", dev)
         pools.append(row_scale.data_ptr())
+    _want_rows(pages, n_seqs, dev)
     if n_k == 0 or n_seqs == 0:
         return
     rc = getattr(load(), name)(ctypes.byref(z), *pools, ctypes.byref(pages), cu_k.data_ptr(),

@@ -50,7 +50,7 @@ bool row_stride_ok(int64_t s, int64_t least) { return s >= least && s % 8 == 0; 
 int write_rows(const psw_latent_t* layer, const psw_latent_norm_t* norm, const void* ckv,
                int64_t ckv_stride, const void* q_rope, int64_t q_token_stride,
                int64_t q_head_stride, const int32_t* cu_new, const int32_t* past_lens,
-               int32_t n_seqs, const psw_pages_t* pages, void* q_rope_out,
+               int32_t n_seqs, int32_t n_new_total, const psw_pages_t* pages, void* q_rope_out,
                int64_t qo_token_stride, int64_t qo_head_stride, void* pool, float* row_scale,
                psw_stream_t stream) {
   LatentArgs L;
@@ -64,6 +64,7 @@ int write_rows(const psw_latent_t* layer, const psw_latent_norm_t* norm, const v
     return PSW_EINVAL_ROPE;
   if ((rc = check_pages(pages)) != PSW_OK) return rc;
   if (n_seqs < 0) return PSW_EINVAL_NSEQS;
+  if (n_new_total < 0) return PSW_ECAPACITY;
   if (!row_stride_ok(ckv_stride, L.row())) return PSW_EINVAL_STRIDE;
   if (q_rope != nullptr) {
     if (!row_stride_ok(q_token_stride, kLatentRope) ||
@@ -79,14 +80,15 @@ int write_rows(const psw_latent_t* layer, const psw_latent_norm_t* norm, const v
   if (!aligned(ckv, 16) || !aligned(q_rope, 16) || !aligned(q_rope_out, 16) ||
       !aligned(pool, 16) || !aligned(norm->latent_weight, 16) || !aligned(row_scale, 16))
     return PSW_EALIGN;
-  if (n_seqs == 0) return PSW_OK;
+  if (n_seqs == 0 || n_new_total == 0) return PSW_OK;
   DeviceInfo info;
   int32_t* err;
   if ((rc = ready(&info, &err)) != PSW_OK) return rc;
   const LatentRows q{q_rope, q_token_stride, q_head_stride,
                      q_rope_out, qo_token_stride, qo_head_stride};
   return launch_latent_write(L, norm->theta, norm->eps, norm->latent_weight, ckv, ckv_stride, q,
-                             cu_new, past_lens, n_seqs, pages_of(pages, pool, row_scale), pool,
+                             cu_new, past_lens, n_seqs, n_new_total,
+                             pages_of(pages, pool, row_scale), pool,
                              row_scale, info.num_sms, err, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -155,25 +157,26 @@ int latent_norm_rope_cache_write(const psw_latent_t* layer, const psw_latent_nor
                                  const void* ckv, int64_t ckv_stride, const void* q_rope,
                                  int64_t q_token_stride, int64_t q_head_stride,
                                  const int32_t* cu_new, const int32_t* past_lens, int32_t n_seqs,
-                                 const psw_pages_t* pages, void* q_rope_out,
+                                 int32_t n_new_total, const psw_pages_t* pages, void* q_rope_out,
                                  int64_t qo_token_stride, int64_t qo_head_stride, void* pool,
                                  psw_stream_t stream) {
   return write_rows(layer, norm, ckv, ckv_stride, q_rope, q_token_stride, q_head_stride, cu_new,
-                    past_lens, n_seqs, pages, q_rope_out, qo_token_stride, qo_head_stride, pool,
-                    nullptr, stream);
+                    past_lens, n_seqs, n_new_total, pages, q_rope_out, qo_token_stride,
+                    qo_head_stride, pool, nullptr, stream);
 }
 
 int latent_norm_rope_cache_write_fp8(const psw_latent_t* layer, const psw_latent_norm_t* norm,
                                      const void* ckv, int64_t ckv_stride, const void* q_rope,
                                      int64_t q_token_stride, int64_t q_head_stride,
                                      const int32_t* cu_new, const int32_t* past_lens,
-                                     int32_t n_seqs, const psw_pages_t* pages, void* q_rope_out,
+                                     int32_t n_seqs, int32_t n_new_total,
+                                     const psw_pages_t* pages, void* q_rope_out,
                                      int64_t qo_token_stride, int64_t qo_head_stride, void* pool8,
                                      float* row_scale, psw_stream_t stream) {
   if (row_scale == nullptr) return PSW_ENULL;
   return write_rows(layer, norm, ckv, ckv_stride, q_rope, q_token_stride, q_head_stride, cu_new,
-                    past_lens, n_seqs, pages, q_rope_out, qo_token_stride, qo_head_stride, pool8,
-                    row_scale, stream);
+                    past_lens, n_seqs, n_new_total, pages, q_rope_out, qo_token_stride,
+                    qo_head_stride, pool8, row_scale, stream);
 }
 
 int attn_decode_latent(const psw_latent_t* layer, const void* q, const void* pool,

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 latent_write_kernel(const __grid_constant__ Freqs freqs, const float* __restrict__ weight,
                     float eps, const __nv_bfloat16* __restrict__ ckv, int64_t ckv_stride,
                     const LatentRows q, int heads, const int32_t* __restrict__ cu_new,
-                    const int32_t* __restrict__ past_lens, int n_seqs,
+                    const int32_t* __restrict__ past_lens, int n_seqs, int n_new_total,
                     const int32_t* __restrict__ block_table, int max_blocks, int64_t num_blocks,
                     void* __restrict__ pool, float* __restrict__ row_scale, int32_t* err) {
   constexpr int kRow = LAT + kLatentRope, kVecs = LAT / 256, kHalf = kLatentRope / 2;
@@ -88,7 +88,9 @@ latent_write_kernel(const __grid_constant__ Freqs freqs, const float* __restrict
   __shared__ float2 s_f2[kHalf];
   if (threadIdx.x < kHalf) s_f2[threadIdx.x] = freqs.f2[threadIdx.x];
   __syncthreads();
-  const int total = __ldg(cu_new + n_seqs);
+  const int named = __ldg(cu_new + n_seqs), total = min(named, n_new_total);
+  if (named > n_new_total && blockIdx.x == 0 && threadIdx.x == 0)
+    flag_error(err, PSW_DEVERR_LENGTH);
   const int per_token = 1 + (q.in != nullptr ? (heads + kHeadsPerUnit - 1) / kHeadsPerUnit : 0);
   const int64_t units = static_cast<int64_t>(total) * per_token;
   // unit u on CTA u mod grid: the few units of a decode batch meet every SM
@@ -216,7 +218,8 @@ latent_write_kernel(const __grid_constant__ Freqs freqs, const float* __restrict
 int launch_latent_write(const LatentArgs& L, float theta, float eps, const float* weight,
                         const void* ckv, int64_t ckv_stride, const LatentRows& q,
                         const int32_t* cu_new, const int32_t* past_lens, int n_seqs,
-                        const LatentPages& pages, void* pool, float* row_scale, int num_sms,
+                        int n_new_total, const LatentPages& pages, void* pool, float* row_scale,
+                        int num_sms,
                         int32_t* err, cudaStream_t stream) {
   Freqs fr;
   const double log_theta = log(static_cast<double>(theta));
@@ -229,7 +232,7 @@ int launch_latent_write(const LatentArgs& L, float theta, float eps, const float
   const auto* x = static_cast<const __nv_bfloat16*>(ckv);
 #define PSW_LAUNCH(LAT_, FP8_)                                                                  \
   latent_write_kernel<LAT_, FP8_><<<grid, kWarps * 32, 0, stream>>>(                            \
-      fr, weight, eps, x, ckv_stride, q, L.n_heads, cu_new, past_lens, n_seqs,                  \
+      fr, weight, eps, x, ckv_stride, q, L.n_heads, cu_new, past_lens, n_seqs, n_new_total,     \
       pages.block_table, pages.max_blocks, pages.num_blocks, pool, row_scale, err)
   if (L.latent == 512) {
     if (row_scale != nullptr) PSW_LAUNCH(512, true);

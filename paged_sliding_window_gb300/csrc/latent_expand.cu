@@ -107,7 +107,8 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
   tc::fence_after();
   const uint32_t tmem = ms->tmem, rank = lat::cluster_rank();
   volatile int32_t* abort_flag = &ms->abort;
-  const int total = max(0, min(n_k, __ldg(cu_k + n_seqs)));
+  const int named = __ldg(cu_k + n_seqs), total = max(0, min(n_k, named));
+  if (named > n_k && blockIdx.x == 0 && tid == 0) flag_error(err, PSW_DEVERR_LENGTH);
   const int per_tile = heads * 2;
   const int pair = blockIdx.x / kCluster, pairs = gridDim.x / kCluster;
   const int64_t units =

@@ -186,7 +186,8 @@ struct LatentPages {
 int launch_latent_write(const LatentArgs& L, float theta, float eps, const float* weight,
                         const void* ckv, int64_t ckv_stride, const LatentRows& q,
                         const int32_t* cu_new, const int32_t* past_lens, int n_seqs,
-                        const LatentPages& pages, void* pool, float* row_scale, int num_sms,
+                        int n_new_total, const LatentPages& pages, void* pool, float* row_scale,
+                        int num_sms,
                         int32_t* err, cudaStream_t stream);
 
 size_t latent_decode_workspace(const LatentArgs& L, int n_seqs);

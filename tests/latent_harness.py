@@ -154,7 +154,8 @@ def rot_mag(x):
 
 def no_error():
     torch.cuda.synchronize()
-    assert binding.get_error() == 0
+    got = binding.get_error()
+    assert got == 0, f"error word {got}"
 
 
 def takes_error(bits):

@@ -150,6 +150,48 @@ def test_write_bad_pages():
     assert bool((out[3] == 5).all())
 
 
+def test_write_offsets_beyond_the_rows():
+    """Offsets that name more rows than there are: the rows there are get written, the rest is
+    flagged."""
+    L, H = 256, 2
+    pg = Pages([64], L, False, 2)
+    ckv, qs = randn(gen(1), 20, L + R).to(BF16), randn(gen(2), 20, H, R).to(BF16)
+    out = torch.empty_like(qs)
+    binding.latent_norm_rope_cache_write(LatentLayer(H, L), binding.make_latent_norm(THETA, EPS), ckv, qs, cu([30]), i32([0]), pg.pages, out, pg.pool)
+    takes_error(binding.DEVERR_LENGTH)
+    pos = torch.arange(20, device="cuda")
+    want = row_of(ckv, pos, L, None)
+    slop = 2.0 ** -20 * torch.cat([want[:, :L].abs(), rot_mag(ckv[:, L:])], 1)
+    check(pg.pool.view(-1, L + R)[pg.slots(0, 0, 20)], want, H_BF16 * want.abs() + slop, "rows")
+    check(out, rotated(qs, pos), H_BF16 * rotated(qs, pos).abs() + 2.0 ** -20 * rot_mag(qs), "queries")
+    assert int((~torch.isnan(pg.pool.float()).all(-1)).sum()) == 20
+
+
+def test_refusals_of_tensors():
+    """Shapes, types and tables that would be read out of bounds are refused before the launch."""
+    layer, pg = LatentLayer(4, 256), Pages([40, 40], 256, False, 1)
+    q, lens = torch.zeros(2, 4, 256 + R, dtype=BF16, device="cuda"), i32([40, 40])
+    out, ws = torch.zeros(2, 4, 256, dtype=BF16, device="cuda"), binding.alloc_latent_workspace(layer, 2)
+    ok = dict(layer=layer, q=q, pool=pg.pool, pages=pg.pages, seq_lens=lens, out=out, ws=ws)
+    binding.attn_decode_latent(**ok)
+    for bad in (dict(q=q[:1]), dict(q=q.float()), dict(q=q.cpu()), dict(q=q.transpose(0, 1)), dict(out=out[..., :128]),
+                dict(pool=pg.pool[1:]), dict(lse=torch.zeros(2, 3, device="cuda")), dict(seq_lens=lens.long()),
+                dict(pages=binding.make_pages(pg.table[:1].contiguous(), pg.blocks))):
+        with pytest.raises(ValueError):
+            binding.attn_decode_latent(**{**ok, **bad})
+    with pytest.raises(binding.PswError) as e:
+        binding.attn_decode_latent(**{**ok, "ws": ws[:1024]})
+    assert binding.ERRORS[e.value.code] == "PSW_EWORKSPACE"
+    w = torch.zeros(4, 256, 256, dtype=BF16, device="cuda")
+    kv, rope = torch.zeros(80, 4, 256, dtype=BF16, device="cuda"), torch.zeros(80, R, dtype=BF16, device="cuda")
+    with pytest.raises(ValueError):
+        binding.latent_kv_expand(layer, pg.pool, pg.pages, cu([40, 40]), w, kv, rope[:79])
+    with pytest.raises(ValueError):
+        binding.attn_prefill_latent(layer, torch.zeros(3, 4, 192, dtype=BF16, device="cuda"), cu([3]), i32([0]), 3, kv, rope,
+                                    cu([80]), torch.zeros(3, 4, 192, dtype=BF16, device="cuda"))
+    no_error()
+
+
 # ---------------------------------------------------------------- absorbed decode
 
 def _decode_inputs(layer, lens, fp8, seed, q_std=1.0, grow=0.0):

@@ -41,7 +41,7 @@ def call(lib, name, layer=None, **kw):
     scale = [g("row_scale")] if name.endswith("fp8") else []
     if name.startswith("latent_norm"):
         return getattr(lib, name)(lp, g("norm", _norm()), g("ckv"), g("ckv_stride", 576), g("q"),
-                                  g("qt", 16 * 192), g("qh", 192), g("cu"), g("past"), n, pages,
+                                  g("qt", 16 * 192), g("qh", 192), g("cu"), g("past"), n, g("nt", 5), pages,
                                   g("qo", FAKE * 2), g("qot", 16 * 64), g("qoh", 64), g("pool"),
                                   *scale, None)
     if name.startswith("attn_decode"):
@@ -90,7 +90,7 @@ def test_layer_refusals(lib, name, kw, code):
     (WRITES, dict(norm=_norm(eps=-1.0)), "PSW_EINVAL_ROPE"),
     (WRITES, dict(norm=_norm(theta=float("nan"))), "PSW_EINVAL_ROPE"),
     (WRITES, dict(ckv_stride=568), "PSW_EINVAL_STRIDE"), (WRITES, dict(ckv_stride=577), "PSW_EINVAL_STRIDE"),
-    (WRITES, dict(qh=60), "PSW_EINVAL_STRIDE"), (WRITES, dict(qot=68), "PSW_EINVAL_STRIDE"),
+    (WRITES, dict(nt=-1), "PSW_ECAPACITY"), (WRITES, dict(qh=60), "PSW_EINVAL_STRIDE"), (WRITES, dict(qot=68), "PSW_EINVAL_STRIDE"),
     (WRITES, dict(qoh=0), "PSW_EINVAL_STRIDE"), (WRITES, dict(qo=FAKE), "PSW_EINVAL_STRIDE"),
     (WRITES, dict(ckv=FAKE + 8), "PSW_EALIGN"), (WRITES, dict(q=FAKE + 2), "PSW_EALIGN"),
     (WRITES, dict(norm=_norm(weight=FAKE + 4)), "PSW_EALIGN"),
