@@ -9,16 +9,24 @@
 // block of rows: bound by the tensor cores and, before them, by what L2 brings
 // to an SM, so a CTA takes 256 rows of one head against every key tile.
 //
-// Schedule: a CTA has two tiles of 128 rows, A and B. Key tiles of 128 go
-// through a ring of 16 KB units (128 keys x 128 B, swizzled): two of key
-// components, one of the shared rotary part, two of values. Warp 8 loads. Warp
-// 9 issues, in turn for A and B, O += P V of a key tile and S = Q K^T of the
-// next: while the softmax of one row tile runs, the tensor cores work for the
-// other. P is written over S in tensor memory as bf16 (rounded once; sums are of
-// the unrounded values). Warps 0-3 and 4-7 are the softmaxes of A and B, a
-// thread per row. The maximum that P is relative to is that of a row's first
-// keys; it moves (O rescaled) only when a score exceeds it by 2^64, which P, O
-// and the sum have the range for. The longest sequences come first in the grid.
+// Schedule: two row tiles, A and B, of 128 rows of a CTA, are worked on in turn:
+// while the softmax of one runs, the tensor cores work for the other (O += P V of
+// a key tile, then S = Q K^T of the next). P is written over S in tensor memory as
+// bf16 (rounded once; sums are of the unrounded values). Warp 8 loads key tiles
+// into stages (swizzled 64-column units), warp 9 issues the products, warps 0-3 and
+// 4-7 are the softmaxes of A and B, a thread per row. The maximum that P is
+// relative to is that of a row's first keys; it moves (O rescaled) only when a
+// score exceeds it by 2^64, which P, O and the sum have the range for.
+//
+// A product of 128 rows by 128 keys reads as many bytes of shared memory as it
+// takes cycles at 128 a cycle, and the key tiles arrive there besides: a CTA by
+// itself is bound by its shared memory (573 us for four chunks of 2048 rows).
+// Chunks of more than 256 rows are therefore done by pairs of CTAs, 512 rows of one
+// head, whose tensor cores share products of 256 rows: each CTA holds half of the
+// keys and half of the value components of a tile, so that both the reads and the
+// arrivals halve and three stages of 128 keys fit (470 us). P is handed over in two
+// parts, so that the products begin while the rest of it is made. The longest
+// sequences come first in the grid.
 #include <math.h>
 
 #include "latent.cuh"
@@ -27,59 +35,89 @@ namespace psw {
 namespace lpre {
 
 constexpr int kQk = kLatentNope + kLatentRope;
-constexpr int kTile = 128;                    // rows of a row tile, keys of a key tile
-constexpr int kUnit = kTile * 128;            // bytes of a ring unit
+constexpr int kRows = 128;                    // of a row tile
 constexpr int kQChunks = kQk / 64;
-constexpr int kQBytes = 2 * kQChunks * kUnit;
-constexpr int kUnits = 8;
+constexpr int kQUnit = kRows * 128;           // 64 columns of a row tile
+constexpr int kQBytes = 2 * kQChunks * kQUnit;
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 320;
-constexpr int kSmemBytes = 1024 + kQBytes + kUnits * kUnit + 2048;
 constexpr int kTmemS = 0, kTmemO = 256;       // + 128 for B
 constexpr float kLag = 64.f;
 constexpr int kRanked = 256;                  // sequences put in order by their length
-static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+constexpr int kMaxStages = 3;
+constexpr int kHead = 64;                     // keys whose P is handed over first
+
+template <int CTAS>
+struct Cfg {
+  static constexpr int kKeys = CTAS == 2 ? 128 : 96;         // of a key tile
+  static constexpr int kStages = CTAS == 2 ? 3 : 2;
+  static constexpr int kHeld = kKeys / CTAS;                 // keys that a CTA holds
+  static constexpr int kKeyUnit = kHeld * 128;               // 64 columns of them
+  static constexpr int kKeyBytes = 3 * kKeyUnit;             // nope, nope, rope
+  static constexpr int kValueUnits = 2 / CTAS;               // 64 components each
+  static constexpr int kValueUnit = kKeys * 128;
+  static constexpr int kValueBytes = kValueUnits * kValueUnit;
+  static constexpr int kSmemBytes = 1024 + kQBytes + kStages * (kKeyBytes + kValueBytes) + 2048;
+  static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+};
 
 struct Misc {
-  uint64_t full[kUnits], empty[kUnits];
-  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], o_full[2];
-  uint64_t v_fix, drained;
+  // (the first CTA of a pair: its own and the second's)
+  uint64_t k_full[kMaxStages], v_full[kMaxStages], q_full[2];
+  uint64_t v_fix[kMaxStages];  // where a value tile with hidden rows lands first
+  uint64_t freed[kMaxStages];  // keys of tile k (and values of tile k - 1) are done with
+  uint64_t s_full[2], o_full[2];
+  uint64_t p_head[2], p_full[2];  // P of the first kHead keys, of all
+  uint64_t drained;
   uint32_t tmem;
   int32_t abort, seq;
   int32_t len[kRanked];
 };
 static_assert(sizeof(Misc) <= 2048, "misc block");
 
-// Ring units in the order of use, and each unit's phase. The two units of a
-// value tile do not wrap: the last unit is then left out.
-struct Ring {
-  int pos = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ int take(int n, uint32_t& parity) {
-    if (pos + n > kUnits) pos = 0;
-    const int s = pos;
-    parity = phase >> s;
-    phase ^= ((1u << n) - 1u) << s;
-    pos = pos + n == kUnits ? 0 : pos + n;
-    return s;
-  }
+// A sequence's rows and keys, and what a block of rows has of them; the same in
+// every thread.
+struct Seq {
+  int q0, nq, k0, nk;   // first row and rows (of q), first key row and keys
+  int64_t past, first;  // positions of the first row and of the first key
 };
-
-// What a CTA works on; the same in every thread.
 struct Work {
-  int q0, rows;         // first row (of q), rows of the CTA
-  int k0, nk;           // first key row, keys of the sequence
-  int64_t p0, first;    // position of the first row; of the first key
   int lo[2], hi[2];     // key tiles [lo, hi) of A and of B
   int t_lo, t_hi;       // of both
   int j_lo, j_hi;       // keys [j_lo, j_hi) that some row sees
 };
+// Of the rows from i0 on, `tile` in each of A and B, and key tiles of `keys`.
+__device__ __forceinline__ Work work_of(const Seq& q, int i0, int tile, int keys, int window) {
+  Work w;
+  w.t_lo = w.j_lo = 0x7fffffff;
+  w.t_hi = w.j_hi = 0;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const int n = min(tile, q.nq - i0 - g * tile);
+    // keys of the tile's rows: from the window of its first to its last
+    const int64_t a = q.past + i0 + g * tile - q.first;
+    const int64_t lo64 = window > 0 ? a - window + 1 : 0;
+    const int lo = static_cast<int>(max(min(lo64, static_cast<int64_t>(q.nk)), static_cast<int64_t>(0)));
+    const int hi = static_cast<int>(max(min(a + n, static_cast<int64_t>(q.nk)), static_cast<int64_t>(0)));
+    const bool some = n > 0 && lo < hi;
+    w.lo[g] = some ? lo / keys : 0;
+    w.hi[g] = some ? (hi + keys - 1) / keys : 0;
+    if (some) {
+      w.t_lo = min(w.t_lo, w.lo[g]);
+      w.t_hi = max(w.t_hi, w.hi[g]);
+      w.j_lo = min(w.j_lo, lo);
+      w.j_hi = max(w.j_hi, hi);
+    }
+  }
+  return w;
+}
 
 __device__ __forceinline__ float tanh_abs(float y) {
   const float t = ex2_approx(-2.f * lat::kLog2e * fabsf(y));
   return copysignf(__fdividef(1.f - t, 1.f + t), y);
 }
 
+template <int CTAS>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
                       const __grid_constant__ CUtensorMap kv_map,
@@ -89,35 +127,47 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
                       const int32_t* __restrict__ k_first, int n_k, int heads, int blocks,
                       int window, float scale, float softcap, __nv_bfloat16* __restrict__ out,
                       float* __restrict__ lse, int32_t* err) {
+  using C = Cfg<CTAS>;
+  constexpr int kKeys = C::kKeys, kStages = C::kStages;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* q_smem = smem;
-  uint8_t* ring = smem + kQBytes;
-  Misc* ms = reinterpret_cast<Misc*>(ring + kUnits * kUnit);
+  uint8_t* k_smem = smem + kQBytes;
+  uint8_t* v_smem = k_smem + kStages * C::kKeyBytes;
+  Misc* ms = reinterpret_cast<Misc*>(v_smem + kStages * C::kValueBytes);
 
-  // ---- the CTA's sequence, head and block of rows: heads innermost within a
-  // sequence's blocks, its last block (the most keys) first
+  // ---- the sequence, head and block of rows: heads innermost within a sequence's
+  // blocks, its last block (the most keys) first
   const int per_seq = heads * blocks;
-  const int rank = blockIdx.x / per_seq, sub = blockIdx.x - rank * per_seq;
+  const int item = blockIdx.x / CTAS, rank = item / per_seq, sub = item - rank * per_seq;
   const int block = blocks - 1 - sub / heads, head = sub % heads;
+  const int peer = CTAS == 2 ? static_cast<int>(lat::cluster_rank()) : 0;  // number in the pair
+  constexpr int kTile = kRows * CTAS;  // rows of A (and of B), of both CTAs
+  const int i0 = block * 2 * kTile;
   if (warp == kMmaWarp) {
-    tc::alloc(&ms->tmem, 512);
-    tc::relinquish();
+    if (CTAS == 2) {
+      lat::alloc_pair(&ms->tmem, 512);
+    } else {
+      tc::alloc(&ms->tmem, 512);
+      tc::relinquish();
+    }
   }
   if (tid == 32 * kLoadWarp) {
-    for (int i = 0; i < kUnits; ++i) {
-      mbar_init(&ms->full[i], 1);
-      mbar_init(&ms->empty[i], 1);
+    const uint32_t arrivals = CTAS - peer;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&ms->k_full[i], arrivals);
+      mbar_init(&ms->v_full[i], arrivals);
+      mbar_init(&ms->v_fix[i], 1);
+      mbar_init(&ms->freed[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ms->q_full[i], 1);
+      mbar_init(&ms->q_full[i], arrivals);
       mbar_init(&ms->s_full[i], 1);
-      mbar_init(&ms->p_full[i], 4);
-      mbar_init(&ms->pv_done[i], 1);
+      mbar_init(&ms->p_head[i], 4 * CTAS);
+      mbar_init(&ms->p_full[i], 4 * CTAS);
       mbar_init(&ms->o_full[i], 1);
     }
-    mbar_init(&ms->v_fix, 1);
     mbar_init(&ms->drained, 1);
     ms->abort = 0;
     fence_mbar_init();
@@ -136,130 +186,104 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
   } else if (tid == 0) {
     ms->seq = rank;
   }
+  __syncwarp();
   tc::fence_before();
-  __syncthreads();
+  if (CTAS == 2) lat::cluster_sync();
+  else __syncthreads();
   tc::fence_after();
   const uint32_t tmem = ms->tmem;
   const int b = ms->seq;
   volatile int32_t* abort_flag = &ms->abort;
 
-  Work w;
-  bool some = true;
+  Seq sq;
   {
-    w.q0 = __ldg(cu_q + b);
-    w.k0 = __ldg(cu_k + b);
-    int nq = __ldg(cu_q + b + 1) - w.q0;
-    w.nk = __ldg(cu_k + b + 1) - w.k0;
-    const int past = __ldg(past_lens + b), first = k_first != nullptr ? __ldg(k_first + b) : 0;
+    sq.q0 = __ldg(cu_q + b);
+    sq.k0 = __ldg(cu_k + b);
+    sq.nq = __ldg(cu_q + b + 1) - sq.q0;
+    sq.nk = __ldg(cu_k + b + 1) - sq.k0;
+    sq.past = __ldg(past_lens + b);
+    sq.first = k_first != nullptr ? __ldg(k_first + b) : 0;
     bool bad = false;
-    if (w.q0 < 0 || nq < 0 || past < 0 || w.k0 < 0 || w.nk < 0 || first < 0) {
+    if (sq.q0 < 0 || sq.nq < 0 || sq.past < 0 || sq.k0 < 0 || sq.nk < 0 || sq.first < 0) {
       bad = true;
-      nq = 0;
-      w.nk = 0;
+      sq.nq = sq.nk = 0;
     }
-    if (nq > max_q_len || static_cast<int64_t>(w.q0) + nq > n_q) {
+    if (sq.nq > max_q_len || static_cast<int64_t>(sq.q0) + sq.nq > n_q) {
       bad = true;
-      nq = max(0, min(nq, min(max_q_len, n_q - w.q0)));
+      sq.nq = max(0, min(sq.nq, min(max_q_len, n_q - sq.q0)));
     }
-    if (static_cast<int64_t>(w.k0) + w.nk > n_k) {
+    if (static_cast<int64_t>(sq.k0) + sq.nk > n_k) {
       bad = true;
-      w.nk = max(0, min(w.nk, n_k - w.k0));
+      sq.nk = max(0, min(sq.nk, n_k - sq.k0));
     }
     if (bad && tid == 0 && block == 0 && head == 0) flag_error(err, PSW_DEVERR_LENGTH);
-    const int i0 = block * 2 * kTile;
-    w.rows = min(2 * kTile, nq - i0);
-    some = w.rows > 0;
-    w.q0 += i0;
-    w.p0 = static_cast<int64_t>(past) + i0;
-    w.first = first;
-    w.t_lo = 0x7fffffff;
-    w.t_hi = 0;
-    w.j_lo = 0x7fffffff;
-    w.j_hi = 0;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int n = min(kTile, w.rows - g * kTile);
-      // keys of the tile's rows: from the window of its first to its last
-      const int64_t a = w.p0 + g * kTile;
-      const int64_t lo64 = window > 0 ? a - window + 1 - first : 0, hi64 = a + n - first;
-      const int lo = static_cast<int>(max(lo64, static_cast<int64_t>(0)));
-      const int hi = static_cast<int>(max(min(hi64, static_cast<int64_t>(w.nk)), static_cast<int64_t>(0)));
-      const bool any = n > 0 && lo < hi;
-      w.lo[g] = any ? lo / kTile : 0;
-      w.hi[g] = any ? (hi + kTile - 1) / kTile : 0;
-      if (any) {
-        w.t_lo = min(w.t_lo, w.lo[g]);
-        w.t_hi = max(w.t_hi, w.hi[g]);
-        w.j_lo = min(w.j_lo, lo);
-        w.j_hi = max(w.j_hi, hi);
-      }
-    }
   }
+  const Work w = work_of(sq, i0, kTile, kKeys, window);
+  const int my_row = i0 + peer * kRows;  // first row of this CTA's part of A; B's is kTile on
   bool ok = true;
-  Ring rg;
 
-  if (!some) {
-    // no rows: nothing to do
+  if (sq.nq <= i0) {
+    // nothing to do
   } else if (warp == kLoadWarp) {
     // ------------------------------------------------------------ loads
     const bool one = lat::elect_one();
-    uint32_t issued = 0;
-    int fixes = 0;
     if (one) {
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         if (w.lo[g] >= w.hi[g]) continue;
-        mbar_arrive_expect_tx(&ms->q_full[g], kQChunks * kUnit);
+        mbar_arrive_expect_tx(&ms->q_full[g], kQChunks * kQUnit);
         for (int c = 0; c < kQChunks; ++c)
-          lat::tma_box(smem_u32(q_smem + (g * kQChunks + c) * kUnit), &q_map, &ms->q_full[g],
-                       c * 64, head, w.q0 + g * kTile);
+          lat::tma_box(smem_u32(q_smem + (g * kQChunks + c) * kQUnit), &q_map, &ms->q_full[g],
+                       c * 64, head, sq.q0 + my_row + g * kTile);
       }
     }
-    auto load = [&](int s, uint64_t* bar, const CUtensorMap* map, int x, int y, int z) {
-      issued |= 1u << s;
-      if (one) lat::tma_box(smem_u32(ring + s * kUnit), map, bar, x, y, z);
-    };
-    for (int j = w.t_lo; ok && j < w.t_hi; ++j) {
-      const int row = w.k0 + j * kTile;
-      for (int c = 0; c < 3; ++c) {  // keys: two of the head's components, the rotary part
-        uint32_t parity;
-        const int s = rg.take(1, parity);
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&ms->empty[s], (parity & 1u) ^ 1u) && *abort_flag == 0);
-        if (!ok) break;
-        if (one) mbar_arrive_expect_tx(&ms->full[s], kUnit);
-        if (c < 2) load(s, &ms->full[s], &kv_map, c * 64, head, row);
-        else load(s, &ms->full[s], &rope_map, 0, row, 0);
+    uint32_t fixes = 0;  // phases of v_fix
+    int n = 0;           // key tiles loaded
+    for (int j = w.t_lo; ok && j < w.t_hi; ++j, ++n) {
+      const int row = sq.k0 + j * kKeys, st = n % kStages;
+      auto freed = [&](int k) {  // keys of tile k, values of the one before
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(&ms->freed[k % kStages], k / kStages & 1u) && *abort_flag == 0);
+        return ok;
+      };
+      if (n == kStages && !freed(0)) break;  // (later keys: known from the values before them)
+      if (one) {  // a pair: half of the keys each
+        const uint32_t k = smem_u32(k_smem + st * C::kKeyBytes);
+        const int mine = row + peer * C::kHeld;
+        mbar_arrive_expect_tx(&ms->k_full[st], C::kKeyBytes);
+        lat::tma_box(k, &kv_map, &ms->k_full[st], 0, head, mine);
+        lat::tma_box(k + C::kKeyUnit, &kv_map, &ms->k_full[st], 64, head, mine);
+        lat::tma_box(k + 2 * C::kKeyUnit, &rope_map, &ms->k_full[st], 0, mine, 0);
       }
-      if (!ok) break;
-      // values; rows of keys that no row sees (other sequences', or anything)
-      // must not enter the second product (P is 0 there, but 0 times NaN is not)
-      uint32_t parity;
-      const int s = rg.take(2, parity);
-      for (int c = 0; c < 2; ++c)
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&ms->empty[s + c], (parity >> c & 1u) ^ 1u) && *abort_flag == 0);
-      if (!ok) break;
-      const int z_lo = max(0, w.j_lo - j * kTile), z_hi = min(kTile, w.j_hi - j * kTile);
-      const bool fix = z_lo > 0 || z_hi < kTile;
+      // values (a pair: half of the components each); rows of keys that no row sees
+      // (other sequences', or anything) must not enter the second product (P is 0
+      // there, but 0 times NaN is not)
+      if (n >= kStages && !freed(n - kStages + 1)) break;
+      const int z_lo = w.j_lo - j * kKeys, z_hi = w.j_hi - j * kKeys;
+      const bool fix = z_lo > 0 || z_hi < kKeys;
+      uint8_t* v = v_smem + st * C::kValueBytes;
       if (one) {
-        if (fix) mbar_arrive_expect_tx(&ms->v_fix, 2 * kUnit);
-        else
-          for (int c = 0; c < 2; ++c) mbar_arrive_expect_tx(&ms->full[s + c], kUnit);
+        uint64_t* bar = fix ? &ms->v_fix[st] : &ms->v_full[st];
+        mbar_arrive_expect_tx(bar, C::kValueBytes);
+#pragma unroll
+        for (int c = 0; c < C::kValueUnits; ++c)
+#pragma unroll
+          for (int h = 0; h < CTAS; ++h)  // (boxes are kHeld rows high)
+            lat::tma_box(smem_u32(v + c * C::kValueUnit + h * C::kKeyUnit), &kv_map, bar,
+                         kLatentNope + (c + peer) * 64, head, row + h * C::kHeld);
       }
       __syncwarp();
-      for (int c = 0; c < 2; ++c)
-        load(s + c, fix ? &ms->v_fix : &ms->full[s + c], &kv_map, kLatentNope + c * 64, head, row);
       if (fix) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&ms->v_fix, fixes & 1));
-        ++fixes;
+        ok = __all_sync(0xffffffffu, mbar_wait(&ms->v_fix[st], fixes >> st & 1u));
+        fixes ^= 1u << st;
         if (!ok) break;
-        for (int i = lane; i < 2 * kTile * 8; i += 32) {
-          const int r = (i >> 3) & (kTile - 1);
-          if (r < z_lo || r >= z_hi)
-            *reinterpret_cast<uint4*>(ring + s * kUnit + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = lane; i < C::kValueUnits * kKeys * 8; i += 32) {
+          const int r = (i >> 3) % kKeys;
+          if (r < z_lo || r >= z_hi) *reinterpret_cast<uint4*>(v + i * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane < 2) mbar_arrive(&ms->full[s + lane]);
+        if (lane == 0) mbar_arrive(&ms->v_full[st]);
       }
     }
     if (!ok && one) {
@@ -269,136 +293,167 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
       for (int g = 0; g < 2; ++g)
         if (w.lo[g] < w.hi[g]) mbar_wait(&ms->q_full[g], 0);
-      for (int s = 0; s < kUnits; ++s)
-        if (issued >> s & 1u) mbar_wait(&ms->full[s], ((rg.phase >> s) & 1u) ^ 1u);
+      for (int i = max(0, n - kStages); i < n; ++i) {
+        mbar_wait(&ms->k_full[i % kStages], i / kStages & 1);
+        mbar_wait(&ms->v_full[i % kStages], i / kStages & 1);
+      }
     }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMAs
+  } else if (warp == kMmaWarp && peer == 1) {
+    // ------------------------------------------------------------ second CTA of a pair
+    // tells the first, which issues the products, what has landed here
     const bool one = lat::elect_one();
-    constexpr uint32_t id_s = tc::idesc_bf16_f32(kTile, kTile, 0, 0);
-    constexpr uint32_t id_o = tc::idesc_bf16_f32(kTile, kLatentV, 0, 1);
-    constexpr uint32_t kStep = kUnit >> 4;
-    const uint64_t q_desc = tc::smem_desc(smem_u32(q_smem), 16, 1024, tc::kSwizzle128B);
-    const uint64_t k_desc = tc::smem_desc(smem_u32(ring), 16, 1024, tc::kSwizzle128B);
-    const uint64_t v_desc = tc::smem_desc(smem_u32(ring), kUnit, 1024, tc::kSwizzle128B);
-    auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && mbar_wait(bar, parity & 1u); };
-    int n[2] = {0, 0};  // S formed for each row tile
-    int ks[3], vs = 0;  // units of the key tile at hand, of the value tile
-    uint32_t kp[3], vp = 0;
-    auto scores = [&](int g) {
-      if (n[g] == 0) wait(&ms->q_full[g], 0);
-#pragma unroll
-      for (int c = 0; c < 3; ++c) {
-        wait(&ms->full[ks[c]], kp[c]);
-        tc::fence_after();
-        const uint64_t kd = k_desc + ks[c] * kStep, qd = q_desc + (g * kQChunks + c) * kStep;
-        if (ok && one) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc::mma_ss(tmem + kTmemS + g * kTile, qd + k * 2, kd + k * 2, id_s, (c > 0 || k > 0) ? 1u : 0u);
-        }
-      }
-      if (ok && one) tc::commit(&ms->s_full[g]);
-      ++n[g];
+    auto pass_on = [&](uint64_t* bar, uint32_t parity) {
+      ok = ok && mbar_wait(bar, parity & 1u);
+      if (ok && one) lat::arrive_at_first(bar);
     };
-    auto take_keys = [&]() {
 #pragma unroll
-      for (int c = 0; c < 3; ++c) ks[c] = rg.take(1, kp[c]);
-    };
-    auto free_keys = [&]() {
-      if (ok && one) {
-#pragma unroll
-        for (int c = 0; c < 3; ++c) tc::commit(&ms->empty[ks[c]]);
-      }
-    };
-    if (w.t_lo < w.t_hi) {
-      take_keys();
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-        if (w.lo[g] == w.t_lo && w.lo[g] < w.hi[g]) scores(g);
-      free_keys();
-    }
-    for (int j = w.t_lo; ok && j < w.t_hi; ++j) {
-      vs = rg.take(2, vp);
-      if (j + 1 < w.t_hi) take_keys();
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if (j >= w.lo[g] && j < w.hi[g]) {
-          wait(&ms->p_full[g], n[g] - 1);
-          wait(&ms->full[vs], vp);
-          wait(&ms->full[vs + 1], vp >> 1);
-          tc::fence_after();
-          if (ok && one) {
-            const uint64_t vd = v_desc + vs * kStep;
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              tc::mma_ts(tmem + kTmemO + g * kLatentV, tmem + kTmemS + g * kTile + k * 8,
-                         vd + k * (2048 >> 4), id_o, (j > w.lo[g] || k > 0) ? 1u : 0u);
-            tc::commit(&ms->pv_done[g]);
-            if (j == w.hi[g] - 1) tc::commit(&ms->o_full[g]);
-          }
-        }
-        if (j + 1 >= w.lo[g] && j + 1 < w.hi[g]) scores(g);
-      }
-      if (ok && one) {
-        tc::commit(&ms->empty[vs]);
-        tc::commit(&ms->empty[vs + 1]);
-      }
-      if (j + 1 < w.t_hi) free_keys();
-      ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
+    for (int g = 0; g < 2; ++g)
+      if (w.lo[g] < w.hi[g]) pass_on(&ms->q_full[g], 0);
+    for (int j = w.t_lo, k = 0; ok && j < w.t_hi; ++j, ++k) {
+      pass_on(&ms->k_full[k % kStages], k / kStages);
+      pass_on(&ms->v_full[k % kStages], k / kStages);
     }
     if (one) {
       if (!ok) {
         *abort_flag = 1;
         flag_error(err, PSW_DEVERR_PIPELINE);
       }
-      tc::commit(&ms->drained);  // every MMA has ended before tensor memory is freed
+      mbar_wait(&ms->drained, 0);  // the last of the first CTA's arrivals here
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMAs
+    const bool one = lat::elect_one();
+    constexpr uint32_t id_s = tc::idesc_bf16_f32(kTile, kKeys, 0, 0);
+    constexpr uint32_t id_o = tc::idesc_bf16_f32(kTile, kLatentV, 0, 1);
+    const uint64_t q_desc = tc::smem_desc(smem_u32(q_smem), 16, 1024, tc::kSwizzle128B);
+    const uint64_t k_desc = tc::smem_desc(smem_u32(k_smem), 16, 1024, tc::kSwizzle128B);
+    const uint64_t v_desc = tc::smem_desc(smem_u32(v_smem), C::kValueUnit, 1024, tc::kSwizzle128B);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = ok && mbar_wait(bar, parity & 1u);
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (CTAS == 2) lat::commit_pair(bar);
+      else tc::commit(bar);
+    };
+    int n[2] = {0, 0};  // S formed for each row tile
+    auto scores = [&](int g, int k) {  // of the k-th key tile loaded
+      if (n[g] == 0) wait(&ms->q_full[g], 0);
+      tc::fence_after();
+      const uint64_t kd = k_desc + (k % kStages) * (C::kKeyBytes >> 4);
+      const uint64_t qd = q_desc + g * kQChunks * (kQUnit >> 4);
+      if (ok && one) {
+#pragma unroll
+        for (int c = 0; c < kQChunks; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint64_t a = qd + (c * kQUnit >> 4) + e * 2, b = kd + (c * C::kKeyUnit >> 4) + e * 2;
+            const uint32_t acc = (c > 0 || e > 0) ? 1u : 0u;
+            if (CTAS == 2) lat::mma_ss_pair(tmem + kTmemS + g * 128, a, b, id_s, acc);
+            else tc::mma_ss(tmem + kTmemS + g * 128, a, b, id_s, acc);
+          }
+        commit(&ms->s_full[g]);
+      }
+      ++n[g];
+    };
+    // the k-th key tile has landed, the k-th value tile has
+    auto keys = [&](int k) { wait(&ms->k_full[k % kStages], k / kStages); };
+    auto values = [&](int k) { wait(&ms->v_full[k % kStages], k / kStages); };
+    if (w.t_lo < w.t_hi) {
+      keys(0);
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        if (w.lo[g] == w.t_lo && w.lo[g] < w.hi[g]) scores(g, 0);
+      if (ok && one) commit(&ms->freed[0]);
+      values(0);
+      if (w.t_lo + 1 < w.t_hi) keys(1);
+    }
+    for (int j = w.t_lo, k = 0; ok && j < w.t_hi; ++j, ++k) {
+      const int st = k % kStages;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (j >= w.lo[g] && j < w.hi[g]) {
+          const uint64_t vd = v_desc + st * (C::kValueBytes >> 4);
+          auto product = [&](int e) {
+            const uint32_t d = tmem + kTmemO + g * kLatentV, a = tmem + kTmemS + g * 128 + e * 8;
+            const uint32_t acc = (j > w.lo[g] || e > 0) ? 1u : 0u;
+            if (CTAS == 2) lat::mma_ts_pair(d, a, vd + e * (2048 >> 4), id_o, acc);
+            else tc::mma_ts(d, a, vd + e * (2048 >> 4), id_o, acc);
+          };
+          wait(&ms->p_head[g], n[g] - 1);
+          tc::fence_after();
+          if (ok && one) {
+#pragma unroll
+            for (int e = 0; e < kHead / 16; ++e) product(e);
+          }
+          wait(&ms->p_full[g], n[g] - 1);
+          tc::fence_after();
+          if (ok && one) {
+#pragma unroll
+            for (int e = kHead / 16; e < kKeys / 16; ++e) product(e);
+            if (j == w.hi[g] - 1) commit(&ms->o_full[g]);
+          }
+        }
+        if (j + 1 >= w.lo[g] && j + 1 < w.hi[g]) scores(g, k + 1);
+        if (g == 0) {  // what the next round needs, while B's softmax runs
+          if (j + 1 < w.t_hi) values(k + 1);
+          if (j + 2 < w.t_hi) keys(k + 2);
+        }
+      }
+      if (ok && one) commit(&ms->freed[(k + 1) % kStages]);
+    }
+    if (one) {
+      if (!ok) {
+        *abort_flag = 1;
+        flag_error(err, PSW_DEVERR_PIPELINE);
+      }
+      commit(&ms->drained);  // every product has ended before tensor memory is freed
       mbar_wait(&ms->drained, 0);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax, epilogue
-    const int g = warp >> 2, r = (warp & 3) * 32 + lane, i = g * kTile + r;
+    const int g = warp >> 2, r = (warp & 3) * 32 + lane, i = my_row + g * kTile + r;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_at = tmem + lanes + kTmemS + g * kTile;
+    const uint32_t s_at = tmem + lanes + kTmemS + g * 128;
     const uint32_t o_at = tmem + lanes + kTmemO + g * kLatentV;
-    const int64_t p = w.p0 + i;
+    const int64_t p = sq.past + i;
     const bool cap = softcap > 0.f;
     const float mul = cap ? 1.f : scale * lat::kLog2e;
     const float cap_in = cap ? scale / softcap : 0.f, cap_out = softcap * lat::kLog2e;
     float m = -INFINITY, l = 0.f;
     int n = 0;
-    const int t_lo = g == 0 ? w.lo[0] : w.lo[1], t_hi = g == 0 ? w.hi[0] : w.hi[1];
-    for (int j = t_lo; j < t_hi; ++j, ++n) {
+    const int g_lo = g == 0 ? w.lo[0] : w.lo[1], g_hi = g == 0 ? w.hi[0] : w.hi[1];
+    for (int j = g_lo; j < g_hi; ++j, ++n) {
       // (every decision is the same in the whole warp)
       ok = __all_sync(0xffffffffu, mbar_wait(&ms->s_full[g], n & 1) && *abort_flag == 0);
       if (!ok) break;
       tc::fence_after();
-      float x[kTile];
+      float x[kKeys];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < kKeys / 32; ++c)
         tc::ld32(s_at + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[c * 32]));
       tc::wait_ld();
       // this row's visible columns of the tile
-      const int64_t at = w.first + static_cast<int64_t>(j) * kTile;
-      const int64_t hi64 = min(p - at, static_cast<int64_t>(w.nk - 1 - j * kTile));
+      const int64_t at = sq.first + static_cast<int64_t>(j) * kKeys;
+      const int64_t hi64 = min(p - at, static_cast<int64_t>(sq.nk - 1 - j * kKeys));
       const int64_t lo64 = window > 0 ? p - window + 1 - at : 0;
-      const int c_hi = static_cast<int>(max(min(hi64, static_cast<int64_t>(kTile - 1)), static_cast<int64_t>(-1)));
-      const int c_lo = static_cast<int>(max(min(lo64, static_cast<int64_t>(kTile)), static_cast<int64_t>(0)));
+      const int c_hi = static_cast<int>(max(min(hi64, static_cast<int64_t>(kKeys - 1)), static_cast<int64_t>(-1)));
+      const int c_lo = static_cast<int>(max(min(lo64, static_cast<int64_t>(kKeys)), static_cast<int64_t>(0)));
       if (cap) {
 #pragma unroll
-        for (int c = 0; c < kTile; ++c) x[c] = cap_out * tanh_abs(x[c] * cap_in);
+        for (int c = 0; c < kKeys; ++c) x[c] = cap_out * tanh_abs(x[c] * cap_in);
       }
-      if (!__all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kTile - 1)) {
+      if (!__all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kKeys - 1)) {
 #pragma unroll
-        for (int c = 0; c < kTile; ++c) x[c] = c >= c_lo && c <= c_hi ? x[c] : -INFINITY;
+        for (int c = 0; c < kKeys; ++c) x[c] = c >= c_lo && c <= c_hi ? x[c] : -INFINITY;
       }
       float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int c = 4; c < kTile; c += 8) {
+      for (int c = 4; c < kKeys; c += 8) {
         mx[0] = max3f(mx[0], x[c], x[c + 1]);
         mx[1] = max3f(mx[1], x[c + 2], x[c + 3]);
-        if (c + 4 < kTile) {
+        if (c + 4 < kKeys) {
           mx[2] = max3f(mx[2], x[c + 4], x[c + 5]);
           mx[3] = max3f(mx[3], x[c + 6], x[c + 7]);
         }
@@ -413,9 +468,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
         m = to;
         l *= a;
         if (__any_sync(0xffffffffu, a != 1.f)) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&ms->pv_done[g], (n - 1) & 1));
-          if (!ok) break;
-          tc::fence_after();
+          // (the product of the tile before was issued before this S, and has ended)
 #pragma unroll 1
           for (int c = 0; c < kLatentV; c += 16) {
             uint32_t v[16];
@@ -430,33 +483,39 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
       }
       const float ref = m == -INFINITY ? 0.f : m;
       const uint64_t mul2 = f2_pack(mul, mul), ref2 = f2_pack(-ref, -ref);
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      uint64_t sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < kKeys / 32; ++c) {
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float2 z = f2_unpack(f2_fma(f2_pack(x[c * 32 + 2 * e], x[c * 32 + 2 * e + 1]), mul2, ref2));
           const float a0 = ex2_approx(z.x), a1 = ex2_approx(z.y);
-          sum[2 * (e & 1)] += a0;
-          sum[2 * (e & 1) + 1] += a1;
+          sum[e & 1] = f2_add(sum[e & 1], f2_pack(a0, a1));
           pk[e] = pack_bf16x2(a0, a1);
         }
         tc::st16(s_at + c * 16, pk);
+        if (c * 32 + 32 == kHead || c * 32 + 32 == kKeys) {
+          tc::wait_st();
+          tc::fence_before();
+          __syncwarp();
+          uint64_t* bar = c * 32 + 32 == kHead ? &ms->p_head[g] : &ms->p_full[g];
+          if (lane == 0) {
+            if (CTAS == 2) lat::arrive_at_first(bar);
+            else mbar_arrive(bar);
+          }
+        }
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tc::wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms->p_full[g]);
+      const float2 sums0 = f2_unpack(sum[0]), sums1 = f2_unpack(sum[1]);
+      l += (sums0.x + sums0.y) + (sums1.x + sums1.y);
     }
     if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&ms->o_full[g], 0));
     if (ok) {
       tc::fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int64_t row = static_cast<int64_t>(w.q0 + i) * heads + head;
+      const int64_t row = static_cast<int64_t>(sq.q0 + i) * heads + head;
       uint4* dst = reinterpret_cast<uint4*>(out + row * kLatentV);
-      const bool mine = i < w.rows;
+      const bool mine = i < sq.nq;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t v[32];
@@ -481,8 +540,12 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
   }
   __syncwarp();
   tc::fence_before();
-  __syncthreads();
-  if (warp == kMmaWarp) tc::dealloc(tmem, 512);
+  if (CTAS == 2) lat::cluster_sync();  // nobody leaves while the other may still reach into it
+  else __syncthreads();
+  if (warp == kMmaWarp) {
+    if (CTAS == 2) lat::dealloc_pair(tmem, 512);
+    else tc::dealloc(tmem, 512);
+  }
 }
 
 }  // namespace lpre
@@ -495,28 +558,44 @@ int launch_latent_prefill(const LatentArgs& L, const void* q, const int32_t* cu_
   using namespace lpre;
   CUtensorMap q_map, kv_map, rope_map;
   const int64_t h = L.n_heads;
-  int rc = make_map_3d(&q_map, false, q, {kQk, h, n_q_total}, {2 * kQk, 2 * kQk * h}, {64, 1, kTile});
+  // pairs of CTAs for chunks that are longer than the 256 rows of one
+  const int ctas = max_q_len > 2 * kRows ? 2 : 1;
+  const int held = ctas == 2 ? Cfg<2>::kHeld : Cfg<1>::kHeld;
+  const int64_t blocks = (static_cast<int64_t>(max_q_len) + 2 * kRows * ctas - 1) / (2 * kRows * ctas);
+  const int64_t grid = blocks * ctas * L.n_heads * n_seqs;
+  if (grid > 0x7fffffffLL) return PSW_ECAPACITY;
+  int rc = make_map_3d(&q_map, false, q, {kQk, h, n_q_total}, {2 * kQk, 2 * kQk * h}, {64, 1, kRows});
   if (rc != PSW_OK) return rc;
   if (n_k_total > 0) {
     rc = make_map_3d(&kv_map, false, kv, {kLatentKv, h, n_k_total}, {2 * kLatentKv, 2 * kLatentKv * h},
-                     {64, 1, kTile});
+                     {64, 1, held});
     if (rc == PSW_OK)
       rc = make_map_3d(&rope_map, false, k_rope, {kLatentRope, n_k_total, 1},
-                       {2 * kLatentRope, 2 * kLatentRope}, {64, kTile, 1});
+                       {2 * kLatentRope, 2 * kLatentRope}, {64, held, 1});
     if (rc != PSW_OK) return rc;
   } else {
     kv_map = rope_map = q_map;  // no key tile will be loaded
   }
-  rc = set_smem_limit(reinterpret_cast<const void*>(latent_prefill_kernel), kSmemBytes);
+  auto* kernel = ctas == 2 ? latent_prefill_kernel<2> : latent_prefill_kernel<1>;
+  const int smem = ctas == 2 ? Cfg<2>::kSmemBytes : Cfg<1>::kSmemBytes;
+  rc = set_smem_limit(reinterpret_cast<const void*>(kernel), smem);
   if (rc != PSW_OK) return rc;
-  const int64_t blocks = (static_cast<int64_t>(max_q_len) + 2 * kTile - 1) / (2 * kTile);
-  if (blocks * L.n_heads * n_seqs > 0x7fffffffLL) return PSW_ECAPACITY;
-  latent_prefill_kernel<<<static_cast<unsigned>(blocks * L.n_heads * n_seqs), kThreads, kSmemBytes,
-                          stream>>>(q_map, kv_map, rope_map, cu_q, past_lens, n_seqs, n_q_total,
-                                    max_q_len, cu_k, k_first, n_k_total, L.n_heads,
-                                    static_cast<int>(blocks), L.window, L.scale, L.softcap,
-                                    static_cast<__nv_bfloat16*>(out), lse, err);
-  return cudaGetLastError() == cudaSuccess ? PSW_OK : PSW_ELAUNCH;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(
+      &cfg, kernel, q_map, kv_map, rope_map, cu_q, past_lens, n_seqs, n_q_total, max_q_len, cu_k,
+      k_first, n_k_total, L.n_heads, static_cast<int>(blocks), L.window, L.scale, L.softcap,
+      static_cast<__nv_bfloat16*>(out), lse, err);
+  return e == cudaSuccess ? PSW_OK : PSW_ELAUNCH;
 }
 
 }  // namespace psw

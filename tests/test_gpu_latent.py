@@ -474,6 +474,14 @@ def _run_prefill(layer, new, past, first=None, keys=None, seed=21, spare=3, q_st
     pytest.param(LatentLayer(128, scale=0.07), [33], [10], {}, id="128-heads"),
     pytest.param(LatentLayer(2, scale=2.0), [300], [500], {}, id="peaked"),
     pytest.param(LatentLayer(1, scale=0.07), [1] * 300, list(range(300)), {}, id="300-sequences"),
+    # chunks of more than 256 rows, done by pairs of CTAs, 512 rows each
+    pytest.param(LatentLayer(3, scale=0.07), [512, 511, 257, 1, 0], [0, 129, 2048, 3000, 7], {}, id="pair-edges"),
+    pytest.param(LatentLayer(2, scale=0.07), [1300, 513], [1, 700], {}, id="pair-blocks"),
+    pytest.param(LatentLayer(2, scale=0.07, window=90, softcap=4.0), [1025, 260], [300, 1], {}, id="pair-window"),
+    pytest.param(LatentLayer(2, scale=0.07), [600, 300], [0, 10], dict(first=[400, 0], keys=[150, 310]), id="pair-rows-with-no-key"),
+    pytest.param(LatentLayer(2, scale=0.07), [600, 400, 300], [10, 10, 0], dict(keys=[0, 5, 128]), id="pair-few-or-no-keys"),
+    pytest.param(LatentLayer(1, scale=0.07, window=64), [300] + [1] * 299, [500] * 300, dict(first=[400] + [437] * 299), id="pair-300-sequences"),
+    pytest.param(LatentLayer(40, scale=0.07), [700, 280, 600], [100, 1500, 0], {}, id="pair-more-work-than-pairs"),
 ])
 def test_prefill(layer, new, past, kw):
     _run_prefill(layer, new, past, **kw)
@@ -489,9 +497,10 @@ def test_prefill_no_keys_at_all():
     assert bool((out == 0).all()) and bool((lse == -math.inf).all())
 
 
-def test_prefill_growing_scores():
+@pytest.mark.parametrize("n,t", [(200, 900), (700, 1500)])
+def test_prefill_growing_scores(n, t):
     """Scores that grow along the context by far more than a running maximum may lag behind."""
-    layer, n, t = LatentLayer(2, scale=1.0), 200, 900
+    layer = LatentLayer(2, scale=1.0)
     g = gen(2)
     q = randn(g, n, 2, NOPE + R).to(BF16)
     q[:, :, :] = q[:1, :1]
