@@ -27,7 +27,8 @@ namespace psw {
 namespace lexp {
 
 constexpr int kTile = 128;
-constexpr int kUnit = kTile * 128;              // bytes of a chunk and of a box of w
+constexpr int kUnit = kTile * 128;              // bytes of a chunk of rows
+constexpr int kBox = kUnit / 2;                 // of a CTA's half of a box of w
 constexpr int kMmaWarp = 4, kWeightWarp = 5, kRowWarp = 6;
 constexpr int kRowThreads = 128;                // warps 6-9
 constexpr int kThreads = 320;
@@ -36,22 +37,22 @@ constexpr int kStage = 4 * 32 * 64;             // epilogue: 32 rows x 64 B per 
 constexpr int kMisc = 3072;
 constexpr int kAhead = 4;                       // chunks of rows in shared memory
 constexpr int kCluster = 2;
-constexpr uint16_t kBoth = 3;
+constexpr int kMaxRing = 18;
 constexpr int kSmemLimit = 232448;
 
 template <int LAT>
 struct Cfg {
   static constexpr int kChunks = LAT / 64;
-  static constexpr int kRing = (kSmemLimit - 1024 - kMisc - kStage - kAhead * kUnit) / kUnit;
-  static constexpr int kSmemBytes = 1024 + (kAhead + kRing) * kUnit + kStage + kMisc;
+  static constexpr int kRing = (kSmemLimit - 1024 - kMisc - kStage - kAhead * kUnit) / kBox;
+  static constexpr int kSmemBytes = 1024 + kAhead * kUnit + kRing * kBox + kStage + kMisc;
   static_assert(kChunks % kAhead == 0, "rows come in groups of chunks");
-  static_assert(kRing >= 4 && kRing <= 16, "boxes of w in flight");
+  static_assert(kRing >= 4 && kRing <= kMaxRing, "boxes of w in flight");
   static constexpr int kTmemD = LAT / 2;          // after the rows
   static_assert(kTmemD + kAcc * kTile <= 512, "tensor memory columns");
 };
 
 struct Misc {
-  uint64_t a_full[8], a_empty[8], w_full[16], w_empty[16], d_full[kAcc], d_empty[kAcc];
+  uint64_t a_full[8], a_empty[8], w_full[kMaxRing], w_empty[kMaxRing], d_full[kAcc], d_empty[kAcc];
   uint64_t rows_done[2], rows_set[2], drained;
   uint32_t tmem;
   int32_t abort;
@@ -73,25 +74,26 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* a_smem = smem;  // rows on their way
   uint8_t* w_ring = smem + kAhead * kUnit;
-  uint8_t* stage = w_ring + C::kRing * kUnit;
+  uint8_t* stage = w_ring + C::kRing * kBox;
   Misc* ms = reinterpret_cast<Misc*>(stage + kStage);
 
   if (warp == kMmaWarp) {
-    tc::alloc(&ms->tmem, 512);
-    tc::relinquish();
+    lat::alloc_pair(&ms->tmem, 512);
   }
+  const uint32_t rank = lat::cluster_rank();
   if (tid == 0) {
+    // (the first CTA issues the products of both: what they wait for arrives there)
     for (int i = 0; i < 8; ++i) {
-      mbar_init(&ms->a_full[i], 4);
+      mbar_init(&ms->a_full[i], 4 * kCluster);
       mbar_init(&ms->a_empty[i], 1);
     }
-    for (int i = 0; i < 16; ++i) {
-      mbar_init(&ms->w_full[i], 1);
-      mbar_init(&ms->w_empty[i], kCluster);
+    for (int i = 0; i < C::kRing; ++i) {
+      mbar_init(&ms->w_full[i], rank == 0 ? kCluster : 1);
+      mbar_init(&ms->w_empty[i], 1);
     }
     for (int i = 0; i < kAcc; ++i) {
       mbar_init(&ms->d_full[i], 1);
-      mbar_init(&ms->d_empty[i], 4);
+      mbar_init(&ms->d_empty[i], 4 * kCluster);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ms->rows_set[i], 4);
@@ -105,7 +107,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
   tc::fence_before();
   lat::cluster_sync();
   tc::fence_after();
-  const uint32_t tmem = ms->tmem, rank = lat::cluster_rank();
+  const uint32_t tmem = ms->tmem;
   volatile int32_t* abort_flag = &ms->abort;
   const int named = __ldg(cu_k + n_seqs), total = max(0, min(n_k, named));
   if (named > n_k && blockIdx.x == 0 && tid == 0) flag_error(err, PSW_DEVERR_LENGTH);
@@ -286,7 +288,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
         tc::wait_st();
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ms->a_full[c]);
+        if (lane == 0) lat::arrive_at_first(&ms->a_full[c]);
       }
       // the rows have been read: the next may come
       if (over || (over = lat::bar_any(1, kRowThreads, !ok))) break;
@@ -311,10 +313,9 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
         const int s = box % C::kRing;
         ok = ok && mbar_wait(&ms->w_empty[s], (box / C::kRing & 1u) ^ 1u);
         if (ok && one) {
-          mbar_arrive_expect_tx(&ms->w_full[s], kUnit);
-          lat::tma_box_multicast(smem_u32(w_ring + s * kUnit + rank * (kUnit / kCluster)), &w_map,
-                                 &ms->w_full[s], c * 64, sub * kTile + rank * (kTile / kCluster),
-                                 0, kBoth);
+          mbar_arrive_expect_tx(&ms->w_full[s], kBox);
+          lat::tma_box(smem_u32(w_ring + s * kBox), &w_map, &ms->w_full[s], c * 64,
+                       sub * kTile + rank * (kTile / kCluster), 0);
         }
       }
       sub = sub + 1 == per_tile ? 0 : sub + 1;
@@ -327,11 +328,32 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
       for (int i = max(0, box - C::kRing); i < box; ++i)
         mbar_wait(&ms->w_full[i % C::kRing], i / C::kRing & 1);
     }
+  } else if (warp == kMmaWarp && rank != 0) {
+    // ------------------------------------------------------------ second CTA
+    // tells the first, which issues the products, what of w has landed here
+    const bool one = lat::elect_one();
+    const int64_t boxes = static_cast<int64_t>(count) * C::kChunks;
+    int s = 0;
+    uint32_t phase = 0;
+    for (int64_t i = 0; ok && i < boxes; ++i) {
+      ok = mbar_wait(&ms->w_full[s], phase);
+      if (ok && one) lat::arrive_at_first(&ms->w_full[s]);
+      s = s + 1 == C::kRing ? 0 : s + 1;
+      phase ^= s == 0 ? 1u : 0u;
+    }
+    if (one) {
+      if (!ok) {
+        *abort_flag = 1;
+        flag_error(err, PSW_DEVERR_PIPELINE);
+      }
+      mbar_wait(&ms->drained, 0);  // the last of the first CTA's arrivals here
+    }
+    __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMAs
     const bool one = lat::elect_one();
-    constexpr uint32_t id = tc::idesc_bf16_f32(kTile, kTile, 0, 0);
-    constexpr uint32_t kStep = kUnit >> 4;
+    constexpr uint32_t id = tc::idesc_bf16_f32(kCluster * kTile, kTile, 0, 0);
+    constexpr uint32_t kStep = kBox >> 4;
     const uint64_t w_desc = tc::smem_desc(smem_u32(w_ring), 16, 1024, tc::kSwizzle128B);
     int sub = first_sub, n = 0, s = 0;
     uint32_t phase = 0;
@@ -359,13 +381,13 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
         if (ok && one) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc::mma_ts(tmem + C::kTmemD + acc * kTile, tmem + c * 32 + k * 8, wd + k * 2, id,
-                       (c > 0 || k > 0) ? 1u : 0u);
-          lat::commit_multicast(empty, kBoth);
-          if (last) tc::commit(&ms->a_empty[c]);
+            lat::mma_ts_pair(tmem + C::kTmemD + acc * kTile, tmem + c * 32 + k * 8, wd + k * 2, id,
+                             (c > 0 || k > 0) ? 1u : 0u);
+          lat::commit_pair(empty);
+          if (last) lat::commit_pair(&ms->a_empty[c]);
         }
       }
-      if (ok && one) tc::commit(&ms->d_full[acc]);
+      if (ok && one) lat::commit_pair(&ms->d_full[acc]);
       if (last) ++n;
       sub = sub + 1 == per_tile ? 0 : sub + 1;
       ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
@@ -375,7 +397,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
         *abort_flag = 1;
         flag_error(err, PSW_DEVERR_PIPELINE);
       }
-      tc::commit(&ms->drained);  // every MMA has ended before tensor memory is freed
+      lat::commit_pair(&ms->drained);  // every MMA has ended before tensor memory is freed
       mbar_wait(&ms->drained, 0);
     }
     __syncwarp();
@@ -403,7 +425,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
         if (g == 3) {  // the accumulator has been read
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ms->d_empty[acc]);
+          if (lane == 0) lat::arrive_at_first(&ms->d_empty[acc]);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -437,7 +459,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
   __syncwarp();
   tc::fence_before();
   lat::cluster_sync();  // nobody leaves while the other may still reach into it
-  if (warp == kMmaWarp) tc::dealloc(tmem, 512);
+  if (warp == kMmaWarp) lat::dealloc_pair(tmem, 512);
 }
 
 template <int LAT, bool FP8>

@@ -388,6 +388,8 @@ def _w(g, H, L):
     pytest.param(256, 3, [700, 65], [0, 33], id="offset"),
     pytest.param(512, 128, [40, 3], [16, 1000], id="128-heads"),
     pytest.param(512, 5, [1] * 300, None, id="300-sequences"),
+    pytest.param(256, 1, [26001, 19000], [0, 7], id="several-tiles"),
+    pytest.param(512, 1, [40001], None, id="several-tiles-512"),
 ])
 def test_expand(L, H, lens, first, fp8):
     g, first_l = gen(7), first or [0] * len(lens)
