@@ -28,7 +28,8 @@ namespace lexp {
 
 constexpr int kTile = 128;
 constexpr int kUnit = kTile * 128;              // bytes of a chunk of rows
-constexpr int kBox = kUnit / 2;                 // of a CTA's half of a box of w
+constexpr int kBoxChunks = 2;                   // chunks of a box of w
+constexpr int kBox = kBoxChunks * kUnit / 2;    // bytes of a CTA's half of one
 constexpr int kMmaWarp = 4, kWeightWarp = 5, kRowWarp = 6;
 constexpr int kRowThreads = 128;                // warps 6-9
 constexpr int kThreads = 320;
@@ -37,7 +38,7 @@ constexpr int kStage = 4 * 32 * 64;             // epilogue: 32 rows x 64 B per 
 constexpr int kMisc = 3072;
 constexpr int kAhead = 4;                       // chunks of rows in shared memory
 constexpr int kCluster = 2;
-constexpr int kMaxRing = 18;
+constexpr int kMaxRing = 9;
 constexpr int kSmemLimit = 232448;
 
 template <int LAT>
@@ -168,55 +169,53 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
       named_bar_sync(1, kRowThreads);
       if (lane == 0) mbar_arrive(&ms->rows_set[buf]);
     };
-    // the group of chunks from c0 on of the rows in slots: on their way (bf16: to
-    // shared memory, a copy group per chunk; FP8: to registers)
-    auto start = [&](const int32_t* slots, int c0) {
+    // chunk c of the rows in slots: on its way (bf16: to shared memory, a copy group;
+    // FP8: to registers)
+    auto start = [&](const int32_t* slots, int c) {
       if constexpr (!FP8) {
         const auto* pool = static_cast<const __nv_bfloat16*>(pages.pool);
         const int v = lane & 7;  // eight lanes to a row's 128 bytes
 #pragma unroll
-        for (int c = 0; c < kAhead; ++c) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int q = k * 16 + rw * 4 + (lane >> 3);
-            const int64_t slot = slots[q];
-            lat::copy16(smem_u32(a_smem + c * kUnit + q * 128 + ((v ^ (q & 7)) << 4)),
-                        pool + max(slot, static_cast<int64_t>(0)) * kRow + (c0 + c) * 64 + v * 8,
-                        slot >= 0 ? 16u : 0u);
-          }
-          asm volatile("cp.async.commit_group;" ::: "memory");
+        for (int k = 0; k < 8; ++k) {
+          const int q = k * 16 + rw * 4 + (lane >> 3);
+          const int64_t slot = slots[q];
+          lat::copy16(smem_u32(a_smem + c % kAhead * kUnit + q * 128 + ((v ^ (q & 7)) << 4)),
+                      pool + max(slot, static_cast<int64_t>(0)) * kRow + c * 64 + v * 8,
+                      slot >= 0 ? 16u : 0u);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
       } else {
         const auto* pool = static_cast<const uint8_t*>(pages.pool);
         const int v = lane & 3;  // four lanes to a row's 64 codes
 #pragma unroll
-        for (int c = 0; c < kAhead; ++c)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int64_t slot = slots[k * 32 + rw * 8 + (lane >> 2)];
-            raw[c][k] = slot >= 0 ? __ldg(reinterpret_cast<const uint4*>(pool + slot * kRow + (c0 + c) * 64) + v)
-                                  : make_uint4(0u, 0u, 0u, 0u);
-          }
+        for (int k = 0; k < 4; ++k) {
+          const int64_t slot = slots[k * 32 + rw * 8 + (lane >> 2)];
+          raw[c % kAhead][k] = slot >= 0 ? __ldg(reinterpret_cast<const uint4*>(pool + slot * kRow + c * 64) + v)
+                                         : make_uint4(0u, 0u, 0u, 0u);
+        }
       }
     };
-    auto convert = [&]() {  // FP8: the codes in registers, as bf16 (exact), to shared memory
+    auto convert = [&](int c) {  // FP8: the codes in registers, as bf16 (exact), to shared memory
       const int v = lane & 3;
 #pragma unroll
-      for (int c = 0; c < kAhead; ++c)
+      for (int k = 0; k < 4; ++k) {
+        const int q = k * 32 + rw * 8 + (lane >> 2);
+        const uint4 x4 = raw[c % kAhead][k];
+        const uint32_t cc[4] = {x4.x, x4.y, x4.z, x4.w};
+        uint32_t y[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int q = k * 32 + rw * 8 + (lane >> 2);
-          const uint32_t cc[4] = {raw[c][k].x, raw[c][k].y, raw[c][k].z, raw[c][k].w};
-          uint32_t y[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 x = lat::e4m3_values(cc[e >> 1] >> (16 * (e & 1)) & 0xFFFFu);
-            y[e] = pack_bf16x2(x.x, x.y);
-          }
-          uint8_t* at = a_smem + c * kUnit + q * 128;
-          *reinterpret_cast<uint4*>(at + (((2 * v) ^ (q & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-          *reinterpret_cast<uint4*>(at + (((2 * v + 1) ^ (q & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+        for (int e = 0; e < 8; ++e) {
+          const float2 x = lat::e4m3_values(cc[e >> 1] >> (16 * (e & 1)) & 0xFFFFu);
+          y[e] = pack_bf16x2(x.x, x.y);
         }
+        uint8_t* at = a_smem + c % kAhead * kUnit + q * 128;
+        *reinterpret_cast<uint4*>(at + (((2 * v) ^ (q & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4*>(at + (((2 * v + 1) ^ (q & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+      }
+    };
+    auto start_first = [&](const int32_t* slots) {
+#pragma unroll
+      for (int c = 0; c < kAhead; ++c) start(slots, c);
     };
     // the rotary part of tile n
     auto rotary = [&](int n) {
@@ -248,31 +247,27 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
       }
     };
     locate(0);
-    start(ms->slot[0], 0);
+    start_first(ms->slot[0]);
     bool over = false;  // the same in all four warps
     for (int n = 0; n < n_tiles; ++n) {
 #pragma unroll
       for (int c = 0; c < C::kChunks; ++c) {
-        if (c % kAhead == 0) {
-          if (c > 0) {
-            named_bar_sync(1, kRowThreads);  // the group before has been read
-            if (!FP8) start(ms->slot[n & 1], c);
-          }
-          if (FP8) {
-            convert();
-            if (c + kAhead < C::kChunks) start(ms->slot[n & 1], c + kAhead);
-          }
+        if constexpr (FP8) {
+          convert(c);
+          if (c + kAhead < C::kChunks) start(ms->slot[n & 1], c + kAhead);
+        } else {
+          // all but the chunks after this one have landed, of those asked for so far
+          const int later = min(C::kChunks, max(kAhead, c + kAhead - 1)) - c - 1;
+          if (later == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+          if (later == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+          if (later == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+          if (later == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
-        if (!FP8) {
-          if (c % kAhead == 0) asm volatile("cp.async.wait_group 3;" ::: "memory");
-          if (c % kAhead == 1) asm volatile("cp.async.wait_group 2;" ::: "memory");
-          if (c % kAhead == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-          if (c % kAhead == 3) asm volatile("cp.async.wait_group 0;" ::: "memory");
-        }
-        // everybody's part of the chunk is there (a warp that gives up takes the
-        // others along)
+        // everybody's part of the chunk is there, and the chunk before has been read (a
+        // warp that gives up takes the others along)
         over = lat::bar_any(1, kRowThreads, !ok || *abort_flag != 0);
         if (over) break;
+        if (!FP8 && c > 0 && c + kAhead - 1 < C::kChunks) start(ms->slot[n & 1], c + kAhead - 1);
         uint32_t y[32];
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
@@ -294,7 +289,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
       if (over || (over = lat::bar_any(1, kRowThreads, !ok))) break;
       if (n + 1 < n_tiles) {
         locate(n + 1);
-        start(ms->slot[(n + 1) & 1], 0);
+        start_first(ms->slot[(n + 1) & 1]);
       }
       if (n > 0 || first_sub == 0) rotary(n);  // by the CTA that has the tile's first unit
     }
@@ -309,13 +304,15 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
     int sub = first_sub, box = 0;
     for (int u = 0; ok && u < count; ++u) {
 #pragma unroll
-      for (int c = 0; c < C::kChunks; ++c, ++box) {
+      for (int c = 0; c < C::kChunks; c += kBoxChunks, ++box) {
         const int s = box % C::kRing;
         ok = ok && mbar_wait(&ms->w_empty[s], (box / C::kRing & 1u) ^ 1u);
         if (ok && one) {
           mbar_arrive_expect_tx(&ms->w_full[s], kBox);
-          lat::tma_box(smem_u32(w_ring + s * kBox), &w_map, &ms->w_full[s], c * 64,
-                       sub * kTile + rank * (kTile / kCluster), 0);
+#pragma unroll
+          for (int i = 0; i < kBoxChunks; ++i)
+            lat::tma_box(smem_u32(w_ring + s * kBox + i * (kUnit / 2)), &w_map, &ms->w_full[s],
+                         (c + i) * 64, sub * kTile + rank * (kTile / kCluster), 0);
         }
       }
       sub = sub + 1 == per_tile ? 0 : sub + 1;
@@ -332,7 +329,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
     // ------------------------------------------------------------ second CTA
     // tells the first, which issues the products, what of w has landed here
     const bool one = lat::elect_one();
-    const int64_t boxes = static_cast<int64_t>(count) * C::kChunks;
+    const int64_t boxes = static_cast<int64_t>(count) * (C::kChunks / kBoxChunks);
     int s = 0;
     uint32_t phase = 0;
     for (int64_t i = 0; ok && i < boxes; ++i) {
@@ -365,27 +362,30 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap w_map, const LatentPage
       ok = mbar_wait(&ms->d_empty[acc], (u / kAcc & 1u) ^ 1u);
       tc::fence_after();
 #pragma unroll
-      for (int c = 0; c < C::kChunks; ++c) {
-        if (begins) {
-          ok = ok && mbar_wait(&ms->a_full[c], n & 1);
-          tc::fence_after();
-        }
+      for (int c0 = 0; c0 < C::kChunks; c0 += kBoxChunks) {
         if (!there) ok = ok && mbar_wait(&ms->w_full[s], phase);
         const uint64_t wd = w_desc + s * kStep;
         uint64_t* empty = &ms->w_empty[s];
-        // a box is 256 cycles of the tensor core and as much of this warp's time:
-        // whether the next has landed is asked while the products are issued
         s = s + 1 == C::kRing ? 0 : s + 1;
         phase ^= s == 0 ? 1u : 0u;
-        there = mbar_test(&ms->w_full[s], phase);
-        if (ok && one) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            lat::mma_ts_pair(tmem + C::kTmemD + acc * kTile, tmem + c * 32 + k * 8, wd + k * 2, id,
-                             (c > 0 || k > 0) ? 1u : 0u);
-          lat::commit_pair(empty);
-          if (last) lat::commit_pair(&ms->a_empty[c]);
+        for (int i = 0; i < kBoxChunks; ++i) {
+          const int c = c0 + i;
+          if (begins) {
+            ok = ok && mbar_wait(&ms->a_full[c], n & 1);
+            tc::fence_after();
+          }
+          if (ok && one) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              lat::mma_ts_pair(tmem + C::kTmemD + acc * kTile, tmem + c * 32 + k * 8,
+                               wd + i * (kUnit / 2 >> 4) + k * 2, id, (c > 0 || k > 0) ? 1u : 0u);
+            if (last) lat::commit_pair(&ms->a_empty[c]);
+          }
+          // whether the next box has landed is asked while the products are issued
+          if (i == 0) there = mbar_test(&ms->w_full[s], phase);
         }
+        if (ok && one) lat::commit_pair(empty);
       }
       if (ok && one) lat::commit_pair(&ms->d_full[acc]);
       if (last) ++n;
