@@ -65,10 +65,7 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, ui
       : "memory");
 }
 
-// ---- clusters: the rank of this CTA, a barrier of all their threads, a box that
-// lands at the same place in every CTA of `mask` (counted on that CTA's barrier at
-// the same place), and an arrival, once this thread's MMAs have ended, on that
-// barrier of each.
+// ---- clusters: the rank of this CTA, a barrier of all their threads.
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -78,22 +75,6 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile(
       "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
           : "memory");
-}
-__device__ __forceinline__ void tma_box_multicast(uint32_t dst, const CUtensorMap* map,
-                                                  uint64_t* bar, int32_t x, int32_t y, int32_t z,
-                                                  uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".multicast::cluster [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "h"(mask)
-      : "memory");
-}
-__device__ __forceinline__ void commit_multicast(uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(smem_u32(bar)),
-      "h"(mask)
-      : "memory");
 }
 
 // ---- pairs of CTAs (clusters of two) whose tensor cores work on one product of
@@ -234,27 +215,6 @@ __device__ __forceinline__ float warp_max(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
-}
-
-// Warp sums of N values at once (N a power of two up to 32): each round a lane
-// keeps one half of its list and trades the other with its partner; lane l ends
-// with the sum number l / (32 / N).
-template <int N>
-__device__ __forceinline__ float warp_sums(float (&x)[N], int lane) {
-#pragma unroll
-  for (int r = 0; (N >> r) > 1; ++r) {
-    const int n = N >> r, mask = 16 >> r;
-    const bool up = (lane & mask) != 0;
-#pragma unroll
-    for (int i = 0; i < n / 2; ++i) {
-      const float keep = up ? x[i + n / 2] : x[i], send = up ? x[i] : x[i + n / 2];
-      x[i] = keep + __shfl_xor_sync(0xffffffffu, send, mask);
-    }
-  }
-  float s = x[0];
-#pragma unroll
-  for (int mask = 16 / N; mask > 0; mask >>= 1) s += __shfl_xor_sync(0xffffffffu, s, mask);
-  return s;
 }
 
 }  // namespace lat

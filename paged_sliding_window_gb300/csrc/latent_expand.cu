@@ -4,23 +4,28 @@
 // A matrix product of gathered rows, 512 or 1024 operations per output byte:
 // bound by the tensor cores, beside writing 512 bytes per row and head.
 //
-// Schedule: the list of units (two tiles of 128 rows, a head, keys or values: 128
-// outputs of each row) is cut evenly over clusters of two CTAs, one per SM, each
-// with one of the two tiles. A CTA holds its rows in tensor memory (A of the
-// products: 128 lanes x L / 2 columns) while w streams past them in boxes of
-// 128 x 64 (warp 5, TMA; each CTA loads half of a box for both). With the rows in
-// shared memory instead, that memory's 128 bytes a cycle were the bound (a product
-// of 128 x 128 then reads as many as it takes cycles, and w's boxes, another
-// half of that, come on top): 144 us for 36k rows of 16 heads. Warp 4 issues
-// tcgen05.mma into two accumulators, warps 0-3 round, turn the rows around through
-// shared memory and write 64-byte pieces. Warps 6-9 gather rows: rows of a tile are
-// any rows of any pages, so they are copied 16 bytes at a time (asynchronously; FP8
-// codes are exact in bf16 and are converted on the way, the row's scale multiplies
-// the fp32 result) into shared memory, four chunks of the next tile ahead, and
-// moved into tensor memory chunk by chunk as the last unit of the tile before is
-// done with them. The rest of shared memory, 147 KB, is w on its way: at 64 bytes a
-// cycle a smaller ring waits for L2's latency (80 KB, with all of the next tile's
-// rows ahead: 135 us).
+// Schedule: the list of units (256 rows, a head, keys or values: 128 outputs of
+// each row) is cut evenly over pairs of CTAs, whose tensor cores share products of
+// 256 rows x 128 outputs: each CTA holds half of the rows, in tensor memory (A of
+// the products: 128 lanes x L / 2 columns), and loads half of the outputs' rows of w
+// (warp 5, TMA, boxes of 64 x 128 columns), so that a byte of w in shared memory
+// serves 256 rows. Warp 4 of the first CTA issues for both, into two accumulators;
+// the second's tells it what of w has landed there. Warps 0-3 round, turn the rows
+// around through shared memory and write 64-byte pieces. Warps 6-9 gather rows:
+// rows of a tile are any rows of any pages, so they are copied 16 bytes at a time
+// (asynchronously; FP8 codes are exact in bf16 and are converted on the way, the
+// row's scale multiplies the fp32 result) into shared memory, four chunks of 64
+// columns ahead, and moved into tensor memory chunk by chunk as the last unit of the
+// tile before is done with them.
+//
+// Measured: 40k rows of 16 heads, latent 512, 170 GFLOP: 109-111 us (1.55 PFLOP/s,
+// 79 % of the measured bf16 rate; the tensor cores are active 78 % of the time). A
+// unit takes ~2330 cycles where its 32 products of 68 cycles take 2176; 13000 cycles
+// pass before the first (20 MB are gathered at once), 3000 to 6000 from one
+// tile to the next. What was slower: rows in shared memory (144 us: that memory's
+// 128 bytes a cycle are then the bound), products of one CTA with w sent to both of a
+// pair (129), the whole of the next tile's rows ahead with a smaller ring of w
+// (115: w at 30 bytes a cycle is all that L2 gives an SM, and rows come slower still).
 #include "latent.cuh"
 
 namespace psw {

@@ -6,8 +6,7 @@
 //   s_j = softcap(scale <q, k_j>),  out = sum_j softmax(s)_j v_j,
 // with the running maximum and sum of an online softmax in fp32. 2 (192 + 128)
 // operations per (row, head, key) against 512 bytes of a key per head and
-// block of rows: bound by the tensor cores and, before them, by what L2 brings
-// to an SM, so a CTA takes 256 rows of one head against every key tile.
+// block of rows: bound by the tensor cores.
 //
 // Schedule: two row tiles, A and B, of 128 rows of a CTA, are worked on in turn:
 // while the softmax of one runs, the tensor cores work for the other (O += P V of
@@ -20,13 +19,19 @@
 //
 // A product of 128 rows by 128 keys reads as many bytes of shared memory as it
 // takes cycles at 128 a cycle, and the key tiles arrive there besides: a CTA by
-// itself is bound by its shared memory (573 us for four chunks of 2048 rows).
+// itself is bound by its shared memory (573 us for four chunks of 2048 rows after
+// 2000 to 16384, 16 heads).
 // Chunks of more than 256 rows are therefore done by pairs of CTAs, 512 rows of one
-// head, whose tensor cores share products of 256 rows: each CTA holds half of the
+// head (so are shorter ones where there are SMs to spare), whose tensor cores share products of 256 rows: each CTA holds half of the
 // keys and half of the value components of a tile, so that both the reads and the
-// arrivals halve and three stages of 128 keys fit (470 us). P is handed over in two
-// parts, so that the products begin while the rest of it is made. The longest
-// sequences come first in the grid.
+// arrivals halve and three stages of 128 keys fit. P is handed over in two parts, so
+// that the products begin while the rest of it is made. A tile pair of keys then
+// takes 2870 cycles, its products 2720. The longest sequences come first in the grid.
+//
+// Measured: those chunks, 735 GFLOP, in 470-476 us (1.55 PFLOP/s, 79 % of the measured
+// bf16 rate; 90 % of the sustained one, which the power limit sets); eight chunks
+// of 512 rows, 166 GFLOP, in 130-136 us (64 %: 128 pieces of unequal length over 76 pairs
+// of CTAs, of which the longest chains are a fifth longer than the mean).
 #include <math.h>
 
 #include "latent.cuh"
@@ -558,8 +563,13 @@ int launch_latent_prefill(const LatentArgs& L, const void* q, const int32_t* cu_
   using namespace lpre;
   CUtensorMap q_map, kv_map, rope_map;
   const int64_t h = L.n_heads;
-  // pairs of CTAs for chunks that are longer than the 256 rows of one
-  const int ctas = max_q_len > 2 * kRows ? 2 : 1;
+  // Pairs of CTAs for chunks that are longer than the 256 rows of one (8 chunks of 384
+  // rows after 4096, 16 heads: 131 us against 155), and where all pairs run at once (1 of
+  // 256 after 16384, 16 heads: 192 against 306). Otherwise a pair would have one row
+  // tile to work on and SMs would be what is short (8 of 256 after 4096, 16 heads: 115
+  // us against 100; 16 of 128: 214 against 134).
+  const bool spare = 2 * static_cast<int64_t>(n_seqs) * L.n_heads <= num_sms;
+  const int ctas = max_q_len > 2 * kRows || spare ? 2 : 1;
   const int held = ctas == 2 ? Cfg<2>::kHeld : Cfg<1>::kHeld;
   const int64_t blocks = (static_cast<int64_t>(max_q_len) + 2 * kRows * ctas - 1) / (2 * kRows * ctas);
   const int64_t grid = blocks * ctas * L.n_heads * n_seqs;

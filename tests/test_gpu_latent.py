@@ -476,6 +476,10 @@ def _run_prefill(layer, new, past, first=None, keys=None, seed=21, spare=3, q_st
     pytest.param(LatentLayer(128, scale=0.07), [33], [10], {}, id="128-heads"),
     pytest.param(LatentLayer(2, scale=2.0), [300], [500], {}, id="peaked"),
     pytest.param(LatentLayer(1, scale=0.07), [1] * 300, list(range(300)), {}, id="300-sequences"),
+    # short chunks of many heads and sequences, done by single CTAs
+    pytest.param(LatentLayer(20, scale=0.07), [128, 129, 255, 256, 1, 0], [0, 1, 95, 96, 300, 7], {}, id="single-edges"),
+    pytest.param(LatentLayer(40, scale=0.07, window=70, softcap=4.0), [200, 30], [333, 1], {}, id="single-window-softcap"),
+    pytest.param(LatentLayer(40, scale=0.07), [200, 250, 130], [0, 10, 0], dict(first=[140, 0, 0], keys=[50, 260, 0]), id="single-few-or-no-keys"),
     # chunks of more than 256 rows, done by pairs of CTAs, 512 rows each
     pytest.param(LatentLayer(3, scale=0.07), [512, 511, 257, 1, 0], [0, 129, 2048, 3000, 7], {}, id="pair-edges"),
     pytest.param(LatentLayer(2, scale=0.07), [1300, 513], [1, 700], {}, id="pair-blocks"),
@@ -499,23 +503,23 @@ def test_prefill_no_keys_at_all():
     assert bool((out == 0).all()) and bool((lse == -math.inf).all())
 
 
-@pytest.mark.parametrize("n,t", [(200, 900), (700, 1500)])
-def test_prefill_growing_scores(n, t):
+@pytest.mark.parametrize("n,t,H", [(200, 900, 2), (700, 1500, 2), (200, 900, 80)])
+def test_prefill_growing_scores(n, t, H):
     """Scores that grow along the context by far more than a running maximum may lag behind."""
-    layer = LatentLayer(2, scale=1.0)
+    layer = LatentLayer(H, scale=1.0)
     g = gen(2)
-    q = randn(g, n, 2, NOPE + R).to(BF16)
+    q = randn(g, n, H, NOPE + R).to(BF16)
     q[:, :, :] = q[:1, :1]
     d = q[0, 0].float()
     ramp = 1.5 * torch.arange(t, device="cuda")[:, None] / d.square().sum()
-    kv = 0.1 * randn(g, t, 2, NOPE + V)
+    kv = 0.1 * randn(g, t, H, NOPE + V)
     kv[:, :, :NOPE] += (ramp * d[:NOPE])[:, None]
-    kv[..., NOPE:] = randn(g, t, 2, V)
+    kv[..., NOPE:] = randn(g, t, H, V)
     kv, rope = kv.to(BF16), (ramp * d[NOPE:]).to(BF16)
-    out, lse = torch.empty(n, 2, V, dtype=BF16, device="cuda"), torch.empty(n, 2, device="cuda")
+    out, lse = torch.empty(n, H, V, dtype=BF16, device="cuda"), torch.empty(n, H, device="cuda")
     binding.attn_prefill_latent(layer, q, cu([n]), i32([t - n]), n, kv, rope, cu([t]), out, lse)
     no_error()
-    k = torch.cat([kv[..., :NOPE], rope[:, None].expand(-1, 2, -1)], -1)
+    k = torch.cat([kv[..., :NOPE], rope[:, None].expand(-1, H, -1)], -1)
     ref = attend(q.to(F64).transpose(0, 1), k.to(F64).transpose(0, 1), kv[..., NOPE:].to(F64).transpose(0, 1),
                  t - n + torch.arange(n, device="cuda"), torch.arange(t, device="cuda"), layer)
     check_attention(out.transpose(0, 1), lse.transpose(0, 1), ref, P_ERR_PREFILL, S_ERR, "growing")
