@@ -513,6 +513,9 @@ PSW_API int latent_kv_expand_fp8(const psw_latent_t *layer, const void *pool8,
  * kv and k_rope may be NULL when n_k_total is 0.
  * A row that sees no key gives zeros and lse = -inf. Rows of q beyond
  * cu_q[n_seqs] are left as they were. Needs no workspace; n_seqs <= 65535.
+ * Keys and values that no row of a block of 512 chunk rows sees may hold anything;
+ * a NaN or infinity in a value row that some of them see makes the others of that
+ * block and head NaN too (0 times it is NaN), as a masked matrix product would.
  */
 PSW_API int attn_prefill_latent(const psw_latent_t *layer, const void *q, const int32_t *cu_q,
                                 const int32_t *past_lens, int32_t n_seqs, int32_t n_q_total,

@@ -563,6 +563,7 @@ int launch_latent_prefill(const LatentArgs& L, const void* q, const int32_t* cu_
   using namespace lpre;
   CUtensorMap q_map, kv_map, rope_map;
   const int64_t h = L.n_heads;
+  max_q_len = min(max_q_len, n_q_total);  // (no chunk within the rows is longer)
   // Pairs of CTAs for chunks that are longer than the 256 rows of one (8 chunks of 384
   // rows after 4096, 16 heads: 131 us against 155), and where all pairs run at once (1 of
   // 256 after 16384, 16 heads: 192 against 306). Otherwise a pair would have one row
