@@ -27,6 +27,8 @@
 // arrivals halve and three stages of 128 keys fit. P is handed over in two parts, so
 // that the products begin while the rest of it is made. A tile pair of keys then
 // takes 2870 cycles, its products 2720. The longest sequences come first in the grid.
+// Where a pair has 256 rows or fewer, A and B are the same rows and take key tiles in
+// turn; their threads join O and the sums at the end.
 //
 // Measured: those chunks, 735 GFLOP, in 470-476 us (1.55 PFLOP/s, 79 % of the measured
 // bf16 rate; 90 % of the sustained one, which the power limit sets); eight chunks
@@ -50,6 +52,7 @@ constexpr int kTmemS = 0, kTmemO = 256;       // + 128 for B
 constexpr float kLag = 64.f;
 constexpr int kRanked = 256;                  // sequences put in order by their length
 constexpr int kMaxStages = 3;
+constexpr int kMisc = 4096;
 constexpr int kHead = 64;                     // keys whose P is handed over first
 
 template <int CTAS>
@@ -62,7 +65,7 @@ struct Cfg {
   static constexpr int kValueUnits = 2 / CTAS;               // 64 components each
   static constexpr int kValueUnit = kKeys * 128;
   static constexpr int kValueBytes = kValueUnits * kValueUnit;
-  static constexpr int kSmemBytes = 1024 + kQBytes + kStages * (kKeyBytes + kValueBytes) + 2048;
+  static constexpr int kSmemBytes = 1024 + kQBytes + kStages * (kKeyBytes + kValueBytes) + kMisc;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 };
 
@@ -77,8 +80,9 @@ struct Misc {
   uint32_t tmem;
   int32_t abort, seq;
   int32_t len[kRanked];
+  float2 ml[2][kRows];   // split: maximum and sum of each row over A's and over B's tiles
 };
-static_assert(sizeof(Misc) <= 2048, "misc block");
+static_assert(sizeof(Misc) <= kMisc, "misc block");
 
 // A sequence's rows and keys, and what a block of rows has of them; the same in
 // every thread.
@@ -91,13 +95,20 @@ struct Work {
   int t_lo, t_hi;       // of both
   int j_lo, j_hi;       // keys [j_lo, j_hi) that some row sees
 };
-// Of the rows from i0 on, `tile` in each of A and B, and key tiles of `keys`.
-__device__ __forceinline__ Work work_of(const Seq& q, int i0, int tile, int keys, int window) {
+// Of the rows from i0 on, `tile` in each of A and B, and key tiles of `keys`. Split:
+// the same rows in both, every second key tile from lo on.
+__device__ __forceinline__ Work work_of(const Seq& q, int i0, int tile, int keys, int window,
+                                        bool split) {
   Work w;
   w.t_lo = w.j_lo = 0x7fffffff;
   w.t_hi = w.j_hi = 0;
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
+    if (g == 1 && split) {
+      w.lo[1] = w.lo[0] + 1;
+      w.hi[1] = w.hi[0];
+      break;
+    }
     const int n = min(tile, q.nq - i0 - g * tile);
     // keys of the tile's rows: from the window of its first to its last
     const int64_t a = q.past + i0 + g * tile - q.first;
@@ -122,7 +133,7 @@ __device__ __forceinline__ float tanh_abs(float y) {
   return copysignf(__fdividef(1.f - t, 1.f + t), y);
 }
 
-template <int CTAS>
+template <int CTAS, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
                       const __grid_constant__ CUtensorMap kv_map,
@@ -223,8 +234,10 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
     }
     if (bad && tid == 0 && block == 0 && head == 0) flag_error(err, PSW_DEVERR_LENGTH);
   }
-  const Work w = work_of(sq, i0, kTile, kKeys, window);
-  const int my_row = i0 + peer * kRows;  // first row of this CTA's part of A; B's is kTile on
+  const Work w = work_of(sq, i0, kTile, kKeys, window, SPLIT);
+  const int my_row = i0 + peer * kRows;      // first row of this CTA's part of A
+  constexpr int b_rows = SPLIT ? 0 : kTile;  // and how much further B's is
+  constexpr int step = SPLIT ? 2 : 1;        // from a key tile of A (or B) to the next
   bool ok = true;
 
   if (sq.nq <= i0) {
@@ -239,7 +252,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
         mbar_arrive_expect_tx(&ms->q_full[g], kQChunks * kQUnit);
         for (int c = 0; c < kQChunks; ++c)
           lat::tma_box(smem_u32(q_smem + (g * kQChunks + c) * kQUnit), &q_map, &ms->q_full[g],
-                       c * 64, head, sq.q0 + my_row + g * kTile);
+                       c * 64, head, sq.q0 + my_row + g * b_rows);
       }
     }
     uint32_t fixes = 0;  // phases of v_fix
@@ -364,6 +377,9 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
     // the k-th key tile has landed, the k-th value tile has
     auto keys = [&](int k) { wait(&ms->k_full[k % kStages], k / kStages); };
     auto values = [&](int k) { wait(&ms->v_full[k % kStages], k / kStages); };
+    auto has = [&](int g, int j) {
+      return j >= w.lo[g] && j < w.hi[g] && (!SPLIT || ((j ^ w.lo[g]) & 1) == 0);
+    };
     if (w.t_lo < w.t_hi) {
       keys(0);
 #pragma unroll
@@ -371,13 +387,16 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
         if (w.lo[g] == w.t_lo && w.lo[g] < w.hi[g]) scores(g, 0);
       if (ok && one) commit(&ms->freed[0]);
       values(0);
-      if (w.t_lo + 1 < w.t_hi) keys(1);
+      if (w.t_lo + 1 < w.t_hi) {
+        keys(1);
+        if (SPLIT) scores(1, 1);
+      }
     }
     for (int j = w.t_lo, k = 0; ok && j < w.t_hi; ++j, ++k) {
       const int st = k % kStages;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        if (j >= w.lo[g] && j < w.hi[g]) {
+        if (has(g, j)) {
           const uint64_t vd = v_desc + st * (C::kValueBytes >> 4);
           auto product = [&](int e) {
             const uint32_t d = tmem + kTmemO + g * kLatentV, a = tmem + kTmemS + g * 128 + e * 8;
@@ -396,10 +415,17 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
           if (ok && one) {
 #pragma unroll
             for (int e = kHead / 16; e < kKeys / 16; ++e) product(e);
-            if (j == w.hi[g] - 1) commit(&ms->o_full[g]);
+            if (j + step >= w.hi[g]) commit(&ms->o_full[g]);
           }
         }
-        if (j + 1 >= w.lo[g] && j + 1 < w.hi[g]) scores(g, k + 1);
+        if (SPLIT) {
+          if (has(g, j) && j + 2 < w.hi[g]) {
+            keys(k + 2);
+            scores(g, k + 2);
+          }
+        } else if (has(g, j + 1)) {
+          scores(g, k + 1);
+        }
         if (g == 0) {  // what the next round needs, while B's softmax runs
           if (j + 1 < w.t_hi) values(k + 1);
           if (j + 2 < w.t_hi) keys(k + 2);
@@ -418,7 +444,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax, epilogue
-    const int g = warp >> 2, r = (warp & 3) * 32 + lane, i = my_row + g * kTile + r;
+    const int g = warp >> 2, r = (warp & 3) * 32 + lane, i = my_row + g * b_rows + r;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + kTmemS + g * 128;
     const uint32_t o_at = tmem + lanes + kTmemO + g * kLatentV;
@@ -429,7 +455,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
     float m = -INFINITY, l = 0.f;
     int n = 0;
     const int g_lo = g == 0 ? w.lo[0] : w.lo[1], g_hi = g == 0 ? w.hi[0] : w.hi[1];
-    for (int j = g_lo; j < g_hi; ++j, ++n) {
+    for (int j = g_lo; j < g_hi; j += step, ++n) {
       // (every decision is the same in the whole warp)
       ok = __all_sync(0xffffffffu, mbar_wait(&ms->s_full[g], n & 1) && *abort_flag == 0);
       if (!ok) break;
@@ -515,12 +541,50 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
       l += (sums0.x + sums0.y) + (sums1.x + sums1.y);
     }
     if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&ms->o_full[g], 0));
-    if (ok) {
+    const int64_t row = static_cast<int64_t>(sq.q0 + i) * heads + head;
+    uint4* dst = reinterpret_cast<uint4*>(out + row * kLatentV);
+    const bool mine = i < sq.nq;
+    if constexpr (SPLIT) {
+      // A's threads and B's have the same rows, each the sums over its own key tiles;
+      // they join them, 64 components each (a lane's O is there for both)
+      const bool other = g == 0 ? w.lo[1] < w.hi[1] : w.lo[0] < w.hi[0];
+      ms->ml[g][r] = make_float2(m, l);
+      named_bar_sync(1, 256);
+      const float2 o = ms->ml[1 - g][r];
+      const float top = fmaxf(m, o.x);
+      float f = m == -INFINITY ? 0.f : ex2_approx(m - top);
+      float f_other = o.x == -INFINITY ? 0.f : ex2_approx(o.x - top);
+      l = l * f + o.y * f_other;
+      m = top;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      f *= inv;
+      f_other *= inv;
+      if (ok && other) ok = __all_sync(0xffffffffu, mbar_wait(&ms->o_full[1 - g], 0));
+      if (ok) {
+        tc::fence_after();
+        const uint32_t o_other = tmem + lanes + kTmemO + (1 - g) * kLatentV;
+#pragma unroll 1
+        for (int c = 2 * g; c < 2 * g + 2; ++c) {
+          uint32_t v[32], u[32];
+          if (n > 0) tc::ld32(o_at + c * 32, v);
+          if (other) tc::ld32(o_other + c * 32, u);
+          tc::wait_ld();
+          if (!mine) continue;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float y[8];
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+              y[d] = f == 0.f ? 0.f : __uint_as_float(v[e * 8 + d]) * f;
+              if (f_other != 0.f) y[d] = fmaf(__uint_as_float(u[e * 8 + d]), f_other, y[d]);
+            }
+            dst[c * 4 + e] = lat::pack8(y);
+          }
+        }
+      }
+    } else if (ok) {
       tc::fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int64_t row = static_cast<int64_t>(sq.q0 + i) * heads + head;
-      uint4* dst = reinterpret_cast<uint4*>(out + row * kLatentV);
-      const bool mine = i < sq.nq;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t v[32];
@@ -537,7 +601,10 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
           dst[c * 4 + e] = lat::pack8(y);
         }
       }
-      if (mine && lse != nullptr) lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * lat::kLn2;
+    }
+    if (ok) {
+      if (mine && lse != nullptr && (g == 0 || !SPLIT))
+        lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * lat::kLn2;
     } else if (lane == 0) {
       *abort_flag = 1;
       flag_error(err, PSW_DEVERR_PIPELINE);
@@ -565,12 +632,15 @@ int launch_latent_prefill(const LatentArgs& L, const void* q, const int32_t* cu_
   const int64_t h = L.n_heads;
   max_q_len = min(max_q_len, n_q_total);  // (no chunk within the rows is longer)
   // Pairs of CTAs for chunks that are longer than the 256 rows of one (8 chunks of 384
-  // rows after 4096, 16 heads: 131 us against 155), and where all pairs run at once (1 of
-  // 256 after 16384, 16 heads: 192 against 306). Otherwise a pair would have one row
-  // tile to work on and SMs would be what is short (8 of 256 after 4096, 16 heads: 115
-  // us against 100; 16 of 128: 214 against 134).
+  // rows after 4096, 16 heads: 131 us against 155), and where all pairs run at once:
+  // shorter ones then have their keys split between A and B (1 of 256 after 8192, 76
+  // heads: 84 us against 173; 4 of 128 after 8192, 16 heads: 79 against 111). With more
+  // work than that SMs are what is short (16 of 128 after 4096, 16 heads: 173 against
+  // 134). Single CTAs do not split: their two stages hold no tile ahead of the two in
+  // use (the same: 180).
   const bool spare = 2 * static_cast<int64_t>(n_seqs) * L.n_heads <= num_sms;
   const int ctas = max_q_len > 2 * kRows || spare ? 2 : 1;
+  const bool split = ctas == 2 && max_q_len <= kRows * ctas;
   const int held = ctas == 2 ? Cfg<2>::kHeld : Cfg<1>::kHeld;
   const int64_t blocks = (static_cast<int64_t>(max_q_len) + 2 * kRows * ctas - 1) / (2 * kRows * ctas);
   const int64_t grid = blocks * ctas * L.n_heads * n_seqs;
@@ -587,7 +657,9 @@ int launch_latent_prefill(const LatentArgs& L, const void* q, const int32_t* cu_
   } else {
     kv_map = rope_map = q_map;  // no key tile will be loaded
   }
-  auto* kernel = ctas == 2 ? latent_prefill_kernel<2> : latent_prefill_kernel<1>;
+  auto* kernel = split       ? latent_prefill_kernel<2, true>
+                 : ctas == 2 ? latent_prefill_kernel<2, false>
+                             : latent_prefill_kernel<1, false>;
   const int smem = ctas == 2 ? Cfg<2>::kSmemBytes : Cfg<1>::kSmemBytes;
   rc = set_smem_limit(reinterpret_cast<const void*>(kernel), smem);
   if (rc != PSW_OK) return rc;

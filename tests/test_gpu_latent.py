@@ -480,6 +480,12 @@ def _run_prefill(layer, new, past, first=None, keys=None, seed=21, spare=3, q_st
     pytest.param(LatentLayer(20, scale=0.07), [128, 129, 255, 256, 1, 0], [0, 1, 95, 96, 300, 7], {}, id="single-edges"),
     pytest.param(LatentLayer(40, scale=0.07, window=70, softcap=4.0), [200, 30], [333, 1], {}, id="single-window-softcap"),
     pytest.param(LatentLayer(40, scale=0.07), [200, 250, 130], [0, 10, 0], dict(first=[140, 0, 0], keys=[50, 260, 0]), id="single-few-or-no-keys"),
+    # keys split between the two halves of a CTA
+    pytest.param(LatentLayer(20, scale=0.07), [128, 127, 1, 0, 50], [0, 97, 95, 0, 1000], {}, id="split-edges"),
+    pytest.param(LatentLayer(40, scale=0.07, window=200, softcap=4.0), [100, 30], [633, 1], {}, id="split-window-softcap"),
+    pytest.param(LatentLayer(40, scale=0.07), [100, 120, 30], [0, 10, 0], dict(first=[60, 0, 0], keys=[30, 130, 0]), id="split-few-or-no-keys"),
+    pytest.param(LatentLayer(4, scale=0.07), [256, 1, 129], [0, 128, 383], {}, id="pair-split-edges"),
+    pytest.param(LatentLayer(3, scale=0.07, window=300), [200, 256], [1333, 1], {}, id="pair-split-window"),
     # chunks of more than 256 rows, done by pairs of CTAs, 512 rows each
     pytest.param(LatentLayer(3, scale=0.07), [512, 511, 257, 1, 0], [0, 129, 2048, 3000, 7], {}, id="pair-edges"),
     pytest.param(LatentLayer(2, scale=0.07), [1300, 513], [1, 700], {}, id="pair-blocks"),
@@ -503,7 +509,7 @@ def test_prefill_no_keys_at_all():
     assert bool((out == 0).all()) and bool((lse == -math.inf).all())
 
 
-@pytest.mark.parametrize("n,t,H", [(200, 900, 2), (700, 1500, 2), (200, 900, 80)])
+@pytest.mark.parametrize("n,t,H", [(200, 900, 2), (700, 1500, 2), (200, 900, 80), (100, 900, 80)])
 def test_prefill_growing_scores(n, t, H):
     """Scores that grow along the context by far more than a running maximum may lag behind."""
     layer = LatentLayer(H, scale=1.0)
