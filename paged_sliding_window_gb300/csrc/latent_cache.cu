@@ -10,10 +10,15 @@
 //
 // The step is bound by memory on a chunk and by its chain of dependent loads
 // (offsets, then the table entry) on a decode batch. A warp's unit is a
-// token's cache row or eight of its query heads, so that a decode batch
-// spreads over many SMs, and the row's own loads are issued before the chain
-// starts. The 32 angles of a token sit one per lane; the query lanes, which
+// token's cache row or eight (of many: sixteen) of its query heads, so that a
+// decode batch spreads over many SMs, and the unit's own loads are issued before
+// the chain starts. The 32 angles of a token sit one per lane; the query lanes, which
 // hold 8 + 8 values each for 16-byte accesses, fetch theirs by shuffles.
+//
+// Measured (latent 512, in a graph): 64 tokens of 16 heads 3.9 us; 4096 tokens 6.9
+// us, 26 MB read and written (3.8 TB/s); 6900 tokens of 32 heads into FP8 pages
+// 16.0 us, 66 MB (4.1 TB/s, 61 % of the measured copy rate). What is left is the
+// wait for the loads: the registers of 32 warps are what an SM has in flight.
 #include <math.h>
 
 #include "latent.cuh"
@@ -22,7 +27,8 @@ namespace psw {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kHeadsPerUnit = 8;
+constexpr int kGroup = 8;  // query heads that a warp turns at once
+constexpr int kCtas = 8;   // per SM
 
 struct Freqs {
   double f[kLatentRope / 2];   // theta^(-i / 32), for positions from 2^24 on
@@ -75,8 +81,8 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
   return lat::e4m3_pair(a * k, b * k) | lat::e4m3_pair(c * k, d * k) << 16;
 }
 
-template <int LAT, bool FP8>
-__global__ void __launch_bounds__(kWarps * 32)
+template <int LAT, bool FP8, int GROUPS>
+__global__ void __launch_bounds__(kWarps * 32, kCtas)
 latent_write_kernel(const __grid_constant__ Freqs freqs, const float* __restrict__ weight,
                     float eps, const __nv_bfloat16* __restrict__ ckv, int64_t ckv_stride,
                     const LatentRows q, int heads, const int32_t* __restrict__ cu_new,
@@ -84,6 +90,7 @@ latent_write_kernel(const __grid_constant__ Freqs freqs, const float* __restrict
                     const int32_t* __restrict__ block_table, int max_blocks, int64_t num_blocks,
                     void* __restrict__ pool, float* __restrict__ row_scale, int32_t* err) {
   constexpr int kRow = LAT + kLatentRope, kVecs = LAT / 256, kHalf = kLatentRope / 2;
+  constexpr int kUnitHeads = kGroup * GROUPS;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __shared__ float2 s_f2[kHalf];
   if (threadIdx.x < kHalf) s_f2[threadIdx.x] = freqs.f2[threadIdx.x];
@@ -91,28 +98,31 @@ latent_write_kernel(const __grid_constant__ Freqs freqs, const float* __restrict
   const int named = __ldg(cu_new + n_seqs), total = min(named, n_new_total);
   if (named > n_new_total && blockIdx.x == 0 && threadIdx.x == 0)
     flag_error(err, PSW_DEVERR_LENGTH);
-  const int per_token = 1 + (q.in != nullptr ? (heads + kHeadsPerUnit - 1) / kHeadsPerUnit : 0);
+  const int per_token = 1 + (q.in != nullptr ? (heads + kUnitHeads - 1) / kUnitHeads : 0);
   const int64_t units = static_cast<int64_t>(total) * per_token;
   // unit u on CTA u mod grid: the few units of a decode batch meet every SM
   for (int64_t u = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x; u < units;
        u += static_cast<int64_t>(kWarps) * gridDim.x) {
     const int t = static_cast<int>(u / per_token), part = static_cast<int>(u - static_cast<int64_t>(t) * per_token);
     // this unit's values
-    uint4 v[2];
+    uint4 v[GROUPS][2];
     float r0 = 0.f, r1 = 0.f;
-    const int head = (part - 1) * kHeadsPerUnit + (lane >> 2);
-    const bool has = part == 0 || head < heads;
+    const int head = (part - 1) * kUnitHeads + (lane >> 2);  // of the first group
     if (part == 0) {
       const __nv_bfloat16* src = ckv + t * ckv_stride;
 #pragma unroll
-      for (int c = 0; c < kVecs; ++c) v[c] = __ldg(reinterpret_cast<const uint4*>(src + c * 256) + lane);
+      for (int c = 0; c < kVecs; ++c) v[0][c] = __ldg(reinterpret_cast<const uint4*>(src + c * 256) + lane);
       r0 = __bfloat162float(src[LAT + lane]);
       r1 = __bfloat162float(src[LAT + kHalf + lane]);
-    } else if (has) {
+    } else {
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(q.in) + t * q.in_token +
                                  head * q.in_head + (lane & 3) * 8;
-      v[0] = *reinterpret_cast<const uint4*>(src);
-      v[1] = *reinterpret_cast<const uint4*>(src + kHalf);
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) {
+        if (head + g * kGroup >= heads) break;
+        v[g][0] = *reinterpret_cast<const uint4*>(src + g * kGroup * q.in_head);
+        v[g][1] = *reinterpret_cast<const uint4*>(src + g * kGroup * q.in_head + kHalf);
+      }
     }
     int b, start;
     if (!lat::owner_of(cu_new, n_seqs, t, lane, b, start)) {
@@ -143,28 +153,34 @@ latent_write_kernel(const __grid_constant__ Freqs freqs, const float* __restrict
     float cs, sn;
     turn_of(pos, s_f2[lane], freqs.f[lane], cs, sn);
     if (part > 0) {
-      float lo[8], hi[8], olo[8], ohi[8];
-      lat::unpack8(v[0], lo);
-      lat::unpack8(v[1], hi);
+      float c[8], sine[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float c = __shfl_sync(0xffffffffu, cs, (lane & 3) * 8 + e);
-        const float s = __shfl_sync(0xffffffffu, sn, (lane & 3) * 8 + e);
-        olo[e] = fmaf(lo[e], c, -(hi[e] * s));
-        ohi[e] = fmaf(hi[e], c, lo[e] * s);
+        c[e] = __shfl_sync(0xffffffffu, cs, (lane & 3) * 8 + e);
+        sine[e] = __shfl_sync(0xffffffffu, sn, (lane & 3) * 8 + e);
       }
-      if (has) {
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(q.out) + t * q.out_token +
-                             head * q.out_head + (lane & 3) * 8;
-        *reinterpret_cast<uint4*>(dst) = lat::pack8(olo);
-        *reinterpret_cast<uint4*>(dst + kHalf) = lat::pack8(ohi);
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(q.out) + t * q.out_token +
+                           head * q.out_head + (lane & 3) * 8;
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) {
+        if (head + g * kGroup >= heads) break;
+        float lo[8], hi[8], olo[8], ohi[8];
+        lat::unpack8(v[g][0], lo);
+        lat::unpack8(v[g][1], hi);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          olo[e] = fmaf(lo[e], c[e], -(hi[e] * sine[e]));
+          ohi[e] = fmaf(hi[e], c[e], lo[e] * sine[e]);
+        }
+        *reinterpret_cast<uint4*>(dst + g * kGroup * q.out_head) = lat::pack8(olo);
+        *reinterpret_cast<uint4*>(dst + g * kGroup * q.out_head + kHalf) = lat::pack8(ohi);
       }
       continue;
     }
     float y[kVecs][8], ss = 0.f;
 #pragma unroll
     for (int c = 0; c < kVecs; ++c) {
-      lat::unpack8(v[c], y[c]);
+      lat::unpack8(v[0][c], y[c]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(y[c][e], y[c][e], ss);
     }
@@ -219,8 +235,7 @@ int launch_latent_write(const LatentArgs& L, float theta, float eps, const float
                         const void* ckv, int64_t ckv_stride, const LatentRows& q,
                         const int32_t* cu_new, const int32_t* past_lens, int n_seqs,
                         int n_new_total, const LatentPages& pages, void* pool, float* row_scale,
-                        int num_sms,
-                        int32_t* err, cudaStream_t stream) {
+                        int num_sms, int32_t* err, cudaStream_t stream) {
   Freqs fr;
   const double log_theta = log(static_cast<double>(theta));
   for (int i = 0; i < kLatentRope / 2; ++i) {
@@ -228,19 +243,34 @@ int launch_latent_write(const LatentArgs& L, float theta, float eps, const float
     const float hi = static_cast<float>(fr.f[i]);
     fr.f2[i] = make_float2(hi, static_cast<float>(fr.f[i] - static_cast<double>(hi)));
   }
-  const int grid = num_sms * 8;
+  // Two groups of heads to a unit (twice the bytes in flight, the angles once) where
+  // all warps have two units or more: 7.5 -> 6.9 us for 4096 tokens of 16 heads, 18.7
+  // -> 16.0 for 6900 of 32. Four (at any number of CTAs): 7.1 and 15.6 at best.
+  // Fewer units are spread over as many warps as there are.
+  const int64_t units = static_cast<int64_t>(n_new_total) * (1 + (L.n_heads + kGroup - 1) / kGroup);
+  const int grid = num_sms * kCtas;
+  const bool many = q.in != nullptr && L.n_heads > kGroup &&
+                    units > 2 * static_cast<int64_t>(grid) * kWarps;
   const auto* x = static_cast<const __nv_bfloat16*>(ckv);
-#define PSW_LAUNCH(LAT_, FP8_)                                                                  \
-  latent_write_kernel<LAT_, FP8_><<<grid, kWarps * 32, 0, stream>>>(                            \
+#define PSW_LAUNCH(LAT_, FP8_, G_)                                                              \
+  latent_write_kernel<LAT_, FP8_, G_><<<grid, kWarps * 32, 0, stream>>>(                        \
       fr, weight, eps, x, ckv_stride, q, L.n_heads, cu_new, past_lens, n_seqs, n_new_total,     \
       pages.block_table, pages.max_blocks, pages.num_blocks, pool, row_scale, err)
+#define PSW_PICK(LAT_, FP8_)     \
+  do {                           \
+    if (many)                    \
+      PSW_LAUNCH(LAT_, FP8_, 2); \
+    else                         \
+      PSW_LAUNCH(LAT_, FP8_, 1); \
+  } while (0)
   if (L.latent == 512) {
-    if (row_scale != nullptr) PSW_LAUNCH(512, true);
-    else PSW_LAUNCH(512, false);
+    if (row_scale != nullptr) PSW_PICK(512, true);
+    else PSW_PICK(512, false);
   } else {
-    if (row_scale != nullptr) PSW_LAUNCH(256, true);
-    else PSW_LAUNCH(256, false);
+    if (row_scale != nullptr) PSW_PICK(256, true);
+    else PSW_PICK(256, false);
   }
+#undef PSW_PICK
 #undef PSW_LAUNCH
   return cudaGetLastError() == cudaSuccess ? PSW_OK : PSW_ELAUNCH;
 }

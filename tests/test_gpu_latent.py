@@ -86,6 +86,9 @@ def _write(L, H, new, past, fp8, weight=True, stride=0, q=True, in_place=False, 
     pytest.param(512, 5, [40], [60000], dict(in_place=True), id="in-place"),
     pytest.param(256, 4, [21], [3], dict(q=False), id="cache-only"),
     pytest.param(512, 2, [0, 1] * 600, [5] * 1200, {}, id="1200-sequences"),
+    # more than 9728 units: sixteen heads to a warp, the last unit of a token short
+    pytest.param(256, 20, [2500, 1, 700], [3, 90, 16], dict(stride=8), id="many-units"),
+    pytest.param(512, 33, [1700], [0], dict(in_place=True), id="many-units-in-place"),
 ])
 def test_write(L, H, new, past, kw, fp8):
     if past[0] > 1 << 20:  # a table for far positions would be a gigabyte: share one page
