@@ -131,6 +131,40 @@ __device__ __forceinline__ void arrive_at_first(uint64_t* bar) {
       : "memory");
 }
 
+// ---- work of clusters of the grid that have not started: asks for one of them (the
+// answer, 16 bytes, comes to `dst`, in a pair to both CTAs, and is counted on `bar`
+// there), and reads the answer: its first CTA's index, or -1 if none is left, after
+// which no other may be asked for.
+template <bool PAIR>
+__device__ __forceinline__ void ask_for_work(void* dst, uint64_t* bar) {
+  if (PAIR)
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+        ".multicast::cluster::all.b128 [%0], [%1];" ::"r"(smem_u32(dst)),
+        "r"(smem_u32(bar))
+        : "memory");
+  else
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+        " [%0], [%1];" ::"r"(smem_u32(dst)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ int work_given(const void* src) {
+  uint32_t given, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t"
+      "ld.shared.b128 a, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+      : "=r"(given), "=r"(x)
+      : "r"(smem_u32(src))
+      : "memory");
+  return given != 0 ? static_cast<int>(x) : -1;
+}
+
 // Plain copy of `bytes` (a multiple of 16; both addresses 16-byte aligned) into
 // shared memory, counted on `bar`. (A tensor copy's destination would have to be
 // 128-byte aligned.)
