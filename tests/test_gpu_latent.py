@@ -483,6 +483,13 @@ def _run_prefill(layer, new, past, first=None, keys=None, seed=21, spare=3, q_st
     pytest.param(LatentLayer(20, scale=0.07), [128, 129, 255, 256, 1, 0], [0, 1, 95, 96, 300, 7], {}, id="single-edges"),
     pytest.param(LatentLayer(40, scale=0.07, window=70, softcap=4.0), [200, 30], [333, 1], {}, id="single-window-softcap"),
     pytest.param(LatentLayer(40, scale=0.07), [200, 250, 130], [0, 10, 0], dict(first=[140, 0, 0], keys=[50, 260, 0]), id="single-few-or-no-keys"),
+    # more pieces than CTAs: those take several, some of them without rows or keys
+    pytest.param(LatentLayer(16, scale=0.07), [37 * i % 200 for i in range(40)], [113 * i % 700 for i in range(40)], {}, id="single-many"),
+    pytest.param(LatentLayer(8, scale=0.07, window=50), [i % 5 for i in range(300)], [7 * i for i in range(300)],
+                 dict(first=[max(0, 7 * i - 60) for i in range(300)]), id="single-many-short"),
+    pytest.param(LatentLayer(24, scale=0.07, window=200), [0, 300, 1, 900, 600, 257], [5, 0, 900, 130, 1, 300], {}, id="pair-many"),
+    pytest.param(LatentLayer(20, scale=0.07, softcap=20.0), [300, 520, 0, 40, 700, 1], [0, 10, 3, 0, 5, 0],
+                 dict(keys=[0, 130, 0, 40, 1, 0]), id="pair-many-few-keys"),
     # keys split between the two halves of a CTA
     pytest.param(LatentLayer(20, scale=0.07), [128, 127, 1, 0, 50], [0, 97, 95, 0, 1000], {}, id="split-edges"),
     pytest.param(LatentLayer(40, scale=0.07, window=200, softcap=4.0), [100, 30], [633, 1], {}, id="split-window-softcap"),
