@@ -40,7 +40,7 @@ constexpr int kRowThreads = 128;                // warps 6-9
 constexpr int kThreads = 320;
 constexpr int kAcc = 2;                         // accumulators of 128 columns
 constexpr int kStage = 4 * 32 * 64;             // epilogue: 32 rows x 64 B per warp
-constexpr int kMisc = 3072;
+constexpr int kMisc = 4096;
 constexpr int kAhead = 4;                       // chunks of rows in shared memory
 constexpr int kCluster = 2;
 constexpr int kMaxRing = 9;
