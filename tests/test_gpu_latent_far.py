@@ -77,7 +77,8 @@ def test_far_expansion():
     assert torch.equal(kv[-last:], a) and torch.equal(rope[-last:], b)
 
 
-@pytest.mark.parametrize("H,new", [(4, [150, 33]), (48, [90, 200]), (4, [600, 20])], ids=["spare-pairs", "singles", "pairs"])
+@pytest.mark.parametrize("H,new", [(4, [150, 33]), (48, [90, 200]), (4, [600, 20]), (48, [600, 300, 513]), (64, [90] * 12)],
+                         ids=["spare-pairs", "singles", "pairs", "many-pairs", "many-singles"])
 def test_chain_captured(H, new):
     """Write, expansion, chunk attention and decode in one graph, replayed with other inputs, and
     on two streams at once; each gives what the calls give one by one."""
