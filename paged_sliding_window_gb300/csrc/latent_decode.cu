@@ -240,7 +240,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                      int n_seqs, int heads, int window, float scale, float softcap,
                      __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
                      Part* __restrict__ parts, float2* __restrict__ part_ml,
-                     float* __restrict__ part_o, int32_t* err) {
+                     float* __restrict__ part_o, int32_t* err, int stall_cta, int stall_tile) {
   using C = Cfg<LAT, NH, FP8>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kSoftThreads = C::kSoftThreads, kScoreWarp = C::kScoreWarp;
@@ -462,10 +462,15 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     const bool one = lat::elect_one();
     uint32_t issued = 0;  // slots whose last load may be in flight, for the drain
     int tile = 0;
-    while (ok && walk.next()) {
+    bool stalled = false;  // testing hook: tile stall_tile of this CTA is never asked for
+    while (ok && !stalled && walk.next()) {
       const int n_tiles = walk.tiles();
       int ids = block_id(lane), next_ids = block_id(32 + lane);
       for (int t = 0; ok && t < n_tiles; ++t, ++tile) {
+        if (static_cast<int>(blockIdx.x) == stall_cta && tile == stall_tile) {
+          stalled = true;  // leave quietly: the waits for it must run out
+          break;
+        }
         if (t > 0 && t % kGroup == 0) {
           ids = next_ids;
           next_ids = block_id((t / kGroup + 1) * 32 + lane);
@@ -509,9 +514,11 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
       }
     }
-    if (!ok && one) {
-      *abort_flag = 1;
-      flag_error(err, PSW_DEVERR_PIPELINE);
+    if ((!ok || stalled) && one) {
+      if (!ok) {
+        *abort_flag = 1;
+        flag_error(err, PSW_DEVERR_PIPELINE);
+      }
       // copies in flight land before the CTA ends: the last phase of each slot
       for (int s = 0; s < C::kSlots; ++s)
         if (issued >> s & 1u) mbar_wait(&ms->full[s], ((rg.phase >> s) & 1u) ^ 1u);
@@ -936,14 +943,16 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 // dims each, takes every groups-th piece, and the groups' sums meet in shared
 // memory. The kernel is a chain of three loads (lengths, which pieces, then
 // statistics and the first eight pieces together). A unit that one piece covered
-// is left alone, an empty sequence gets its zeros.
+// is left alone, an empty sequence gets its zeros. Where a wait of the first kernel
+// ran out, what it should have noted was not: the workspace may hold anything there, so
+// pieces that the first kernel does not have are flagged and their unit is left alone.
 constexpr int kMergeThreads = 512;
 template <int LAT>
 __global__ void __launch_bounds__(kMergeThreads)
-latent_merge_kernel(const int32_t* __restrict__ seq_lens, int heads,
+latent_merge_kernel(const int32_t* __restrict__ seq_lens, int heads, int max_pieces,
                     const Part* __restrict__ parts, const float2* __restrict__ part_ml,
                     const float* __restrict__ part_o, __nv_bfloat16* __restrict__ out,
-                    float* __restrict__ lse) {
+                    float* __restrict__ lse, int32_t* err) {
   constexpr int kRow = LAT / 4;  // threads of a group
   __shared__ float s_w[kMergeThreads / 32][kMaxCtas];
   __shared__ float4 s_o[kMergeThreads];
@@ -962,7 +971,11 @@ latent_merge_kernel(const int32_t* __restrict__ seq_lens, int heads,
     return;
   }
   if (pt.x < 0) return;
-  const int n = pt.y - pt.x + 1;
+  if (pt.y < pt.x || pt.y >= max_pieces) {
+    if (tid == 0) flag_error(err, PSW_DEVERR_PIPELINE);
+    return;
+  }
+  const int n = pt.y - pt.x + 1;  // at most max_pieces, which is at most kMaxCtas
   auto slot = [&](int i) { return i == 0 ? 2 * pt.x + 1 : 2 * (pt.x + i); };
   auto piece = [&](int i) -> float4 {
     return i < n ? __ldcg(reinterpret_cast<const float4*>(
@@ -1073,9 +1086,11 @@ int launch(const LatentArgs& L, const void* q, const LatentPages& pages, const i
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  const StallHook stall = stall_hook(kStallDecode);
   if (cudaLaunchKernelEx(&cfg, kernel, q_map, pool_map, pages,
                          static_cast<const __nv_bfloat16*>(q), seq_lens, n_seqs, L.n_heads,
-                         L.window, L.scale, L.softcap, ob, lse, parts, ml, o, err) != cudaSuccess)
+                         L.window, L.scale, L.softcap, ob, lse, parts, ml, o, err, stall.cta,
+                         stall.tile) != cudaSuccess)
     return PSW_ELAUNCH;
   cfg.gridDim = dim3(n_seqs, L.n_heads);
   cfg.dynamicSmemBytes = 0;
@@ -1086,9 +1101,9 @@ int launch(const LatentArgs& L, const void* q, const LatentPages& pages, const i
   const int fit = kMergeThreads / row_threads;
   cfg.blockDim = dim3(row_threads * (want < fit ? want : fit));
   const cudaError_t e = cudaLaunchKernelEx(
-      &cfg, latent_merge_kernel<LAT>, seq_lens, L.n_heads,
+      &cfg, latent_merge_kernel<LAT>, seq_lens, L.n_heads, grid,
       static_cast<const Part*>(parts), static_cast<const float2*>(ml),
-      static_cast<const float*>(o), ob, lse);
+      static_cast<const float*>(o), ob, lse, err);
   return e == cudaSuccess ? PSW_OK : PSW_ELAUNCH;
 }
 
