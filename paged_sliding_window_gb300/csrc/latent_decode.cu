@@ -179,7 +179,7 @@ struct Walk {
   int seg_first, seg_count;  // pages of the segment, relative to the span's first
   __device__ __forceinline__ bool next() {
     while (left > 0 && next_b < n_seqs) {
-      span = span_of(__ldg(seq_lens + next_b), window, max_blocks);
+      span = span_of(seq_lens[next_b], window, max_blocks);
       b = next_b;
       chunk = next_chunk;
       const int cost = span.cost(begin);
@@ -227,7 +227,9 @@ __device__ __forceinline__ float tanh_abs(float y) {
 
 // The kernels of a call are launched while what is ahead of them in the stream
 // may still run: nothing of the inputs, the outputs or the workspace is touched
-// before this.
+// before this. What they read may thus be written while they are alive, which rules
+// out the read-only path (`__ldg`, and inputs marked const __restrict__): loads
+// are plain ones here.
 __device__ __forceinline__ void wait_for_inputs() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -236,7 +238,7 @@ template <int LAT, int NH, bool FP8>
 __global__ void __launch_bounds__(Cfg<LAT, NH, FP8>::kThreads, 1)
 latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                      const __grid_constant__ CUtensorMap pool_map, const LatentPages pages,
-                     const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ seq_lens,
+                     const __nv_bfloat16* q, const int32_t* seq_lens,
                      int n_seqs, int heads, int window, float scale, float softcap,
                      __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
                      Part* __restrict__ parts, float2* __restrict__ part_ml,
@@ -281,7 +283,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     int mine = 0;  // (the host has seen to it that 32 bits hold the sum)
 #pragma unroll 4
     for (int b = b0; b < b1; ++b) {
-      const int raw = __ldg(seq_lens + b);
+      const int raw = seq_lens[b];
       mine += span_of(raw, window, pages.max_blocks).cost(C::kBegin) * chunks;
       if (blockIdx.x == 0) {
         if (raw < 0) flag_error(err, PSW_DEVERR_LENGTH);
@@ -303,7 +305,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     if (p0 < p1 && p0 >= incl - mine && p0 < incl) {
       int at = incl - mine;
       for (int b = b0; b < b1; ++b) {
-        const int n = span_of(__ldg(seq_lens + b), window, pages.max_blocks).cost(C::kBegin);
+        const int n = span_of(seq_lens[b], window, pages.max_blocks).cost(C::kBegin);
         if (p0 < at + n * chunks) {
           int c = 0;
           for (; p0 >= at + n; at += n) ++c;
@@ -392,7 +394,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
               q + (static_cast<int64_t>(walk.b) * heads + h) * kRow);
 #pragma unroll
           for (int i = 0; i < kWords; ++i)
-            raw[j][i] = (h < heads && i * 32 + lane < kPairs) ? __ldg(src + i * 32 + lane) : 0u;
+            raw[j][i] = (h < heads && i * 32 + lane < kPairs) ? src[i * 32 + lane] : 0u;
         }
         if (seg > 0) ok = __all_sync(0xffffffffu, mbar_wait(&ms->q_free, (seg - 1) & 1));
         if (!ok) break;
@@ -448,8 +450,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     // block id of page i of the segment; -1: zero rows
     auto block_id = [&](int i) -> int {
       if (i >= walk.seg_count) return -1;
-      const int blk = __ldg(pages.block_table + static_cast<int64_t>(walk.b) * pages.max_blocks +
-                            walk.span.first + walk.seg_first + i);
+      const int blk = pages.block_table[static_cast<int64_t>(walk.b) * pages.max_blocks +
+                                        walk.span.first + walk.seg_first + i];
       if (blk >= 0 && blk < pages.num_blocks) return blk;
       flag_error(err, PSW_DEVERR_BLOCK_ID);
       return -1;
@@ -949,9 +951,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 constexpr int kMergeThreads = 512;
 template <int LAT>
 __global__ void __launch_bounds__(kMergeThreads)
-latent_merge_kernel(const int32_t* __restrict__ seq_lens, int heads, int max_pieces,
-                    const Part* __restrict__ parts, const float2* __restrict__ part_ml,
-                    const float* __restrict__ part_o, __nv_bfloat16* __restrict__ out,
+latent_merge_kernel(const int32_t* seq_lens, int heads, int max_pieces, const Part* parts,
+                    const float2* part_ml, const float* part_o, __nv_bfloat16* __restrict__ out,
                     float* __restrict__ lse, int32_t* err) {
   constexpr int kRow = LAT / 4;  // threads of a group
   __shared__ float s_w[kMergeThreads / 32][kMaxCtas];
@@ -963,7 +964,7 @@ latent_merge_kernel(const int32_t* __restrict__ seq_lens, int heads, int max_pie
   const int64_t row = static_cast<int64_t>(b) * heads + h;
   uint2* dst = reinterpret_cast<uint2*>(out + row * LAT) + col;
   wait_for_inputs();
-  const int len = __ldg(seq_lens + b);
+  const int len = seq_lens[b];
   const Part pt = len > 0 ? parts[b * chunks_of(heads) + chunk] : Part{-1, -1};
   if (len <= 0) {
     if (group == 0) *dst = make_uint2(0u, 0u);
