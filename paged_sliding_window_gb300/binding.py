@@ -393,11 +393,20 @@ def qkv_norm_rope_cache_write(layer, rn: PswNormRope, q, k, v, cu_new, past_lens
 
 
 # ---------------------------------------------------------------- latent attention
+class _SharedLatent(PswLatent):
+    """A layer's struct that every caller with the same fields is given: its fields stay."""
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{name}: this struct is shared by all layers of the same fields; "
+                             "make a PswLatent (or a layer) with the fields wanted")
+
+
 _LATENT_STRUCTS: dict = {}
 
 
 def make_latent_layer(layer) -> PswLatent:
-    """From any object with the psw_latent_t fields (e.g. workloads.LatentLayer)."""
+    """From any object with the psw_latent_t fields (e.g. workloads.LatentLayer). The struct is
+    read-only, one for all layers of the same fields; a PswLatent is returned as it is."""
     if isinstance(layer, PswLatent):
         return layer
     key = (int(layer.n_heads), int(layer.latent_dim), int(layer.rope_dim), int(layer.nope_dim),
@@ -407,7 +416,7 @@ def make_latent_layer(layer) -> PswLatent:
     if got is None:
         if len(_LATENT_STRUCTS) >= 1024:
             _LATENT_STRUCTS.clear()
-        got = _LATENT_STRUCTS[key] = PswLatent(*key)
+        got = _LATENT_STRUCTS[key] = _SharedLatent.from_buffer_copy(PswLatent(*key))
     return got
 
 
