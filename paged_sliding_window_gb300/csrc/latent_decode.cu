@@ -16,9 +16,14 @@
 // column groups of one N (the A side is read once for both; one part alone
 // would add as much error as the output's own rounding). FP8 pages: the codes
 // are A as they are. q, times a power of two, is the exact sum of two E4M3
-// parts (8 significant bits), P (times the row's scale over the largest of the
-// segment) is taken in three, 2^-12 relative; again column groups. Row scales
-// multiply scores and P in fp32. Maxima and sums are fp32.
+// parts (8 significant bits); P times the row's scale, times a power of two per
+// head, is taken in three, each 16 times finer than the one before: 2^-12 of itself,
+// or 2^-18 of the unit where the third is subnormal. The power of two is chosen so
+// that the largest of a tile is 8 units, and anew (O rescaled) for a tile whose
+// largest would be beyond the codes or below 2^-4: what follows a row of large score
+// or scale weighs little beside it, but there may be much of it. A tile's 64 rows
+// are thus off by 2^-12 + 2^-8 of their sum at worst. Row scales multiply scores and
+// P in fp32. Maxima and sums are fp32.
 //
 // Schedule: one CTA per SM. The visible pages of all (sequence, head chunk)
 // units form one list that is cut evenly; a CTA whose piece covers a unit
@@ -35,8 +40,7 @@
 // and four heads) and the epilogue (a thread per dim); one warp loads pages,
 // one (FP8, which splits them into parts: four) the queries. The maximum that P
 // is relative to is taken from a segment's first tile and moved (O rescaled)
-// only when a score exceeds it by 2^64 (bf16, whose P has the range) or 2^4
-// (E4M3), so a tile costs its threads one barrier.
+// only when a score exceeds it by 2^64, so a tile costs its threads one barrier.
 //
 // Measured (latent 512, GPU time in a graph, joins included). 64 sequences of 512
 // to 4096 rows, 16 heads: bf16 171 MB in 39.8 us (4.3 TB/s; a kernel that only
@@ -109,12 +113,13 @@ struct Cfg {
   static constexpr int kBegin = FP8 ? 12 : 8;
   static constexpr int kHeads = 4;                     // heads of a softmax thread
   static_assert(kSlots <= 32, "phase bits");
-  // log2 distance by which a score may exceed the maximum in use, and the
-  // largest row scale relative to the one in use; E4M3 P = 16 p v then stays
-  // within 16 * 16 * 1.75 = 448
-  static constexpr float kLag = FP8 ? 4.f : 64.f;
-  static constexpr float kVLag = 1.75f;
-  static constexpr float kPUnit = FP8 ? 16.f : 1.f;
+  // log2 distance by which a score may exceed the maximum in use
+  static constexpr float kLag = 64.f;
+  // FP8, a row's weight (2^score times its scale) in units, as log2: the largest of a tile
+  // may be at most kMost (448 is the largest code), is at least kLeast (64 keys), and is kAim where
+  // the unit is chosen; a head's unit never falls kReach below what its largest so far
+  // asked for (that one's share of O then still fits fp32; what is left out is 2^-40 of it)
+  static constexpr float kMost = 8.75f, kLeast = -4.f, kAim = 3.f, kReach = 40.f;
 };
 
 // The list, cut into n pieces: of q + 1 for the first r, of q for the others.
@@ -136,11 +141,17 @@ struct Misc {
   Cut cut;                   // of what all units count for
   int32_t p0, p1;            // this CTA's piece of it
   float red[4][kMaxHeads];
-  float vred[4];
+  alignas(16) uint32_t near[8];  // FP8, by warp: see kNear
   float qs[3][kMaxHeads];    // FP8, segments in turn: scale * log2(e) * a unit of q's codes
   float lsum[kMaxHeads];
   float alpha[kMaxHeads];    // factors of a rescale; at a segment's end, the maxima
+  float top[kMaxHeads];      // FP8: the largest weight (log2) seen when units were chosen; at a
+                             // segment's end, the root of what a unit stands for
 };
+// FP8: what a warp says of a tile: for each of its 16 heads whether some key weighs
+// 2^kLeast units or more; whether any key has a scale at all; whether the maximum or a
+// unit has to move up.
+constexpr uint32_t kNear = 0xFFFFu, kScaled = 1u << 16, kOver = 1u << 17;
 static_assert(sizeof(Misc) <= 2048, "misc block");
 
 // Row scales of a page that is not there (its codes read as zeros).
@@ -660,9 +671,16 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       }
       const int h0 = w.chunk * NH, nh = min(NH, heads - h0), n_tiles = w.tiles();
       constexpr int HN = C::kHeads;
-      float m[HN], l[HN], vref = 0.f;
+      // FP8: ref is the log2 of the unit; bit i of `stuck`: head i's is as small as it may be
+      float m[HN], l[HN], ref[HN];
+      uint32_t stuck = 0;
 #pragma unroll
-      for (int i = 0; i < HN; ++i) m[i] = 0.f, l[i] = 0.f;
+      for (int i = 0; i < HN; ++i) m[i] = 0.f, l[i] = 0.f, ref[i] = 0.f;
+      // FP8: a last tile of few keys is as near to their sum with a smaller largest weight
+      const int page0 = w.span.first + w.seg_first;
+      const float last_least =
+          C::kLeast - 6.f + __log2f(static_cast<float>(min(w.span.len, (page0 + w.seg_count) * kBlockSize) -
+                                                       (page0 + (n_tiles - 1) * kPages) * kBlockSize));
       for (int t = seg < 0 ? -1 : 0; t < n_tiles; ++t) {
         const bool live = t >= 0;
         const bool in_seg = live && t * kPages + row_warp < w.seg_count;  // a page per warp
@@ -713,14 +731,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
             for (int j = 0; j < 2; ++j) z[j][i] = cap2 * tanh_abs(z[j][i]);
         }
-        float over = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
-          for (int i = 0; i < HN; ++i) {
-            z[j][i] = seen[j] ? z[j][i] : -INFINITY;
-            over = fmaxf(over, z[j][i] - m[i]);
-          }
+          for (int i = 0; i < HN; ++i) z[j][i] = seen[j] ? z[j][i] : -INFINITY;
           // rows of a loaded page that hold no visible key must not enter the
           // second product (P is 0 there, but 0 times NaN is not)
           if (in_seg && !seen[j] && head0 == 0) {
@@ -734,9 +748,60 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
               }
           }
         }
+        float over = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < HN; ++i) over = fmaxf(over, fmaxf(z[0][i], z[1][i]) - m[i]);
         bool move = !ok || t <= 0 || over > C::kLag;
-        if (FP8) move |= fmaxf(vs[0], vs[1]) > C::kVLag * vref;
-        if (lat::bar_any(1, kSoftThreads, move)) {
+        // FP8: log2 of the rows' scales. A head's unit is too large if all of the tile's weights
+        // are small. Each thread with that head then finds its two small: where that is so (of
+        // some head) in all eight lanes that have the same heads, in the first row warp, all
+        // warps look head by head.
+        float lv[2];
+        const float least = t == n_tiles - 1 ? last_least : C::kLeast;
+        if constexpr (FP8) {
+          lv[0] = __log2f(fabsf(vs[0]));
+          lv[1] = __log2f(fabsf(vs[1]));
+          float hi = -INFINITY, lo = INFINITY;
+#pragma unroll
+          for (int i = 0; i < HN; ++i) {
+            const float at = fmaxf(z[0][i] + lv[0], z[1][i] + lv[1]) - ref[i];
+            hi = fmaxf(hi, at);
+            lo = fminf(lo, at);
+          }
+          move |= hi > C::kMost;
+          bool small = false;
+          if (row_warp == 0) {
+            uint32_t b = __ballot_sync(0xffffffffu, lo < least);
+            b &= b >> 16;
+            b &= b >> 8;
+            b &= b >> 4;
+            small = (b & 15u) != 0;
+          }
+          if (lat::bar_any(1, kSoftThreads, move || small)) {
+            uint32_t near = stuck;
+#pragma unroll
+            for (int i = 0; i < HN; ++i)
+              near |= fmaxf(z[0][i] + lv[0], z[1][i] + lv[1]) - ref[i] >= least ? 1u << i : 0u;
+            const uint32_t w = __reduce_or_sync(
+                0xffffffffu, near << (4 * quad) | (fmaxf(lv[0], lv[1]) > -INFINITY ? kScaled : 0u) | (move ? kOver : 0u));
+            if (lane == 0) ms->near[warp] = w;
+            named_bar_sync(1, kSoftThreads);
+            uint32_t any = 0, all = kNear;
+#pragma unroll
+            for (int k = 0; k < C::kGroups; ++k) {
+              const uint4 four = *reinterpret_cast<const uint4*>(&ms->near[4 * k]);
+              const uint32_t of = (four.x | four.y) | (four.z | four.w);
+              any |= of;
+              all &= of;
+            }
+            move = (any & kOver) || ((any & kScaled) && all != kNear);
+          } else {
+            move = false;
+          }
+        } else {
+          move = lat::bar_any(1, kSoftThreads, move);
+        }
+        if (move) {
           // the tile's maxima; the ones in use move to them where they lag
 #pragma unroll
           for (int i = 0; i < HN; ++i) {
@@ -745,10 +810,6 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
             if (lane < 4) ms->red[row_warp][head_of(i)] = x;
           }
-          if (FP8) {
-            const float x = lat::warp_max(fmaxf(vs[0], vs[1]));
-            if (lane == 0 && head0 == 0) ms->vred[row_warp] = x;
-          }
           // O is rescaled below: the products up to the tile before have ended
           if (t > 0 && ok) ok = mbar_wait(&ms->pv_done[(tile - 1) % 3], (tile - 1) / 3 & 1);
           if (lat::bar_any(1, kSoftThreads, !ok)) {
@@ -756,31 +817,59 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             break;
           }
           tc::fence_after();
-          float vmul = 1.f;
-          if (FP8) {
-            const float x = fmaxf(fmaxf(ms->vred[0], ms->vred[1]), fmaxf(ms->vred[2], ms->vred[3]));
-            if (t <= 0 || x > C::kVLag * vref) {
-              const float to = fmaxf(x, 1e-30f);
-              vmul = t <= 0 ? 1.f : vref / to;
-              vref = to;
-            }
-          }
+          float a[HN];
 #pragma unroll
           for (int i = 0; i < HN; ++i) {
             const int h = head_of(i);
             const float x = fmaxf(fmaxf(ms->red[0][h], ms->red[1][h]), fmaxf(ms->red[2][h], ms->red[3][h]));
-            float a = 1.f;
+            a[i] = 1.f;
             if (t <= 0) {
               l[i] = 0.f;
               m[i] = x == -INFINITY ? 0.f : x;
             } else if (x > m[i] + C::kLag) {
-              a = ex2_approx(m[i] - x);
-              l[i] *= a;
+              a[i] = ex2_approx(m[i] - x);
+              l[i] *= a[i];
               m[i] = x;
             }
-            if (row_warp == 0 && lane < 4) ms->alpha[h] = a * vmul;
           }
+          float top[HN];
+          if constexpr (FP8) {
+            // the units, from the tile's largest weights (O is in units whatever the maximum)
+            named_bar_sync(1, kSoftThreads);  // the maxima have been read
+#pragma unroll
+            for (int i = 0; i < HN; ++i) {
+              float x = fmaxf(z[0][i] + lv[0], z[1][i] + lv[1]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+              if (lane < 4) ms->red[row_warp][head_of(i)] = x;
+            }
+            named_bar_sync(1, kSoftThreads);
+            stuck = 0;
+#pragma unroll
+            for (int i = 0; i < HN; ++i) {
+              const int h = head_of(i);
+              const float x = fmaxf(fmaxf(ms->red[0][h], ms->red[1][h]), fmaxf(ms->red[2][h], ms->red[3][h]));
+              const float old = ref[i];
+              top[i] = t <= 0 ? x : fmaxf(ms->top[h], x);
+              if (t <= 0) {
+                ref[i] = x > -INFINITY ? x - C::kAim : m[i];
+              } else if (x > -INFINITY && (x - old > C::kMost || x - old < least)) {
+                // (by a power of two, so that O keeps its bits)
+                ref[i] = fmaxf(old + rintf(x - C::kAim - old), top[i] - (C::kAim + C::kReach));
+                if (x - ref[i] < least) stuck |= 1u << i;
+              }
+              a[i] = ex2_approx(fminf(old - ref[i], 100.f));  // (beyond: O is still zero)
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < HN; ++i)
+            if (row_warp == 0 && lane < 4) ms->alpha[head_of(i)] = a[i];
           named_bar_sync(1, kSoftThreads);
+          if constexpr (FP8) {
+#pragma unroll
+            for (int i = 0; i < HN; ++i)
+              if (row_warp == 0 && lane < 4) ms->top[head_of(i)] = top[i];
+          }
           if (t > 0) {
 #pragma unroll 1
             for (int blk = warp >> 2; blk < C::kBlocks; blk += C::kGroups) {
@@ -798,7 +887,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             }
             tc::wait_st();
           }
-          named_bar_sync(1, kSoftThreads);  // red, vred and alpha may be written again
+          named_bar_sync(1, kSoftThreads);  // red, top and alpha may be written again
         }
         // P into the rope slot: a key's row holds the parts of all heads,
         // 16-byte vectors swizzled by the row
@@ -806,7 +895,6 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         for (int j = 0; j < 2; ++j) {
           const int r = r0 + 8 * j, sw = r & 7;
           uint8_t* prow = ring + slot[0] * kSlotBytes + r * 128;
-          const float pv = FP8 ? vs[j] * (C::kPUnit / vref) : 1.f;
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             float a = ex2_approx(z[j][2 * g] - m[2 * g]);
@@ -822,8 +910,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
               *reinterpret_cast<uint32_t*>(prow + (((vec + NH / 8) ^ sw) << 4) + quad * 4) =
                   pack_bf16x2(a - got.x, b - got.y);
             } else {
-              a *= pv;
-              b *= pv;
+              a = copysignf(ex2_approx(z[j][2 * g] + lv[j] - ref[2 * g]), vs[j]);
+              b = copysignf(ex2_approx(z[j][2 * g + 1] + lv[j] - ref[2 * g + 1]), vs[j]);
 #pragma unroll
               for (int p = 0; p < 3; ++p) {
                 const uint32_t c = lat::e4m3_pair(a, b);
@@ -862,7 +950,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         const int h = head_of(i);
         if (lane < 4) ms->red[row_warp][h] = x;
-        if (row_warp == 0 && lane < 4) ms->alpha[h] = m[i];
+        if (row_warp == 0 && lane < 4) {
+          ms->alpha[h] = m[i];
+          if (FP8) ms->top[h] = ex2_approx(0.5f * (ref[i] - m[i]));
+        }
       }
       ok = mbar_wait(&ms->o_full, seg & 1);
       if (lat::bar_any(1, kSoftThreads, !ok)) {
@@ -875,7 +966,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       if (tid < nh) {  // thread h: the statistics of head h
         const float mh = ms->alpha[tid];
         const float s = ms->red[0][tid] + ms->red[1][tid] + ms->red[2][tid] + ms->red[3][tid];
-        ms->lsum[tid] = whole ? (s == 0.f ? 0.f : 1.f / s) : 1.f;
+        ms->lsum[tid] = (whole ? (s == 0.f ? 0.f : 1.f / s) : 1.f) * (FP8 ? ms->top[tid] : 1.f);
         if (whole) {
           if (lse != nullptr)
             lse[static_cast<int64_t>(w.b) * heads + h0 + tid] = (mh + __log2f(s)) * lat::kLn2;
@@ -891,7 +982,6 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         parts[w.b * chunks + w.chunk] = whole ? Part{-1, -1} : Part{static_cast<int32_t>(blockIdx.x), last};
       }
       named_bar_sync(1, kSoftThreads);
-      const float ov = FP8 ? vref / C::kPUnit : 1.f;
 #pragma unroll 1
       for (int blk = warp >> 2; blk < C::kBlocks; blk += C::kGroups) {
         const int d = blk * 128 + row_warp * 32 + lane;
@@ -914,12 +1004,12 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
           __nv_bfloat16* dst = out + (static_cast<int64_t>(w.b) * heads + h0) * LAT + d;
 #pragma unroll
           for (int h = 0; h < NH; ++h)
-            if (h < nh) dst[h * LAT] = __float2bfloat16_rn(o[h] * (ov * ms->lsum[h]));
+            if (h < nh) dst[h * LAT] = __float2bfloat16_rn((FP8 ? o[h] * ms->top[h] : o[h]) * ms->lsum[h]);
         } else {
           float* dst = part_o + static_cast<int64_t>(slot_id) * kMaxHeads * LAT + d;
 #pragma unroll
           for (int h = 0; h < NH; ++h)
-            if (h < nh) dst[h * LAT] = o[h] * ov;
+            if (h < nh) dst[h * LAT] = FP8 ? o[h] * ms->top[h] * ms->lsum[h] : o[h];
         }
       }
       tc::fence_before();
