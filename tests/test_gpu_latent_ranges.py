@@ -44,6 +44,17 @@ def run_decode(layer, pg, q, lens, what, p_err=None):
     return out, lse
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("L,H,lens,grow,scale", [(256, 4, [1500, 300], 2.0, 1.0), (512, 16, [3000, 129], 0.0, 1.0),
+                                                 (512, 16, [3000, 129], 0.0, 1e-4), (512, 24, [700, 65], 0.3, 0.3)])
+def test_decode_bounds(L, H, lens, grow, scale, fp8):
+    """Growing, peaked and flat scores within bounds that are as tight on FP8 pages as on bf16
+    pages but for P's parts."""
+    layer = LatentLayer(H, L, scale=scale)
+    pg, q = _decode_inputs(layer, lens, fp8, 5, grow=grow)
+    run_decode(layer, pg, q, lens, "bounds")
+
+
 def sink_inputs(layer, lens, bits, ratio, seed, at=0):
     """Rows of equal scores behind one (row `at`) whose score is `bits` powers of two above theirs and
     whose row scale is `ratio` times theirs; its latent is small, as that of such a row mostly is."""
