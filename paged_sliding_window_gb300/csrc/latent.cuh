@@ -54,6 +54,24 @@ __device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
                     pack_bf16x2(y[6], y[7]));
 }
 
+// tanh, for the softcap of scores cap tanh(s / cap). From t = e^-2|y|, 1 - t over 1 + t is
+// good to 2^-22, and a score to that of the cap: 2^-13 up to a cap of kNearCap. Beyond,
+// where the cap is far above the scores, they have to stay as near to s as fp32 is: up to
+// |y| = 1/4 the odd Taylor polynomial through y^7 (what follows is 3.3e-7 of it at most),
+// above it 1 - t keeps all but two of its bits.
+constexpr float kNearCap = 512.f;
+constexpr float kTanhSmall = 0.25f;
+__device__ __forceinline__ float tanh_small_over(float y2) {  // tanh(y) / y
+  return fmaf(y2, fmaf(y2, fmaf(y2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+}
+__device__ __forceinline__ float tanh_large(float y) {
+  const float t = ex2_approx(-2.f * kLog2e * fabsf(y));
+  return copysignf(__fdividef(1.f - t, 1.f + t), y);
+}
+__device__ __forceinline__ float tanh_of(float y) {
+  return fabsf(y) <= kTanhSmall ? y * tanh_small_over(y * y) : tanh_large(y);
+}
+
 // 2-D view of a pool (or of any rows) as the 3-D map's first two dimensions:
 // one box of shared memory rows at (x, y); z selects within a third dimension.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint64_t* bar,

@@ -28,7 +28,8 @@ int check_latent(const psw_latent_t* layer, LatentArgs* out) {
   out->n_heads = layer->n_heads;
   out->latent = layer->latent_dim;
   out->window = layer->window;
-  out->softcap = layer->softcap;
+  // (beyond these fp32 cannot tell a cap from none, or from one that leaves every score 0)
+  out->softcap = layer->softcap == 0.f ? 0.f : fminf(fmaxf(layer->softcap, 0x1p-100f), 0x1p100f);
   out->scale = layer->scale;
   return PSW_OK;
 }

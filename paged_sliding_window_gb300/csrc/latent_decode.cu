@@ -230,12 +230,6 @@ struct Ring {
   }
 };
 
-// tanh to a few units in the last place of 1, which is what the softcap needs.
-__device__ __forceinline__ float tanh_abs(float y) {
-  const float t = ex2_approx(-2.f * lat::kLog2e * fabsf(y));
-  return copysignf(__fdividef(1.f - t, 1.f + t), y);
-}
-
 // The kernels of a call are launched while what is ahead of them in the stream
 // may still run: nothing of the inputs, the outputs or the workspace is touched
 // before this. What they read may thus be written while they are alive, which rules
@@ -245,7 +239,7 @@ __device__ __forceinline__ void wait_for_inputs() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-template <int LAT, int NH, bool FP8>
+template <int LAT, int NH, bool FP8, bool FAR_CAP>
 __global__ void __launch_bounds__(Cfg<LAT, NH, FP8>::kThreads, 1)
 latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                      const __grid_constant__ CUtensorMap pool_map, const LatentPages pages,
@@ -729,7 +723,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
           for (int i = 0; i < HN; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) z[j][i] = cap2 * tanh_abs(z[j][i]);
+            for (int j = 0; j < 2; ++j)
+              z[j][i] = cap2 * (FAR_CAP ? lat::tanh_of(z[j][i]) : lat::tanh_large(z[j][i]));
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -1157,7 +1152,9 @@ int launch(const LatentArgs& L, const void* q, const LatentPages& pages, const i
                    {row_bytes, row_bytes},
                    {C::kElems, kBlockSize, 1});
   if (rc != PSW_OK) return rc;
-  auto* kernel = latent_decode_kernel<LAT, NH, FP8>;
+  // (as a run-time choice the form for large caps cost the others 1 to 10 %)
+  auto* kernel = L.softcap > lat::kNearCap ? latent_decode_kernel<LAT, NH, FP8, true>
+                                           : latent_decode_kernel<LAT, NH, FP8, false>;
   rc = set_smem_limit(reinterpret_cast<const void*>(kernel), C::kSmemBytes);
   if (rc != PSW_OK) return rc;
   const Layout y = layout(L, n_seqs);

@@ -143,12 +143,7 @@ __device__ __forceinline__ Work work_of(const Seq& q, int i0, int tile, int keys
   return w;
 }
 
-__device__ __forceinline__ float tanh_abs(float y) {
-  const float t = ex2_approx(-2.f * lat::kLog2e * fabsf(y));
-  return copysignf(__fdividef(1.f - t, 1.f + t), y);
-}
-
-template <int CTAS, bool SPLIT>
+template <int CTAS, bool SPLIT, bool FAR_CAP>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
                       const __grid_constant__ CUtensorMap kv_map,
@@ -582,7 +577,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
         const int c_hi = min(x.last - j * kKeys, kKeys - 1), c_lo = max(x.first - j * kKeys, 0);
         if (cap) {
 #pragma unroll
-          for (int c = 0; c < kKeys; ++c) z[c] = cap_out * tanh_abs(z[c] * cap_in);
+          for (int c = 0; c < kKeys; ++c)
+            z[c] = cap_out * (FAR_CAP ? lat::tanh_of(z[c] * cap_in) : lat::tanh_large(z[c] * cap_in));
         }
         if (!__all_sync(0xffffffffu, c_lo <= 0 && c_hi >= kKeys - 1)) {
 #pragma unroll
@@ -779,9 +775,11 @@ int launch_latent_prefill(const LatentArgs& L, const void* q, const int32_t* cu_
   } else {
     kv_map = rope_map = q_map;  // no key tile will be loaded
   }
-  auto* kernel = split       ? latent_prefill_kernel<2, true>
-                 : ctas == 2 ? latent_prefill_kernel<2, false>
-                             : latent_prefill_kernel<1, false>;
+  // (as a run-time choice the form for large caps cost the others 3 to 10 %)
+  const bool far = L.softcap > lat::kNearCap;
+  auto* kernel = split       ? (far ? latent_prefill_kernel<2, true, true> : latent_prefill_kernel<2, true, false>)
+                 : ctas == 2 ? (far ? latent_prefill_kernel<2, false, true> : latent_prefill_kernel<2, false, false>)
+                             : (far ? latent_prefill_kernel<1, false, true> : latent_prefill_kernel<1, false, false>);
   const int smem = ctas == 2 ? Cfg<2>::kSmemBytes : Cfg<1>::kSmemBytes;
   rc = set_smem_limit(reinterpret_cast<const void*>(kernel), smem);
   if (rc != PSW_OK) return rc;

@@ -117,3 +117,31 @@ def test_decode_fp8_levels(H, L, cap):
         rows[::5] = 0
         pg.put(b, rows)
     run_decode(layer, pg, q, lens, "levels")
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("cap", [1e3, 1e6, 1e30])
+def test_decode_large_softcap(cap, fp8):
+    """A cap far above the scores leaves them as they are."""
+    layer, lens = LatentLayer(16, 512, scale=0.07, softcap=cap), [700, 65]
+    pg, q = _decode_inputs(layer, lens, fp8, 5)
+    run_decode(layer, pg, q, lens, f"softcap {cap}")
+
+
+@pytest.mark.parametrize("cap", [1e3, 1e6, 1e30])
+@pytest.mark.parametrize("H,new,past", [(2, [200, 64], [300, 0]), (2, [520], [100]), (90, [150, 30], [100, 0])], ids=["split", "pair", "single"])
+def test_prefill_large_softcap(H, new, past, cap):
+    layer, g = LatentLayer(H, scale=0.07, softcap=cap), gen(3)
+    keys, T = [n + p for n, p in zip(new, past)], sum(new)
+    q = randn(g, T, H, NOPE + R).to(BF16)
+    kv, rope = randn(g, sum(keys), H, NOPE + V).to(BF16), randn(g, sum(keys), R).to(BF16)
+    out, lse = torch.empty(T, H, V, dtype=BF16, device="cuda"), torch.empty(T, H, device="cuda")
+    binding.attn_prefill_latent(layer, q, cu(new), i32(past), max(new), kv, rope, cu(keys), out, lse)
+    no_error()
+    q0 = k0 = 0
+    for n, p, t in zip(new, past, keys):
+        k = torch.cat([kv[k0:k0 + t, :, :NOPE], rope[k0:k0 + t, None].expand(-1, H, -1)], -1)
+        ref = attend(q[q0:q0 + n].to(F64).transpose(0, 1), k.to(F64).transpose(0, 1), kv[k0:k0 + t, :, NOPE:].to(F64).transpose(0, 1),
+                     p + torch.arange(n, device="cuda"), torch.arange(t, device="cuda"), layer)
+        check_attention(out[q0:q0 + n].transpose(0, 1), lse[q0:q0 + n].transpose(0, 1), ref, P_ERR_PREFILL, S_ERR, f"softcap {cap}")
+        q0, k0 = q0 + n, k0 + t
