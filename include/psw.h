@@ -437,7 +437,7 @@ PSW_API int latent_norm_rope_cache_write(
 /* The same into FP8 pages: pool8 uint8 [num_blocks][16][L + 64] of E4M3 codes
  * and row_scale fp32 [num_blocks][16] (16-byte aligned), one scale per row by the rule of
  * kv_cache_write_fp8 applied to the row's fp32 values (amax over all L + 64,
- * rounded once, to the code). */
+ * rounded once, to the code; a row whose amax is below 2^-117 becomes a zero row). */
 PSW_API int latent_norm_rope_cache_write_fp8(
     const psw_latent_t *layer, const psw_latent_norm_t *norm, const void *ckv, int64_t ckv_stride,
     const void *q_rope, int64_t q_token_stride, int64_t q_head_stride, const int32_t *cu_new,

@@ -29,6 +29,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kGroup = 8;  // query heads that a warp turns at once
 constexpr int kCtas = 8;   // per SM
+constexpr float kLeastRow = 0x1p-117f;  // FP8: largest value of a row that is not taken for zeros
 
 struct Freqs {
   double f[kLatentRope / 2];   // theta^(-i / 32), for positions from 2^24 on
@@ -214,6 +215,8 @@ latent_write_kernel(const __grid_constant__ Freqs freqs, const float* __restrict
         for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[c][e]));
 #pragma unroll
       for (int m = 16; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+      // (448 / amax and amax / 448 are fp32 numbers from here on; below, a zero row)
+      if (amax < kLeastRow) amax = 0.f;
       const float k = amax > 0.f ? __fdiv_rn(448.f, amax) : 0.f;
       uint8_t* dst = static_cast<uint8_t*>(pool) + slot * kRow;
 #pragma unroll

@@ -145,3 +145,27 @@ def test_prefill_large_softcap(H, new, past, cap):
                      p + torch.arange(n, device="cuda"), torch.arange(t, device="cuda"), layer)
         check_attention(out[q0:q0 + n].transpose(0, 1), lse[q0:q0 + n].transpose(0, 1), ref, P_ERR_PREFILL, S_ERR, f"softcap {cap}")
         q0, k0 = q0 + n, k0 + t
+
+
+def test_write_fp8_tiny_rows():
+    """Rows so small that 448 / amax has no fp32 value are zero rows; somewhat larger ones are
+    rows like any other. None becomes NaN."""
+    L, n = 256, 40
+    layer, g, pg = LatentLayer(1, L), gen(2), Pages([n, n, n], L, True, 2)
+    ckv = randn(g, n, L + R).to(BF16)
+    ckv[:, L:] = 0
+    ckv[:, :8] = 0
+    want0 = ckv[:, :L].to(F64)
+    want0 = want0 / (want0.square().mean(1, keepdim=True) + EPS).sqrt()
+    for b, size in enumerate((2.0 ** -100, 2.0 ** -115, 2.0 ** -122)):
+        w = torch.full((L,), size, device="cuda")
+        table = pg.table[b:b + 1].contiguous()
+        binding.latent_norm_rope_cache_write_fp8(layer, binding.make_latent_norm(THETA, EPS, w), ckv, None, cu([n]), i32([0]),
+                                                 binding.make_pages(table, pg.blocks), None, pg.pool, pg.scale)
+        no_error()
+        got, sc = pg.rows(b, 0, n), pg.scale.view(-1)[pg.slots(b, 0, n)].to(F64)[:, None]
+        want = torch.cat([want0 * size, torch.zeros(n, R, dtype=F64, device="cuda")], 1)
+        if size < 2.0 ** -121:
+            assert bool((got == 0).all()) and bool((sc == 0).all())
+        else:
+            check(got, want, (H_E4M3 + 2.0 ** -17) * want.abs() + 2.0 ** -10 * sc, f"rows of {size}")
