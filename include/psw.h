@@ -87,7 +87,7 @@ typedef struct CUstream_st *psw_stream_t;
 #define PSW_ETENSORMAP       -15  /* the TMA descriptor for a pool could not be built */
 #define PSW_ESCRATCH         -16  /* the batch needs more scratch than the static buffer of
                                      attn_decode_paged_noalloc holds */
-#define PSW_EINVAL_ROPE      -17  /* theta <= 0, partial_rotary_factor outside (0, 1], eps < 0,
+#define PSW_EINVAL_ROPE      -17  /* theta <= 0 (latent layers: < 1), partial_rotary_factor outside (0, 1], eps < 0,
                                      or one of them not finite */
 #define PSW_EINVAL_LAYERS    -18  /* n_layers or pattern <= 0, n_shared outside [0, n_layers),
                                      or a shared layer with no cache-owning layer of its type */
@@ -396,7 +396,7 @@ typedef struct {
 
 /* Norm of the latent and rotation of the shared key part and of the queries. */
 typedef struct {
-  float theta;                 /* RoPE base, > 0 */
+  float theta;                 /* RoPE base, >= 1 (PSW_EINVAL_ROPE) */
   float eps;                   /* RMS-norm epsilon, >= 0 */
   const float *latent_weight;  /* device fp32 [L], 16-byte aligned, or NULL (weightless) */
 } psw_latent_norm_t;

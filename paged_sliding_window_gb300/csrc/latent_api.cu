@@ -60,7 +60,8 @@ int write_rows(const psw_latent_t* layer, const psw_latent_norm_t* norm, const v
   if (norm == nullptr || ckv == nullptr || cu_new == nullptr || past_lens == nullptr ||
       pool == nullptr || (q_rope == nullptr) != (q_rope_out == nullptr))
     return PSW_ENULL;
-  if (!(norm->theta > 0.f) || !isfinite(norm->theta) || !(norm->eps >= 0.f) ||
+  // (a base below 1 has frequencies above 1, whose angles the reduction does not cover)
+  if (!(norm->theta >= 1.f) || !isfinite(norm->theta) || !(norm->eps >= 0.f) ||
       !isfinite(norm->eps))
     return PSW_EINVAL_ROPE;
   if ((rc = check_pages(pages)) != PSW_OK) return rc;
