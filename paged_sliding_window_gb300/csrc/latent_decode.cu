@@ -743,9 +743,13 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
               }
           }
         }
-        float over = -INFINITY;
+        float over = -INFINITY, hi = -INFINITY, lo = INFINITY;
 #pragma unroll
-        for (int i = 0; i < HN; ++i) over = fmaxf(over, fmaxf(z[0][i], z[1][i]) - m[i]);
+        for (int i = 0; i < HN; ++i) {
+          const float x = fmaxf(z[0][i], z[1][i]);
+          over = fmaxf(over, x - m[i]);
+          if (FP8) hi = fmaxf(hi, x - ref[i]), lo = fminf(lo, x - ref[i]);
+        }
         bool move = !ok || t <= 0 || over > C::kLag;
         // FP8: log2 of the rows' scales. A head's unit is too large if all of the tile's weights
         // are small. Each thread with that head then finds its two small: where that is so (of
@@ -756,27 +760,25 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         if constexpr (FP8) {
           lv[0] = __log2f(fabsf(vs[0]));
           lv[1] = __log2f(fabsf(vs[1]));
-          float hi = -INFINITY, lo = INFINITY;
-#pragma unroll
-          for (int i = 0; i < HN; ++i) {
-            const float at = fmaxf(z[0][i] + lv[0], z[1][i] + lv[1]) - ref[i];
-            hi = fmaxf(hi, at);
-            lo = fminf(lo, at);
-          }
-          move |= hi > C::kMost;
+          // (looked at without telling this thread's two keys apart, so that at worst it is
+          // looked at in vain)
+          const bool most = hi + fmaxf(lv[0], lv[1]) > C::kMost;
           bool small = false;
           if (row_warp == 0) {
-            uint32_t b = __ballot_sync(0xffffffffu, lo < least);
+            uint32_t b = __ballot_sync(0xffffffffu, lo + fminf(lv[0], lv[1]) < least);
             b &= b >> 16;
             b &= b >> 8;
             b &= b >> 4;
             small = (b & 15u) != 0;
           }
-          if (lat::bar_any(1, kSoftThreads, move || small)) {
+          if (lat::bar_any(1, kSoftThreads, move || most || small)) {
             uint32_t near = stuck;
 #pragma unroll
-            for (int i = 0; i < HN; ++i)
-              near |= fmaxf(z[0][i] + lv[0], z[1][i] + lv[1]) - ref[i] >= least ? 1u << i : 0u;
+            for (int i = 0; i < HN; ++i) {
+              const float at = fmaxf(z[0][i] + lv[0], z[1][i] + lv[1]) - ref[i];
+              near |= at >= least ? 1u << i : 0u;
+              move |= at > C::kMost;
+            }
             const uint32_t w = __reduce_or_sync(
                 0xffffffffu, near << (4 * quad) | (fmaxf(lv[0], lv[1]) > -INFINITY ? kScaled : 0u) | (move ? kOver : 0u));
             if (lane == 0) ms->near[warp] = w;
