@@ -17,8 +17,10 @@
 //
 // Measured (latent 512, in a graph): 64 tokens of 16 heads 3.9 us; 4096 tokens 6.9
 // us, 26 MB read and written (3.8 TB/s); 6900 tokens of 32 heads into FP8 pages
-// 16.0 us, 66 MB (4.1 TB/s, 61 % of the measured copy rate). What is left is the
-// wait for the loads: the registers of 32 warps are what an SM has in flight.
+// 16.0 us, 66 MB (4.1 TB/s, 61 % of the measured copy rate). A single call takes the
+// 20 to 30 us that the host needs for it. What is left: a warp's loads are in flight for
+// part of the time only. It finds its token, computes and stores before it asks for the
+// next unit's values, and each unit of a token finds position and angles again.
 #include <math.h>
 
 #include "latent.cuh"

@@ -8,15 +8,15 @@
 // at 32 heads. That is far beyond what the CUDA cores and more than what
 // mma.sync sustain beside the loads, so both products run on tcgen05, turned
 // so that the padded operand side is the large one:
-//   S^T [128 keys x heads]  = K Q^T      (A: key rows as stored, K-major)
+//   S^T [64 keys x heads]   = K Q^T      (A: key rows as stored, K-major)
 //   O^T [128 dims x heads] += V^T P^T    (A: the same rows, read MN-major)
 // with the heads as the N side (16 or 32) and no wasted rows.
 //
 // Precision. bf16 pages: P enters as a bf16 part and the bf16 of the rest, two
 // column groups of one N (the A side is read once for both; one part alone
 // would add as much error as the output's own rounding). FP8 pages: the codes
-// are A as they are. q, times a power of two, is the exact sum of two E4M3
-// parts (8 significant bits); P times the row's scale, times a power of two per
+// are A as they are. q, times a power of two, is the sum of two E4M3 parts (all 8
+// bits of a value, but for 2^-21 of the head's largest); P times the row's scale, times a power of two per
 // head, is taken in three, each 16 times finer than the one before: 2^-12 of itself,
 // or 2^-18 of the unit where the third is subnormal. The power of two is chosen so
 // that the largest of a tile is 8 units, and anew (O rescaled) for a tile whose
@@ -42,15 +42,17 @@
 // is relative to is taken from a segment's first tile and moved (O rescaled)
 // only when a score exceeds it by 2^64, so a tile costs its threads one barrier.
 //
-// Measured (latent 512, GPU time in a graph, joins included). 64 sequences of 512
-// to 4096 rows, 16 heads: bf16 171 MB in 39.8 us (4.3 TB/s; a kernel that only
-// gathers the pages takes 30), FP8 86 MB in 29.7 us (17). 32 sequences of 1024 to
-// 32768 rows, 32 heads, bf16: 321 MB in 67.6 us (4.7 TB/s). 3 sequences of 40001 to
-// 65536 rows, 24 heads, FP8: 80 MB in 36.8 us. About 4 us are start-up (lengths,
+// Measured (latent 512, GPU time of a call in a graph of twelve, joins included; single
+// calls that follow on one another take the same). 64 sequences of 512 to 4096 rows, 16
+// heads: bf16 171 MB in 39.5 us (4.3 TB/s; a kernel that only gathers the pages takes
+// 30), FP8 86 MB in 32.5 us (with units that only ever rose, 30). 32 sequences of 1024
+// to 32768 rows, 32 heads, bf16: 321 MB in 67 us (4.8 TB/s). 3 sequences of 40001 to
+// 65536 rows, 24 heads, FP8: 80 MB in 38 us. About 4 us are start-up (lengths,
 // the cut, the first block ids and pages: loads that follow on one another) and 4
-// the join. In between bf16 is bound by the loads; FP8, whose operands for q and P
-// are two and three parts, by shared memory, which at 32 heads is read or written
-// 80 % of the time.
+// the join. In between bf16 is bound by the loads; FP8 by a tile's chain (scores,
+// softmax, three parts of P) and, at more than 16 heads, by shared memory, from which
+// two parts of q and three of P are read. A move of a unit costs 0.7 us. Heads beyond 32
+// are further units, each of which reads its pages again.
 #include <math.h>
 
 #include "latent.cuh"

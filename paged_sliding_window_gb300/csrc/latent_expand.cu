@@ -18,8 +18,9 @@
 // columns ahead, and moved into tensor memory chunk by chunk as the last unit of the
 // tile before is done with them.
 //
-// Measured: 40k rows of 16 heads, latent 512, 170 GFLOP: 109-111 us (1.55 PFLOP/s,
-// 79 % of the measured bf16 rate; the tensor cores are active 78 % of the time). A
+// Measured: 40k rows of 16 heads, latent 512, 170 GFLOP: 106 us in a graph of twelve
+// calls, 109 by itself (1.55 PFLOP/s, 79 % of the measured bf16 rate; the tensor cores
+// are active 78 % of the time), 120 in a long run of calls on changing inputs. A
 // unit takes ~2330 cycles where its 32 products of 68 cycles take 2176; 13000 cycles
 // pass before the first (20 MB are gathered at once), 3000 to 6000 from one
 // tile to the next. What was slower: rows in shared memory (144 us: that memory's

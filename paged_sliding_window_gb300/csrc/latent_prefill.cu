@@ -11,7 +11,10 @@
 // Schedule: two row tiles, A and B, of 128 rows of a CTA, are worked on in turn:
 // while the softmax of one runs, the tensor cores work for the other (O += P V of
 // a key tile, then S = Q K^T of the next). P is written over S in tensor memory as
-// bf16 (rounded once; sums are of the unrounded values). Warp 8 loads key tiles
+// bf16, rounded once; sums are of the unrounded values. That leaves 0.0023 of the output's
+// scale against 64 bits, where exact sums rounded to the output's bf16 leave 0.0017. The
+// rest of P as a second part would add 128 columns to the 320 that a key tile's products
+// have now, 40 % of the time, to take away less than the output's own rounding. Warp 8 loads key tiles
 // into stages (swizzled 64-column units), warp 9 issues the products, warps 0-3 and
 // 4-7 are the softmaxes of A and B, a thread per row. The maximum that P is
 // relative to is that of a row's first keys; it moves (O rescaled) only when a
@@ -35,11 +38,13 @@
 // first loads and epilogue of consecutive pieces then overlap (16 chunks of 300 rows,
 // 64 heads, nothing before: 203 -> 141 us; 7 of 1265, 58 heads: 395 -> 294).
 //
-// Measured: four chunks of 2048 rows after 2000 to 16384, 16 heads, 735 GFLOP, in 455 us
-// (1.62 PFLOP/s, 82 % of the measured bf16 rate, 94 % of the sustained one, which the
-// power limit sets); eight chunks of 512 rows after 0 to 8192, 166 GFLOP, in 124 us
-// (68 %: 128 pieces of unequal length over 76 pairs of CTAs, of which the longest
-// chains are a fifth longer than the mean).
+// Measured, per call in a graph of twelve: four chunks of 2048 rows after 2000 to 16384,
+// 16 heads, 735 GFLOP, in 455 us (1.62 PFLOP/s, 82 % of the measured bf16 rate, 94 % of
+// the sustained one, which the power limit sets); eight chunks of 512 rows after 0 to
+// 8192, 166 GFLOP, in 124 us (68 %: 128 pieces of unequal length over 76 pairs of CTAs,
+// of which the longest chains are a fifth longer than the mean). In a long run of single
+// calls on changing inputs 490 (76 %) and 130 us (65 %). A softcap costs as much again (the
+// special-function units): 228 us for eight chunks of 512 that take 111 without.
 #include <math.h>
 
 #include "latent.cuh"
