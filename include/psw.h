@@ -87,8 +87,8 @@ typedef struct CUstream_st *psw_stream_t;
 #define PSW_ETENSORMAP       -15  /* the TMA descriptor for a pool could not be built */
 #define PSW_ESCRATCH         -16  /* the batch needs more scratch than the static buffer of
                                      attn_decode_paged_noalloc holds */
-#define PSW_EINVAL_ROPE      -17  /* theta <= 0 (latent layers: < 1), partial_rotary_factor outside (0, 1], eps < 0,
-                                     or one of them not finite */
+#define PSW_EINVAL_ROPE      -17  /* theta <= 0 (latent layers: < 1), partial_rotary_factor
+                                     outside (0, 1], eps < 0, or one of them not finite */
 #define PSW_EINVAL_LAYERS    -18  /* n_layers or pattern <= 0, n_shared outside [0, n_layers),
                                      or a shared layer with no cache-owning layer of its type */
 #define PSW_ENOBLOCKS        -19  /* the block pool has fewer free blocks than asked for */
@@ -465,7 +465,9 @@ PSW_API int attn_decode_latent(const psw_latent_t *layer, const void *q, const v
                                void *out, float *lse, void *ws, size_t ws_bytes,
                                psw_stream_t stream);
 
-/* The same over FP8 pages (row_scale device fp32 [num_blocks][16]). */
+/* The same over FP8 pages (row_scale device fp32 [num_blocks][16]). Rows enter the sum
+ * with their probability times row_scale; of a run of 64 rows, those for which that is
+ * below 2^-21 of the run's largest may count as nothing. */
 PSW_API int attn_decode_latent_fp8(const psw_latent_t *layer, const void *q, const void *pool8,
                                    const float *row_scale, const psw_pages_t *pages,
                                    const int32_t *seq_lens, int32_t n_seqs, void *out, float *lse,

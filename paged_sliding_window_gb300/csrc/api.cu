@@ -619,7 +619,8 @@ const char* psw_strerror(int code) {
     case PSW_EINVAL_STRIDE:
       return "strides must be multiples of 8 elements and at least one row (or head) long";
     case PSW_EINVAL_ROPE:
-      return "theta must be > 0 (latent layers: >= 1), partial_rotary_factor in (0, 1], eps >= 0, all finite";
+      return "theta must be > 0 (latent layers: >= 1), partial_rotary_factor in (0, 1], eps >= 0, "
+             "all finite";
     default: return "unknown error";
   }
 }

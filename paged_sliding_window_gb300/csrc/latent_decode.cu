@@ -16,14 +16,14 @@
 // column groups of one N (the A side is read once for both; one part alone
 // would add as much error as the output's own rounding). FP8 pages: the codes
 // are A as they are. q, times a power of two, is the sum of two E4M3 parts (all 8
-// bits of a value, but for 2^-21 of the head's largest); P times the row's scale, times a power of two per
-// head, is taken in three, each 16 times finer than the one before: 2^-12 of itself,
-// or 2^-18 of the unit where the third is subnormal. The power of two is chosen so
-// that the largest of a tile is 8 units, and anew (O rescaled) for a tile whose
-// largest would be beyond the codes or below 2^-4: what follows a row of large score
-// or scale weighs little beside it, but there may be much of it. A tile's 64 rows
-// are thus off by 2^-12 + 2^-8 of their sum at worst. Row scales multiply scores and
-// P in fp32. Maxima and sums are fp32.
+// bits of a value, but for 2^-21 of the head's largest). A row's weight, P times its
+// scale, is taken in three parts, each 16 times finer than the one before: off by 2^-12
+// of itself, or by 2^-18 units where the third is subnormal. A head's unit is a power
+// of two, chosen so that the largest weight of a tile is 8 units, and chosen anew (O
+// rescaled) at a tile whose largest is beyond the codes or below 2^-4: rows that follow
+// one of large score or scale weigh little beside it, but there may be many. A tile's 64
+// rows are thus off by 2^-12 + 2^-8 of their sum at worst. Row scales multiply scores
+// and P in fp32. Maxima and sums are fp32.
 //
 // Schedule: one CTA per SM. The visible pages of all (sequence, head chunk)
 // units form one list that is cut evenly; a CTA whose piece covers a unit
@@ -117,10 +117,11 @@ struct Cfg {
   static_assert(kSlots <= 32, "phase bits");
   // log2 distance by which a score may exceed the maximum in use
   static constexpr float kLag = 64.f;
-  // FP8, a row's weight (2^score times its scale) in units, as log2: the largest of a tile
-  // may be at most kMost (448 is the largest code), is at least kLeast (64 keys), and is kAim where
-  // the unit is chosen; a head's unit never falls kReach below what its largest so far
-  // asked for (that one's share of O then still fits fp32; what is left out is 2^-40 of it)
+  // FP8, log2 of a row's weight in units: the largest of a tile may be at most kMost (448
+  // is the largest code), is at least kLeast (of a tile of 64 keys), and is kAim where the
+  // unit is chosen (3: 4 and 5 moved it more often; 2: the same time). A head's unit never
+  // falls kReach below what its largest weight so far asked for: that one's share of O
+  // then still fits fp32, and what is left out is 2^-40 of it.
   static constexpr float kMost = 8.75f, kLeast = -4.f, kAim = 3.f, kReach = 40.f;
 };
 
