@@ -466,8 +466,8 @@ PSW_API int attn_decode_latent(const psw_latent_t *layer, const void *q, const v
                                psw_stream_t stream);
 
 /* The same over FP8 pages (row_scale device fp32 [num_blocks][16]). Rows enter the sum
- * with their probability times row_scale; of a run of 64 rows, those for which that is
- * below 2^-21 of the run's largest may count as nothing. */
+ * with their probability times row_scale, which is resolved to 2^-21 of the largest of a
+ * run of 64 rows, or coarser where that loses 2^-9 of the probability at most. */
 PSW_API int attn_decode_latent_fp8(const psw_latent_t *layer, const void *q, const void *pool8,
                                    const float *row_scale, const psw_pages_t *pages,
                                    const int32_t *seq_lens, int32_t n_seqs, void *out, float *lse,

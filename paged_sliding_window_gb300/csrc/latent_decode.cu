@@ -20,9 +20,13 @@
 // scale, is taken in three parts, each 16 times finer than the one before: off by 2^-12
 // of itself, or by 2^-18 units where the third is subnormal. A head's unit is a power
 // of two, chosen so that the largest weight of a tile is 8 units, and chosen anew (O
-// rescaled) at a tile whose largest is beyond the codes or below 2^-4: rows that follow
-// one of large score or scale weigh little beside it, but there may be many. A tile's 64
-// rows are thus off by 2^-12 + 2^-8 of their sum at worst. Row scales multiply scores
+// rescaled) at a tile whose largest is beyond the codes, or below 2^-4 while 2^-18 units
+// of each of the segment's rows could add up to more than 2^-9 of the probability: rows
+// that follow one of large score or scale weigh little beside it, but there may be
+// many. (Where the rows' scales are alike that is so of segments of 2000 rows or more;
+// always when it is below 2^-4: 45 us instead of 37 for 64 sequences whose scores have
+// a deviation of 2.9.) What a tile's 64 rows are off by is thus 2^-12 + 2^-8 of their
+// sum at worst, or at most 2^-9 of the probability in all. Row scales multiply scores
 // and P in fp32. Maxima and sums are fp32.
 //
 // Schedule: one CTA per SM. The visible pages of all (sequence, head chunk)
@@ -45,13 +49,12 @@
 // Measured (latent 512, GPU time of a call in a graph of twelve, joins included; single
 // calls that follow on one another take the same). 64 sequences of 512 to 4096 rows, 16
 // heads: bf16 171 MB in 39.5 us (4.3 TB/s; a kernel that only gathers the pages takes
-// 30), FP8 86 MB in 32.5 us (with units that only ever rose, 30). 32 sequences of 1024
-// to 32768 rows, 32 heads, bf16: 321 MB in 67 us (4.8 TB/s). 3 sequences of 40001 to
-// 65536 rows, 24 heads, FP8: 80 MB in 38 us. About 4 us are start-up (lengths,
-// the cut, the first block ids and pages: loads that follow on one another) and 4
-// the join. In between bf16 is bound by the loads; FP8 by a tile's chain (scores,
-// softmax, three parts of P) and, at more than 16 heads, by shared memory, from which
-// two parts of q and three of P are read. A move of a unit costs 0.7 us. Heads beyond 32
+// 30), FP8 86 MB in 31.5 us. 32 sequences of 1024 to 32768 rows, 32 heads, bf16: 321 MB
+// in 67 us (4.8 TB/s). 3 sequences of 40001 to 65536 rows, 24 heads, FP8: 80 MB in 36
+// us. About 4 us are start-up (lengths, the cut, the first block ids and pages: loads
+// that follow on one another) and 4 the join. In between bf16 is bound by the loads;
+// FP8 by a tile's chain (scores, softmax, three parts of P) and, at more than 16 heads,
+// by shared memory, from which two parts of q and three of P are read. Heads beyond 32
 // are further units, each of which reads its pages again.
 #include <math.h>
 
@@ -95,7 +98,7 @@ struct Cfg {
   static constexpr int kLoadWarp = kScoreWarp + 2, kQueryWarp = kScoreWarp + 3;
   static constexpr int kQueryWarps = FP8 ? 4 : 1;
   static constexpr int kThreads = 32 * (kQueryWarp + kQueryWarps);
-  static constexpr int kMisc = FP8 ? 6144 : 2048;
+  static constexpr int kMisc = FP8 ? 6144 : 2560;
   static constexpr int kTileSlots = 1 + kBlocks * kSlotsPerBlock;
   static constexpr int kSlots = (kSmemLimit - 1024 - kMisc - kQBytes) / kSlotBytes;
   static constexpr int kSmemBytes = 1024 + kQBytes + kSlots * kSlotBytes + kMisc;
@@ -103,8 +106,8 @@ struct Cfg {
   static_assert(kTmemO + kBlocks * kPCols <= 512, "tensor memory columns");
   static_assert(kSlots >= 2 * kTileSlots + 1, "two tiles fit, a slot left out included");
   // FP8: row scales of the tiles in the ring, in turn (after the misc block)
-  static constexpr int kScaleTiles = 16;
-  static constexpr int kScales = 2048, kScaleBytes = kTile * 4;
+  static constexpr int kScaleTiles = 14;
+  static constexpr int kScales = 2560, kScaleBytes = kTile * 4;
   static_assert(!FP8 || (kScales + kScaleTiles * kScaleBytes <= kMisc &&
                          kSlots / kTileSlots + 2 <= kScaleTiles),
                 "no tile's scales are overwritten while it is in the ring");
@@ -118,11 +121,14 @@ struct Cfg {
   // log2 distance by which a score may exceed the maximum in use
   static constexpr float kLag = 64.f;
   // FP8, log2 of a row's weight in units: the largest of a tile may be at most kMost (448
-  // is the largest code), is at least kLeast (of a tile of 64 keys), and is kAim where the
-  // unit is chosen (3: 4 and 5 moved it more often; 2: the same time). A head's unit never
-  // falls kReach below what its largest weight so far asked for: that one's share of O
-  // then still fits fp32, and what is left out is 2^-40 of it.
-  static constexpr float kMost = 8.75f, kLeast = -4.f, kAim = 3.f, kReach = 40.f;
+  // is the largest code), and is kAim where the unit is chosen (3: 4 and 5 moved it more
+  // often). It is chosen anew too where the largest is below kLeast and the unit is
+  // coarse for some row of the tile: 2^-18 units of every row of the segment, with that
+  // row's scale, would be more than 2^(kSpare - 18) of the probability. (kSpare 8 is
+  // within what alike scales differ by in segments of 1000 rows: 34 us instead of 32.) A
+  // head's unit never falls kReach below what its largest weight so far asked for: that
+  // one's share of O then still fits fp32, and what is left out is 2^-40 of it.
+  static constexpr float kMost = 8.75f, kLeast = -4.f, kAim = 3.f, kSpare = 9.f, kReach = 40.f;
 };
 
 // The list, cut into n pieces: of q + 1 for the first r, of q for the others.
@@ -144,18 +150,15 @@ struct Misc {
   Cut cut;                   // of what all units count for
   int32_t p0, p1;            // this CTA's piece of it
   float red[4][kMaxHeads];
-  alignas(16) uint32_t near[8];  // FP8, by warp: see kNear
+  float heavy[4][kMaxHeads];  // FP8: by row warp, log2 of the largest weights
+  float faint[4];            // and of the smallest scale
   float qs[3][kMaxHeads];    // FP8, segments in turn: scale * log2(e) * a unit of q's codes
   float lsum[kMaxHeads];
   float alpha[kMaxHeads];    // factors of a rescale; at a segment's end, the maxima
   float top[kMaxHeads];      // FP8: the largest weight (log2) seen when units were chosen; at a
                              // segment's end, the root of what a unit stands for
 };
-// FP8: what a warp says of a tile: for each of its 16 heads whether some key weighs
-// 2^kLeast units or more; whether any key has a scale at all; whether the maximum or a
-// unit has to move up.
-constexpr uint32_t kNear = 0xFFFFu, kScaled = 1u << 16, kOver = 1u << 17;
-static_assert(sizeof(Misc) <= 2048, "misc block");
+static_assert(sizeof(Misc) <= 2560, "misc block");
 
 // Row scales of a page that is not there (its codes read as zeros).
 __device__ const float4 g_zero_scales[kBlockSize / 4] = {};
@@ -668,16 +671,13 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
       }
       const int h0 = w.chunk * NH, nh = min(NH, heads - h0), n_tiles = w.tiles();
       constexpr int HN = C::kHeads;
-      // FP8: ref is the log2 of the unit; bit i of `stuck`: head i's is as small as it may be
+      // FP8: ref is the log2 of the unit
       float m[HN], l[HN], ref[HN];
-      uint32_t stuck = 0;
+      // FP8: the unit of some head is coarse for a row if log2 of its scale is below `fine`
+      float fine = -INFINITY;
+      const float spare = C::kSpare - __log2f(static_cast<float>(w.seg_count * kBlockSize));
 #pragma unroll
       for (int i = 0; i < HN; ++i) m[i] = 0.f, l[i] = 0.f, ref[i] = 0.f;
-      // FP8: a last tile of few keys is as near to their sum with a smaller largest weight
-      const int page0 = w.span.first + w.seg_first;
-      const float last_least =
-          C::kLeast - 6.f + __log2f(static_cast<float>(min(w.span.len, (page0 + w.seg_count) * kBlockSize) -
-                                                       (page0 + (n_tiles - 1) * kPages) * kBlockSize));
       for (int t = seg < 0 ? -1 : 0; t < n_tiles; ++t) {
         const bool live = t >= 0;
         const bool in_seg = live && t * kPages + row_warp < w.seg_count;  // a page per warp
@@ -754,54 +754,25 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
           if (FP8) hi = fmaxf(hi, x - ref[i]), lo = fminf(lo, x - ref[i]);
         }
         bool move = !ok || t <= 0 || over > C::kLag;
-        // FP8: log2 of the rows' scales. A head's unit is too large if all of the tile's weights
-        // are small. Each thread with that head then finds its two small: where that is so (of
-        // some head) in all eight lanes that have the same heads, in the first row warp, all
-        // warps look head by head.
+        // FP8: log2 of the rows' scales, and whether a unit may have to move. One that is too
+        // coarse is so for a key of some warp, in which then each of the eight lanes of that
+        // head finds its two keys small; and a thread's two keys are not told apart here. Where
+        // that says yes, it is settled below head by head.
         float lv[2];
-        const float least = t == n_tiles - 1 ? last_least : C::kLeast;
         if constexpr (FP8) {
           lv[0] = __log2f(fabsf(vs[0]));
           lv[1] = __log2f(fabsf(vs[1]));
-          // (looked at without telling this thread's two keys apart, so that at worst it is
-          // looked at in vain)
-          const bool most = hi + fmaxf(lv[0], lv[1]) > C::kMost;
-          bool small = false;
-          if (row_warp == 0) {
-            uint32_t b = __ballot_sync(0xffffffffu, lo + fminf(lv[0], lv[1]) < least);
+          move |= hi + fmaxf(lv[0], lv[1]) > C::kMost;
+          if (__any_sync(0xffffffffu, (lv[0] > -INFINITY && lv[0] < fine) ||
+                                          (lv[1] > -INFINITY && lv[1] < fine))) {
+            uint32_t b = __ballot_sync(0xffffffffu, lo + fminf(lv[0], lv[1]) < C::kLeast);
             b &= b >> 16;
             b &= b >> 8;
             b &= b >> 4;
-            small = (b & 15u) != 0;
+            move |= (b & 15u) != 0;
           }
-          if (lat::bar_any(1, kSoftThreads, move || most || small)) {
-            uint32_t near = stuck;
-#pragma unroll
-            for (int i = 0; i < HN; ++i) {
-              const float at = fmaxf(z[0][i] + lv[0], z[1][i] + lv[1]) - ref[i];
-              near |= at >= least ? 1u << i : 0u;
-              move |= at > C::kMost;
-            }
-            const uint32_t w = __reduce_or_sync(
-                0xffffffffu, near << (4 * quad) | (fmaxf(lv[0], lv[1]) > -INFINITY ? kScaled : 0u) | (move ? kOver : 0u));
-            if (lane == 0) ms->near[warp] = w;
-            named_bar_sync(1, kSoftThreads);
-            uint32_t any = 0, all = kNear;
-#pragma unroll
-            for (int k = 0; k < C::kGroups; ++k) {
-              const uint4 four = *reinterpret_cast<const uint4*>(&ms->near[4 * k]);
-              const uint32_t of = (four.x | four.y) | (four.z | four.w);
-              any |= of;
-              all &= of;
-            }
-            move = (any & kOver) || ((any & kScaled) && all != kNear);
-          } else {
-            move = false;
-          }
-        } else {
-          move = lat::bar_any(1, kSoftThreads, move);
         }
-        if (move) {
+        if (lat::bar_any(1, kSoftThreads, move)) {
           // the tile's maxima; the ones in use move to them where they lag
 #pragma unroll
           for (int i = 0; i < HN; ++i) {
@@ -810,14 +781,21 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
             if (lane < 4) ms->red[row_warp][head_of(i)] = x;
           }
-          // O is rescaled below: the products up to the tile before have ended
-          if (t > 0 && ok) ok = mbar_wait(&ms->pv_done[(tile - 1) % 3], (tile - 1) / 3 & 1);
-          if (lat::bar_any(1, kSoftThreads, !ok)) {
-            ok = false;
-            break;
+          if constexpr (FP8) {  // the largest weights, the smallest scale
+#pragma unroll
+            for (int i = 0; i < HN; ++i) {
+              float x = fmaxf(z[0][i] + lv[0], z[1][i] + lv[1]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+              if (lane < 4) ms->heavy[row_warp][head_of(i)] = x;
+            }
+            const float x = lat::warp_max(fmaxf(lv[0] > -INFINITY ? -lv[0] : -INFINITY,
+                                                lv[1] > -INFINITY ? -lv[1] : -INFINITY));
+            if (lane == 0 && head0 == 0) ms->faint[row_warp] = -x;
           }
-          tc::fence_after();
-          float a[HN];
+          named_bar_sync(1, kSoftThreads);
+          float a[HN], top[HN];
+          bool moved = false;
 #pragma unroll
           for (int i = 0; i < HN; ++i) {
             const int h = head_of(i);
@@ -826,68 +804,71 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             if (t <= 0) {
               l[i] = 0.f;
               m[i] = x == -INFINITY ? 0.f : x;
-            } else if (x > m[i] + C::kLag) {
+            } else if (x > m[i] + (FP8 ? 0.f : C::kLag)) {  // (FP8: O does not depend on it)
               a[i] = ex2_approx(m[i] - x);
               l[i] *= a[i];
               m[i] = x;
             }
           }
-          float top[HN];
           if constexpr (FP8) {
-            // the units, from the tile's largest weights (O is in units whatever the maximum)
-            named_bar_sync(1, kSoftThreads);  // the maxima have been read
-#pragma unroll
-            for (int i = 0; i < HN; ++i) {
-              float x = fmaxf(z[0][i] + lv[0], z[1][i] + lv[1]);
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-              if (lane < 4) ms->red[row_warp][head_of(i)] = x;
-            }
-            named_bar_sync(1, kSoftThreads);
-            stuck = 0;
+            const float faint = fminf(fminf(ms->faint[0], ms->faint[1]), fminf(ms->faint[2], ms->faint[3]));
+            fine = -INFINITY;
 #pragma unroll
             for (int i = 0; i < HN; ++i) {
               const int h = head_of(i);
-              const float x = fmaxf(fmaxf(ms->red[0][h], ms->red[1][h]), fmaxf(ms->red[2][h], ms->red[3][h]));
+              const float x = fmaxf(fmaxf(ms->heavy[0][h], ms->heavy[1][h]), fmaxf(ms->heavy[2][h], ms->heavy[3][h]));
               const float old = ref[i];
               top[i] = t <= 0 ? x : fmaxf(ms->top[h], x);
               if (t <= 0) {
                 ref[i] = x > -INFINITY ? x - C::kAim : m[i];
-              } else if (x > -INFINITY && (x - old > C::kMost || x - old < least)) {
+              } else if (x - old > C::kMost ||
+                         (x > -INFINITY && x - old < C::kLeast && old - m[i] - spare > faint)) {
                 // (by a power of two, so that O keeps its bits)
                 ref[i] = fmaxf(old + rintf(x - C::kAim - old), top[i] - (C::kAim + C::kReach));
-                if (x - ref[i] < least) stuck |= 1u << i;
               }
+              fine = fmaxf(fine, ref[i] - m[i] - spare);
               a[i] = ex2_approx(fminf(old - ref[i], 100.f));  // (beyond: O is still zero)
             }
           }
 #pragma unroll
-          for (int i = 0; i < HN; ++i)
+          for (int i = 0; i < HN; ++i) {
+            moved |= a[i] != 1.f;
             if (row_warp == 0 && lane < 4) ms->alpha[head_of(i)] = a[i];
-          named_bar_sync(1, kSoftThreads);
+          }
+          moved = lat::bar_any(1, kSoftThreads, !ok || (t > 0 && moved));
           if constexpr (FP8) {
 #pragma unroll
             for (int i = 0; i < HN; ++i)
               if (row_warp == 0 && lane < 4) ms->top[head_of(i)] = top[i];
           }
-          if (t > 0) {
+          if (moved) {
+            // O is rescaled: the products up to the tile before have ended
+            if (t > 0) {
+              ok = __all_sync(0xffffffffu, ok && mbar_wait(&ms->pv_done[(tile - 1) % 3], (tile - 1) / 3 & 1));
+              if (ok) {
+                tc::fence_after();
 #pragma unroll 1
-            for (int blk = warp >> 2; blk < C::kBlocks; blk += C::kGroups) {
+                for (int blk = warp >> 2; blk < C::kBlocks; blk += C::kGroups) {
 #pragma unroll
-              for (int c = 0; c < C::kPCols / 16; ++c) {
-                uint32_t v[16];
-                const uint32_t at = tmem + lanes + C::kTmemO + blk * C::kPCols + c * 16;
-                tc::ld16(at, v);
-                tc::wait_ld();
+                  for (int c = 0; c < C::kPCols / 16; ++c) {
+                    uint32_t v[16];
+                    const uint32_t at = tmem + lanes + C::kTmemO + blk * C::kPCols + c * 16;
+                    tc::ld16(at, v);
+                    tc::wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  v[i] = __float_as_uint(__uint_as_float(v[i]) * ms->alpha[(c * 16 + i) % NH]);
-                tc::st16(at, v);
+                    for (int i = 0; i < 16; ++i)
+                      v[i] = __float_as_uint(__uint_as_float(v[i]) * ms->alpha[(c * 16 + i) % NH]);
+                    tc::st16(at, v);
+                  }
+                }
+                tc::wait_st();
               }
             }
-            tc::wait_st();
+            if (lat::bar_any(1, kSoftThreads, !ok)) {  // (and alpha may be written again)
+              ok = false;
+              break;
+            }
           }
-          named_bar_sync(1, kSoftThreads);  // red, top and alpha may be written again
         }
         // P into the rope slot: a key's row holds the parts of all heads,
         // 16-byte vectors swizzled by the row

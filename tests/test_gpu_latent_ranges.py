@@ -14,7 +14,8 @@ pytestmark = pytest.mark.gpu
 
 # FP8 pages. P times the row's scale is taken in three E4M3 parts, each 16 times finer than the one
 # before: off by 2^-12 of itself, or where the last part is subnormal by 2^-10 / 256 of the unit in
-# use, in which the largest of a tile's 64 rows is 2^-4 or more: 64 * 2^-18 / 2^-4 of their sum
+# use, in which the largest of a tile's 64 rows is 2^-4 or more: 64 * 2^-18 / 2^-4 of their sum;
+# or less, where all that it loses is 2^-9 of the probability at most
 P_ERR8 = 2.0 ** -12 + 2.0 ** -8
 
 
