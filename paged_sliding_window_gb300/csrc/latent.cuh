@@ -262,6 +262,14 @@ __device__ __forceinline__ void ld16x256_x2(uint32_t taddr, uint32_t (&r)[8]) {
       : "r"(taddr));
 }
 
+// 32 lanes x 32 bits of one column.
+__device__ __forceinline__ void ld1(uint32_t taddr, uint32_t& r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+}
+__device__ __forceinline__ void st1(uint32_t taddr, uint32_t r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
+}
+
 // Maximum over a warp (NaN inputs are ignored).
 __device__ __forceinline__ float warp_max(float v) {
   float r;

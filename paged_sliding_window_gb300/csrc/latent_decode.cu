@@ -44,13 +44,14 @@
 // and four heads) and the epilogue (a thread per dim); one warp loads pages,
 // one (FP8, which splits them into parts: four) the queries. The maximum that P
 // is relative to is taken from a segment's first tile and moved (O rescaled)
-// only when a score exceeds it by 2^64, so a tile costs its threads one barrier.
+// only when a score exceeds it by 2^64 (FP8: wherever units move), so that most tiles
+// cost their threads one barrier.
 //
 // Measured (latent 512, GPU time of a call in a graph of twelve, joins included; single
 // calls that follow on one another take the same). 64 sequences of 512 to 4096 rows, 16
 // heads: bf16 171 MB in 39.5 us (4.3 TB/s; a kernel that only gathers the pages takes
-// 30), FP8 86 MB in 31.5 us. 32 sequences of 1024 to 32768 rows, 32 heads, bf16: 321 MB
-// in 67 us (4.8 TB/s). 3 sequences of 40001 to 65536 rows, 24 heads, FP8: 80 MB in 36
+// 30), FP8 86 MB in 31 us. 32 sequences of 1024 to 32768 rows, 32 heads, bf16: 321 MB
+// in 67.5 us (4.8 TB/s). 3 sequences of 40001 to 65536 rows, 24 heads, FP8: 80 MB in 36
 // us. About 4 us are start-up (lengths, the cut, the first block ids and pages: loads
 // that follow on one another) and 4 the join. In between bf16 is bound by the loads;
 // FP8 by a tile's chain (scores, softmax, three parts of P) and, at more than 16 heads,
@@ -70,6 +71,11 @@ constexpr int kMaxCtas = 160;                   // pieces of the page list
 constexpr int kMinPages = 4;                    // pages a piece has at least
 constexpr int kMaxHeads = 32;                   // heads of a chunk
 constexpr int kSmemLimit = 232448;
+// FP8: up to so many heads whose O is rescaled are so column by column, and nothing of
+// the others is touched (3 long sequences: 48.7 -> 45.0 us for scores of a deviation of
+// 2.9, 39.0 -> 38.1 of 1.7); more go through all columns, as on bf16 pages, where a
+// maximum hardly ever moves.
+constexpr int kFewHeads = 4;
 
 __host__ __device__ inline int chunk_heads(int heads) { return heads <= 16 ? 16 : 32; }
 __host__ __device__ inline int chunks_of(int heads) {
@@ -151,7 +157,10 @@ struct Misc {
   int32_t p0, p1;            // this CTA's piece of it
   float red[4][kMaxHeads];
   float heavy[4][kMaxHeads];  // FP8: by row warp, log2 of the largest weights
-  float faint[4];            // and of the smallest scale
+  // FP8, by warp: a bit for each of its 16 heads, some key of the tile weighs 2^kLeast units
+  // or more, and 16 up, the unit is coarse for some key; whether something has to move up
+  alignas(16) uint32_t says[8];
+  alignas(16) uint32_t up[8];
   float qs[3][kMaxHeads];    // FP8, segments in turn: scale * log2(e) * a unit of q's codes
   float lsum[kMaxHeads];
   float alpha[kMaxHeads];    // factors of a rescale; at a segment's end, the maxima
@@ -757,8 +766,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         // FP8: log2 of the rows' scales, and whether a unit may have to move. One that is too
         // coarse is so for a key of some warp, in which then each of the eight lanes of that
         // head finds its two keys small; and a thread's two keys are not told apart here. Where
-        // that says yes, it is settled below head by head.
+        // that says yes, all warps look head by head.
         float lv[2];
+        uint32_t anew = 0;  // of this warp's heads: small and coarse
         if constexpr (FP8) {
           lv[0] = __log2f(fabsf(vs[0]));
           lv[1] = __log2f(fabsf(vs[1]));
@@ -772,7 +782,40 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             move |= (b & 15u) != 0;
           }
         }
-        if (lat::bar_any(1, kSoftThreads, move)) {
+        bool settle = lat::bar_any(1, kSoftThreads, move);
+        if constexpr (FP8) {
+          if (settle) {
+            move = !ok || t <= 0 || over > C::kLag;
+            uint32_t says = 0;
+#pragma unroll
+            for (int i = 0; i < HN; ++i) {
+              const float at = fmaxf(z[0][i] + lv[0], z[1][i] + lv[1]) - ref[i];
+              const float least = ref[i] - m[i] - spare;
+              move |= at > C::kMost;
+              says |= at >= C::kLeast ? 1u << i : 0u;
+              says |= (lv[0] > -INFINITY && lv[0] < least) || (lv[1] > -INFINITY && lv[1] < least)
+                          ? 0x10000u << i
+                          : 0u;
+            }
+            says = __reduce_or_sync(0xffffffffu, says << (4 * quad));
+            const bool up = __any_sync(0xffffffffu, move);
+            if (lane == 0) {
+              ms->says[warp] = says;
+              ms->up[warp] = up;
+            }
+            named_bar_sync(1, kSoftThreads);
+            settle = false;
+#pragma unroll
+            for (int k = 0; k < C::kGroups; ++k) {
+              const uint4 a4 = *reinterpret_cast<const uint4*>(&ms->says[4 * k]);
+              const uint4 u4 = *reinterpret_cast<const uint4*>(&ms->up[4 * k]);
+              const uint32_t of = (a4.x | a4.y) | (a4.z | a4.w);
+              settle |= ((u4.x | u4.y) | (u4.z | u4.w) | (of >> 16 & ~of)) != 0;
+              if (k == warp >> 2) anew = of >> 16 & ~of;
+            }
+          }
+        }
+        if (settle) {
           // the tile's maxima; the ones in use move to them where they lag
 #pragma unroll
           for (int i = 0; i < HN; ++i) {
@@ -781,7 +824,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
             if (lane < 4) ms->red[row_warp][head_of(i)] = x;
           }
-          if constexpr (FP8) {  // the largest weights, the smallest scale
+          if constexpr (FP8) {  // and the largest weights
 #pragma unroll
             for (int i = 0; i < HN; ++i) {
               float x = fmaxf(z[0][i] + lv[0], z[1][i] + lv[1]);
@@ -789,9 +832,6 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
               for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
               if (lane < 4) ms->heavy[row_warp][head_of(i)] = x;
             }
-            const float x = lat::warp_max(fmaxf(lv[0] > -INFINITY ? -lv[0] : -INFINITY,
-                                                lv[1] > -INFINITY ? -lv[1] : -INFINITY));
-            if (lane == 0 && head0 == 0) ms->faint[row_warp] = -x;
           }
           named_bar_sync(1, kSoftThreads);
           float a[HN], top[HN];
@@ -811,7 +851,6 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             }
           }
           if constexpr (FP8) {
-            const float faint = fminf(fminf(ms->faint[0], ms->faint[1]), fminf(ms->faint[2], ms->faint[3]));
             fine = -INFINITY;
 #pragma unroll
             for (int i = 0; i < HN; ++i) {
@@ -821,8 +860,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
               top[i] = t <= 0 ? x : fmaxf(ms->top[h], x);
               if (t <= 0) {
                 ref[i] = x > -INFINITY ? x - C::kAim : m[i];
-              } else if (x - old > C::kMost ||
-                         (x > -INFINITY && x - old < C::kLeast && old - m[i] - spare > faint)) {
+              } else if (x > -INFINITY &&
+                         (x - old > C::kMost || (anew >> (4 * quad + i) & 1u) != 0)) {
                 // (by a power of two, so that O keeps its bits)
                 ref[i] = fmaxf(old + rintf(x - C::kAim - old), top[i] - (C::kAim + C::kReach));
               }
@@ -847,18 +886,40 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap q_map,
               ok = __all_sync(0xffffffffu, ok && mbar_wait(&ms->pv_done[(tile - 1) % 3], (tile - 1) / 3 & 1));
               if (ok) {
                 tc::fence_after();
-#pragma unroll 1
-                for (int blk = warp >> 2; blk < C::kBlocks; blk += C::kGroups) {
+                const float f = FP8 && lane < NH ? ms->alpha[lane] : 1.f;
+                const uint32_t heads_moved = __ballot_sync(0xffffffffu, f != 1.f);
+                if (FP8 && __popc(heads_moved) <= kFewHeads) {  // their columns alone
+                  for (uint32_t left = heads_moved; left != 0; left &= left - 1) {
+                    const int h = __ffs(static_cast<int>(left)) - 1;
+                    const float by = __shfl_sync(0xffffffffu, f, h);
+                    constexpr int kMine = C::kBlocks / C::kGroups * C::kPParts;
+                    uint32_t v[kMine];
+                    auto at = [&](int k) {
+                      return tmem + lanes + C::kTmemO + h +
+                             ((warp >> 2) + k / C::kPParts * C::kGroups) * C::kPCols +
+                             k % C::kPParts * NH;
+                    };
 #pragma unroll
-                  for (int c = 0; c < C::kPCols / 16; ++c) {
-                    uint32_t v[16];
-                    const uint32_t at = tmem + lanes + C::kTmemO + blk * C::kPCols + c * 16;
-                    tc::ld16(at, v);
+                    for (int k = 0; k < kMine; ++k) lat::ld1(at(k), v[k]);
                     tc::wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                      v[i] = __float_as_uint(__uint_as_float(v[i]) * ms->alpha[(c * 16 + i) % NH]);
-                    tc::st16(at, v);
+                    for (int k = 0; k < kMine; ++k)
+                      lat::st1(at(k), __float_as_uint(__uint_as_float(v[k]) * by));
+                  }
+                } else {
+#pragma unroll 1
+                  for (int blk = warp >> 2; blk < C::kBlocks; blk += C::kGroups) {
+#pragma unroll
+                    for (int c = 0; c < C::kPCols / 16; ++c) {
+                      uint32_t v[16];
+                      const uint32_t at = tmem + lanes + C::kTmemO + blk * C::kPCols + c * 16;
+                      tc::ld16(at, v);
+                      tc::wait_ld();
+#pragma unroll
+                      for (int i = 0; i < 16; ++i)
+                        v[i] = __float_as_uint(__uint_as_float(v[i]) * ms->alpha[(c * 16 + i) % NH]);
+                      tc::st16(at, v);
+                    }
                   }
                 }
                 tc::wait_st();
