@@ -101,6 +101,7 @@ typedef struct CUstream_st *psw_stream_t;
 #define PSW_DEVERR_CAPACITY    2  /* sequence longer than its block-table row: clamped */
 #define PSW_DEVERR_LENGTH      4  /* negative length or non-monotone offsets: row skipped */
 #define PSW_DEVERR_PIPELINE    8  /* a bounded pipeline wait timed out: tile abandoned */
+#define PSW_DEVERR_NOBLOCKS   16  /* block_table_extend: the free list ran out, entries became -1 */
 
 /* Per-layer attention parameters. */
 typedef struct {
@@ -362,6 +363,120 @@ PSW_API int attn_decode_paged_fp8(const psw_layer_t *layer, const void *q, const
                                   const float *v_scale, const psw_pages_t *pages,
                                   const int32_t *seq_lens, int32_t n_seqs, float *out,
                                   float *lse, void *ws, size_t ws_bytes, psw_stream_t stream);
+
+/*
+ * ---- 4-bit KV pages: codes of 4 bits with a scale for every 16 values
+ *
+ * The library's own format, 9/32 of the bf16 bytes. With one float gs per
+ * tensor (k_scale, v_scale; the caller's, a power of two or not, in [2^-60,
+ * 2^60], the same in every call on a pool), a head vector x is taken in blocks
+ * of 16 values:
+ *   y = x * (1 / gs), limited to [-4096, 4096]
+ *   s = e4m3(max |y| * (1 / 6)), saturating at 448
+ *   code = e2m1(y / s): nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ *          negatives, ties to the even code, saturating
+ * in fp32 steps that round to nearest (1 / gs and 1 / 6 are fp32 numbers); a
+ * block whose s is 0 (max |y| below about 0.006) becomes zeros. The block stands
+ * for code * s * gs, and attention runs on those values. Magnitudes above 2688 gs
+ * saturate (4 bits hold no infinity or NaN: both become that end, and the
+ * others of their block lose to it), so gs = 1 serves
+ * normalised keys and values and others want max |x| / gs between 0.1 and 2688.
+ *
+ * A pool is uint8 [num_blocks][n_kv_heads][PSW_FP4_PAGE_BYTES(head_dim)], a page
+ * of one KV head being one run of bytes, 16-byte aligned:
+ *   codes  head_dim / 256 parts of [16 tokens][128 bytes]; part p of a token
+ *          holds values 256 p .. 256 p + 255 in eight 16-byte units of 32
+ *          values; unit u stands at place u ^ (token & 7). Byte b of a unit
+ *          holds the codes of its values 2 b (low half) and 2 b + 1; a code is
+ *          sign, two bits of exponent, one of mantissa.
+ *   scales [16 tokens][head_dim / 16] E4M3 bytes; block k = 8 c + 2 t + e (e in
+ *          {0, 1}, t in 0 .. 3) stands at byte t * (head_dim / 64) + 2 c' + e with
+ *          c' = c at head_dim 256 and 2 (c mod 2) + c / 2 at 512.
+ */
+#define PSW_FP4_PAGE_BYTES(head_dim) (9 * (head_dim))
+
+/* kv_cache_write into 4-bit pools: arguments as kv_cache_write, with the bf16
+ * rows k, v [n_new_total][n_kv_heads][head_dim] quantised as above. n_new_total is
+ * the host's count of rows: rows that cu_new names beyond it are not touched and
+ * flagged (PSW_DEVERR_LENGTH). Errors as kv_cache_write, PSW_EINVAL_SCALE for a
+ * tensor scale out of range. */
+PSW_API int kv_cache_write_fp4(const psw_layer_t *layer, const void *k, const void *v,
+                               const int32_t *cu_new, const int32_t *past_lens, int32_t n_seqs,
+                               int32_t n_new_total, const psw_pages_t *pages, void *k_pool4,
+                               void *v_pool4, float k_scale, float v_scale, psw_stream_t stream);
+
+/*
+ * Rows of 4-bit pages as bf16 pages: position pos of sequence b, for first[b] <=
+ * pos < seq_lens[b], goes to its slot of out_pages' pools (rounded once). A chunk's
+ * attention (attn_prefill_chunked) then runs on those; on a sliding layer only
+ * the positions that the chunk sees are wanted.
+ *   first      device int32 [n_seqs], or NULL (all 0)
+ *   pages, out_pages  tables of the 4-bit and of the bf16 pools
+ *   k_pool, v_pool    device bf16 [out_pages->num_blocks][16][n_kv_heads][head_dim];
+ *              rows outside the range keep what they held
+ * A source page with a bad block id gives zero rows, a bad id in out_pages writes
+ * nothing; both are flagged (PSW_DEVERR_BLOCK_ID). Lengths beyond either table's
+ * row are clamped and flagged, a negative length or first position flagged and the
+ * sequence skipped. n_seqs * max_blocks_per_seq must stay below 2^31
+ * (PSW_ECAPACITY).
+ */
+PSW_API int kv_cache_read_fp4(const psw_layer_t *layer, const void *k_pool4, const void *v_pool4,
+                              const psw_pages_t *pages, const int32_t *first,
+                              const int32_t *seq_lens, int32_t n_seqs,
+                              const psw_pages_t *out_pages, void *k_pool, void *v_pool,
+                              float k_scale, float v_scale, psw_stream_t stream);
+
+/* Workspace bytes of attn_decode_paged_fp4 for up to n_seqs sequences (host
+ * arithmetic). Its first PSW_FP4_COUNTER_BYTES bytes must be zero before the
+ * first call that uses it; every call leaves them zero again (but one that
+ * flagged PSW_DEVERR_PIPELINE: zero them then). Calls of any layer may share one
+ * in turn; calls that could overlap on the GPU need one each, and no other call
+ * of this library takes it. */
+#define PSW_FP4_COUNTER_BYTES 8192
+PSW_API int psw_fp4_workspace_bytes(const psw_layer_t *layer, int32_t n_seqs, size_t *bytes);
+
+/* attn_decode_paged over 4-bit pools: arguments, masks and errors as
+ * attn_decode_paged, but
+ *   out  device bf16 [n_seqs][n_q_heads][head_dim] (it feeds the next projection)
+ *   ws   device workspace, 16-byte aligned, of psw_fp4_workspace_bytes
+ * A page whose block id is outside the pool reads as zero rows and is flagged.
+ * n_seqs * max_blocks_per_seq * n_kv_heads * ceil(n_q_heads / n_kv_heads / 8) must
+ * stay below 2^31 (PSW_ECAPACITY). */
+PSW_API int attn_decode_paged_fp4(const psw_layer_t *layer, const void *q, const void *k_pool4,
+                                  const void *v_pool4, const psw_pages_t *pages,
+                                  const int32_t *seq_lens, int32_t n_seqs, void *out, float *lse,
+                                  void *ws, size_t ws_bytes, float k_scale, float v_scale,
+                                  psw_stream_t stream);
+
+/*
+ * The tables of a step, built on the device from the requests' lengths (so that a
+ * captured step needs nothing from the host): sequence b with past_lens[b] cached
+ * tokens gets new_lens[b] more.
+ *   cu_new     device int32 [n_seqs + 1], written: offsets of the new tokens
+ *   seq_lens   device int32 [n_seqs], written: past_lens + new_lens
+ *   block_table  device int32 [n_seqs][max_blocks_per_seq]: entries of the pages
+ *              that the new tokens begin, ceil(past / 16) .. ceil((past + new) / 16) - 1,
+ *              are written; the others are left as they are
+ *   free_ids   device int32 [n_free], ids of free pages, taken in order from
+ *              *free_pos on (device int32), sequence by sequence
+ *   free_next  device int32, written: *free_pos plus the pages taken; it may be
+ *              free_pos itself
+ *   slots      device int64 [n_slots], written for rows t below cu_new[n_seqs]:
+ *              block id * 16 + position mod 16 of the new token, -1 where it has
+ *              no page; or NULL
+ * No other two buffers may overlap. Entries that the list has no id for become -1
+ * (PSW_DEVERR_NOBLOCKS), pages beyond the row are left out
+ * (PSW_DEVERR_CAPACITY), a sequence with a negative length gets no new token and
+ * a past of at least 0, tokens beyond n_slots get no slot, a cursor outside [0,
+ * n_free] takes nothing (all PSW_DEVERR_LENGTH), a token on a page that the table had
+ * as negative gets -1 (PSW_DEVERR_BLOCK_ID). n_seqs * max_blocks_per_seq must stay
+ * below 2^31 (PSW_ECAPACITY). n_seqs 0 launches nothing.
+ */
+PSW_API int block_table_extend(int32_t *block_table, int32_t max_blocks_per_seq,
+                               const int32_t *past_lens, const int32_t *new_lens, int32_t n_seqs,
+                               const int32_t *free_ids, int32_t n_free, const int32_t *free_pos,
+                               int32_t *free_next, int32_t *cu_new, int32_t *seq_lens,
+                               int64_t *slots, int32_t n_slots, psw_stream_t stream);
 
 /*
  * ---- latent attention: keys and values from one shared latent row per token

@@ -27,6 +27,7 @@ ERRORS = {
     -21: "PSW_EINVAL_STRIDE",
 }
 DEVERR_BLOCK_ID, DEVERR_CAPACITY, DEVERR_LENGTH, DEVERR_PIPELINE = 1, 2, 4, 8
+DEVERR_NOBLOCKS = 16
 EXPORTED = ("psw_workspace_bytes", "kv_cache_write", "attn_decode_paged",
             "attn_prefill_chunked", "psw_get_error", "psw_strerror",
             "attn_decode_paged_noalloc", "qkv_norm_rope_cache_write", "psw_kv_share_map",
@@ -37,7 +38,9 @@ EXPORTED = ("psw_workspace_bytes", "kv_cache_write", "attn_decode_paged",
             "attn_decode_paged_fp8", "psw_testing_stall", "attn_decode_paged_append",
             "psw_latent_workspace_bytes", "latent_norm_rope_cache_write",
             "latent_norm_rope_cache_write_fp8", "attn_decode_latent", "attn_decode_latent_fp8",
-            "latent_kv_expand", "latent_kv_expand_fp8", "attn_prefill_latent")
+            "latent_kv_expand", "latent_kv_expand_fp8", "attn_prefill_latent",
+            "block_table_extend", "kv_cache_write_fp4", "kv_cache_read_fp4",
+            "psw_fp4_workspace_bytes", "attn_decode_paged_fp4")
 
 
 class PswLayer(ctypes.Structure):
@@ -156,6 +159,17 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                      "latent_norm_rope_cache_write_fp8", "attn_decode_latent",
                      "attn_decode_latent_fp8", "latent_kv_expand", "latent_kv_expand_fp8",
                      "attn_prefill_latent"):
+            getattr(lib, name).restype = ctypes.c_int
+        f32 = ctypes.c_float
+        lib.block_table_extend.argtypes = [vp, i32, vp, vp, i32, vp, i32, vp, vp, vp, vp, vp, i32,
+                                           vp]
+        lib.kv_cache_write_fp4.argtypes = [lp, vp, vp, vp, vp, i32, i32, pp, vp, vp, f32, f32, vp]
+        lib.kv_cache_read_fp4.argtypes = [lp, vp, vp, pp, vp, vp, i32, pp, vp, vp, f32, f32, vp]
+        lib.psw_fp4_workspace_bytes.argtypes = [lp, i32, ctypes.POINTER(sz)]
+        lib.attn_decode_paged_fp4.argtypes = [lp, vp, vp, vp, pp, vp, i32, vp, vp, vp, sz, f32, f32,
+                                              vp]
+        for name in ("block_table_extend", "kv_cache_write_fp4", "kv_cache_read_fp4",
+                     "psw_fp4_workspace_bytes", "attn_decode_paged_fp4"):
             getattr(lib, name).restype = ctypes.c_int
         lib.psw_testing_stall.argtypes = [i32, i32, i32]
         lib.psw_testing_stall.restype = ctypes.c_int
@@ -665,6 +679,185 @@ def attn_prefill_latent(layer, q, cu_q, past_lens, max_q_len: int, kv, k_rope, c
                                     _stream_of(dev, stream))
     if rc:
         _raise(rc, "attn_prefill_latent")
+
+
+# ---------------------------------------------------------------- 4-bit pages
+_LAYER_STRUCTS: dict = {}
+
+
+def _layer_struct(layer) -> PswLayer:
+    """make_layer's struct, one for all layers of the same fields (never handed out)."""
+    key = (int(layer.n_q_heads), int(layer.n_kv_heads), int(layer.head_dim), int(layer.window),
+           float(layer.softcap), float(layer.scale), int(bool(layer.k_eq_v)),
+           int(getattr(layer, "block_size", 16)))
+    got = _LAYER_STRUCTS.get(key)
+    if got is None:
+        if len(_LAYER_STRUCTS) >= 1024:
+            _LAYER_STRUCTS.clear()
+        got = _LAYER_STRUCTS[key] = PswLayer(*key)
+    return got
+
+
+def fp4_page_bytes(layer) -> int:
+    """Bytes of one page of one KV head in a 4-bit pool (PSW_FP4_PAGE_BYTES)."""
+    return 9 * int(layer.head_dim)
+
+
+def alloc_fp4_pool(layer, num_blocks: int, device="cuda") -> torch.Tensor:
+    """A zero-filled 4-bit pool, uint8 [num_blocks, n_kv_heads, fp4_page_bytes]."""
+    return torch.zeros(int(num_blocks), int(layer.n_kv_heads), fp4_page_bytes(layer),
+                       dtype=torch.uint8, device=device)
+
+
+def fp4_workspace_bytes(layer, n_seqs: int) -> int:
+    out = ctypes.c_size_t(0)
+    _raise(load().psw_fp4_workspace_bytes(ctypes.byref(_layer_struct(layer)), int(n_seqs),
+                                          ctypes.byref(out)), "psw_fp4_workspace_bytes")
+    return int(out.value)
+
+
+def alloc_fp4_workspace(layer, n_seqs: int, device="cuda") -> torch.Tensor:
+    """A caller-owned workspace for attn_decode_paged_fp4, its counters zeroed (calls keep them
+    zero); the rest of it needs no zeroing."""
+    ws = torch.empty(fp4_workspace_bytes(layer, n_seqs), dtype=torch.uint8, device=device)
+    ws[:FP4_COUNTER_BYTES].zero_()
+    return ws
+
+
+FP4_COUNTER_BYTES = 8192  # PSW_FP4_COUNTER_BYTES
+
+
+def _want_v(z, *vs):
+    for v, name in vs:
+        if (v is None) != bool(z.k_eq_v):
+            raise PswError(-7, f"{name} (k_eq_v is {bool(z.k_eq_v)})")
+
+
+def block_table_extend(block_table, past_lens, new_lens, free_ids, free_pos, free_next, cu_new,
+                       seq_lens, slots=None, stream=None) -> None:
+    """The tables of a step, built on the device: block_table int32 [n, max_blocks] gets entries
+    for the pages that new_lens int32 [n] tokens after past_lens [n] begin, from free_ids int32
+    [n_free] at the cursor free_pos int32 [1] on; free_next [1] (may be free_pos), cu_new [n + 1],
+    seq_lens [n] and slots int64 [rows] or None are written."""
+    dev, n = block_table.get_device(), past_lens.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] < n:
+        raise ValueError(f"block_table must have {n} rows or more, got {tuple(block_table.shape)}")
+    _want(block_table, _I32, block_table.shape, "block_table", dev)
+    _want(past_lens, _I32, (n,), "past_lens", dev)
+    _want(new_lens, _I32, (n,), "new_lens", dev)
+    _want(free_ids, _I32, (free_ids.numel(),), "free_ids", dev)
+    _want(free_pos, _I32, (1,), "free_pos", dev)
+    _want(free_next, _I32, (1,), "free_next", dev)
+    _want(cu_new, _I32, (n + 1,), "cu_new", dev)
+    _want(seq_lens, _I32, (n,), "seq_lens", dev)
+    slot_args = (None, 0)
+    if slots is not None:
+        _want(slots, torch.int64, (slots.numel(),), "slots", dev)
+        slot_args = (slots.data_ptr(), slots.shape[0])
+    if n == 0:
+        return
+    rc = load().block_table_extend(block_table.data_ptr(), block_table.shape[1],
+                                   past_lens.data_ptr(), new_lens.data_ptr(), n,
+                                   free_ids.data_ptr() or None, free_ids.shape[0],
+                                   free_pos.data_ptr(), free_next.data_ptr(), cu_new.data_ptr(),
+                                   seq_lens.data_ptr(), *slot_args, _stream_of(dev, stream))
+    if rc:
+        _raise(rc, "block_table_extend")
+
+
+def kv_cache_write_fp4(layer, k, v, cu_new, past_lens, pages: PswPages, k_pool4, v_pool4,
+                       k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
+    """kv_cache_write into 4-bit pools (alloc_fp4_pool): k, v bf16 [n_new, n_kv, head_dim], v and
+    v_pool4 None with k_eq_v; k_scale and v_scale are the pools' own, the same in every call."""
+    z = _layer_struct(layer)
+    dev, n, rows = k.get_device(), past_lens.shape[0], k.shape[0]
+    shape, pool = (rows, z.n_kv_heads, z.head_dim), (pages.num_blocks, z.n_kv_heads,
+                                                     9 * z.head_dim)
+    _want_v(z, (v, "v"), (v_pool4, "v_pool4"))
+    _want(k, _BF16, shape, "k", dev)
+    _want(cu_new, _I32, (n + 1,), "cu_new", dev)
+    _want(past_lens, _I32, (n,), "past_lens", dev)
+    _want(k_pool4, _U8, pool, "k_pool4", dev)
+    if v is not None:
+        _want(v, _BF16, shape, "v", dev)
+        _want(v_pool4, _U8, pool, "v_pool4", dev)
+    _want_rows(pages, n, dev)
+    if n == 0 or rows == 0:
+        return
+    rc = load().kv_cache_write_fp4(ctypes.byref(z), k.data_ptr(),
+                                   None if v is None else v.data_ptr(), cu_new.data_ptr(),
+                                   past_lens.data_ptr(), n, rows, ctypes.byref(pages),
+                                   k_pool4.data_ptr(), None if v is None else v_pool4.data_ptr(),
+                                   k_scale, v_scale, _stream_of(dev, stream))
+    if rc:
+        _raise(rc, "kv_cache_write_fp4")
+
+
+def kv_cache_read_fp4(layer, k_pool4, v_pool4, pages: PswPages, first, seq_lens,
+                      out_pages: PswPages, k_pool, v_pool, k_scale: float = 1.0,
+                      v_scale: float = 1.0, stream=None) -> None:
+    """Rows of 4-bit pages into bf16 pages: positions first[b] (int32 [n], or None: 0) to
+    seq_lens[b] of every sequence, from pages into the pools of out_pages (for the attention of a
+    chunk, attn_prefill_chunked)."""
+    z = _layer_struct(layer)
+    dev, n = k_pool4.get_device(), seq_lens.shape[0]
+    pool = (pages.num_blocks, z.n_kv_heads, 9 * z.head_dim)
+    wide = (out_pages.num_blocks, 16, z.n_kv_heads, z.head_dim)
+    _want_v(z, (v_pool4, "v_pool4"), (v_pool, "v_pool"))
+    _want(k_pool4, _U8, pool, "k_pool4", dev)
+    _want(k_pool, _BF16, wide, "k_pool", dev)
+    _want(seq_lens, _I32, (n,), "seq_lens", dev)
+    if first is not None:
+        _want(first, _I32, (n,), "first", dev)
+    if v_pool is not None:
+        _want(v_pool4, _U8, pool, "v_pool4", dev)
+        _want(v_pool, _BF16, wide, "v_pool", dev)
+    _want_rows(pages, n, dev)
+    _want_rows(out_pages, n, dev)
+    if n == 0:
+        return
+    rc = load().kv_cache_read_fp4(ctypes.byref(z), k_pool4.data_ptr(),
+                                  None if v_pool is None else v_pool4.data_ptr(),
+                                  ctypes.byref(pages), None if first is None else first.data_ptr(),
+                                  seq_lens.data_ptr(), n, ctypes.byref(out_pages),
+                                  k_pool.data_ptr(), None if v_pool is None else v_pool.data_ptr(),
+                                  k_scale, v_scale, _stream_of(dev, stream))
+    if rc:
+        _raise(rc, "kv_cache_read_fp4")
+
+
+def attn_decode_paged_fp4(layer, q, k_pool4, v_pool4, pages: PswPages, seq_lens, out, lse=None,
+                          ws=None, k_scale: float = 1.0, v_scale: float = 1.0,
+                          stream=None) -> None:
+    """attn_decode_paged over 4-bit pools; out is bf16 [n, n_q, head_dim], ws from
+    alloc_fp4_workspace (calls that may overlap on the GPU need one each)."""
+    z = _layer_struct(layer)
+    dev, n = q.get_device(), seq_lens.shape[0]
+    rows, pool = (n, z.n_q_heads, z.head_dim), (pages.num_blocks, z.n_kv_heads, 9 * z.head_dim)
+    _want_v(z, (v_pool4, "v_pool4"))
+    _want(q, _BF16, rows, "q", dev)
+    _want(k_pool4, _U8, pool, "k_pool4", dev)
+    if v_pool4 is not None:
+        _want(v_pool4, _U8, pool, "v_pool4", dev)
+    _want(seq_lens, _I32, (n,), "seq_lens", dev)
+    _want(out, _BF16, rows, "out", dev)
+    if lse is not None:
+        _want(lse, _F32, (n, z.n_q_heads), "lse", dev)
+    ws_ptr, ws_bytes = None, 0
+    if ws is not None:
+        if not ws.is_cuda or ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be a contiguous CUDA tensor on device {dev}")
+        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    _want_rows(pages, n, dev)
+    if n == 0:
+        return
+    rc = load().attn_decode_paged_fp4(ctypes.byref(z), q.data_ptr(), k_pool4.data_ptr(),
+                                      None if v_pool4 is None else v_pool4.data_ptr(),
+                                      ctypes.byref(pages), seq_lens.data_ptr(), n, out.data_ptr(),
+                                      None if lse is None else lse.data_ptr(), ws_ptr, ws_bytes,
+                                      k_scale, v_scale, _stream_of(dev, stream))
+    if rc:
+        _raise(rc, "attn_decode_paged_fp4")
 
 
 def kv_share_map(n_layers: int, pattern: int, n_shared: int = 0):

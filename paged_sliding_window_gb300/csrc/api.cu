@@ -72,6 +72,8 @@ DeviceState* current_device() {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+}  // namespace
+
 int check_layer(const psw_layer_t* layer, LayerArgs* out) {
   if (layer == nullptr) return PSW_ENULL;
   if (layer->n_q_heads <= 0 || layer->n_kv_heads <= 0 ||
@@ -93,8 +95,6 @@ int check_layer(const psw_layer_t* layer, LayerArgs* out) {
   return PSW_OK;
 }
 
-}  // namespace
-
 int check_pages(const psw_pages_t* pages) {
   if (pages == nullptr || pages->block_table == nullptr) return PSW_ENULL;
   if (pages->max_blocks_per_seq <= 0 || pages->num_blocks <= 0) return PSW_ECAPACITY;
@@ -105,14 +105,13 @@ int check_pages(const psw_pages_t* pages) {
   return PSW_OK;
 }
 
-namespace {
-
-// k_eq_v: V must be absent; otherwise present.
 int check_v(const LayerArgs& L, const void* v_ptr) {
   if (L.k_eq_v && v_ptr != nullptr) return PSW_EINVAL_KEQV;
   if (!L.k_eq_v && v_ptr == nullptr) return PSW_EINVAL_KEQV;
   return PSW_OK;
 }
+
+namespace {
 
 int device_ready(DeviceState** st) {
   *st = current_device();

@@ -1,0 +1,297 @@
+// fp4_cache.cu -- rows into 4-bit pages and back.
+//
+// Write: a head vector x of HD bf16 values becomes, per block of 16 values,
+//   y = x * (1 / gs) in [-4096, 4096],  s = e4m3(max|y| / 6),  code = e2m1(y / s)
+// (fp32 steps rounded to nearest; gs is the tensor's scale, given by the
+// caller), so that code * s * gs stands for x. The division is the correctly
+// rounded one: the codes' borders are numbers that y / s meets exactly, and a
+// product with 1 / s would put some of those on the wrong side.
+//
+// Both directions are bound by memory: 2 HD bytes on one side of a row, 9/16
+// HD on the other.
+#include "fp4.cuh"
+#include "latent.cuh"
+
+namespace psw {
+namespace {
+
+using fp4::Page;
+
+constexpr int kWarps = 8;
+constexpr int kRows = 4;  // rows (heads of one token, K's before V's) per warp
+
+// One warp takes kRows rows of one token: at HD 256 a lane holds 8 values (a
+// block is two lanes), at HD 512 16 (a block each). The rows are asked for
+// before the token's sequence, page and slot are looked up.
+template <int HD>
+__global__ void __launch_bounds__(kWarps * 32)
+fp4_write_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
+                 const int32_t* __restrict__ cu_new, const int32_t* __restrict__ past_lens,
+                 int n_seqs, int n_new_total, const int32_t* __restrict__ block_table,
+                 int max_blocks, int64_t num_blocks, int n_kv, int groups, float k_inv,
+                 float v_inv, uint8_t* __restrict__ k_pool, uint8_t* __restrict__ v_pool,
+                 int32_t* err) {
+  constexpr int kVec = HD / 256;  // 16-byte vectors per lane and row
+  const int lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int t = static_cast<int>(item / groups);
+  const int row0 = static_cast<int>(item - static_cast<int64_t>(t) * groups) * kRows;
+  if (t >= n_new_total) return;
+  const int total = __ldg(cu_new + n_seqs);
+  if (t == 0 && row0 == 0 && lane == 0 && total > n_new_total) flag_error(err, PSW_DEVERR_LENGTH);
+  const int rows = v_pool != nullptr ? 2 * n_kv : n_kv;
+  uint4 in[kRows][kVec];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int row = row0 + i;
+    if (row < rows) {
+      const bool is_v = row >= n_kv;
+      const uint4* src = (is_v ? v : k) +
+                         (static_cast<int64_t>(t) * n_kv + (is_v ? row - n_kv : row)) * (HD / 8) +
+                         lane * kVec;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) in[i][e] = __ldg(src + e);
+    }
+  }
+  if (t >= total) return;
+  int b, start;
+  if (!lat::owner_of(cu_new, n_seqs, t, lane, b, start)) {
+    if (lane == 0) flag_error(err, PSW_DEVERR_LENGTH);
+    return;
+  }
+  const int64_t pos = static_cast<int64_t>(__ldg(past_lens + b)) + (t - start);
+  const int64_t page = pos / kBlockSize;
+  if (pos < 0 || page >= max_blocks) {
+    if (lane == 0) flag_error(err, pos < 0 ? PSW_DEVERR_LENGTH : PSW_DEVERR_CAPACITY);
+    return;
+  }
+  const int32_t blk = __ldg(block_table + static_cast<int64_t>(b) * max_blocks + page);
+  if (blk < 0 || blk >= num_blocks) {
+    if (lane == 0) flag_error(err, PSW_DEVERR_BLOCK_ID);
+    return;
+  }
+  const int r = static_cast<int>(pos % kBlockSize);
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int row = row0 + i;
+    if (row >= rows) break;
+    const bool is_v = row >= n_kv;
+    uint8_t* dst = (is_v ? v_pool : k_pool) +
+                   (static_cast<int64_t>(blk) * n_kv + (is_v ? row - n_kv : row)) * Page<HD>::kBytes;
+    const float inv = is_v ? v_inv : k_inv;
+    float y[8 * kVec], amax = 0.f;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      float x[8];
+      lat::unpack8(in[i][e], x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // (a NaN becomes the upper end)
+        y[8 * e + j] = fmaxf(fminf(__fmul_rn(x[j], inv), 4096.f), -4096.f);
+        amax = fmaxf(amax, fabsf(y[8 * e + j]));
+      }
+    }
+    if (HD == 256) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    const uint32_t s8 = fp4::block_scale(amax);
+    const float s = fp4::e4m3_float(s8);
+    const float rs = s > 0.f ? __frcp_rn(s) : 0.f;
+    uint32_t w[kVec];
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      w[e] = 0;
+#pragma unroll
+      for (int j = 0; j < 8; j += 2)
+        w[e] |= fp4::e2m1_pair(fp4::quotient(y[8 * e + j], s, rs),
+                               fp4::quotient(y[8 * e + j + 1], s, rs))
+                << (4 * j);
+    }
+    if constexpr (HD == 256) {
+      *reinterpret_cast<uint32_t*>(dst + Page<HD>::unit(r, lane >> 2) + (lane & 3) * 4) = w[0];
+      if ((lane & 1) == 0) dst[Page<HD>::scale(r, lane >> 1)] = static_cast<uint8_t>(s8);
+    } else {
+      *reinterpret_cast<uint2*>(dst + Page<HD>::unit(r, lane >> 1) + (lane & 1) * 8) =
+          make_uint2(w[0], w[1]);
+      dst[Page<HD>::scale(r, lane)] = static_cast<uint8_t>(s8);
+    }
+  }
+}
+
+}  // namespace
+
+int launch_fp4_write(const LayerArgs& L, const void* k, const void* v, const int32_t* cu_new,
+                     const int32_t* past_lens, int n_seqs, int n_new_total,
+                     const psw_pages_t& pages, void* k_pool, void* v_pool, float k_scale,
+                     float v_scale, int32_t* err, cudaStream_t stream) {
+  const int rows = L.n_kv * (L.k_eq_v ? 1 : 2);
+  const int groups = (rows + kRows - 1) / kRows;
+  const int64_t items = static_cast<int64_t>(n_new_total) * groups;
+  const int64_t blocks = (items + kWarps - 1) / kWarps;
+  if (blocks > INT32_MAX) return PSW_ECAPACITY;
+  auto* fn = L.hd == 256 ? fp4_write_kernel<256> : fp4_write_kernel<512>;
+  fn<<<static_cast<unsigned>(blocks), kWarps * 32, 0, stream>>>(
+      static_cast<const uint4*>(k), static_cast<const uint4*>(v), cu_new, past_lens, n_seqs,
+      n_new_total, pages.block_table, pages.max_blocks_per_seq, pages.num_blocks, L.n_kv, groups,
+      1.f / k_scale, 1.f / v_scale, static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool),
+      err);
+  return cudaGetLastError() == cudaSuccess ? PSW_OK : PSW_ELAUNCH;
+}
+
+// ---------------------------------------------------------------- read-back
+namespace {
+
+constexpr int kReadThreads = 256;
+
+// The pages wanted of all sequences form one list; with every (KV head, tensor)
+// of a page they are the items, of which each warp of a persistent grid takes
+// an equal run. A lane turns one block of 16 values (8 bytes and a scale) of a
+// token into 32 bytes, so that a warp's store is whole rows: two tokens at HD
+// 256, one at HD 512.
+template <int HD>
+__global__ void __launch_bounds__(kReadThreads)
+fp4_read_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ v_pool,
+                const int32_t* __restrict__ table, int max_blocks, int64_t num_blocks,
+                const int32_t* __restrict__ first, const int32_t* __restrict__ seq_lens,
+                int n_seqs, const int32_t* __restrict__ out_table, int out_max_blocks,
+                int64_t out_num_blocks, int n_kv, float k_scale, float v_scale,
+                uint8_t* __restrict__ k_out, uint8_t* __restrict__ v_out, int32_t* err) {
+  constexpr int kTok = 512 / HD;               // tokens per warp store
+  constexpr int kSteps = kBlockSize / kTok;
+  constexpr int kLanes = HD / 16;              // lanes of a token
+  __shared__ int s_run[kReadThreads + 1];
+  __shared__ int s_warp[kReadThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cap = min(max_blocks, out_max_blocks) * kBlockSize;
+  auto pages_of = [&](int b, bool flag) {
+    int len = __ldg(seq_lens + b), lo = first != nullptr ? __ldg(first + b) : 0;
+    if (len < 0 || lo < 0) {
+      if (flag) flag_error(err, PSW_DEVERR_LENGTH);
+      len = 0;
+    } else if (len > cap) {
+      if (flag) flag_error(err, PSW_DEVERR_CAPACITY);
+      len = cap;
+    }
+    return fp4::seq_pages(len, max(lo, 0));
+  };
+  // pages before each thread's run of sequences
+  const int per = (n_seqs + kReadThreads - 1) / kReadThreads;
+  int mine = 0;
+  for (int b = tid * per; b < min(n_seqs, (tid + 1) * per); ++b)
+    mine += pages_of(b, blockIdx.x == 0).np;
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  int before = 0;
+  for (int i = 0; i < warp; ++i) before += s_warp[i];
+  s_run[tid + 1] = before + incl;
+  if (tid == 0) s_run[0] = 0;
+  __syncthreads();
+  const int rows = v_out != nullptr ? 2 * n_kv : n_kv;
+  const int64_t items = static_cast<int64_t>(s_run[kReadThreads]) * rows;
+  const int64_t workers = static_cast<int64_t>(gridDim.x) * (kReadThreads / 32);
+  const int64_t me = static_cast<int64_t>(blockIdx.x) * (kReadThreads / 32) + warp;
+  int64_t item = items * me / workers;
+  const int64_t end = items * (me + 1) / workers;
+  if (item >= end) return;
+  // the sequence of the first item
+  int page = static_cast<int>(item / rows), row = static_cast<int>(item - static_cast<int64_t>(page) * rows);
+  int a = 0, z = kReadThreads;  // s_run[a] <= page < s_run[z]
+  while (z - a > 1) {
+    const int mid = (a + z) >> 1;
+    if (s_run[mid] <= page) a = mid; else z = mid;
+  }
+  int b = a * per, off = s_run[a];
+  fp4::SeqPages s = pages_of(b, false);
+  while (page >= off + s.np) {
+    off += s.np;
+    s = pages_of(++b, false);
+  }
+  const int tok = lane / kLanes, blk16 = lane % kLanes;
+  bool looked_up = false;
+  int32_t src = 0, dst = 0;
+  for (; item < end; ++item) {
+    if (!looked_up) {
+      const int p = s.p0 + page - off;
+      src = __ldg(table + static_cast<int64_t>(b) * max_blocks + p);
+      dst = __ldg(out_table + static_cast<int64_t>(b) * out_max_blocks + p);
+      if ((src < 0 || src >= num_blocks || dst < 0 || dst >= out_num_blocks) && row == 0 &&
+          lane == 0)
+        flag_error(err, PSW_DEVERR_BLOCK_ID);
+      looked_up = true;
+    }
+    if (dst >= 0 && dst < out_num_blocks) {
+      const bool is_v = row >= n_kv;
+      const int head = is_v ? row - n_kv : row;
+      const bool have = src >= 0 && src < num_blocks;
+      const uint8_t* in = (is_v ? v_pool : k_pool) +
+                          (static_cast<int64_t>(have ? src : 0) * n_kv + head) * Page<HD>::kBytes;
+      uint8_t* out = (is_v ? v_out : k_out) +
+                     (static_cast<int64_t>(dst) * kBlockSize * n_kv + head) * (HD * 2) + blk16 * 32;
+      const float gs = is_v ? v_scale : k_scale;
+      uint2 c[kSteps];
+      uint32_t s8[kSteps];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int r = i * kTok + tok;
+        c[i] = __ldg(reinterpret_cast<const uint2*>(in + Page<HD>::unit(r, blk16 >> 1) +
+                                                    (blk16 & 1) * 8));
+        s8[i] = __ldg(in + Page<HD>::scale(r, blk16));
+      }
+      const int pos0 = (s.p0 + page - off) * kBlockSize;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int r = i * kTok + tok;
+        const float f = have ? fp4::e4m3_float(s8[i]) : 0.f;
+        uint32_t w[8];
+        const uint32_t cw[2] = {have ? c[i].x : 0u, have ? c[i].y : 0u};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t p[4] = {fp4::codes_f16<0>(cw[h]), fp4::codes_f16<1>(cw[h]),
+                                 fp4::codes_f16<2>(cw[h]), fp4::codes_f16<3>(cw[h])};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 x = fp4::f16x2_to_float2(p[j]);  // (code * scale is exact)
+            w[4 * h + j] = pack_bf16x2(x.x * f * gs, x.y * f * gs);
+          }
+        }
+        const int pos = pos0 + r;
+        if (pos >= s.lo && pos < s.len) {
+          uint8_t* o = out + static_cast<int64_t>(r) * n_kv * (HD * 2);
+          *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(o + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+    }
+    if (++row == rows) {
+      row = 0;
+      looked_up = false;
+      ++page;
+      while (item + 1 < end && page >= off + s.np) {
+        off += s.np;
+        s = pages_of(++b, false);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+int launch_fp4_read(const LayerArgs& L, const void* k_pool, const void* v_pool,
+                    const psw_pages_t& pages, const int32_t* first, const int32_t* seq_lens,
+                    int n_seqs, const psw_pages_t& out_pages, void* k_out, void* v_out,
+                    float k_scale, float v_scale, int num_sms, int32_t* err,
+                    cudaStream_t stream) {
+  auto* fn = L.hd == 256 ? fp4_read_kernel<256> : fp4_read_kernel<512>;
+  fn<<<num_sms * 4, kReadThreads, 0, stream>>>(
+      static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), pages.block_table,
+      pages.max_blocks_per_seq, pages.num_blocks, first, seq_lens, n_seqs, out_pages.block_table,
+      out_pages.max_blocks_per_seq, out_pages.num_blocks, L.n_kv, k_scale, v_scale,
+      static_cast<uint8_t*>(k_out), static_cast<uint8_t*>(v_out), err);
+  return cudaGetLastError() == cudaSuccess ? PSW_OK : PSW_ELAUNCH;
+}
+
+}  // namespace psw

@@ -42,6 +42,12 @@ int check_decode_args(const psw_layer_t* layer, const void* q, const void* k_poo
                       const void* v_pool, const psw_pages_t* pages, const int32_t* seq_lens,
                       int32_t n_seqs, const float* out, LayerArgs* L);
 
+// Host checks of a layer; fills *out on success. Returns a PSW_* code.
+int check_layer(const psw_layer_t* layer, LayerArgs* out);
+
+// A V pointer is absent with k_eq_v and present without. Returns a PSW_* code.
+int check_v(const LayerArgs& L, const void* v_ptr);
+
 // Host checks of a page table argument. Returns a PSW_* code.
 int check_pages(const psw_pages_t* pages);
 
@@ -204,5 +210,33 @@ int launch_latent_prefill(const LatentArgs& L, const void* q, const int32_t* cu_
                           const void* kv, const void* k_rope, const int32_t* cu_k,
                           const int32_t* k_first, int n_k_total, void* out, float* lse,
                           int num_sms, int32_t* err, cudaStream_t stream);
+
+// ---- 4-bit pages (fp4_*.cu) and tables built on the device (block_tables.cu)
+// Decode workspace: merge tickets (one int32 per worker, a warp of the grid;
+// zero between calls), then one slot of partial results per worker and unit.
+constexpr int kFp4MaxWorkers = PSW_FP4_COUNTER_BYTES / 4;
+constexpr size_t kFp4CounterBytes = PSW_FP4_COUNTER_BYTES;
+
+int launch_block_table_extend(int32_t* block_table, int max_blocks, const int32_t* past_lens,
+                              const int32_t* new_lens, int n_seqs, const int32_t* free_ids,
+                              int n_free, const int32_t* free_pos, int32_t* free_next,
+                              int32_t* cu_new, int32_t* seq_lens, int64_t* slots, int n_slots,
+                              int32_t* err, cudaStream_t stream);
+
+int launch_fp4_write(const LayerArgs& L, const void* k, const void* v, const int32_t* cu_new,
+                     const int32_t* past_lens, int n_seqs, int n_new_total,
+                     const psw_pages_t& pages, void* k_pool, void* v_pool, float k_scale,
+                     float v_scale, int32_t* err, cudaStream_t stream);
+
+int launch_fp4_read(const LayerArgs& L, const void* k_pool, const void* v_pool,
+                    const psw_pages_t& pages, const int32_t* first, const int32_t* seq_lens,
+                    int n_seqs, const psw_pages_t& out_pages, void* k_out, void* v_out,
+                    float k_scale, float v_scale, int num_sms, int32_t* err, cudaStream_t stream);
+
+size_t fp4_decode_workspace(const LayerArgs& L, int n_seqs);
+int launch_fp4_decode(const LayerArgs& L, const void* q, const void* k_pool, const void* v_pool,
+                      const psw_pages_t& pages, const int32_t* seq_lens, int n_seqs, void* out,
+                      float* lse, void* ws, float k_scale, float v_scale, int num_sms,
+                      int32_t* err, cudaStream_t stream);
 
 }  // namespace psw
