@@ -736,10 +736,11 @@ PSW_API const char *psw_strerror(int code);
 /*
  * Testing hook for the bounded pipeline waits; not for production use.
  * kernel 1 (attn_decode_paged, attn_decode_paged_fp8, attn_decode_latent,
- * attn_decode_latent_fp8) or 2 (attn_prefill_chunked): from the next launch of
+ * attn_decode_latent_fp8, attn_decode_paged_fp4) or 2 (attn_prefill_chunked): from
+ * the next launch of
  * such a kernel on, the TMA producer of CTA `cta` leaves its copy number `tile`
- * (counted from 0 over its own K tiles) unissued and stops, without flagging
- * anything. The
+ * (counted from 0 over its own K tiles; attn_decode_paged_fp4: over the pages of
+ * its first warp) unissued and stops, without flagging anything. The
  * consumer waiting for that copy then gives up after its bound (about one
  * second), sets PSW_DEVERR_PIPELINE and abandons the CTA's remaining work;
  * the producer still waits for every copy it did issue, and kernels that

@@ -4,20 +4,23 @@ so any slot that a kernel should not use shows."""
 import numpy as np
 import torch
 
-from latent_harness import BF16, F64, attend, check, check_attention, cu, gen, i32, no_error, randn, takes_error  # noqa: F401
+from latent_harness import BF16, F64, attend, check, cu, gen, i32, no_error, randn, takes_error  # noqa: F401
 from paged_sliding_window_gb300 import binding
 from paged_sliding_window_gb300.workloads import Layer  # noqa: F401
 
 PAGE = 16
 GRID = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 
-# What a decode's weights and scores may be off by (check_attention). P is rounded once, to fp16: half
-# a step, 2^-11 of it, and 2^-25 of the unit of the smallest (which is at most 2^-6 of the largest
-# weight: at most 2^-31 of it for each of up to 2^16 keys). A score: q in fp16 is exact but for 2^-39
-# of the head's largest, K's codes times scales are exact in fp16; 32 products of 16 terms are summed
-# in fp32, each step off by at most 17 units of 2^-24 of what is summed so far (32 * 17 * 2^-24 < 2^-14).
+# What a decode's weights and scores may be off by. P = 2^(z - m) is rounded once, to fp16: by half a
+# step, 2^-11 of it, or by 2^-25 where it is below 2^-14. As m is at least 6 below the largest z, the sum
+# of P is at least 2^6, so the second adds at most 2^-25 / 2^6 |v_j| for every key j to a result:
+# P_ABS * sum |v_j|. A score: q in fp16 is exact but for 2^-39 of the head's largest, K's codes times
+# scales are exact in fp16; 32 products of 16 terms are summed in fp32, each step off by at most 17
+# units of 2^-24 of what is summed so far (32 * 17 * 2^-24 < 2^-14).
 P_ERR = 2.0 ** -11 + 2.0 ** -15
+P_ABS = 2.0 ** -31
 S_ERR = 2.0 ** -14
+H_BF16 = 2.0 ** -8  # half a step of the result
 
 
 def places(hd, device="cuda"):
@@ -98,9 +101,19 @@ class Cache:
         return unpack(pool[used], self.layer.head_dim, gs)[at, :, pos % PAGE]
 
 
+def check_decode(out, lse, ref, what):
+    """Bounds of a decode [heads, hd]: the weights' and the scores' errors (once in the numerator, once in
+    the sum; 2^-18 covers the exponential, the sums and the division), one rounding to bf16."""
+    o, l, absv, mag, all_v = ref
+    e = (mag * S_ERR).clamp(max=0.25)
+    check(out, o, H_BF16 * o.abs() * 1.01 + absv * (P_ERR + 3 * e + 2.0 ** -18)[:, None] + 1.01 * P_ABS * all_v, what + " out")
+    if lse is not None:
+        check(lse, l, 1.2 * e + 2.0 ** -20 * (l.abs() + 4), what + " lse")
+
+
 def decode_ref(layer, cache, q, b, n, gs=(1.0, 1.0), zero=()):
-    """Attention of sequence b of n keys: per query head, (out, lse, weighted |v|, magnitude), heads first.
-    zero: positions whose rows are zeros."""
+    """Attention of sequence b of n keys: per query head, (out, lse, weighted |v|, magnitude of a score,
+    sum of |v|). zero: positions whose rows are zeros."""
     lo = max(0, n - layer.window) if layer.window else 0
     k = cache.rows(cache.k, b, lo, n, gs[0])
     v = k if layer.k_eq_v else cache.rows(cache.v, b, lo, n, gs[1])
@@ -110,7 +123,8 @@ def decode_ref(layer, cache, q, b, n, gs=(1.0, 1.0), zero=()):
             k[p - lo], v[p - lo] = 0, 0
     G = layer.n_q_heads // layer.n_kv_heads
     k, v = (x.transpose(0, 1).repeat_interleave(G, 0) for x in (k, v))
-    return attend(q[b].to(F64)[:, None], k, v, torch.tensor([n - 1], device="cuda"), torch.arange(lo, n, device="cuda"), layer)
+    ref = attend(q[b].to(F64)[:, None], k, v, torch.tensor([n - 1], device="cuda"), torch.arange(lo, n, device="cuda"), layer)
+    return (*(x[:, 0] for x in ref), v.abs().sum(1))
 
 
 def normed(g, *shape):
