@@ -432,7 +432,7 @@ PSW_API int kv_cache_read_fp4(const psw_layer_t *layer, const void *k_pool4, con
  * flagged PSW_DEVERR_PIPELINE: zero them then). Calls of any layer may share one
  * in turn; calls that could overlap on the GPU need one each, and no other call
  * of this library takes it. */
-#define PSW_FP4_COUNTER_BYTES 8192
+#define PSW_FP4_COUNTER_BYTES 2048
 PSW_API int psw_fp4_workspace_bytes(const psw_layer_t *layer, int32_t n_seqs, size_t *bytes);
 
 /* attn_decode_paged over 4-bit pools: arguments, masks and errors as
@@ -440,8 +440,9 @@ PSW_API int psw_fp4_workspace_bytes(const psw_layer_t *layer, int32_t n_seqs, si
  *   out  device bf16 [n_seqs][n_q_heads][head_dim] (it feeds the next projection)
  *   ws   device workspace, 16-byte aligned, of psw_fp4_workspace_bytes
  * A page whose block id is outside the pool reads as zero rows and is flagged.
- * n_seqs * max_blocks_per_seq * n_kv_heads * ceil(n_q_heads / n_kv_heads / 8) must
- * stay below 2^31 (PSW_ECAPACITY). */
+ * n_seqs * max_blocks_per_seq * n_kv_heads * ceil(n_q_heads / n_kv_heads / 8) and
+ * the bytes of a block, n_kv_heads * PSW_FP4_PAGE_BYTES, must stay below 2^31
+ * (PSW_ECAPACITY). */
 PSW_API int attn_decode_paged_fp4(const psw_layer_t *layer, const void *q, const void *k_pool4,
                                   const void *v_pool4, const psw_pages_t *pages,
                                   const int32_t *seq_lens, int32_t n_seqs, void *out, float *lse,

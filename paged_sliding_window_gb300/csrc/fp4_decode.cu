@@ -25,10 +25,13 @@
 //    below 2^14 and what lies 30 octaves below the largest is still counted.
 //  * q is multiplied by a power of two per head so that its largest value lies in
 //    [2^14, 2^15): in f16 all but values 2^-28 of that are exact.
-//  * A worker's pieces: units that lie in its run alone are written out. The last
-//    piece of every warp meets those of the CTA's other warps in shared memory;
-//    what is left of a unit goes to the workspace, and whoever adds the
-//    unit's last pages (a ticket counts them) joins its pieces, in their order.
+//  * A worker's pieces: units that lie in its run alone are written out. Of the
+//    others it has at most two, the end of one unit (kept in the workspace, its CTA
+//    alone reads it) and the beginning or middle of another (left in shared memory
+//    where the ring was). The CTA joins what its warps have of a unit; only units
+//    that other CTAs have pages of, two at most, go on to the workspace, and the CTA
+//    that adds a unit's last pages (a ticket counts them) joins the CTAs' parts, in
+//    their order.
 #include "fp4.cuh"
 #include "latent.cuh"
 
@@ -36,6 +39,9 @@ namespace psw {
 namespace {
 
 using fp4::Page;
+
+constexpr int kMaxCtas = 160;  // one per SM; what they need of workspace is counted with it
+constexpr int kMaxWarps = 12;
 
 template <int HD, bool KEQV>
 struct Cfg {
@@ -48,14 +54,15 @@ struct Cfg {
   static constexpr int kStages = kRingBytes / kStageBytes;
   static constexpr int kQBytes = HD == 256 ? 0 : HD * 8 * 2;  // per warp: q as operands (HD 512)
   static constexpr int kSmem = kWarps * (kRingBytes + kQBytes);
+  static_assert(kWarps <= kMaxWarps && 2 * kWarps <= 32, "pieces of a CTA");
+  static_assert(2 * kQHeadsPerUnit * kMaxCtas * 4 <= kRingBytes, "weights of two units");
   static_assert(kStages * kStageBytes == kRingBytes, "ring");
   static_assert(HD * 8 * 4 <= kRingBytes, "a piece's output fits where the ring was");
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
       "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -93,8 +100,8 @@ struct Args {
   const __nv_bfloat16* q;
   const uint8_t *k_pool, *v_pool;
   const int32_t *table, *seq_lens;
-  int max_blocks;
-  int64_t num_blocks;
+  int max_blocks, num_blocks;
+  uint32_t page_stride;  // bytes of a block in a pool
   int n_seqs, n_q, n_kv, group, qchunks, window;
   float scale, softcap;  // scale: the layer's times K's tensor scale
   float v_scale;
@@ -102,7 +109,7 @@ struct Args {
   float* lse;
   float4* ws_o;      // [slot][half of a row's pairs ...], see piece_unit
   float2* ws_ml;     // [slot][rows]
-  int32_t* tickets;  // [worker]
+  int32_t* tickets;  // [CTA]: of the unit that it begins and does not end
   int rows;          // rows of a slot: the group's heads, 8 at most, made even
   int32_t* err;
   int stall_cta, stall_tile;
@@ -135,6 +142,14 @@ struct Cursor {
   }
 };
 
+// A unit's first query head, and how many it has.
+__device__ __forceinline__ int first_head(const Args& a, int j) {
+  return j / a.qchunks * a.group + j % a.qchunks * kQHeadsPerUnit;
+}
+__device__ __forceinline__ int heads_of(const Args& a, int j) {
+  return min(kQHeadsPerUnit, a.group - j % a.qchunks * kQHeadsPerUnit);
+}
+
 // What a piece is to the others: its unit and how many of the unit's pages it has.
 struct Piece {
   int b, j, tile0, np, pages;
@@ -156,70 +171,38 @@ template <int HD>
 __device__ __forceinline__ void write_out(const Args& a, const Piece& p, int nh, const Unit4& u,
                                           const float4& o, float inv) {
   if (u.head >= nh) return;
-  const int kv = p.j / a.qchunks, h0 = kv * a.group + p.j % a.qchunks * kQHeadsPerUnit;
-  __nv_bfloat16* dst = a.out + (static_cast<int64_t>(p.b) * a.n_q + h0 + u.head) * HD + u.d;
+  __nv_bfloat16* dst =
+      a.out + (static_cast<int64_t>(p.b) * a.n_q + first_head(a, p.j) + u.head) * HD + u.d;
   const float f = inv * a.v_scale;
   *reinterpret_cast<uint2*>(dst) =
       make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
 }
 __device__ __forceinline__ void write_lse(const Args& a, const Piece& p, int head, float m,
                                           float l) {
-  const int kv = p.j / a.qchunks, h0 = kv * a.group + p.j % a.qchunks * kQHeadsPerUnit;
   if (a.lse != nullptr)
-    a.lse[static_cast<int64_t>(p.b) * a.n_q + h0 + head] = (m + log2f(l)) * lat::kLn2;
-}
-__device__ __forceinline__ int heads_of(const Args& a, int j) {
-  return min(kQHeadsPerUnit, a.group - j % a.qchunks * kQHeadsPerUnit);
+    a.lse[static_cast<int64_t>(p.b) * a.n_q + first_head(a, p.j) + head] =
+        (m + log2f(l)) * lat::kLn2;
 }
 
-// The worker that has entry x of a list of `tiles` pages cut for `workers`.
-__device__ __forceinline__ int worker_of(int x, int tiles, int workers) {
-  return static_cast<int>(((static_cast<int64_t>(x) + 1) * workers - 1) / tiles);
-}
-__device__ __forceinline__ int run_begin(int w, int tiles, int workers) {
-  return static_cast<int>(static_cast<int64_t>(w) * tiles / workers);
-}
 
-// Joins all pieces of a unit from the workspace: M = max m_i, l = sum l_i 2^(m_i - M),
-// out = sum O_i 2^(m_i - M) / l. There is one piece per CTA (of the unit's first warp there),
-// and one more if the last worker's run goes on behind the unit.
-template <int HD, bool KEQV>
-__device__ void join(const Args& a, const Piece& p, int tiles, int workers, int tid, int threads) {
-  constexpr int W = Cfg<HD, KEQV>::kWarps;
-  const int ups = a.n_kv * a.qchunks, u = p.b * ups + p.j, nh = heads_of(a, p.j);
-  const int hp = a.rows / 2, units = HD / 256 * 128 * hp;
-  const int wf = worker_of(p.tile0, tiles, workers);
-  const int wl = worker_of(p.tile0 + p.np - 1, tiles, workers);
-  const int cf = wf / W, cl = wl / W;
-  const bool extra =
-      run_begin(wl + 1, tiles, workers) > p.tile0 + p.np && max(wf, cl * W) < wl;
-  const int n = cl - cf + 1 + (extra ? 1 : 0);
-  auto slot = [&](int i) {
-    const int c = cf + i;
-    return static_cast<int64_t>(c > cl ? wl : max(wf, c * W)) + u;
-  };
-  for (int x = tid; x < units; x += threads) {
-    const Unit4 q = piece_unit(x, hp);
-    if (q.head >= nh) continue;
-    float M = -INFINITY, l = 0.f;
-    for (int i = 0; i < n; ++i) M = fmaxf(M, __ldcg(&a.ws_ml[slot(i) * a.rows + q.head]).x);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const int64_t s = slot(i);
-      const float2 ml = __ldcg(&a.ws_ml[s * a.rows + q.head]);
-      const float4 v = __ldcg(&a.ws_o[s * units + x]);
-      const float f = exp2f(ml.x - M);
-      l += ml.y * f;
-      o.x += v.x * f;
-      o.y += v.y * f;
-      o.z += v.z * f;
-      o.w += v.w * f;
-    }
-    write_out<HD>(a, p, nh, q, o, 1.f / l);
-    if (q.d == 0) write_lse(a, p, q.head, M, l);
+// The list of `tiles` pages cut into runs for `workers`: of each + 1 pages for the first
+// `more` of them, of `each` for the others.
+struct Cut {
+  int each, more;
+  __device__ int begin(int w) const { return w * each + min(w, more); }
+  __device__ int worker(int x) const {  // that has entry x
+    const int y = x - more * (each + 1);
+    return y < 0 ? x / (each + 1) : more + y / each;
   }
-}
+};
+
+// What a CTA has of one unit: pieces `members` (bit 2 w: the end of the unit that warp w
+// began with, bit 2 w + 1: the last unit of warp w), `pages` of its pages.
+struct Group {
+  Piece p;
+  uint32_t members;
+  int pages;
+};
 
 template <int HD, bool KEQV>
 __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1)
@@ -230,9 +213,12 @@ fp4_decode_kernel(const Args a) {
   __shared__ uint64_t s_full[W][C::kStages];
   __shared__ int s_run[C::kThreads + 1];
   __shared__ int s_sum[W];
-  __shared__ Piece s_piece[W];
-  __shared__ float2 s_ml[W][kQHeadsPerUnit];
-  __shared__ int s_last[W];
+  __shared__ Piece s_piece[2 * W];
+  __shared__ float2 s_ml[2 * W][kQHeadsPerUnit];
+  __shared__ Group s_group[2 * W];
+  __shared__ float s_weight[2 * W][kQHeadsPerUnit];
+  __shared__ int s_groups;
+  __shared__ int s_last[2];  // group + 1
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * C::kRingBytes;
@@ -251,7 +237,8 @@ fp4_decode_kernel(const Args a) {
     if (lane >= o) incl += x;
   }
   if (lane == 31) s_sum[warp] = incl;
-  if (lane == 0) s_piece[warp].pages = 0;
+  if (lane < 2) s_piece[2 * warp + lane].pages = 0;
+  if (tid < 2) s_last[tid] = 0;
   __syncthreads();
   int before = 0, all = 0;
   for (int i = 0; i < W; ++i) {
@@ -262,13 +249,13 @@ fp4_decode_kernel(const Args a) {
   if (tid == 0) s_run[0] = 0;
   __syncthreads();
   const int tiles = all * ups;
-  const int workers = min(static_cast<int>(gridDim.x) * W, tiles);
+  const int workers = max(1, min(static_cast<int>(gridDim.x) * W, tiles));
+  const Cut cut{tiles / workers, tiles % workers};
   const int me = blockIdx.x * W + warp;
 
   bool failed = false;
-  if (me < workers) {
-    const int begin = run_begin(me, tiles, workers);
-    const int n = run_begin(me + 1, tiles, workers) - begin;
+  if (me < min(workers, tiles)) {
+    const int begin = cut.begin(me), n = cut.begin(me + 1) - begin;
     Cursor c;  // of the page that is worked on
     {
       const int page = begin / ups;  // units of a sequence are equal: find its sequence by pages
@@ -290,45 +277,49 @@ fp4_decode_kernel(const Args a) {
       c.tile0 = begin - c.page;
     }
     Cursor f = c;  // of the next page to fetch
-    int fetched = 0, ids_at = 0;
-    int32_t ids = 0;
-    uint32_t bad = 0;  // a bit per stage: its page has no valid block
-    bool ids_ok = false;
-    auto fetch = [&]() {
+    const uint8_t *f_k, *f_v;  // its KV head in block 0
+    int32_t ids;               // lane i: block of page 32 n + i, the 32 that f.page is among
+    uint32_t bad = 0;          // a bit per stage: its page has no valid block
+    const int stall = static_cast<int>(blockIdx.x) == a.stall_cta && warp == 0 ? a.stall_tile : -1;
+    auto fetch_head = [&]() {
+      const int64_t at = static_cast<int64_t>(f.j / a.qchunks) * Page<HD>::kBytes;
+      f_k = a.k_pool + at;
+      if (!KEQV) f_v = a.v_pool + at;
+    };
+    auto fetch_ids = [&]() {
+      const int at = (f.page & ~31) + lane;
+      ids = at < f.s.np
+                ? __ldg(a.table + static_cast<int64_t>(f.b) * a.max_blocks + f.s.p0 + at)
+                : 0;
+    };
+    auto fetch = [&](int i) {  // page i of the run
       if (f.page == f.s.np) {
         f.next_unit(a, ups);
-        ids_ok = false;
+        fetch_head();
+        // its queries are wanted when the pages before it are done
+        const char* q = reinterpret_cast<const char*>(
+            a.q + (static_cast<int64_t>(f.b) * a.n_q + first_head(a, f.j)) * HD);
+        for (int k = lane * 128; k < heads_of(a, f.j) * HD * 2; k += 32 * 128)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q + k));
       }
-      if (!ids_ok || f.page - ids_at >= 32) {
-        ids_at = f.page;
-        ids_ok = true;
-        ids = f.page + lane < f.s.np
-                  ? __ldg(a.table + static_cast<int64_t>(f.b) * a.max_blocks + f.s.p0 + f.page + lane)
-                  : 0;
-      }
-      int32_t blk = __shfl_sync(0xffffffffu, ids, f.page - ids_at);
-      const int st = fetched % C::kStages;
-      bad &= ~(1u << st);
-      if (blk < 0 || blk >= a.num_blocks) {
+      if ((f.page & 31) == 0) fetch_ids();
+      int32_t blk = __shfl_sync(0xffffffffu, ids, f.page & 31);
+      const int st = i & (C::kStages - 1);
+      if (static_cast<uint32_t>(blk) >= static_cast<uint32_t>(a.num_blocks)) {
         bad |= 1u << st;
         if (lane == 0) flag_error(a.err, PSW_DEVERR_BLOCK_ID);
         blk = 0;
       }
-      if (lane == 0 && !(static_cast<int>(blockIdx.x) == a.stall_cta && warp == 0 &&
-                         fetched == a.stall_tile)) {
-        const int64_t at =
-            (static_cast<int64_t>(blk) * a.n_kv + f.j / a.qchunks) * Page<HD>::kBytes;
+      if (lane == 0 && i != stall) {
+        const int64_t at = static_cast<int64_t>(blk) * a.page_stride;
         const uint32_t dst = smem_u32(ring + st * C::kStageBytes);
         mbar_arrive_expect_tx(&s_full[warp][st], C::kStageBytes);
-        lat::bulk_load(dst, a.k_pool + at, Page<HD>::kBytes, &s_full[warp][st]);
+        lat::bulk_load(dst, f_k + at, Page<HD>::kBytes, &s_full[warp][st]);
         if (!KEQV)
-          lat::bulk_load(dst + Page<HD>::kBytes, a.v_pool + at, Page<HD>::kBytes,
-                         &s_full[warp][st]);
+          lat::bulk_load(dst + Page<HD>::kBytes, f_v + at, Page<HD>::kBytes, &s_full[warp][st]);
       }
       ++f.page;
-      ++fetched;
     };
-    for (int i = 0; i < min(n, C::kStages); ++i) fetch();
 
     // tokens of this lane: rows g, g + 8 of S^T are tokens r0, r0 + 8; key slots 2 t, 2 t + 1
     // (and + 8) of P are tokens ra, rb (and + 8). This order keeps both products' loads free of
@@ -345,20 +336,21 @@ fp4_decode_kernel(const Args a) {
     float qf[2];              // factor of the scores of heads 2 t, 2 t + 1
     float acc[HD / 16][4];    // value 32 g + 2 i (+ 256 part): heads 2 t, 2 t + 1; the next value: same
     float m[2], l[2];
-    bool open = false;
     int piece_from = 0;
+    uint32_t first_seen = 0, last_seen = 0;  // a bit per token of the unit's first and last page
+    uint4 raw[C::kChunks][4];
 
-    auto begin_piece = [&]() {
-      const int nh = heads_of(a, c.j);
-      const int kv = c.j / a.qchunks, h0 = kv * a.group + c.j % a.qchunks * kQHeadsPerUnit;
-      const uint4* src = reinterpret_cast<const uint4*>(
-                             a.q + (static_cast<int64_t>(c.b) * a.n_q + h0 + min(g, nh - 1)) * HD) +
-                         t * 4;
-      uint4 raw[C::kChunks][4];
+    auto load_q = [&]() {
+      const int row = first_head(a, c.j) + min(g, heads_of(a, c.j) - 1);
+      const uint4* src =
+          reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(c.b) * a.n_q + row) * HD) +
+          t * 4;
 #pragma unroll
       for (int k = 0; k < C::kChunks; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) raw[k][i] = __ldg(src + k * 16 + i);
+    };
+    auto begin_piece = [&]() {
       uint32_t top = 0;  // the largest |q|, as bf16 bits
 #pragma unroll
       for (int k = 0; k < C::kChunks; ++k)
@@ -374,7 +366,7 @@ fp4_decode_kernel(const Args a) {
       const int e = max(static_cast<int>(big >> 7), 15);  // exponent of 2 + 127
       const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);    // 2^(141 - e)
       const float down = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);   // 2^(e - 141)
-      const bool live = g < nh;
+      const bool live = g < heads_of(a, c.j);
       uint32_t pk[HD == 256 ? 1 : 4];
 #pragma unroll
       for (int k = 0; k < C::kChunks; ++k)
@@ -398,8 +390,9 @@ fp4_decode_kernel(const Args a) {
         for (int x = 0; x < 4; ++x) acc[i][x] = 0.f;
       m[0] = m[1] = -INFINITY;
       l[0] = l[1] = 0.f;
-      open = true;
       piece_from = c.page;
+      first_seen = (0xFFFFu << (c.s.lo & (kBlockSize - 1))) & 0xFFFFu;
+      last_seen = 0xFFFFu >> (kBlockSize - 1 - ((c.s.len - 1) & (kBlockSize - 1)));
     };
     auto sum_l = [&]() {
 #pragma unroll
@@ -424,20 +417,24 @@ fp4_decode_kernel(const Args a) {
           }
     };
 
+    load_q();  // (in front of the pages: behind them it would wait for all)
+    fetch_head();
+    fetch_ids();
+    for (int i = 0; i < min(n, C::kStages); ++i) fetch(i);
+    begin_piece();
     for (int it = 0; it < n; ++it) {
-      if (c.page == c.s.np) c.next_unit(a, ups);
-      if (!open) begin_piece();
-      const int st = it % C::kStages;
+      const int st = it & (C::kStages - 1);
       if (!mbar_wait(&s_full[warp][st], (it / C::kStages) & 1)) {
+        if (lane == 0) flag_error(a.err, PSW_DEVERR_PIPELINE);
         failed = true;
+        for (int i = it + 1; i < min(n, it + C::kStages); ++i)  // copies in flight have to land
+          mbar_wait(&s_full[warp][i & (C::kStages - 1)], (i / C::kStages) & 1);
         break;
       }
       const uint8_t* page = ring + st * C::kStageBytes;
+      uint32_t seen = c.page == 0 ? first_seen : 0xFFFFu;  // a bit per token: visible
+      if (c.page == c.s.np - 1) seen &= last_seen;
       const bool is_bad = (bad >> st) & 1;
-      const int pos0 = (c.s.p0 + c.page) * kBlockSize;
-      uint32_t seen = 0xFFFFu;  // a bit per token: visible
-      if (c.s.len - pos0 < kBlockSize) seen &= (1u << (c.s.len - pos0)) - 1u;
-      if (c.s.lo > pos0) seen &= 0xFFFFu << (c.s.lo - pos0);
 
       // ---- S^T = K Q^T
       float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
@@ -511,13 +508,15 @@ fp4_decode_kernel(const Args a) {
           m[x] = mn;
           l[x] *= al[x];
         }
+        const uint64_t al2 = f2_pack(al[0], al[1]);
 #pragma unroll
-        for (int i = 0; i < HD / 16; ++i) {
-          acc[i][0] *= al[0];
-          acc[i][1] *= al[1];
-          acc[i][2] *= al[0];
-          acc[i][3] *= al[1];
-        }
+        for (int i = 0; i < HD / 16; ++i)
+#pragma unroll
+          for (int x = 0; x < 4; x += 2) {
+            const float2 r = f2_unpack(f2_mul(f2_pack(acc[i][x], acc[i][x + 1]), al2));
+            acc[i][x] = r.x;
+            acc[i][x + 1] = r.y;
+          }
       }
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -577,7 +576,8 @@ fp4_decode_kernel(const Args a) {
         }
       }
       __syncwarp();  // every lane has read the stage
-      if (fetched < n) fetch();
+      bad &= ~(1u << st);
+      if (it + C::kStages < n) fetch(it + C::kStages);
       ++c.page;
       if (c.page == c.s.np && it + 1 < n) {  // the unit ends and the run goes on
         const Piece p{c.b, c.j, c.tile0, c.s.np, c.page - piece_from};
@@ -585,7 +585,7 @@ fp4_decode_kernel(const Args a) {
         const int nh = heads_of(a, c.j);
         if (p.pages == p.np) {
           const float inv[2] = {1.f / l[0], 1.f / l[1]};
-          const int kv = c.j / a.qchunks, h0 = kv * a.group + c.j % a.qchunks * kQHeadsPerUnit;
+          const int h0 = first_head(a, c.j);
 #pragma unroll
           for (int odd = 0; odd < 2; ++odd) {
             if (2 * t + odd >= nh) continue;
@@ -607,115 +607,169 @@ fp4_decode_kernel(const Args a) {
             if (g == 0) write_lse(a, p, 2 * t + odd, m[odd], l[odd]);
           }
         } else {
-          const int64_t slot = static_cast<int64_t>(me) + c.b * ups + c.j;
-          put(a.ws_o + slot * (C::kParts * 128 * hp));
-          if (g == 0 && t < hp) {
-            a.ws_ml[slot * a.rows + 2 * t] = make_float2(m[0], l[0]);
-            a.ws_ml[slot * a.rows + 2 * t + 1] = make_float2(m[1], l[1]);
+          put(a.ws_o + static_cast<int64_t>(me) * (C::kParts * 128 * hp));
+          if (g == 0) {
+            s_ml[2 * warp][2 * t] = make_float2(m[0], l[0]);
+            s_ml[2 * warp][2 * t + 1] = make_float2(m[1], l[1]);
           }
-          __threadfence();
-          __syncwarp();
-          int last = 0;
-          if (lane == 0) {
-            int32_t* ticket = a.tickets + worker_of(p.tile0, tiles, workers);
-            last = atomicAdd(ticket, p.pages) + p.pages == p.np;
-            if (last) *ticket = 0;
-          }
-          if (__shfl_sync(0xffffffffu, last, 0)) {
-            __threadfence();
-            join<HD, KEQV>(a, p, tiles, workers, lane, 32);
-          }
+          if (lane == 0) s_piece[2 * warp] = p;
         }
-        open = false;
+        c.next_unit(a, ups);
+        load_q();
+        begin_piece();
       }
     }
-    if (failed) {  // give up, but not before the copies in flight have landed
-      if (lane == 0) flag_error(a.err, PSW_DEVERR_PIPELINE);
-      const int at = c.tile0 + c.page - begin;
-      for (int i = at + 1; i < fetched; ++i)
-        mbar_wait(&s_full[warp][i % C::kStages], (i / C::kStages) & 1);
-    } else {
+    if (!failed) {
       sum_l();
       put(reinterpret_cast<float4*>(ring));
       if (g == 0) {
-        s_ml[warp][2 * t] = make_float2(m[0], l[0]);
-        s_ml[warp][2 * t + 1] = make_float2(m[1], l[1]);
+        s_ml[2 * warp + 1][2 * t] = make_float2(m[0], l[0]);
+        s_ml[2 * warp + 1][2 * t + 1] = make_float2(m[1], l[1]);
       }
-      if (lane == 0) s_piece[warp] = Piece{c.b, c.j, c.tile0, c.s.np, c.page - piece_from};
+      if (lane == 0) s_piece[2 * warp + 1] = Piece{c.b, c.j, c.tile0, c.s.np, c.page - piece_from};
     }
   }
   __syncthreads();
 
-  // ---- the warps' last pieces: runs of warps that share a unit
-  const int units = C::kParts * 128 * hp;
-  auto first_of_run = [&](int w) {
-    return s_piece[w].pages > 0 &&
-           (w == 0 || s_piece[w - 1].pages == 0 || s_piece[w - 1].tile0 != s_piece[w].tile0);
-  };
-  auto run_end = [&](int w, int& pages) {
-    int e = w;
-    pages = 0;
-    for (; e < W && s_piece[e].pages > 0 && s_piece[e].tile0 == s_piece[w].tile0; ++e)
-      pages += s_piece[e].pages;
-    return e;
-  };
-  bool cut = false;  // some run is not its whole unit
-  for (int w = 0; w < W; ++w) {
-    if (!first_of_run(w)) continue;
-    const Piece p = s_piece[w];
-    int pages;
-    const int e = run_end(w, pages);
-    const bool whole = pages == p.np;
-    cut |= !whole;
-    const int nh = heads_of(a, p.j);
-    const int64_t slot = static_cast<int64_t>(blockIdx.x) * W + w + p.b * ups + p.j;
-    for (int x = tid; x < units; x += C::kThreads) {
-      const Unit4 u = piece_unit(x, hp);
-      if (u.head >= nh) continue;
+  // ---- the pieces of one unit are neighbours: groups of them
+  if (warp == 0) {
+    const Piece p = s_piece[min(lane, 2 * W - 1)];
+    const bool valid = lane < 2 * W && p.pages > 0;
+    const uint32_t have = __ballot_sync(0xffffffffu, valid);
+    const uint32_t prev = have & ((1u << lane) - 1u);
+    const int before_me = __shfl_sync(0xffffffffu, p.tile0, prev != 0 ? 31 - __clz(prev) : 0);
+    const bool starts = valid && (prev == 0 || before_me != p.tile0);
+    const uint32_t start = __ballot_sync(0xffffffffu, starts);
+    if (starts) {
+      const uint32_t after = start & ~((2u << lane) - 1u);
+      const uint32_t members = have & ~((1u << lane) - 1u) & (after != 0 ? (after & -after) - 1u : ~0u);
+      int pages = 0;
+      for (uint32_t i = members; i != 0; i &= i - 1) pages += s_piece[__ffs(i) - 1].pages;
+      s_group[__popc(start & ((1u << lane) - 1u))] = Group{p, members, pages};
+    }
+    if (lane == 0) s_groups = __popc(start);
+  }
+  __syncthreads();
+  const int units = C::kParts * 128 * hp, groups = s_groups;
+  const int64_t part0 = static_cast<int64_t>(gridDim.x) * W;  // slots of the CTAs' parts
+  // weights of a group's pieces, a lane each: M = max m_i, 2^(m_i - M), over the sum of l where
+  // the unit is complete
+  for (int y = warp; y < groups * kQHeadsPerUnit; y += W) {
+    const Group& gr = s_group[y / kQHeadsPerUnit];
+    const int head = y % kQHeadsPerUnit;
+    if (head >= heads_of(a, gr.p.j)) continue;
+    const bool mine_too = (gr.members >> lane) & 1;
+    const float2 ml = mine_too ? s_ml[lane][head] : make_float2(-INFINITY, 0.f);
+    const float M = lat::warp_max(ml.x);
+    float w = mine_too ? ex2_approx(ml.x - M) : 0.f;
+    float L = w * ml.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const bool whole = gr.pages == gr.p.np;
+    if (whole) w *= 1.f / L;
+    if (mine_too) s_weight[lane][head] = w;
+    if (lane == 0) {
+      if (whole)
+        write_lse(a, gr.p, head, M, L);
+      else
+        a.ws_ml[(part0 + blockIdx.x + gr.p.b * ups + gr.p.j) * a.rows + head] = make_float2(M, L);
+    }
+  }
+  __syncthreads();
+  for (int y = warp; y < groups * (units / 32); y += W) {
+    const int gi = y / (units / 32), x = (y - gi * (units / 32)) * 32 + lane;
+    const Group& gr = s_group[gi];
+    const Unit4 u = piece_unit(x, hp);
+    const int nh = heads_of(a, gr.p.j);
+    if (u.head >= nh) continue;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4& v, float w) {
+      o.x += v.x * w;
+      o.y += v.y * w;
+      o.z += v.z * w;
+      o.w += v.w * w;
+    };
+    // (a first piece can only be the last of a group: the run that it begins goes on elsewhere)
+    const int last = 31 - __clz(gr.members);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!(last & 1))
+      v = __ldcg(a.ws_o + (static_cast<int64_t>(blockIdx.x) * W + (last >> 1)) * units + x);
+    const int w0 = (__ffs(gr.members) - 1) >> 1, w1 = (last - 1) >> 1;  // its last pieces
+#pragma unroll 4
+    for (int i = w0; i <= w1; ++i)
+      add(reinterpret_cast<const float4*>(smem + i * C::kRingBytes)[x],
+          s_weight[2 * i + 1][u.head]);
+    if (!(last & 1)) add(v, s_weight[last][u.head]);
+    if (gr.pages == gr.p.np)
+      write_out<HD>(a, gr.p, nh, u, o, 1.f);
+    else
+      a.ws_o[(part0 + blockIdx.x + gr.p.b * ups + gr.p.j) * units + x] = o;
+  }
+  // ---- units that other CTAs have pages of: this CTA's first or last
+  __syncthreads();
+  if (tid < 2 && groups > tid) {
+    const int gi = tid == 0 ? 0 : groups - 1;
+    const Group& gr = s_group[gi];
+    if (gr.pages != gr.p.np) {
+      int32_t* ticket = a.tickets + cut.worker(gr.p.tile0) / W;
+      __threadfence();
+      if (atomicAdd(ticket, gr.pages) + gr.pages == gr.p.np) {
+        *ticket = 0;
+        s_last[tid] = gi + 1;
+      }
+      __threadfence();
+    }
+  }
+  __syncthreads();
+  if (s_last[0] != 0 || s_last[1] != 0) {
+    // M = max m_i, l = sum l_i 2^(m_i - M), weights 2^(m_i - M) / l; then out = sum O_i weight_i
+    // (the warps' pieces have been read: their place takes the weights)
+    auto s_join = reinterpret_cast<float(*)[kQHeadsPerUnit][kMaxCtas]>(smem);
+    for (int y = warp; y < 2 * kQHeadsPerUnit; y += W) {
+      const int which = y / kQHeadsPerUnit, head = y % kQHeadsPerUnit;
+      if (s_last[which] == 0) continue;
+      const Piece& p = s_group[s_last[which] - 1].p;
+      if (head >= heads_of(a, p.j)) continue;
+      const int c0 = cut.worker(p.tile0) / W;
+      const int n = cut.worker(p.tile0 + p.np - 1) / W - c0 + 1;
+      const float2* ml = a.ws_ml + (part0 + c0 + p.b * ups + p.j) * a.rows + head;
       float M = -INFINITY, L = 0.f;
-      for (int i = w; i < e; ++i) M = fmaxf(M, s_ml[i][u.head].x);
+      for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(ml + i * a.rows).x);
+      M = lat::warp_max(M);
+      for (int i = lane; i < n; i += 32) {
+        const float2 x = __ldcg(ml + i * a.rows);
+        const float fo = ex2_approx(x.x - M);
+        s_join[which][head][i] = fo;
+        L += x.y * fo;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      const float inv = 1.f / L;
+      for (int i = lane; i < n; i += 32) s_join[which][head][i] *= inv;
+      if (lane == 0) write_lse(a, p, head, M, L);
+    }
+    __syncthreads();
+    for (int y = warp; y < 2 * (units / 32); y += W) {
+      const int which = y / (units / 32), x = (y - which * (units / 32)) * 32 + lane;
+      if (s_last[which] == 0) continue;
+      const Piece& p = s_group[s_last[which] - 1].p;
+      const Unit4 u = piece_unit(x, hp);
+      const int nh = heads_of(a, p.j);
+      if (u.head >= nh) continue;
+      const int c0 = cut.worker(p.tile0) / W;
+      const int n = cut.worker(p.tile0 + p.np - 1) / W - c0 + 1;
+      const float4* src = a.ws_o + (part0 + c0 + p.b * ups + p.j) * units + x;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i = w; i < e; ++i) {
-        const float2 ml = s_ml[i][u.head];
-        const float4 v = reinterpret_cast<const float4*>(smem + i * C::kRingBytes)[x];
-        const float fo = exp2f(ml.x - M);
-        L += ml.y * fo;
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        const float4 v = __ldcg(src + static_cast<int64_t>(i) * units);
+        const float fo = s_join[which][u.head][i];
         o.x += v.x * fo;
         o.y += v.y * fo;
         o.z += v.z * fo;
         o.w += v.w * fo;
       }
-      if (whole) {
-        write_out<HD>(a, p, nh, u, o, 1.f / L);
-        if (u.d == 0) write_lse(a, p, u.head, M, L);
-      } else {
-        a.ws_o[slot * units + x] = o;
-        if (u.d == 0) a.ws_ml[slot * a.rows + u.head] = make_float2(M, L);
-      }
-    }
-  }
-  if (cut) {  // (the same for all threads)
-    __threadfence();
-    __syncthreads();
-    if (tid < W) {
-      int last = 0;
-      if (first_of_run(tid)) {
-        const Piece p = s_piece[tid];
-        int pages;
-        run_end(tid, pages);
-        if (pages != p.np) {
-          int32_t* ticket = a.tickets + worker_of(p.tile0, tiles, workers);
-          last = atomicAdd(ticket, pages) + pages == p.np;
-          if (last) *ticket = 0;
-        }
-      }
-      s_last[tid] = last;
-    }
-    __syncthreads();
-    for (int w = 0; w < W; ++w) {
-      if (!s_last[w]) continue;
-      __threadfence();
-      join<HD, KEQV>(a, s_piece[w], tiles, workers, tid, C::kThreads);
+      write_out<HD>(a, p, nh, u, o, 1.f);
     }
   }
   // ---- sequences without keys, and lengths that are wrong
@@ -738,7 +792,7 @@ int launch(const Args& a, int num_sms, cudaStream_t stream) {
   auto* fn = fp4_decode_kernel<HD, KEQV>;
   const int rc = set_smem_limit(reinterpret_cast<const void*>(fn), C::kSmem);
   if (rc != PSW_OK) return rc;
-  const int grid = min(num_sms, kFp4MaxWorkers / C::kWarps);
+  const int grid = min(num_sms, kMaxCtas);
   fn<<<grid, C::kThreads, C::kSmem, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? PSW_OK : PSW_ELAUNCH;
 }
@@ -748,11 +802,16 @@ int slot_rows(const LayerArgs& L) {
   return (heads + 1) / 2 * 2;
 }
 
+// Slots of a call: one for every worker's first piece, then those of the CTAs' parts of
+// units (CTA + unit: the units of neighbouring CTAs are neighbours, so no two share one).
+size_t slots_of(const LayerArgs& L, int n_seqs) {
+  return kMaxCtas * (kMaxWarps + 1) + static_cast<size_t>(n_seqs) * L.n_kv * L.qchunks();
+}
+
 }  // namespace
 
 size_t fp4_decode_workspace(const LayerArgs& L, int n_seqs) {
-  const size_t slots = kFp4MaxWorkers + static_cast<size_t>(n_seqs) * L.n_kv * L.qchunks();
-  return kFp4CounterBytes + slots * slot_rows(L) * (static_cast<size_t>(L.hd) * 4 + 8);
+  return kFp4CounterBytes + slots_of(L, n_seqs) * slot_rows(L) * (static_cast<size_t>(L.hd) * 4 + 8);
 }
 
 int launch_fp4_decode(const LayerArgs& L, const void* q, const void* k_pool, const void* v_pool,
@@ -766,7 +825,8 @@ int launch_fp4_decode(const LayerArgs& L, const void* q, const void* k_pool, con
   a.table = pages.block_table;
   a.seq_lens = seq_lens;
   a.max_blocks = pages.max_blocks_per_seq;
-  a.num_blocks = pages.num_blocks;
+  a.num_blocks = static_cast<int>(pages.num_blocks);
+  a.page_stride = static_cast<uint32_t>(L.n_kv) * PSW_FP4_PAGE_BYTES(L.hd);
   a.n_seqs = n_seqs;
   a.n_q = L.n_q;
   a.n_kv = L.n_kv;
@@ -780,11 +840,11 @@ int launch_fp4_decode(const LayerArgs& L, const void* q, const void* k_pool, con
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
   a.rows = slot_rows(L);
-  const size_t slots = kFp4MaxWorkers + static_cast<size_t>(n_seqs) * L.n_kv * L.qchunks();
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.tickets = reinterpret_cast<int32_t*>(w);
   a.ws_o = reinterpret_cast<float4*>(w + kFp4CounterBytes);
-  a.ws_ml = reinterpret_cast<float2*>(w + kFp4CounterBytes + slots * a.rows * L.hd * 4);
+  a.ws_ml = reinterpret_cast<float2*>(w + kFp4CounterBytes +
+                                      slots_of(L, n_seqs) * a.rows * L.hd * 4);
   a.err = err;
   const StallHook hook = stall_hook(kStallDecode);
   a.stall_cta = hook.cta;

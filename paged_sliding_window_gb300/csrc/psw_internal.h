@@ -212,9 +212,8 @@ int launch_latent_prefill(const LatentArgs& L, const void* q, const int32_t* cu_
                           int num_sms, int32_t* err, cudaStream_t stream);
 
 // ---- 4-bit pages (fp4_*.cu) and tables built on the device (block_tables.cu)
-// Decode workspace: merge tickets (one int32 per worker, a warp of the grid;
-// zero between calls), then one slot of partial results per worker and unit.
-constexpr int kFp4MaxWorkers = PSW_FP4_COUNTER_BYTES / 4;
+// Decode workspace: join tickets (one int32 per CTA; zero between calls), then slots of
+// partial results.
 constexpr size_t kFp4CounterBytes = PSW_FP4_COUNTER_BYTES;
 
 int launch_block_table_extend(int32_t* block_table, int max_blocks, const int32_t* past_lens,

@@ -112,14 +112,14 @@ def test_table_refusals(lib, kw, code):
 
 
 def test_workspace_and_constants(lib):
-    """Counters, then one slot of partial rows and their (m, l) per worker and unit."""
+    """Counters, then slots of partial rows and their (m, l): one per warp and CTA of the largest grid and per unit."""
     text = open(HEADER).read()
     assert int(re.search(r"#define\s+PSW_FP4_COUNTER_BYTES\s+(\d+)", text).group(1)) == binding.FP4_COUNTER_BYTES
     assert int(re.search(r"#define\s+PSW_DEVERR_NOBLOCKS\s+(\d+)", text).group(1)) == binding.DEVERR_NOBLOCKS
     for layer, n in ((_layer(), 64), (_layer(n_q_heads=32, n_kv_heads=4, head_dim=512), 7), (_layer(n_q_heads=22, n_kv_heads=2), 0)):
         G = layer.n_q_heads // layer.n_kv_heads
         units = n * layer.n_kv_heads * -(-G // 8)
-        assert binding.fp4_workspace_bytes(layer, n) == 8192 + (2048 + units) * ((min(G, 8) + 1) // 2 * 2) * (4 * layer.head_dim + 8)
+        assert binding.fp4_workspace_bytes(layer, n) == 2048 + (160 * 13 + units) * ((min(G, 8) + 1) // 2 * 2) * (4 * layer.head_dim + 8)
     assert binding.fp4_page_bytes(_layer()) == 2304
 
 
