@@ -23,9 +23,9 @@ int ready(DeviceInfo* info, int32_t** err) {
   return PSW_OK;
 }
 
-// Pages of all sequences, times `units`, must be countable in 32 bits.
-bool countable(const psw_pages_t* pages, int32_t n_seqs, int64_t units) {
-  return static_cast<int64_t>(n_seqs) * pages->max_blocks_per_seq <= INT32_MAX / units;
+// Pages of all sequences (and `more` entries each), times `units`, must be countable in 32 bits.
+bool countable(const psw_pages_t* pages, int32_t n_seqs, int64_t units, int64_t more) {
+  return n_seqs * (pages->max_blocks_per_seq + more) <= INT32_MAX / units;
 }
 
 }  // namespace
@@ -103,7 +103,7 @@ int kv_cache_read_fp4(const psw_layer_t* layer, const void* k_pool4, const void*
   if (!aligned(k_pool4, 16) || !aligned(v_pool4, 16) || !aligned(k_pool, 16) ||
       !aligned(v_pool, 16))
     return PSW_EALIGN;
-  if (!countable(pages, n_seqs, 1)) return PSW_ECAPACITY;
+  if (!countable(pages, n_seqs, 1, 0)) return PSW_ECAPACITY;
   if (n_seqs == 0) return PSW_OK;
   DeviceInfo info;
   int32_t* err;
@@ -133,7 +133,7 @@ int attn_decode_paged_fp4(const psw_layer_t* layer, const void* q, const void* k
   if (rc != PSW_OK) return rc;
   if (!tensor_scale_ok(k_scale) || !tensor_scale_ok(v_scale)) return PSW_EINVAL_SCALE;
   if (!aligned(ws, 16) || !aligned(lse, 4)) return PSW_EALIGN;
-  if (!countable(pages, n_seqs, static_cast<int64_t>(L.n_kv) * L.qchunks()) ||
+  if (!countable(pages, n_seqs, static_cast<int64_t>(L.n_kv) * L.qchunks(), kFp4UnitCost) ||
       static_cast<int64_t>(L.n_kv) * PSW_FP4_PAGE_BYTES(L.hd) > INT32_MAX)
     return PSW_ECAPACITY;
   if (n_seqs == 0) return PSW_OK;

@@ -7,7 +7,7 @@
 // page serves as both (k_eq_v).
 //
 //  * Unit = (sequence, KV head, up to 8 query heads). The visible pages of all
-//    units form one list; every warp of a persistent grid (one CTA per SM) is a
+//    units form one list, in which a unit's beginning counts as kUnitCost pages; every warp of a persistent grid (one CTA per SM) is a
 //    worker of its own with an equal run of it: its own ring of pages in shared
 //    memory, filled by plain bulk copies (a page of a head is one run of bytes),
 //    its own running maximum, sum and output. No warp waits for another.
@@ -42,22 +42,26 @@ using fp4::Page;
 
 constexpr int kMaxCtas = 160;  // one per SM; what they need of workspace is counted with it
 constexpr int kMaxWarps = 12;
+constexpr int kUnitCost = kFp4UnitCost;  // what beginning and ending a unit takes, in pages
+constexpr int kRuns = 256;     // runs of sequences whose entries are summed
 
 template <int HD, bool KEQV>
 struct Cfg {
   static constexpr int kWarps = HD == 256 ? 12 : 8;  // registers: 168 and 255 a thread
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kParts = HD / 256;
-  static constexpr int kChunks = HD / 128;
-  static constexpr int kStageBytes = Page<HD>::kBytes * (KEQV ? 1 : 2);
-  static constexpr int kRingBytes = 18432;  // per warp: 8, 4 or 2 stages
-  static constexpr int kStages = kRingBytes / kStageBytes;
+  static constexpr int kTensors = KEQV ? 1 : 2;
+  static constexpr int kTile = HD == 512 && !KEQV ? 1 : 2;  // pages that a warp works on at a time
+  static constexpr int kPageBytes = Page<HD>::kBytes * kTensors;
+  static constexpr int kTileBytes = kTile * kPageBytes;
+  static constexpr int kRingBytes = 18432;  // per warp
+  static constexpr int kStages = kRingBytes / kTileBytes;
   static constexpr int kQBytes = HD == 256 ? 0 : HD * 8 * 2;  // per warp: q as operands (HD 512)
   static constexpr int kSmem = kWarps * (kRingBytes + kQBytes);
   static_assert(kWarps <= kMaxWarps && 2 * kWarps <= 32, "pieces of a CTA");
-  static_assert(2 * kQHeadsPerUnit * kMaxCtas * 4 <= kRingBytes, "weights of two units");
-  static_assert(kStages * kStageBytes == kRingBytes, "ring");
+  static_assert(kStages * kTileBytes == kRingBytes && kStages >= 2 && kStages <= 8, "ring");
   static_assert(HD * 8 * 4 <= kRingBytes, "a piece's output fits where the ring was");
+  static_assert(2 * kQHeadsPerUnit * kMaxCtas * 4 <= kRingBytes, "weights of two units");
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -88,6 +92,28 @@ __device__ __forceinline__ uint32_t codes_at(uint32_t w, int i) {
          : i == 1 ? fp4::codes_f16<1>(w)
          : i == 2 ? fp4::codes_f16<2>(w)
                   : fp4::codes_f16<3>(w);
+}
+// The bounded wait of a whole warp: the same for all its lanes.
+__device__ __forceinline__ bool landed(uint64_t* bar, uint32_t phase) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, phase));
+}
+// A bulk copy that only lanes with `p` ask for.
+__device__ __forceinline__ void bulk_load_if(bool p, uint32_t dst, const void* src, uint32_t bytes,
+                                             uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+      "[%3];\n\t}" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "r"(static_cast<uint32_t>(p))
+      : "memory");
+}
+__device__ __forceinline__ void expect_if(bool p, uint64_t* bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+      "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(bytes), "r"(static_cast<uint32_t>(p))
+      : "memory");
 }
 // bits of a where m has ones, of b elsewhere
 __device__ __forceinline__ uint32_t select_bits(uint32_t m, uint32_t a, uint32_t b) {
@@ -127,13 +153,12 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
   return Seq{len, s.p0, s.np, lo};
 }
 
-// A place in the list of pages: sequence, unit of it, page of the unit.
-struct Cursor {
-  int b, j, page, tile0;  // tile0: the list's index of the unit's first page
+// A unit of the list: sequence, unit of it, the list's index of its beginning.
+struct Place {
+  int b, j, tile0;
   Seq s;
-  __device__ void next_unit(const Args& a, int ups) {
-    page = 0;
-    tile0 += s.np;
+  __device__ void next(const Args& a, int ups) {
+    tile0 += s.np + kUnitCost;
     if (++j < ups) return;
     j = 0;
     do {
@@ -185,7 +210,7 @@ __device__ __forceinline__ void write_lse(const Args& a, const Piece& p, int hea
 }
 
 
-// The list of `tiles` pages cut into runs for `workers`: of each + 1 pages for the first
+// The list of `tiles` entries cut into runs for `workers`: of each + 1 entries for the first
 // `more` of them, of `each` for the others.
 struct Cut {
   int each, more;
@@ -203,20 +228,32 @@ struct Group {
   uint32_t members;
   int pages;
 };
+// The CTAs (of K workers) that have pages of a unit: the first of them and how many.
+struct Ctas {
+  int first, n;
+};
+template <int K>
+__device__ __forceinline__ Ctas ctas_of(const Cut& cut, const Piece& p) {
+  const int first = cut.worker(p.tile0 + kUnitCost) / K;
+  return Ctas{first, cut.worker(p.tile0 + kUnitCost + p.np - 1) / K - first + 1};
+}
 
 template <int HD, bool KEQV>
-__global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1)
-fp4_decode_kernel(const Args a) {
+__global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(const Args a) {
   using C = Cfg<HD, KEQV>;
-  constexpr int W = C::kWarps;
+  constexpr int W = C::kWarps, S = C::kStages, TP = C::kTile;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t s_full[W][C::kStages];
-  __shared__ int s_run[C::kThreads + 1];
-  __shared__ int s_sum[W];
+  __shared__ uint64_t s_full[W][S];
   __shared__ Piece s_piece[2 * W];
   __shared__ float2 s_ml[2 * W][kQHeadsPerUnit];
-  __shared__ Group s_group[2 * W];
-  __shared__ float s_weight[2 * W][kQHeadsPerUnit];
+  __shared__ union {
+    int run[kRuns + 1];  // at the beginning
+    struct {             // at the end
+      float weight[2 * W][kQHeadsPerUnit];
+      Group group[2 * W];
+    };
+  } s_u;
+  __shared__ int s_sum[kRuns / 32];
   __shared__ int s_groups;
   __shared__ int s_last[2];  // group + 1
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -224,101 +261,123 @@ fp4_decode_kernel(const Args a) {
   uint8_t* ring = smem + warp * C::kRingBytes;
   const int ups = a.n_kv * a.qchunks, hp = a.rows / 2;
 
-  // ---- the list: pages of the sequences before each thread's run of them
-  if (lane < C::kStages) mbar_init(&s_full[warp][lane], 1);
+  // ---- the list: entries of the sequences before each run of them
+  if (lane < S) mbar_init(&s_full[warp][lane], 1);
   fence_mbar_init();
-  const int per = (a.n_seqs + C::kThreads - 1) / C::kThreads;
-  int mine = 0;
-  for (int b = tid * per; b < min(a.n_seqs, (tid + 1) * per); ++b) mine += seq_of(a, b).np;
-  int incl = mine;
+  const int per = (a.n_seqs + kRuns - 1) / kRuns;
+  int incl = 0;
+  if (tid < kRuns) {
+    for (int b = tid * per; b < min(a.n_seqs, (tid + 1) * per); ++b) {
+      const int np = seq_of(a, b).np;
+      if (np > 0) incl += np + kUnitCost;
+    }
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) s_sum[warp] = incl;
   }
-  if (lane == 31) s_sum[warp] = incl;
-  if (lane < 2) s_piece[2 * warp + lane].pages = 0;
+  if (tid < 2 * W) s_piece[tid].pages = 0;
   if (tid < 2) s_last[tid] = 0;
   __syncthreads();
-  int before = 0, all = 0;
-  for (int i = 0; i < W; ++i) {
-    if (i < warp) before += s_sum[i];
+  int all = 0;
+#pragma unroll
+  for (int i = 0; i < kRuns / 32; ++i) {
+    if (i == warp) incl += all;
     all += s_sum[i];
   }
-  s_run[tid + 1] = before + incl;
-  if (tid == 0) s_run[0] = 0;
+  if (tid < kRuns) s_u.run[tid + 1] = incl;
+  if (tid == 0) s_u.run[0] = 0;
   __syncthreads();
   const int tiles = all * ups;
   const int workers = max(1, min(static_cast<int>(gridDim.x) * W, tiles));
   const Cut cut{tiles / workers, tiles % workers};
   const int me = blockIdx.x * W + warp;
 
-  bool failed = false;
+  Place c;        // the unit that is worked on
+  int page = 0;   // its next page
+  int left = 0;   // entries of the run from the next page to fetch on
   if (me < min(workers, tiles)) {
-    const int begin = cut.begin(me), n = cut.begin(me + 1) - begin;
-    Cursor c;  // of the page that is worked on
-    {
-      const int page = begin / ups;  // units of a sequence are equal: find its sequence by pages
-      int lo = 0, hi = C::kThreads;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_run[mid] <= page) lo = mid; else hi = mid;
-      }
-      c.b = lo * per;
-      int off = s_run[lo];
-      c.s = seq_of(a, c.b);
-      while (page >= off + c.s.np) {
-        off += c.s.np;
-        c.s = seq_of(a, ++c.b);
-      }
-      const int rem = begin - off * ups;
-      c.j = rem / c.s.np;
-      c.page = rem - c.j * c.s.np;
-      c.tile0 = begin - c.page;
+    const int begin = cut.begin(me);
+    left = cut.begin(me + 1) - begin;
+    const int x = begin / ups;  // units of a sequence are equal: find its sequence by entries
+    int lo = 0, hi = kRuns;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_u.run[mid] <= x) lo = mid; else hi = mid;
     }
-    Cursor f = c;  // of the next page to fetch
-    const uint8_t *f_k, *f_v;  // its KV head in block 0
-    int32_t ids;               // lane i: block of page 32 n + i, the 32 that f.page is among
-    uint32_t bad = 0;          // a bit per stage: its page has no valid block
+    c.b = lo * per;
+    int off = s_u.run[lo];
+    c.s = seq_of(a, c.b);
+    while (c.s.np == 0 || x >= off + c.s.np + kUnitCost) {
+      if (c.s.np > 0) off += c.s.np + kUnitCost;
+      c.s = seq_of(a, ++c.b);
+    }
+    const int rem = begin - off * ups, entries = c.s.np + kUnitCost;
+    c.j = rem / entries;
+    const int at = rem - c.j * entries;
+    c.tile0 = begin - at;
+    page = max(0, at - kUnitCost);
+    left -= max(0, kUnitCost - at);
+  }
+  if (left > 0) {
+    // ---- fetching: a tile's blocks, a copy by each of the first lanes
+    Place f = c;
+    int f_page = page, ids_at = 0;
+    int32_t ids = 0;     // lane i: block of page ids_at + i
+    int n = 0;           // tiles asked for
+    uint32_t info = 0;   // four bits per stage: more than one page; pages without a valid block
     const int stall = static_cast<int>(blockIdx.x) == a.stall_cta && warp == 0 ? a.stall_tile : -1;
-    auto fetch_head = [&]() {
-      const int64_t at = static_cast<int64_t>(f.j / a.qchunks) * Page<HD>::kBytes;
-      f_k = a.k_pool + at;
-      if (!KEQV) f_v = a.v_pool + at;
+    const int my_page = lane / C::kTensors;  // of a tile (lanes below kTile * kTensors)
+    const bool my_v = C::kTensors == 2 && (lane & 1);
+    const uint8_t* f_from = nullptr;  // this lane's tensor, at the unit's KV head of block 0
+    auto fetch_unit = [&]() {
+      f_from = (my_v ? a.v_pool : a.k_pool) +
+               static_cast<int64_t>(f.j / a.qchunks) * Page<HD>::kBytes;
     };
     auto fetch_ids = [&]() {
-      const int at = (f.page & ~31) + lane;
+      ids_at = f_page;
+      const int at = f_page + lane;
       ids = at < f.s.np
                 ? __ldg(a.table + static_cast<int64_t>(f.b) * a.max_blocks + f.s.p0 + at)
                 : 0;
     };
-    auto fetch = [&](int i) {  // page i of the run
-      if (f.page == f.s.np) {
-        f.next_unit(a, ups);
-        fetch_head();
+    auto fetch = [&]() {  // the next tile of the run, if there is one
+      if (f_page == f.s.np) {
+        left -= kUnitCost;
+        if (left <= 0) return;
+        f.next(a, ups);
+        f_page = 0;
+        fetch_unit();
+        fetch_ids();
         // its queries are wanted when the pages before it are done
         const char* q = reinterpret_cast<const char*>(
             a.q + (static_cast<int64_t>(f.b) * a.n_q + first_head(a, f.j)) * HD);
         for (int k = lane * 128; k < heads_of(a, f.j) * HD * 2; k += 32 * 128)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(q + k));
       }
-      if ((f.page & 31) == 0) fetch_ids();
-      int32_t blk = __shfl_sync(0xffffffffu, ids, f.page & 31);
-      const int st = i & (C::kStages - 1);
-      if (static_cast<uint32_t>(blk) >= static_cast<uint32_t>(a.num_blocks)) {
-        bad |= 1u << st;
+      if (f_page - ids_at > 32 - TP) fetch_ids();
+      const int pages = min(min(TP, f.s.np - f_page), left);
+      int32_t blk = __shfl_sync(0xffffffffu, ids, (f_page - ids_at + my_page) & 31);
+      const int st = n & (S - 1);
+      const bool mine = lane < pages * C::kTensors;
+      const bool wrong = mine && static_cast<uint32_t>(blk) >= static_cast<uint32_t>(a.num_blocks);
+      uint32_t word = pages > 1 ? 1u : 0u;
+      if (const uint32_t no = __ballot_sync(0xffffffffu, wrong)) {  // (a lane of a tensor each)
+        if (wrong) blk = 0;
+        word |= (no & 1u ? 2u : 0u) | (no >> C::kTensors & 1u ? 4u : 0u);
         if (lane == 0) flag_error(a.err, PSW_DEVERR_BLOCK_ID);
-        blk = 0;
       }
-      if (lane == 0 && i != stall) {
-        const int64_t at = static_cast<int64_t>(blk) * a.page_stride;
-        const uint32_t dst = smem_u32(ring + st * C::kStageBytes);
-        mbar_arrive_expect_tx(&s_full[warp][st], C::kStageBytes);
-        lat::bulk_load(dst, f_k + at, Page<HD>::kBytes, &s_full[warp][st]);
-        if (!KEQV)
-          lat::bulk_load(dst + Page<HD>::kBytes, f_v + at, Page<HD>::kBytes, &s_full[warp][st]);
-      }
-      ++f.page;
+      info = (info & ~(15u << (4 * st))) | word << (4 * st);
+      const bool ask = n != stall;
+      expect_if(lane == 0 && ask, &s_full[warp][st], pages * C::kPageBytes);
+      bulk_load_if(mine && ask, smem_u32(ring + st * C::kTileBytes + lane * Page<HD>::kBytes),
+                   f_from + static_cast<int64_t>(blk) * a.page_stride, Page<HD>::kBytes,
+                   &s_full[warp][st]);
+      f_page += pages;
+      left -= pages;
+      ++n;
     };
 
     // tokens of this lane: rows g, g + 8 of S^T are tokens r0, r0 + 8; key slots 2 t, 2 t + 1
@@ -326,10 +385,11 @@ fp4_decode_kernel(const Args a) {
     // bank conflicts (the pages' units are exchanged by the token's low bits).
     const int r0 = (g & 1) ? (((g & 6) ^ 4) | 1) : g;
     const int ra = 2 * t, rb = ((2 * t) ^ 4) | 1;
+    constexpr int kRow = Page<HD>::kScaleRow, kCodes = Page<HD>::kCodeBytes;
     const int k_at = r0 * 128 + ((t ^ (r0 & 7)) << 4);  // unit t; unit 4 + t: ^ 64
-    const int ks_at = Page<HD>::kCodeBytes + r0 * Page<HD>::kScaleRow + t * Page<HD>::kLaneScales;
+    const int ks_at = kCodes + r0 * kRow + t * Page<HD>::kLaneScales;
     const int va_at = ra * 128 + ((g ^ ra) << 4), vb_at = rb * 128 + ((g ^ rb) << 4);
-    const int vs_at = Page<HD>::kCodeBytes + (g & 3) * Page<HD>::kLaneScales + (g >> 2) * (HD / 128);
+    const int vs_at = kCodes + (g & 3) * Page<HD>::kLaneScales + (g >> 2) * (HD / 128);
 
     uint32_t qr[HD == 256 ? 32 : 1];  // q as operands: HD 256 in registers, HD 512 in shared memory
     uint4* q_smem = reinterpret_cast<uint4*>(smem + W * C::kRingBytes + warp * C::kQBytes) + lane;
@@ -337,8 +397,8 @@ fp4_decode_kernel(const Args a) {
     float acc[HD / 16][4];    // value 32 g + 2 i (+ 256 part): heads 2 t, 2 t + 1; the next value: same
     float m[2], l[2];
     int piece_from = 0;
-    uint32_t first_seen = 0, last_seen = 0;  // a bit per token of the unit's first and last page
-    uint4 raw[C::kChunks][4];
+    uint32_t ends = 0;  // a bit per token seen of the unit's first page, and of its last
+    uint4 raw[HD / 128][4];
 
     auto load_q = [&]() {
       const int row = first_head(a, c.j) + min(g, heads_of(a, c.j) - 1);
@@ -346,14 +406,14 @@ fp4_decode_kernel(const Args a) {
           reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(c.b) * a.n_q + row) * HD) +
           t * 4;
 #pragma unroll
-      for (int k = 0; k < C::kChunks; ++k)
+      for (int k = 0; k < HD / 128; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) raw[k][i] = __ldg(src + k * 16 + i);
     };
     auto begin_piece = [&]() {
       uint32_t top = 0;  // the largest |q|, as bf16 bits
 #pragma unroll
-      for (int k = 0; k < C::kChunks; ++k)
+      for (int k = 0; k < HD / 128; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t w[4] = {raw[k][i].x, raw[k][i].y, raw[k][i].z, raw[k][i].w};
@@ -364,22 +424,22 @@ fp4_decode_kernel(const Args a) {
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
       const int e = max(static_cast<int>(big >> 7), 15);  // exponent of 2 + 127
-      const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);    // 2^(141 - e)
-      const float down = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);   // 2^(e - 141)
-      const bool live = g < heads_of(a, c.j);
-      uint32_t pk[HD == 256 ? 1 : 4];
+      const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);   // 2^(141 - e)
+      const float down = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);  // 2^(e - 141)
+      // (columns of heads that are not there repeat the last one: their results go nowhere)
 #pragma unroll
-      for (int k = 0; k < C::kChunks; ++k)
+      for (int k = 0; k < HD / 128; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t w[4] = {raw[k][i].x, raw[k][i].y, raw[k][i].z, raw[k][i].w};
+          uint32_t h[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const float2 v = unpack_bf16x2(w[x]);
-            const uint32_t h = live ? pack_f16x2(v.x * up, v.y * up) : 0u;
-            if constexpr (HD == 256) qr[(k * 4 + i) * 4 + x] = h; else pk[x] = h;
+            h[x] = pack_f16x2(v.x * up, v.y * up);
+            if constexpr (HD == 256) qr[(k * 4 + i) * 4 + x] = h[x];
           }
-          if constexpr (HD != 256) q_smem[(k * 4 + i) * 32] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          if constexpr (HD != 256) q_smem[(k * 4 + i) * 32] = make_uint4(h[0], h[1], h[2], h[3]);
         }
       const float fac = a.scale * down * (a.softcap > 0.f ? 1.f / a.softcap : lat::kLog2e);
       qf[0] = __shfl_sync(0xffffffffu, fac, 8 * t);
@@ -390,9 +450,9 @@ fp4_decode_kernel(const Args a) {
         for (int x = 0; x < 4; ++x) acc[i][x] = 0.f;
       m[0] = m[1] = -INFINITY;
       l[0] = l[1] = 0.f;
-      piece_from = c.page;
-      first_seen = (0xFFFFu << (c.s.lo & (kBlockSize - 1))) & 0xFFFFu;
-      last_seen = 0xFFFFu >> (kBlockSize - 1 - ((c.s.len - 1) & (kBlockSize - 1)));
+      piece_from = page;
+      ends = ((0xFFFFu << (c.s.lo & (kBlockSize - 1))) & 0xFFFFu) |
+             (0xFFFFu >> (kBlockSize - 1 - ((c.s.len - 1) & (kBlockSize - 1)))) << 16;
     };
     auto sum_l = [&]() {
 #pragma unroll
@@ -416,54 +476,77 @@ fp4_decode_kernel(const Args a) {
                 make_float4(x[odd], x[2 + odd], y[odd], y[2 + odd]);
           }
     };
+    auto note = [&](int at) {  // the piece, for the CTA
+      if (g == 0) {
+        s_ml[at][2 * t] = make_float2(m[0], l[0]);
+        s_ml[at][2 * t + 1] = make_float2(m[1], l[1]);
+      }
+      if (lane == 0) s_piece[at] = Piece{c.b, c.j, c.tile0, c.s.np, page - piece_from};
+    };
 
     load_q();  // (in front of the pages: behind them it would wait for all)
-    fetch_head();
+    fetch_unit();
     fetch_ids();
-    for (int i = 0; i < min(n, C::kStages); ++i) fetch(i);
+    for (int i = 0; i < S && left > 0; ++i) fetch();
     begin_piece();
+    bool failed = false;
     for (int it = 0; it < n; ++it) {
-      const int st = it & (C::kStages - 1);
-      if (!mbar_wait(&s_full[warp][st], (it / C::kStages) & 1)) {
-        if (lane == 0) flag_error(a.err, PSW_DEVERR_PIPELINE);
+      const int st = it & (S - 1);
+      if (!landed(&s_full[warp][st], (it / S) & 1)) {
         failed = true;
-        for (int i = it + 1; i < min(n, it + C::kStages); ++i)  // copies in flight have to land
-          mbar_wait(&s_full[warp][i & (C::kStages - 1)], (i / C::kStages) & 1);
         break;
       }
-      const uint8_t* page = ring + st * C::kStageBytes;
-      uint32_t seen = c.page == 0 ? first_seen : 0xFFFFu;  // a bit per token: visible
-      if (c.page == c.s.np - 1) seen &= last_seen;
-      const bool is_bad = (bad >> st) & 1;
+      const uint8_t* tile = ring + st * C::kTileBytes;
+      const uint32_t word = info >> (4 * st);
+      const int pages = TP == 1 ? 1 : 1 + (word & 1);
+      // a bit per token of the tile: visible
+      constexpr uint32_t kAll = TP == 1 ? 0xFFFFu : 0xFFFFFFFFu;
+      uint32_t seen = pages == TP ? kAll : 0xFFFFu;
+      if (page == 0) seen &= 0xFFFF0000u | ends;
+      if (page + pages == c.s.np)
+        seen &= pages == 1 ? ends >> 16 : (ends & 0xFFFF0000u) | 0xFFFFu;
+      const bool edge = seen != kAll || (word & 6) != 0;
 
       // ---- S^T = K Q^T
-      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+      float s[TP][4];
+#pragma unroll
+      for (int pg = 0; pg < TP; ++pg)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[pg][x] = 0.f;
       {
-        uint32_t ks[2][C::kChunks / 2];  // scale bytes of tokens r0, r0 + 8: two blocks per chunk
+        uint32_t ks[TP][2][HD / 256];  // scale bytes of tokens r0, r0 + 8: two blocks per 128 values
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const uint8_t* p = page + ks_at + r * 8 * Page<HD>::kScaleRow;
-          if constexpr (HD == 256) {
-            ks[r][0] = *reinterpret_cast<const uint32_t*>(p);
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(p);
-            ks[r][0] = x.x;
-            ks[r][1] = x.y;
+        for (int pg = 0; pg < TP; ++pg)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint8_t* p = tile + pg * C::kPageBytes + ks_at + r * 8 * kRow;
+            if constexpr (HD == 256) {
+              ks[pg][r][0] = *reinterpret_cast<const uint32_t*>(p);
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(p);
+              ks[pg][r][0] = x.x;
+              ks[pg][r][1] = x.y;
+            }
           }
-        }
 #pragma unroll
-        for (int k = 0; k < C::kChunks; ++k) {
-          const uint8_t* p = page + (k >> 1) * 2048 + (k_at ^ ((k & 1) * 64));
-          const uint4 ka = *reinterpret_cast<const uint4*>(p);
-          const uint4 kb = *reinterpret_cast<const uint4*>(p + 1024);
-          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-          const int place = HD == 256 ? k : 2 * (k & 1) + (k >> 1);  // of the chunk's scales
-          const uint32_t sa = fp4::scales_f16(ks[0][place >> 1] >> (16 * (place & 1)));
-          const uint32_t sb = fp4::scales_f16(ks[1][place >> 1] >> (16 * (place & 1)));
-          const uint32_t ea[2] = {__byte_perm(sa, 0, 0x1010), __byte_perm(sa, 0, 0x3232)};
-          const uint32_t eb[2] = {__byte_perm(sb, 0, 0x1010), __byte_perm(sb, 0, 0x3232)};
+        for (int k = 0; k < HD / 128; ++k) {
+          const int place = HD == 256 ? k : 2 * (k & 1) + (k >> 1);  // of the 128 values' scales
+          uint4 ka[TP], kb[TP];
+          uint32_t ea[TP][2], eb[TP][2];
 #pragma unroll
-          for (int jp = 0; jp < 4; ++jp) {  // two products: 4 values each of 32 lanes' units
+          for (int pg = 0; pg < TP; ++pg) {
+            const uint8_t* p = tile + pg * C::kPageBytes + (k >> 1) * 2048 + (k_at ^ ((k & 1) * 64));
+            ka[pg] = *reinterpret_cast<const uint4*>(p);
+            kb[pg] = *reinterpret_cast<const uint4*>(p + 1024);
+            const uint32_t sa = fp4::scales_f16(ks[pg][0][place >> 1] >> (16 * (place & 1)));
+            const uint32_t sb = fp4::scales_f16(ks[pg][1][place >> 1] >> (16 * (place & 1)));
+            ea[pg][0] = __byte_perm(sa, 0, 0x1010);
+            ea[pg][1] = __byte_perm(sa, 0, 0x3232);
+            eb[pg][0] = __byte_perm(sb, 0, 0x1010);
+            eb[pg][1] = __byte_perm(sb, 0, 0x3232);
+          }
+#pragma unroll
+          for (int jp = 0; jp < 4; ++jp) {  // two products, of 4 values each of every lane's unit
             uint4 qq;
             if constexpr (HD == 256)
               qq = make_uint4(qr[k * 16 + jp * 4], qr[k * 16 + jp * 4 + 1], qr[k * 16 + jp * 4 + 2],
@@ -471,31 +554,51 @@ fp4_decode_kernel(const Args a) {
             else
               qq = q_smem[(k * 4 + jp) * 32];
             const int h = jp >> 1;
-            const uint32_t x0[4] = {mul_f16x2(codes_at(wa[jp], 0), ea[h]),
-                                    mul_f16x2(codes_at(wb[jp], 0), eb[h]),
-                                    mul_f16x2(codes_at(wa[jp], 1), ea[h]),
-                                    mul_f16x2(codes_at(wb[jp], 1), eb[h])};
-            mma_f16(s0, x0, qq.x, qq.y);
-            const uint32_t x1[4] = {mul_f16x2(codes_at(wa[jp], 2), ea[h]),
-                                    mul_f16x2(codes_at(wb[jp], 2), eb[h]),
-                                    mul_f16x2(codes_at(wa[jp], 3), ea[h]),
-                                    mul_f16x2(codes_at(wb[jp], 3), eb[h])};
-            mma_f16(s1, x1, qq.z, qq.w);
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+              for (int pg = 0; pg < TP; ++pg) {
+                const uint32_t wa = jp == 0 ? ka[pg].x : jp == 1 ? ka[pg].y : jp == 2 ? ka[pg].z : ka[pg].w;
+                const uint32_t wb = jp == 0 ? kb[pg].x : jp == 1 ? kb[pg].y : jp == 2 ? kb[pg].z : kb[pg].w;
+                const uint32_t x[4] = {mul_f16x2(codes_at(wa, 2 * half), ea[pg][h]),
+                                       mul_f16x2(codes_at(wb, 2 * half), eb[pg][h]),
+                                       mul_f16x2(codes_at(wa, 2 * half + 1), ea[pg][h]),
+                                       mul_f16x2(codes_at(wb, 2 * half + 1), eb[pg][h])};
+                mma_f16(s[pg], x, half ? qq.z : qq.x, half ? qq.w : qq.y);
+              }
           }
         }
       }
       // ---- softmax: tokens r0, r0 + 8 of heads 2 t, 2 t + 1
-      float z[4];
+      float z[TP][4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        z[x] = (is_bad ? 0.f : s0[x] + s1[x]) * qf[x & 1];
-        if (a.softcap > 0.f) z[x] = a.softcap * lat::kLog2e * lat::tanh_of(z[x]);
+      for (int pg = 0; pg < TP; ++pg)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) z[pg][x] = s[pg][x] * qf[x & 1];
+      if (a.softcap > 0.f) {
+#pragma unroll
+        for (int pg = 0; pg < TP; ++pg)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            z[pg][x] = a.softcap * lat::kLog2e * lat::tanh_of(z[pg][x]);
       }
-      if (seen != 0xFFFFu) {
-        if (!((seen >> r0) & 1)) z[0] = z[1] = -INFINITY;
-        if (!((seen >> (r0 + 8)) & 1)) z[2] = z[3] = -INFINITY;
+      if (edge) {
+#pragma unroll
+        for (int pg = 0; pg < TP; ++pg) {
+          const uint32_t mask = seen >> (16 * pg);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if ((word >> (1 + pg)) & 1) z[pg][x] = 0.f;
+            if (!((mask >> (r0 + (x >> 1) * 8)) & 1)) z[pg][x] = -INFINITY;
+          }
+        }
       }
-      float top[2] = {fmaxf(z[0], z[2]), fmaxf(z[1], z[3])};
+      float top[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        top[x] = fmaxf(z[0][x], z[0][2 + x]);
+        if (TP == 2) top[x] = max3f(top[x], z[TP - 1][x], z[TP - 1][2 + x]);
+      }
       if (__any_sync(0xffffffffu, top[0] > m[0] + 14.f || top[1] > m[1] + 14.f)) {
         float al[2];
 #pragma unroll
@@ -518,31 +621,37 @@ fp4_decode_kernel(const Args a) {
             acc[i][x + 1] = r.y;
           }
       }
+      uint32_t p[TP][2];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        z[x] = ex2_approx(z[x] - m[x & 1]);
-        l[x & 1] += z[x];
+      for (int pg = 0; pg < TP; ++pg) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          z[pg][x] = ex2_approx(z[pg][x] - m[x & 1]);
+          l[x & 1] += z[pg][x];
+        }
+        p[pg][0] = transposed(pack_f16x2(z[pg][0], z[pg][1]));
+        p[pg][1] = transposed(pack_f16x2(z[pg][2], z[pg][3]));
       }
-      const uint32_t p0 = transposed(pack_f16x2(z[0], z[1]));
-      const uint32_t p1 = transposed(pack_f16x2(z[2], z[3]));
 
       // ---- O^T += V^T P^T
-      {
-        const uint8_t* vp = page + (KEQV ? 0 : Page<HD>::kBytes);
+#pragma unroll
+      for (int pg = 0; pg < TP; ++pg) {
+        if (pg > 0 && pages == 1) break;
+        const uint8_t* vp = tile + pg * C::kPageBytes + (KEQV ? 0 : Page<HD>::kBytes);
         uint32_t vs[4];  // scale bytes of tokens ra, rb, ra + 8, rb + 8: two blocks per part
         const int rows[4] = {ra, rb, ra + 8, rb + 8};
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const uint8_t* p = vp + vs_at + rows[r] * Page<HD>::kScaleRow;
+          const uint8_t* x = vp + vs_at + rows[r] * kRow;
           if constexpr (HD == 256)
-            vs[r] = *reinterpret_cast<const uint16_t*>(p);
+            vs[r] = *reinterpret_cast<const uint16_t*>(x);
           else
-            vs[r] = *reinterpret_cast<const uint32_t*>(p);
+            vs[r] = *reinterpret_cast<const uint32_t*>(x);
         }
-        if (seen != 0xFFFFu || is_bad) {  // what these rows hold may be anything: 0 times a number
+        if (edge) {  // what rows without a key hold may be anything: 0 times a number
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            if (is_bad || !((seen >> rows[r]) & 1)) vs[r] = 0;
+            if (((word >> (1 + pg)) & 1) || !((seen >> (16 * pg + rows[r])) & 1)) vs[r] = 0;
         }
 #pragma unroll
         for (int part = 0; part < C::kParts; ++part) {
@@ -570,26 +679,22 @@ fp4_decode_kernel(const Args a) {
               const uint32_t x[4] = {
                   mul_f16x2(codes_at(lo01, i), f01), mul_f16x2(codes_at(hi01, i), f01),
                   mul_f16x2(codes_at(lo89, i), f89), mul_f16x2(codes_at(hi89, i), f89)};
-              mma_f16(acc[part * 16 + w * 4 + i], x, p0, p1);
+              mma_f16(acc[part * 16 + w * 4 + i], x, p[pg][0], p[pg][1]);
             }
           }
         }
       }
-      __syncwarp();  // every lane has read the stage
-      bad &= ~(1u << st);
-      if (it + C::kStages < n) fetch(it + C::kStages);
-      ++c.page;
-      if (c.page == c.s.np && it + 1 < n) {  // the unit ends and the run goes on
-        const Piece p{c.b, c.j, c.tile0, c.s.np, c.page - piece_from};
+      __syncwarp();  // every lane has read the tile
+      if (left > 0) fetch();
+      page += pages;
+      if (page == c.s.np && it + 1 < n) {  // the unit ends and the run goes on
         sum_l();
-        const int nh = heads_of(a, c.j);
-        if (p.pages == p.np) {
-          const float inv[2] = {1.f / l[0], 1.f / l[1]};
-          const int h0 = first_head(a, c.j);
+        if (page - piece_from == c.s.np) {
+          const int nh = heads_of(a, c.j), h0 = first_head(a, c.j);
 #pragma unroll
           for (int odd = 0; odd < 2; ++odd) {
             if (2 * t + odd >= nh) continue;
-            const float fo = inv[odd] * a.v_scale;
+            const float fo = a.v_scale / l[odd];
             uint4* dst = reinterpret_cast<uint4*>(
                 a.out + (static_cast<int64_t>(c.b) * a.n_q + h0 + 2 * t + odd) * HD + 32 * g);
 #pragma unroll
@@ -604,29 +709,28 @@ fp4_decode_kernel(const Args a) {
                 }
                 dst[part * 32 + i] = make_uint4(w[0], w[1], w[2], w[3]);
               }
-            if (g == 0) write_lse(a, p, 2 * t + odd, m[odd], l[odd]);
+            if (g == 0) write_lse(a, Piece{c.b, c.j, 0, 0, 0}, 2 * t + odd, m[odd], l[odd]);
           }
         } else {
           put(a.ws_o + static_cast<int64_t>(me) * (C::kParts * 128 * hp));
-          if (g == 0) {
-            s_ml[2 * warp][2 * t] = make_float2(m[0], l[0]);
-            s_ml[2 * warp][2 * t + 1] = make_float2(m[1], l[1]);
-          }
-          if (lane == 0) s_piece[2 * warp] = p;
+          note(2 * warp);
         }
-        c.next_unit(a, ups);
+        c.next(a, ups);
+        page = 0;
         load_q();
         begin_piece();
       }
     }
-    if (!failed) {
+    if (failed) {
+      if (lane == 0) flag_error(a.err, PSW_DEVERR_PIPELINE);
+      for (int i = 0; i < S; ++i) {  // copies in flight have to land: a stage's last phase
+        const int last = n - 1 - ((n - 1 - i) & (S - 1));
+        if (last >= 0) mbar_wait(&s_full[warp][i], (last / S) & 1);
+      }
+    } else {
       sum_l();
       put(reinterpret_cast<float4*>(ring));
-      if (g == 0) {
-        s_ml[2 * warp + 1][2 * t] = make_float2(m[0], l[0]);
-        s_ml[2 * warp + 1][2 * t + 1] = make_float2(m[1], l[1]);
-      }
-      if (lane == 0) s_piece[2 * warp + 1] = Piece{c.b, c.j, c.tile0, c.s.np, c.page - piece_from};
+      note(2 * warp + 1);
     }
   }
   __syncthreads();
@@ -645,7 +749,7 @@ fp4_decode_kernel(const Args a) {
       const uint32_t members = have & ~((1u << lane) - 1u) & (after != 0 ? (after & -after) - 1u : ~0u);
       int pages = 0;
       for (uint32_t i = members; i != 0; i &= i - 1) pages += s_piece[__ffs(i) - 1].pages;
-      s_group[__popc(start & ((1u << lane) - 1u))] = Group{p, members, pages};
+      s_u.group[__popc(start & ((1u << lane) - 1u))] = Group{p, members, pages};
     }
     if (lane == 0) s_groups = __popc(start);
   }
@@ -655,7 +759,7 @@ fp4_decode_kernel(const Args a) {
   // weights of a group's pieces, a lane each: M = max m_i, 2^(m_i - M), over the sum of l where
   // the unit is complete
   for (int y = warp; y < groups * kQHeadsPerUnit; y += W) {
-    const Group& gr = s_group[y / kQHeadsPerUnit];
+    const Group& gr = s_u.group[y / kQHeadsPerUnit];
     const int head = y % kQHeadsPerUnit;
     if (head >= heads_of(a, gr.p.j)) continue;
     const bool mine_too = (gr.members >> lane) & 1;
@@ -667,7 +771,7 @@ fp4_decode_kernel(const Args a) {
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     const bool whole = gr.pages == gr.p.np;
     if (whole) w *= 1.f / L;
-    if (mine_too) s_weight[lane][head] = w;
+    if (mine_too) s_u.weight[lane][head] = w;
     if (lane == 0) {
       if (whole)
         write_lse(a, gr.p, head, M, L);
@@ -676,42 +780,57 @@ fp4_decode_kernel(const Args a) {
     }
   }
   __syncthreads();
-  for (int y = warp; y < groups * (units / 32); y += W) {
-    const int gi = y / (units / 32), x = (y - gi * (units / 32)) * 32 + lane;
-    const Group& gr = s_group[gi];
-    const Unit4 u = piece_unit(x, hp);
+  // four neighbours of 32 float4 a warp at a time: a first piece's are loads from afar
+  for (int y = warp; y < groups * (units / 128); y += W) {
+    const int gi = y / (units / 128), x0 = (y - gi * (units / 128)) * 128 + lane;
+    const Group& gr = s_u.group[gi];
     const int nh = heads_of(a, gr.p.j);
-    if (u.head >= nh) continue;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float4& v, float w) {
-      o.x += v.x * w;
-      o.y += v.y * w;
-      o.z += v.z * w;
-      o.w += v.w * w;
-    };
     // (a first piece can only be the last of a group: the run that it begins goes on elsewhere)
     const int last = 31 - __clz(gr.members);
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (!(last & 1))
-      v = __ldcg(a.ws_o + (static_cast<int64_t>(blockIdx.x) * W + (last >> 1)) * units + x);
     const int w0 = (__ffs(gr.members) - 1) >> 1, w1 = (last - 1) >> 1;  // its last pieces
-#pragma unroll 4
-    for (int i = w0; i <= w1; ++i)
-      add(reinterpret_cast<const float4*>(smem + i * C::kRingBytes)[x],
-          s_weight[2 * i + 1][u.head]);
-    if (!(last & 1)) add(v, s_weight[last][u.head]);
-    if (gr.pages == gr.p.np)
-      write_out<HD>(a, gr.p, nh, u, o, 1.f);
-    else
-      a.ws_o[(part0 + blockIdx.x + gr.p.b * ups + gr.p.j) * units + x] = o;
+    float4 o[4];
+    int head[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      head[k] = piece_unit(x0 + 32 * k, hp).head;
+      o[k] = (last & 1) ? make_float4(0.f, 0.f, 0.f, 0.f)
+                        : __ldcg(a.ws_o + (static_cast<int64_t>(blockIdx.x) * W + (last >> 1)) * units +
+                                 x0 + 32 * k);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float w = (last & 1) ? 0.f : s_u.weight[last][head[k]];
+      o[k] = make_float4(o[k].x * w, o[k].y * w, o[k].z * w, o[k].w * w);
+    }
+    for (int i = w0; i <= w1; ++i) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 v = reinterpret_cast<const float4*>(smem + i * C::kRingBytes)[x0 + 32 * k];
+        const float w = s_u.weight[2 * i + 1][head[k]];
+        o[k].x += v.x * w;
+        o[k].y += v.y * w;
+        o[k].z += v.z * w;
+        o[k].w += v.w * w;
+      }
+    }
+    const int64_t slot = part0 + blockIdx.x + gr.p.b * ups + gr.p.j;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int x = x0 + 32 * k;
+      if (head[k] >= nh) continue;
+      if (gr.pages == gr.p.np)
+        write_out<HD>(a, gr.p, nh, piece_unit(x, hp), o[k], 1.f);
+      else
+        a.ws_o[slot * units + x] = o[k];
+    }
   }
   // ---- units that other CTAs have pages of: this CTA's first or last
   __syncthreads();
   if (tid < 2 && groups > tid) {
     const int gi = tid == 0 ? 0 : groups - 1;
-    const Group& gr = s_group[gi];
+    const Group& gr = s_u.group[gi];
     if (gr.pages != gr.p.np) {
-      int32_t* ticket = a.tickets + cut.worker(gr.p.tile0) / W;
+      int32_t* ticket = a.tickets + ctas_of<W>(cut, gr.p).first;
       __threadfence();
       if (atomicAdd(ticket, gr.pages) + gr.pages == gr.p.np) {
         *ticket = 0;
@@ -728,11 +847,11 @@ fp4_decode_kernel(const Args a) {
     for (int y = warp; y < 2 * kQHeadsPerUnit; y += W) {
       const int which = y / kQHeadsPerUnit, head = y % kQHeadsPerUnit;
       if (s_last[which] == 0) continue;
-      const Piece& p = s_group[s_last[which] - 1].p;
+      const Piece& p = s_u.group[s_last[which] - 1].p;
       if (head >= heads_of(a, p.j)) continue;
-      const int c0 = cut.worker(p.tile0) / W;
-      const int n = cut.worker(p.tile0 + p.np - 1) / W - c0 + 1;
-      const float2* ml = a.ws_ml + (part0 + c0 + p.b * ups + p.j) * a.rows + head;
+      const Ctas cs = ctas_of<W>(cut, p);
+      const int n = cs.n;
+      const float2* ml = a.ws_ml + (part0 + cs.first + p.b * ups + p.j) * a.rows + head;
       float M = -INFINITY, L = 0.f;
       for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(ml + i * a.rows).x);
       M = lat::warp_max(M);
@@ -749,27 +868,35 @@ fp4_decode_kernel(const Args a) {
       if (lane == 0) write_lse(a, p, head, M, L);
     }
     __syncthreads();
-    for (int y = warp; y < 2 * (units / 32); y += W) {
-      const int which = y / (units / 32), x = (y - which * (units / 32)) * 32 + lane;
+    for (int y = warp; y < 2 * (units / 128); y += W) {
+      const int which = y / (units / 128), x0 = (y - which * (units / 128)) * 128 + lane;
       if (s_last[which] == 0) continue;
-      const Piece& p = s_group[s_last[which] - 1].p;
-      const Unit4 u = piece_unit(x, hp);
+      const Piece& p = s_u.group[s_last[which] - 1].p;
       const int nh = heads_of(a, p.j);
-      if (u.head >= nh) continue;
-      const int c0 = cut.worker(p.tile0) / W;
-      const int n = cut.worker(p.tile0 + p.np - 1) / W - c0 + 1;
-      const float4* src = a.ws_o + (part0 + c0 + p.b * ups + p.j) * units + x;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) {
-        const float4 v = __ldcg(src + static_cast<int64_t>(i) * units);
-        const float fo = s_join[which][u.head][i];
-        o.x += v.x * fo;
-        o.y += v.y * fo;
-        o.z += v.z * fo;
-        o.w += v.w * fo;
+      const Ctas cs = ctas_of<W>(cut, p);
+      const float4* src = a.ws_o + (part0 + cs.first + p.b * ups + p.j) * units + x0;
+      float4 o[4];
+      int head[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        head[k] = piece_unit(x0 + 32 * k, hp).head;
       }
-      write_out<HD>(a, p, nh, u, o, 1.f);
+#pragma unroll 4
+      for (int i = 0; i < cs.n; ++i) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 v = __ldcg(src + static_cast<int64_t>(i) * units + 32 * k);
+          const float w = s_join[which][head[k]][i];
+          o[k].x += v.x * w;
+          o[k].y += v.y * w;
+          o[k].z += v.z * w;
+          o[k].w += v.w * w;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        write_out<HD>(a, p, nh, piece_unit(x0 + 32 * k, hp), o[k], 1.f);
     }
   }
   // ---- sequences without keys, and lengths that are wrong

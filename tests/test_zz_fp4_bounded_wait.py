@@ -16,7 +16,7 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("cta,tile", [(0, 0), (0, 2), (3, 1)])
 @pytest.mark.parametrize("layer", [Layer(4, 2, 256), Layer(8, 1, 512, k_eq_v=True)], ids=["256", "512-keqv"])
 def test_wait_runs_out_and_the_next_call_is_exact(layer, cta, tile):
-    lens = [19000, 15000, 40, 60000]  # (three pages or more for every warp)
+    lens = [38000, 30000, 40, 120000]  # (several tiles for every warp)
     cache, q = filled(layer, lens, 41)
     ws = binding.alloc_fp4_workspace(layer, 4)
     want = decode(layer, cache, q, lens, ws=ws)
