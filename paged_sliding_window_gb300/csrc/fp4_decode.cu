@@ -167,6 +167,16 @@ struct Place {
   }
 };
 
+// The unit after a warp's `at`, which it becomes.
+__device__ __forceinline__ Place next_place(Place* at, const Args& a, int ups) {
+  Place p = *at;
+  p.next(a, ups);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) *at = p;
+  __syncwarp();
+  return p;
+}
+
 // A unit's first query head, and how many it has.
 __device__ __forceinline__ int first_head(const Args& a, int j) {
   return j / a.qchunks * a.group + j % a.qchunks * kQHeadsPerUnit;
@@ -254,6 +264,9 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
     };
   } s_u;
   __shared__ int s_sum[kRuns / 32];
+  // a warp's unit that is worked on, and that of the next page to fetch: wanted at a unit's
+  // ends alone, and no registers are to spare between them
+  __shared__ Place s_now[W], s_next[W];
   __shared__ int s_groups;
   __shared__ int s_last[2];  // group + 1
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -295,8 +308,8 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
   const Cut cut{tiles / workers, tiles % workers};
   const int me = blockIdx.x * W + warp;
 
-  Place c;        // the unit that is worked on
-  int page = 0;   // its next page
+  int page = 0;   // the next page of the unit that is worked on
+  int np = 0;     // its pages
   int left = 0;   // entries of the run from the next page to fetch on
   if (me < min(workers, tiles)) {
     const int begin = cut.begin(me);
@@ -307,6 +320,7 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
       const int mid = (lo + hi) >> 1;
       if (s_u.run[mid] <= x) lo = mid; else hi = mid;
     }
+    Place c;
     c.b = lo * per;
     int off = s_u.run[lo];
     c.s = seq_of(a, c.b);
@@ -320,11 +334,13 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
     c.tile0 = begin - at;
     page = max(0, at - kUnitCost);
     left -= max(0, kUnitCost - at);
+    np = c.s.np;
+    if (lane == 0) s_now[warp] = s_next[warp] = c;
+    __syncwarp();
   }
   if (left > 0) {
     // ---- fetching: a tile's blocks, a copy by each of the first lanes
-    Place f = c;
-    int f_page = page, ids_at = 0;
+    int f_page = page, f_np = np, ids_at = 0;
     int32_t ids = 0;     // lane i: block of page ids_at + i
     int n = 0;           // tiles asked for
     uint32_t info = 0;   // four bits per stage: more than one page; pages without a valid block
@@ -333,21 +349,24 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
     const bool my_v = C::kTensors == 2 && (lane & 1);
     const uint8_t* f_from = nullptr;  // this lane's tensor, at the unit's KV head of block 0
     auto fetch_unit = [&]() {
+      const Place& f = s_next[warp];
       f_from = (my_v ? a.v_pool : a.k_pool) +
                static_cast<int64_t>(f.j / a.qchunks) * Page<HD>::kBytes;
     };
     auto fetch_ids = [&]() {
+      const Place& f = s_next[warp];
       ids_at = f_page;
       const int at = f_page + lane;
-      ids = at < f.s.np
+      ids = at < f_np
                 ? __ldg(a.table + static_cast<int64_t>(f.b) * a.max_blocks + f.s.p0 + at)
                 : 0;
     };
     auto fetch = [&]() {  // the next tile of the run, if there is one
-      if (f_page == f.s.np) {
+      if (f_page == f_np) {
         left -= kUnitCost;
         if (left <= 0) return;
-        f.next(a, ups);
+        const Place f = next_place(&s_next[warp], a, ups);
+        f_np = f.s.np;
         f_page = 0;
         fetch_unit();
         fetch_ids();
@@ -358,7 +377,7 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
           asm volatile("prefetch.global.L2 [%0];" ::"l"(q + k));
       }
       if (f_page - ids_at > 32 - TP) fetch_ids();
-      const int pages = min(min(TP, f.s.np - f_page), left);
+      const int pages = min(min(TP, f_np - f_page), left);
       int32_t blk = __shfl_sync(0xffffffffu, ids, (f_page - ids_at + my_page) & 31);
       const int st = n & (S - 1);
       const bool mine = lane < pages * C::kTensors;
@@ -386,10 +405,13 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
     const int r0 = (g & 1) ? (((g & 6) ^ 4) | 1) : g;
     const int ra = 2 * t, rb = ((2 * t) ^ 4) | 1;
     constexpr int kRow = Page<HD>::kScaleRow, kCodes = Page<HD>::kCodeBytes;
-    const int k_at = r0 * 128 + ((t ^ (r0 & 7)) << 4);  // unit t; unit 4 + t: ^ 64
-    const int ks_at = kCodes + r0 * kRow + t * Page<HD>::kLaneScales;
-    const int va_at = ra * 128 + ((g ^ ra) << 4), vb_at = rb * 128 + ((g ^ rb) << 4);
-    const int vs_at = kCodes + (g & 3) * Page<HD>::kLaneScales + (g >> 2) * (HD / 128);
+    int k_at = r0 * 128 + ((t ^ (r0 & 7)) << 4);  // unit t; unit 4 + t: ^ 64
+    int ks_at = kCodes + r0 * kRow + t * Page<HD>::kLaneScales;
+    int va_at = ra * 128 + ((g ^ ra) << 4), vb_at = rb * 128 + ((g ^ rb) << 4);
+    int vs_at = kCodes + (g & 3) * Page<HD>::kLaneScales + (g >> 2) * (HD / 128) + ra * kRow;
+    // (kept in registers: formed anew for every tile they would cost as much as the softmax)
+    asm volatile("" : "+r"(k_at), "+r"(ks_at), "+r"(va_at), "+r"(vb_at), "+r"(vs_at));
+    const int vs_b = (rb - ra) * kRow;
 
     uint32_t qr[HD == 256 ? 32 : 1];  // q as operands: HD 256 in registers, HD 512 in shared memory
     uint4* q_smem = reinterpret_cast<uint4*>(smem + W * C::kRingBytes + warp * C::kQBytes) + lane;
@@ -401,6 +423,7 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
     uint4 raw[HD / 128][4];
 
     auto load_q = [&]() {
+      const Place& c = s_now[warp];
       const int row = first_head(a, c.j) + min(g, heads_of(a, c.j) - 1);
       const uint4* src =
           reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(c.b) * a.n_q + row) * HD) +
@@ -451,6 +474,7 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
       m[0] = m[1] = -INFINITY;
       l[0] = l[1] = 0.f;
       piece_from = page;
+      const Place& c = s_now[warp];
       ends = ((0xFFFFu << (c.s.lo & (kBlockSize - 1))) & 0xFFFFu) |
              (0xFFFFu >> (kBlockSize - 1 - ((c.s.len - 1) & (kBlockSize - 1)))) << 16;
     };
@@ -481,6 +505,7 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
         s_ml[at][2 * t] = make_float2(m[0], l[0]);
         s_ml[at][2 * t + 1] = make_float2(m[1], l[1]);
       }
+      const Place& c = s_now[warp];
       if (lane == 0) s_piece[at] = Piece{c.b, c.j, c.tile0, c.s.np, page - piece_from};
     };
 
@@ -503,7 +528,7 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
       constexpr uint32_t kAll = TP == 1 ? 0xFFFFu : 0xFFFFFFFFu;
       uint32_t seen = pages == TP ? kAll : 0xFFFFu;
       if (page == 0) seen &= 0xFFFF0000u | ends;
-      if (page + pages == c.s.np)
+      if (page + pages == np)
         seen &= pages == 1 ? ends >> 16 : (ends & 0xFFFF0000u) | 0xFFFFu;
       const bool edge = seen != kAll || (word & 6) != 0;
 
@@ -642,7 +667,7 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
         const int rows[4] = {ra, rb, ra + 8, rb + 8};
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const uint8_t* x = vp + vs_at + rows[r] * kRow;
+          const uint8_t* x = vp + vs_at + (r & 1 ? vs_b : 0) + (r >> 1) * 8 * kRow;
           if constexpr (HD == 256)
             vs[r] = *reinterpret_cast<const uint16_t*>(x);
           else
@@ -687,9 +712,10 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
       __syncwarp();  // every lane has read the tile
       if (left > 0) fetch();
       page += pages;
-      if (page == c.s.np && it + 1 < n) {  // the unit ends and the run goes on
+      if (page == np && it + 1 < n) {  // the unit ends and the run goes on
         sum_l();
-        if (page - piece_from == c.s.np) {
+        if (page - piece_from == np) {
+          const Place& c = s_now[warp];
           const int nh = heads_of(a, c.j), h0 = first_head(a, c.j);
 #pragma unroll
           for (int odd = 0; odd < 2; ++odd) {
@@ -715,7 +741,7 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
           put(a.ws_o + static_cast<int64_t>(me) * (C::kParts * 128 * hp));
           note(2 * warp);
         }
-        c.next(a, ups);
+        np = next_place(&s_now[warp], a, ups).s.np;
         page = 0;
         load_q();
         begin_piece();
