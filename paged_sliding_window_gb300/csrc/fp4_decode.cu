@@ -29,7 +29,7 @@
 //    others it has at most two, the end of one unit (kept in the workspace, its CTA
 //    alone reads it) and the beginning or middle of another (left in shared memory
 //    where the ring was). The CTA joins what its warps have of a unit; only units
-//    that other CTAs have pages of, two at most, go on to the workspace, and the CTA
+//    that other CTAs have pages of, two at most, go on to the workspace, and the warp
 //    that adds a unit's last pages (a ticket counts them) joins the CTAs' parts, in
 //    their order.
 #include "fp4.cuh"
@@ -42,6 +42,7 @@ using fp4::Page;
 
 constexpr int kMaxCtas = 160;  // one per SM; what they need of workspace is counted with it
 constexpr int kMaxWarps = 12;
+constexpr int kMaxJobs = 8;    // parts of a unit's output that are joined apart, at most
 constexpr int kUnitCost = kFp4UnitCost;  // what beginning and ending a unit takes, in pages
 constexpr int kRuns = 256;     // runs of sequences whose entries are summed
 
@@ -61,7 +62,8 @@ struct Cfg {
   static_assert(kWarps <= kMaxWarps && 2 * kWarps <= 32, "pieces of a CTA");
   static_assert(kStages * kTileBytes == kRingBytes && kStages >= 2 && kStages <= 8, "ring");
   static_assert(HD * 8 * 4 <= kRingBytes, "a piece's output fits where the ring was");
-  static_assert(2 * kQHeadsPerUnit * kMaxCtas * 4 <= kRingBytes, "weights of two units");
+  static_assert(HD * 8 * 4 + 2 * kWarps * 8 * 4 <= kRingBytes, "and its weights");
+  static_assert(kMaxCtas * kMaxJobs * 4 <= PSW_FP4_COUNTER_BYTES && kParts * 4 <= kMaxJobs, "tickets");
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -134,8 +136,8 @@ struct Args {
   __nv_bfloat16* out;
   float* lse;
   float4* ws_o;      // [slot][half of a row's pairs ...], see piece_unit
-  float2* ws_ml;     // [slot][rows]
-  int32_t* tickets;  // [CTA]: of the unit that it begins and does not end
+  float2* ws_ml;     // [slot][job][rows]
+  int32_t* tickets;  // [CTA][job]: pages joined of the unit that the CTA begins and does not end
   int rows;          // rows of a slot: the group's heads, 8 at most, made even
   int32_t* err;
   int stall_cta, stall_tile;
@@ -231,13 +233,6 @@ struct Cut {
   }
 };
 
-// What a CTA has of one unit: pieces `members` (bit 2 w: the end of the unit that warp w
-// began with, bit 2 w + 1: the last unit of warp w), `pages` of its pages.
-struct Group {
-  Piece p;
-  uint32_t members;
-  int pages;
-};
 // The CTAs (of K workers) that have pages of a unit: the first of them and how many.
 struct Ctas {
   int first, n;
@@ -256,19 +251,11 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
   __shared__ uint64_t s_full[W][S];
   __shared__ Piece s_piece[2 * W];
   __shared__ float2 s_ml[2 * W][kQHeadsPerUnit];
-  __shared__ union {
-    int run[kRuns + 1];  // at the beginning
-    struct {             // at the end
-      float weight[2 * W][kQHeadsPerUnit];
-      Group group[2 * W];
-    };
-  } s_u;
+  __shared__ int s_run[kRuns + 1];
   __shared__ int s_sum[kRuns / 32];
   // a warp's unit that is worked on, and that of the next page to fetch: wanted at a unit's
   // ends alone, and no registers are to spare between them
   __shared__ Place s_now[W], s_next[W];
-  __shared__ int s_groups;
-  __shared__ int s_last[2];  // group + 1
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * C::kRingBytes;
@@ -292,7 +279,6 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
     if (lane == 31) s_sum[warp] = incl;
   }
   if (tid < 2 * W) s_piece[tid].pages = 0;
-  if (tid < 2) s_last[tid] = 0;
   __syncthreads();
   int all = 0;
 #pragma unroll
@@ -300,8 +286,8 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
     if (i == warp) incl += all;
     all += s_sum[i];
   }
-  if (tid < kRuns) s_u.run[tid + 1] = incl;
-  if (tid == 0) s_u.run[0] = 0;
+  if (tid < kRuns) s_run[tid + 1] = incl;
+  if (tid == 0) s_run[0] = 0;
   __syncthreads();
   const int tiles = all * ups;
   const int workers = max(1, min(static_cast<int>(gridDim.x) * W, tiles));
@@ -318,11 +304,11 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
     int lo = 0, hi = kRuns;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (s_u.run[mid] <= x) lo = mid; else hi = mid;
+      if (s_run[mid] <= x) lo = mid; else hi = mid;
     }
     Place c;
     c.b = lo * per;
-    int off = s_u.run[lo];
+    int off = s_run[lo];
     c.s = seq_of(a, c.b);
     while (c.s.np == 0 || x >= off + c.s.np + kUnitCost) {
       if (c.s.np > 0) off += c.s.np + kUnitCost;
@@ -761,59 +747,40 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
   }
   __syncthreads();
 
-  // ---- the pieces of one unit are neighbours: groups of them
-  if (warp == 0) {
-    const Piece p = s_piece[min(lane, 2 * W - 1)];
-    const bool valid = lane < 2 * W && p.pages > 0;
-    const uint32_t have = __ballot_sync(0xffffffffu, valid);
+  // ---- joining: the pieces of a unit are neighbours. A warp takes 128 float4 of what the CTA
+  // has of a unit at a time and needs no other warp for the rest of the way: it writes the
+  // result, or this CTA's part and, if its part is the last to come, the result of all parts.
+  const Piece mine = s_piece[min(lane, 2 * W - 1)];
+  const bool valid = lane < 2 * W && mine.pages > 0;
+  const uint32_t have = __ballot_sync(0xffffffffu, valid);
+  uint32_t start;  // the first piece of every unit
+  {
     const uint32_t prev = have & ((1u << lane) - 1u);
-    const int before_me = __shfl_sync(0xffffffffu, p.tile0, prev != 0 ? 31 - __clz(prev) : 0);
-    const bool starts = valid && (prev == 0 || before_me != p.tile0);
-    const uint32_t start = __ballot_sync(0xffffffffu, starts);
-    if (starts) {
-      const uint32_t after = start & ~((2u << lane) - 1u);
-      const uint32_t members = have & ~((1u << lane) - 1u) & (after != 0 ? (after & -after) - 1u : ~0u);
-      int pages = 0;
-      for (uint32_t i = members; i != 0; i &= i - 1) pages += s_piece[__ffs(i) - 1].pages;
-      s_u.group[__popc(start & ((1u << lane) - 1u))] = Group{p, members, pages};
-    }
-    if (lane == 0) s_groups = __popc(start);
+    const int other = __shfl_sync(0xffffffffu, mine.tile0, prev != 0 ? 31 - __clz(prev) : 0);
+    start = __ballot_sync(0xffffffffu, valid && (prev == 0 || other != mine.tile0));
   }
-  __syncthreads();
-  const int units = C::kParts * 128 * hp, groups = s_groups;
+  const int jobs = C::kParts * hp, units = jobs * 128;  // of a unit; its float4s
   const int64_t part0 = static_cast<int64_t>(gridDim.x) * W;  // slots of the CTAs' parts
-  // weights of a group's pieces, a lane each: M = max m_i, 2^(m_i - M), over the sum of l where
-  // the unit is complete
-  for (int y = warp; y < groups * kQHeadsPerUnit; y += W) {
-    const Group& gr = s_u.group[y / kQHeadsPerUnit];
-    const int head = y % kQHeadsPerUnit;
-    if (head >= heads_of(a, gr.p.j)) continue;
-    const bool mine_too = (gr.members >> lane) & 1;
-    const float2 ml = mine_too ? s_ml[lane][head] : make_float2(-INFINITY, 0.f);
-    const float M = lat::warp_max(ml.x);
-    float w = mine_too ? ex2_approx(ml.x - M) : 0.f;
-    float L = w * ml.y;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    const bool whole = gr.pages == gr.p.np;
-    if (whole) w *= 1.f / L;
-    if (mine_too) s_u.weight[lane][head] = w;
-    if (lane == 0) {
-      if (whole)
-        write_lse(a, gr.p, head, M, L);
-      else
-        a.ws_ml[(part0 + blockIdx.x + gr.p.b * ups + gr.p.j) * a.rows + head] = make_float2(M, L);
-    }
-  }
-  __syncthreads();
-  // four neighbours of 32 float4 a warp at a time: a first piece's are loads from afar
-  for (int y = warp; y < groups * (units / 128); y += W) {
-    const int gi = y / (units / 128), x0 = (y - gi * (units / 128)) * 128 + lane;
-    const Group& gr = s_u.group[gi];
-    const int nh = heads_of(a, gr.p.j);
-    // (a first piece can only be the last of a group: the run that it begins goes on elsewhere)
-    const int last = 31 - __clz(gr.members);
-    const int w0 = (__ffs(gr.members) - 1) >> 1, w1 = (last - 1) >> 1;  // its last pieces
+  float* weight = reinterpret_cast<float*>(ring + HD * 8 * 4);  // [piece][head], of this warp
+  const int h = lane & 7, sub = lane >> 3;
+  for (int y = warp; y < __popc(start) * jobs; y += W) {
+    const int gi = y / jobs, job = y - gi * jobs, x0 = job * 128 + lane;
+    uint32_t from = start;
+    for (int k = 0; k < gi; ++k) from &= from - 1;
+    const int first = __ffs(from) - 1;
+    from &= from - 1;  // the starts behind it
+    const uint32_t members =
+        have & ~((1u << first) - 1u) & (from != 0 ? (from & -from) - 1u : ~0u);
+    const int pages = __reduce_add_sync(0xffffffffu, (members >> lane) & 1 ? mine.pages : 0);
+    Piece p;
+    p.b = __shfl_sync(0xffffffffu, mine.b, first);
+    p.j = __shfl_sync(0xffffffffu, mine.j, first);
+    p.tile0 = __shfl_sync(0xffffffffu, mine.tile0, first);
+    p.np = __shfl_sync(0xffffffffu, mine.np, first);
+    const int nh = heads_of(a, p.j);
+    // (a first piece can only be the last of a unit: the run that it begins goes on elsewhere)
+    const int last = 31 - __clz(members);
+    const int w0 = first >> 1, w1 = (last - 1) >> 1;  // its last pieces
     float4 o[4];
     int head[4];
 #pragma unroll
@@ -823,106 +790,101 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
                         : __ldcg(a.ws_o + (static_cast<int64_t>(blockIdx.x) * W + (last >> 1)) * units +
                                  x0 + 32 * k);
     }
+    // M = max m_i, weights 2^(m_i - M), their sum of l; a lane has every fourth piece of head h
+    float M = -INFINITY, L = 0.f;
+    for (int i = sub; i < 2 * W; i += 4)
+      if ((members >> i) & 1) M = fmaxf(M, s_ml[i][h].x);
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+    __syncwarp();
+    for (int i = sub; i < 2 * W; i += 4) {
+      if (!((members >> i) & 1)) continue;
+      const float2 ml = s_ml[i][h];
+      const float w = ex2_approx(ml.x - M);
+      weight[i * 8 + h] = w;
+      L += w * ml.y;
+    }
+    L += __shfl_xor_sync(0xffffffffu, L, 8);
+    L += __shfl_xor_sync(0xffffffffu, L, 16);
+    __syncwarp();
+    auto add = [](float4& s, const float4& v, float w) {
+      s.x += v.x * w;
+      s.y += v.y * w;
+      s.z += v.z * w;
+      s.w += v.w * w;
+    };
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float w = (last & 1) ? 0.f : s_u.weight[last][head[k]];
+      const float w = (last & 1) ? 0.f : weight[last * 8 + head[k]];
       o[k] = make_float4(o[k].x * w, o[k].y * w, o[k].z * w, o[k].w * w);
     }
     for (int i = w0; i <= w1; ++i) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 v = reinterpret_cast<const float4*>(smem + i * C::kRingBytes)[x0 + 32 * k];
-        const float w = s_u.weight[2 * i + 1][head[k]];
-        o[k].x += v.x * w;
-        o[k].y += v.y * w;
-        o[k].z += v.z * w;
-        o[k].w += v.w * w;
-      }
+      for (int k = 0; k < 4; ++k)
+        add(o[k], reinterpret_cast<const float4*>(smem + i * C::kRingBytes)[x0 + 32 * k],
+            weight[(2 * i + 1) * 8 + head[k]]);
     }
-    const int64_t slot = part0 + blockIdx.x + gr.p.b * ups + gr.p.j;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int x = x0 + 32 * k;
-      if (head[k] >= nh) continue;
-      if (gr.pages == gr.p.np)
-        write_out<HD>(a, gr.p, nh, piece_unit(x, hp), o[k], 1.f);
-      else
-        a.ws_o[slot * units + x] = o[k];
-    }
-  }
-  // ---- units that other CTAs have pages of: this CTA's first or last
-  __syncthreads();
-  if (tid < 2 && groups > tid) {
-    const int gi = tid == 0 ? 0 : groups - 1;
-    const Group& gr = s_u.group[gi];
-    if (gr.pages != gr.p.np) {
-      int32_t* ticket = a.tickets + ctas_of<W>(cut, gr.p).first;
-      __threadfence();
-      if (atomicAdd(ticket, gr.pages) + gr.pages == gr.p.np) {
-        *ticket = 0;
-        s_last[tid] = gi + 1;
-      }
-      __threadfence();
-    }
-  }
-  __syncthreads();
-  if (s_last[0] != 0 || s_last[1] != 0) {
-    // M = max m_i, l = sum l_i 2^(m_i - M), weights 2^(m_i - M) / l; then out = sum O_i weight_i
-    // (the warps' pieces have been read: their place takes the weights)
-    auto s_join = reinterpret_cast<float(*)[kQHeadsPerUnit][kMaxCtas]>(smem);
-    for (int y = warp; y < 2 * kQHeadsPerUnit; y += W) {
-      const int which = y / kQHeadsPerUnit, head = y % kQHeadsPerUnit;
-      if (s_last[which] == 0) continue;
-      const Piece& p = s_u.group[s_last[which] - 1].p;
-      if (head >= heads_of(a, p.j)) continue;
-      const Ctas cs = ctas_of<W>(cut, p);
-      const int n = cs.n;
-      const float2* ml = a.ws_ml + (part0 + cs.first + p.b * ups + p.j) * a.rows + head;
-      float M = -INFINITY, L = 0.f;
-      for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(ml + i * a.rows).x);
-      M = lat::warp_max(M);
-      for (int i = lane; i < n; i += 32) {
-        const float2 x = __ldcg(ml + i * a.rows);
-        const float fo = ex2_approx(x.x - M);
-        s_join[which][head][i] = fo;
-        L += x.y * fo;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (pages == p.np) {
       const float inv = 1.f / L;
-      for (int i = lane; i < n; i += 32) s_join[which][head][i] *= inv;
-      if (lane == 0) write_lse(a, p, head, M, L);
-    }
-    __syncthreads();
-    for (int y = warp; y < 2 * (units / 128); y += W) {
-      const int which = y / (units / 128), x0 = (y - which * (units / 128)) * 128 + lane;
-      if (s_last[which] == 0) continue;
-      const Piece& p = s_u.group[s_last[which] - 1].p;
-      const int nh = heads_of(a, p.j);
-      const Ctas cs = ctas_of<W>(cut, p);
-      const float4* src = a.ws_o + (part0 + cs.first + p.b * ups + p.j) * units + x0;
-      float4 o[4];
-      int head[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        head[k] = piece_unit(x0 + 32 * k, hp).head;
-      }
-#pragma unroll 4
-      for (int i = 0; i < cs.n; ++i) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float4 v = __ldcg(src + static_cast<int64_t>(i) * units + 32 * k);
-          const float w = s_join[which][head[k]][i];
-          o[k].x += v.x * w;
-          o[k].y += v.y * w;
-          o[k].z += v.z * w;
-          o[k].w += v.w * w;
-        }
-      }
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        write_out<HD>(a, p, nh, piece_unit(x0 + 32 * k, hp), o[k], 1.f);
+        write_out<HD>(a, p, nh, piece_unit(x0 + 32 * k, hp), o[k],
+                      __shfl_sync(0xffffffffu, inv, head[k]));
+      if (job == 0 && lane < nh) write_lse(a, p, lane, M, L);
+      continue;
+    }
+    // a unit that other CTAs have pages of: this CTA's first or last
+    const Ctas cs = ctas_of<W>(cut, p);
+    const int64_t slot0 = part0 + cs.first + p.b * ups + p.j;  // of the first CTA's part
+    const int64_t slot = slot0 + static_cast<int>(blockIdx.x) - cs.first;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a.ws_o[slot * units + x0 + 32 * k] = o[k];
+    if (lane < a.rows) a.ws_ml[(slot * jobs + job) * a.rows + lane] = make_float2(M, L);
+    __syncwarp();
+    int done = 0;
+    if (lane == 0) {
+      int32_t* ticket = a.tickets + cs.first * kMaxJobs + job;
+      __threadfence();
+      done = atomicAdd(ticket, pages) + pages == p.np;
+      if (done) *ticket = 0;
+    }
+    if (__shfl_sync(0xffffffffu, done, 0) == 0) continue;
+    __threadfence();
+    // one pass over the parts with the running maximum and sum of every lane's four
+    const float4* src = a.ws_o + slot0 * units + x0;
+    const float2* ml = a.ws_ml + (slot0 * jobs + job) * a.rows;
+    float top[4], sum[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      top[k] = -INFINITY;
+      sum[k] = 0.f;
+      o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 2
+    for (int i = 0; i < cs.n; ++i) {
+      float4 v[4];
+      float2 x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[k] = __ldcg(src + static_cast<int64_t>(i) * units + 32 * k);
+        x[k] = __ldcg(ml + static_cast<int64_t>(i) * jobs * a.rows + head[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float mn = fmaxf(top[k], x[k].x);
+        const float f0 = top[k] == mn ? 1.f : ex2_approx(top[k] - mn);
+        const float f1 = ex2_approx(x[k].x - mn);
+        top[k] = mn;
+        sum[k] = sum[k] * f0 + x[k].y * f1;
+        o[k] = make_float4(o[k].x * f0, o[k].y * f0, o[k].z * f0, o[k].w * f0);
+        add(o[k], v[k], f1);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const Unit4 u = piece_unit(x0 + 32 * k, hp);
+      write_out<HD>(a, p, nh, u, o[k], 1.f / sum[k]);
+      if (u.d == 0 && u.head < nh) write_lse(a, p, u.head, top[k], sum[k]);
     }
   }
   // ---- sequences without keys, and lengths that are wrong
@@ -964,7 +926,8 @@ size_t slots_of(const LayerArgs& L, int n_seqs) {
 }  // namespace
 
 size_t fp4_decode_workspace(const LayerArgs& L, int n_seqs) {
-  return kFp4CounterBytes + slots_of(L, n_seqs) * slot_rows(L) * (static_cast<size_t>(L.hd) * 4 + 8);
+  const size_t jobs = static_cast<size_t>(L.hd) / 256 * (slot_rows(L) / 2);
+  return kFp4CounterBytes + slots_of(L, n_seqs) * slot_rows(L) * (L.hd * 4 + jobs * 8);
 }
 
 int launch_fp4_decode(const LayerArgs& L, const void* q, const void* k_pool, const void* v_pool,

@@ -119,7 +119,9 @@ def test_workspace_and_constants(lib):
     for layer, n in ((_layer(), 64), (_layer(n_q_heads=32, n_kv_heads=4, head_dim=512), 7), (_layer(n_q_heads=22, n_kv_heads=2), 0)):
         G = layer.n_q_heads // layer.n_kv_heads
         units = n * layer.n_kv_heads * -(-G // 8)
-        assert binding.fp4_workspace_bytes(layer, n) == 2048 + (160 * 13 + units) * ((min(G, 8) + 1) // 2 * 2) * (4 * layer.head_dim + 8)
+        rows = (min(G, 8) + 1) // 2 * 2
+        jobs = layer.head_dim // 256 * (rows // 2)
+        assert binding.fp4_workspace_bytes(layer, n) == 8192 + (160 * 13 + units) * rows * (4 * layer.head_dim + 8 * jobs)
     assert binding.fp4_page_bytes(_layer()) == 2304
 
 
