@@ -440,7 +440,7 @@ PSW_API int psw_fp4_workspace_bytes(const psw_layer_t *layer, int32_t n_seqs, si
  *   out  device bf16 [n_seqs][n_q_heads][head_dim] (it feeds the next projection)
  *   ws   device workspace, 16-byte aligned, of psw_fp4_workspace_bytes
  * A page whose block id is outside the pool reads as zero rows and is flagged.
- * n_seqs * (max_blocks_per_seq + 4) * n_kv_heads * ceil(n_q_heads / n_kv_heads / 8) and
+ * n_seqs * (max_blocks_per_seq + 8) * n_kv_heads * ceil(n_q_heads / n_kv_heads / 8) and
  * the bytes of a block, n_kv_heads * PSW_FP4_PAGE_BYTES, must stay below 2^31
  * (PSW_ECAPACITY). */
 PSW_API int attn_decode_paged_fp4(const psw_layer_t *layer, const void *q, const void *k_pool4,

@@ -133,7 +133,7 @@ int attn_decode_paged_fp4(const psw_layer_t* layer, const void* q, const void* k
   if (rc != PSW_OK) return rc;
   if (!tensor_scale_ok(k_scale) || !tensor_scale_ok(v_scale)) return PSW_EINVAL_SCALE;
   if (!aligned(ws, 16) || !aligned(lse, 4)) return PSW_EALIGN;
-  if (!countable(pages, n_seqs, static_cast<int64_t>(L.n_kv) * L.qchunks(), kFp4UnitCost) ||
+  if (!countable(pages, n_seqs, static_cast<int64_t>(L.n_kv) * L.qchunks(), fp4_unit_cost(L.hd)) ||
       static_cast<int64_t>(L.n_kv) * PSW_FP4_PAGE_BYTES(L.hd) > INT32_MAX)
     return PSW_ECAPACITY;
   if (n_seqs == 0) return PSW_OK;

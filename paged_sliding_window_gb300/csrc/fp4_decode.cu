@@ -7,7 +7,7 @@
 // page serves as both (k_eq_v).
 //
 //  * Unit = (sequence, KV head, up to 8 query heads). The visible pages of all
-//    units form one list, in which a unit's beginning counts as kUnitCost pages; every warp of a persistent grid (one CTA per SM) is a
+//    units form one list, in which every unit has kUnitCost more entries; every warp of a persistent grid (one CTA per SM) is a
 //    worker of its own with an equal run of it: its own ring of pages in shared
 //    memory, filled by plain bulk copies (a page of a head is one run of bytes),
 //    its own running maximum, sum and output. No warp waits for another.
@@ -32,6 +32,8 @@
 //    that other CTAs have pages of, two at most, go on to the workspace, and the warp
 //    that adds a unit's last pages (a ticket counts them) joins the CTAs' parts, in
 //    their order.
+#include <type_traits>
+
 #include "fp4.cuh"
 #include "latent.cuh"
 
@@ -43,7 +45,6 @@ using fp4::Page;
 constexpr int kMaxCtas = 160;  // one per SM; what they need of workspace is counted with it
 constexpr int kMaxWarps = 12;
 constexpr int kMaxJobs = 8;    // parts of a unit's output that are joined apart, at most
-constexpr int kUnitCost = kFp4UnitCost;  // what beginning and ending a unit takes, in pages
 constexpr int kRuns = 256;     // runs of sequences whose entries are summed
 
 template <int HD, bool KEQV>
@@ -63,7 +64,7 @@ struct Cfg {
   static_assert(kStages * kTileBytes == kRingBytes && kStages >= 2 && kStages <= 8, "ring");
   static_assert(HD * 8 * 4 <= kRingBytes, "a piece's output fits where the ring was");
   static_assert(HD * 8 * 4 + 2 * kWarps * 8 * 4 <= kRingBytes, "and its weights");
-  static_assert(kMaxCtas * kMaxJobs * 4 <= PSW_FP4_COUNTER_BYTES && kParts * 4 <= kMaxJobs, "tickets");
+  static_assert(kMaxCtas * kMaxJobs * 4 <= PSW_FP4_COUNTER_BYTES && kMaxJobs == 8, "tickets");
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -146,21 +147,22 @@ struct Args {
 struct Seq {
   int len, p0, np, lo;
 };
-__device__ __forceinline__ Seq seq_of(const Args& a, int b) {
-  int len = __ldg(a.seq_lens + b);
-  const int cap = a.max_blocks * kBlockSize;
-  len = len < 0 ? 0 : (len > cap ? cap : len);
+__device__ __forceinline__ Seq seq_of_len(const Args& a, int len) {
   const int lo = a.window > 0 && len > a.window ? len - a.window : 0;
   const fp4::SeqPages s = fp4::seq_pages(len, lo);
   return Seq{len, s.p0, s.np, lo};
+}
+__device__ __forceinline__ Seq seq_of(const Args& a, int b) {
+  const int len = __ldg(a.seq_lens + b), cap = a.max_blocks * kBlockSize;
+  return seq_of_len(a, len < 0 ? 0 : (len > cap ? cap : len));
 }
 
 // A unit of the list: sequence, unit of it, the list's index of its beginning.
 struct Place {
   int b, j, tile0;
   Seq s;
-  __device__ void next(const Args& a, int ups) {
-    tile0 += s.np + kUnitCost;
+  __device__ void next(const Args& a, int ups, int cost) {
+    tile0 += s.np + cost;
     if (++j < ups) return;
     j = 0;
     do {
@@ -170,13 +172,20 @@ struct Place {
 };
 
 // The unit after a warp's `at`, which it becomes.
-__device__ __forceinline__ Place next_place(Place* at, const Args& a, int ups) {
+__device__ __forceinline__ Place next_place(Place* at, const Args& a, int ups, int cost) {
   Place p = *at;
-  p.next(a, ups);
+  p.next(a, ups, cost);
   __syncwarp();
   if ((threadIdx.x & 31) == 0) *at = p;
   __syncwarp();
   return p;
+}
+
+// Adds to a ticket: what this thread's warp has written before is seen by whoever sees the sum.
+__device__ __forceinline__ int add_acq_rel(int32_t* p, int v) {
+  int old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
 }
 
 // A unit's first query head, and how many it has.
@@ -233,25 +242,26 @@ struct Cut {
   }
 };
 
-// The CTAs (of K workers) that have pages of a unit: the first of them and how many.
+// The CTAs (of W workers) that have pages of a unit: the first of them and how many.
 struct Ctas {
   int first, n;
 };
-template <int K>
-__device__ __forceinline__ Ctas ctas_of(const Cut& cut, const Piece& p) {
-  const int first = cut.worker(p.tile0 + kUnitCost) / K;
-  return Ctas{first, cut.worker(p.tile0 + kUnitCost + p.np - 1) / K - first + 1};
+template <int W>
+__device__ __forceinline__ Ctas ctas_of(const Cut& cut, const Piece& p, int cost) {
+  const int first = cut.worker(p.tile0 + cost) / W;
+  return Ctas{first, cut.worker(p.tile0 + cost + p.np - 1) / W - first + 1};
 }
 
 template <int HD, bool KEQV>
 __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(const Args a) {
   using C = Cfg<HD, KEQV>;
   constexpr int W = C::kWarps, S = C::kStages, TP = C::kTile;
+  constexpr int kUnitCost = fp4_unit_cost(HD);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t s_full[W][S];
   __shared__ Piece s_piece[2 * W];
   __shared__ float2 s_ml[2 * W][kQHeadsPerUnit];
-  __shared__ int s_run[kRuns + 1];
+  __shared__ int s_run[kRuns + 1], s_len[kRuns];  // s_len: where a run is one sequence
   __shared__ int s_sum[kRuns / 32];
   // a warp's unit that is worked on, and that of the next page to fetch: wanted at a unit's
   // ends alone, and no registers are to spare between them
@@ -268,8 +278,9 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
   int incl = 0;
   if (tid < kRuns) {
     for (int b = tid * per; b < min(a.n_seqs, (tid + 1) * per); ++b) {
-      const int np = seq_of(a, b).np;
-      if (np > 0) incl += np + kUnitCost;
+      const Seq s = seq_of(a, b);
+      if (s.np > 0) incl += s.np + kUnitCost;
+      s_len[tid] = s.len;
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -301,15 +312,13 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
     const int begin = cut.begin(me);
     left = cut.begin(me + 1) - begin;
     const int x = begin / ups;  // units of a sequence are equal: find its sequence by entries
-    int lo = 0, hi = kRuns;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_run[mid] <= x) lo = mid; else hi = mid;
-    }
+    int lo = 31 - __clz(__ballot_sync(0xffffffffu, s_run[lane * (kRuns / 32)] <= x));
+    lo = lo * (kRuns / 32);
+    lo += 31 - __clz(__ballot_sync(0xffffffffu, lane < kRuns / 32 && s_run[lo + lane] <= x));
     Place c;
     c.b = lo * per;
     int off = s_run[lo];
-    c.s = seq_of(a, c.b);
+    c.s = per == 1 ? seq_of_len(a, s_len[c.b]) : seq_of(a, c.b);
     while (c.s.np == 0 || x >= off + c.s.np + kUnitCost) {
       if (c.s.np > 0) off += c.s.np + kUnitCost;
       c.s = seq_of(a, ++c.b);
@@ -351,7 +360,7 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
       if (f_page == f_np) {
         left -= kUnitCost;
         if (left <= 0) return;
-        const Place f = next_place(&s_next[warp], a, ups);
+        const Place f = next_place(&s_next[warp], a, ups, kUnitCost);
         f_np = f.s.np;
         f_page = 0;
         fetch_unit();
@@ -727,7 +736,7 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
           put(a.ws_o + static_cast<int64_t>(me) * (C::kParts * 128 * hp));
           note(2 * warp);
         }
-        np = next_place(&s_now[warp], a, ups).s.np;
+        np = next_place(&s_now[warp], a, ups, kUnitCost).s.np;
         page = 0;
         load_q();
         begin_piece();
@@ -747,9 +756,9 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
   }
   __syncthreads();
 
-  // ---- joining: the pieces of a unit are neighbours. A warp takes 128 float4 of what the CTA
-  // has of a unit at a time and needs no other warp for the rest of the way: it writes the
-  // result, or this CTA's part and, if its part is the last to come, the result of all parts.
+  // ---- joining: the pieces of a unit are neighbours. A warp takes a part of what the CTA has of a
+  // unit at a time (32 PER float4) and needs no other warp for the rest of the way: it writes
+  // the result, or this CTA's part and, if its part is the last to come, the result of all.
   const Piece mine = s_piece[min(lane, 2 * W - 1)];
   const bool valid = lane < 2 * W && mine.pages > 0;
   const uint32_t have = __ballot_sync(0xffffffffu, valid);
@@ -759,133 +768,145 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
     const int other = __shfl_sync(0xffffffffu, mine.tile0, prev != 0 ? 31 - __clz(prev) : 0);
     start = __ballot_sync(0xffffffffu, valid && (prev == 0 || other != mine.tile0));
   }
-  const int jobs = C::kParts * hp, units = jobs * 128;  // of a unit; its float4s
+  const int units = C::kParts * 128 * hp;  // float4s of a unit
   const int64_t part0 = static_cast<int64_t>(gridDim.x) * W;  // slots of the CTAs' parts
   float* weight = reinterpret_cast<float*>(ring + HD * 8 * 4);  // [piece][head], of this warp
   const int h = lane & 7, sub = lane >> 3;
-  for (int y = warp; y < __popc(start) * jobs; y += W) {
-    const int gi = y / jobs, job = y - gi * jobs, x0 = job * 128 + lane;
-    uint32_t from = start;
-    for (int k = 0; k < gi; ++k) from &= from - 1;
-    const int first = __ffs(from) - 1;
-    from &= from - 1;  // the starts behind it
-    const uint32_t members =
-        have & ~((1u << first) - 1u) & (from != 0 ? (from & -from) - 1u : ~0u);
-    const int pages = __reduce_add_sync(0xffffffffu, (members >> lane) & 1 ? mine.pages : 0);
-    Piece p;
-    p.b = __shfl_sync(0xffffffffu, mine.b, first);
-    p.j = __shfl_sync(0xffffffffu, mine.j, first);
-    p.tile0 = __shfl_sync(0xffffffffu, mine.tile0, first);
-    p.np = __shfl_sync(0xffffffffu, mine.np, first);
-    const int nh = heads_of(a, p.j);
-    // (a first piece can only be the last of a unit: the run that it begins goes on elsewhere)
-    const int last = 31 - __clz(members);
-    const int w0 = first >> 1, w1 = (last - 1) >> 1;  // its last pieces
-    float4 o[4];
-    int head[4];
+  auto join = [&](auto per) {
+    constexpr int PER = decltype(per)::value;
+    const int jobs = units / (32 * PER);
+    for (int y = warp; y < __popc(start) * jobs; y += W) {
+      const int gi = y / jobs, job = y - gi * jobs, x0 = job * 32 * PER + lane;
+      uint32_t from = start;
+      for (int k = 0; k < gi; ++k) from &= from - 1;
+      const int first = __ffs(from) - 1;
+      from &= from - 1;  // the starts behind it
+      const uint32_t members =
+          have & ~((1u << first) - 1u) & (from != 0 ? (from & -from) - 1u : ~0u);
+      // (a first piece can only be the last of a unit: the run that it begins goes on elsewhere)
+      const int last = 31 - __clz(members);
+      float4 o[PER];
+      int head[PER];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      head[k] = piece_unit(x0 + 32 * k, hp).head;
-      o[k] = (last & 1) ? make_float4(0.f, 0.f, 0.f, 0.f)
-                        : __ldcg(a.ws_o + (static_cast<int64_t>(blockIdx.x) * W + (last >> 1)) * units +
-                                 x0 + 32 * k);
-    }
-    // M = max m_i, weights 2^(m_i - M), their sum of l; a lane has every fourth piece of head h
-    float M = -INFINITY, L = 0.f;
-    for (int i = sub; i < 2 * W; i += 4)
-      if ((members >> i) & 1) M = fmaxf(M, s_ml[i][h].x);
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
-    __syncwarp();
-    for (int i = sub; i < 2 * W; i += 4) {
-      if (!((members >> i) & 1)) continue;
-      const float2 ml = s_ml[i][h];
-      const float w = ex2_approx(ml.x - M);
-      weight[i * 8 + h] = w;
-      L += w * ml.y;
-    }
-    L += __shfl_xor_sync(0xffffffffu, L, 8);
-    L += __shfl_xor_sync(0xffffffffu, L, 16);
-    __syncwarp();
-    auto add = [](float4& s, const float4& v, float w) {
-      s.x += v.x * w;
-      s.y += v.y * w;
-      s.z += v.z * w;
-      s.w += v.w * w;
-    };
+      for (int k = 0; k < PER; ++k) {
+        head[k] = piece_unit(x0 + 32 * k, hp).head;
+        o[k] = (last & 1) ? make_float4(0.f, 0.f, 0.f, 0.f)
+                          : __ldcg(a.ws_o + (static_cast<int64_t>(blockIdx.x) * W + (last >> 1)) * units +
+                                   x0 + 32 * k);
+      }
+      const int pages = __reduce_add_sync(0xffffffffu, (members >> lane) & 1 ? mine.pages : 0);
+      Piece p;
+      p.b = __shfl_sync(0xffffffffu, mine.b, first);
+      p.j = __shfl_sync(0xffffffffu, mine.j, first);
+      p.tile0 = __shfl_sync(0xffffffffu, mine.tile0, first);
+      p.np = __shfl_sync(0xffffffffu, mine.np, first);
+      const int nh = heads_of(a, p.j);
+      const int w0 = first >> 1, w1 = (last - 1) >> 1;  // its last pieces
+      // M = max m_i, weights 2^(m_i - M), their sum of l; a lane has every fourth piece of head h
+      float M = -INFINITY, L = 0.f;
+      for (int i = sub; i < 2 * W; i += 4)
+        if ((members >> i) & 1) M = fmaxf(M, s_ml[i][h].x);
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+      __syncwarp();
+      for (int i = sub; i < 2 * W; i += 4) {
+        if (!((members >> i) & 1)) continue;
+        const float2 ml = s_ml[i][h];
+        const float w = ex2_approx(ml.x - M);
+        weight[i * 8 + h] = w;
+        L += w * ml.y;
+      }
+      L += __shfl_xor_sync(0xffffffffu, L, 8);
+      L += __shfl_xor_sync(0xffffffffu, L, 16);
+      __syncwarp();
+      auto add = [](float4& s, const float4& v, float w) {
+        s.x += v.x * w;
+        s.y += v.y * w;
+        s.z += v.z * w;
+        s.w += v.w * w;
+      };
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float w = (last & 1) ? 0.f : weight[last * 8 + head[k]];
-      o[k] = make_float4(o[k].x * w, o[k].y * w, o[k].z * w, o[k].w * w);
-    }
-    for (int i = w0; i <= w1; ++i) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        add(o[k], reinterpret_cast<const float4*>(smem + i * C::kRingBytes)[x0 + 32 * k],
-            weight[(2 * i + 1) * 8 + head[k]]);
-    }
-    if (pages == p.np) {
-      const float inv = 1.f / L;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        write_out<HD>(a, p, nh, piece_unit(x0 + 32 * k, hp), o[k],
-                      __shfl_sync(0xffffffffu, inv, head[k]));
-      if (job == 0 && lane < nh) write_lse(a, p, lane, M, L);
-      continue;
-    }
-    // a unit that other CTAs have pages of: this CTA's first or last
-    const Ctas cs = ctas_of<W>(cut, p);
-    const int64_t slot0 = part0 + cs.first + p.b * ups + p.j;  // of the first CTA's part
-    const int64_t slot = slot0 + static_cast<int>(blockIdx.x) - cs.first;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) a.ws_o[slot * units + x0 + 32 * k] = o[k];
-    if (lane < a.rows) a.ws_ml[(slot * jobs + job) * a.rows + lane] = make_float2(M, L);
-    __syncwarp();
-    int done = 0;
-    if (lane == 0) {
-      int32_t* ticket = a.tickets + cs.first * kMaxJobs + job;
-      __threadfence();
-      done = atomicAdd(ticket, pages) + pages == p.np;
-      if (done) *ticket = 0;
-    }
-    if (__shfl_sync(0xffffffffu, done, 0) == 0) continue;
-    __threadfence();
-    // one pass over the parts with the running maximum and sum of every lane's four
-    const float4* src = a.ws_o + slot0 * units + x0;
-    const float2* ml = a.ws_ml + (slot0 * jobs + job) * a.rows;
-    float top[4], sum[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      top[k] = -INFINITY;
-      sum[k] = 0.f;
-      o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+      for (int k = 0; k < PER; ++k) {
+        const float w = (last & 1) ? 0.f : weight[last * 8 + head[k]];
+        o[k] = make_float4(o[k].x * w, o[k].y * w, o[k].z * w, o[k].w * w);
+      }
 #pragma unroll 2
-    for (int i = 0; i < cs.n; ++i) {
-      float4 v[4];
-      float2 x[4];
+      for (int i = w0; i <= w1; ++i) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[k] = __ldcg(src + static_cast<int64_t>(i) * units + 32 * k);
-        x[k] = __ldcg(ml + static_cast<int64_t>(i) * jobs * a.rows + head[k]);
+        for (int k = 0; k < PER; ++k)
+          add(o[k], reinterpret_cast<const float4*>(smem + i * C::kRingBytes)[x0 + 32 * k],
+              weight[(2 * i + 1) * 8 + head[k]]);
+      }
+      if (pages == p.np) {
+        const float inv = 1.f / L;
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+          write_out<HD>(a, p, nh, piece_unit(x0 + 32 * k, hp), o[k],
+                        __shfl_sync(0xffffffffu, inv, head[k]));
+        if (job == 0 && lane < nh) write_lse(a, p, lane, M, L);
+        continue;
+      }
+      // a unit that other CTAs have pages of: this CTA's first or last
+      const Ctas cs = ctas_of<W>(cut, p, kUnitCost);
+      const int64_t slot0 = part0 + cs.first + p.b * ups + p.j;  // of the first CTA's part
+      const int64_t slot = slot0 + static_cast<int>(blockIdx.x) - cs.first;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) a.ws_o[slot * units + x0 + 32 * k] = o[k];
+      if (lane < a.rows) a.ws_ml[(slot * jobs + job) * a.rows + lane] = make_float2(M, L);
+      __syncwarp();
+      int done = 0;
+      if (lane == 0) {
+        int32_t* ticket = a.tickets + cs.first * kMaxJobs + job;
+        done = add_acq_rel(ticket, pages) + pages == p.np;
+        if (done) *ticket = 0;
+      }
+      if (__shfl_sync(0xffffffffu, done, 0) == 0) continue;
+      __syncwarp();
+      // one pass over the parts with the running maximum and sum of every lane's float4s
+      const float4* src = a.ws_o + slot0 * units + x0;
+      const float2* ml = a.ws_ml + (slot0 * jobs + job) * a.rows;
+      float top[PER], sum[PER];
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        top[k] = -INFINITY;
+        sum[k] = 0.f;
+        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll(8 / PER)
+      for (int i = 0; i < cs.n; ++i) {
+        float4 v[PER];
+        float2 x[PER];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+          v[k] = __ldcg(src + static_cast<int64_t>(i) * units + 32 * k);
+          x[k] = __ldcg(ml + static_cast<int64_t>(i) * jobs * a.rows + head[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+          const float mn = fmaxf(top[k], x[k].x);
+          const float f0 = top[k] == mn ? 1.f : ex2_approx(top[k] - mn);
+          const float f1 = ex2_approx(x[k].x - mn);
+          top[k] = mn;
+          sum[k] = sum[k] * f0 + x[k].y * f1;
+          o[k] = make_float4(o[k].x * f0, o[k].y * f0, o[k].z * f0, o[k].w * f0);
+          add(o[k], v[k], f1);
+        }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float mn = fmaxf(top[k], x[k].x);
-        const float f0 = top[k] == mn ? 1.f : ex2_approx(top[k] - mn);
-        const float f1 = ex2_approx(x[k].x - mn);
-        top[k] = mn;
-        sum[k] = sum[k] * f0 + x[k].y * f1;
-        o[k] = make_float4(o[k].x * f0, o[k].y * f0, o[k].z * f0, o[k].w * f0);
-        add(o[k], v[k], f1);
+      for (int k = 0; k < PER; ++k) {
+        const Unit4 u = piece_unit(x0 + 32 * k, hp);
+        write_out<HD>(a, p, nh, u, o[k], 1.f / sum[k]);
+        if (u.d == 0 && u.head < nh) write_lse(a, p, u.head, top[k], sum[k]);
       }
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const Unit4 u = piece_unit(x0 + 32 * k, hp);
-      write_out<HD>(a, p, nh, u, o[k], 1.f / sum[k]);
-      if (u.d == 0 && u.head < nh) write_lse(a, p, u.head, top[k], sum[k]);
-    }
+  };
+  // (at most kMaxJobs parts)
+  if (units <= 256) {
+    join(std::integral_constant<int, 1>{});
+  } else if (HD == 256 || units <= 512) {
+    join(std::integral_constant<int, 2>{});
+  } else {
+    join(std::integral_constant<int, 4>{});
   }
   // ---- sequences without keys, and lengths that are wrong
   for (int b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
@@ -926,8 +947,7 @@ size_t slots_of(const LayerArgs& L, int n_seqs) {
 }  // namespace
 
 size_t fp4_decode_workspace(const LayerArgs& L, int n_seqs) {
-  const size_t jobs = static_cast<size_t>(L.hd) / 256 * (slot_rows(L) / 2);
-  return kFp4CounterBytes + slots_of(L, n_seqs) * slot_rows(L) * (L.hd * 4 + jobs * 8);
+  return kFp4CounterBytes + slots_of(L, n_seqs) * slot_rows(L) * (L.hd * 4 + kMaxJobs * 8);
 }
 
 int launch_fp4_decode(const LayerArgs& L, const void* q, const void* k_pool, const void* v_pool,

@@ -215,7 +215,9 @@ int launch_latent_prefill(const LatentArgs& L, const void* q, const int32_t* cu_
 // Decode workspace: join tickets (one int32 per CTA; zero between calls), then slots of
 // partial results.
 constexpr size_t kFp4CounterBytes = PSW_FP4_COUNTER_BYTES;
-constexpr int kFp4UnitCost = 2;  // entries that a unit has in the decode's list beside its pages
+// Entries that a unit has in the decode's list beside its pages: what beginning, ending and
+// joining it takes.
+constexpr int fp4_unit_cost(int head_dim) { return head_dim == 256 ? 3 : 6; }
 
 int launch_block_table_extend(int32_t* block_table, int max_blocks, const int32_t* past_lens,
                               const int32_t* new_lens, int n_seqs, const int32_t* free_ids,
