@@ -685,17 +685,27 @@ def attn_prefill_latent(layer, q, cu_q, past_lens, max_q_len: int, kv, k_rope, c
 _LAYER_STRUCTS: dict = {}
 
 
-def _layer_struct(layer) -> PswLayer:
-    """make_layer's struct, one for all layers of the same fields (never handed out)."""
-    key = (int(layer.n_q_heads), int(layer.n_kv_heads), int(layer.head_dim), int(layer.window),
-           float(layer.softcap), float(layer.scale), int(bool(layer.k_eq_v)),
-           int(getattr(layer, "block_size", 16)))
+def _layer_struct(layer):
+    """make_layer's struct and a reference to it, one for all layers of the same fields (never
+    handed out)."""
+    key = (layer.n_q_heads, layer.n_kv_heads, layer.head_dim, layer.window, layer.softcap,
+           layer.scale, layer.k_eq_v, getattr(layer, "block_size", 16))
     got = _LAYER_STRUCTS.get(key)
     if got is None:
         if len(_LAYER_STRUCTS) >= 1024:
             _LAYER_STRUCTS.clear()
-        got = _LAYER_STRUCTS[key] = PswLayer(*key)
+        z = make_layer(layer)
+        got = _LAYER_STRUCTS[key] = (z, ctypes.byref(z))
     return got
+
+
+def _stream_here(device, stream):
+    """_stream_of for tensors that exist, so that CUDA is up."""
+    if device != torch._C._cuda_getDevice():
+        return _stream_of(device, stream)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream
 
 
 def fp4_page_bytes(layer) -> int:
@@ -711,7 +721,7 @@ def alloc_fp4_pool(layer, num_blocks: int, device="cuda") -> torch.Tensor:
 
 def fp4_workspace_bytes(layer, n_seqs: int) -> int:
     out = ctypes.c_size_t(0)
-    _raise(load().psw_fp4_workspace_bytes(ctypes.byref(_layer_struct(layer)), int(n_seqs),
+    _raise(load().psw_fp4_workspace_bytes(_layer_struct(layer)[1], int(n_seqs),
                                           ctypes.byref(out)), "psw_fp4_workspace_bytes")
     return int(out.value)
 
@@ -760,7 +770,7 @@ def block_table_extend(block_table, past_lens, new_lens, free_ids, free_pos, fre
                                    past_lens.data_ptr(), new_lens.data_ptr(), n,
                                    free_ids.data_ptr() or None, free_ids.shape[0],
                                    free_pos.data_ptr(), free_next.data_ptr(), cu_new.data_ptr(),
-                                   seq_lens.data_ptr(), *slot_args, _stream_of(dev, stream))
+                                   seq_lens.data_ptr(), *slot_args, _stream_here(dev, stream))
     if rc:
         _raise(rc, "block_table_extend")
 
@@ -769,7 +779,7 @@ def kv_cache_write_fp4(layer, k, v, cu_new, past_lens, pages: PswPages, k_pool4,
                        k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
     """kv_cache_write into 4-bit pools (alloc_fp4_pool): k, v bf16 [n_new, n_kv, head_dim], v and
     v_pool4 None with k_eq_v; k_scale and v_scale are the pools' own, the same in every call."""
-    z = _layer_struct(layer)
+    z, z_ref = _layer_struct(layer)
     dev, n, rows = k.get_device(), past_lens.shape[0], k.shape[0]
     shape, pool = (rows, z.n_kv_heads, z.head_dim), (pages.num_blocks, z.n_kv_heads,
                                                      9 * z.head_dim)
@@ -784,11 +794,11 @@ def kv_cache_write_fp4(layer, k, v, cu_new, past_lens, pages: PswPages, k_pool4,
     _want_rows(pages, n, dev)
     if n == 0 or rows == 0:
         return
-    rc = load().kv_cache_write_fp4(ctypes.byref(z), k.data_ptr(),
+    rc = load().kv_cache_write_fp4(z_ref, k.data_ptr(),
                                    None if v is None else v.data_ptr(), cu_new.data_ptr(),
                                    past_lens.data_ptr(), n, rows, ctypes.byref(pages),
                                    k_pool4.data_ptr(), None if v is None else v_pool4.data_ptr(),
-                                   k_scale, v_scale, _stream_of(dev, stream))
+                                   k_scale, v_scale, _stream_here(dev, stream))
     if rc:
         _raise(rc, "kv_cache_write_fp4")
 
@@ -799,7 +809,7 @@ def kv_cache_read_fp4(layer, k_pool4, v_pool4, pages: PswPages, first, seq_lens,
     """Rows of 4-bit pages into bf16 pages: positions first[b] (int32 [n], or None: 0) to
     seq_lens[b] of every sequence, from pages into the pools of out_pages (for the attention of a
     chunk, attn_prefill_chunked)."""
-    z = _layer_struct(layer)
+    z, z_ref = _layer_struct(layer)
     dev, n = k_pool4.get_device(), seq_lens.shape[0]
     pool = (pages.num_blocks, z.n_kv_heads, 9 * z.head_dim)
     wide = (out_pages.num_blocks, 16, z.n_kv_heads, z.head_dim)
@@ -816,12 +826,12 @@ def kv_cache_read_fp4(layer, k_pool4, v_pool4, pages: PswPages, first, seq_lens,
     _want_rows(out_pages, n, dev)
     if n == 0:
         return
-    rc = load().kv_cache_read_fp4(ctypes.byref(z), k_pool4.data_ptr(),
+    rc = load().kv_cache_read_fp4(z_ref, k_pool4.data_ptr(),
                                   None if v_pool is None else v_pool4.data_ptr(),
                                   ctypes.byref(pages), None if first is None else first.data_ptr(),
                                   seq_lens.data_ptr(), n, ctypes.byref(out_pages),
                                   k_pool.data_ptr(), None if v_pool is None else v_pool.data_ptr(),
-                                  k_scale, v_scale, _stream_of(dev, stream))
+                                  k_scale, v_scale, _stream_here(dev, stream))
     if rc:
         _raise(rc, "kv_cache_read_fp4")
 
@@ -831,7 +841,7 @@ def attn_decode_paged_fp4(layer, q, k_pool4, v_pool4, pages: PswPages, seq_lens,
                           stream=None) -> None:
     """attn_decode_paged over 4-bit pools; out is bf16 [n, n_q, head_dim], ws from
     alloc_fp4_workspace (calls that may overlap on the GPU need one each)."""
-    z = _layer_struct(layer)
+    z, z_ref = _layer_struct(layer)
     dev, n = q.get_device(), seq_lens.shape[0]
     rows, pool = (n, z.n_q_heads, z.head_dim), (pages.num_blocks, z.n_kv_heads, 9 * z.head_dim)
     _want_v(z, (v_pool4, "v_pool4"))
@@ -851,11 +861,11 @@ def attn_decode_paged_fp4(layer, q, k_pool4, v_pool4, pages: PswPages, seq_lens,
     _want_rows(pages, n, dev)
     if n == 0:
         return
-    rc = load().attn_decode_paged_fp4(ctypes.byref(z), q.data_ptr(), k_pool4.data_ptr(),
+    rc = load().attn_decode_paged_fp4(z_ref, q.data_ptr(), k_pool4.data_ptr(),
                                       None if v_pool4 is None else v_pool4.data_ptr(),
                                       ctypes.byref(pages), seq_lens.data_ptr(), n, out.data_ptr(),
                                       None if lse is None else lse.data_ptr(), ws_ptr, ws_bytes,
-                                      k_scale, v_scale, _stream_of(dev, stream))
+                                      k_scale, v_scale, _stream_here(dev, stream))
     if rc:
         _raise(rc, "attn_decode_paged_fp4")
 

@@ -900,10 +900,9 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
       }
     }
   };
-  // (at most kMaxJobs parts)
+  // (2: more warps share few heads' units; 4: fewer rounds where there are many, and kMaxJobs
+  // parts at most. 64 sequences of 64 pages, G 2: 35.8 us with 2, 38.2 with 1, 36.2 with 4)
   if (units <= 256) {
-    join(std::integral_constant<int, 1>{});
-  } else if (HD == 256 || units <= 512) {
     join(std::integral_constant<int, 2>{});
   } else {
     join(std::integral_constant<int, 4>{});
