@@ -38,7 +38,6 @@ fp4_write_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
   const int row0 = static_cast<int>(item - static_cast<int64_t>(t) * groups) * kRows;
   if (t >= n_new_total) return;
   const int total = __ldg(cu_new + n_seqs);
-  if (t == 0 && row0 == 0 && lane == 0 && total > n_new_total) flag_error(err, PSW_DEVERR_LENGTH);
   const int rows = v_pool != nullptr ? 2 * n_kv : n_kv;
   uint4 in[kRows][kVec];
 #pragma unroll
@@ -53,13 +52,28 @@ fp4_write_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
       for (int e = 0; e < kVec; ++e) in[i][e] = __ldg(src + e);
     }
   }
+  // the token's sequence; up to 31 of them are looked at together with their past lengths
+  int b = 0, start = 0, past = 0;
+  bool found;
+  if (n_seqs <= 31) {
+    const int c = lane <= n_seqs ? __ldg(cu_new + lane) : 0;
+    const int p = lane < n_seqs ? __ldg(past_lens + lane) : 0;
+    const unsigned at = __ballot_sync(0xffffffffu, lane < n_seqs && c <= t);
+    b = 31 - __clz(at);
+    found = at != 0 && t < __shfl_sync(0xffffffffu, c, (b + 1) & 31);
+    start = __shfl_sync(0xffffffffu, c, b & 31);
+    past = __shfl_sync(0xffffffffu, p, b & 31);
+  } else {
+    found = lat::owner_of(cu_new, n_seqs, t, lane, b, start);
+    if (found) past = __ldg(past_lens + b);
+  }
+  if (t == 0 && row0 == 0 && lane == 0 && total > n_new_total) flag_error(err, PSW_DEVERR_LENGTH);
   if (t >= total) return;
-  int b, start;
-  if (!lat::owner_of(cu_new, n_seqs, t, lane, b, start)) {
+  if (!found) {
     if (lane == 0) flag_error(err, PSW_DEVERR_LENGTH);
     return;
   }
-  const int64_t pos = static_cast<int64_t>(__ldg(past_lens + b)) + (t - start);
+  const int64_t pos = static_cast<int64_t>(past) + (t - start);
   const int64_t page = pos / kBlockSize;
   if (pos < 0 || page >= max_blocks) {
     if (lane == 0) flag_error(err, pos < 0 ? PSW_DEVERR_LENGTH : PSW_DEVERR_CAPACITY);
@@ -141,21 +155,37 @@ namespace {
 
 constexpr int kReadThreads = 256;
 
-// The pages wanted of all sequences form one list; with every (KV head, tensor)
-// of a page they are the items, of which each warp of a persistent grid takes
-// an equal run. A lane turns one block of 16 values (8 bytes and a scale) of a
-// token into 32 bytes, so that a warp's store is whole rows: two tokens at HD
-// 256, one at HD 512.
+// 32 bytes to a 16-byte aligned address; in one store where `wide` says that it is a
+// multiple of 32 (two stores of 16 bytes each touch every sector twice: 8 contexts of 512 to
+// 8704 tokens took 82.8 us with them).
+__device__ __forceinline__ void store32(uint8_t* p, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(p + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// The pages wanted of all sequences form one list; with every (KV head, tensor) of a page,
+// and at HD 512 every half of its tokens, they are the items, of which each warp of a
+// persistent grid takes an equal run. A lane turns one block of 16 values (8 bytes and a
+// scale) of a token into 32 bytes, so that a warp's store is whole rows: two tokens at HD 256,
+// one at HD 512.
 template <int HD>
-__global__ void __launch_bounds__(kReadThreads)
+__global__ void __launch_bounds__(kReadThreads, 4)
 fp4_read_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ v_pool,
                 const int32_t* __restrict__ table, int max_blocks, int64_t num_blocks,
                 const int32_t* __restrict__ first, const int32_t* __restrict__ seq_lens,
                 int n_seqs, const int32_t* __restrict__ out_table, int out_max_blocks,
                 int64_t out_num_blocks, int n_kv, float k_scale, float v_scale,
-                uint8_t* __restrict__ k_out, uint8_t* __restrict__ v_out, int32_t* err) {
+                bool wide, uint8_t* __restrict__ k_out, uint8_t* __restrict__ v_out,
+                int32_t* err) {
   constexpr int kTok = 512 / HD;               // tokens per warp store
-  constexpr int kSteps = kBlockSize / kTok;
+  constexpr int kSteps = 8;                    // stores of an item
+  constexpr int kHalves = kBlockSize / (kTok * kSteps);
   constexpr int kLanes = HD / 16;              // lanes of a token
   __shared__ int s_run[kReadThreads + 1];
   __shared__ int s_warp[kReadThreads / 32];
@@ -190,7 +220,7 @@ fp4_read_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ 
   s_run[tid + 1] = before + incl;
   if (tid == 0) s_run[0] = 0;
   __syncthreads();
-  const int rows = v_out != nullptr ? 2 * n_kv : n_kv;
+  const int rows = (v_out != nullptr ? 2 * n_kv : n_kv) * kHalves;  // items of a page
   const int64_t items = static_cast<int64_t>(s_run[kReadThreads]) * rows;
   const int64_t workers = static_cast<int64_t>(gridDim.x) * (kReadThreads / 32);
   const int64_t me = static_cast<int64_t>(blockIdx.x) * (kReadThreads / 32) + warp;
@@ -224,8 +254,9 @@ fp4_read_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ 
       looked_up = true;
     }
     if (dst >= 0 && dst < out_num_blocks) {
-      const bool is_v = row >= n_kv;
-      const int head = is_v ? row - n_kv : row;
+      const int r0 = kHalves == 1 ? 0 : (row & 1) * (kBlockSize / 2);
+      const bool is_v = row / kHalves >= n_kv;
+      const int head = is_v ? row / kHalves - n_kv : row / kHalves;
       const bool have = src >= 0 && src < num_blocks;
       const uint8_t* in = (is_v ? v_pool : k_pool) +
                           (static_cast<int64_t>(have ? src : 0) * n_kv + head) * Page<HD>::kBytes;
@@ -236,7 +267,7 @@ fp4_read_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ 
       uint32_t s8[kSteps];
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const int r = i * kTok + tok;
+        const int r = r0 + i * kTok + tok;
         c[i] = __ldg(reinterpret_cast<const uint2*>(in + Page<HD>::unit(r, blk16 >> 1) +
                                                     (blk16 & 1) * 8));
         s8[i] = __ldg(in + Page<HD>::scale(r, blk16));
@@ -244,8 +275,8 @@ fp4_read_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ 
       const int pos0 = (s.p0 + page - off) * kBlockSize;
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const int r = i * kTok + tok;
-        const float f = have ? fp4::e4m3_float(s8[i]) : 0.f;
+        const int r = r0 + i * kTok + tok;
+        const float f = have ? fp4::e4m3_float(s8[i]) * gs : 0.f;
         uint32_t w[8];
         const uint32_t cw[2] = {have ? c[i].x : 0u, have ? c[i].y : 0u};
 #pragma unroll
@@ -254,15 +285,13 @@ fp4_read_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ 
                                  fp4::codes_f16<2>(cw[h]), fp4::codes_f16<3>(cw[h])};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 x = fp4::f16x2_to_float2(p[j]);  // (code * scale is exact)
-            w[4 * h + j] = pack_bf16x2(x.x * f * gs, x.y * f * gs);
+            const float2 x = fp4::f16x2_to_float2(p[j]);
+            w[4 * h + j] = pack_bf16x2(x.x * f, x.y * f);
           }
         }
         const int pos = pos0 + r;
         if (pos >= s.lo && pos < s.len) {
-          uint8_t* o = out + static_cast<int64_t>(r) * n_kv * (HD * 2);
-          *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(o + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+          store32(out + static_cast<int64_t>(r) * n_kv * (HD * 2), w, wide);
         }
       }
     }
@@ -285,11 +314,13 @@ int launch_fp4_read(const LayerArgs& L, const void* k_pool, const void* v_pool,
                     int n_seqs, const psw_pages_t& out_pages, void* k_out, void* v_out,
                     float k_scale, float v_scale, int num_sms, int32_t* err,
                     cudaStream_t stream) {
+  const bool wide =
+      ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0;
   auto* fn = L.hd == 256 ? fp4_read_kernel<256> : fp4_read_kernel<512>;
   fn<<<num_sms * 4, kReadThreads, 0, stream>>>(
       static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), pages.block_table,
       pages.max_blocks_per_seq, pages.num_blocks, first, seq_lens, n_seqs, out_pages.block_table,
-      out_pages.max_blocks_per_seq, out_pages.num_blocks, L.n_kv, k_scale, v_scale,
+      out_pages.max_blocks_per_seq, out_pages.num_blocks, L.n_kv, k_scale, v_scale, wide,
       static_cast<uint8_t*>(k_out), static_cast<uint8_t*>(v_out), err);
   return cudaGetLastError() == cudaSuccess ? PSW_OK : PSW_ELAUNCH;
 }
