@@ -804,12 +804,12 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
       const int w0 = first >> 1, w1 = (last - 1) >> 1;  // its last pieces
       // M = max m_i, weights 2^(m_i - M), their sum of l; a lane has every fourth piece of head h
       float M = -INFINITY, L = 0.f;
-      for (int i = sub; i < 2 * W; i += 4)
+      for (int i = first + sub; i <= last; i += 4)
         if ((members >> i) & 1) M = fmaxf(M, s_ml[i][h].x);
       M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
       M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
       __syncwarp();
-      for (int i = sub; i < 2 * W; i += 4) {
+      for (int i = first + sub; i <= last; i += 4) {
         if (!((members >> i) & 1)) continue;
         const float2 ml = s_ml[i][h];
         const float w = ex2_approx(ml.x - M);
@@ -837,59 +837,56 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
           add(o[k], reinterpret_cast<const float4*>(smem + i * C::kRingBytes)[x0 + 32 * k],
               weight[(2 * i + 1) * 8 + head[k]]);
       }
-      if (pages == p.np) {
-        const float inv = 1.f / L;
-#pragma unroll
-        for (int k = 0; k < PER; ++k)
-          write_out<HD>(a, p, nh, piece_unit(x0 + 32 * k, hp), o[k],
-                        __shfl_sync(0xffffffffu, inv, head[k]));
-        if (job == 0 && lane < nh) write_lse(a, p, lane, M, L);
-        continue;
-      }
-      // a unit that other CTAs have pages of: this CTA's first or last
-      const Ctas cs = ctas_of<W>(cut, p, kUnitCost);
-      const int64_t slot0 = part0 + cs.first + p.b * ups + p.j;  // of the first CTA's part
-      const int64_t slot = slot0 + static_cast<int>(blockIdx.x) - cs.first;
-#pragma unroll
-      for (int k = 0; k < PER; ++k) a.ws_o[slot * units + x0 + 32 * k] = o[k];
-      if (lane < a.rows) a.ws_ml[(slot * jobs + job) * a.rows + lane] = make_float2(M, L);
-      __syncwarp();
-      int done = 0;
-      if (lane == 0) {
-        int32_t* ticket = a.tickets + cs.first * kMaxJobs + job;
-        done = add_acq_rel(ticket, pages) + pages == p.np;
-        if (done) *ticket = 0;
-      }
-      if (__shfl_sync(0xffffffffu, done, 0) == 0) continue;
-      __syncwarp();
-      // one pass over the parts with the running maximum and sum of every lane's float4s
-      const float4* src = a.ws_o + slot0 * units + x0;
-      const float2* ml = a.ws_ml + (slot0 * jobs + job) * a.rows;
       float top[PER], sum[PER];
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
-        top[k] = -INFINITY;
-        sum[k] = 0.f;
-        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        top[k] = __shfl_sync(0xffffffffu, M, head[k]);
+        sum[k] = __shfl_sync(0xffffffffu, L, head[k]);
       }
-#pragma unroll(8 / PER)
-      for (int i = 0; i < cs.n; ++i) {
-        float4 v[PER];
-        float2 x[PER];
+      if (pages != p.np) {  // other CTAs have pages of it: it is this CTA's first or last unit
+        const Ctas cs = ctas_of<W>(cut, p, kUnitCost);
+        const int64_t slot0 = part0 + cs.first + p.b * ups + p.j;  // of the first CTA's part
+        const int64_t slot = slot0 + static_cast<int>(blockIdx.x) - cs.first;
 #pragma unroll
-        for (int k = 0; k < PER; ++k) {
-          v[k] = __ldcg(src + static_cast<int64_t>(i) * units + 32 * k);
-          x[k] = __ldcg(ml + static_cast<int64_t>(i) * jobs * a.rows + head[k]);
+        for (int k = 0; k < PER; ++k) a.ws_o[slot * units + x0 + 32 * k] = o[k];
+        if (lane < a.rows) a.ws_ml[(slot * jobs + job) * a.rows + lane] = make_float2(M, L);
+        __syncwarp();
+        int done = 0;
+        if (lane == 0) {
+          int32_t* ticket = a.tickets + cs.first * kMaxJobs + job;
+          done = add_acq_rel(ticket, pages) + pages == p.np;
+          if (done) *ticket = 0;
         }
+        if (__shfl_sync(0xffffffffu, done, 0) == 0) continue;
+        __syncwarp();
+        // one pass over the parts with the running maximum and sum of every lane's float4s
+        const float4* src = a.ws_o + slot0 * units + x0;
+        const float2* ml = a.ws_ml + (slot0 * jobs + job) * a.rows;
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
-          const float mn = fmaxf(top[k], x[k].x);
-          const float f0 = top[k] == mn ? 1.f : ex2_approx(top[k] - mn);
-          const float f1 = ex2_approx(x[k].x - mn);
-          top[k] = mn;
-          sum[k] = sum[k] * f0 + x[k].y * f1;
-          o[k] = make_float4(o[k].x * f0, o[k].y * f0, o[k].z * f0, o[k].w * f0);
-          add(o[k], v[k], f1);
+          top[k] = -INFINITY;
+          sum[k] = 0.f;
+          o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll(8 / PER)
+        for (int i = 0; i < cs.n; ++i) {
+          float4 v[PER];
+          float2 x[PER];
+#pragma unroll
+          for (int k = 0; k < PER; ++k) {
+            v[k] = __ldcg(src + static_cast<int64_t>(i) * units + 32 * k);
+            x[k] = __ldcg(ml + static_cast<int64_t>(i) * jobs * a.rows + head[k]);
+          }
+#pragma unroll
+          for (int k = 0; k < PER; ++k) {
+            const float mn = fmaxf(top[k], x[k].x);
+            const float f0 = top[k] == mn ? 1.f : ex2_approx(top[k] - mn);
+            const float f1 = ex2_approx(x[k].x - mn);
+            top[k] = mn;
+            sum[k] = sum[k] * f0 + x[k].y * f1;
+            o[k] = make_float4(o[k].x * f0, o[k].y * f0, o[k].z * f0, o[k].w * f0);
+            add(o[k], v[k], f1);
+          }
         }
       }
 #pragma unroll
