@@ -22,7 +22,7 @@ SOURCES = ["api.cu", "kv_cache_write.cu", "decode.cu", "decode_noalloc.cu", "pre
            "norm_rope.cu", "latent_api.cu", "latent_cache.cu", "latent_decode.cu",
            "latent_expand.cu", "latent_prefill.cu", "fp4_api.cu", "fp4_cache.cu",
            "fp4_decode.cu", "block_tables.cu", "block_pool.cpp"]
-HEADERS = ["ptx.cuh", "latent.cuh", "fp4.cuh", "psw_internal.h"]
+HEADERS = ["ptx.cuh", "latent.cuh", "fp4.cuh", "fp4_decode.cuh", "psw_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -32,20 +32,12 @@
 //    that other CTAs have pages of, two at most, go on to the workspace, and the warp
 //    that adds a unit's last pages (a ticket counts them) joins the CTAs' parts, in
 //    their order.
-#include <type_traits>
-
-#include "fp4.cuh"
-#include "latent.cuh"
+#include "fp4_decode.cuh"
 
 namespace psw {
 namespace {
 
-using fp4::Page;
-
-constexpr int kMaxCtas = 160;  // one per SM; what they need of workspace is counted with it
-constexpr int kMaxWarps = 12;
-constexpr int kMaxJobs = 8;    // parts of a unit's output that are joined apart, at most
-constexpr int kRuns = 256;     // runs of sequences whose entries are summed
+using namespace fp4;
 
 template <int HD, bool KEQV>
 struct Cfg {
@@ -60,197 +52,12 @@ struct Cfg {
   static constexpr int kStages = kRingBytes / kTileBytes;
   static constexpr int kQBytes = HD == 256 ? 0 : HD * 8 * 2;  // per warp: q as operands (HD 512)
   static constexpr int kSmem = kWarps * (kRingBytes + kQBytes);
-  static_assert(kWarps <= kMaxWarps && 2 * kWarps <= 32, "pieces of a CTA");
+  static_assert(kWarps <= kMaxWorkers && 2 * kWarps <= 32, "pieces of a CTA");
   static_assert(kStages * kTileBytes == kRingBytes && kStages >= 2 && kStages <= 8, "ring");
   static_assert(HD * 8 * 4 <= kRingBytes, "a piece's output fits where the ring was");
   static_assert(HD * 8 * 4 + 2 * kWarps * 8 * 4 <= kRingBytes, "and its weights");
   static_assert(kMaxCtas * kMaxJobs * 4 <= PSW_FP4_COUNTER_BYTES && kMaxJobs == 8, "tickets");
 };
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                        uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t transposed(uint32_t a) {
-  uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-// i is a constant where this is used
-__device__ __forceinline__ uint32_t codes_at(uint32_t w, int i) {
-  return i == 0 ? fp4::codes_f16<0>(w)
-         : i == 1 ? fp4::codes_f16<1>(w)
-         : i == 2 ? fp4::codes_f16<2>(w)
-                  : fp4::codes_f16<3>(w);
-}
-// The bounded wait of a whole warp: the same for all its lanes.
-__device__ __forceinline__ bool landed(uint64_t* bar, uint32_t phase) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase))) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar, phase));
-}
-// A bulk copy that only lanes with `p` ask for.
-__device__ __forceinline__ void bulk_load_if(bool p, uint32_t dst, const void* src, uint32_t bytes,
-                                             uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
-      "[%3];\n\t}" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "r"(static_cast<uint32_t>(p))
-      : "memory");
-}
-__device__ __forceinline__ void expect_if(bool p, uint64_t* bar, uint32_t bytes) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t"
-      "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
-      "r"(bytes), "r"(static_cast<uint32_t>(p))
-      : "memory");
-}
-// bits of a where m has ones, of b elsewhere
-__device__ __forceinline__ uint32_t select_bits(uint32_t m, uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xCA;" : "=r"(d) : "r"(m), "r"(a), "r"(b));
-  return d;
-}
-
-struct Args {
-  const __nv_bfloat16* q;
-  const uint8_t *k_pool, *v_pool;
-  const int32_t *table, *seq_lens;
-  int max_blocks, num_blocks;
-  uint32_t page_stride;  // bytes of a block in a pool
-  int n_seqs, n_q, n_kv, group, qchunks, window;
-  float scale, softcap;  // scale: the layer's times K's tensor scale
-  float v_scale;
-  __nv_bfloat16* out;
-  float* lse;
-  float4* ws_o;      // [slot][half of a row's pairs ...], see piece_unit
-  float2* ws_ml;     // [slot][job][rows]
-  int32_t* tickets;  // [CTA][job]: pages joined of the unit that the CTA begins and does not end
-  int rows;          // rows of a slot: the group's heads, 8 at most, made even
-  int32_t* err;
-  int stall_cta, stall_tile;
-};
-
-struct Seq {
-  int len, p0, np, lo;
-};
-__device__ __forceinline__ Seq seq_of_len(const Args& a, int len) {
-  const int lo = a.window > 0 && len > a.window ? len - a.window : 0;
-  const fp4::SeqPages s = fp4::seq_pages(len, lo);
-  return Seq{len, s.p0, s.np, lo};
-}
-__device__ __forceinline__ Seq seq_of(const Args& a, int b) {
-  const int len = __ldg(a.seq_lens + b), cap = a.max_blocks * kBlockSize;
-  return seq_of_len(a, len < 0 ? 0 : (len > cap ? cap : len));
-}
-
-// A unit of the list: sequence, unit of it, the list's index of its beginning.
-struct Place {
-  int b, j, tile0;
-  Seq s;
-  __device__ void next(const Args& a, int ups, int cost) {
-    tile0 += s.np + cost;
-    if (++j < ups) return;
-    j = 0;
-    do {
-      s = seq_of(a, ++b);
-    } while (s.np == 0);  // (only called where the list goes on)
-  }
-};
-
-// The unit after a warp's `at`, which it becomes.
-__device__ __forceinline__ Place next_place(Place* at, const Args& a, int ups, int cost) {
-  Place p = *at;
-  p.next(a, ups, cost);
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) *at = p;
-  __syncwarp();
-  return p;
-}
-
-// Adds to a ticket: what this thread's warp has written before is seen by whoever sees the sum.
-__device__ __forceinline__ int add_acq_rel(int32_t* p, int v) {
-  int old;
-  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
-  return old;
-}
-
-// A unit's first query head, and how many it has.
-__device__ __forceinline__ int first_head(const Args& a, int j) {
-  return j / a.qchunks * a.group + j % a.qchunks * kQHeadsPerUnit;
-}
-__device__ __forceinline__ int heads_of(const Args& a, int j) {
-  return min(kQHeadsPerUnit, a.group - j % a.qchunks * kQHeadsPerUnit);
-}
-
-// What a piece is to the others: its unit and how many of the unit's pages it has.
-struct Piece {
-  int b, j, tile0, np, pages;
-};
-
-// ---- outputs of a piece: float4 number ((part * 2 + odd) * 8 + i) * 8 hp + g hp + t
-// holds values 256 part + 32 g + 4 i .. + 3 of head 2 t + odd (hp pairs of heads):
-// lane (g, t) of a warp holds 32 neighbouring values of two heads per part.
-struct Unit4 {
-  int head, d;
-};
-__device__ __forceinline__ Unit4 piece_unit(int x, int hp) {
-  const int t = x % hp, r = x / hp;
-  const int g = r & 7, i = (r >> 3) & 7, odd = (r >> 6) & 1, part = r >> 7;
-  return Unit4{2 * t + odd, 256 * part + 32 * g + 4 * i};
-}
-
-template <int HD>
-__device__ __forceinline__ void write_out(const Args& a, const Piece& p, int nh, const Unit4& u,
-                                          const float4& o, float inv) {
-  if (u.head >= nh) return;
-  __nv_bfloat16* dst =
-      a.out + (static_cast<int64_t>(p.b) * a.n_q + first_head(a, p.j) + u.head) * HD + u.d;
-  const float f = inv * a.v_scale;
-  *reinterpret_cast<uint2*>(dst) =
-      make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
-}
-__device__ __forceinline__ void write_lse(const Args& a, const Piece& p, int head, float m,
-                                          float l) {
-  if (a.lse != nullptr)
-    a.lse[static_cast<int64_t>(p.b) * a.n_q + first_head(a, p.j) + head] =
-        (m + log2f(l)) * lat::kLn2;
-}
-
-
-// The list of `tiles` entries cut into runs for `workers`: of each + 1 entries for the first
-// `more` of them, of `each` for the others.
-struct Cut {
-  int each, more;
-  __device__ int begin(int w) const { return w * each + min(w, more); }
-  __device__ int worker(int x) const {  // that has entry x
-    const int y = x - more * (each + 1);
-    return y < 0 ? x / (each + 1) : more + y / each;
-  }
-};
-
-// The CTAs (of W workers) that have pages of a unit: the first of them and how many.
-struct Ctas {
-  int first, n;
-};
-template <int W>
-__device__ __forceinline__ Ctas ctas_of(const Cut& cut, const Piece& p, int cost) {
-  const int first = cut.worker(p.tile0 + cost) / W;
-  return Ctas{first, cut.worker(p.tile0 + cost + p.np - 1) / W - first + 1};
-}
 
 template <int HD, bool KEQV>
 __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(const Args a) {
@@ -261,8 +68,7 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
   __shared__ uint64_t s_full[W][S];
   __shared__ Piece s_piece[2 * W];
   __shared__ float2 s_ml[2 * W][kQHeadsPerUnit];
-  __shared__ int s_run[kRuns + 1], s_len[kRuns];  // s_len: where a run is one sequence
-  __shared__ int s_sum[kRuns / 32];
+  __shared__ ListSmem s_list;
   // a warp's unit that is worked on, and that of the next page to fetch: wanted at a unit's
   // ends alone, and no registers are to spare between them
   __shared__ Place s_now[W], s_next[W];
@@ -271,69 +77,18 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
   uint8_t* ring = smem + warp * C::kRingBytes;
   const int ups = a.n_kv * a.qchunks, hp = a.rows / 2;
 
-  // ---- the list: entries of the sequences before each run of them
   if (lane < S) mbar_init(&s_full[warp][lane], 1);
   fence_mbar_init();
-  const int per = (a.n_seqs + kRuns - 1) / kRuns;
-  int incl = 0;
-  if (tid < kRuns) {
-    for (int b = tid * per; b < min(a.n_seqs, (tid + 1) * per); ++b) {
-      const Seq s = seq_of(a, b);
-      if (s.np > 0) incl += s.np + kUnitCost;
-      s_len[tid] = s.len;
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
-    if (lane == 31) s_sum[warp] = incl;
-  }
   if (tid < 2 * W) s_piece[tid].pages = 0;
-  __syncthreads();
-  int all = 0;
-#pragma unroll
-  for (int i = 0; i < kRuns / 32; ++i) {
-    if (i == warp) incl += all;
-    all += s_sum[i];
-  }
-  if (tid < kRuns) s_run[tid + 1] = incl;
-  if (tid == 0) s_run[0] = 0;
-  __syncthreads();
-  const int tiles = all * ups;
-  const int workers = max(1, min(static_cast<int>(gridDim.x) * W, tiles));
-  const Cut cut{tiles / workers, tiles % workers};
-  const int me = blockIdx.x * W + warp;
-
-  int page = 0;   // the next page of the unit that is worked on
-  int np = 0;     // its pages
-  int left = 0;   // entries of the run from the next page to fetch on
-  if (me < min(workers, tiles)) {
-    const int begin = cut.begin(me);
-    left = cut.begin(me + 1) - begin;
-    const int x = begin / ups;  // units of a sequence are equal: find its sequence by entries
-    int lo = 31 - __clz(__ballot_sync(0xffffffffu, s_run[lane * (kRuns / 32)] <= x));
-    lo = lo * (kRuns / 32);
-    lo += 31 - __clz(__ballot_sync(0xffffffffu, lane < kRuns / 32 && s_run[lo + lane] <= x));
-    Place c;
-    c.b = lo * per;
-    int off = s_run[lo];
-    c.s = per == 1 ? seq_of_len(a, s_len[c.b]) : seq_of(a, c.b);
-    while (c.s.np == 0 || x >= off + c.s.np + kUnitCost) {
-      if (c.s.np > 0) off += c.s.np + kUnitCost;
-      c.s = seq_of(a, ++c.b);
-    }
-    const int rem = begin - off * ups, entries = c.s.np + kUnitCost;
-    c.j = rem / entries;
-    const int at = rem - c.j * entries;
-    c.tile0 = begin - at;
-    page = max(0, at - kUnitCost);
-    left -= max(0, kUnitCost - at);
-    np = c.s.np;
-    if (lane == 0) s_now[warp] = s_next[warp] = c;
-    __syncwarp();
-  }
+  const Run run = begin_run<W>(a, s_list, warp, kUnitCost);
+  const int me = run.me;
+  int page = run.page;   // the next page of the unit that is worked on
+  int left = run.left;   // entries of the run from the next page to fetch on
+  int np = 0;            // pages of the unit
   if (left > 0) {
+    np = run.c.s.np;
+    if (lane == 0) s_now[warp] = s_next[warp] = run.c;
+    __syncwarp();
     // ---- fetching: a tile's blocks, a copy by each of the first lanes
     int f_page = page, f_np = np, ids_at = 0;
     int32_t ids = 0;     // lane i: block of page ids_at + i
@@ -756,166 +511,9 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
   }
   __syncthreads();
 
-  // ---- joining: the pieces of a unit are neighbours. A warp takes a part of what the CTA has of a
-  // unit at a time (32 PER float4) and needs no other warp for the rest of the way: it writes
-  // the result, or this CTA's part and, if its part is the last to come, the result of all.
-  const Piece mine = s_piece[min(lane, 2 * W - 1)];
-  const bool valid = lane < 2 * W && mine.pages > 0;
-  const uint32_t have = __ballot_sync(0xffffffffu, valid);
-  uint32_t start;  // the first piece of every unit
-  {
-    const uint32_t prev = have & ((1u << lane) - 1u);
-    const int other = __shfl_sync(0xffffffffu, mine.tile0, prev != 0 ? 31 - __clz(prev) : 0);
-    start = __ballot_sync(0xffffffffu, valid && (prev == 0 || other != mine.tile0));
-  }
-  const int units = C::kParts * 128 * hp;  // float4s of a unit
-  const int64_t part0 = static_cast<int64_t>(gridDim.x) * W;  // slots of the CTAs' parts
-  float* weight = reinterpret_cast<float*>(ring + HD * 8 * 4);  // [piece][head], of this warp
-  const int h = lane & 7, sub = lane >> 3;
-  auto join = [&](auto per) {
-    constexpr int PER = decltype(per)::value;
-    const int jobs = units / (32 * PER);
-    for (int y = warp; y < __popc(start) * jobs; y += W) {
-      const int gi = y / jobs, job = y - gi * jobs, x0 = job * 32 * PER + lane;
-      uint32_t from = start;
-      for (int k = 0; k < gi; ++k) from &= from - 1;
-      const int first = __ffs(from) - 1;
-      from &= from - 1;  // the starts behind it
-      const uint32_t members =
-          have & ~((1u << first) - 1u) & (from != 0 ? (from & -from) - 1u : ~0u);
-      // (a first piece can only be the last of a unit: the run that it begins goes on elsewhere)
-      const int last = 31 - __clz(members);
-      float4 o[PER];
-      int head[PER];
-#pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        head[k] = piece_unit(x0 + 32 * k, hp).head;
-        o[k] = (last & 1) ? make_float4(0.f, 0.f, 0.f, 0.f)
-                          : __ldcg(a.ws_o + (static_cast<int64_t>(blockIdx.x) * W + (last >> 1)) * units +
-                                   x0 + 32 * k);
-      }
-      const int pages = __reduce_add_sync(0xffffffffu, (members >> lane) & 1 ? mine.pages : 0);
-      Piece p;
-      p.b = __shfl_sync(0xffffffffu, mine.b, first);
-      p.j = __shfl_sync(0xffffffffu, mine.j, first);
-      p.tile0 = __shfl_sync(0xffffffffu, mine.tile0, first);
-      p.np = __shfl_sync(0xffffffffu, mine.np, first);
-      const int nh = heads_of(a, p.j);
-      const int w0 = first >> 1, w1 = (last - 1) >> 1;  // its last pieces
-      // M = max m_i, weights 2^(m_i - M), their sum of l; a lane has every fourth piece of head h
-      float M = -INFINITY, L = 0.f;
-      for (int i = first + sub; i <= last; i += 4)
-        if ((members >> i) & 1) M = fmaxf(M, s_ml[i][h].x);
-      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
-      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
-      __syncwarp();
-      for (int i = first + sub; i <= last; i += 4) {
-        if (!((members >> i) & 1)) continue;
-        const float2 ml = s_ml[i][h];
-        const float w = ex2_approx(ml.x - M);
-        weight[i * 8 + h] = w;
-        L += w * ml.y;
-      }
-      L += __shfl_xor_sync(0xffffffffu, L, 8);
-      L += __shfl_xor_sync(0xffffffffu, L, 16);
-      __syncwarp();
-      auto add = [](float4& s, const float4& v, float w) {
-        s.x += v.x * w;
-        s.y += v.y * w;
-        s.z += v.z * w;
-        s.w += v.w * w;
-      };
-#pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        const float w = (last & 1) ? 0.f : weight[last * 8 + head[k]];
-        o[k] = make_float4(o[k].x * w, o[k].y * w, o[k].z * w, o[k].w * w);
-      }
-#pragma unroll 2
-      for (int i = w0; i <= w1; ++i) {
-#pragma unroll
-        for (int k = 0; k < PER; ++k)
-          add(o[k], reinterpret_cast<const float4*>(smem + i * C::kRingBytes)[x0 + 32 * k],
-              weight[(2 * i + 1) * 8 + head[k]]);
-      }
-      float top[PER], sum[PER];
-#pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        top[k] = __shfl_sync(0xffffffffu, M, head[k]);
-        sum[k] = __shfl_sync(0xffffffffu, L, head[k]);
-      }
-      if (pages != p.np) {  // other CTAs have pages of it: it is this CTA's first or last unit
-        const Ctas cs = ctas_of<W>(cut, p, kUnitCost);
-        const int64_t slot0 = part0 + cs.first + p.b * ups + p.j;  // of the first CTA's part
-        const int64_t slot = slot0 + static_cast<int>(blockIdx.x) - cs.first;
-#pragma unroll
-        for (int k = 0; k < PER; ++k) a.ws_o[slot * units + x0 + 32 * k] = o[k];
-        if (lane < a.rows) a.ws_ml[(slot * jobs + job) * a.rows + lane] = make_float2(M, L);
-        __syncwarp();
-        int done = 0;
-        if (lane == 0) {
-          int32_t* ticket = a.tickets + cs.first * kMaxJobs + job;
-          done = add_acq_rel(ticket, pages) + pages == p.np;
-          if (done) *ticket = 0;
-        }
-        if (__shfl_sync(0xffffffffu, done, 0) == 0) continue;
-        __syncwarp();
-        // one pass over the parts with the running maximum and sum of every lane's float4s
-        const float4* src = a.ws_o + slot0 * units + x0;
-        const float2* ml = a.ws_ml + (slot0 * jobs + job) * a.rows;
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-          top[k] = -INFINITY;
-          sum[k] = 0.f;
-          o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll(8 / PER)
-        for (int i = 0; i < cs.n; ++i) {
-          float4 v[PER];
-          float2 x[PER];
-#pragma unroll
-          for (int k = 0; k < PER; ++k) {
-            v[k] = __ldcg(src + static_cast<int64_t>(i) * units + 32 * k);
-            x[k] = __ldcg(ml + static_cast<int64_t>(i) * jobs * a.rows + head[k]);
-          }
-#pragma unroll
-          for (int k = 0; k < PER; ++k) {
-            const float mn = fmaxf(top[k], x[k].x);
-            const float f0 = top[k] == mn ? 1.f : ex2_approx(top[k] - mn);
-            const float f1 = ex2_approx(x[k].x - mn);
-            top[k] = mn;
-            sum[k] = sum[k] * f0 + x[k].y * f1;
-            o[k] = make_float4(o[k].x * f0, o[k].y * f0, o[k].z * f0, o[k].w * f0);
-            add(o[k], v[k], f1);
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        const Unit4 u = piece_unit(x0 + 32 * k, hp);
-        write_out<HD>(a, p, nh, u, o[k], 1.f / sum[k]);
-        if (u.d == 0 && u.head < nh) write_lse(a, p, u.head, top[k], sum[k]);
-      }
-    }
-  };
-  // (2: more warps share few heads' units; 4: fewer rounds where there are many, and kMaxJobs
-  // parts at most. 64 sequences of 64 pages, G 2: 35.8 us with 2, 38.2 with 1, 36.2 with 4)
-  if (units <= 256) {
-    join(std::integral_constant<int, 2>{});
-  } else {
-    join(std::integral_constant<int, 4>{});
-  }
-  // ---- sequences without keys, and lengths that are wrong
-  for (int b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
-    const int len = __ldg(a.seq_lens + b);
-    if (tid == 0 && (len < 0 || len > a.max_blocks * kBlockSize))
-      flag_error(a.err, len < 0 ? PSW_DEVERR_LENGTH : PSW_DEVERR_CAPACITY);
-    if (len > 0) continue;
-    uint4* dst = reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(b) * a.n_q * HD);
-    for (int i = tid; i < a.n_q * (HD / 8); i += C::kThreads) dst[i] = make_uint4(0, 0, 0, 0);
-    if (a.lse != nullptr)
-      for (int i = tid; i < a.n_q; i += C::kThreads)
-        a.lse[static_cast<int64_t>(b) * a.n_q + i] = -INFINITY;
-  }
+  join_pieces<HD, W, W, C::kRingBytes>(a, run.cut, kUnitCost, s_piece, s_ml, smem,
+                                       reinterpret_cast<float*>(ring + HD * 8 * 4));
+  finish_empty<HD>(a);
 }
 
 template <int HD, bool KEQV>
@@ -937,7 +535,7 @@ int slot_rows(const LayerArgs& L) {
 // Slots of a call: one for every worker's first piece, then those of the CTAs' parts of
 // units (CTA + unit: the units of neighbouring CTAs are neighbours, so no two share one).
 size_t slots_of(const LayerArgs& L, int n_seqs) {
-  return kMaxCtas * (kMaxWarps + 1) + static_cast<size_t>(n_seqs) * L.n_kv * L.qchunks();
+  return kMaxCtas * (kMaxWorkers + 1) + static_cast<size_t>(n_seqs) * L.n_kv * L.qchunks();
 }
 
 }  // namespace
