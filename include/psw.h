@@ -432,7 +432,7 @@ PSW_API int kv_cache_read_fp4(const psw_layer_t *layer, const void *k_pool4, con
  * flagged PSW_DEVERR_PIPELINE: zero them then). Calls of any layer may share one
  * in turn; calls that could overlap on the GPU need one each, and no other call
  * of this library takes it. */
-#define PSW_FP4_COUNTER_BYTES 8192
+#define PSW_FP4_COUNTER_BYTES 16384
 PSW_API int psw_fp4_workspace_bytes(const psw_layer_t *layer, int32_t n_seqs, size_t *bytes);
 
 /* attn_decode_paged over 4-bit pools: arguments, masks and errors as

@@ -734,7 +734,7 @@ def alloc_fp4_workspace(layer, n_seqs: int, device="cuda") -> torch.Tensor:
     return ws
 
 
-FP4_COUNTER_BYTES = 8192  # PSW_FP4_COUNTER_BYTES
+FP4_COUNTER_BYTES = 16384  # PSW_FP4_COUNTER_BYTES
 
 
 def _want_v(z, *vs):

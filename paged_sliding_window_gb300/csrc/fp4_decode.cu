@@ -56,7 +56,7 @@ struct Cfg {
   static_assert(kStages * kTileBytes == kRingBytes && kStages >= 2 && kStages <= 8, "ring");
   static_assert(HD * 8 * 4 <= kRingBytes, "a piece's output fits where the ring was");
   static_assert(HD * 8 * 4 + 2 * kWarps * 8 * 4 <= kRingBytes, "and its weights");
-  static_assert(kMaxCtas * kMaxJobs * 4 <= PSW_FP4_COUNTER_BYTES && kMaxJobs == 8, "tickets");
+  static_assert(3 * kMaxCtas * kMaxJobs * 4 <= PSW_FP4_COUNTER_BYTES && kMaxJobs == 8, "tickets");
 };
 
 template <int HD, bool KEQV>

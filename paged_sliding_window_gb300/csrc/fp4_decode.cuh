@@ -25,6 +25,7 @@ namespace fp4 {
 constexpr int kMaxCtas = 160;  // one per SM; what they need of workspace is counted with it
 constexpr int kMaxWorkers = 12;  // of a CTA
 constexpr int kMaxJobs = 8;    // parts of a unit's output that are joined apart, at most
+constexpr int kGroup = 8;      // CTAs whose parts of a unit are joined first, where there are many
 constexpr int kRuns = 256;     // runs of sequences whose entries are summed
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -98,7 +99,9 @@ struct Args {
   float* lse;
   float4* ws_o;      // [slot][half of a row's pairs ...], see piece_unit
   float2* ws_ml;     // [slot][job][rows]
-  int32_t* tickets;  // [CTA][job]: pages joined of the unit that the CTA begins and does not end
+  // [3][CTA][job]: pages joined of the unit that the CTA begins and does not end; of its first
+  // group of CTAs; of the later group that begins with the CTA
+  int32_t* tickets;
   int rows;          // rows of a slot: the group's heads, 8 at most, made even
   int32_t* err;
   int stall_cta, stall_tile;
@@ -254,7 +257,9 @@ __device__ __forceinline__ Run begin_run(const Args& a, ListSmem& s, int worker,
   if (tid == 0) s.run[0] = 0;
   __syncthreads();
   const int tiles = all * ups;
-  const int workers = max(1, min(static_cast<int>(gridDim.x) * W, tiles));
+  // (two tiles each at least: a worker more is a piece more to join. One sequence of 40000 with
+  // one KV head takes 17.4 us, with a tile each 18.9, with 3 or 4 one or two more)
+  const int workers = max(1, min(static_cast<int>(gridDim.x) * W, tiles / 2));
   Run r;
   r.cut = Cut{tiles / workers, tiles % workers};
   r.me = blockIdx.x * W + worker;
@@ -381,50 +386,80 @@ __device__ __forceinline__ void join_pieces(const Args& a, const Cut& cut, int c
         sum[k] = __shfl_sync(0xffffffffu, L, head[k]);
       }
       if (pages != p.np) {  // other CTAs have pages of it: it is this CTA's first or last unit
+        // Where many CTAs have, kGroup neighbours' parts are joined into one first (in the place
+        // of the group's first), and the groups' then: one sequence of 40000
+        // with one KV head: 17.4 us, 44.5 with all its parts in a row.
         const Ctas cs = ctas_of<W>(cut, p, cost);
         const int64_t slot0 = part0 + cs.first + p.b * ups + p.j;  // of the first CTA's part
-        const int64_t slot = slot0 + static_cast<int>(blockIdx.x) - cs.first;
+        const int at = static_cast<int>(blockIdx.x) - cs.first;
+        // the parts from the `from`th on, n of them `step` apart: one pass with the running
+        // maximum and sum of every lane's float4s
+        auto add_parts = [&](int from, int step, int n) {
+          const float4* src = a.ws_o + (slot0 + from) * units + x0;
+          const float2* ml = a.ws_ml + ((slot0 + from) * jobs + job) * a.rows;
+          const int so = step * units, sm = step * jobs * a.rows;
+#pragma unroll
+          for (int k = 0; k < PER; ++k) {
+            top[k] = -INFINITY;
+            sum[k] = 0.f;
+            o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+#pragma unroll(8 / PER)
+          for (int i = 0; i < n; ++i) {
+            float4 v[PER];
+            float2 x[PER];
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+              v[k] = __ldcg(src + static_cast<int64_t>(i) * so + 32 * k);
+              x[k] = __ldcg(ml + static_cast<int64_t>(i) * sm + head[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+              const float mn = fmaxf(top[k], x[k].x);
+              const float f0 = top[k] == mn ? 1.f : ex2_approx(top[k] - mn);
+              const float f1 = ex2_approx(x[k].x - mn);
+              top[k] = mn;
+              sum[k] = sum[k] * f0 + x[k].y * f1;
+              o[k] = make_float4(o[k].x * f0, o[k].y * f0, o[k].z * f0, o[k].w * f0);
+              add(o[k], v[k], f1);
+            }
+          }
+        };
+        // adds what is ready to a ticket: whether that was the last of `want`
+        auto last_of = [&](int32_t* ticket, int ready, int want) {
+          __syncwarp();
+          int done = 0;
+          if (lane == 0) {
+            done = add_acq_rel(ticket, ready) + ready == want;
+            if (done) *ticket = 0;
+          }
+          done = __shfl_sync(0xffffffffu, done, 0);
+          __syncwarp();
+          return done != 0;
+        };
+        const int64_t slot = slot0 + at;
 #pragma unroll
         for (int k = 0; k < PER; ++k) a.ws_o[slot * units + x0 + 32 * k] = o[k];
         if (lane < a.rows) a.ws_ml[(slot * jobs + job) * a.rows + lane] = make_float2(M, L);
-        __syncwarp();
-        int done = 0;
-        if (lane == 0) {
-          int32_t* ticket = a.tickets + cs.first * kMaxJobs + job;
-          done = add_acq_rel(ticket, pages) + pages == p.np;
-          if (done) *ticket = 0;
-        }
-        if (__shfl_sync(0xffffffffu, done, 0) == 0) continue;
-        __syncwarp();
-        // one pass over the parts with the running maximum and sum of every lane's float4s
-        const float4* src = a.ws_o + slot0 * units + x0;
-        const float2* ml = a.ws_ml + (slot0 * jobs + job) * a.rows;
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-          top[k] = -INFINITY;
-          sum[k] = 0.f;
-          o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll(8 / PER)
-        for (int i = 0; i < cs.n; ++i) {
-          float4 v[PER];
-          float2 x[PER];
+        int32_t* ticket = a.tickets + cs.first * kMaxJobs + job;
+        int ready = pages, step = 1, n = cs.n;
+        if (n > 2 * kGroup) {
+          const int from = at & ~(kGroup - 1), c0 = cs.first + from, m = min(kGroup, n - from);
+          const int begin = p.tile0 + cost;
+          ready = min(begin + p.np, cut.begin((c0 + m) * W)) - max(begin, cut.begin(c0 * W));
+          int32_t* first = ticket + ((from == 0 ? 1 : 2) * kMaxCtas + from) * kMaxJobs;
+          if (!last_of(first, pages, ready)) continue;
+          add_parts(from, 1, m);
 #pragma unroll
           for (int k = 0; k < PER; ++k) {
-            v[k] = __ldcg(src + static_cast<int64_t>(i) * units + 32 * k);
-            x[k] = __ldcg(ml + static_cast<int64_t>(i) * jobs * a.rows + head[k]);
+            a.ws_o[(slot0 + from) * units + x0 + 32 * k] = o[k];
+            a.ws_ml[((slot0 + from) * jobs + job) * a.rows + head[k]] = make_float2(top[k], sum[k]);
           }
-#pragma unroll
-          for (int k = 0; k < PER; ++k) {
-            const float mn = fmaxf(top[k], x[k].x);
-            const float f0 = top[k] == mn ? 1.f : ex2_approx(top[k] - mn);
-            const float f1 = ex2_approx(x[k].x - mn);
-            top[k] = mn;
-            sum[k] = sum[k] * f0 + x[k].y * f1;
-            o[k] = make_float4(o[k].x * f0, o[k].y * f0, o[k].z * f0, o[k].w * f0);
-            add(o[k], v[k], f1);
-          }
+          step = kGroup;
+          n = (n + kGroup - 1) / kGroup;
         }
+        if (!last_of(ticket, ready, p.np)) continue;
+        add_parts(0, step, n);
       }
 #pragma unroll
       for (int k = 0; k < PER; ++k) {

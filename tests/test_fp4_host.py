@@ -120,7 +120,7 @@ def test_workspace_and_constants(lib):
         G = layer.n_q_heads // layer.n_kv_heads
         units = n * layer.n_kv_heads * -(-G // 8)
         rows = (min(G, 8) + 1) // 2 * 2
-        assert binding.fp4_workspace_bytes(layer, n) == 8192 + (160 * 13 + units) * rows * (4 * layer.head_dim + 8 * 8)
+        assert binding.fp4_workspace_bytes(layer, n) == 16384 + (160 * 13 + units) * rows * (4 * layer.head_dim + 8 * 8)
     assert binding.fp4_page_bytes(_layer()) == 2304
 
 

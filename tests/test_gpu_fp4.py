@@ -256,6 +256,26 @@ def test_decode_batches(layer, lens):
     compare(layer, cache, q, lens, got)
 
 
+@pytest.mark.parametrize("layer,lens", [
+    pytest.param(Layer(3, 1, 256, scale=0.05), [40000], id="256"),
+    pytest.param(Layer(8, 1, 256, window=30000), [9, 33000, 40], id="256-window"),
+    pytest.param(Layer(16, 1, 256, softcap=20.0), [12001, 30011], id="256-two-chunks"),
+    pytest.param(Layer(2, 1, 512, scale=0.04), [33333], id="512"),
+    pytest.param(Layer(16, 2, 512, k_eq_v=True, scale=0.04), [20000, 0, 31000], id="512-keqv"),
+])
+def test_decode_units_of_many_parts(layer, lens):
+    """Contexts that dozens of thread blocks share: their parts are joined in two steps."""
+    cache, q = filled(layer, lens, 29)
+    ws = binding.alloc_fp4_workspace(layer, len(lens))
+    got = decode(layer, cache, q, lens, ws=ws)
+    no_error()
+    compare(layer, cache, q, lens, got)
+    for _ in range(5):
+        again = decode(layer, cache, q, lens, ws=ws)
+        assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+    assert bool((ws[:binding.FP4_COUNTER_BYTES] == 0).all())
+
+
 @pytest.mark.parametrize("gs", [(0.37, 2.5), (2.0 ** -20, 2.0 ** 20)])
 @pytest.mark.parametrize("layer", [L256, L512], ids=["256", "512"])
 def test_decode_tensor_scales(layer, gs):
