@@ -91,6 +91,8 @@ def lib_path() -> str:
 def load(build_if_missing: bool = True) -> ctypes.CDLL:
     """Loads libpsw.so (building it first if asked and missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -686,8 +688,8 @@ _LAYER_STRUCTS: dict = {}
 
 
 def _layer_struct(layer):
-    """make_layer's struct and a reference to it, one for all layers of the same fields (never
-    handed out)."""
+    """(reference to make_layer's struct, n_q_heads, n_kv_heads, head_dim, k_eq_v), one for all
+    layers of the same fields (never handed out)."""
     key = (layer.n_q_heads, layer.n_kv_heads, layer.head_dim, layer.window, layer.softcap,
            layer.scale, layer.k_eq_v, getattr(layer, "block_size", 16))
     got = _LAYER_STRUCTS.get(key)
@@ -695,7 +697,8 @@ def _layer_struct(layer):
         if len(_LAYER_STRUCTS) >= 1024:
             _LAYER_STRUCTS.clear()
         z = make_layer(layer)
-        got = _LAYER_STRUCTS[key] = (z, ctypes.byref(z))
+        got = _LAYER_STRUCTS[key] = (ctypes.byref(z), z.n_q_heads, z.n_kv_heads, z.head_dim,
+                                     bool(z.k_eq_v))
     return got
 
 
@@ -721,7 +724,7 @@ def alloc_fp4_pool(layer, num_blocks: int, device="cuda") -> torch.Tensor:
 
 def fp4_workspace_bytes(layer, n_seqs: int) -> int:
     out = ctypes.c_size_t(0)
-    _raise(load().psw_fp4_workspace_bytes(_layer_struct(layer)[1], int(n_seqs),
+    _raise(load().psw_fp4_workspace_bytes(_layer_struct(layer)[0], int(n_seqs),
                                           ctypes.byref(out)), "psw_fp4_workspace_bytes")
     return int(out.value)
 
@@ -737,10 +740,9 @@ def alloc_fp4_workspace(layer, n_seqs: int, device="cuda") -> torch.Tensor:
 FP4_COUNTER_BYTES = 16384  # PSW_FP4_COUNTER_BYTES
 
 
-def _want_v(z, *vs):
-    for v, name in vs:
-        if (v is None) != bool(z.k_eq_v):
-            raise PswError(-7, f"{name} (k_eq_v is {bool(z.k_eq_v)})")
+def _want_v(v, k_eq_v, name):
+    if (v is None) != k_eq_v:
+        raise PswError(-7, f"{name} (k_eq_v is {k_eq_v})")
 
 
 def block_table_extend(block_table, past_lens, new_lens, free_ids, free_pos, free_next, cu_new,
@@ -779,11 +781,11 @@ def kv_cache_write_fp4(layer, k, v, cu_new, past_lens, pages: PswPages, k_pool4,
                        k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
     """kv_cache_write into 4-bit pools (alloc_fp4_pool): k, v bf16 [n_new, n_kv, head_dim], v and
     v_pool4 None with k_eq_v; k_scale and v_scale are the pools' own, the same in every call."""
-    z, z_ref = _layer_struct(layer)
+    z_ref, n_q, n_kv, hd, k_eq_v = _layer_struct(layer)
     dev, n, rows = k.get_device(), past_lens.shape[0], k.shape[0]
-    shape, pool = (rows, z.n_kv_heads, z.head_dim), (pages.num_blocks, z.n_kv_heads,
-                                                     9 * z.head_dim)
-    _want_v(z, (v, "v"), (v_pool4, "v_pool4"))
+    shape, pool = (rows, n_kv, hd), (pages.num_blocks, n_kv, 9 * hd)
+    _want_v(v, k_eq_v, "v")
+    _want_v(v_pool4, k_eq_v, "v_pool4")
     _want(k, _BF16, shape, "k", dev)
     _want(cu_new, _I32, (n + 1,), "cu_new", dev)
     _want(past_lens, _I32, (n,), "past_lens", dev)
@@ -809,11 +811,11 @@ def kv_cache_read_fp4(layer, k_pool4, v_pool4, pages: PswPages, first, seq_lens,
     """Rows of 4-bit pages into bf16 pages: positions first[b] (int32 [n], or None: 0) to
     seq_lens[b] of every sequence, from pages into the pools of out_pages (for the attention of a
     chunk, attn_prefill_chunked)."""
-    z, z_ref = _layer_struct(layer)
+    z_ref, n_q, n_kv, hd, k_eq_v = _layer_struct(layer)
     dev, n = k_pool4.get_device(), seq_lens.shape[0]
-    pool = (pages.num_blocks, z.n_kv_heads, 9 * z.head_dim)
-    wide = (out_pages.num_blocks, 16, z.n_kv_heads, z.head_dim)
-    _want_v(z, (v_pool4, "v_pool4"), (v_pool, "v_pool"))
+    pool, wide = (pages.num_blocks, n_kv, 9 * hd), (out_pages.num_blocks, 16, n_kv, hd)
+    _want_v(v_pool4, k_eq_v, "v_pool4")
+    _want_v(v_pool, k_eq_v, "v_pool")
     _want(k_pool4, _U8, pool, "k_pool4", dev)
     _want(k_pool, _BF16, wide, "k_pool", dev)
     _want(seq_lens, _I32, (n,), "seq_lens", dev)
@@ -841,10 +843,10 @@ def attn_decode_paged_fp4(layer, q, k_pool4, v_pool4, pages: PswPages, seq_lens,
                           stream=None) -> None:
     """attn_decode_paged over 4-bit pools; out is bf16 [n, n_q, head_dim], ws from
     alloc_fp4_workspace (calls that may overlap on the GPU need one each)."""
-    z, z_ref = _layer_struct(layer)
+    z_ref, n_q, n_kv, hd, k_eq_v = _layer_struct(layer)
     dev, n = q.get_device(), seq_lens.shape[0]
-    rows, pool = (n, z.n_q_heads, z.head_dim), (pages.num_blocks, z.n_kv_heads, 9 * z.head_dim)
-    _want_v(z, (v_pool4, "v_pool4"))
+    rows, pool = (n, n_q, hd), (pages.num_blocks, n_kv, 9 * hd)
+    _want_v(v_pool4, k_eq_v, "v_pool4")
     _want(q, _BF16, rows, "q", dev)
     _want(k_pool4, _U8, pool, "k_pool4", dev)
     if v_pool4 is not None:
@@ -852,12 +854,12 @@ def attn_decode_paged_fp4(layer, q, k_pool4, v_pool4, pages: PswPages, seq_lens,
     _want(seq_lens, _I32, (n,), "seq_lens", dev)
     _want(out, _BF16, rows, "out", dev)
     if lse is not None:
-        _want(lse, _F32, (n, z.n_q_heads), "lse", dev)
+        _want(lse, _F32, (n, n_q), "lse", dev)
     ws_ptr, ws_bytes = None, 0
     if ws is not None:
-        if not ws.is_cuda or ws.get_device() != dev or not ws.is_contiguous():
+        if ws.get_device() != dev or not ws.is_contiguous():
             raise ValueError(f"ws must be a contiguous CUDA tensor on device {dev}")
-        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+        ws_ptr, ws_bytes = ws.data_ptr(), ws.nbytes
     _want_rows(pages, n, dev)
     if n == 0:
         return
