@@ -437,7 +437,8 @@ PSW_API int psw_fp4_workspace_bytes(const psw_layer_t *layer, int32_t n_seqs, si
 
 /* attn_decode_paged over 4-bit pools: arguments, masks and errors as
  * attn_decode_paged, but
- *   out  device bf16 [n_seqs][n_q_heads][head_dim] (it feeds the next projection)
+ *   out  device bf16 [n_seqs][n_q_heads][head_dim] (it feeds the next projection);
+ *        it must not overlap q
  *   ws   device workspace, 16-byte aligned, of psw_fp4_workspace_bytes
  * A page whose block id is outside the pool reads as zero rows and is flagged.
  * n_seqs * (max_blocks_per_seq + 8) * n_kv_heads * ceil(n_q_heads / n_kv_heads / 8) and
@@ -738,8 +739,7 @@ PSW_API const char *psw_strerror(int code);
  * Testing hook for the bounded pipeline waits; not for production use.
  * kernel 1 (attn_decode_paged, attn_decode_paged_fp8, attn_decode_latent,
  * attn_decode_latent_fp8, attn_decode_paged_fp4) or 2 (attn_prefill_chunked): from
- * the next launch of
- * such a kernel on, the TMA producer of CTA `cta` leaves its copy number `tile`
+ * the next launch of such a kernel on, the TMA producer of CTA `cta` leaves its copy number `tile`
  * (counted from 0 over its own K tiles; attn_decode_paged_fp4: over the tiles of
  * its first warp) unissued and stops, without flagging anything. The
  * consumer waiting for that copy then gives up after its bound (about one

@@ -2,15 +2,22 @@
 //
 //   s_j = scale * <q, K_j>, capped;  out = sum_j softmax(s)_j V_j
 // over the keys that window and length leave, K_j and V_j being code * block
-// scale * tensor scale. One kernel launch, bound by the pages' bytes where
-// K and V are two pools, and by the conversion of codes next to that where one
-// page serves as both (k_eq_v).
+// scale * tensor scale. One kernel launch.
 //
-//  * Unit = (sequence, KV head, up to 8 query heads). The visible pages of all
-//    units form one list, in which every unit has kUnitCost more entries; every warp of a persistent grid (one CTA per SM) is a
-//    worker of its own with an equal run of it: its own ring of pages in shared
-//    memory, filled by plain bulk copies (a page of a head is one run of bytes),
-//    its own running maximum, sum and output. No warp waits for another.
+// What bounds it (GPU time of a call, 16-token pages): with K and V in two pools the
+// pages' bytes, read at 5.9 of the measured 6.7 TB/s once under way, and about 5 us each
+// to begin (lengths, places, queries, first pages) and to end (the slowest warp, joins):
+// 3 sequences of 40001 to 65536, 7 KV heads, 59.6 us for 302 MB; 64 that see 1024
+// keys, 8 KV heads, 35.7 us for 149 MB. Where one page serves as both (k_eq_v) it is
+// read once and worked on twice: 32 sequences of 1024 to 32768, head size 512, take 122 us
+// for 365 MB, a page 1460 cycles of an SM quarter, 1030 of which are the products and
+// the scalings of codes, which share the quarter's half-precision port.
+//
+//  * Every warp of a persistent grid is a worker of its own (list, runs and joins are
+//    in fp4_decode.cuh): its own ring of pages in shared memory, filled by plain bulk
+//    copies (a page of a head is one run of bytes), its own running maximum, sum and
+//    output. No warp waits for another before the joins. Scores and values in warps of
+//    their own (head size 512) took 141 us instead of 122, two warps to a unit 151.
 //  * A page is 16 keys, the M side of S^T = K Q^T (mma.sync, 16 keys x 16 values x 8
 //    heads); the values are the M side of O^T = V^T P^T. With the large operand
 //    on the M side a product takes 8 of its values per lane and no operand is
@@ -25,13 +32,6 @@
 //    below 2^14 and what lies 30 octaves below the largest is still counted.
 //  * q is multiplied by a power of two per head so that its largest value lies in
 //    [2^14, 2^15): in f16 all but values 2^-28 of that are exact.
-//  * A worker's pieces: units that lie in its run alone are written out. Of the
-//    others it has at most two, the end of one unit (kept in the workspace, its CTA
-//    alone reads it) and the beginning or middle of another (left in shared memory
-//    where the ring was). The CTA joins what its warps have of a unit; only units
-//    that other CTAs have pages of, two at most, go on to the workspace, and the warp
-//    that adds a unit's last pages (a ticket counts them) joins the CTAs' parts, in
-//    their order.
 #include "fp4_decode.cuh"
 
 namespace psw {
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
     uint32_t qr[HD == 256 ? 32 : 1];  // q as operands: HD 256 in registers, HD 512 in shared memory
     uint4* q_smem = reinterpret_cast<uint4*>(smem + W * C::kRingBytes + warp * C::kQBytes) + lane;
     float qf[2];              // factor of the scores of heads 2 t, 2 t + 1
-    float acc[HD / 16][4];    // value 32 g + 2 i (+ 256 part): heads 2 t, 2 t + 1; the next value: same
+    float acc[HD / 16][4];    // value 32 g + 2 i (+ 256 part): heads 2 t, 2 t + 1; then the next
     float m[2], l[2];
     int piece_from = 0;
     uint32_t ends = 0;  // a bit per token seen of the unit's first page, and of its last
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
 #pragma unroll
         for (int x = 0; x < 4; ++x) s[pg][x] = 0.f;
       {
-        uint32_t ks[TP][2][HD / 256];  // scale bytes of tokens r0, r0 + 8: two blocks per 128 values
+        uint32_t ks[TP][2][HD / 256];  // scale bytes of tokens r0, r0 + 8
 #pragma unroll
         for (int pg = 0; pg < TP; ++pg)
 #pragma unroll
@@ -310,7 +310,8 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
           uint32_t ea[TP][2], eb[TP][2];
 #pragma unroll
           for (int pg = 0; pg < TP; ++pg) {
-            const uint8_t* p = tile + pg * C::kPageBytes + (k >> 1) * 2048 + (k_at ^ ((k & 1) * 64));
+            const uint8_t* p =
+                tile + pg * C::kPageBytes + (k >> 1) * 2048 + (k_at ^ ((k & 1) * 64));
             ka[pg] = *reinterpret_cast<const uint4*>(p);
             kb[pg] = *reinterpret_cast<const uint4*>(p + 1024);
             const uint32_t sa = fp4::scales_f16(ks[pg][0][place >> 1] >> (16 * (place & 1)));
@@ -333,8 +334,7 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
             for (int half = 0; half < 2; ++half)
 #pragma unroll
               for (int pg = 0; pg < TP; ++pg) {
-                const uint32_t wa = jp == 0 ? ka[pg].x : jp == 1 ? ka[pg].y : jp == 2 ? ka[pg].z : ka[pg].w;
-                const uint32_t wb = jp == 0 ? kb[pg].x : jp == 1 ? kb[pg].y : jp == 2 ? kb[pg].z : kb[pg].w;
+                const uint32_t wa = word_at(ka[pg], jp), wb = word_at(kb[pg], jp);
                 const uint32_t x[4] = {mul_f16x2(codes_at(wa, 2 * half), ea[pg][h]),
                                        mul_f16x2(codes_at(wb, 2 * half), eb[pg][h]),
                                        mul_f16x2(codes_at(wa, 2 * half + 1), ea[pg][h]),
@@ -580,7 +580,8 @@ int launch_fp4_decode(const LayerArgs& L, const void* q, const void* k_pool, con
   a.stall_cta = hook.cta;
   a.stall_tile = hook.tile;
   if (L.hd == 256)
-    return L.k_eq_v ? launch<256, true>(a, num_sms, stream) : launch<256, false>(a, num_sms, stream);
+    return L.k_eq_v ? launch<256, true>(a, num_sms, stream)
+                    : launch<256, false>(a, num_sms, stream);
   return L.k_eq_v ? launch<512, true>(a, num_sms, stream) : launch<512, false>(a, num_sms, stream);
 }
 

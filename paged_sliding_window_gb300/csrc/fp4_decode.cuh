@@ -1,6 +1,5 @@
-// fp4_decode.cuh -- what the 4-bit decode's two kernels share: the list of pages and
-// its cut into runs, the pieces that runs leave of units and their joining.
-// Library-internal.
+// fp4_decode.cuh -- the list of pages that the 4-bit decode works through, its cut into runs,
+// the pieces that runs leave of units and their joining. Library-internal.
 //
 // Unit = (sequence, KV head, up to 8 query heads). The visible pages of all units form one list,
 // in which every unit has some more entries (what it takes beside its pages); the workers of a
@@ -56,6 +55,9 @@ __device__ __forceinline__ uint32_t codes_at(uint32_t w, int i) {
          : i == 1 ? codes_f16<1>(w)
          : i == 2 ? codes_f16<2>(w)
                   : codes_f16<3>(w);
+}
+__device__ __forceinline__ uint32_t word_at(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 // The bounded wait of a whole warp: the same for all its lanes.
 __device__ __forceinline__ bool landed(uint64_t* bar, uint32_t phase) {
@@ -147,7 +149,8 @@ __device__ __forceinline__ Place next_place(Place* at, const Args& a, int ups, i
 // Adds to a ticket: what this thread's warp has written before is seen by whoever sees the sum.
 __device__ __forceinline__ int add_acq_rel(int32_t* p, int v) {
   int old;
-  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;"
+               : "=r"(old) : "l"(p), "r"(v) : "memory");
   return old;
 }
 
@@ -193,7 +196,6 @@ __device__ __forceinline__ void write_lse(const Args& a, const Piece& p, int hea
         (m + log2f(l)) * lat::kLn2;
 }
 
-
 // The list of `tiles` entries cut into runs for `workers`: of each + 1 entries for the first
 // `more` of them, of `each` for the others.
 struct Cut {
@@ -226,7 +228,8 @@ struct ListSmem {
   int run[kRuns + 1], len[kRuns], sum[kRuns / 32];  // len: where a run is one sequence
 };
 
-// W workers a CTA; called by all its threads (kRuns at least), with the worker that the calling warp is of.
+// W workers a CTA; called by all its threads (kRuns at least), with the worker that the calling
+// warp is of.
 template <int W>
 __device__ __forceinline__ Run begin_run(const Args& a, ListSmem& s, int worker, int cost) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ups = a.n_kv * a.qchunks;
@@ -290,8 +293,8 @@ __device__ __forceinline__ Run begin_run(const Args& a, ListSmem& s, int worker,
   return r;
 }
 
-// Joins the pieces of a CTA's W workers, WARPS warps, whose last pieces lie RING bytes apart in smem;
-// weight: [2 W][8] floats of the calling warp's own.
+// Joins the pieces of a CTA's W workers, WARPS warps, whose last pieces lie RING bytes apart in
+// smem; weight: [2 W][8] floats of the calling warp's own.
 template <int HD, int W, int WARPS, int RING>
 __device__ __forceinline__ void join_pieces(const Args& a, const Cut& cut, int cost,
                                             const Piece (&s_piece)[2 * W],
@@ -333,7 +336,8 @@ __device__ __forceinline__ void join_pieces(const Args& a, const Cut& cut, int c
       for (int k = 0; k < PER; ++k) {
         head[k] = piece_unit(x0 + 32 * k, hp).head;
         o[k] = (last & 1) ? make_float4(0.f, 0.f, 0.f, 0.f)
-                          : __ldcg(a.ws_o + (static_cast<int64_t>(blockIdx.x) * W + (last >> 1)) * units +
+                          : __ldcg(a.ws_o +
+                                   (static_cast<int64_t>(blockIdx.x) * W + (last >> 1)) * units +
                                    x0 + 32 * k);
       }
       const int pages = __reduce_add_sync(0xffffffffu, (members >> lane) & 1 ? mine.pages : 0);
@@ -387,8 +391,8 @@ __device__ __forceinline__ void join_pieces(const Args& a, const Cut& cut, int c
       }
       if (pages != p.np) {  // other CTAs have pages of it: it is this CTA's first or last unit
         // Where many CTAs have, kGroup neighbours' parts are joined into one first (in the place
-        // of the group's first), and the groups' then: one sequence of 40000
-        // with one KV head: 17.4 us, 44.5 with all its parts in a row.
+        // of the group's first), and the groups' then: one sequence of 40000 with one KV head
+        // takes 17.4 us, with all its parts in a row 44.5.
         const Ctas cs = ctas_of<W>(cut, p, cost);
         const int64_t slot0 = part0 + cs.first + p.b * ups + p.j;  // of the first CTA's part
         const int at = static_cast<int>(blockIdx.x) - cs.first;

@@ -212,8 +212,7 @@ int launch_latent_prefill(const LatentArgs& L, const void* q, const int32_t* cu_
                           int num_sms, int32_t* err, cudaStream_t stream);
 
 // ---- 4-bit pages (fp4_*.cu) and tables built on the device (block_tables.cu)
-// Decode workspace: join tickets (one int32 per CTA; zero between calls), then slots of
-// partial results.
+// Decode workspace: tickets of the joins (zero between calls), then slots of partial results.
 constexpr size_t kFp4CounterBytes = PSW_FP4_COUNTER_BYTES;
 // Entries that a unit has in the decode's list beside its pages: what beginning, ending and
 // joining it takes.
