@@ -8,9 +8,9 @@
 // product with 1 / s would put some of those on the wrong side.
 //
 // Both directions are bound by memory: 2 HD bytes on one side of a row, 9/16
-// HD on the other. On the GPU, three sets of inputs in turn: 8 chunks of 512 tokens, 8 KV heads,
-// K and V (34 MB in) 7.4 us written, start-up and latency; 4 ragged chunks of one tensor
-// (about 51 MB in) 9.8 us; 8 contexts of 512 to 8704 read back (391 MB in all) 73 us,
+// HD on the other. On the GPU, three sets of inputs in turn: 8 chunks of 512 tokens, 4 KV heads,
+// K and V (16.8 MB in) 7.4 us written, most of it start-up and latency; 5 ragged chunks of one
+// tensor (25.7 MB in) 9.8 us; 8 contexts of 512 to 8704 read back (391 MB in all) 73 us,
 // 5.3 TB/s, four fifths of it stores.
 #include "fp4.cuh"
 #include "latent.cuh"
