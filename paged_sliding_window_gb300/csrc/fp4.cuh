@@ -78,11 +78,15 @@ __device__ __forceinline__ float e4m3_float(uint32_t byte) {
   return f16x2_to_float2(scales_f16(byte)).x;
 }
 
-// Two floats as E2M1 codes in one byte (nearest, ties to even, saturating).
-__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
+// Eight floats as E2M1 codes, the first in the lowest bits (nearest, ties to even, saturating).
+__device__ __forceinline__ uint32_t e2m1_codes(const float2 (&x)[4]) {
   uint32_t d;
-  asm("{\n\t.reg .b8 a;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-      "mov.b32 %0, {a, 0, 0, 0};\n\t}" : "=r"(d) : "f"(lo), "f"(hi));
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(d)
+      : "f"(x[0].x), "f"(x[0].y), "f"(x[1].x), "f"(x[1].y), "f"(x[2].x), "f"(x[2].y),
+        "f"(x[3].x), "f"(x[3].y));
   return d;
 }
 
@@ -91,12 +95,22 @@ __device__ __forceinline__ uint32_t block_scale(float amax) {
   return __nv_cvt_float_to_fp8(__fmul_rn(amax, 1.f / 6.f), __NV_SATFINITE, __NV_E4M3);
 }
 
-// y / s rounded as a division is, given r = 1 / s (rounded to nearest): a
+// 1 / s of a block's scale, rounded to nearest (0 where s is 0). s has four significant bits, so
+// what the approximation r is off by, 1 - s r, is exact, and the correction leaves 2^-44 of
+// the quotient, which no quotient of so few bits comes near a border by.
+__device__ __forceinline__ float scale_reciprocal(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  r = __fmaf_rn(r, __fmaf_rn(-s, r, 1.f), r);
+  return s > 0.f ? r : 0.f;
+}
+
+// Two y / s rounded as a division is, given -s and r = 1 / s (rounded to nearest) twice: a
 // quotient from the reciprocal, corrected by its remainder. Where s is 0, r is
 // 0 and so is the result.
-__device__ __forceinline__ float quotient(float y, float s, float r) {
-  const float q = __fmul_rn(y, r);
-  return __fmaf_rn(__fmaf_rn(-q, s, y), r, q);
+__device__ __forceinline__ float2 quotients(uint64_t y, uint64_t minus_s, uint64_t r) {
+  const uint64_t q = f2_mul(y, r);
+  return f2_unpack(f2_fma(f2_fma(q, minus_s, y), r, q));
 }
 
 // ---- the visible pages of a batch, in sequence order

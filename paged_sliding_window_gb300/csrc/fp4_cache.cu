@@ -8,10 +8,11 @@
 // product with 1 / s would put some of those on the wrong side.
 //
 // Both directions are bound by memory: 2 HD bytes on one side of a row, 9/16
-// HD on the other. On the GPU, three sets of inputs in turn: 8 chunks of 512 tokens, 4 KV heads,
-// K and V (16.8 MB in) 7.4 us written, most of it start-up and latency; 5 ragged chunks of one
-// tensor (25.7 MB in) 9.8 us; 8 contexts of 512 to 8704 read back (391 MB in all) 73 us,
-// 5.3 TB/s, four fifths of it stores.
+// HD on the other. On the GPU, inputs from memory: 8 chunks of 512 tokens, 4 KV heads, K and V
+// (16.8 MB in) 7.4 us written, 2.2 of them start-up (9.4 with 218 instructions a row instead of
+// 134: limits and products one at a time, rows of both tensors in a warp); 5 ragged
+// chunks of one tensor at HD 512 (25.7 MB in) 8.8 us; 8 contexts of 512 to 8704 read back
+// (391 MB in all) 72 us, 5.4 TB/s, four fifths of it stores.
 #include "fp4.cuh"
 #include "latent.cuh"
 
@@ -20,14 +21,39 @@ namespace {
 
 using fp4::Page;
 
-constexpr int kWarps = 8;
-constexpr int kRows = 4;  // rows (heads of one token, K's before V's) per warp
+constexpr int kWarps = 4;
+constexpr uint32_t kMagnitudes = 0x7FFF7FFFu;
+// Heads of a warp. Small blocks of little work, 16 of them on an SM (12 at HD 512): 64 tokens
+// 2.2 us, 8 chunks of 512 7.4, ragged chunks 8.8; with 4 heads 2.4, 7.5 and 9.0, with 1 2.2, 9.3
+// and 10.1.
+constexpr int kRows = 2;
 
-// One warp takes kRows rows of one token: at HD 256 a lane holds 8 values (a
-// block is two lanes), at HD 512 16 (a block each). The rows are asked for
-// before the token's sequence, page and slot are looked up.
+// Eight values (`v`) as codes: y / s of y = x * inv, given -s and 1 / s. LIMIT: where y may be
+// an infinity or NaN, which the limits of y are for (finite magnitudes above 4096 become the
+// largest code as 4096 does).
+template <bool LIMIT>
+__device__ __forceinline__ uint32_t codes_of(const uint4& v, float inv, float minus_s, float r) {
+  const uint64_t inv2 = f2_pack(inv, inv), r2 = f2_pack(r, r), s2 = f2_pack(minus_s, minus_s);
+  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+  float2 c[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 xx = unpack_bf16x2(x[j]);
+    uint64_t y = f2_mul(f2_pack(xx.x, xx.y), inv2);
+    if (LIMIT) {
+      const float2 z = f2_unpack(y);
+      y = f2_pack(fmaxf(fminf(z.x, 4096.f), -4096.f), fmaxf(fminf(z.y, 4096.f), -4096.f));
+    }
+    c[j] = fp4::quotients(y, s2, r2);
+  }
+  return fp4::e2m1_codes(c);
+}
+
+// One warp takes kRows heads of one token and one tensor, the warps of a block neighbouring
+// tokens: at HD 256 a lane holds 8 values of a head (a block is two lanes), at HD 512 16 (a block
+// each). The rows are asked for before the token's sequence, page and slot are looked up.
 template <int HD>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, HD == 256 ? 16 : 12)
 fp4_write_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
                  const int32_t* __restrict__ cu_new, const int32_t* __restrict__ past_lens,
                  int n_seqs, int n_new_total, const int32_t* __restrict__ block_table,
@@ -36,24 +62,22 @@ fp4_write_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
                  int32_t* err) {
   constexpr int kVec = HD / 256;  // 16-byte vectors per lane and row
   const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int t = static_cast<int>(item / groups);
-  const int row0 = static_cast<int>(item - static_cast<int64_t>(t) * groups) * kRows;
-  if (t >= n_new_total) return;
+  const uint32_t warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (warp >= static_cast<uint32_t>(n_new_total)) return;
+  const int t = static_cast<int>(warp);
+  const bool is_v = static_cast<int>(blockIdx.y) >= groups;
+  const int head0 = (static_cast<int>(blockIdx.y) - (is_v ? groups : 0)) * kRows;
   const int total = __ldg(cu_new + n_seqs);
-  const int rows = v_pool != nullptr ? 2 * n_kv : n_kv;
+  const int heads = min(kRows, n_kv - head0);
   uint4 in[kRows][kVec];
+  {
+    const uint4* src = (is_v ? v : k) +
+                       (static_cast<int64_t>(t) * n_kv + head0) * (HD / 8) + lane * kVec;
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int row = row0 + i;
-    if (row < rows) {
-      const bool is_v = row >= n_kv;
-      const uint4* src = (is_v ? v : k) +
-                         (static_cast<int64_t>(t) * n_kv + (is_v ? row - n_kv : row)) * (HD / 8) +
-                         lane * kVec;
+    for (int i = 0; i < kRows; ++i)
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) in[i][e] = __ldg(src + e);
-    }
+      for (int e = 0; e < kVec; ++e)
+        if (i < heads) in[i][e] = __ldg(src + i * (HD / 8) + e);
   }
   // the token's sequence; up to 31 of them are looked at together with their past lengths
   int b = 0, start = 0, past = 0;
@@ -70,7 +94,8 @@ fp4_write_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
     found = lat::owner_of(cu_new, n_seqs, t, lane, b, start);
     if (found) past = __ldg(past_lens + b);
   }
-  if (t == 0 && row0 == 0 && lane == 0 && total > n_new_total) flag_error(err, PSW_DEVERR_LENGTH);
+  if (t == 0 && blockIdx.y == 0 && lane == 0 && total > n_new_total)
+    flag_error(err, PSW_DEVERR_LENGTH);
   if (t >= total) return;
   if (!found) {
     if (lane == 0) flag_error(err, PSW_DEVERR_LENGTH);
@@ -88,48 +113,41 @@ fp4_write_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
     return;
   }
   const int r = static_cast<int>(pos % kBlockSize);
+  const float inv = is_v ? v_inv : k_inv;
+  uint8_t* to = (is_v ? v_pool : k_pool) +
+                (static_cast<int64_t>(blk) * n_kv + head0) * Page<HD>::kBytes;
+  uint8_t* codes = to + (HD == 256 ? Page<HD>::unit(r, lane >> 2) + (lane & 3) * 4
+                                   : Page<HD>::unit(r, lane >> 1) + (lane & 1) * 8);
+  uint8_t* scale = to + Page<HD>::scale(r, HD == 256 ? lane >> 1 : lane);
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const int row = row0 + i;
-    if (row >= rows) break;
-    const bool is_v = row >= n_kv;
-    uint8_t* dst = (is_v ? v_pool : k_pool) +
-                   (static_cast<int64_t>(blk) * n_kv + (is_v ? row - n_kv : row)) *
-                       Page<HD>::kBytes;
-    const float inv = is_v ? v_inv : k_inv;
-    float y[8 * kVec], amax = 0.f;
+    if (i >= heads) break;
+    // the largest |x| as bf16 bits; its product is the largest |y| (rounding keeps order)
+    uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      float x[8];
-      lat::unpack8(in[i][e], x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        // (a NaN becomes the upper end)
-        y[8 * e + j] = fmaxf(fminf(__fmul_rn(x[j], inv), 4096.f), -4096.f);
-        amax = fmaxf(amax, fabsf(y[8 * e + j]));
-      }
-    }
-    if (HD == 256) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    const uint32_t s8 = fp4::block_scale(amax);
+    for (int e = 0; e < kVec; ++e)
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(in[i][e].x & kMagnitudes, in[i][e].y & kMagnitudes),
+                                   __vmaxu2(in[i][e].z & kMagnitudes, in[i][e].w & kMagnitudes)));
+    if (HD == 256) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    const uint32_t big = max(top << 16, top & 0xFFFF0000u);
+    const float peak = __fmul_rn(__uint_as_float(big), inv);
+    const uint32_t s8 = fp4::block_scale(fminf(peak, 4096.f));  // (a NaN becomes the upper end)
     const float s = fp4::e4m3_float(s8);
-    const float rs = s > 0.f ? __frcp_rn(s) : 0.f;
+    const float rs = fp4::scale_reciprocal(s);
     uint32_t w[kVec];
+    if (__all_sync(0xffffffffu, peak < INFINITY)) {
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      w[e] = 0;
+      for (int e = 0; e < kVec; ++e) w[e] = codes_of<false>(in[i][e], inv, -s, rs);
+    } else {
 #pragma unroll
-      for (int j = 0; j < 8; j += 2)
-        w[e] |= fp4::e2m1_pair(fp4::quotient(y[8 * e + j], s, rs),
-                               fp4::quotient(y[8 * e + j + 1], s, rs))
-                << (4 * j);
+      for (int e = 0; e < kVec; ++e) w[e] = codes_of<true>(in[i][e], inv, -s, rs);
     }
     if constexpr (HD == 256) {
-      *reinterpret_cast<uint32_t*>(dst + Page<HD>::unit(r, lane >> 2) + (lane & 3) * 4) = w[0];
-      if ((lane & 1) == 0) dst[Page<HD>::scale(r, lane >> 1)] = static_cast<uint8_t>(s8);
+      *reinterpret_cast<uint32_t*>(codes + i * Page<HD>::kBytes) = w[0];
+      if ((lane & 1) == 0) scale[i * Page<HD>::kBytes] = static_cast<uint8_t>(s8);
     } else {
-      *reinterpret_cast<uint2*>(dst + Page<HD>::unit(r, lane >> 1) + (lane & 1) * 8) =
-          make_uint2(w[0], w[1]);
-      dst[Page<HD>::scale(r, lane)] = static_cast<uint8_t>(s8);
+      *reinterpret_cast<uint2*>(codes + i * Page<HD>::kBytes) = make_uint2(w[0], w[1]);
+      scale[i * Page<HD>::kBytes] = static_cast<uint8_t>(s8);
     }
   }
 }
@@ -140,13 +158,11 @@ int launch_fp4_write(const LayerArgs& L, const void* k, const void* v, const int
                      const int32_t* past_lens, int n_seqs, int n_new_total,
                      const psw_pages_t& pages, void* k_pool, void* v_pool, float k_scale,
                      float v_scale, int32_t* err, cudaStream_t stream) {
-  const int rows = L.n_kv * (L.k_eq_v ? 1 : 2);
-  const int groups = (rows + kRows - 1) / kRows;
-  const int64_t items = static_cast<int64_t>(n_new_total) * groups;
-  const int64_t blocks = (items + kWarps - 1) / kWarps;
-  if (blocks > INT32_MAX) return PSW_ECAPACITY;
+  const int groups = (L.n_kv + kRows - 1) / kRows, rows = groups * (L.k_eq_v ? 1 : 2);
+  if (rows > 65535) return PSW_ECAPACITY;
+  const dim3 grid((n_new_total - 1) / kWarps + 1, rows);
   auto* fn = L.hd == 256 ? fp4_write_kernel<256> : fp4_write_kernel<512>;
-  fn<<<static_cast<unsigned>(blocks), kWarps * 32, 0, stream>>>(
+  fn<<<grid, kWarps * 32, 0, stream>>>(
       static_cast<const uint4*>(k), static_cast<const uint4*>(v), cu_new, past_lens, n_seqs,
       n_new_total, pages.block_table, pages.max_blocks_per_seq, pages.num_blocks, L.n_kv, groups,
       1.f / k_scale, 1.f / v_scale, static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool),
@@ -157,7 +173,13 @@ int launch_fp4_write(const LayerArgs& L, const void* k, const void* v, const int
 // ---------------------------------------------------------------- read-back
 namespace {
 
+// (two blocks on an SM: with 4 the chunks of 512 take 8.4 us instead of 7.8, with 3 8.1)
 constexpr int kReadThreads = 256;
+
+// a / b: a division of 64 bits only where it takes one
+__device__ __forceinline__ int64_t divided(int64_t a, uint32_t b) {
+  return (a >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / b) : a / b;
+}
 
 // 32 bytes to a 16-byte aligned address; in one store where `wide` says that it is a
 // multiple of 32 (two stores of 16 bytes each touch every sector twice: 8 contexts of 512 to
@@ -179,7 +201,7 @@ __device__ __forceinline__ void store32(uint8_t* p, const uint32_t (&w)[8], bool
 // scale) of a token into 32 bytes, so that a warp's store is whole rows: two tokens at HD 256,
 // one at HD 512.
 template <int HD>
-__global__ void __launch_bounds__(kReadThreads, 4)
+__global__ void __launch_bounds__(kReadThreads, 2)
 fp4_read_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ v_pool,
                 const int32_t* __restrict__ table, int max_blocks, int64_t num_blocks,
                 const int32_t* __restrict__ first, const int32_t* __restrict__ seq_lens,
@@ -226,13 +248,15 @@ fp4_read_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ 
   __syncthreads();
   const int rows = (v_out != nullptr ? 2 * n_kv : n_kv) * kHalves;  // items of a page
   const int64_t items = static_cast<int64_t>(s_run[kReadThreads]) * rows;
-  const int64_t workers = static_cast<int64_t>(gridDim.x) * (kReadThreads / 32);
-  const int64_t me = static_cast<int64_t>(blockIdx.x) * (kReadThreads / 32) + warp;
-  int64_t item = items * me / workers;
-  const int64_t end = items * (me + 1) / workers;
+  const int workers = gridDim.x * (kReadThreads / 32);
+  const int me = blockIdx.x * (kReadThreads / 32) + warp;
+  const int64_t each = divided(items, workers);
+  const int more = static_cast<int>(items - each * workers);  // runs of an item more
+  int64_t item = each * me + min(me, more);
+  const int64_t end = item + each + (me < more ? 1 : 0);
   if (item >= end) return;
   // the sequence of the first item
-  int page = static_cast<int>(item / rows);
+  int page = static_cast<int>(divided(item, rows));
   int row = static_cast<int>(item - static_cast<int64_t>(page) * rows);
   int a = 0, z = kReadThreads;  // s_run[a] <= page < s_run[z]
   while (z - a > 1) {
@@ -322,7 +346,7 @@ int launch_fp4_read(const LayerArgs& L, const void* k_pool, const void* v_pool,
   const bool wide =
       ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0;
   auto* fn = L.hd == 256 ? fp4_read_kernel<256> : fp4_read_kernel<512>;
-  fn<<<num_sms * 4, kReadThreads, 0, stream>>>(
+  fn<<<num_sms * 2, kReadThreads, 0, stream>>>(
       static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), pages.block_table,
       pages.max_blocks_per_seq, pages.num_blocks, first, seq_lens, n_seqs, out_pages.block_table,
       out_pages.max_blocks_per_seq, out_pages.num_blocks, L.n_kv, k_scale, v_scale, wide,
