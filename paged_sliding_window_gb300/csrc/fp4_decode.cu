@@ -50,6 +50,11 @@ struct Cfg {
   static constexpr int kTileBytes = kTile * kPageBytes;
   static constexpr int kRingBytes = 18432;  // per warp
   static constexpr int kStages = kRingBytes / kTileBytes;
+  // Pages that a CTA could work on while the parts of several are joined: a sequence of 256, 8 KV
+  // heads, takes 7.3 us with a CTA for each head and 9.9 cut into equal runs, one of 1024 takes
+  // 13.5 and 10.7; 19 of 1024 (152 units) 13.9 and 15.8. (Head size 512, 4 heads: 256 11.2 and
+  // 12.3, 1024 22.0 and 13.6; k_eq_v 512 14.6 and 14.7, 1024 20.7 and 14.7.)
+  static constexpr int kApart = HD == 256 ? 28 : KEQV ? 32 : 18;
   static constexpr int kQBytes = HD == 256 ? 0 : HD * 8 * 2;  // per warp: q as operands (HD 512)
   static constexpr int kSmem = kWarps * (kRingBytes + kQBytes);
   static_assert(kWarps <= kMaxWorkers && 2 * kWarps <= 32, "pieces of a CTA");
@@ -80,7 +85,7 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
   if (lane < S) mbar_init(&s_full[warp][lane], 1);
   fence_mbar_init();
   if (tid < 2 * W) s_piece[tid].pages = 0;
-  const Run run = begin_run<W>(a, s_list, warp, kUnitCost);
+  const Run run = begin_run<W>(a, s_list, warp, kUnitCost, C::kApart);
   const int me = run.me;
   int page = run.page;   // the next page of the unit that is worked on
   int left = run.left;   // entries of the run from the next page to fetch on

@@ -225,21 +225,25 @@ struct Run {
   Place c;
 };
 struct ListSmem {
-  int run[kRuns + 1], len[kRuns], sum[kRuns / 32];  // len: where a run is one sequence
+  int run[kRuns + 1], len[kRuns];  // len: where a run is one sequence
+  int sum[kRuns / 32], most[kRuns / 32];
 };
 
 // W workers a CTA; called by all its threads (kRuns at least), with the worker that the calling
-// warp is of.
+// warp is of. apart: what the joining of CTAs' parts takes, in pages of a CTA.
 template <int W>
-__device__ __forceinline__ Run begin_run(const Args& a, ListSmem& s, int worker, int cost) {
+__device__ __forceinline__ Run begin_run(const Args& a, ListSmem& s, int worker, int cost,
+                                         int apart) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ups = a.n_kv * a.qchunks;
   // entries of the sequences before each of kRuns runs of them
   const int per = (a.n_seqs + kRuns - 1) / kRuns;
   int incl = 0;
   if (tid < kRuns) {
+    int most = 0;
     for (int b = tid * per; b < min(a.n_seqs, (tid + 1) * per); ++b) {
       const Seq q = seq_of(a, b);
       if (q.np > 0) incl += q.np + cost;
+      most = max(most, q.np);
       s.len[tid] = q.len;
     }
 #pragma unroll
@@ -248,6 +252,8 @@ __device__ __forceinline__ Run begin_run(const Args& a, ListSmem& s, int worker,
       if (lane >= o) incl += x;
     }
     if (lane == 31) s.sum[warp] = incl;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) s.most[warp] = most;
   }
   __syncthreads();
   int all = 0;
@@ -259,14 +265,36 @@ __device__ __forceinline__ Run begin_run(const Args& a, ListSmem& s, int worker,
   if (tid < kRuns) s.run[tid + 1] = incl;
   if (tid == 0) s.run[0] = 0;
   __syncthreads();
+  Run r;
+  r.me = blockIdx.x * W + worker;
+  r.page = r.left = 0;
   const int tiles = all * ups;
+  // Where the CTAs are at least as many as the units, and an equal share of all pages would save
+  // less than the joins take, a CTA has a unit and no part leaves it.
+  const int64_t ctas = gridDim.x;
+  if (static_cast<int64_t>(a.n_seqs) * ups <= ctas) {
+    int most = 0;
+#pragma unroll
+    for (int i = 0; i < kRuns / 32; ++i) most = max(most, s.most[i]);
+    if ((most - apart) * ctas <= tiles) {
+      const int stretch = most + cost;  // (a worker's in the list, had it all these entries)
+      r.cut = Cut{stretch, 0};
+      r.c.b = blockIdx.x / ups;
+      r.c.j = blockIdx.x - r.c.b * ups;
+      r.c.tile0 = blockIdx.x * W * stretch;
+      if (r.c.b < a.n_seqs) {
+        r.c.s = seq_of_len(a, s.len[r.c.b]);
+        const int each = (r.c.s.np + W - 1) / W;
+        r.page = worker * each;
+        r.left = max(0, min(each, r.c.s.np - r.page));
+      }
+      return r;
+    }
+  }
   // (two tiles each at least: a worker more is a piece more to join. One sequence of 40000 with
   // one KV head takes 17.4 us, with a tile each 18.9, with 3 or 4 one or two more)
   const int workers = max(1, min(static_cast<int>(gridDim.x) * W, tiles / 2));
-  Run r;
   r.cut = Cut{tiles / workers, tiles % workers};
-  r.me = blockIdx.x * W + worker;
-  r.page = r.left = 0;
   if (r.me < min(workers, tiles)) {
     const int begin = r.cut.begin(r.me);
     r.left = r.cut.begin(r.me + 1) - begin;

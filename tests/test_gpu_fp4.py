@@ -276,6 +276,23 @@ def test_decode_units_of_many_parts(layer, lens):
     assert bool((ws[:binding.FP4_COUNTER_BYTES] == 0).all())
 
 
+@pytest.mark.parametrize("n", [1, 18, 19, 20])
+@pytest.mark.parametrize("layer", [Layer(16, 8, 256, window=900), Layer(8, 8, 512, scale=0.04),
+                                   Layer(72, 4, 256, k_eq_v=True, scale=0.05)], ids=["256", "512", "256-keqv-chunks"])
+def test_decode_as_many_units_as_blocks(layer, n):
+    """Short contexts, some empty, with up to and just beyond as many units as thread blocks; then
+    the same with one longer context among them."""
+    lens = [(97 * i) % 450 for i in range(1, n)] + [431]
+    for extra in (0, 2500):
+        lens[n // 2] += extra
+        cache, q = filled(layer, lens, 30)
+        ws = binding.alloc_fp4_workspace(layer, n)
+        got = decode(layer, cache, q, lens, ws=ws)
+        no_error()
+        compare(layer, cache, q, lens, got)
+        assert bool((ws[:binding.FP4_COUNTER_BYTES] == 0).all())
+
+
 @pytest.mark.parametrize("gs", [(0.37, 2.5), (2.0 ** -20, 2.0 ** 20)])
 @pytest.mark.parametrize("layer", [L256, L512], ids=["256", "512"])
 def test_decode_tensor_scales(layer, gs):

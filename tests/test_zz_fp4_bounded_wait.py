@@ -16,9 +16,18 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("cta,tile", [(0, 0), (1, 2), (3, 1)])
 @pytest.mark.parametrize("layer", [Layer(4, 2, 256), Layer(8, 1, 512, k_eq_v=True)], ids=["256", "512-keqv"])
 def test_wait_runs_out_and_the_next_call_is_exact(layer, cta, tile):
-    lens = [38000, 30000, 40, 120000]  # (several tiles for every warp)
+    run_out(layer, [38000, 30000, 40, 120000], cta, tile)  # (several tiles for every warp)
+
+
+@pytest.mark.parametrize("cta", [0, 2])
+@pytest.mark.parametrize("layer", [Layer(4, 2, 256), Layer(4, 2, 512, k_eq_v=True)], ids=["256", "512-keqv"])
+def test_wait_runs_out_where_a_block_has_a_unit(layer, cta):
+    run_out(layer, [300, 40], cta, 0)
+
+
+def run_out(layer, lens, cta, tile):
     cache, q = filled(layer, lens, 41)
-    ws = binding.alloc_fp4_workspace(layer, 4)
+    ws = binding.alloc_fp4_workspace(layer, len(lens))
     want = decode(layer, cache, q, lens, ws=ws)
     no_error()
     compare(layer, cache, q, lens, want)
