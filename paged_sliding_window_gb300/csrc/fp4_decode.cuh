@@ -25,6 +25,7 @@ constexpr int kMaxCtas = 160;  // one per SM; what they need of workspace is cou
 constexpr int kMaxWorkers = 12;  // of a CTA
 constexpr int kMaxJobs = 8;    // parts of a unit's output that are joined apart, at most
 constexpr int kGroup = 8;      // CTAs whose parts of a unit are joined first, where there are many
+constexpr int kMostWhole = 1 << 16;  // pages of a unit that is not shared out among CTAs, at most
 constexpr int kRuns = 256;     // runs of sequences whose entries are summed
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -269,23 +270,32 @@ __device__ __forceinline__ Run begin_run(const Args& a, ListSmem& s, int worker,
   r.me = blockIdx.x * W + worker;
   r.page = r.left = 0;
   const int tiles = all * ups;
-  // Where the CTAs are at least as many as the units, and an equal share of all pages would save
-  // less than the joins take, a CTA has a unit and no part leaves it.
-  const int64_t ctas = gridDim.x;
-  if (static_cast<int64_t>(a.n_seqs) * ups <= ctas) {
+  // Where units are few and an equal share of all pages would save less than the joins take, a CTA
+  // has whole units (one, or as many as divide its workers) and no part leaves it: 220
+  // sequences of 1 or 2 with one KV head 8.0 us, cut into equal runs 10.9.
+  {
+    const int64_t ctas = gridDim.x, units = static_cast<int64_t>(a.n_seqs) * ups;
+    int of_cta = 0, team = 0;
+#pragma unroll
+    for (int i = W; i >= 1; --i)
+      if (W % i == 0 && units <= ctas * i) {
+        of_cta = i;
+        team = W / i;
+      }
     int most = 0;
 #pragma unroll
     for (int i = 0; i < kRuns / 32; ++i) most = max(most, s.most[i]);
-    if ((most - apart) * ctas <= tiles) {
+    if (team > 0 && most <= kMostWhole && (most * of_cta - apart) * ctas <= tiles) {
       const int stretch = most + cost;  // (a worker's in the list, had it all these entries)
+      const int mine = worker / team, unit = mine * gridDim.x + blockIdx.x;
       r.cut = Cut{stretch, 0};
-      r.c.b = blockIdx.x / ups;
-      r.c.j = blockIdx.x - r.c.b * ups;
-      r.c.tile0 = blockIdx.x * W * stretch;
+      r.c.b = unit / ups;
+      r.c.j = unit - r.c.b * ups;
+      r.c.tile0 = (blockIdx.x * W + mine * team) * stretch;
       if (r.c.b < a.n_seqs) {
-        r.c.s = seq_of_len(a, s.len[r.c.b]);
-        const int each = (r.c.s.np + W - 1) / W;
-        r.page = worker * each;
+        r.c.s = per == 1 ? seq_of_len(a, s.len[r.c.b]) : seq_of(a, r.c.b);
+        const int each = (r.c.s.np + team - 1) / team;
+        r.page = (worker - mine * team) * each;
         r.left = max(0, min(each, r.c.s.np - r.page));
       }
       return r;
