@@ -7,8 +7,8 @@
 // What bounds it (GPU time of a call, 16-token pages): with K and V in two pools the
 // pages' bytes, read at 5.9 of the measured 6.7 TB/s once under way, and about 5 us each
 // to begin (lengths, places, queries, first pages) and to end (the slowest warp, joins):
-// 3 sequences of 40001 to 65536, 7 KV heads, 59.6 us for 302 MB; 64 that see 1024
-// keys, 8 KV heads, 35.7 us for 149 MB. Where one page serves as both (k_eq_v) it is
+// 3 sequences of 40001 to 65536, 7 KV heads, 60 us for 302 MB; 64 that see 1024
+// keys, 8 KV heads, 36 us for 149 MB. Where one page serves as both (k_eq_v) it is
 // read once and worked on twice: 32 sequences of 1024 to 32768, head size 512, take 122 us
 // for 365 MB, a page 1460 cycles of an SM quarter, 1030 of which are the products and
 // the scalings of codes, which share the quarter's half-precision port.
