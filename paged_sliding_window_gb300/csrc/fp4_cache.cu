@@ -12,7 +12,7 @@
 // (16.8 MB in) 7.4 us written, 2.2 of them start-up (9.4 with 218 instructions a row instead of
 // 134: limits and products one at a time, rows of both tensors in a warp); 5 ragged
 // chunks of one tensor at HD 512 (25.7 MB in) 8.8 us; 8 contexts of 512 to 8704 read back
-// (391 MB in all) 72 us, 5.4 TB/s, four fifths of it stores.
+// (391 MB in all) 68 us, 5.8 TB/s, four fifths of it stores.
 #include "fp4.cuh"
 #include "latent.cuh"
 
@@ -173,8 +173,12 @@ int launch_fp4_write(const LayerArgs& L, const void* k, const void* v, const int
 // ---------------------------------------------------------------- read-back
 namespace {
 
-// (two blocks on an SM: with 4 the chunks of 512 take 8.4 us instead of 7.8, with 3 8.1)
-constexpr int kReadThreads = 256;
+// Four blocks on an SM; where each warp has many items, three of them do all: the memory
+// takes the stores of fewer warps better (8 contexts of 512 to 8704: 67.6 us with 3, 70.5 with 4;
+// 8 chunks of 512 8.1 and 7.7). With twice the threads and half the blocks 70.7 and 7.8.
+constexpr int kReadThreads = 128;
+constexpr int kReadBlocks = 4;
+constexpr int kManyItems = 8;  // of a warp
 
 // a / b: a division of 64 bits only where it takes one
 __device__ __forceinline__ int64_t divided(int64_t a, uint32_t b) {
@@ -183,7 +187,7 @@ __device__ __forceinline__ int64_t divided(int64_t a, uint32_t b) {
 
 // 32 bytes to a 16-byte aligned address; in one store where `wide` says that it is a
 // multiple of 32 (two stores of 16 bytes each touch every sector twice: 8 contexts of 512 to
-// 8704 tokens took 82.8 us with them).
+// 8704 tokens took 82.8 us with them, 73.4 without, in an earlier form).
 __device__ __forceinline__ void store32(uint8_t* p, const uint32_t (&w)[8], bool wide) {
   if (wide) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
@@ -195,13 +199,13 @@ __device__ __forceinline__ void store32(uint8_t* p, const uint32_t (&w)[8], bool
   }
 }
 
-// The pages wanted of all sequences form one list; with every (KV head, tensor) of a page,
-// and at HD 512 every half of its tokens, they are the items, of which each warp of a
-// persistent grid takes an equal run. A lane turns one block of 16 values (8 bytes and a
-// scale) of a token into 32 bytes, so that a warp's store is whole rows: two tokens at HD 256,
+// The pages wanted of all sequences form one list; with every (KV head, tensor) of a page, and
+// every half (HD 256) or quarter (HD 512) of its tokens, they are the items, of which each
+// warp of a persistent grid takes an equal run. A lane turns one block of 16 values (8 bytes and
+// a scale) of a token into 32 bytes, so that a warp's store is whole rows: two tokens at HD 256,
 // one at HD 512.
 template <int HD>
-__global__ void __launch_bounds__(kReadThreads, 2)
+__global__ void __launch_bounds__(kReadThreads, kReadBlocks)
 fp4_read_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ v_pool,
                 const int32_t* __restrict__ table, int max_blocks, int64_t num_blocks,
                 const int32_t* __restrict__ first, const int32_t* __restrict__ seq_lens,
@@ -210,8 +214,8 @@ fp4_read_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ 
                 bool wide, uint8_t* __restrict__ k_out, uint8_t* __restrict__ v_out,
                 int32_t* err) {
   constexpr int kTok = 512 / HD;               // tokens per warp store
-  constexpr int kSteps = 8;                    // stores of an item
-  constexpr int kHalves = kBlockSize / (kTok * kSteps);
+  constexpr int kSteps = 4;                    // stores of an item
+  constexpr int kSplit = kBlockSize / (kTok * kSteps);  // items of a page of a head
   constexpr int kLanes = HD / 16;              // lanes of a token
   __shared__ int s_run[kReadThreads + 1];
   __shared__ int s_warp[kReadThreads / 32];
@@ -246,10 +250,12 @@ fp4_read_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ 
   s_run[tid + 1] = before + incl;
   if (tid == 0) s_run[0] = 0;
   __syncthreads();
-  const int rows = (v_out != nullptr ? 2 * n_kv : n_kv) * kHalves;  // items of a page
+  const int rows = (v_out != nullptr ? 2 * n_kv : n_kv) * kSplit;  // items of a page
   const int64_t items = static_cast<int64_t>(s_run[kReadThreads]) * rows;
-  const int workers = gridDim.x * (kReadThreads / 32);
+  int workers = gridDim.x * (kReadThreads / 32);
+  if (items > static_cast<int64_t>(workers) * kManyItems) workers -= workers / kReadBlocks;
   const int me = blockIdx.x * (kReadThreads / 32) + warp;
+  if (me >= workers) return;
   const int64_t each = divided(items, workers);
   const int more = static_cast<int>(items - each * workers);  // runs of an item more
   int64_t item = each * me + min(me, more);
@@ -272,7 +278,15 @@ fp4_read_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ 
   const int tok = lane / kLanes, blk16 = lane % kLanes;
   bool looked_up = false;
   int32_t src = 0, dst = 0;
-  for (; item < end; ++item) {
+  // what is on its way: an item's codes and scales, where its rows go, and which are wanted
+  struct Asked {
+    uint2 c[kSteps];
+    uint32_t s8[kSteps];
+    uint8_t* out;
+    float gs;
+    int lo, hi;
+  };
+  auto ask = [&](Asked& x) {
     if (!looked_up) {
       const int p = s.p0 + page - off;
       src = __ldg(table + static_cast<int64_t>(b) * max_blocks + p);
@@ -282,58 +296,64 @@ fp4_read_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ 
         flag_error(err, PSW_DEVERR_BLOCK_ID);
       looked_up = true;
     }
-    if (dst >= 0 && dst < out_num_blocks) {
-      const int r0 = kHalves == 1 ? 0 : (row & 1) * (kBlockSize / 2);
-      const bool is_v = row / kHalves >= n_kv;
-      const int head = is_v ? row / kHalves - n_kv : row / kHalves;
-      const bool have = src >= 0 && src < num_blocks;
-      const uint8_t* in = (is_v ? v_pool : k_pool) +
-                          (static_cast<int64_t>(have ? src : 0) * n_kv + head) * Page<HD>::kBytes;
-      uint8_t* out = (is_v ? v_out : k_out) +
-                     (static_cast<int64_t>(dst) * kBlockSize * n_kv + head) * (HD * 2) + blk16 * 32;
-      const float gs = is_v ? v_scale : k_scale;
-      uint2 c[kSteps];
-      uint32_t s8[kSteps];
+    const int part = row / kSplit, r0 = (row - part * kSplit) * (kTok * kSteps) + tok;
+    const bool is_v = part >= n_kv, have = src >= 0 && src < num_blocks;
+    const int head = is_v ? part - n_kv : part, pos0 = (s.p0 + page - off) * kBlockSize + r0;
+    const uint8_t* in = (is_v ? v_pool : k_pool) +
+                        (static_cast<int64_t>(src) * n_kv + head) * Page<HD>::kBytes;
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const int r = r0 + i * kTok + tok;
-        c[i] = __ldg(reinterpret_cast<const uint2*>(in + Page<HD>::unit(r, blk16 >> 1) +
-                                                    (blk16 & 1) * 8));
-        s8[i] = __ldg(in + Page<HD>::scale(r, blk16));
-      }
-      const int pos0 = (s.p0 + page - off) * kBlockSize;
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const int r = r0 + i * kTok + tok;
-        const float f = have ? fp4::e4m3_float(s8[i]) * gs : 0.f;
-        uint32_t w[8];
-        const uint32_t cw[2] = {have ? c[i].x : 0u, have ? c[i].y : 0u};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t p[4] = {fp4::codes_f16<0>(cw[h]), fp4::codes_f16<1>(cw[h]),
-                                 fp4::codes_f16<2>(cw[h]), fp4::codes_f16<3>(cw[h])};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 x = fp4::f16x2_to_float2(p[j]);
-            w[4 * h + j] = pack_bf16x2(x.x * f, x.y * f);
-          }
-        }
-        const int pos = pos0 + r;
-        if (pos >= s.lo && pos < s.len) {
-          store32(out + static_cast<int64_t>(r) * n_kv * (HD * 2), w, wide);
-        }
-      }
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = r0 + i * kTok;
+      x.c[i] = have ? __ldg(reinterpret_cast<const uint2*>(in + Page<HD>::unit(r, blk16 >> 1) +
+                                                           (blk16 & 1) * 8))
+                    : make_uint2(0, 0);
+      x.s8[i] = have ? __ldg(in + Page<HD>::scale(r, blk16)) : 0;
     }
+    x.out = (is_v ? v_out : k_out) +
+            ((static_cast<int64_t>(dst) * kBlockSize + r0) * n_kv + head) * (HD * 2) + blk16 * 32;
+    x.gs = is_v ? v_scale : k_scale;
+    x.lo = s.lo - pos0;
+    x.hi = dst >= 0 && dst < out_num_blocks ? s.len - pos0 : INT32_MIN;
+    ++item;
     if (++row == rows) {
       row = 0;
       looked_up = false;
       ++page;
-      while (item + 1 < end && page >= off + s.np) {
+      while (item < end && page >= off + s.np) {
         off += s.np;
         s = pages_of(++b, false);
       }
     }
+  };
+  auto give = [&](const Asked& x) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const float f = fp4::e4m3_float(x.s8[i]) * x.gs;
+      uint32_t w[8];
+      const uint32_t cw[2] = {x.c[i].x, x.c[i].y};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t p[4] = {fp4::codes_f16<0>(cw[h]), fp4::codes_f16<1>(cw[h]),
+                               fp4::codes_f16<2>(cw[h]), fp4::codes_f16<3>(cw[h])};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 y = fp4::f16x2_to_float2(p[j]);
+          w[4 * h + j] = pack_bf16x2(y.x * f, y.y * f);
+        }
+      }
+      if (i * kTok >= x.lo && i * kTok < x.hi)
+        store32(x.out + static_cast<int64_t>(i * kTok) * n_kv * (HD * 2), w, wide);
+    }
+  };
+  Asked now;
+  ask(now);
+  while (item < end) {  // (the next item is on its way while this one's rows are stored)
+    Asked next;
+    ask(next);
+    give(now);
+    now = next;
   }
+  give(now);
 }
 
 }  // namespace
@@ -346,7 +366,7 @@ int launch_fp4_read(const LayerArgs& L, const void* k_pool, const void* v_pool,
   const bool wide =
       ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0;
   auto* fn = L.hd == 256 ? fp4_read_kernel<256> : fp4_read_kernel<512>;
-  fn<<<num_sms * 2, kReadThreads, 0, stream>>>(
+  fn<<<num_sms * kReadBlocks, kReadThreads, 0, stream>>>(
       static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), pages.block_table,
       pages.max_blocks_per_seq, pages.num_blocks, first, seq_lens, n_seqs, out_pages.block_table,
       out_pages.max_blocks_per_seq, out_pages.num_blocks, L.n_kv, k_scale, v_scale, wide,

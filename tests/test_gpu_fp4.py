@@ -139,6 +139,8 @@ def wide_pages(cache, lens, firsts, seed, spare=2):
     pytest.param(Layer(3, 3, 512), [70, 5], [69, 0], (2.0, 0.37), id="512"),
     pytest.param(KEQV, [40, 300], [0, 131], (0.5, 1.0), id="keqv"),
     pytest.param(L512, [(7 * i) % 90 for i in range(700)], [(7 * i) % 90 // 2 for i in range(700)], (1.0, 1.0), id="700-sequences"),
+    pytest.param(Layer(8, 8, 256), [7001, 3, 5555], [11, 0, 1003], (1.0, 0.37), id="many"),
+    pytest.param(Layer(4, 4, 512, k_eq_v=True), [333, 20001], [300, 17], (1.0, 1.0), id="many-512-keqv"),
 ])
 def test_read(layer, lens, firsts, gs):
     g = gen(8)
