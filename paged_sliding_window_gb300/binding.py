@@ -754,14 +754,27 @@ def block_table_extend(block_table, past_lens, new_lens, free_ids, free_pos, fre
     dev, n = block_table.get_device(), past_lens.shape[0]
     if block_table.dim() != 2 or block_table.shape[0] < n:
         raise ValueError(f"block_table must have {n} rows or more, got {tuple(block_table.shape)}")
-    _want(block_table, _I32, block_table.shape, "block_table", dev)
-    _want(past_lens, _I32, (n,), "past_lens", dev)
-    _want(new_lens, _I32, (n,), "new_lens", dev)
-    _want(free_ids, _I32, (free_ids.numel(),), "free_ids", dev)
-    _want(free_pos, _I32, (1,), "free_pos", dev)
-    _want(free_next, _I32, (1,), "free_next", dev)
-    _want(cu_new, _I32, (n + 1,), "cu_new", dev)
-    _want(seq_lens, _I32, (n,), "seq_lens", dev)
+    one, each = (1,), (n,)
+    # (what _want looks at in one expression, and by _want where something is wrong: 1 us)
+    if not (block_table.dtype is _I32 and block_table.is_contiguous()
+            and past_lens.dtype is _I32 and past_lens.shape == each and past_lens.is_contiguous()
+            and new_lens.dtype is _I32 and new_lens.shape == each and new_lens.is_contiguous()
+            and free_ids.dtype is _I32 and free_ids.dim() == 1 and free_ids.is_contiguous()
+            and free_pos.dtype is _I32 and free_pos.shape == one
+            and free_next.dtype is _I32 and free_next.shape == one
+            and cu_new.dtype is _I32 and cu_new.shape == (n + 1,) and cu_new.is_contiguous()
+            and seq_lens.dtype is _I32 and seq_lens.shape == each and seq_lens.is_contiguous()
+            and past_lens.get_device() == new_lens.get_device() == free_ids.get_device()
+            == free_pos.get_device() == free_next.get_device() == cu_new.get_device()
+            == seq_lens.get_device() == dev):
+        _want(block_table, _I32, block_table.shape, "block_table", dev)
+        _want(past_lens, _I32, each, "past_lens", dev)
+        _want(new_lens, _I32, each, "new_lens", dev)
+        _want(free_ids, _I32, (free_ids.numel(),), "free_ids", dev)
+        _want(free_pos, _I32, one, "free_pos", dev)
+        _want(free_next, _I32, one, "free_next", dev)
+        _want(cu_new, _I32, (n + 1,), "cu_new", dev)
+        _want(seq_lens, _I32, each, "seq_lens", dev)
     slot_args = (None, 0)
     if slots is not None:
         _want(slots, torch.int64, (slots.numel(),), "slots", dev)
@@ -786,11 +799,20 @@ def kv_cache_write_fp4(layer, k, v, cu_new, past_lens, pages: PswPages, k_pool4,
     shape, pool = (rows, n_kv, hd), (pages.num_blocks, n_kv, 9 * hd)
     _want_v(v, k_eq_v, "v")
     _want_v(v_pool4, k_eq_v, "v_pool4")
-    _want(k, _BF16, shape, "k", dev)
-    _want(cu_new, _I32, (n + 1,), "cu_new", dev)
-    _want(past_lens, _I32, (n,), "past_lens", dev)
-    _want(k_pool4, _U8, pool, "k_pool4", dev)
-    if v is not None:
+    # (what _want looks at in one expression, and by _want where something is wrong: 0.4 us)
+    if not (k.dtype is _BF16 and k.shape == shape and k.is_contiguous()
+            and cu_new.dtype is _I32 and cu_new.shape == (n + 1,) and cu_new.is_contiguous()
+            and past_lens.dtype is _I32 and past_lens.shape == (n,) and past_lens.is_contiguous()
+            and k_pool4.dtype is _U8 and k_pool4.shape == pool and k_pool4.is_contiguous()
+            and cu_new.get_device() == past_lens.get_device() == k_pool4.get_device() == dev):
+        _want(k, _BF16, shape, "k", dev)
+        _want(cu_new, _I32, (n + 1,), "cu_new", dev)
+        _want(past_lens, _I32, (n,), "past_lens", dev)
+        _want(k_pool4, _U8, pool, "k_pool4", dev)
+    if not (k_eq_v or (
+            v.dtype is _BF16 and v.shape == shape and v.is_contiguous()
+            and v_pool4.dtype is _U8 and v_pool4.shape == pool and v_pool4.is_contiguous()
+            and v.get_device() == v_pool4.get_device() == dev)):
         _want(v, _BF16, shape, "v", dev)
         _want(v_pool4, _U8, pool, "v_pool4", dev)
     _want_rows(pages, n, dev)
