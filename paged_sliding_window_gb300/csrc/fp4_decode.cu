@@ -9,7 +9,7 @@
 // to begin (lengths, places, queries, first pages) and to end (the slowest warp, joins):
 // 3 sequences of 40001 to 65536, 7 KV heads, 60 us for 302 MB; 64 that see 1024
 // keys, 8 KV heads, 36 us for 149 MB. Where one page serves as both (k_eq_v) it is
-// read once and worked on twice: 32 sequences of 1024 to 32768, head size 512, take 122 us
+// read once and worked on twice: 32 sequences of 1024 to 32768, head size 512, take 121 us
 // for 365 MB, a page 1460 cycles of an SM quarter, 1030 of which are the products and
 // the scalings of codes, which share the quarter's half-precision port.
 //
@@ -17,7 +17,7 @@
 //    in fp4_decode.cuh): its own ring of pages in shared memory, filled by plain bulk
 //    copies (a page of a head is one run of bytes), its own running maximum, sum and
 //    output. No warp waits for another before the joins. Scores and values in warps of
-//    their own (head size 512) took 141 us instead of 122, two warps to a unit 151.
+//    their own (head size 512) took 141 us instead of 121, two warps to a unit 151.
 //  * A page is 16 keys, the M side of S^T = K Q^T (mma.sync, 16 keys x 16 values x 8
 //    heads); the values are the M side of O^T = V^T P^T. With the large operand
 //    on the M side a product takes 8 of its values per lane and no operand is
@@ -288,9 +288,12 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
       const bool edge = seen != kAll || (word & 6) != 0;
 
       // ---- S^T = K Q^T
-      float s[TP][4];
+      // a page's products in two sums where there are few warps (71.2 -> 69.9 us, k_eq_v 122.2
+      // -> 121.2; at HD 256 the registers cost more: 36.1 -> 37.0)
+      constexpr int kSums = HD == 512 ? 2 : 1;
+      float s[TP * kSums][4];
 #pragma unroll
-      for (int pg = 0; pg < TP; ++pg)
+      for (int pg = 0; pg < TP * kSums; ++pg)
 #pragma unroll
         for (int x = 0; x < 4; ++x) s[pg][x] = 0.f;
       {
@@ -344,7 +347,7 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
                                        mul_f16x2(codes_at(wb, 2 * half), eb[pg][h]),
                                        mul_f16x2(codes_at(wa, 2 * half + 1), ea[pg][h]),
                                        mul_f16x2(codes_at(wb, 2 * half + 1), eb[pg][h])};
-                mma_f16(s[pg], x, half ? qq.z : qq.x, half ? qq.w : qq.y);
+                mma_f16(s[pg * kSums + half % kSums], x, half ? qq.z : qq.x, half ? qq.w : qq.y);
               }
           }
         }
@@ -354,7 +357,9 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
 #pragma unroll
       for (int pg = 0; pg < TP; ++pg)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) z[pg][x] = s[pg][x] * qf[x & 1];
+        for (int x = 0; x < 4; ++x)
+          z[pg][x] = (kSums == 1 ? s[pg][x] : s[pg * kSums][x] + s[pg * kSums + kSums - 1][x]) *
+                     qf[x & 1];
       if (a.softcap > 0.f) {
 #pragma unroll
         for (int pg = 0; pg < TP; ++pg)
