@@ -398,7 +398,8 @@ PSW_API int attn_decode_paged_fp8(const psw_layer_t *layer, const void *q, const
 /* kv_cache_write into 4-bit pools: arguments as kv_cache_write, with the bf16
  * rows k, v [n_new_total][n_kv_heads][head_dim] quantised as above. n_new_total is
  * the host's count of rows: rows that cu_new names beyond it are not touched and
- * flagged (PSW_DEVERR_LENGTH). Errors as kv_cache_write, PSW_EINVAL_SCALE for a
+ * flagged (PSW_DEVERR_LENGTH), as are all rows of a sequence with a negative past
+ * length. Errors as kv_cache_write, PSW_EINVAL_SCALE for a
  * tensor scale out of range, PSW_ECAPACITY for more than 65534 KV heads. */
 PSW_API int kv_cache_write_fp4(const psw_layer_t *layer, const void *k, const void *v,
                                const int32_t *cu_new, const int32_t *past_lens, int32_t n_seqs,

@@ -103,8 +103,8 @@ fp4_write_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
   }
   const int64_t pos = static_cast<int64_t>(past) + (t - start);
   const int64_t page = pos / kBlockSize;
-  if (pos < 0 || page >= max_blocks) {
-    if (lane == 0) flag_error(err, pos < 0 ? PSW_DEVERR_LENGTH : PSW_DEVERR_CAPACITY);
+  if (past < 0 || page >= max_blocks) {  // (a negative past: no row of its sequence is written)
+    if (lane == 0) flag_error(err, past < 0 ? PSW_DEVERR_LENGTH : PSW_DEVERR_CAPACITY);
     return;
   }
   const int32_t blk = __ldg(block_table + static_cast<int64_t>(b) * max_blocks + page);
