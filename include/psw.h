@@ -469,11 +469,12 @@ PSW_API int attn_decode_paged_fp4(const psw_layer_t *layer, const void *q, const
  *              no page; or NULL
  * No other two buffers may overlap. Entries that the list has no id for become -1
  * (PSW_DEVERR_NOBLOCKS), pages beyond the row are left out
- * (PSW_DEVERR_CAPACITY), a sequence with a negative length gets no new token and
- * a past of at least 0, tokens beyond n_slots get no slot, a cursor outside [0,
- * n_free] takes nothing (all PSW_DEVERR_LENGTH), a token on a page that the table had
- * as negative gets -1 (PSW_DEVERR_BLOCK_ID). n_seqs * max_blocks_per_seq must stay
- * below 2^31 (PSW_ECAPACITY). n_seqs 0 launches nothing.
+ * (PSW_DEVERR_CAPACITY), a sequence with a negative length, or that would have more
+ * than 2^31 - 17 tokens, gets no new token and a past of at least 0, tokens beyond
+ * n_slots get no slot, a cursor outside [0, n_free] takes nothing (all
+ * PSW_DEVERR_LENGTH), a token on a page that the table had as negative gets -1
+ * (PSW_DEVERR_BLOCK_ID). n_seqs * max_blocks_per_seq must stay below 2^31
+ * (PSW_ECAPACITY). n_seqs 0 launches nothing.
  */
 PSW_API int block_table_extend(int32_t *block_table, int32_t max_blocks_per_seq,
                                const int32_t *past_lens, const int32_t *new_lens, int32_t n_seqs,

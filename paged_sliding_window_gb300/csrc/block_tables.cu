@@ -16,6 +16,11 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWideCtas = 8;  // a cluster of these where there are many tokens
 
+// Pages of n tokens (n up to INT32_MAX).
+__device__ __forceinline__ int pages_of(int n) {
+  return n / kBlockSize + (n % kBlockSize != 0);
+}
+
 // Exclusive prefix sum over the block; *total is the sum.
 template <class T>
 __device__ __forceinline__ T block_scan(T x, T* s_warp, T* total) {
@@ -92,8 +97,7 @@ block_table_extend_kernel(int32_t* block_table, int max_blocks, const int32_t* p
         past = max(past, 0);
         add = 0;
       }
-      const int have = (past + kBlockSize - 1) / kBlockSize;
-      const int want = (past + add + kBlockSize - 1) / kBlockSize;
+      const int have = pages_of(past), want = pages_of(past + add);
       if (want > max_blocks) bits |= PSW_DEVERR_CAPACITY;
       need = max(0, min(want, max_blocks) - have);
     }
@@ -111,7 +115,7 @@ block_table_extend_kernel(int32_t* block_table, int max_blocks, const int32_t* p
     __syncthreads();
     for (int k = me; k < pages; k += all) {
       const int i = last_at_most(s_page, n, k);
-      const int have = (s_past[i] + kBlockSize - 1) / kBlockSize;
+      const int have = pages_of(s_past[i]);
       const int at = page0 + k;
       int32_t id = -1;
       if (at < avail) id = free_ids[pos0 + at]; else bits |= PSW_DEVERR_NOBLOCKS;
@@ -123,7 +127,7 @@ block_table_extend_kernel(int32_t* block_table, int max_blocks, const int32_t* p
       for (int64_t t = me; t < min(toks, room); t += all) {
         const int i = last_at_most(s_tok, n, t);
         const int pos = s_past[i] + static_cast<int>(t - s_tok[i]);
-        const int have = (s_past[i] + kBlockSize - 1) / kBlockSize, page = pos / kBlockSize;
+        const int have = pages_of(s_past[i]), page = pos / kBlockSize;
         int32_t id = -1;
         if (page < max_blocks) {
           if (page < have) {
