@@ -474,7 +474,8 @@ PSW_API int attn_decode_paged_fp4(const psw_layer_t *layer, const void *q, const
  * n_slots get no slot, a cursor outside [0, n_free] takes nothing (all
  * PSW_DEVERR_LENGTH), a token on a page that the table had as negative gets -1
  * (PSW_DEVERR_BLOCK_ID). n_seqs * max_blocks_per_seq must stay below 2^31
- * (PSW_ECAPACITY). n_seqs 0 launches nothing.
+ * (PSW_ECAPACITY). With n_seqs 0, cu_new[0] and *free_next are written as always where
+ * free_next is not free_pos; where it is, nothing is launched and cu_new is left.
  */
 PSW_API int block_table_extend(int32_t *block_table, int32_t max_blocks_per_seq,
                                const int32_t *past_lens, const int32_t *new_lens, int32_t n_seqs,

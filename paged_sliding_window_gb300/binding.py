@@ -750,7 +750,8 @@ def block_table_extend(block_table, past_lens, new_lens, free_ids, free_pos, fre
     """The tables of a step, built on the device: block_table int32 [n, max_blocks] gets entries
     for the pages that new_lens int32 [n] tokens after past_lens [n] begin, from free_ids int32
     [n_free] at the cursor free_pos int32 [1] on; free_next [1] (may be free_pos), cu_new [n + 1],
-    seq_lens [n] and slots int64 [rows] or None are written."""
+    seq_lens [n] and slots int64 [rows] or None are written (n 0: the cursor, where it is not in
+    place, and cu_new with it)."""
     dev, n = block_table.get_device(), past_lens.shape[0]
     if block_table.dim() != 2 or block_table.shape[0] < n:
         raise ValueError(f"block_table must have {n} rows or more, got {tuple(block_table.shape)}")
@@ -779,7 +780,14 @@ def block_table_extend(block_table, past_lens, new_lens, free_ids, free_pos, fre
     if slots is not None:
         _want(slots, torch.int64, (slots.numel(),), "slots", dev)
         slot_args = (slots.data_ptr(), slots.shape[0])
-    if n == 0:
+    if n == 0:  # (empty tensors have no address, and none of theirs is used)
+        at = cu_new.data_ptr()
+        rc = load().block_table_extend(at, max(1, block_table.shape[1]), at, at, 0,
+                                       free_ids.data_ptr() or None, free_ids.shape[0],
+                                       free_pos.data_ptr(), free_next.data_ptr(), at, at,
+                                       *slot_args, _stream_here(dev, stream))
+        if rc:
+            _raise(rc, "block_table_extend")
         return
     rc = load().block_table_extend(block_table.data_ptr(), block_table.shape[1],
                                    past_lens.data_ptr(), new_lens.data_ptr(), n,

@@ -62,7 +62,8 @@ __device__ __forceinline__ int last_at_most(const T* s, int n, T x) {
 
 // One cluster (of one CTA or of kWideCtas). Sequences are taken kThreads at a
 // time, one a thread; every CTA scans them all, and the pages and tokens that
-// they bring are shared out among all threads of the cluster.
+// they bring are shared out among all threads of the cluster. Without sequences (free_next is
+// then not free_pos) the offsets' end and the cursor are all there is to write.
 __global__ void __launch_bounds__(kThreads)
 block_table_extend_kernel(int32_t* block_table, int max_blocks, const int32_t* past_lens,
                           const int32_t* new_lens, int n_seqs, const int32_t* free_ids,

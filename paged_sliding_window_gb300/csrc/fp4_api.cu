@@ -50,7 +50,8 @@ int block_table_extend(int32_t* block_table, int32_t max_blocks_per_seq, const i
       !aligned(free_ids, 4) || !aligned(free_pos, 4) || !aligned(free_next, 4) ||
       !aligned(cu_new, 4) || !aligned(seq_lens, 4) || !aligned(slots, 8))
     return PSW_EALIGN;
-  if (n_seqs == 0) return PSW_OK;
+  // (without sequences a cursor kept in place stays as it is; a second one has to follow it)
+  if (n_seqs == 0 && free_next == free_pos) return PSW_OK;
   DeviceInfo info;
   int32_t* err;
   const int rc = ready(&info, &err);
