@@ -492,6 +492,7 @@ __device__ __forceinline__ void join_pieces(const Args& a, const Cut& cut, int c
           int32_t* first = ticket + ((from == 0 ? 1 : 2) * kMaxCtas + from) * kMaxJobs;
           if (!last_of(first, pages, ready)) continue;
           add_parts(from, 1, m);
+          __syncwarp();  // every lane has read the first part, whose place the group's takes
 #pragma unroll
           for (int k = 0; k < PER; ++k) {
             a.ws_o[(slot0 + from) * units + x0 + 32 * k] = o[k];
