@@ -95,9 +95,13 @@ __device__ __forceinline__ uint32_t block_scale(float amax) {
   return __nv_cvt_float_to_fp8(__fmul_rn(amax, 1.f / 6.f), __NV_SATFINITE, __NV_E4M3);
 }
 
+// Markstein's division (IBM RS/6000, 1990): a quotient from the reciprocal rounded to nearest,
+// corrected by its exact remainder, is the correctly rounded one (but for divisors whose bits are all
+// ones, which four bits are not).
+//
 // 1 / s of a block's scale, rounded to nearest (0 where s is 0). s has four significant bits, so
-// what the approximation r is off by, 1 - s r, is exact, and the correction leaves 2^-44 of
-// the quotient, which no quotient of so few bits comes near a border by.
+// 1 - s r is exact for an approximation r off by up to two units in the last place, and one
+// correction by it gives the nearest number for each of the eight significands.
 __device__ __forceinline__ float scale_reciprocal(float s) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
@@ -105,9 +109,8 @@ __device__ __forceinline__ float scale_reciprocal(float s) {
   return s > 0.f ? r : 0.f;
 }
 
-// Two y / s rounded as a division is, given -s and r = 1 / s (rounded to nearest) twice: a
-// quotient from the reciprocal, corrected by its remainder. Where s is 0, r is
-// 0 and so is the result.
+// Two y / s rounded as a division is, given -s and r = 1 / s (rounded to nearest, which the
+// method asks for) twice. Where s is 0, r is 0 and so is the result.
 __device__ __forceinline__ float2 quotients(uint64_t y, uint64_t minus_s, uint64_t r) {
   const uint64_t q = f2_mul(y, r);
   return f2_unpack(f2_fma(f2_fma(q, minus_s, y), r, q));
