@@ -399,8 +399,8 @@ PSW_API int attn_decode_paged_fp8(const psw_layer_t *layer, const void *q, const
  * rows k, v [n_new_total][n_kv_heads][head_dim] quantised as above. n_new_total is
  * the host's count of rows: rows that cu_new names beyond it are not touched and
  * flagged (PSW_DEVERR_LENGTH), as are all rows of a sequence with a negative past
- * length. Errors as kv_cache_write, PSW_EINVAL_SCALE for a
- * tensor scale out of range, PSW_ECAPACITY for more than 65534 KV heads. */
+ * length. Errors as kv_cache_write, PSW_EINVAL_SCALE for a tensor scale out of
+ * range, PSW_ECAPACITY for more than 65534 KV heads. */
 PSW_API int kv_cache_write_fp4(const psw_layer_t *layer, const void *k, const void *v,
                                const int32_t *cu_new, const int32_t *past_lens, int32_t n_seqs,
                                int32_t n_new_total, const psw_pages_t *pages, void *k_pool4,
@@ -441,6 +441,13 @@ PSW_API int psw_fp4_workspace_bytes(const psw_layer_t *layer, int32_t n_seqs, si
  *   out  device bf16 [n_seqs][n_q_heads][head_dim] (it feeds the next projection);
  *        it must not overlap q
  *   ws   device workspace, 16-byte aligned, of psw_fp4_workspace_bytes
+ * Roundings: q is multiplied by a power of two per head and held in fp16 (values
+ * below 2^-28 of their head's largest lose bits), a key's weight exp(s - m) is
+ * rounded once to fp16 (by at most 2^-11 of it; the bf16 result by 2^-8) where it
+ * multiplies V; codes times block scales are exact, scores, maxima, the sum of the
+ * weights and O are fp32. A result near the middle of two bf16 values may so become
+ * the other of them than an fp32 form's does (1 to 10 in 100 do, with errors against
+ * 64 bits within 1 % of that form's); attn_decode_paged carries a remainder of each weight.
  * A page whose block id is outside the pool reads as zero rows and is flagged.
  * n_seqs * (max_blocks_per_seq + 8) * n_kv_heads * ceil(n_q_heads / n_kv_heads / 8) and
  * the bytes of a block, n_kv_heads * PSW_FP4_PAGE_BYTES, must stay below 2^31
