@@ -7,12 +7,13 @@
 // rounded one: the codes' borders are numbers that y / s meets exactly, and a
 // product with 1 / s would put some of those on the wrong side.
 //
-// Both directions are bound by memory: 2 HD bytes on one side of a row, 9/16
-// HD on the other. On the GPU, inputs from memory: 8 chunks of 512 tokens, 4 KV heads, K and V
-// (16.8 MB in) 7.4 us written, 2.2 of them start-up (9.4 with 218 instructions a row instead of
-// 134: limits and products one at a time, rows of both tensors in a warp); 5 ragged
-// chunks of one tensor at HD 512 (25.7 MB in) 8.8 us; 8 contexts of 512 to 8704 read back
-// (391 MB in all) 68 us, 5.8 TB/s, four fifths of it stores.
+// A row has 2 HD bytes on one side and 9/16 HD on the other. On the GPU, inputs from memory: 8 chunks
+// of 512 tokens, 4 KV heads, K and V (16.8 MB in) are written in 7.4 us, 2.2 of them start-up; 5
+// ragged chunks of one tensor at HD 512 (25.7 MB in) in 8.7. What bounds the write behind its
+// start is instructions: 134 for a row of 256 values, which take 7200 of the 11,600 cycles that an
+// SM quarter is at work (9.4 us with 218: limits and products one at a time, rows of both tensors in a
+// warp), 167 for a row of 512, 6900 of 14,400; memory is at 24 and 31 %. The read-back is bound by
+// memory: 8 contexts of 512 to 8704 (391 MB in all) 68 us, 5.8 TB/s, four fifths of it stores.
 #include "fp4.cuh"
 #include "latent.cuh"
 

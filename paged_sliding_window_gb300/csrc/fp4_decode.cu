@@ -10,8 +10,13 @@
 // 3 sequences of 40001 to 65536, 7 KV heads, 60 us for 302 MB; 64 that see 1024
 // keys, 8 KV heads, 36 us for 149 MB. Where one page serves as both (k_eq_v) it is
 // read once and worked on twice: 32 sequences of 1024 to 32768, head size 512, take 121 us
-// for 365 MB, a page 1460 cycles of an SM quarter, 1030 of which are the products and
-// the scalings of codes, which share the quarter's half-precision port.
+// for 365 MB, a page 1460 cycles of an SM quarter. 1030 of those are the products and
+// the scalings of codes, which share the quarter's half-precision port; the others are latency that
+// two warps of 255 registers do not hide (890 instructions a page; for each of them a warp stands 0.94
+// cycles at one that it depends on, 0.44 at the port, 0.25 at instructions not fetched yet).
+// More than 8 query heads to a KV head are units of their own, which read and convert the pages
+// again: 16 sequences of 6000 to 16384, 4 KV heads, take 42.6 us with 8 query heads to each
+// and 69.6 with 16, at head size 512 with k_eq_v 68.1 and 121.
 //
 //  * Every warp of a persistent grid is a worker of its own (list, runs and joins are
 //    in fp4_decode.cuh): its own ring of pages in shared memory, filled by plain bulk
@@ -51,9 +56,10 @@ struct Cfg {
   static constexpr int kRingBytes = 18432;  // per warp
   static constexpr int kStages = kRingBytes / kTileBytes;
   // Pages that a CTA could work on while the parts of several are joined: a sequence of 256, 8 KV
-  // heads, takes 7.3 us with a CTA for each head and 9.9 cut into equal runs, one of 1024 takes
-  // 13.5 and 10.7; 19 of 1024 (152 units) 13.9 and 15.8. (Head size 512, 4 heads: 256 11.2 and
-  // 12.3, 1024 22.0 and 13.6; k_eq_v 512 14.6 and 14.7, 1024 20.7 and 14.7.)
+  // heads, takes 7.8 us with a CTA for each head and 9.9 cut into equal runs, 19 of 1024 (152
+  // units) 17.2 and 19.0, pages from memory. With pages in L2: one of 1024 13.5 and 10.7, 19 of them
+  // 13.9 and 15.8. (Head size 512, 4 heads, in L2: 256 11.2 and 12.3, 1024 22.0 and 13.6; k_eq_v 512
+  // 14.6 and 14.7, 1024 20.7 and 14.7.)
   static constexpr int kApart = HD == 256 ? 28 : KEQV ? 32 : 18;
   static constexpr int kQBytes = HD == 256 ? 0 : HD * 8 * 2;  // per warp: q as operands (HD 512)
   static constexpr int kSmem = kWarps * (kRingBytes + kQBytes);
@@ -288,8 +294,9 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
       const bool edge = seen != kAll || (word & 6) != 0;
 
       // ---- S^T = K Q^T
-      // a page's products in two sums where there are few warps (71.2 -> 69.9 us, k_eq_v 122.2
-      // -> 121.2; at HD 256 the registers cost more: 36.1 -> 37.0)
+      // a page's products in two sums where there are few warps (16 sequences of 6000 to 16384, 4 KV
+      // heads, 71.2 -> 69.9 us; k_eq_v, 32 of 1024 to 32768, 122.2 -> 121.2; at HD 256 the registers
+      // cost more: 64 of 512 to 4096 36.1 -> 37.0)
       constexpr int kSums = HD == 512 ? 2 : 1;
       float s[TP * kSums][4];
 #pragma unroll
