@@ -37,6 +37,8 @@
 //    below 2^14 and what lies 30 octaves below the largest is still counted.
 //  * q is multiplied by a power of two per head so that its largest value lies in
 //    [2^14, 2^15): in f16 all but values 2^-28 of that are exact.
+#include <float.h>
+
 #include "fp4_decode.cuh"
 
 namespace psw {
@@ -225,7 +227,9 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
           }
           if constexpr (HD != 256) q_smem[(k * 4 + i) * 32] = make_uint4(h[0], h[1], h[2], h[3]);
         }
-      const float fac = a.scale * down * (a.softcap > 0.f ? 1.f / a.softcap : lat::kLog2e);
+      // (limited: under a cap far below the scores it can pass fp32, and a score of 0 has to stay 0)
+      const float fac =
+          fminf(a.scale * down * (a.softcap > 0.f ? 1.f / a.softcap : lat::kLog2e), FLT_MAX);
       qf[0] = __shfl_sync(0xffffffffu, fac, 8 * t);
       qf[1] = __shfl_sync(0xffffffffu, fac, 8 * t + 4);
 #pragma unroll
