@@ -395,14 +395,16 @@ __global__ void __launch_bounds__(Cfg<HD, KEQV>::kThreads, 1) fp4_decode_kernel(
         top[x] = fmaxf(z[0][x], z[0][2 + x]);
         if (TP == 2) top[x] = max3f(top[x], z[TP - 1][x], z[TP - 1][2 + x]);
       }
-      if (__any_sync(0xffffffffu, top[0] > m[0] + 14.f || top[1] > m[1] + 14.f)) {
+      // (m + 14 rounded down: to nearest, it would be m + 16 where m is above 2^25, and P infinite)
+      const float lim[2] = {__fadd_rd(m[0], 14.f), __fadd_rd(m[1], 14.f)};
+      if (__any_sync(0xffffffffu, top[0] > lim[0] || top[1] > lim[1])) {
         float al[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1)
             top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], o));
-          const float mn = top[x] > m[x] + 14.f ? top[x] - 6.f : m[x];
+          const float mn = top[x] > lim[x] ? top[x] - 6.f : m[x];
           al[x] = m[x] == mn ? 1.f : ex2_approx(m[x] - mn);
           m[x] = mn;
           l[x] *= al[x];
