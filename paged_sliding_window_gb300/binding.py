@@ -751,7 +751,8 @@ def block_table_extend(block_table, past_lens, new_lens, free_ids, free_pos, fre
     for the pages that new_lens int32 [n] tokens after past_lens [n] begin, from free_ids int32
     [n_free] at the cursor free_pos int32 [1] on; free_next [1] (may be free_pos), cu_new [n + 1],
     seq_lens [n] and slots int64 [rows] or None are written (n 0: the cursor, where it is not in
-    place, and cu_new with it)."""
+    place, and cu_new with it). Only free_next may be another of the tensors: not seq_lens past_lens,
+    which is copied for the next step."""
     dev, n = block_table.get_device(), past_lens.shape[0]
     if block_table.dim() != 2 or block_table.shape[0] < n:
         raise ValueError(f"block_table must have {n} rows or more, got {tuple(block_table.shape)}")
@@ -871,7 +872,7 @@ def kv_cache_read_fp4(layer, k_pool4, v_pool4, pages: PswPages, first, seq_lens,
 def attn_decode_paged_fp4(layer, q, k_pool4, v_pool4, pages: PswPages, seq_lens, out, lse=None,
                           ws=None, k_scale: float = 1.0, v_scale: float = 1.0,
                           stream=None) -> None:
-    """attn_decode_paged over 4-bit pools; out is bf16 [n, n_q, head_dim], ws from
+    """attn_decode_paged over 4-bit pools; out is bf16 [n, n_q, head_dim] and must not overlap q, ws from
     alloc_fp4_workspace (calls that may overlap on the GPU need one each)."""
     z_ref, n_q, n_kv, hd, k_eq_v = _layer_struct(layer)
     dev, n = q.get_device(), seq_lens.shape[0]
