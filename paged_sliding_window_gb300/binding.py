@@ -751,8 +751,8 @@ def block_table_extend(block_table, past_lens, new_lens, free_ids, free_pos, fre
     for the pages that new_lens int32 [n] tokens after past_lens [n] begin, from free_ids int32
     [n_free] at the cursor free_pos int32 [1] on; free_next [1] (may be free_pos), cu_new [n + 1],
     seq_lens [n] and slots int64 [rows] or None are written (n 0: the cursor, where it is not in
-    place, and cu_new with it). Only free_next may be another of the tensors: not seq_lens past_lens,
-    which is copied for the next step."""
+    place, and cu_new with it). No other two may overlap: seq_lens is copied to past_lens for the
+    next step, not written there."""
     dev, n = block_table.get_device(), past_lens.shape[0]
     if block_table.dim() != 2 or block_table.shape[0] < n:
         raise ValueError(f"block_table must have {n} rows or more, got {tuple(block_table.shape)}")
